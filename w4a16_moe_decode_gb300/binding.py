@@ -14,6 +14,7 @@ import os
 from .build import LIB
 
 c_int32 = ctypes.c_int32
+c_int64 = ctypes.c_int64
 c_void_p = ctypes.c_void_p
 c_size_t = ctypes.c_size_t
 
@@ -46,6 +47,11 @@ class flint_moe_nvfp4_src(ctypes.Structure):
 class flint_moe_src(ctypes.Structure):
     _fields_ = [("gate", flint_moe_nvfp4_src), ("up", flint_moe_nvfp4_src), ("down", flint_moe_nvfp4_src),
                 ("gate_bf16", c_void_p), ("up_bf16", c_void_p), ("down_bf16", c_void_p)]
+
+
+class flint_lora(ctypes.Structure):
+    _fields_ = [("in_dim", c_int32), ("out_dim", c_int32), ("rank", c_int32), ("num_adapters", c_int32),
+                ("a", c_void_p), ("b", c_void_p), ("scale", c_void_p)]
 
 
 class flint_gemv_src(ctypes.Structure):
@@ -104,6 +110,25 @@ def lib() -> ctypes.CDLL:
                                                     c_size_t, c_void_p]),
             "flint_moe_prefill_debug_routing": (c_int32, [P(flint_moe_config), c_void_p, c_int32, c_void_p, c_void_p,
                                                           c_void_p, c_void_p]),
+            "flint_lora_init": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
+                                          P(flint_lora)]),
+            "flint_lora_workspace_bytes": (c_size_t, [P(flint_lora), c_int32]),
+            "flint_lora_apply": (c_int32, [P(flint_lora), c_void_p, c_int64, c_void_p, c_int32, c_void_p, c_void_p,
+                                           c_int64, c_void_p, c_size_t, c_void_p]),
+            "flint_gemv_lora_workspace_bytes": (c_size_t, [P(flint_lora), c_int32]),
+            "flint_gemv_lora": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_void_p, c_int32, c_void_p,
+                                          P(flint_lora), c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+            "flint_lora_backward_workspace_bytes": (c_size_t, [P(flint_lora), c_int32]),
+            "flint_lora_backward": (c_int32, [P(flint_lora), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int32,
+                                              c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_size_t,
+                                              c_void_p]),
+            "flint_moe_balance_workspace_bytes": (c_size_t, [P(flint_moe_config), c_int32, c_int32]),
+            "flint_moe_balance": (c_int32, [P(flint_moe_config), c_void_p, c_void_p, c_int32, c_void_p, c_int32,
+                                            ctypes.c_float, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                            c_size_t, c_void_p]),
+            "flint_moe_balance_backward": (c_int32, [P(flint_moe_config), c_void_p, c_void_p, c_int32, c_void_p,
+                                                     c_int32, ctypes.c_float, c_void_p, c_void_p, c_void_p, c_void_p,
+                                                     c_void_p, c_void_p]),
             "flint_synth_stream_key": (ctypes.c_uint64, [ctypes.c_uint64, ctypes.c_uint32, ctypes.c_uint32,
                                                          ctypes.c_uint32]),
             "flint_synth_normal": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_uint64, c_size_t, ctypes.c_float, c_int32,
@@ -324,6 +349,95 @@ def flint_gemv(packed, N: int, K: int, fmt, x, B: int, y, norm_weight=None, eps:
                stream=None) -> None:
     _check("flint_gemv", lib().flint_gemv(_ptr(packed), N, K, fmt, _ptr(x), B, _ptr(y), _ptr(norm_weight),
                                           float(eps), _ptr(dev_status), _stream(stream)))
+
+
+def _nbytes(workspace, workspace_bytes) -> int:
+    return workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+
+
+def _ld(t, rows: int, cols: int, ld) -> int:
+    """Elements between the rows of t: `ld` if given, else a 2-D tensor's own row stride (cols where
+    there is one row, no tensor or a bare pointer)."""
+    if ld is not None:
+        return ld
+    if rows < 2 or t is None or isinstance(t, int) or t.dim() != 2:
+        return cols
+    return t.stride(0)
+
+
+def flint_lora_init(a, b, scale, in_dim=None, out_dim=None, rank=None, num_adapters=None) -> flint_lora:
+    """A pool of adapters: a [n][R][K], b [n][N][R] (bf16), scale [n] (float32). The shapes come from the
+    tensors unless given. The caller keeps the tensors alive."""
+    if num_adapters is None:
+        num_adapters, rank, in_dim = a.shape
+        out_dim = b.shape[1]
+    lora = flint_lora()
+    _check("flint_lora_init", lib().flint_lora_init(in_dim, out_dim, rank, num_adapters, _ptr(a), _ptr(b),
+                                                    _ptr(scale), ctypes.byref(lora)))
+    return lora
+
+
+def flint_lora_workspace_bytes(lora: flint_lora, max_tokens: int) -> int:
+    return lib().flint_lora_workspace_bytes(ctypes.byref(lora), max_tokens)
+
+
+def flint_lora_apply(lora: flint_lora, x, adapter, T: int, y_in, y_out, workspace, ldx=None, ldy=None,
+                     workspace_bytes=None, stream=None) -> None:
+    """y_out[t] = bf16(y_in[t] + scale_a B_a (A_a x[t])), a = adapter[t] (include/flint_lora.h). Row strides
+    are those of x and y_out (y_in has y_out's)."""
+    _check("flint_lora_apply",
+           lib().flint_lora_apply(ctypes.byref(lora), _ptr(x), _ld(x, T, lora.in_dim, ldx), _ptr(adapter), T,
+                                  _ptr(y_in), _ptr(y_out), _ld(y_out, T, lora.out_dim, ldy), _ptr(workspace),
+                                  _nbytes(workspace, workspace_bytes), _stream(stream)))
+
+
+def flint_gemv_lora_workspace_bytes(lora: flint_lora, max_batch: int) -> int:
+    return lib().flint_gemv_lora_workspace_bytes(ctypes.byref(lora), max_batch)
+
+
+def flint_gemv_lora(packed, N: int, K: int, fmt, x, B: int, y, lora: flint_lora, adapter, workspace,
+                    workspace_bytes=None, dev_status=None, stream=None) -> None:
+    """flint_gemv with adapters beside the matrix, one rounding (include/flint_lora.h)."""
+    _check("flint_gemv_lora",
+           lib().flint_gemv_lora(_ptr(packed), N, K, fmt, _ptr(x), B, _ptr(y), ctypes.byref(lora), _ptr(adapter),
+                                 _ptr(workspace), _nbytes(workspace, workspace_bytes), _ptr(dev_status),
+                                 _stream(stream)))
+
+
+def flint_lora_backward_workspace_bytes(lora: flint_lora, max_tokens: int) -> int:
+    return lib().flint_lora_backward_workspace_bytes(ctypes.byref(lora), max_tokens)
+
+
+def flint_lora_backward(lora: flint_lora, x, dy, adapter, T: int, dx_in, dx_out, da, db, workspace, ldx=None,
+                        lddy=None, lddx=None, workspace_bytes=None, stream=None) -> None:
+    """dx_out, da, db of flint_lora_apply from dy (include/flint_lora.h); dx_out None skips it."""
+    _check("flint_lora_backward",
+           lib().flint_lora_backward(ctypes.byref(lora), _ptr(x), _ld(x, T, lora.in_dim, ldx), _ptr(dy),
+                                     _ld(dy, T, lora.out_dim, lddy), _ptr(adapter), T, _ptr(dx_in), _ptr(dx_out),
+                                     _ld(dx_out, T, lora.in_dim, lddx), _ptr(da), _ptr(db), _ptr(workspace),
+                                     _nbytes(workspace, workspace_bytes), _stream(stream)))
+
+
+def flint_moe_balance_workspace_bytes(cfg: flint_moe_config, max_tokens: int, max_seqs: int) -> int:
+    return lib().flint_moe_balance_workspace_bytes(ctypes.byref(cfg), max_tokens, max_seqs)
+
+
+def flint_moe_balance(cfg: flint_moe_config, logits, idx, T: int, seq_start, n_seq: int, alpha: float, loss, counts,
+                      seq_counts, seq_tokens, workspace, workspace_bytes=None, stream=None) -> None:
+    """Balance loss and per-expert counts of T routed tokens (include/flint_moe_balance.h)."""
+    _check("flint_moe_balance",
+           lib().flint_moe_balance(ctypes.byref(cfg), _ptr(logits), _ptr(idx), T, _ptr(seq_start), n_seq, alpha,
+                                   _ptr(loss), _ptr(counts), _ptr(seq_counts), _ptr(seq_tokens), _ptr(workspace),
+                                   _nbytes(workspace, workspace_bytes), _stream(stream)))
+
+
+def flint_moe_balance_backward(cfg: flint_moe_config, logits, idx, T: int, seq_start, n_seq: int, alpha: float,
+                               seq_counts, seq_tokens, dloss, dw, dlogits, stream=None) -> None:
+    """The logits' gradient of the balance loss and (dw) of the routing weights (include/flint_moe_balance.h)."""
+    _check("flint_moe_balance_backward",
+           lib().flint_moe_balance_backward(ctypes.byref(cfg), _ptr(logits), _ptr(idx), T, _ptr(seq_start), n_seq,
+                                            alpha, _ptr(seq_counts), _ptr(seq_tokens), _ptr(dloss), _ptr(dw),
+                                            _ptr(dlogits), _stream(stream)))
 
 
 def flint_synth_stream_key(seed, layer, tensor, expert) -> int:

@@ -2,7 +2,7 @@
 
 Each .cu file compiles to an object in parallel, then one shared library is
 linked against the CUDA runtime. No CMake, no torch extension machinery: the
-library exposes a plain C ABI (include/flint_moe.h, include/flint_synth.h).
+library exposes a plain C ABI (the headers in include/).
 """
 from __future__ import annotations
 
@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.environ.get("FLINT_MOE_LIB") or os.path.join(PKG, "libflint_moe.so")
-SOURCES = ["decode.cu", "pack.cu", "synth.cu", "prefill.cu"]
+SOURCES = ["decode.cu", "pack.cu", "synth.cu", "prefill.cu", "lora.cu", "balance.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -464,5 +464,10 @@ static __device__ __noinline__ uint4 norm8_huge(const uint4 x, const uint4 w, co
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// The dense GEMV behind flint_gemv (decode.cu): with y32 not null the FP32 sums
+// go there, [B][N], and y is left alone.
+flint_moe_status gemv_impl(const void* packed, int32_t N, int32_t K, int32_t fmt, const uint16_t* x, int32_t B,
+                           uint16_t* y, float* y32, const uint16_t* norm_weight, float eps, int32_t* dev_status,
+                           cudaStream_t stream);
 
 }  // namespace flint

@@ -1686,6 +1686,7 @@ struct GemvArgs {
   int N, K, B, fmt, prenorm;
   const uint16_t* x;
   uint16_t* y;
+  float* y32;  // not null: the FP32 sums are written here instead of y (flint_gemv_lora adds to them)
   const uint8_t* packed;
   const float* G;  // the tensor scale word after the tiles
   Layout L;
@@ -1780,7 +1781,12 @@ __global__ void __launch_bounds__(256) k_gemv(GemvArgs a) {
     const int ln = 4 * (r & 7) + (c >> 1), i = 2 * (r >> 3) + (c & 1);
     float v = 0.f;
     for (int w2 = 0; w2 < nw; ++w2) v += red[((w2 * NTMAX + nt) * 32 + ln) * 4 + i];
-    const __nv_bfloat16 o = __float2bfloat16_rn((v * s_inv[t]) * G);
+    const float vg = (v * s_inv[t]) * G;
+    if (a.y32) {
+      a.y32[(size_t)t * a.N + blockIdx.x * 16 + r] = vg;
+      continue;
+    }
+    const __nv_bfloat16 o = __float2bfloat16_rn(vg);
     a.y[(size_t)t * a.N + blockIdx.x * 16 + r] = *reinterpret_cast<const uint16_t*>(&o);
   }
 }
@@ -1973,6 +1979,10 @@ __global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
       float v2 = 0.f;
       for (uint32_t r = 0; r < S; ++r) v2 += ld_dsmem_f32(part + p, r);  // rank order
       const int rr = p & 15, t = p >> 4;
+      if (a.y32) {
+        a.y32[(size_t)t * a.N + blockIdx.x * 16 + rr] = v2 * G;
+        continue;
+      }
       const __nv_bfloat16 o = __float2bfloat16_rn(v2 * G);
       a.y[(size_t)t * a.N + blockIdx.x * 16 + rr] = *reinterpret_cast<const uint16_t*>(&o);
     }
@@ -2499,6 +2509,13 @@ extern "C" flint_moe_status flint_moe_debug_wait_timeout(int32_t* dev_status, cu
 extern "C" flint_moe_status flint_gemv(const void* packed, int32_t N, int32_t K, int32_t fmt, const uint16_t* x,
                                        int32_t B, uint16_t* y, const uint16_t* norm_weight, float eps,
                                        int32_t* dev_status, cudaStream_t stream) {
+  return flint::gemv_impl(packed, N, K, fmt, x, B, y, nullptr, norm_weight, eps, dev_status, stream);
+}
+
+// flint_gemv, or with y32 the same product left in FP32 [B][N] (y is then only checked).
+flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int32_t fmt, const uint16_t* x, int32_t B,
+                                  uint16_t* y, float* y32, const uint16_t* norm_weight, float eps, int32_t* dev_status,
+                                  cudaStream_t stream) {
   if (flint_gemv_packed_bytes(N, K, fmt) == 0) return FLINT_MOE_EUNSUPPORTED;
   if (B < 0 || B > MAX_BATCH || !(eps >= 0.f) || !(eps <= 3.0e38f)) return FLINT_MOE_EINVAL;
   if (B == 0) return FLINT_MOE_OK;
@@ -2513,6 +2530,7 @@ extern "C" flint_moe_status flint_gemv(const void* packed, int32_t N, int32_t K,
   a.prenorm = norm_weight != nullptr;
   a.x = x;
   a.y = y;
+  a.y32 = y32;
   a.packed = static_cast<const uint8_t*>(packed);
   a.L = make_dense_layout(N, K, fmt);
   a.G = reinterpret_cast<const float*>(a.packed + a.L.globals_off + 8);  // [G, G, G, 0]: the third word
