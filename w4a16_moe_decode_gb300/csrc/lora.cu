@@ -6,14 +6,748 @@
 //   g_t = s_a B_a^T dy_t           dx_t = bf16(dx_in_t + A_a^T g_t)
 //   dA_a = sum_t g_t x_t^T         dB_a = sum_t dy_t h_t^T
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "flint_lora.h"
+#include "tensor.cuh"
 
 namespace flint {
 namespace lora {
 
+constexpr int TM = 128;       // tokens of a tile (the tensor cores' M)
+constexpr int BK = 64;        // columns of one 128-byte swizzled row
+constexpr int BOX = TM * BK * 2;   // 16 KiB: 128 rows x 64 columns
+constexpr int HALF = BOX / 2;      // 8 KiB: 64 rows x 64 columns
+enum : int { H_STATUS = HDR_STATUS, H_TILES = 2, H_CHUNKS = 3 };
+
+// A tile: up to 128 tokens of one adapter (-1: tokens without one). Its row r is
+// token rowmap[tile * 128 + r]; rows past `count` repeat the last token there, so
+// that every row can be loaded, and are zero in h and g.
 struct Args {
+  int K, N, R, Rp, n, T;  // Rp: R rounded up to 16, the tensor cores' step
+  const float* scale;
+  const int* adapter;
+  int with_none;  // tokens without an adapter get tiles (their output rows have to be written)
+  int max_tiles;
+  int* hdr;
+  int2* tiles;   // {adapter, count}
+  int* rowmap;   // [max_tiles * 128]
+  uint16_t* h;   // s A x as bf16 halves hi, lo: [2][max_tiles * 128][R]
+  uint16_t* g;   // s B^T dy likewise
+  const uint16_t* in;  // y_in or dx_in, or null
+  uint16_t* out;
+  int64_t ldo;
+  // weights' gradients
+  int CT;              // tiles of a chunk at most
+  int slabs_a, slabs_b;  // 128-wide slabs of K and of N
+  int4* chunks;        // {adapter, first tile, tiles, partial slot or -1}
+  int2* of_adapter;    // {first partial slot, chunks} of each adapter
+  float* part;         // [slot][R K + N R]
+  uint16_t* dA;
+  uint16_t* dB;
+};
+
+struct Maps {
+  CUtensorMap x, dy;    // token rows, gathered: boxes of 64 columns x 1 row
+  CUtensorMap in;       // base rows, gathered
+  CUtensorMap a, b;     // A [n][R][K]: boxes 64 x Rp; B [n][N][R]: boxes 64 x 128
+  CUtensorMap b64;      // B, boxes 64 x 64
+  CUtensorMap h, g;     // [2 * max_tiles * 128][R], boxes 64 x 64
+};
+
+__device__ __forceinline__ uint16_t f2b(float v) {
+  const __nv_bfloat16 o = __float2bfloat16_rn(v);
+  return *reinterpret_cast<const uint16_t*>(&o);
+}
+__device__ __forceinline__ uint32_t f2b2(float lo, float hi) {
+  const __nv_bfloat162 o = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&o);
+}
+
+// ---------------------------------------------------------------------------
+// Plan (one block): tokens sorted by adapter, stably, into tiles. Warp w owns a
+// run of consecutive tokens; the 32 tokens of a step find their fellows with
+// match_any, so every token's place follows from counts and lane masks alone.
+// ---------------------------------------------------------------------------
+__host__ __device__ inline size_t plan_smem(int n) { return sizeof(int) * ((size_t)33 * (n + 1) + 3 * (n + 2)); }
+
+// Exclusive sums of f(0 .. n-1) into out[0 .. n], by one warp.
+template <typename F>
+__device__ __forceinline__ void warp_scan(int n, int lane, int* out, F f) {
+  const int per = (n + 31) / 32, i0 = min(n, lane * per), i1 = min(n, i0 + per);
+  int own = 0;
+  for (int i = i0; i < i1; ++i) own += f(i);
+  int inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  int at = inc - own;
+  for (int i = i0; i < i1; ++i) {
+    out[i] = at;
+    at += f(i);
+  }
+  if (lane == 31) out[n] = inc;
+}
+
+// The last g in [0, n) with first[g] <= i: the group of item i < first[n].
+__device__ __forceinline__ int group_of(const int* first, int n, int i) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (first[m] <= i)
+      lo = m;
+    else
+      hi = m;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(1024) k_lora_plan(const Args a) {
+  extern __shared__ int sm[];
+  const int G = a.n + 1;  // group n: tokens without an adapter
+  int* hist = sm;         // [32][G], then each warp's next place in the group
+  int* cnt = hist + 32 * G;
+  int* tf = cnt + G;       // first tile of each group
+  int* cf = tf + G + 1;    // first chunk
+  int* sf = cf + G + 1;    // first partial slot
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < 32 * G; i += 1024) hist[i] = 0;
+  pdl_wait();
+  pdl_trigger();
+  __syncthreads();
+  const int L = (a.T + 1023) / 1024 * 32, t0 = warp * L, t1 = min(a.T, t0 + L);
+  int* mine = hist + warp * G;
+  for (int i = t0; i < t1; i += 32) {
+    const int t = i + lane;
+    int g = -1;
+    if (t < t1) {
+      g = __ldg(a.adapter + t);
+      if (g < 0 || g >= a.n) g = a.n;
+    }
+    const unsigned same = __match_any_sync(0xffffffffu, g);
+    if (g >= 0 && lane == __ffs(same) - 1) mine[g] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int g = threadIdx.x; g < G; g += 1024) {
+    int at = 0;
+    for (int w = 0; w < 32; ++w) {
+      const int c = hist[w * G + g];
+      hist[w * G + g] = at;
+      at += c;
+    }
+    cnt[g] = g == a.n && !a.with_none ? 0 : at;
+  }
+  __syncthreads();
+  auto tiles_of = [&](int g) { return (cnt[g] + TM - 1) / TM; };
+  auto chunks_of = [&](int g) { return g == a.n ? 0 : (tiles_of(g) + a.CT - 1) / a.CT; };
+  if (warp == 0) warp_scan(G, lane, tf, tiles_of);
+  if (warp == 1 && a.chunks) warp_scan(G, lane, cf, chunks_of);
+  if (warp == 2 && a.chunks) warp_scan(G, lane, sf, [&](int g) { return chunks_of(g) > 1 ? chunks_of(g) : 0; });
+  __syncthreads();
+  for (int i = t0; i < t1; i += 32) {
+    const int t = i + lane;
+    int g = -1;
+    if (t < t1) {
+      g = __ldg(a.adapter + t);
+      if (g < 0 || g >= a.n) g = a.n;
+    }
+    const unsigned same = __match_any_sync(0xffffffffu, g);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    int at = 0;
+    if (g >= 0) at = mine[g] + rank;
+    __syncwarp();
+    if (g >= 0 && rank == 0) mine[g] += __popc(same);
+    __syncwarp();
+    if (g >= 0 && (g < a.n || a.with_none)) a.rowmap[tf[g] * TM + at] = t;
+  }
+  __syncthreads();
+  const int ntiles = tf[G];
+  for (int i = threadIdx.x; i < ntiles; i += 1024) {
+    const int g = group_of(tf, G, i);
+    a.tiles[i] = make_int2(g == a.n ? -1 : g, min(TM, cnt[g] - TM * (i - tf[g])));
+  }
+  for (int i = warp; i < ntiles; i += 32) {  // rows past a tile's count repeat its last token
+    const int g = group_of(tf, G, i), count = min(TM, cnt[g] - TM * (i - tf[g]));
+    if (count < TM) {
+      const int t = a.rowmap[i * TM + count - 1];
+      for (int r = count + lane; r < TM; r += 32) a.rowmap[i * TM + r] = t;
+    }
+  }
+  if (a.chunks) {
+    const int nchunks = cf[G];
+    for (int c = threadIdx.x; c < nchunks; c += 1024) {
+      const int g = group_of(cf, G, c), j = c - cf[g];
+      a.chunks[c] = make_int4(g, tf[g] + j * a.CT, min(a.CT, tiles_of(g) - j * a.CT), chunks_of(g) > 1 ? sf[g] + j : -1);
+    }
+    for (int g = threadIdx.x; g < a.n; g += 1024) a.of_adapter[g] = make_int2(sf[g], chunks_of(g));
+    if (threadIdx.x == 0) a.hdr[H_CHUNKS] = nchunks;
+  }
+  if (threadIdx.x == 0) {
+    a.hdr[H_STATUS] = 0;
+    a.hdr[H_TILES] = ntiles;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Shrink: h = s A x of one tile (z = 0) or g = s B^T dy (z = 1), [128 x D] times
+// [D x R] on the tensor cores. A cluster of S CTAs shares a tile; CTA s takes a
+// run of the 64-column k-blocks, and the partial sums meet in distributed shared
+// memory, added in CTA order. Bound by the token rows it reads: per k-block 16 KiB
+// of them against at most 16 KiB of weights from L2.
+//   warp 0     one TMA gather of four rows per lane and k-block, plus the weights
+//   warp 1     the MMAs (A stored [R][K] is K-major; B stored [N][R] has R
+//              contiguous, an MN-major operand: no transposed copy)
+//   warps 2-5  the accumulator, tensor memory -> shared memory
+// ---------------------------------------------------------------------------
+constexpr int SHR_STAGES = 4;
+constexpr int SHR_THREADS = 192;
+
+__host__ __device__ inline int shrink_wbytes(int R) { return R > 64 ? 2 * HALF : HALF; }
+__host__ __device__ inline size_t shrink_smem(int R) { return 1024 + (size_t)SHR_STAGES * (BOX + shrink_wbytes(R)); }
+__host__ __device__ inline uint32_t tmem_cols(int c) { return c <= 32 ? 32 : c <= 64 ? 64 : c <= 128 ? 128 : 256; }
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+}
+
+__global__ void __launch_bounds__(SHR_THREADS) k_lora_shrink(const Args a, const __grid_constant__ Maps maps) {
+  extern __shared__ uint8_t dsmem[];
+  __shared__ uint64_t full[SHR_STAGES], empty[SHR_STAGES], acc_full;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
+  uint8_t* const basep = dsmem + (base - smem_addr(dsmem));
+  volatile int* abort = &abort_flag;
+  int* status = a.hdr + H_STATUS;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < SHR_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&acc_full, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+  const int tile = blockIdx.y;
+  if (tile >= __ldcg(a.hdr + H_TILES)) return;
+  const int2 tl = __ldcg(a.tiles + tile);
+  if (tl.x < 0) return;  // the whole cluster leaves: nothing waits for it
+  const bool grad = blockIdx.z != 0;
+  const int S = gridDim.x, rank = blockIdx.x;
+  const int D = grad ? a.N : a.K, KB = (D + BK - 1) / BK;
+  const int kb0 = rank * KB / S, nkb = (rank + 1) * KB / S - kb0;
+  const int wbytes = shrink_wbytes(a.R), stage = BOX + wbytes;
+  const uint32_t cols = tmem_cols(a.Rp);
+  if (warp == 1) tmem_alloc(&tmem_base, cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  if (warp == 0) {
+    const int4 rows = __ldcg(reinterpret_cast<const int4*>(a.rowmap + tile * TM) + lane);
+    const int groups = (tl.y + 3) / 4;  // rows past the count stay as they are: a tensor-core row reads only itself
+    const CUtensorMap* xm = grad ? &maps.dy : &maps.x;
+    const uint32_t tx = groups * 512 + (grad ? (a.R > 64 ? 2 : 1) * HALF : a.Rp * 128);
+    int i = 0;
+    for (; i < nkb; ++i) {
+      const int s = i % SHR_STAGES;
+      const bool ok = i < SHR_STAGES || wait_ab(&empty[s], ((i / SHR_STAGES) - 1) & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int col = (kb0 + i) * BK;
+      const uint32_t xs = base + s * stage, wsm = xs + BOX;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[s], tx);
+        if (grad) {
+          tma_load_3d(wsm, &maps.b64, 0, col, tl.x, &full[s]);
+          if (a.R > 64) tma_load_3d(wsm + HALF, &maps.b64, 64, col, tl.x, &full[s]);
+        } else {
+          tma_load_3d(wsm, &maps.a, col, 0, tl.x, &full[s]);
+        }
+      }
+      __syncwarp();
+      if (lane < groups) tma_gather4(xs + lane * 512, xm, col, rows, &full[s]);
+    }
+    // the CTA's memory must outlive every copy in flight
+    for (int r = (i > SHR_STAGES ? i - SHR_STAGES : 0); r < i; ++r) mbar_drain(&full[r % SHR_STAGES], (r / SHR_STAGES) & 1);
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_f32acc(TM, a.Rp, true) | (grad ? IDESC_B_MN : 0u);
+    int i = 0;
+    for (; i < nkb; ++i) {
+      const int s = i % SHR_STAGES;
+      const bool ok = wait_ab(&full[s], (i / SHR_STAGES) & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t xs = base + s * stage, wsm = xs + BOX;
+        const uint64_t ad = sw128_desc(xs);
+        const uint64_t bd = grad ? sw128_desc_mn(wsm, HALF) : sw128_desc(wsm);
+        const uint64_t bstep = grad ? 2048 >> 4 : 32 >> 4;  // 16 rows of B, or 16 columns of A
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          tc_mma(tmem, ad + (uint64_t)(ks * 2), bd + ks * bstep, idesc, (i > 0 || ks > 0) ? 1u : 0u);
+        tc_commit(&empty[s]);
+        if (i == nkb - 1) tc_commit(&acc_full);
+      }
+      __syncwarp();
+    }
+    for (int r = (i > SHR_STAGES ? i - SHR_STAGES : 0); r < i; ++r) mbar_drain(&empty[r % SHR_STAGES], (r / SHR_STAGES) & 1);
+  }
+  // Every CTA's sums to its shared memory (the stages are free by then), [128][Rp] padded by 16 bytes a row.
+  const int PP = a.Rp + 4;
+  float* part = reinterpret_cast<float*>(basep);
+  bool ok = true;
+  if (warp >= 2) {
+    ok = wait_ab(&acc_full, 0, abort, status);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      const int q = warp & 3, row = q * 32 + lane;
+      if (q * 32 < tl.y) {
+        for (int c = 0; c < a.Rp; c += 16) {
+          uint32_t v[16];
+          tc_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(part + row * PP + c + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free(tmem, cols);
+  }
+  cluster_sync();
+  const int rows = TM / S, r0 = rank * rows, R4 = a.R / 4;
+  const float sc = __ldg(a.scale + tl.x);
+  uint16_t* hi = grad ? a.g : a.h;
+  uint16_t* lo = hi + (size_t)a.max_tiles * TM * a.R;
+  for (int i = threadIdx.x; i < rows * R4; i += SHR_THREADS) {
+    const int r = r0 + i / R4, c = (i % R4) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < tl.y) {
+      for (int q = 0; q < S; ++q) {
+        const float4 u = ld_dsmem_f4(part + r * PP + c, q);
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
+      }
+      v.x *= sc;
+      v.y *= sc;
+      v.z *= sc;
+      v.w *= sc;
+    }
+    // hi + lo carries 16 significant bits of the FP32 sum into the next product
+    const uint2 hv = make_uint2(f2b2(v.x, v.y), f2b2(v.z, v.w));
+    const uint2 lv = make_uint2(f2b2(v.x - bf16lo(hv.x), v.y - bf16hi(hv.x)), f2b2(v.z - bf16lo(hv.y), v.w - bf16hi(hv.y)));
+    const size_t at = ((size_t)tile * TM + r) * a.R + c;
+    *reinterpret_cast<uint2*>(hi + at) = hv;
+    *reinterpret_cast<uint2*>(lo + at) = lv;
+  }
+  cluster_sync();  // the others' shared memory stays until it has been read
+}
+
+// ---------------------------------------------------------------------------
+// Expand: out = bf16(in + h B^T) (GRAD: in + g A), per tile [128 x R] times
+// [R x 128 columns] for both halves of h. The (tile, 128 columns) items are one
+// list, and each CTA takes a run of it, so that a tile's h is loaded once per run.
+// Bound by the base rows it reads and the rows it writes.
+//   warp 0     TMA: base rows (gathered, four rows a lane), weights, a tile's h
+//   warp 1     the MMAs into two accumulators of 128 columns
+//   warps 2-9  tensor memory + base -> bf16 in place in shared memory -> rows
+// ---------------------------------------------------------------------------
+constexpr int EXP_THREADS = 320;
+__host__ __device__ inline int exp_stages(int R) { return R > 64 ? 2 : 3; }
+__host__ __device__ inline int exp_hbufs(int R) { return R > 64 ? 1 : 2; }
+__host__ __device__ inline int exp_wbytes(int R) { return R > 64 ? 2 * BOX : BOX; }   // one stage's weights
+__host__ __device__ inline int exp_hbytes(int R) { return R > 64 ? 4 * BOX : 2 * BOX; }  // hi and lo of a tile
+__host__ __device__ inline size_t exp_smem(int R) {
+  return 1024 + (size_t)exp_stages(R) * (2 * BOX + exp_wbytes(R)) + (size_t)exp_hbufs(R) * exp_hbytes(R);
+}
+
+template <bool GRAD>
+__global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, const __grid_constant__ Maps maps) {
+  extern __shared__ uint8_t dsmem[];
+  __shared__ uint64_t full[3], empty[3], acc_full[2], acc_empty[2], h_full[2], h_empty[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
+  uint8_t* const basep = dsmem + (base - smem_addr(dsmem));
+  volatile int* abort = &abort_flag;
+  int* status = a.hdr + H_STATUS;
+  const int ST = exp_stages(a.R), HB = exp_hbufs(a.R), nbox = a.R > 64 ? 2 : 1;
+  const int stage = 2 * BOX + exp_wbytes(a.R), hbytes = exp_hbytes(a.R);
+  const uint32_t hbase = base + ST * stage;
+  const int D = GRAD ? a.K : a.N, nsub = (D + 127) / 128;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 8);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8);
+      mbar_init(&h_full[b], 1);
+      mbar_init(&h_empty[b], 1);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(&tmem_base, 256);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_wait();
+  // This CTA's run [u0, u1) of the items.
+  const long long items = (long long)__ldcg(a.hdr + H_TILES) * nsub;
+  const int u0 = (int)(items * blockIdx.x / gridDim.x), u1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
+  const size_t plane = (size_t)a.max_tiles * TM;
+  if (warp == 0) {
+    int v = 0, hn = 0, tile = -1;  // items, h loads
+    int2 tl = make_int2(-1, 0);
+    int4 rows = make_int4(0, 0, 0, 0);
+    for (int u = u0; u < u1; ++u, ++v) {
+      const int s = v % ST, col = (u % nsub) * 128;
+      bool ok = true;
+      if (u / nsub != tile) {
+        tile = u / nsub;
+        tl = __ldcg(a.tiles + tile);
+        rows = __ldcg(reinterpret_cast<const int4*>(a.rowmap + tile * TM) + lane);
+        if (tl.x >= 0) {
+          const int b = hn % HB;
+          ok = hn < HB || wait_ab(&h_empty[b], ((hn / HB) - 1) & 1, abort, status);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          if (lane == 0) {
+            const CUtensorMap* m = GRAD ? &maps.g : &maps.h;
+            mbar_arrive_expect_tx(&h_full[b], (uint32_t)hbytes);
+            for (int p = 0; p < 2; ++p)
+              for (int x = 0; x < nbox; ++x)
+                for (int y = 0; y < 2; ++y)
+                  tma_load_2d(hbase + b * hbytes + (p * nbox + x) * BOX + y * HALF, m, x * 64,
+                              (int)(p * plane) + tile * TM + y * 64, &h_full[b]);
+          }
+          ++hn;
+        }
+      }
+      ok = v < ST || wait_ab(&empty[s], ((v / ST) - 1) & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint32_t ys = base + s * stage, wsm = ys + 2 * BOX;
+      const int groups = a.in ? (tl.y + 3) / 4 : 0;
+      const int boxes = col + 64 < D ? 2 : 1;  // 64-column halves that hold columns at all
+      if (lane == 0) {
+        const uint32_t wtx = tl.x < 0 ? 0 : (GRAD ? boxes * a.Rp * 128 : nbox * BOX);
+        mbar_arrive_expect_tx(&full[s], (uint32_t)(groups * 512 * boxes) + wtx);
+        if (tl.x >= 0) {
+          if (GRAD) {
+            for (int y = 0; y < boxes; ++y) tma_load_3d(wsm + y * a.Rp * 128, &maps.a, col + 64 * y, 0, tl.x, &full[s]);
+          } else {
+            for (int x = 0; x < nbox; ++x) tma_load_3d(wsm + x * BOX, &maps.b, x * 64, col, tl.x, &full[s]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane < groups)
+        for (int y = 0; y < boxes; ++y) tma_gather4(ys + y * BOX + lane * 512, &maps.in, col + 64 * y, rows, &full[s]);
+    }
+    for (int r = (v > ST ? v - ST : 0); r < v; ++r) mbar_drain(&full[r % ST], (r / ST) & 1);
+    for (int r = (hn > HB ? hn - HB : 0); r < hn; ++r) mbar_drain(&h_full[r % HB], (r / HB) & 1);
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_f32acc(TM, 128, true) | (GRAD ? IDESC_B_MN : 0u);
+    int v = 0, m = 0, hn = 0, tile = -1;  // items, accumulators, h loads
+    int2 tl = make_int2(-1, 0);
+    for (int u = u0; u < u1; ++u, ++v) {
+      const int s = v % ST;
+      bool ok = true;
+      if (u / nsub != tile) {
+        tile = u / nsub;
+        tl = __ldcg(a.tiles + tile);
+        if (tl.x >= 0) {
+          ok = wait_ab(&h_full[hn % HB], (hn / HB) & 1, abort, status);
+          ++hn;
+        }
+      }
+      if (tl.x < 0) continue;
+      const int b = m & 1, hb = (hn - 1) % HB;
+      ok = ok && (m < 2 || wait_ab(&acc_empty[b], ((m / 2) - 1) & 1, abort, status));
+      ok = ok && wait_ab(&full[s], (v / ST) & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t wsm = base + s * stage + 2 * BOX, hs = hbase + hb * hbytes, acc = tmem + b * 128;
+        uint32_t on = 0;
+        for (int p = 0; p < 2; ++p)
+          for (int ks = 0; ks < a.Rp / 16; ++ks) {
+            const uint64_t ad = sw128_desc(hs + (p * nbox + (ks >> 2)) * BOX) + (uint64_t)((ks & 3) * 2);
+            const uint64_t bd = GRAD ? sw128_desc_mn(wsm + ks * 2048, a.Rp * 128)
+                                     : sw128_desc(wsm + (ks >> 2) * BOX) + (uint64_t)((ks & 3) * 2);
+            tc_mma(acc, ad, bd, idesc, on);
+            on = 1;
+          }
+        tc_commit(&acc_full[b]);
+        if (u + 1 == u1 || (u + 1) / nsub != tile) tc_commit(&h_empty[hb]);
+      }
+      __syncwarp();
+      ++m;
+    }
+    for (int r = (m > 2 ? m - 2 : 0); r < m; ++r) mbar_drain(&acc_full[r & 1], (r / 2) & 1);
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2, r = q * 32 + lane;
+    int v = 0, m = 0, tile = -1, tok = 0;
+    int2 tl = make_int2(-1, 0);
+    for (int u = u0; u < u1; ++u, ++v) {
+      const int s = v % ST, col = (u % nsub) * 128 + half * 64;
+      if (u / nsub != tile) {
+        tile = u / nsub;
+        tl = __ldcg(a.tiles + tile);
+        tok = __ldcg(a.rowmap + tile * TM + r);
+      }
+      const bool mma = tl.x >= 0;
+      const int b = m & 1;
+      bool ok = wait_ab(&full[s], (v / ST) & 1, abort, status);
+      ok = ok && (!mma || wait_ab(&acc_full[b], (m / 2) & 1, abort, status));
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      uint8_t* yrow = basep + s * stage + half * BOX + r * 128;
+      const bool live = q * 32 < tl.y && col < D;  // this warp's rows and columns hold something
+      if (live) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+          if (mma) {
+            tc_ld16(tmem + b * 128 + half * 64 + c * 16 + ((uint32_t)(q * 32) << 16), w);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint4* p = reinterpret_cast<uint4*>(yrow + (((2 * c + j) ^ (r & 7)) << 4));
+            uint4 y = make_uint4(0u, 0u, 0u, 0u);
+            if (a.in) y = *p;
+            const uint32_t* d = w + 8 * j;
+            y.x = f2b2(bf16lo(y.x) + __uint_as_float(d[0]), bf16hi(y.x) + __uint_as_float(d[1]));
+            y.y = f2b2(bf16lo(y.y) + __uint_as_float(d[2]), bf16hi(y.y) + __uint_as_float(d[3]));
+            y.z = f2b2(bf16lo(y.z) + __uint_as_float(d[4]), bf16hi(y.z) + __uint_as_float(d[5]));
+            y.w = f2b2(bf16lo(y.w) + __uint_as_float(d[6]), bf16hi(y.w) + __uint_as_float(d[7]));
+            *p = y;
+          }
+        }
+      }
+      if (mma) {  // the accumulator is free for the MMAs
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[b]);
+        ++m;
+      }
+      __syncwarp();
+      if (live) {
+        const int cc = lane & 7, c = col + cc * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = i * 4 + (lane >> 3), row = q * 32 + rr;
+          const int t = __shfl_sync(0xffffffffu, tok, rr);
+          const uint4 y = lds128(basep + s * stage + half * BOX + row * 128 + ((cc ^ (row & 7)) << 4));
+          if (row < tl.y && c < D) *reinterpret_cast<uint4*>(a.out + t * a.ldo + c) = y;
+        }
+      }
+      fence_proxy_async();  // these accesses come before the next TMA write of the stage
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free(tmem, 256);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Weights' gradients: for a chunk of one adapter's tiles and a 128-wide slab of K
+// (dA) or of N (dB), [slab x tokens] times [tokens x R] on the tensor cores. Both
+// operands lie with the reduction (the tokens) as rows, so both are MN-major and
+// x, dy, g, h are used as they lie in memory. A chunk that is its adapter's only
+// one writes bf16 itself; the others leave FP32 partial sums, which k_lora_dw_sum
+// adds in chunk order.
+//   warp 0 TMA, warp 1 MMA, warps 2-5 epilogue (a thread is one column of the slab)
+// ---------------------------------------------------------------------------
+constexpr int DW_THREADS = 192;
+__host__ __device__ inline int dw_stages(int R) { return R > 64 ? 2 : 3; }
+__host__ __device__ inline int dw_stage_bytes(int R) { return 2 * HALF + (R > 64 ? 4 : 2) * HALF; }
+__host__ __device__ inline size_t dw_smem(int R) { return 1024 + (size_t)dw_stages(R) * dw_stage_bytes(R); }
+
+__global__ void __launch_bounds__(DW_THREADS) k_lora_dw(const Args a, const __grid_constant__ Maps maps) {
+  extern __shared__ uint8_t dsmem[];
+  __shared__ uint64_t full[3], empty[3], acc_full;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
+  volatile int* abort = &abort_flag;
+  int* status = a.hdr + H_STATUS;
+  const int ST = dw_stages(a.R), stage = dw_stage_bytes(a.R), nbox = a.R > 64 ? 2 : 1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&acc_full, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  const int slab = blockIdx.x;
+  if ((int)blockIdx.y >= __ldcg(a.hdr + H_CHUNKS)) return;
+  const int4 ch = __ldcg(a.chunks + blockIdx.y);
+  const bool is_b = slab >= a.slabs_a;
+  const int D = is_b ? a.N : a.K, col0 = (is_b ? slab - a.slabs_a : slab) * 128;
+  const int last = __ldcg(a.tiles + ch.y + ch.z - 1).y;
+  const int steps = 2 * (ch.z - 1) + (last > 64 ? 2 : 1);  // half tiles of 64 tokens
+  const uint32_t cols = tmem_cols(a.Rp);
+  if (warp == 1) tmem_alloc(&tmem_base, cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const int boxes = col0 + 64 < D ? 2 : 1;
+  if (warp == 0) {
+    const size_t plane = (size_t)a.max_tiles * TM;
+    const CUtensorMap* xm = is_b ? &maps.dy : &maps.x;
+    const CUtensorMap* gm = is_b ? &maps.h : &maps.g;
+    int i = 0;
+    for (; i < steps; ++i) {
+      const int s = i % ST, row0 = ch.y * TM + i * 64;
+      // lane l: four rows of the half tile, for the 64-column half l / 16
+      const int4 rows = __ldcg(reinterpret_cast<const int4*>(a.rowmap + row0) + (lane & 15));
+      const bool ok = i < ST || wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint32_t xs = base + s * stage, gs = xs + 2 * HALF;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[s], (uint32_t)(boxes * HALF + 2 * nbox * HALF));
+        for (int p = 0; p < 2; ++p)
+          for (int x = 0; x < nbox; ++x)
+            tma_load_2d(gs + (p * nbox + x) * HALF, gm, x * 64, (int)(p * plane) + row0, &full[s]);
+      }
+      __syncwarp();
+      if ((lane >> 4) < boxes)
+        tma_gather4(xs + (lane >> 4) * HALF + (lane & 15) * 512, xm, col0 + (lane >> 4) * 64, rows, &full[s]);
+    }
+    for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&full[r % ST], (r / ST) & 1);
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_f32acc(TM, a.Rp, true) | IDESC_A_MN | IDESC_B_MN;
+    int i = 0;
+    for (; i < steps; ++i) {
+      const int s = i % ST;
+      const bool ok = wait_ab(&full[s], (i / ST) & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t xs = base + s * stage, gs = xs + 2 * HALF;
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc_mma(tmem, sw128_desc_mn(xs + ks * 2048, HALF), sw128_desc_mn(gs + p * nbox * HALF + ks * 2048, HALF), idesc,
+                   (i > 0 || p > 0 || ks > 0) ? 1u : 0u);
+        tc_commit(&empty[s]);
+        if (i == steps - 1) tc_commit(&acc_full);
+      }
+      __syncwarp();
+    }
+    for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&empty[r % ST], (r / ST) & 1);
+  } else {
+    bool ok = wait_ab(&acc_full, 0, abort, status);
+    ok = __all_sync(0xffffffffu, ok);
+    const int q = warp & 3, col = col0 + q * 32 + lane;
+    if (ok && col0 + q * 32 < D) {
+      tc_fence_after();
+      float* part = ch.w >= 0 ? a.part + (size_t)ch.w * a.R * (a.K + a.N) + (is_b ? (size_t)a.R * a.K : 0) : nullptr;
+      uint16_t* out = is_b ? a.dB + (size_t)ch.x * a.N * a.R : a.dA + (size_t)ch.x * a.R * a.K;
+      for (int c = 0; c < a.Rp; c += 16) {
+        uint32_t v[16];
+        tc_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+        if (col >= D) continue;
+        if (is_b) {  // [N][R]: a thread's row
+#pragma unroll
+          for (int j = 0; j < 16; j += 8) {
+            if (c + j >= a.R) break;
+            const size_t at = (size_t)col * a.R + c + j;
+            if (part) {
+              *reinterpret_cast<uint4*>(part + at) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+              *reinterpret_cast<uint4*>(part + at + 4) = make_uint4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
+            } else {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[e] = f2b2(__uint_as_float(v[j + 2 * e]), __uint_as_float(v[j + 2 * e + 1]));
+              *reinterpret_cast<uint4*>(out + at) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+        } else {  // [R][K]: a warp's 32 neighbours of each rank row
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (c + j >= a.R) break;
+            const size_t at = (size_t)(c + j) * a.K + col;
+            if (part)
+              part[at] = __uint_as_float(v[j]);
+            else
+              out[at] = f2b(__uint_as_float(v[j]));
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free(tmem, cols);
+  }
+}
+
+// Gradients of the adapters with several chunks (their partial sums, in chunk order) or none (zero).
+__global__ void __launch_bounds__(256) k_lora_dw_sum(const Args a) {
+  pdl_wait();
+  const int2 of = __ldcg(a.of_adapter + blockIdx.y);
+  if (of.y == 1) return;
+  const size_t na = (size_t)a.R * a.K, all = na + (size_t)a.N * a.R;
+  const float* p = a.part + (size_t)of.x * all;
+  uint16_t* dA = a.dA + blockIdx.y * na;
+  uint16_t* dB = a.dB + blockIdx.y * (all - na);
+  for (size_t e = 8 * ((size_t)blockIdx.x * 256 + threadIdx.x); e < all; e += (size_t)gridDim.x * 2048) {
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < of.y; ++c) {
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(p + c * all + e));
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p + c * all + e) + 1);
+      s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w;
+      s[4] += v.x, s[5] += v.y, s[6] += v.z, s[7] += v.w;
+    }
+    const uint4 o = make_uint4(f2b2(s[0], s[1]), f2b2(s[2], s[3]), f2b2(s[4], s[5]), f2b2(s[6], s[7]));
+    *reinterpret_cast<uint4*>(e < na ? dA + e : dB + (e - na)) = o;  // R K is a multiple of 8: no piece straddles
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Up to 32 rows.
+// ---------------------------------------------------------------------------
+struct SArgs {
   int K, N, R, n, T;
   const uint16_t* A;
   const uint16_t* B;
@@ -29,19 +763,13 @@ struct Args {
   int64_t ldo;
   float* h;  // [T][R]
   float* g;  // [T][R]
-  uint16_t* dA;
-  uint16_t* dB;
 };
 
 __device__ __forceinline__ float b2f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-__device__ __forceinline__ uint16_t f2b(float v) {
-  const __nv_bfloat16 o = __float2bfloat16_rn(v);
-  return *reinterpret_cast<const uint16_t*>(&o);
-}
 
 // One warp per (token, rank): h = s A x, or with GRAD g = s B^T dy.
 template <bool GRAD>
-__global__ void __launch_bounds__(256) k_lora_shrink(const Args p) {
+__global__ void __launch_bounds__(256) k_small_shrink(const SArgs p) {
   const int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (u >= (int64_t)p.T * p.R) return;
@@ -60,7 +788,7 @@ __global__ void __launch_bounds__(256) k_lora_shrink(const Args p) {
 }
 
 template <bool GRAD>
-__global__ void __launch_bounds__(256) k_lora_expand(const Args p) {
+__global__ void __launch_bounds__(256) k_small_expand(const SArgs p) {
   const int D = GRAD ? p.K : p.N;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < (int64_t)p.T * D; u += (int64_t)gridDim.x * 256) {
     const int t = (int)(u / D), c = (int)(u % D), a = p.adapter[t];
@@ -71,26 +799,6 @@ __global__ void __launch_bounds__(256) k_lora_expand(const Args p) {
                     : p.h[(int64_t)t * p.R + r] * b2f(p.B[((int64_t)a * p.N + c) * p.R + r]);
     const float base = p.in32 ? p.in32[u] : (p.in ? b2f(p.in[t * p.ldo + c]) : 0.f);
     p.out[t * p.ldo + c] = f2b(base + acc);
-  }
-}
-
-// dA (threads over [n][R][K]) and dB (over [n][N][R]).
-__global__ void __launch_bounds__(256) k_lora_dw(const Args p) {
-  const int64_t na = (int64_t)p.n * p.R * p.K, nb = (int64_t)p.n * p.N * p.R;
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < na + nb; u += (int64_t)gridDim.x * 256) {
-    float acc = 0.f;
-    if (u < na) {
-      const int k = (int)(u % p.K), r = (int)(u / p.K % p.R), a = (int)(u / p.K / p.R);
-      for (int t = 0; t < p.T; ++t)
-        if (p.adapter[t] == a) acc += p.g[(int64_t)t * p.R + r] * b2f(p.x[t * p.ldx + k]);
-      p.dA[u] = f2b(acc);
-    } else {
-      const int64_t v = u - na;
-      const int r = (int)(v % p.R), n = (int)(v / p.R % p.N), a = (int)(v / p.R / p.N);
-      for (int t = 0; t < p.T; ++t)
-        if (p.adapter[t] == a) acc += p.h[(int64_t)t * p.R + r] * b2f(p.dy[t * p.lddy + n]);
-      p.dB[v] = f2b(acc);
-    }
   }
 }
 
@@ -129,21 +837,71 @@ flint_moe_status check_pool(const flint_lora* l) {
   return FLINT_MOE_OK;
 }
 
+constexpr int SMALL_T = 32;  // calls of up to this many tokens take the kernels for few rows
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    n = 152;
+  return n;
+}
+
+// Tiles at most: full ones, and a part-filled one for each group of tokens.
+int tiles_most(const flint_lora* l, int T) { return T / TM + std::min(l->num_adapters + 1, T); }
+
+// Tiles of a chunk of the weights' gradients, so that slabs x chunks fill the SMs about
+// four times (two CTAs of an SM, twice).
+constexpr int DW_CTAS = 152 * 4;
+int slabs(const flint_lora* l) { return (l->in_dim + 127) / 128 + (l->out_dim + 127) / 128; }
+int chunk_tiles(const flint_lora* l, int T) {
+  return std::max(1, (int)(((int64_t)T / TM * slabs(l) + DW_CTAS - 1) / DW_CTAS));
+}
+// Partial sums are kept for adapters of more than one chunk: those have more than CT 128 tokens, so there are
+// m <= T / (128 CT) of them, with at most T / 128 + m tiles and so (T / 128 + m) / CT + m chunks.
+int64_t slots_most(const flint_lora* l, int T) {
+  const int CT = chunk_tiles(l, T), m = T / (TM * CT);
+  return (T / TM + m) / CT + m;
+}
+
 struct WsPlan {
-  size_t h, g, y32, total;
+  size_t tiles, rowmap, h, g, chunks, of_adapter, part, y32, total;
 };
+// The workspace of a call of T tokens: a header, then 256-byte aligned regions.
 WsPlan ws_plan(const flint_lora* l, int T, bool grad, bool base) {
-  WsPlan w;
-  size_t o = 0;
-  w.h = o;    o = ws_align(o + sizeof(float) * (size_t)T * l->rank);
-  w.g = o;    o = ws_align(o + (grad ? sizeof(float) * (size_t)T * l->rank : 0));
-  w.y32 = o;  o = ws_align(o + (base ? sizeof(float) * (size_t)T * l->out_dim : 0));
+  WsPlan w = {};
+  size_t o = 256;
+  if (T <= SMALL_T && !grad) {
+    w.h = o;    o = ws_align(o + sizeof(float) * (size_t)T * l->rank);
+    w.y32 = o;  o = ws_align(o + (base ? sizeof(float) * (size_t)T * l->out_dim : 0));
+    w.total = o;
+    return w;
+  }
+  const size_t mt = tiles_most(l, T), plane = 2 * mt * TM * l->rank * 2;
+  w.tiles = o;   o = ws_align(o + sizeof(int2) * mt);
+  w.rowmap = o;  o = ws_align(o + sizeof(int) * mt * TM);
+  w.h = o;       o = ws_align(o + plane);
+  if (grad) {
+    w.g = o;           o = ws_align(o + plane);
+    w.chunks = o;      o = ws_align(o + sizeof(int4) * mt);
+    w.of_adapter = o;  o = ws_align(o + sizeof(int2) * l->num_adapters);
+    w.part = o;        o = ws_align(o + sizeof(float) * (size_t)slots_most(l, T) * l->rank * (l->in_dim + l->out_dim));
+  }
   w.total = o;
   return w;
 }
 
-Args make_args(const flint_lora* l, const int32_t* adapter, int T) {
-  Args p = {};
+// What a workspace for up to T tokens must hold: the partial sums of a shorter call can be more (its chunks are
+// shorter), by a count that never passes 3 T / 128, nor 3 DW_CTAS / slabs + 8.
+size_t ws_most(const flint_lora* l, int T, bool grad, bool base) {
+  size_t most = ws_plan(l, T, grad, base).total;
+  if (!grad) return std::max(most, ws_plan(l, std::min(T, SMALL_T), false, base).total);
+  const int64_t slots = std::min<int64_t>(3 * (T / TM), 3 * (DW_CTAS / slabs(l)) + 8);
+  const int64_t more = slots - slots_most(l, T);
+  return most + (more > 0 ? ws_align((size_t)more * sizeof(float) * l->rank * (l->in_dim + l->out_dim)) : 0);
+}
+
+SArgs small_args(const flint_lora* l, const int32_t* adapter, int T) {
+  SArgs p = {};
   p.K = l->in_dim;
   p.N = l->out_dim;
   p.R = l->rank;
@@ -154,6 +912,105 @@ Args make_args(const flint_lora* l, const int32_t* adapter, int T) {
   p.scale = l->scale;
   p.adapter = adapter;
   return p;
+}
+
+Args tile_args(const flint_lora* l, const int32_t* adapter, int T, uint8_t* ws, const WsPlan& w) {
+  Args p = {};
+  p.K = l->in_dim;
+  p.N = l->out_dim;
+  p.R = l->rank;
+  p.Rp = (l->rank + 15) & ~15;
+  p.n = l->num_adapters;
+  p.T = T;
+  p.scale = l->scale;
+  p.adapter = adapter;
+  p.max_tiles = tiles_most(l, T);
+  p.hdr = reinterpret_cast<int*>(ws);
+  p.tiles = reinterpret_cast<int2*>(ws + w.tiles);
+  p.rowmap = reinterpret_cast<int*>(ws + w.rowmap);
+  p.h = reinterpret_cast<uint16_t*>(ws + w.h);
+  p.CT = 1;
+  return p;
+}
+
+// Rows of `cols` bf16 values ld apart, gathered four at a time.
+bool map_rows(CUtensorMap* m, const uint16_t* p, int cols, int64_t ld, int rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {BK, 1};
+  return encode_bf16(m, p, 2, dims, strides, box);
+}
+// A pool [n][rows][cols] in boxes of 64 columns x brows rows of one adapter: what lies past an adapter's rows
+// reads as zero, not as the next adapter's.
+bool map_pool(CUtensorMap* m, const uint16_t* p, int cols, int rows, int n, int brows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * rows * 2};
+  const cuuint32_t box[3] = {BK, (cuuint32_t)brows, 1};
+  return encode_bf16(m, p, 3, dims, strides, box);
+}
+bool map_low(CUtensorMap* m, const uint16_t* p, int R, int max_tiles) {
+  const cuuint64_t dims[2] = {(cuuint64_t)R, (cuuint64_t)2 * max_tiles * TM};
+  const cuuint64_t strides[1] = {(cuuint64_t)R * 2};
+  const cuuint32_t box[2] = {BK, 64};
+  return encode_bf16(m, p, 2, dims, strides, box);
+}
+
+// Opts a kernel in to its dynamic shared memory, once for each device.
+template <typename K>
+bool want_smem(K kernel, std::atomic<uint64_t>& done, size_t smem) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return false;
+  if ((done.load() >> dev) & 1) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
+  done.fetch_or((uint64_t)1 << dev);
+  return true;
+}
+
+// A launch that may start while the kernel before it drains (each kernel waits for it itself), in clusters of `cx`.
+template <typename... P>
+bool launch(void (*kernel)(P...), dim3 grid, int block, size_t smem, int cx, cudaStream_t stream, const P&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cx;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cx > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+std::atomic<uint64_t> g_plan{0}, g_shrink{0}, g_expand{0}, g_expand_grad{0}, g_dw{0};
+constexpr size_t SMEM_MOST = 227 * 1024;
+
+bool run_plan(const Args& p, cudaStream_t stream) {
+  return want_smem(k_lora_plan, g_plan, plan_smem(FLINT_LORA_MAX_ADAPTERS)) &&
+         launch(k_lora_plan, dim3(1), 1024, plan_smem(p.n), 0, stream, p);
+}
+
+// h (and with `grads` g) of every tile. CTAs of a tile's cluster: as many as keep two CTAs on every SM busy, were
+// the tiles half filled on average, and no more than a CTA has k-blocks to take.
+bool run_shrink(const Args& p, const Maps& m, bool grads, cudaStream_t stream) {
+  const int kb = (std::min(p.K, grads ? p.N : p.K) + BK - 1) / BK, per = p.max_tiles * (grads ? 2 : 1);
+  int S = 1;
+  while (S < 8 && per * S * 2 <= 4 * sm_count() && S * 2 <= kb) S *= 2;
+  return want_smem(k_lora_shrink, g_shrink, shrink_smem(FLINT_LORA_MAX_RANK)) &&
+         launch(k_lora_shrink, dim3(S, p.max_tiles, grads ? 2 : 1), SHR_THREADS, shrink_smem(p.R), S, stream, p, m);
+}
+
+template <bool GRAD>
+bool run_expand(const Args& p, const Maps& m, cudaStream_t stream) {
+  const int D = GRAD ? p.K : p.N;
+  const int64_t items = (int64_t)p.max_tiles * ((D + 127) / 128);
+  return want_smem(k_lora_expand<GRAD>, GRAD ? g_expand_grad : g_expand, SMEM_MOST - 1024) &&
+         launch(k_lora_expand<GRAD>, dim3((unsigned)std::min<int64_t>(sm_count(), items)), EXP_THREADS, exp_smem(p.R), 0,
+                stream, p, m);
 }
 
 int blocks(int64_t threads) { return (int)std::min<int64_t>(152 * 16, (threads + 255) / 256); }
@@ -171,17 +1028,17 @@ extern "C" flint_moe_status flint_lora_init(int32_t in_dim, int32_t out_dim, int
 
 extern "C" size_t flint_lora_workspace_bytes(const flint_lora* l, int32_t max_tokens) {
   if (check_lora(l) != FLINT_MOE_OK || max_tokens < 1 || max_tokens > FLINT_LORA_MAX_TOKENS) return 0;
-  return ws_plan(l, max_tokens, false, false).total;
+  return ws_most(l, max_tokens, false, false);
 }
 
 extern "C" size_t flint_gemv_lora_workspace_bytes(const flint_lora* l, int32_t max_batch) {
   if (check_lora(l) != FLINT_MOE_OK || max_batch < 1 || max_batch > MAX_BATCH) return 0;
-  return ws_plan(l, max_batch, false, true).total;
+  return ws_most(l, max_batch, false, true);
 }
 
 extern "C" size_t flint_lora_backward_workspace_bytes(const flint_lora* l, int32_t max_tokens) {
   if (check_lora(l) != FLINT_MOE_OK || max_tokens < 1 || max_tokens > FLINT_LORA_MAX_TOKENS) return 0;
-  return ws_plan(l, max_tokens, true, false).total;
+  return ws_most(l, max_tokens, true, false);
 }
 
 extern "C" flint_moe_status flint_lora_apply(const flint_lora* l, const uint16_t* x, int64_t ldx, const int32_t* adapter,
@@ -200,16 +1057,34 @@ extern "C" flint_moe_status flint_lora_apply(const flint_lora* l, const uint16_t
     return FLINT_MOE_EINVAL;
   const WsPlan w = ws_plan(l, T, false, false);
   if (ws_bytes < w.total) return FLINT_MOE_EINVAL;
-  Args p = make_args(l, adapter, T);
-  p.x = x;
-  p.ldx = ldx;
+  uint8_t* wb = static_cast<uint8_t*>(ws);
+  if (T <= SMALL_T) {
+    SArgs p = small_args(l, adapter, T);
+    p.x = x;
+    p.ldx = ldx;
+    p.in = y_in;
+    p.out = y_out;
+    p.ldo = ldy;
+    p.h = reinterpret_cast<float*>(wb + w.h);
+    k_small_shrink<false><<<(int)(((int64_t)T * p.R + 7) / 8), 256, 0, stream>>>(p);
+    k_small_expand<false><<<blocks((int64_t)T * p.N), 256, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
+  }
+  Args p = tile_args(l, adapter, T, wb, w);
+  p.with_none = y_in != y_out;
   p.in = y_in;
   p.out = y_out;
   p.ldo = ldy;
-  p.h = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.h);
-  k_lora_shrink<false><<<(int)(((int64_t)T * p.R + 7) / 8), 256, 0, stream>>>(p);
-  k_lora_expand<false><<<blocks((int64_t)T * p.N), 256, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
+  Maps m;
+  if (!map_rows(&m.x, x, p.K, ldx, T) || !map_rows(&m.in, y_in ? y_in : y_out, p.N, ldy, T) ||
+      !map_pool(&m.a, l->a, p.K, p.R, p.n, p.Rp) || !map_pool(&m.b, l->b, p.R, p.N, p.n, TM) ||
+      !map_low(&m.h, p.h, p.R, p.max_tiles))
+    return FLINT_MOE_ECUDA;
+  m.dy = m.x;
+  m.b64 = m.b;
+  m.g = m.h;
+  return run_plan(p, stream) && run_shrink(p, m, false, stream) && run_expand<false>(p, m, stream) ? FLINT_MOE_OK
+                                                                                                   : FLINT_MOE_ECUDA;
 }
 
 extern "C" flint_moe_status flint_gemv_lora(const void* packed, int32_t N, int32_t K, int32_t fmt, const uint16_t* x,
@@ -225,7 +1100,7 @@ extern "C" flint_moe_status flint_gemv_lora(const void* packed, int32_t N, int32
   if (overlap(y, N, N, x, K, K, B)) return FLINT_MOE_EINVAL;
   const WsPlan w = ws_plan(l, B, false, true);
   if (ws_bytes < w.total) return FLINT_MOE_EINVAL;
-  Args p = make_args(l, adapter, B);
+  SArgs p = small_args(l, adapter, B);
   p.x = x;
   p.ldx = K;
   float* y32 = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.y32);
@@ -235,8 +1110,8 @@ extern "C" flint_moe_status flint_gemv_lora(const void* packed, int32_t N, int32
   p.h = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.h);
   st = gemv_impl(packed, N, K, fmt, x, B, y, y32, nullptr, 0.f, dev_status, stream);
   if (st != FLINT_MOE_OK) return st;
-  k_lora_shrink<false><<<(int)(((int64_t)B * p.R + 7) / 8), 256, 0, stream>>>(p);
-  k_lora_expand<false><<<blocks((int64_t)B * p.N), 256, 0, stream>>>(p);
+  k_small_shrink<false><<<(int)(((int64_t)B * p.R + 7) / 8), 256, 0, stream>>>(p);
+  k_small_expand<false><<<blocks((int64_t)B * p.N), 256, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
 }
 
@@ -267,22 +1142,37 @@ extern "C" flint_moe_status flint_lora_backward(const flint_lora* l, const uint1
     return FLINT_MOE_EINVAL;
   const WsPlan w = ws_plan(l, T, true, false);
   if (ws_bytes < w.total) return FLINT_MOE_EINVAL;
-  Args p = make_args(l, adapter, T);
-  p.x = x;
-  p.ldx = ldx;
-  p.dy = dy;
-  p.lddy = lddy;
+  Args p = tile_args(l, adapter, T, static_cast<uint8_t*>(ws), w);
+  p.with_none = dx_out && dx_in != dx_out;
+  p.g = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + w.g);
   p.in = dx_in;
   p.out = dx_out;
   p.ldo = lddx;
-  p.h = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.h);
-  p.g = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.g);
+  p.CT = chunk_tiles(l, T);
+  p.slabs_a = (p.K + 127) / 128;
+  p.slabs_b = (p.N + 127) / 128;
+  p.chunks = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + w.chunks);
+  p.of_adapter = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + w.of_adapter);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part);
   p.dA = da;
   p.dB = db;
-  const int sg = (int)(((int64_t)T * p.R + 7) / 8);
-  k_lora_shrink<false><<<sg, 256, 0, stream>>>(p);
-  k_lora_shrink<true><<<sg, 256, 0, stream>>>(p);
-  if (dx_out) k_lora_expand<true><<<blocks((int64_t)T * p.K), 256, 0, stream>>>(p);
-  k_lora_dw<<<blocks((int64_t)nw * (p.K + p.N)), 256, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
+  Maps m;
+  if (!map_rows(&m.x, x, p.K, ldx, T) || !map_rows(&m.dy, dy, p.N, lddy, T) ||
+      !map_rows(&m.in, dx_in ? dx_in : (dx_out ? dx_out : x), p.K, dx_out ? lddx : ldx, T) ||
+      !map_pool(&m.a, l->a, p.K, p.R, p.n, p.Rp) || !map_pool(&m.b64, l->b, p.R, p.N, p.n, 64) ||
+      !map_low(&m.h, p.h, p.R, p.max_tiles) || !map_low(&m.g, p.g, p.R, p.max_tiles))
+    return FLINT_MOE_ECUDA;
+  m.b = m.b64;
+  if (!run_plan(p, stream) || !run_shrink(p, m, true, stream)) return FLINT_MOE_ECUDA;
+  if (dx_out && !run_expand<true>(p, m, stream)) return FLINT_MOE_ECUDA;
+  // chunks: the tiles of adapters in runs of CT, and a shorter run for each adapter
+  const int chunks = p.max_tiles / p.CT + std::min(p.n, T) + 1;
+  if (!want_smem(k_lora_dw, g_dw, dw_smem(FLINT_LORA_MAX_RANK)) ||
+      !launch(k_lora_dw, dim3(p.slabs_a + p.slabs_b, std::min(chunks, p.max_tiles)), DW_THREADS, dw_smem(p.R), 0, stream, p, m))
+    return FLINT_MOE_ECUDA;
+  const int64_t all = (int64_t)p.R * (p.K + p.N);
+  if (!launch(k_lora_dw_sum, dim3((unsigned)std::min<int64_t>((all + 2047) / 2048, std::max(1, 152 * 8 / p.n)), p.n), 256, 0, 0,
+              stream, p))
+    return FLINT_MOE_ECUDA;
+  return FLINT_MOE_OK;
 }

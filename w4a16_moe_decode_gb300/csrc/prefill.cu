@@ -27,10 +27,9 @@
 #include <atomic>
 #include <cmath>
 
-#include <cuda.h>  // CUtensorMap and its enums (types only; the encoder comes through the runtime)
-
 #include "common.cuh"
 #include "flint_moe_prefill.h"
+#include "tensor.cuh"
 
 namespace flint {
 namespace pf {
@@ -137,61 +136,8 @@ __device__ __forceinline__ T* ws_at(const PfArgs& a, size_t off) {
 }
 
 // ---------------------------------------------------------------------------
-// tcgen05 / cp.async helpers.
+// cp.async helpers (the tcgen05 and TMA ones are in tensor.cuh).
 // ---------------------------------------------------------------------------
-
-// Shared-memory matrix descriptor for a K-major operand in the 128-byte
-// swizzle layout: 8-row x 128-byte atoms (row r of an atom at r * 128, its
-// 16-byte chunk c at chunk position c ^ r), atoms stacked along M/N every
-// 1024 bytes (stride byte offset). Fields: start address >> 4 (bits 0-13),
-// leading byte offset >> 4 (16-29; unused for swizzled K-major, set to 1),
-// stride byte offset >> 4 (32-45), descriptor version 1 (46-47), base offset 0
-// (atoms are 1024-byte aligned), layout type 2 = 128-byte swizzle (61-63).
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-// Instruction descriptor of kind::f16: D f32 (bits 4-5 = 1), A and B both
-// bf16 (bits 7-9 = 1, 10-12 = 1) or both f16 (0, 0), both K-major (bits 15,
-// 16 = 0), N >> 3 in bits 17-22, M >> 4 in bits 24-28.
-__device__ __forceinline__ uint32_t idesc_f32acc(int M, int N, bool bf16) {
-  const uint32_t t = bf16 ? 1u : 0u;
-  return (1u << 4) | (t << 7) | (t << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Arrives once on bar when every tcgen05 operation this thread issued so far has completed.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_addr(bar))
-               : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 16 consecutive 32-bit columns of this warp's 32 tensor-memory lanes.
-__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
 
 // 16-byte copy global -> shared; src_bytes 0 fills the 16 bytes with zeros.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
@@ -201,12 +147,6 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Byte offset of element (row r, column c) of a 64-column bf16 block stored
-// K-major with the 128-byte swizzle.
-__device__ __forceinline__ uint32_t sw128_off(int r, int c) {
-  return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((((c * 2) >> 4) ^ (r & 7)) << 4) + ((c * 2) & 15));
 }
 
 // bf16x2 -> f16x2 of the values times sc (a power of two).
@@ -267,20 +207,6 @@ struct GemmSmem {  // per pipeline
 
 constexpr size_t gemm_dyn_smem() { return 1024 + (size_t)NPIPE * PIPE_BYTES; }
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-// One lane of the (fully active) warp returns true.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred = 0;
-  asm volatile(
-      "{\n\t.reg .b32 rx;\n\t.reg .pred px;\n\telect.sync rx|px, %1;\n\t@px mov.s32 %0, 1;\n\t}"
-      : "+r"(pred)
-      : "r"(0xffffffffu));
-  return pred != 0;
-}
-
 __device__ __forceinline__ uint64_t l2_evict_first_policy() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
@@ -295,32 +221,6 @@ __device__ __forceinline__ void bulk_g2s_pol(uint32_t dst, const void* src, uint
           dst),
       "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(pol)
       : "memory");
-}
-
-// 2-D TMA tile load (box from the descriptor) into shared memory, completing on bar.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
-      : "memory");
-}
-
-// Bounded wait that also gives up as soon as another warp of the CTA has given up.
-__device__ __forceinline__ bool wait_ab(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63) == 63) {
-      if (*abort) return false;
-      if (global_ns() - t0 > WAIT_LIMIT_NS) {
-        atomicOr(status, FLINT_MOE_DEV_ERR_TIMEOUT);
-        *abort = 1;
-        return false;
-      }
-    }
-  }
 }
 
 struct TileInfo {
@@ -1236,24 +1136,6 @@ static int sm_count() {
     n.store(v);
   }
   return v;
-}
-
-// cuTensorMapEncodeTiled, reached through the runtime (no link against the driver library).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn tensor_map_encoder() {
-  static std::atomic<void*> fn{nullptr};
-  void* f = fn.load();
-  if (!f) {
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !f)
-      return nullptr;
-    fn.store(f);
-  }
-  return reinterpret_cast<EncodeTiledFn>(f);
 }
 
 // bf16 matrix [rows][cols] (row stride cols * 2 bytes), boxes of 64 columns x
