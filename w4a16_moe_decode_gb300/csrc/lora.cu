@@ -35,6 +35,10 @@ struct Args {
   int* rowmap;   // [max_tiles * 128]
   uint16_t* h;   // s A x as bf16 halves hi, lo: [2][max_tiles * 128][R]
   uint16_t* g;   // s B^T dy likewise
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* dy;
+  int64_t lddy;
   const uint16_t* in;  // y_in or dx_in, or null
   uint16_t* out;
   int64_t ldo;
@@ -49,11 +53,9 @@ struct Args {
 };
 
 struct Maps {
-  CUtensorMap x, dy;    // token rows, gathered: boxes of 64 columns x 1 row
-  CUtensorMap in;       // base rows, gathered
-  CUtensorMap a, b;     // A [n][R][K]: boxes 64 x Rp; B [n][N][R]: boxes 64 x 128
-  CUtensorMap b64;      // B, boxes 64 x 64
-  CUtensorMap h, g;     // [2 * max_tiles * 128][R], boxes 64 x 64
+  CUtensorMap a;     // A [n][R][K]: boxes 64 x Rp
+  CUtensorMap b;     // B [n][N][R]: boxes 64 x 64
+  CUtensorMap h, g;  // [2 * max_tiles * 128][R], boxes 64 x 64
 };
 
 __device__ __forceinline__ uint16_t f2b(float v) {
@@ -193,18 +195,24 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const Args a) {
 }
 
 // ---------------------------------------------------------------------------
+// Token rows come in any order, so they are gathered with 16-byte asynchronous
+// copies, eight lanes to a row's 128 bytes (TMA's four-row gather delivered one
+// such group every 50 to 60 ns and SM, 1.2 TB/s over the card, whatever the order).
+//
 // Shrink: h = s A x of one tile (z = 0) or g = s B^T dy (z = 1), [128 x D] times
 // [D x R] on the tensor cores. A cluster of S CTAs shares a tile; CTA s takes a
 // run of the 64-column k-blocks, and the partial sums meet in distributed shared
 // memory, added in CTA order. Bound by the token rows it reads: per k-block 16 KiB
 // of them against at most 16 KiB of weights from L2.
-//   warp 0     one TMA gather of four rows per lane and k-block, plus the weights
-//   warp 1     the MMAs (A stored [R][K] is K-major; B stored [N][R] has R
+//   warps 0-3  token rows into the stages; later the accumulator, tensor memory
+//              -> shared memory
+//   warp 4     the weights (TMA) and a stage's count of bytes
+//   warp 5     the MMAs (A stored [R][K] is K-major; B stored [N][R] has R
 //              contiguous, an MN-major operand: no transposed copy)
-//   warps 2-5  the accumulator, tensor memory -> shared memory
 // ---------------------------------------------------------------------------
 constexpr int SHR_STAGES = 4;
 constexpr int SHR_THREADS = 192;
+constexpr int LAG = SHR_STAGES - 1;  // stages in flight before the oldest is waited for
 
 __host__ __device__ inline int shrink_wbytes(int R) { return R > 64 ? 2 * HALF : HALF; }
 __host__ __device__ inline size_t shrink_smem(int R) { return 1024 + (size_t)SHR_STAGES * (BOX + shrink_wbytes(R)); }
@@ -219,7 +227,7 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
 }
 
-__global__ void __launch_bounds__(SHR_THREADS) k_lora_shrink(const Args a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, const __grid_constant__ Maps maps) {
   extern __shared__ uint8_t dsmem[];
   __shared__ uint64_t full[SHR_STAGES], empty[SHR_STAGES], acc_full;
   __shared__ uint32_t tmem_base;
@@ -231,7 +239,7 @@ __global__ void __launch_bounds__(SHR_THREADS) k_lora_shrink(const Args a, const
   int* status = a.hdr + H_STATUS;
   if (threadIdx.x == 0) {
     for (int s = 0; s < SHR_STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 5);  // four warps of token rows, the weights' expect-tx arrival
       mbar_init(&empty[s], 1);
     }
     mbar_init(&acc_full, 1);
@@ -248,40 +256,84 @@ __global__ void __launch_bounds__(SHR_THREADS) k_lora_shrink(const Args a, const
   const int S = gridDim.x, rank = blockIdx.x;
   const int D = grad ? a.N : a.K, KB = (D + BK - 1) / BK;
   const int kb0 = rank * KB / S, nkb = (rank + 1) * KB / S - kb0;
-  const int wbytes = shrink_wbytes(a.R), stage = BOX + wbytes;
+  const int stage = BOX + shrink_wbytes(a.R);
   const uint32_t cols = tmem_cols(a.Rp);
-  if (warp == 1) tmem_alloc(&tmem_base, cols);
+  if (warp == 5) tmem_alloc(&tmem_base, cols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  if (warp == 0) {
-    const int4 rows = __ldcg(reinterpret_cast<const int4*>(a.rowmap + tile * TM) + lane);
-    const int groups = (tl.y + 3) / 4;  // rows past the count stay as they are: a tensor-core row reads only itself
-    const CUtensorMap* xm = grad ? &maps.dy : &maps.x;
-    const uint32_t tx = groups * 512 + (grad ? (a.R > 64 ? 2 : 1) * HALF : a.Rp * 128);
+  float* part = reinterpret_cast<float*>(basep);
+  const int PP = a.Rp + 4;  // row pitch of the partial sums, padded by 16 bytes
+  if (warp < 4) {
+    const uint16_t* src = grad ? a.dy : a.x;
+    const int64_t ld = grad ? a.lddy : a.ldx;
+    const int c8 = (lane & 7) * 8;
+    const bool any = warp * 32 < tl.y;
+    const uint16_t* row[8];
+    uint32_t dst[2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      row[i] = src + __ldcg(a.rowmap + tile * TM + warp * 32 + i * 4 + (lane >> 3)) * ld + c8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) dst[i] = base + sw128_off(warp * 32 + i * 4 + (lane >> 3), c8);
     int i = 0;
-    for (; i < nkb; ++i) {
-      const int s = i % SHR_STAGES;
-      const bool ok = i < SHR_STAGES || wait_ab(&empty[s], ((i / SHR_STAGES) - 1) & 1, abort, status);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const int col = (kb0 + i) * BK;
-      const uint32_t xs = base + s * stage, wsm = xs + BOX;
-      if (lane == 0) {
+    for (; i < nkb + LAG; ++i) {
+      if (i < nkb) {
+        const int s = i % SHR_STAGES, col = (kb0 + i) * BK;
+        const bool ok = i < SHR_STAGES || wait_ab(&empty[s], ((i / SHR_STAGES) - 1) & 1, abort, status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (any) {
+          const bool in = col + c8 < D;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            cp_async16(dst[j & 1] + s * stage + (j >> 1) * 1024, row[j] + (in ? col : 0), in ? 16u : 0u);
+        }
+      }
+      cp_async_commit();
+      if (i >= LAG) {
+        cp_async_wait<LAG>();
+        fence_proxy_async();  // these copies -> visible to the tensor core
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[(i - LAG) % SHR_STAGES]);
+      }
+    }
+    cp_async_wait<0>();
+    // Every CTA's sums to its shared memory (the stages are free by then), [128][Rp].
+    bool ok = wait_ab(&acc_full, 0, abort, status);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok && any) {
+      tc_fence_after();
+      const int r = warp * 32 + lane;
+      for (int c = 0; c < a.Rp; c += 16) {
+        uint32_t v[16];
+        tc_ld16(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)c, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(part + r * PP + c + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      }
+      tc_fence_before();
+    }
+  } else if (warp == 4) {
+    const uint32_t tx = grad ? (a.R > 64 ? 2 : 1) * HALF : a.Rp * 128;
+    int i = 0;
+    if (lane == 0) {
+      for (; i < nkb; ++i) {
+        const int s = i % SHR_STAGES, col = (kb0 + i) * BK;
+        if (i >= SHR_STAGES && !wait_ab(&empty[s], ((i / SHR_STAGES) - 1) & 1, abort, status)) break;
+        const uint32_t wsm = base + s * stage + BOX;
         mbar_arrive_expect_tx(&full[s], tx);
         if (grad) {
-          tma_load_3d(wsm, &maps.b64, 0, col, tl.x, &full[s]);
-          if (a.R > 64) tma_load_3d(wsm + HALF, &maps.b64, 64, col, tl.x, &full[s]);
+          tma_load_3d(wsm, &maps.b, 0, col, tl.x, &full[s]);
+          if (a.R > 64) tma_load_3d(wsm + HALF, &maps.b, 64, col, tl.x, &full[s]);
         } else {
           tma_load_3d(wsm, &maps.a, col, 0, tl.x, &full[s]);
         }
       }
-      __syncwarp();
-      if (lane < groups) tma_gather4(xs + lane * 512, xm, col, rows, &full[s]);
+      // the CTA's memory must outlive every copy in flight
+      for (int r = (i > SHR_STAGES ? i - SHR_STAGES : 0); r < i; ++r) mbar_drain(&full[r % SHR_STAGES], (r / SHR_STAGES) & 1);
     }
-    // the CTA's memory must outlive every copy in flight
-    for (int r = (i > SHR_STAGES ? i - SHR_STAGES : 0); r < i; ++r) mbar_drain(&full[r % SHR_STAGES], (r / SHR_STAGES) & 1);
-  } else if (warp == 1) {
+  } else {
     const uint32_t idesc = idesc_f32acc(TM, a.Rp, true) | (grad ? IDESC_B_MN : 0u);
     int i = 0;
     for (; i < nkb; ++i) {
@@ -304,30 +356,8 @@ __global__ void __launch_bounds__(SHR_THREADS) k_lora_shrink(const Args a, const
     }
     for (int r = (i > SHR_STAGES ? i - SHR_STAGES : 0); r < i; ++r) mbar_drain(&empty[r % SHR_STAGES], (r / SHR_STAGES) & 1);
   }
-  // Every CTA's sums to its shared memory (the stages are free by then), [128][Rp] padded by 16 bytes a row.
-  const int PP = a.Rp + 4;
-  float* part = reinterpret_cast<float*>(basep);
-  bool ok = true;
-  if (warp >= 2) {
-    ok = wait_ab(&acc_full, 0, abort, status);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      tc_fence_after();
-      const int q = warp & 3, row = q * 32 + lane;
-      if (q * 32 < tl.y) {
-        for (int c = 0; c < a.Rp; c += 16) {
-          uint32_t v[16];
-          tc_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(part + row * PP + c + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        }
-      }
-      tc_fence_before();
-    }
-  }
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 5) {
     tc_fence_after();
     tmem_free(tmem, cols);
   }
@@ -366,41 +396,44 @@ __global__ void __launch_bounds__(SHR_THREADS) k_lora_shrink(const Args a, const
 // Expand: out = bf16(in + h B^T) (GRAD: in + g A), per tile [128 x R] times
 // [R x 128 columns] for both halves of h. The (tile, 128 columns) items are one
 // list, and each CTA takes a run of it, so that a tile's h is loaded once per run.
-// Bound by the base rows it reads and the rows it writes.
-//   warp 0     TMA: base rows (gathered, four rows a lane), weights, a tile's h
+// Bound by the base rows it reads and the rows it writes: those go through each
+// epilogue warp's own ring of shared memory (32 rows x 64 columns an item, up
+// to three items ahead), without any barrier.
+//   warp 0     weights and a tile's h (TMA)
 //   warp 1     the MMAs into two accumulators of 128 columns
-//   warps 2-9  tensor memory + base -> bf16 in place in shared memory -> rows
+//   warps 2-9  base rows (asynchronous copies); tensor memory + base -> bf16 in
+//              place in shared memory -> whole 128-byte pieces of rows
 // ---------------------------------------------------------------------------
 constexpr int EXP_THREADS = 320;
-__host__ __device__ inline int exp_stages(int R) { return R > 64 ? 2 : 3; }
+constexpr int YSLOT = 32 * 128;  // one warp's rows of an item
 __host__ __device__ inline int exp_hbufs(int R) { return R > 64 ? 1 : 2; }
-__host__ __device__ inline int exp_wbytes(int R) { return R > 64 ? 2 * BOX : BOX; }   // one stage's weights
+__host__ __device__ inline int exp_yslots(int R) { return R > 64 ? 3 : 4; }
+__host__ __device__ inline int exp_wbytes(int R) { return R > 64 ? 2 * BOX : BOX; }      // one stage's weights
 __host__ __device__ inline int exp_hbytes(int R) { return R > 64 ? 4 * BOX : 2 * BOX; }  // hi and lo of a tile
 __host__ __device__ inline size_t exp_smem(int R) {
-  return 1024 + (size_t)exp_stages(R) * (2 * BOX + exp_wbytes(R)) + (size_t)exp_hbufs(R) * exp_hbytes(R);
+  return 1024 + (size_t)2 * exp_wbytes(R) + (size_t)exp_hbufs(R) * exp_hbytes(R) + (size_t)exp_yslots(R) * 8 * YSLOT;
 }
 
-template <bool GRAD>
+template <bool GRAD, bool WIDE>  // WIDE: rank above 64
 __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, const __grid_constant__ Maps maps) {
   extern __shared__ uint8_t dsmem[];
-  __shared__ uint64_t full[3], empty[3], acc_full[2], acc_empty[2], h_full[2], h_empty[2];
+  __shared__ uint64_t full[2], empty[2], acc_full[2], acc_empty[2], h_full[2], h_empty[2];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
+  constexpr int ANY_R = WIDE ? 128 : 64;
+  constexpr int HB = WIDE ? 1 : 2, nbox = WIDE ? 2 : 1, YS = WIDE ? 3 : 4, LY = YS - 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
   uint8_t* const basep = dsmem + (base - smem_addr(dsmem));
   volatile int* abort = &abort_flag;
   int* status = a.hdr + H_STATUS;
-  const int ST = exp_stages(a.R), HB = exp_hbufs(a.R), nbox = a.R > 64 ? 2 : 1;
-  const int stage = 2 * BOX + exp_wbytes(a.R), hbytes = exp_hbytes(a.R);
-  const uint32_t hbase = base + ST * stage;
+  const int stage = exp_wbytes(ANY_R), hbytes = exp_hbytes(ANY_R);
+  const uint32_t hbase = base + 2 * stage, ybase = hbase + HB * hbytes;
   const int D = GRAD ? a.K : a.N, nsub = (D + 127) / 128;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 8);
-    }
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&full[b], 1);
+      mbar_init(&empty[b], 1);
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 8);
       mbar_init(&h_full[b], 1);
@@ -420,60 +453,51 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
   const int u0 = (int)(items * blockIdx.x / gridDim.x), u1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
   const size_t plane = (size_t)a.max_tiles * TM;
   if (warp == 0) {
-    int v = 0, hn = 0, tile = -1;  // items, h loads
-    int2 tl = make_int2(-1, 0);
-    int4 rows = make_int4(0, 0, 0, 0);
-    for (int u = u0; u < u1; ++u, ++v) {
-      const int s = v % ST, col = (u % nsub) * 128;
-      bool ok = true;
-      if (u / nsub != tile) {
-        tile = u / nsub;
-        tl = __ldcg(a.tiles + tile);
-        rows = __ldcg(reinterpret_cast<const int4*>(a.rowmap + tile * TM) + lane);
-        if (tl.x >= 0) {
-          const int b = hn % HB;
-          ok = hn < HB || wait_ab(&h_empty[b], ((hn / HB) - 1) & 1, abort, status);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          if (lane == 0) {
-            const CUtensorMap* m = GRAD ? &maps.g : &maps.h;
+    if (lane == 0) {
+      int m = 0, hn = 0, tile = -1;  // items with an adapter, h loads
+      int2 tl = make_int2(-1, 0);
+      for (int u = u0; u < u1; ++u) {
+        const int col = (u % nsub) * 128;
+        if (u / nsub != tile) {
+          tile = u / nsub;
+          tl = __ldcg(a.tiles + tile);
+          if (tl.x >= 0) {
+            const int b = hn % HB;
+            if (hn >= HB && !wait_ab(&h_empty[b], ((hn / HB) - 1) & 1, abort, status)) break;
+            const CUtensorMap* mp = GRAD ? &maps.g : &maps.h;
             mbar_arrive_expect_tx(&h_full[b], (uint32_t)hbytes);
             for (int p = 0; p < 2; ++p)
               for (int x = 0; x < nbox; ++x)
                 for (int y = 0; y < 2; ++y)
-                  tma_load_2d(hbase + b * hbytes + (p * nbox + x) * BOX + y * HALF, m, x * 64,
+                  tma_load_2d(hbase + b * hbytes + (p * nbox + x) * BOX + y * HALF, mp, x * 64,
                               (int)(p * plane) + tile * TM + y * 64, &h_full[b]);
-          }
-          ++hn;
-        }
-      }
-      ok = v < ST || wait_ab(&empty[s], ((v / ST) - 1) & 1, abort, status);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const uint32_t ys = base + s * stage, wsm = ys + 2 * BOX;
-      const int groups = a.in ? (tl.y + 3) / 4 : 0;
-      const int boxes = col + 64 < D ? 2 : 1;  // 64-column halves that hold columns at all
-      if (lane == 0) {
-        const uint32_t wtx = tl.x < 0 ? 0 : (GRAD ? boxes * a.Rp * 128 : nbox * BOX);
-        mbar_arrive_expect_tx(&full[s], (uint32_t)(groups * 512 * boxes) + wtx);
-        if (tl.x >= 0) {
-          if (GRAD) {
-            for (int y = 0; y < boxes; ++y) tma_load_3d(wsm + y * a.Rp * 128, &maps.a, col + 64 * y, 0, tl.x, &full[s]);
-          } else {
-            for (int x = 0; x < nbox; ++x) tma_load_3d(wsm + x * BOX, &maps.b, x * 64, col, tl.x, &full[s]);
+            ++hn;
           }
         }
+        if (tl.x < 0) continue;
+        const int s = m & 1;
+        if (m >= 2 && !wait_ab(&empty[s], ((m >> 1) - 1) & 1, abort, status)) break;
+        const uint32_t wsm = base + s * stage;
+        const int boxes = col + 64 < D ? 2 : 1;  // 64-column halves that hold columns at all
+        if (GRAD) {
+          mbar_arrive_expect_tx(&full[s], (uint32_t)(boxes * a.Rp * 128));
+          for (int y = 0; y < boxes; ++y) tma_load_3d(wsm + y * a.Rp * 128, &maps.a, col + 64 * y, 0, tl.x, &full[s]);
+        } else {
+          mbar_arrive_expect_tx(&full[s], (uint32_t)(boxes * nbox * HALF));
+          for (int x = 0; x < nbox; ++x)
+            for (int y = 0; y < boxes; ++y)
+              tma_load_3d(wsm + x * BOX + y * HALF, &maps.b, x * 64, col + 64 * y, tl.x, &full[s]);
+        }
+        ++m;
       }
-      __syncwarp();
-      if (lane < groups)
-        for (int y = 0; y < boxes; ++y) tma_gather4(ys + y * BOX + lane * 512, &maps.in, col + 64 * y, rows, &full[s]);
+      for (int r = (m > 2 ? m - 2 : 0); r < m; ++r) mbar_drain(&full[r & 1], (r >> 1) & 1);
+      for (int r = (hn > HB ? hn - HB : 0); r < hn; ++r) mbar_drain(&h_full[r % HB], (r / HB) & 1);
     }
-    for (int r = (v > ST ? v - ST : 0); r < v; ++r) mbar_drain(&full[r % ST], (r / ST) & 1);
-    for (int r = (hn > HB ? hn - HB : 0); r < hn; ++r) mbar_drain(&h_full[r % HB], (r / HB) & 1);
   } else if (warp == 1) {
     const uint32_t idesc = idesc_f32acc(TM, 128, true) | (GRAD ? IDESC_B_MN : 0u);
-    int v = 0, m = 0, hn = 0, tile = -1;  // items, accumulators, h loads
+    int m = 0, hn = 0, tile = -1;
     int2 tl = make_int2(-1, 0);
-    for (int u = u0; u < u1; ++u, ++v) {
-      const int s = v % ST;
+    for (int u = u0; u < u1; ++u) {
       bool ok = true;
       if (u / nsub != tile) {
         tile = u / nsub;
@@ -485,12 +509,12 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
       }
       if (tl.x < 0) continue;
       const int b = m & 1, hb = (hn - 1) % HB;
-      ok = ok && (m < 2 || wait_ab(&acc_empty[b], ((m / 2) - 1) & 1, abort, status));
-      ok = ok && wait_ab(&full[s], (v / ST) & 1, abort, status);
+      ok = ok && (m < 2 || wait_ab(&acc_empty[b], ((m >> 1) - 1) & 1, abort, status));
+      ok = ok && wait_ab(&full[b], (m >> 1) & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t wsm = base + s * stage + 2 * BOX, hs = hbase + hb * hbytes, acc = tmem + b * 128;
+        const uint32_t wsm = base + b * stage, hs = hbase + hb * hbytes, acc = tmem + b * 128;
         uint32_t on = 0;
         for (int p = 0; p < 2; ++p)
           for (int ks = 0; ks < a.Rp / 16; ++ks) {
@@ -500,77 +524,105 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
             tc_mma(acc, ad, bd, idesc, on);
             on = 1;
           }
+        tc_commit(&empty[b]);
         tc_commit(&acc_full[b]);
         if (u + 1 == u1 || (u + 1) / nsub != tile) tc_commit(&h_empty[hb]);
       }
       __syncwarp();
       ++m;
     }
-    for (int r = (m > 2 ? m - 2 : 0); r < m; ++r) mbar_drain(&acc_full[r & 1], (r / 2) & 1);
+    for (int r = (m > 2 ? m - 2 : 0); r < m; ++r) mbar_drain(&acc_full[r & 1], (r >> 1) & 1);
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2, r = q * 32 + lane;
-    int v = 0, m = 0, tile = -1, tok = 0;
+    const int q = warp & 3, half = (warp - 2) >> 2;  // tensor-memory lanes 32 q .., columns 64 half ..
+    const int rsub = lane >> 3, c8 = (lane & 7) * 8;  // this lane's place in a copy of four rows
+    const uint32_t ys = ybase + (uint32_t)((warp - 2) * YS * YSLOT);
+    uint8_t* const yp = basep + (ys - base);
+    int ptile = -1, ptok = 0, pcount = 0;  // the tile of the copies in flight
+    auto fetch = [&](int u) {
+      if (a.in && u < u1) {
+        if (u / nsub != ptile) {
+          ptile = u / nsub;
+          pcount = __ldcg(&a.tiles[ptile].y);
+          ptok = __ldcg(a.rowmap + ptile * TM + q * 32 + lane);
+        }
+        const int col = (u % nsub) * 128 + half * 64;
+        if (q * 32 < pcount && col < D) {
+          const uint32_t slot = ys + (uint32_t)((u - u0) % YS) * YSLOT;
+          const bool in = col + c8 < D;
+          const uint16_t* src = a.in + (in ? col + c8 : 0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + rsub;
+            const int t = __shfl_sync(0xffffffffu, ptok, r);
+            cp_async16(slot + sw128_off(r, c8), src + t * a.ldo, in ? 16u : 0u);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+    int m = 0, tile = -1, tok = 0;
     int2 tl = make_int2(-1, 0);
-    for (int u = u0; u < u1; ++u, ++v) {
-      const int s = v % ST, col = (u % nsub) * 128 + half * 64;
+#pragma unroll
+    for (int i = 0; i < LY; ++i) fetch(u0 + i);
+    for (int u = u0; u < u1; ++u) {
+      const int col = (u % nsub) * 128 + half * 64;
+      fetch(u + LY);
       if (u / nsub != tile) {
         tile = u / nsub;
         tl = __ldcg(a.tiles + tile);
-        tok = __ldcg(a.rowmap + tile * TM + r);
+        tok = __ldcg(a.rowmap + tile * TM + q * 32 + lane);
       }
-      const bool mma = tl.x >= 0;
+      const bool mma = tl.x >= 0, live = q * 32 < tl.y && col < D;  // live: this warp's rows and columns hold something
       const int b = m & 1;
-      bool ok = wait_ab(&full[s], (v / ST) & 1, abort, status);
-      ok = ok && (!mma || wait_ab(&acc_full[b], (m / 2) & 1, abort, status));
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      uint8_t* yrow = basep + s * stage + half * BOX + r * 128;
-      const bool live = q * 32 < tl.y && col < D;  // this warp's rows and columns hold something
-      if (live) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
-          if (mma) {
-            tc_ld16(tmem + b * 128 + half * 64 + c * 16 + ((uint32_t)(q * 32) << 16), w);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = 0u;
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint4* p = reinterpret_cast<uint4*>(yrow + (((2 * c + j) ^ (r & 7)) << 4));
-            uint4 y = make_uint4(0u, 0u, 0u, 0u);
-            if (a.in) y = *p;
-            const uint32_t* d = w + 8 * j;
-            y.x = f2b2(bf16lo(y.x) + __uint_as_float(d[0]), bf16hi(y.x) + __uint_as_float(d[1]));
-            y.y = f2b2(bf16lo(y.y) + __uint_as_float(d[2]), bf16hi(y.y) + __uint_as_float(d[3]));
-            y.z = f2b2(bf16lo(y.z) + __uint_as_float(d[4]), bf16hi(y.z) + __uint_as_float(d[5]));
-            y.w = f2b2(bf16lo(y.w) + __uint_as_float(d[6]), bf16hi(y.w) + __uint_as_float(d[7]));
-            *p = y;
-          }
+      uint32_t w[2][32];
+      if (mma) {
+        bool ok = wait_ab(&acc_full[b], (m >> 1) & 1, abort, status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        if (live) {
+          const uint32_t acc = tmem + b * 128 + half * 64 + ((uint32_t)(q * 32) << 16);
+          tc_ld32_async(acc, w[0]);
+          tc_ld32_async(acc + 32, w[1]);
+          tc_wait_ld();
         }
-      }
-      if (mma) {  // the accumulator is free for the MMAs
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[b]);
+        if (lane == 0) mbar_arrive(&acc_empty[b]);  // the accumulator is free for the MMAs
         ++m;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) w[0][j] = w[1][j] = 0u;
       }
+      cp_async_wait<LY>();
       __syncwarp();
       if (live) {
-        const int cc = lane & 7, c = col + cc * 8;
+        uint8_t* slot = yp + ((u - u0) % YS) * YSLOT;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint4* p = reinterpret_cast<uint4*>(slot + lane * 128 + ((j ^ (lane & 7)) << 4));
+          uint4 y = make_uint4(0u, 0u, 0u, 0u);
+          if (a.in) y = *p;
+          const uint32_t* d = &w[j >> 2][8 * (j & 3)];
+          y.x = f2b2(bf16lo(y.x) + __uint_as_float(d[0]), bf16hi(y.x) + __uint_as_float(d[1]));
+          y.y = f2b2(bf16lo(y.y) + __uint_as_float(d[2]), bf16hi(y.y) + __uint_as_float(d[3]));
+          y.z = f2b2(bf16lo(y.z) + __uint_as_float(d[4]), bf16hi(y.z) + __uint_as_float(d[5]));
+          y.w = f2b2(bf16lo(y.w) + __uint_as_float(d[6]), bf16hi(y.w) + __uint_as_float(d[7]));
+          *p = y;
+        }
+        __syncwarp();
+        const bool in = col + c8 < D;
+        uint16_t* dst = a.out + col + c8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int rr = i * 4 + (lane >> 3), row = q * 32 + rr;
-          const int t = __shfl_sync(0xffffffffu, tok, rr);
-          const uint4 y = lds128(basep + s * stage + half * BOX + row * 128 + ((cc ^ (row & 7)) << 4));
-          if (row < tl.y && c < D) *reinterpret_cast<uint4*>(a.out + t * a.ldo + c) = y;
+          const int r = i * 4 + rsub;
+          const int t = __shfl_sync(0xffffffffu, tok, r);
+          const uint4 y = lds128(slot + sw128_off(r, c8));
+          if (q * 32 + r < tl.y && in) *reinterpret_cast<uint4*>(dst + t * a.ldo) = y;
         }
+        __syncwarp();  // read before the slot's next copies
       }
-      fence_proxy_async();  // these accesses come before the next TMA write of the stage
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
     }
+    cp_async_wait<0>();
   }
   tc_fence_before();
   __syncthreads();
@@ -587,26 +639,29 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
 // x, dy, g, h are used as they lie in memory. A chunk that is its adapter's only
 // one writes bf16 itself; the others leave FP32 partial sums, which k_lora_dw_sum
 // adds in chunk order.
-//   warp 0 TMA, warp 1 MMA, warps 2-5 epilogue (a thread is one column of the slab)
+//   warps 0-3 token rows, then the accumulator (a thread is one column of the
+//   slab); warp 4 g or h (TMA); warp 5 the MMAs
 // ---------------------------------------------------------------------------
 constexpr int DW_THREADS = 192;
 __host__ __device__ inline int dw_stages(int R) { return R > 64 ? 2 : 3; }
 __host__ __device__ inline int dw_stage_bytes(int R) { return 2 * HALF + (R > 64 ? 4 : 2) * HALF; }
 __host__ __device__ inline size_t dw_smem(int R) { return 1024 + (size_t)dw_stages(R) * dw_stage_bytes(R); }
 
-__global__ void __launch_bounds__(DW_THREADS) k_lora_dw(const Args a, const __grid_constant__ Maps maps) {
+template <bool WIDE>
+__global__ void __launch_bounds__(DW_THREADS, 2) k_lora_dw(const Args a, const __grid_constant__ Maps maps) {
   extern __shared__ uint8_t dsmem[];
   __shared__ uint64_t full[3], empty[3], acc_full;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
+  constexpr int ST = WIDE ? 2 : 3, nbox = WIDE ? 2 : 1, LG = ST - 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
   volatile int* abort = &abort_flag;
   int* status = a.hdr + H_STATUS;
-  const int ST = dw_stages(a.R), stage = dw_stage_bytes(a.R), nbox = a.R > 64 ? 2 : 1;
+  const int stage = dw_stage_bytes(WIDE ? 128 : 64);
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 5);
       mbar_init(&empty[s], 1);
     }
     mbar_init(&acc_full, 1);
@@ -622,67 +677,54 @@ __global__ void __launch_bounds__(DW_THREADS) k_lora_dw(const Args a, const __gr
   const int last = __ldcg(a.tiles + ch.y + ch.z - 1).y;
   const int steps = 2 * (ch.z - 1) + (last > 64 ? 2 : 1);  // half tiles of 64 tokens
   const uint32_t cols = tmem_cols(a.Rp);
-  if (warp == 1) tmem_alloc(&tmem_base, cols);
+  if (warp == 5) tmem_alloc(&tmem_base, cols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  const int boxes = col0 + 64 < D ? 2 : 1;
-  if (warp == 0) {
-    const size_t plane = (size_t)a.max_tiles * TM;
-    const CUtensorMap* xm = is_b ? &maps.dy : &maps.x;
-    const CUtensorMap* gm = is_b ? &maps.h : &maps.g;
-    int i = 0;
-    for (; i < steps; ++i) {
-      const int s = i % ST, row0 = ch.y * TM + i * 64;
-      // lane l: four rows of the half tile, for the 64-column half l / 16
-      const int4 rows = __ldcg(reinterpret_cast<const int4*>(a.rowmap + row0) + (lane & 15));
-      const bool ok = i < ST || wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, status);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const uint32_t xs = base + s * stage, gs = xs + 2 * HALF;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[s], (uint32_t)(boxes * HALF + 2 * nbox * HALF));
-        for (int p = 0; p < 2; ++p)
-          for (int x = 0; x < nbox; ++x)
-            tma_load_2d(gs + (p * nbox + x) * HALF, gm, x * 64, (int)(p * plane) + row0, &full[s]);
-      }
-      __syncwarp();
-      if ((lane >> 4) < boxes)
-        tma_gather4(xs + (lane >> 4) * HALF + (lane & 15) * 512, xm, col0 + (lane >> 4) * 64, rows, &full[s]);
-    }
-    for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&full[r % ST], (r / ST) & 1);
-  } else if (warp == 1) {
-    const uint32_t idesc = idesc_f32acc(TM, a.Rp, true) | IDESC_A_MN | IDESC_B_MN;
-    int i = 0;
-    for (; i < steps; ++i) {
-      const int s = i % ST;
-      const bool ok = wait_ab(&full[s], (i / ST) & 1, abort, status);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t xs = base + s * stage, gs = xs + 2 * HALF;
-        for (int p = 0; p < 2; ++p)
+  if (warp < 4) {
+    // Rows 16 warp .. + 15 of a half tile, two rows of 256 bytes a copy: lane = row parity, 16-byte piece.
+    const uint16_t* src = is_b ? a.dy : a.x;
+    const int64_t ld = is_b ? a.lddy : a.ldx;
+    const int c8 = (lane & 15) * 8;
+    const bool in = col0 + c8 < D;
+    src += in ? col0 + c8 : 0;
+    const int* map = a.rowmap + ch.y * TM + warp * 16 + (lane & 15);
+    int tok = __ldcg(map);
+    for (int i = 0; i < steps + LG; ++i) {
+      if (i < steps) {
+        const int s = i % ST;
+        const int next = i + 1 < steps ? __ldcg(map + (i + 1) * 64) : 0;
+        const bool ok = i < ST || wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t xs = base + s * stage + (lane & 8 ? HALF : 0);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc_mma(tmem, sw128_desc_mn(xs + ks * 2048, HALF), sw128_desc_mn(gs + p * nbox * HALF + ks * 2048, HALF), idesc,
-                   (i > 0 || p > 0 || ks > 0) ? 1u : 0u);
-        tc_commit(&empty[s]);
-        if (i == steps - 1) tc_commit(&acc_full);
+        for (int j = 0; j < 8; ++j) {
+          const int r = 2 * j + (lane >> 4);
+          const int t = __shfl_sync(0xffffffffu, tok, r);
+          cp_async16(xs + sw128_off(warp * 16 + r, c8 & 63), src + t * ld, in ? 16u : 0u);
+        }
+        tok = next;
       }
-      __syncwarp();
+      cp_async_commit();
+      if (i >= LG) {
+        cp_async_wait<LG>();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[(i - LG) % ST]);
+      }
     }
-    for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&empty[r % ST], (r / ST) & 1);
-  } else {
+    cp_async_wait<0>();
     bool ok = wait_ab(&acc_full, 0, abort, status);
     ok = __all_sync(0xffffffffu, ok);
-    const int q = warp & 3, col = col0 + q * 32 + lane;
-    if (ok && col0 + q * 32 < D) {
+    const int col = col0 + warp * 32 + lane;
+    if (ok && col0 + warp * 32 < D) {
       tc_fence_after();
       float* part = ch.w >= 0 ? a.part + (size_t)ch.w * a.R * (a.K + a.N) + (is_b ? (size_t)a.R * a.K : 0) : nullptr;
       uint16_t* out = is_b ? a.dB + (size_t)ch.x * a.N * a.R : a.dA + (size_t)ch.x * a.R * a.K;
       for (int c = 0; c < a.Rp; c += 16) {
         uint32_t v[16];
-        tc_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+        tc_ld16(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)c, v);
         if (col >= D) continue;
         if (is_b) {  // [N][R]: a thread's row
 #pragma unroll
@@ -713,10 +755,48 @@ __global__ void __launch_bounds__(DW_THREADS) k_lora_dw(const Args a, const __gr
       }
       tc_fence_before();
     }
+  } else if (warp == 4) {
+    if (lane == 0) {
+      const size_t plane = (size_t)a.max_tiles * TM;
+      const CUtensorMap* gm = is_b ? &maps.h : &maps.g;
+      int i = 0;
+      for (; i < steps; ++i) {
+        const int s = i % ST, row0 = ch.y * TM + i * 64;
+        if (i >= ST && !wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, status)) break;
+        const uint32_t gs = base + s * stage + 2 * HALF;
+        mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * nbox * HALF));
+        for (int p = 0; p < 2; ++p)
+          for (int x = 0; x < nbox; ++x)
+            tma_load_2d(gs + (p * nbox + x) * HALF, gm, x * 64, (int)(p * plane) + row0, &full[s]);
+      }
+      for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&full[r % ST], (r / ST) & 1);
+    }
+  } else {
+    const uint32_t idesc = idesc_f32acc(TM, a.Rp, true) | IDESC_A_MN | IDESC_B_MN;
+    int i = 0;
+    for (; i < steps; ++i) {
+      const int s = i % ST;
+      const bool ok = wait_ab(&full[s], (i / ST) & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t xs = base + s * stage, gs = xs + 2 * HALF;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc_mma(tmem, sw128_desc_mn(xs + ks * 2048, HALF), sw128_desc_mn(gs + p * nbox * HALF + ks * 2048, HALF), idesc,
+                   (i > 0 || p > 0 || ks > 0) ? 1u : 0u);
+        tc_commit(&empty[s]);
+        if (i == steps - 1) tc_commit(&acc_full);
+      }
+      __syncwarp();
+    }
+    for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&empty[r % ST], (r / ST) & 1);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 5) {
     tc_fence_after();
     tmem_free(tmem, cols);
   }
@@ -933,13 +1013,6 @@ Args tile_args(const flint_lora* l, const int32_t* adapter, int T, uint8_t* ws, 
   return p;
 }
 
-// Rows of `cols` bf16 values ld apart, gathered four at a time.
-bool map_rows(CUtensorMap* m, const uint16_t* p, int cols, int64_t ld, int rows) {
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {BK, 1};
-  return encode_bf16(m, p, 2, dims, strides, box);
-}
 // A pool [n][rows][cols] in boxes of 64 columns x brows rows of one adapter: what lies past an adapter's rows
 // reads as zero, not as the next adapter's.
 bool map_pool(CUtensorMap* m, const uint16_t* p, int cols, int rows, int n, int brows) {
@@ -953,6 +1026,14 @@ bool map_low(CUtensorMap* m, const uint16_t* p, int R, int max_tiles) {
   const cuuint64_t strides[1] = {(cuuint64_t)R * 2};
   const cuuint32_t box[2] = {BK, 64};
   return encode_bf16(m, p, 2, dims, strides, box);
+}
+
+bool make_maps(Maps* m, const flint_lora* l, const Args& p) {
+  if (!map_pool(&m->a, l->a, p.K, p.R, p.n, p.Rp) || !map_pool(&m->b, l->b, p.R, p.N, p.n, 64) ||
+      !map_low(&m->h, p.h, p.R, p.max_tiles))
+    return false;
+  m->g = m->h;
+  return !p.g || map_low(&m->g, p.g, p.R, p.max_tiles);
 }
 
 // Opts a kernel in to its dynamic shared memory, once for each device.
@@ -986,8 +1067,7 @@ bool launch(void (*kernel)(P...), dim3 grid, int block, size_t smem, int cx, cud
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
-std::atomic<uint64_t> g_plan{0}, g_shrink{0}, g_expand{0}, g_expand_grad{0}, g_dw{0};
-constexpr size_t SMEM_MOST = 227 * 1024;
+std::atomic<uint64_t> g_plan{0}, g_shrink{0};
 
 bool run_plan(const Args& p, cudaStream_t stream) {
   return want_smem(k_lora_plan, g_plan, plan_smem(FLINT_LORA_MAX_ADAPTERS)) &&
@@ -1004,13 +1084,27 @@ bool run_shrink(const Args& p, const Maps& m, bool grads, cudaStream_t stream) {
          launch(k_lora_shrink, dim3(S, p.max_tiles, grads ? 2 : 1), SHR_THREADS, shrink_smem(p.R), S, stream, p, m);
 }
 
-template <bool GRAD>
-bool run_expand(const Args& p, const Maps& m, cudaStream_t stream) {
+template <bool GRAD, bool WIDE>
+bool run_expand_as(const Args& p, const Maps& m, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
   const int D = GRAD ? p.K : p.N;
   const int64_t items = (int64_t)p.max_tiles * ((D + 127) / 128);
-  return want_smem(k_lora_expand<GRAD>, GRAD ? g_expand_grad : g_expand, SMEM_MOST - 1024) &&
-         launch(k_lora_expand<GRAD>, dim3((unsigned)std::min<int64_t>(sm_count(), items)), EXP_THREADS, exp_smem(p.R), 0,
-                stream, p, m);
+  const size_t smem = exp_smem(p.R);
+  return want_smem(k_lora_expand<GRAD, WIDE>, done, smem) &&
+         launch(k_lora_expand<GRAD, WIDE>, dim3((unsigned)std::min<int64_t>(sm_count(), items)), EXP_THREADS, smem, 0, stream, p, m);
+}
+template <bool GRAD>
+bool run_expand(const Args& p, const Maps& m, cudaStream_t stream) {
+  return p.R > 64 ? run_expand_as<GRAD, true>(p, m, stream) : run_expand_as<GRAD, false>(p, m, stream);
+}
+
+template <bool WIDE>
+bool run_dw(const Args& p, const Maps& m, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  // chunks: the tiles of adapters in runs of CT, and a shorter run for each adapter
+  const int chunks = std::min(p.max_tiles, p.max_tiles / p.CT + std::min(p.n, p.T) + 1);
+  return want_smem(k_lora_dw<WIDE>, done, dw_smem(p.R)) &&
+         launch(k_lora_dw<WIDE>, dim3(p.slabs_a + p.slabs_b, chunks), DW_THREADS, dw_smem(p.R), 0, stream, p, m);
 }
 
 int blocks(int64_t threads) { return (int)std::min<int64_t>(152 * 16, (threads + 255) / 256); }
@@ -1075,14 +1169,10 @@ extern "C" flint_moe_status flint_lora_apply(const flint_lora* l, const uint16_t
   p.in = y_in;
   p.out = y_out;
   p.ldo = ldy;
+  p.x = x;
+  p.ldx = ldx;
   Maps m;
-  if (!map_rows(&m.x, x, p.K, ldx, T) || !map_rows(&m.in, y_in ? y_in : y_out, p.N, ldy, T) ||
-      !map_pool(&m.a, l->a, p.K, p.R, p.n, p.Rp) || !map_pool(&m.b, l->b, p.R, p.N, p.n, TM) ||
-      !map_low(&m.h, p.h, p.R, p.max_tiles))
-    return FLINT_MOE_ECUDA;
-  m.dy = m.x;
-  m.b64 = m.b;
-  m.g = m.h;
+  if (!make_maps(&m, l, p)) return FLINT_MOE_ECUDA;
   return run_plan(p, stream) && run_shrink(p, m, false, stream) && run_expand<false>(p, m, stream) ? FLINT_MOE_OK
                                                                                                    : FLINT_MOE_ECUDA;
 }
@@ -1156,20 +1246,15 @@ extern "C" flint_moe_status flint_lora_backward(const flint_lora* l, const uint1
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part);
   p.dA = da;
   p.dB = db;
+  p.x = x;
+  p.ldx = ldx;
+  p.dy = dy;
+  p.lddy = lddy;
   Maps m;
-  if (!map_rows(&m.x, x, p.K, ldx, T) || !map_rows(&m.dy, dy, p.N, lddy, T) ||
-      !map_rows(&m.in, dx_in ? dx_in : (dx_out ? dx_out : x), p.K, dx_out ? lddx : ldx, T) ||
-      !map_pool(&m.a, l->a, p.K, p.R, p.n, p.Rp) || !map_pool(&m.b64, l->b, p.R, p.N, p.n, 64) ||
-      !map_low(&m.h, p.h, p.R, p.max_tiles) || !map_low(&m.g, p.g, p.R, p.max_tiles))
-    return FLINT_MOE_ECUDA;
-  m.b = m.b64;
+  if (!make_maps(&m, l, p)) return FLINT_MOE_ECUDA;
   if (!run_plan(p, stream) || !run_shrink(p, m, true, stream)) return FLINT_MOE_ECUDA;
   if (dx_out && !run_expand<true>(p, m, stream)) return FLINT_MOE_ECUDA;
-  // chunks: the tiles of adapters in runs of CT, and a shorter run for each adapter
-  const int chunks = p.max_tiles / p.CT + std::min(p.n, T) + 1;
-  if (!want_smem(k_lora_dw, g_dw, dw_smem(FLINT_LORA_MAX_RANK)) ||
-      !launch(k_lora_dw, dim3(p.slabs_a + p.slabs_b, std::min(chunks, p.max_tiles)), DW_THREADS, dw_smem(p.R), 0, stream, p, m))
-    return FLINT_MOE_ECUDA;
+  if (!(p.R > 64 ? run_dw<true>(p, m, stream) : run_dw<false>(p, m, stream))) return FLINT_MOE_ECUDA;
   const int64_t all = (int64_t)p.R * (p.K + p.N);
   if (!launch(k_lora_dw_sum, dim3((unsigned)std::min<int64_t>((all + 2047) / 2048, std::max(1, 152 * 8 / p.n)), p.n), 256, 0, 0,
               stream, p))

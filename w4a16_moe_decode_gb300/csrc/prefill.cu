@@ -135,20 +135,6 @@ __device__ __forceinline__ T* ws_at(const PfArgs& a, size_t off) {
   return reinterpret_cast<T*>(a.ws + off);
 }
 
-// ---------------------------------------------------------------------------
-// cp.async helpers (the tcgen05 and TMA ones are in tensor.cuh).
-// ---------------------------------------------------------------------------
-
-// 16-byte copy global -> shared; src_bytes 0 fills the 16 bytes with zeros.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // bf16x2 -> f16x2 of the values times sc (a power of two).
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2_scaled(uint32_t w, float sc) {
   const __half2 hv = __floats2half2_rn(bf16lo(w) * sc, bf16hi(w) * sc);
