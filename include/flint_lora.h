@@ -60,7 +60,7 @@ size_t flint_lora_workspace_bytes(const flint_lora* lora, int32_t max_tokens);
 /* y_out[t] = bf16(y_in[t] + s_a B_a (A_a x[t])) for t < T, 0 <= T <=
  * FLINT_LORA_MAX_TOKENS (0 is a no-op). x bf16 [T] rows of K, ldx elements
  * apart; y_in, y_out bf16 [T] rows of N, ldy elements apart (ldx >= K, ldy >=
- * N, multiples of 8). adapter: int32 [T]. y_in NULL means zero. y_out may be
+ * N, multiples of 8 below 2^31). adapter: int32 [T]. y_in NULL means zero. y_out may be
  * y_in (rows without an adapter are then left untouched); any other overlap of
  * y_out with x or y_in is refused (FLINT_MOE_EINVAL). */
 flint_moe_status flint_lora_apply(const flint_lora* lora, const uint16_t* x, int64_t ldx, const int32_t* adapter,

@@ -31,17 +31,15 @@ struct Args {
   int with_none;  // tokens without an adapter get tiles (their output rows have to be written)
   int max_tiles;
   int* hdr;
-  int2* tiles;   // {adapter, count}
+  int2* tiles;   // [max_tiles]: {adapter, count}, {-2, 0} past the last
   int* rowmap;   // [max_tiles * 128]
   uint16_t* h;   // s A x as bf16 halves hi, lo: [2][max_tiles * 128][R]
   uint16_t* g;   // s B^T dy likewise
   const uint16_t* x;
-  int64_t ldx;
   const uint16_t* dy;
-  int64_t lddy;
   const uint16_t* in;  // y_in or dx_in, or null
   uint16_t* out;
-  int64_t ldo;
+  int ldx, lddy, ldo;  // row strides in elements (offsets of rows are 64-bit products)
   // weights' gradients
   int CT;              // tiles of a chunk at most
   int slabs_a, slabs_b;  // 128-wide slabs of K and of N
@@ -72,7 +70,8 @@ __device__ __forceinline__ uint32_t f2b2(float lo, float hi) {
 // run of consecutive tokens; the 32 tokens of a step find their fellows with
 // match_any, so every token's place follows from counts and lane masks alone.
 // ---------------------------------------------------------------------------
-__host__ __device__ inline size_t plan_smem(int n) { return sizeof(int) * ((size_t)33 * (n + 1) + 3 * (n + 2)); }
+__host__ __device__ inline size_t plan_smem(int n) { return sizeof(int) * ((size_t)34 * (n + 1) + 3 * (n + 2)); }
+constexpr int PB = 8;  // steps of 32 tokens whose adapters a warp holds at once
 
 // Exclusive sums of f(0 .. n-1) into out[0 .. n], by one warp.
 template <typename F>
@@ -112,80 +111,100 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const Args a) {
   const int G = a.n + 1;  // group n: tokens without an adapter
   int* hist = sm;         // [32][G], then each warp's next place in the group
   int* cnt = hist + 32 * G;
-  int* tf = cnt + G;       // first tile of each group
+  int* lasts = cnt + G;    // last token of each group
+  int* tf = lasts + G;     // first tile of each group
   int* cf = tf + G + 1;    // first chunk
   int* sf = cf + G + 1;    // first partial slot
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < 32 * G; i += 1024) hist[i] = 0;
   pdl_wait();
   pdl_trigger();
-  __syncthreads();
   const int L = (a.T + 1023) / 1024 * 32, t0 = warp * L, t1 = min(a.T, t0 + L);
   int* mine = hist + warp * G;
-  for (int i = t0; i < t1; i += 32) {
-    const int t = i + lane;
-    int g = -1;
-    if (t < t1) {
-      g = __ldg(a.adapter + t);
-      if (g < 0 || g >= a.n) g = a.n;
+  // Groups of up to PB steps of 32 tokens, all loaded at once (-1 past the run).
+  int g[PB];
+  auto load = [&](int i) {
+#pragma unroll
+    for (int j = 0; j < PB; ++j) {
+      const int t = i + 32 * j + lane;
+      g[j] = t < t1 ? __ldg(a.adapter + t) : 0;
     }
-    const unsigned same = __match_any_sync(0xffffffffu, g);
-    if (g >= 0 && lane == __ffs(same) - 1) mine[g] += __popc(same);
-    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < PB; ++j) {
+      if (g[j] < 0 || g[j] >= a.n) g[j] = a.n;
+      if (i + 32 * j + lane >= t1) g[j] = -1;
+    }
+  };
+  load(t0);
+  __syncthreads();
+  for (int i = t0; i < t1; i += 32 * PB) {
+    if (i > t0) load(i);
+#pragma unroll
+    for (int j = 0; j < PB; ++j) {
+      if (i + 32 * j >= t1) break;
+      const unsigned same = __match_any_sync(0xffffffffu, g[j]);
+      if (g[j] >= 0 && lane == __ffs(same) - 1) mine[g[j]] += __popc(same);
+      __syncwarp();
+    }
   }
   __syncthreads();
-  for (int g = threadIdx.x; g < G; g += 1024) {
+  for (int c = threadIdx.x; c < G; c += 1024) {
     int at = 0;
+#pragma unroll 8
     for (int w = 0; w < 32; ++w) {
-      const int c = hist[w * G + g];
-      hist[w * G + g] = at;
-      at += c;
+      const int v = hist[w * G + c];
+      hist[w * G + c] = at;
+      at += v;
     }
-    cnt[g] = g == a.n && !a.with_none ? 0 : at;
+    cnt[c] = c == a.n && !a.with_none ? 0 : at;
   }
   __syncthreads();
-  auto tiles_of = [&](int g) { return (cnt[g] + TM - 1) / TM; };
-  auto chunks_of = [&](int g) { return g == a.n ? 0 : (tiles_of(g) + a.CT - 1) / a.CT; };
+  auto tiles_of = [&](int c) { return (cnt[c] + TM - 1) / TM; };
+  auto chunks_of = [&](int c) { return c == a.n ? 0 : (tiles_of(c) + a.CT - 1) / a.CT; };
   if (warp == 0) warp_scan(G, lane, tf, tiles_of);
   if (warp == 1 && a.chunks) warp_scan(G, lane, cf, chunks_of);
-  if (warp == 2 && a.chunks) warp_scan(G, lane, sf, [&](int g) { return chunks_of(g) > 1 ? chunks_of(g) : 0; });
+  if (warp == 2 && a.chunks) warp_scan(G, lane, sf, [&](int c) { return chunks_of(c) > 1 ? chunks_of(c) : 0; });
   __syncthreads();
-  for (int i = t0; i < t1; i += 32) {
-    const int t = i + lane;
-    int g = -1;
-    if (t < t1) {
-      g = __ldg(a.adapter + t);
-      if (g < 0 || g >= a.n) g = a.n;
+  for (int i = t0; i < t1; i += 32 * PB) {
+    if (L > 32 * PB) load(i);  // a run of one batch is still in registers
+#pragma unroll
+    for (int j = 0; j < PB; ++j) {
+      if (i + 32 * j >= t1) break;
+      const unsigned same = __match_any_sync(0xffffffffu, g[j]);
+      const int rank = __popc(same & ((1u << lane) - 1));
+      int at = 0;
+      if (g[j] >= 0) at = mine[g[j]] + rank;
+      __syncwarp();
+      if (g[j] >= 0 && rank == 0) mine[g[j]] += __popc(same);
+      __syncwarp();
+      if (g[j] >= 0 && at < cnt[g[j]]) {  // (no place for tokens without an adapter where they need none)
+        const int t = i + 32 * j + lane;
+        a.rowmap[tf[g[j]] * TM + at] = t;
+        if (at == cnt[g[j]] - 1) lasts[g[j]] = t;
+      }
     }
-    const unsigned same = __match_any_sync(0xffffffffu, g);
-    const int rank = __popc(same & ((1u << lane) - 1));
-    int at = 0;
-    if (g >= 0) at = mine[g] + rank;
-    __syncwarp();
-    if (g >= 0 && rank == 0) mine[g] += __popc(same);
-    __syncwarp();
-    if (g >= 0 && (g < a.n || a.with_none)) a.rowmap[tf[g] * TM + at] = t;
   }
   __syncthreads();
   const int ntiles = tf[G];
-  for (int i = threadIdx.x; i < ntiles; i += 1024) {
-    const int g = group_of(tf, G, i);
-    a.tiles[i] = make_int2(g == a.n ? -1 : g, min(TM, cnt[g] - TM * (i - tf[g])));
-  }
-  for (int i = warp; i < ntiles; i += 32) {  // rows past a tile's count repeat its last token
-    const int g = group_of(tf, G, i), count = min(TM, cnt[g] - TM * (i - tf[g]));
-    if (count < TM) {
-      const int t = a.rowmap[i * TM + count - 1];
-      for (int r = count + lane; r < TM; r += 32) a.rowmap[i * TM + r] = t;
+  for (int i = threadIdx.x; i < a.max_tiles; i += 1024) {
+    int2 tile = make_int2(-2, 0);  // no tile
+    if (i < ntiles) {
+      const int c = group_of(tf, G, i);
+      tile = make_int2(c == a.n ? -1 : c, min(TM, cnt[c] - TM * (i - tf[c])));
     }
+    a.tiles[i] = tile;
+  }
+  for (int c = warp; c < G; c += 32) {  // rows past the count of a group's last tile repeat its last token
+    const int end = tf[c + 1] * TM;
+    for (int r = tf[c] * TM + cnt[c] + lane; r < end; r += 32) a.rowmap[r] = lasts[c];
   }
   if (a.chunks) {
     const int nchunks = cf[G];
-    for (int c = threadIdx.x; c < nchunks; c += 1024) {
-      const int g = group_of(cf, G, c), j = c - cf[g];
-      a.chunks[c] = make_int4(g, tf[g] + j * a.CT, min(a.CT, tiles_of(g) - j * a.CT), chunks_of(g) > 1 ? sf[g] + j : -1);
+    for (int i = threadIdx.x; i < nchunks; i += 1024) {
+      const int c = group_of(cf, G, i), j = i - cf[c];
+      a.chunks[i] = make_int4(c, tf[c] + j * a.CT, min(a.CT, tiles_of(c) - j * a.CT), chunks_of(c) > 1 ? sf[c] + j : -1);
     }
-    for (int g = threadIdx.x; g < a.n; g += 1024) a.of_adapter[g] = make_int2(sf[g], chunks_of(g));
+    for (int c = threadIdx.x; c < a.n; c += 1024) a.of_adapter[c] = make_int2(sf[c], chunks_of(c));
     if (threadIdx.x == 0) a.hdr[H_CHUNKS] = nchunks;
   }
   if (threadIdx.x == 0) {
@@ -196,7 +215,7 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const Args a) {
 
 // ---------------------------------------------------------------------------
 // Token rows come in any order, so they are gathered with 16-byte asynchronous
-// copies, eight lanes to a row's 128 bytes (TMA's four-row gather delivered one
+// copies that arrive on the stage's mbarrier by themselves, eight lanes to a row's 128 bytes (TMA's four-row gather delivered one
 // such group every 50 to 60 ns and SM, 1.2 TB/s over the card, whatever the order).
 //
 // Shrink: h = s A x of one tile (z = 0) or g = s B^T dy (z = 1), [128 x D] times
@@ -212,7 +231,6 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const Args a) {
 // ---------------------------------------------------------------------------
 constexpr int SHR_STAGES = 4;
 constexpr int SHR_THREADS = 192;
-constexpr int LAG = SHR_STAGES - 1;  // stages in flight before the oldest is waited for
 
 __host__ __device__ inline int shrink_wbytes(int R) { return R > 64 ? 2 * HALF : HALF; }
 __host__ __device__ inline size_t shrink_smem(int R) { return 1024 + (size_t)SHR_STAGES * (BOX + shrink_wbytes(R)); }
@@ -239,7 +257,7 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
   int* status = a.hdr + H_STATUS;
   if (threadIdx.x == 0) {
     for (int s = 0; s < SHR_STAGES; ++s) {
-      mbar_init(&full[s], 5);  // four warps of token rows, the weights' expect-tx arrival
+      mbar_init(&full[s], 129);  // 128 threads' copies of token rows, the weights' expect-tx arrival
       mbar_init(&empty[s], 1);
     }
     mbar_init(&acc_full, 1);
@@ -249,9 +267,12 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
   pdl_wait();
   pdl_trigger();
   const int tile = blockIdx.y;
-  if (tile >= __ldcg(a.hdr + H_TILES)) return;
   const int2 tl = __ldcg(a.tiles + tile);
-  if (tl.x < 0) return;  // the whole cluster leaves: nothing waits for it
+  // rows of this thread's copies: i * 4 + lane / 8 of its warp's 32
+  int tok[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) tok[i] = __ldcg(a.rowmap + tile * TM + (warp & 3) * 32 + i * 4 + (lane >> 3));
+  if (tl.x < 0) return;  // the whole cluster leaves: nothing waits for it (a tile past the last has no rows either)
   const bool grad = blockIdx.z != 0;
   const int S = gridDim.x, rank = blockIdx.x;
   const int D = grad ? a.N : a.K, KB = (D + BK - 1) / BK;
@@ -267,36 +288,24 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
   const int PP = a.Rp + 4;  // row pitch of the partial sums, padded by 16 bytes
   if (warp < 4) {
     const uint16_t* src = grad ? a.dy : a.x;
-    const int64_t ld = grad ? a.lddy : a.ldx;
+    const int ld = grad ? a.lddy : a.ldx;
     const int c8 = (lane & 7) * 8;
     const bool any = warp * 32 < tl.y;
-    const uint16_t* row[8];
     uint32_t dst[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      row[i] = src + __ldcg(a.rowmap + tile * TM + warp * 32 + i * 4 + (lane >> 3)) * ld + c8;
-#pragma unroll
     for (int i = 0; i < 2; ++i) dst[i] = base + sw128_off(warp * 32 + i * 4 + (lane >> 3), c8);
-    int i = 0;
-    for (; i < nkb + LAG; ++i) {
-      if (i < nkb) {
-        const int s = i % SHR_STAGES, col = (kb0 + i) * BK;
-        const bool ok = i < SHR_STAGES || wait_ab(&empty[s], ((i / SHR_STAGES) - 1) & 1, abort, status);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        if (any) {
-          const bool in = col + c8 < D;
+    for (int i = 0; i < nkb; ++i) {
+      const int s = i % SHR_STAGES, col = (kb0 + i) * BK;
+      const bool ok = i < SHR_STAGES || wait_ab(&empty[s], ((i / SHR_STAGES) - 1) & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (any) {
+        const bool in = col + c8 < D;
+        const uint16_t* at = src + (in ? col + c8 : 0);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            cp_async16(dst[j & 1] + s * stage + (j >> 1) * 1024, row[j] + (in ? col : 0), in ? 16u : 0u);
-        }
+        for (int j = 0; j < 8; ++j)
+          cp_async16(dst[j & 1] + s * stage + (j >> 1) * 1024, at + (int64_t)tok[j] * ld, in ? 16u : 0u);
       }
-      cp_async_commit();
-      if (i >= LAG) {
-        cp_async_wait<LAG>();
-        fence_proxy_async();  // these copies -> visible to the tensor core
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[(i - LAG) % SHR_STAGES]);
-      }
+      cp_async_arrive(&full[s]);
     }
     cp_async_wait<0>();
     // Every CTA's sums to its shared memory (the stages are free by then), [128][Rp].
@@ -340,6 +349,7 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
       const int s = i % SHR_STAGES;
       const bool ok = wait_ab(&full[s], (i / SHR_STAGES) & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
+      fence_proxy_async();  // the copies that arrived -> visible to the tensor core
       tc_fence_after();
       if (elect_one()) {
         const uint32_t xs = base + s * stage, wsm = xs + BOX;
@@ -447,19 +457,27 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  pdl_wait();
-  // This CTA's run [u0, u1) of the items.
+  pdl_trigger();
+  // The plan is complete (the shrink kernel lets this one start only after its own wait for it), and so are the
+  // base rows; only h has to be waited for, by the warp that loads it.
+  // This CTA's run [u0, u1) of the items: tile u / nsub, columns 128 (u % nsub) ...
   const long long items = (long long)__ldcg(a.hdr + H_TILES) * nsub;
   const int u0 = (int)(items * blockIdx.x / gridDim.x), u1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
+  const int tile0 = u0 / nsub, sub0 = u0 - tile0 * nsub;
   const size_t plane = (size_t)a.max_tiles * TM;
   if (warp == 0) {
     if (lane == 0) {
-      int m = 0, hn = 0, tile = -1;  // items with an adapter, h loads
+      pdl_wait();
+      int m = 0, hn = 0;  // items with an adapter, h loads
+      int tile = tile0, sub = sub0;
       int2 tl = make_int2(-1, 0);
-      for (int u = u0; u < u1; ++u) {
-        const int col = (u % nsub) * 128;
-        if (u / nsub != tile) {
-          tile = u / nsub;
+      for (int u = u0; u < u1; ++u, ++sub) {
+        if (sub == nsub) {
+          sub = 0;
+          ++tile;
+        }
+        const int col = sub * 128;
+        if (u == u0 || sub == 0) {
           tl = __ldcg(a.tiles + tile);
           if (tl.x >= 0) {
             const int b = hn % HB;
@@ -495,12 +513,15 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
     }
   } else if (warp == 1) {
     const uint32_t idesc = idesc_f32acc(TM, 128, true) | (GRAD ? IDESC_B_MN : 0u);
-    int m = 0, hn = 0, tile = -1;
+    int m = 0, hn = 0, tile = tile0, sub = sub0;
     int2 tl = make_int2(-1, 0);
-    for (int u = u0; u < u1; ++u) {
+    for (int u = u0; u < u1; ++u, ++sub) {
       bool ok = true;
-      if (u / nsub != tile) {
-        tile = u / nsub;
+      if (sub == nsub) {
+        sub = 0;
+        ++tile;
+      }
+      if (u == u0 || sub == 0) {
         tl = __ldcg(a.tiles + tile);
         if (tl.x >= 0) {
           ok = wait_ab(&h_full[hn % HB], (hn / HB) & 1, abort, status);
@@ -526,7 +547,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
           }
         tc_commit(&empty[b]);
         tc_commit(&acc_full[b]);
-        if (u + 1 == u1 || (u + 1) / nsub != tile) tc_commit(&h_empty[hb]);
+        if (u + 1 == u1 || sub + 1 == nsub) tc_commit(&h_empty[hb]);
       }
       __syncwarp();
       ++m;
@@ -537,41 +558,59 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
     const int rsub = lane >> 3, c8 = (lane & 7) * 8;  // this lane's place in a copy of four rows
     const uint32_t ys = ybase + (uint32_t)((warp - 2) * YS * YSLOT);
     uint8_t* const yp = basep + (ys - base);
-    int ptile = -1, ptok = 0, pcount = 0;  // the tile of the copies in flight
-    auto fetch = [&](int u) {
-      if (a.in && u < u1) {
-        if (u / nsub != ptile) {
-          ptile = u / nsub;
+    // Copies run LY items ahead: item (ptile, psub) goes to slot `pslot`, for rows i * 4 + rsub of this warp's 32.
+    int ptile = tile0, psub = sub0, pslot = 0, pcount = 0, left = u1 - u0;
+    int ptok[8];
+    auto rows_of = [&](int tile, int (&t)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = __ldcg(a.rowmap + tile * TM + q * 32 + i * 4 + rsub);
+    };
+    if (left > 0) {
+      pcount = __ldcg(&a.tiles[ptile].y);
+      rows_of(ptile, ptok);
+    }
+    uint32_t off[2];  // this lane's place in rows 0 and 4, 32 bytes swizzled apart
+    off[0] = sw128_off(rsub, c8);
+    off[1] = sw128_off(4 + rsub, c8);
+    auto fetch = [&]() {
+      if (a.in && left > 0) {
+        if (psub == nsub) {
+          psub = 0;
+          ++ptile;
           pcount = __ldcg(&a.tiles[ptile].y);
-          ptok = __ldcg(a.rowmap + ptile * TM + q * 32 + lane);
+          rows_of(ptile, ptok);
         }
-        const int col = (u % nsub) * 128 + half * 64;
+        const int col = psub * 128 + half * 64;
         if (q * 32 < pcount && col < D) {
-          const uint32_t slot = ys + (uint32_t)((u - u0) % YS) * YSLOT;
+          const uint32_t slot = ys + (uint32_t)pslot * YSLOT;
           const bool in = col + c8 < D;
           const uint16_t* src = a.in + (in ? col + c8 : 0);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + rsub;
-            const int t = __shfl_sync(0xffffffffu, ptok, r);
-            cp_async16(slot + sw128_off(r, c8), src + t * a.ldo, in ? 16u : 0u);
-          }
+          for (int i = 0; i < 8; ++i)
+            cp_async16(slot + off[i & 1] + (i >> 1) * 1024, src + (int64_t)ptok[i] * a.ldo, in ? 16u : 0u);
         }
+        ++psub;
+        --left;
+        pslot = pslot + 1 == YS ? 0 : pslot + 1;
       }
       cp_async_commit();
     };
-    int m = 0, tile = -1, tok = 0;
+    int m = 0, tile = tile0, sub = sub0, slot_i = 0;
+    int tok[8];
     int2 tl = make_int2(-1, 0);
 #pragma unroll
-    for (int i = 0; i < LY; ++i) fetch(u0 + i);
-    for (int u = u0; u < u1; ++u) {
-      const int col = (u % nsub) * 128 + half * 64;
-      fetch(u + LY);
-      if (u / nsub != tile) {
-        tile = u / nsub;
-        tl = __ldcg(a.tiles + tile);
-        tok = __ldcg(a.rowmap + tile * TM + q * 32 + lane);
+    for (int i = 0; i < LY; ++i) fetch();
+    for (int u = u0; u < u1; ++u, ++sub) {
+      fetch();
+      if (sub == nsub) {
+        sub = 0;
+        ++tile;
       }
+      if (u == u0 || sub == 0) {
+        tl = __ldcg(a.tiles + tile);
+        rows_of(tile, tok);
+      }
+      const int col = sub * 128 + half * 64;
       const bool mma = tl.x >= 0, live = q * 32 < tl.y && col < D;  // live: this warp's rows and columns hold something
       const int b = m & 1;
       uint32_t w[2][32];
@@ -596,10 +635,11 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
       cp_async_wait<LY>();
       __syncwarp();
       if (live) {
-        uint8_t* slot = yp + ((u - u0) % YS) * YSLOT;
+        uint8_t* slot = yp + slot_i * YSLOT;
+        uint8_t* mine = slot + lane * 128;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          uint4* p = reinterpret_cast<uint4*>(slot + lane * 128 + ((j ^ (lane & 7)) << 4));
+          uint4* p = reinterpret_cast<uint4*>(mine + ((lane & 7) << 4 ^ j << 4));
           uint4 y = make_uint4(0u, 0u, 0u, 0u);
           if (a.in) y = *p;
           const uint32_t* d = &w[j >> 2][8 * (j & 3)];
@@ -610,17 +650,18 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
           *p = y;
         }
         __syncwarp();
-        const bool in = col + c8 < D;
-        uint16_t* dst = a.out + col + c8;
+        if (col + c8 < D) {
+          uint16_t* dst = a.out + col + c8;
+          const int rows = tl.y - q * 32 - rsub;  // row i * 4 + rsub is one of the tile's
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 4 + rsub;
-          const int t = __shfl_sync(0xffffffffu, tok, r);
-          const uint4 y = lds128(slot + sw128_off(r, c8));
-          if (q * 32 + r < tl.y && in) *reinterpret_cast<uint4*>(dst + t * a.ldo) = y;
+          for (int i = 0; i < 8; ++i) {
+            const uint4 y = lds128(slot + off[i & 1] + (i >> 1) * 1024);
+            if (i * 4 < rows) *reinterpret_cast<uint4*>(dst + (int64_t)tok[i] * a.ldo) = y;
+          }
         }
         __syncwarp();  // read before the slot's next copies
       }
+      slot_i = slot_i + 1 == YS ? 0 : slot_i + 1;
     }
     cp_async_wait<0>();
   }
@@ -653,7 +694,7 @@ __global__ void __launch_bounds__(DW_THREADS, 2) k_lora_dw(const Args a, const _
   __shared__ uint64_t full[3], empty[3], acc_full;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  constexpr int ST = WIDE ? 2 : 3, nbox = WIDE ? 2 : 1, LG = ST - 1;
+  constexpr int ST = WIDE ? 2 : 3, nbox = WIDE ? 2 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
   volatile int* abort = &abort_flag;
@@ -661,7 +702,7 @@ __global__ void __launch_bounds__(DW_THREADS, 2) k_lora_dw(const Args a, const _
   const int stage = dw_stage_bytes(WIDE ? 128 : 64);
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&full[s], 5);
+      mbar_init(&full[s], 129);
       mbar_init(&empty[s], 1);
     }
     mbar_init(&acc_full, 1);
@@ -685,34 +726,26 @@ __global__ void __launch_bounds__(DW_THREADS, 2) k_lora_dw(const Args a, const _
   if (warp < 4) {
     // Rows 16 warp .. + 15 of a half tile, two rows of 256 bytes a copy: lane = row parity, 16-byte piece.
     const uint16_t* src = is_b ? a.dy : a.x;
-    const int64_t ld = is_b ? a.lddy : a.ldx;
+    const int ld = is_b ? a.lddy : a.ldx;
     const int c8 = (lane & 15) * 8;
     const bool in = col0 + c8 < D;
     src += in ? col0 + c8 : 0;
     const int* map = a.rowmap + ch.y * TM + warp * 16 + (lane & 15);
     int tok = __ldcg(map);
-    for (int i = 0; i < steps + LG; ++i) {
-      if (i < steps) {
-        const int s = i % ST;
-        const int next = i + 1 < steps ? __ldcg(map + (i + 1) * 64) : 0;
-        const bool ok = i < ST || wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, status);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        const uint32_t xs = base + s * stage + (lane & 8 ? HALF : 0);
+    for (int i = 0; i < steps; ++i) {
+      const int s = i % ST;
+      const int next = i + 1 < steps ? __ldcg(map + (i + 1) * 64) : 0;
+      const bool ok = i < ST || wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint32_t xs = base + s * stage + (lane & 8 ? HALF : 0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = 2 * j + (lane >> 4);
-          const int t = __shfl_sync(0xffffffffu, tok, r);
-          cp_async16(xs + sw128_off(warp * 16 + r, c8 & 63), src + t * ld, in ? 16u : 0u);
-        }
-        tok = next;
+      for (int j = 0; j < 8; ++j) {
+        const int r = 2 * j + (lane >> 4);
+        const int t = __shfl_sync(0xffffffffu, tok, r);
+        cp_async16(xs + sw128_off(warp * 16 + r, c8 & 63), src + (int64_t)t * ld, in ? 16u : 0u);
       }
-      cp_async_commit();
-      if (i >= LG) {
-        cp_async_wait<LG>();
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[(i - LG) % ST]);
-      }
+      cp_async_arrive(&full[s]);
+      tok = next;
     }
     cp_async_wait<0>();
     bool ok = wait_ab(&acc_full, 0, abort, status);
@@ -778,6 +811,7 @@ __global__ void __launch_bounds__(DW_THREADS, 2) k_lora_dw(const Args a, const _
       const int s = i % ST;
       const bool ok = wait_ab(&full[s], (i / ST) & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
+      fence_proxy_async();  // the copies that arrived -> visible to the tensor core
       tc_fence_after();
       if (elect_one()) {
         const uint32_t xs = base + s * stage, gs = xs + 2 * HALF;
@@ -917,6 +951,7 @@ flint_moe_status check_pool(const flint_lora* l) {
   return FLINT_MOE_OK;
 }
 
+constexpr int64_t LD_MOST = 0x7fffffff;  // row strides are kept in 32 bits
 constexpr int SMALL_T = 32;  // calls of up to this many tokens take the kernels for few rows
 
 int sm_count() {
@@ -1140,7 +1175,8 @@ extern "C" flint_moe_status flint_lora_apply(const flint_lora* l, const uint16_t
                                              size_t ws_bytes, cudaStream_t stream) {
   const flint_moe_status st = check_pool(l);
   if (st != FLINT_MOE_OK) return st;
-  if (T < 0 || T > FLINT_LORA_MAX_TOKENS || ldx < l->in_dim || ldy < l->out_dim) return FLINT_MOE_EINVAL;
+  if (T < 0 || T > FLINT_LORA_MAX_TOKENS || ldx < l->in_dim || ldy < l->out_dim || ldx > LD_MOST || ldy > LD_MOST)
+    return FLINT_MOE_EINVAL;
   if (T == 0) return FLINT_MOE_OK;
   if (!x || !adapter || !y_out || !ws) return FLINT_MOE_EINVAL;
   if (!aligned(x, 16) || !aligned(y_in, 16) || !aligned(y_out, 16) || !aligned(ws, 256) || !aligned(adapter, 4) || ldx % 8 ||
@@ -1168,9 +1204,9 @@ extern "C" flint_moe_status flint_lora_apply(const flint_lora* l, const uint16_t
   p.with_none = y_in != y_out;
   p.in = y_in;
   p.out = y_out;
-  p.ldo = ldy;
+  p.ldo = (int)ldy;
   p.x = x;
-  p.ldx = ldx;
+  p.ldx = (int)ldx;
   Maps m;
   if (!make_maps(&m, l, p)) return FLINT_MOE_ECUDA;
   return run_plan(p, stream) && run_shrink(p, m, false, stream) && run_expand<false>(p, m, stream) ? FLINT_MOE_OK
@@ -1211,7 +1247,8 @@ extern "C" flint_moe_status flint_lora_backward(const flint_lora* l, const uint1
                                                 size_t ws_bytes, cudaStream_t stream) {
   const flint_moe_status st = check_pool(l);
   if (st != FLINT_MOE_OK) return st;
-  if (T < 0 || T > FLINT_LORA_MAX_TOKENS || ldx < l->in_dim || lddy < l->out_dim || (dx_out && lddx < l->in_dim))
+  if (T < 0 || T > FLINT_LORA_MAX_TOKENS || ldx < l->in_dim || lddy < l->out_dim || ldx > LD_MOST || lddy > LD_MOST ||
+      (dx_out && (lddx < l->in_dim || lddx > LD_MOST)))
     return FLINT_MOE_EINVAL;
   if (!da || !db) return FLINT_MOE_EINVAL;
   if (!aligned(da, 16) || !aligned(db, 16)) return FLINT_MOE_EALIGN;
@@ -1237,7 +1274,7 @@ extern "C" flint_moe_status flint_lora_backward(const flint_lora* l, const uint1
   p.g = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + w.g);
   p.in = dx_in;
   p.out = dx_out;
-  p.ldo = lddx;
+  p.ldo = (int)lddx;
   p.CT = chunk_tiles(l, T);
   p.slabs_a = (p.K + 127) / 128;
   p.slabs_b = (p.N + 127) / 128;
@@ -1247,9 +1284,9 @@ extern "C" flint_moe_status flint_lora_backward(const flint_lora* l, const uint1
   p.dA = da;
   p.dB = db;
   p.x = x;
-  p.ldx = ldx;
+  p.ldx = (int)ldx;
   p.dy = dy;
-  p.lddy = lddy;
+  p.lddy = (int)lddy;
   Maps m;
   if (!make_maps(&m, l, p)) return FLINT_MOE_ECUDA;
   if (!run_plan(p, stream) || !run_shrink(p, m, true, stream)) return FLINT_MOE_ECUDA;
