@@ -12,6 +12,7 @@
 // One warp per token row, 16-byte loads. Both kernels move T E floats and are
 // bound by memory bandwidth.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "flint_moe_balance.h"
@@ -68,13 +69,26 @@ __device__ __forceinline__ double warp_sum_d(double v) {
   return v;
 }
 
+// The hardware's exponential and reciprocal with subnormal results flushed: none occur below, and the rows are
+// bound by instructions otherwise (the forms that keep them take three times as many).
+__device__ __forceinline__ float exp_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float rcp_of(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // s = sigmoid(z) and q = 1 - s without cancellation: with e = exp(-z), s = 1 / (1 + e) and
 // q = e s. e is held at 1e37, where s is still an FP32 normal; rows in which no s is above
 // 1e-30 take the exact shares below instead.
 constexpr float LOW_ROW = 1e-30f;
 __device__ __forceinline__ void sigmoid2(float z, float& s, float& q) {
-  const float e = fminf(__expf(-z), 1e37f);
-  s = __fdividef(1.0f, 1.0f + e);
+  const float e = fminf(exp_of(-z), 1e37f);
+  s = rcp_of(1.0f + e);
   q = e * s;
 }
 
@@ -84,13 +98,14 @@ __device__ __forceinline__ int elem(int lane, int j) {
   return VEC ? 4 * (lane + 32 * (j >> 2)) + (j & 3) : lane + 32 * j;
 }
 
+// -infinity stands for the places past E: their s of 1e-37 is lost in any sum that counts.
 template <int PER, bool VEC>
 __device__ __forceinline__ void load_row(const float* row, int E, int lane, float (&z)[PER]) {
   if (VEC) {
 #pragma unroll
     for (int i = 0; i < PER / 4; ++i) {
       const int e = 4 * (lane + 32 * i);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
       if (e < E) v = __ldg(reinterpret_cast<const float4*>(row + e));
       z[4 * i] = v.x;
       z[4 * i + 1] = v.y;
@@ -99,33 +114,30 @@ __device__ __forceinline__ void load_row(const float* row, int E, int lane, floa
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < PER; ++j) z[j] = lane + 32 * j < E ? __ldg(row + lane + 32 * j) : 0.f;
+    for (int j = 0; j < PER; ++j) z[j] = lane + 32 * j < E ? __ldg(row + lane + 32 * j) : -INFINITY;
   }
 }
 
 // s (the row's scores, or for a low row exp(z - max z), which has the same shares) and
 // q = 1 - sigmoid(z) of this lane's elements, and the row's sum of s.
-template <int PER, bool VEC>
-__device__ __forceinline__ float scores(const float (&z)[PER], int E, int lane, float (&s)[PER], float (&q)[PER]) {
+template <int PER>
+__device__ __forceinline__ float scores(const float (&z)[PER], int E, float (&s)[PER], float (&q)[PER]) {
   float S = 0.f;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    const bool in = elem<VEC>(lane, j) < E;
     sigmoid2(z[j], s[j], q[j]);
-    if (!in) s[j] = q[j] = 0.f;
     S += s[j];
   }
   S = warp_sum(S);
   if (S < LOW_ROW * E) {
-    float m = -INFINITY;
+    float m = z[0];
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (elem<VEC>(lane, j) < E) m = fmaxf(m, z[j]);
+    for (int j = 1; j < PER; ++j) m = fmaxf(m, z[j]);
     m = warp_max(m);
     float acc = 0.f;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      s[j] = elem<VEC>(lane, j) < E && m > -INFINITY ? __expf(z[j] - m) : 0.f;
+      s[j] = m > -INFINITY ? exp_of(z[j] - m) : 0.f;
       acc += s[j];
     }
     S = warp_sum(acc);
@@ -133,17 +145,17 @@ __device__ __forceinline__ float scores(const float (&z)[PER], int E, int lane, 
   return S;
 }
 
-// f - 1 of this lane's experts in sequence b.
-template <int PER, bool VEC>
-__device__ __forceinline__ void load_f(const BalArgs& a, int b, int Tb, int lane, float (&f)[PER]) {
-  const int* c = a.seq_counts + (size_t)b * a.E;
-  const long long even = (long long)a.k * Tb;
-  const float inv = even > 0 ? 1.0f / (float)even : 0.f;
+template <int PER>
+__device__ __forceinline__ float dot(const float (&f)[PER], const float (&s)[PER]) {
+  float F = 0.f;
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int e = elem<VEC>(lane, j);
-    f[j] = e < a.E ? (float)((long long)__ldcg(c + e) * a.E - even) * inv : 0.f;
-  }
+  for (int j = 0; j < PER; ++j) F = fmaf(f[j], s[j], F);
+  return warp_sum(F);
+}
+
+// f - 1 of an expert with c of a sequence's picks, even = k T_b and inv = 1 / even (0 for none).
+__device__ __forceinline__ float load_of(int c, int E, long long even, float inv) {
+  return (float)((long long)c * E - even) * inv;
 }
 
 __global__ void __launch_bounds__(256) k_bal_zero(const BalArgs a) {
@@ -234,9 +246,16 @@ struct Cursor {
     b = seq_of(a, t, lane);
     end = max(t + 1, b < 0 ? seq_at(a, 0) : (b < a.n_seq ? seq_at(a, b + 1) : a.T));
     if (inside(a)) {
+      const int* c = a.seq_counts + (size_t)b * a.E;
       const int Tb = __ldcg(a.seq_tokens + b);
+      const long long even = (long long)a.k * Tb;
+      const float inv_even = Tb > 0 ? 1.0f / (float)even : 0.f;
       inv = Tb > 0 ? 1.0f / (float)Tb : 0.f;
-      load_f<PER, VEC>(a, b, Tb, lane, f);
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int e = elem<VEC>(lane, j);
+        f[j] = e < a.E ? load_of(__ldcg(c + e), a.E, even, inv_even) : 0.f;
+      }
     }
   }
 };
@@ -248,7 +267,16 @@ __device__ __forceinline__ void warp_run(const BalArgs& a, int warp, int& t0, in
   t1 = min(a.T, t0 + per);
 }
 
-// Blocks of an SM by registers: a row's values and the next row's take 4 PER of them.
+// (1 + F_t) / T_b of one row. FP32 is enough for one token's share; the long sum is held in FP64.
+template <int PER>
+__device__ __forceinline__ float row_share(const float (&z)[PER], const float (&f)[PER], float inv, int E) {
+  float s[PER], q[PER];
+  const float S = scores<PER>(z, E, s, q);
+  const float F = dot<PER>(f, s);
+  return S > 0.f ? (1.0f + __fdividef(F, S)) * inv : 0.f;
+}
+
+// Blocks of an SM by registers: a row's values and the next row's take 4 to 5 PER of them.
 template <int PER>
 constexpr int loss_blocks() { return PER > 8 ? 2 : 4; }
 template <int PER>
@@ -280,16 +308,7 @@ __global__ void __launch_bounds__(256, loss_blocks<PER>()) k_bal_loss(const BalA
       load_row<PER, VEC>(a.logits + (size_t)(t + 1) * a.E, a.E, lane, zn);
       firstn = __ldg(a.idx + (size_t)(t + 1) * a.k);
     }
-    if (cur.inside(a) && first >= 0) {
-      float s[PER], q[PER];
-      const float S = scores<PER, VEC>(z, a.E, lane, s, q);
-      float F = 0.f;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) F = fmaf(cur.f[j], s[j], F);
-      F = warp_sum(F);
-      // FP32 is enough for one token's share of 1 + F; the long sum is held in FP64
-      if (S > 0.f) acc += (double)((1.0f + F / S) * cur.inv);
-    }
+    if (cur.inside(a) && first >= 0) acc += (double)row_share<PER>(z, cur.f, cur.inv, a.E);
 #pragma unroll
     for (int j = 0; j < PER; ++j) z[j] = zn[j];
     first = firstn;
@@ -312,122 +331,187 @@ __global__ void __launch_bounds__(256, loss_blocks<PER>()) k_bal_loss(const BalA
   if (lane == 0) *a.loss = (float)(v * ((double)a.alpha / (double)a.n_seq));
 }
 
+// Counts and loss of a small call in one block: the counts stay in shared memory, and one launch replaces three.
+// Its rule (one_block below) is where one SM's share of the work takes no longer than the launches it saves: 300 x 16
+// takes 15 us in three kernels.
+constexpr int ONE_COUNTS = 8192, ONE_ELEMS = 65536, ONE_TOKENS = 1024;
 template <int PER, bool VEC>
-__global__ void __launch_bounds__(256, backward_blocks<PER>()) k_bal_backward(const BalArgs a) {
-  __shared__ float extra_s[8][MAX_E];
+__global__ void __launch_bounds__(1024) k_bal_one(const BalArgs g) {
+  constexpr int AT = PER > 8 ? 1 : 4;  // rows of a warp in flight
+  __shared__ int counts[ONE_COUNTS], tokens[ONE_TOKENS], starts[ONE_TOKENS + 1], seq[ONE_TOKENS];
+  __shared__ double red[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int t0, t1;
-  warp_run(a, warp, t0, t1);
-  float* extra = extra_s[warp];  // routing-weight part of the row's gradient, zero but at its picks
-  for (int e = lane; e < a.E; e += 32) extra[e] = 0.f;
+  for (int i = threadIdx.x; i < g.n_seq * g.E; i += 1024) counts[i] = 0;
+  for (int i = threadIdx.x; i < g.n_seq; i += 1024) tokens[i] = 0;
   pdl_wait();
   pdl_trigger();
-  __syncwarp();
-  const float up = (a.dloss ? __ldg(a.dloss) : 1.0f) * (a.alpha / (float)a.n_seq);
-  const bool mine = lane < a.k;
-  float z[PER];
-  int e = -1;
-  float g = 0.f;
-  if (t0 < t1) {
-    load_row<PER, VEC>(a.logits + (size_t)t0 * a.E, a.E, lane, z);
-    if (mine) e = __ldg(a.idx + (size_t)t0 * a.k + lane);
-    if (mine && a.dw) g = __ldg(a.dw + (size_t)t0 * a.k + lane);
+  const int t = threadIdx.x;  // this thread's token
+  int first = -1;
+  if (t < g.T) first = __ldg(g.idx + (size_t)t * g.k);
+  for (int i = threadIdx.x; i <= g.n_seq; i += 1024) starts[i] = seq_at(g, i);
+  __syncthreads();
+  if (t < g.T) {
+    int lo = -1, hi = g.n_seq + 1;  // the last sequence that starts at or before t
+    while (hi - lo > 1) {
+      const int m = (lo + hi) >> 1;
+      if (starts[m] <= t)
+        lo = m;
+      else
+        hi = m;
+    }
+    const bool counted = lo >= 0 && lo < g.n_seq && first >= 0;
+    seq[t] = counted ? lo : -1;
+    if (counted) {
+      atomicAdd(tokens + lo, 1);
+      for (int j = 0; j < g.k; ++j) {
+        const int e = j ? __ldg(g.idx + (size_t)t * g.k + j) : first;
+        if (e >= 0 && e < g.E) atomicAdd(counts + lo * g.E + e, 1);
+      }
+    }
   }
+  const int per = (g.T + 31) / 32, t0 = min(g.T, warp * per), t1 = min(g.T, t0 + per);
+  float z[AT][PER];
+#pragma unroll
+  for (int i = 0; i < AT; ++i)
+    if (t0 + i < t1) load_row<PER, VEC>(g.logits + (size_t)(t0 + i) * g.E, g.E, lane, z[i]);
+  __syncthreads();
+  for (int i = threadIdx.x; i < g.n_seq * g.E; i += 1024) g.seq_counts[i] = counts[i];
+  for (int i = threadIdx.x; i < g.n_seq; i += 1024) g.seq_tokens[i] = tokens[i];
+  for (int e = threadIdx.x; e < g.E; e += 1024) {
+    int c = 0;
+    for (int b = 0; b < g.n_seq; ++b) c += counts[b * g.E + e];
+    g.counts[e] = c;
+  }
+  int b = -1;
+  float f[PER], inv = 0.f;
+  double acc = 0.0;
+  for (int i0 = t0; i0 < t1; i0 += AT) {
+#pragma unroll
+    for (int i = 0; i < AT; ++i) {
+      if (i0 + i >= t1) break;
+      const int own = seq[i0 + i];
+      if (own >= 0 && own != b) {
+        b = own;
+        const long long even = (long long)g.k * tokens[b];
+        inv = 1.0f / (float)tokens[b];
+        const float inv_even = 1.0f / (float)even;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          const int e = elem<VEC>(lane, j);
+          f[j] = e < g.E ? load_of(counts[b * g.E + e], g.E, even, inv_even) : 0.f;
+        }
+      }
+      if (own >= 0) acc += (double)row_share<PER>(z[i], f, inv, g.E);
+      if (i0 + AT + i < t1) load_row<PER, VEC>(g.logits + (size_t)(i0 + AT + i) * g.E, g.E, lane, z[i]);
+    }
+  }
+  if (lane == 0) red[warp] = acc;
+  __syncthreads();
+  if (warp == 0) {
+    const double v = warp_sum_d(red[lane]);
+    if (lane == 0) *g.loss = (float)(v * ((double)g.alpha / (double)g.n_seq));
+  }
+}
+
+// A warp works on NB tokens at a time: a row each for the loss's part (the next row on its way meanwhile), then the
+// NB tokens' picks side by side, 32 / NB lanes to a token (k <= 8: four tokens; picks of one token at a time would
+// leave three lanes in four idle, and the kernel is bound by instructions before it is bound by memory). A pick
+// adds its part to its place in the row just written.
+template <int PER, bool VEC, int NB>
+__global__ void __launch_bounds__(256, backward_blocks<PER>()) k_bal_backward(const BalArgs a) {
+  constexpr int W = 32 / NB;  // lanes of a token's picks
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = lane / W, pick = lane % W;
+  int t0, t1;
+  warp_run(a, warp, t0, t1);
+  pdl_wait();
+  pdl_trigger();
+  const float up = (a.dloss ? __ldg(a.dloss) : 1.0f) * (a.alpha / (float)a.n_seq);
+  float z[PER];
+  if (t0 < t1) load_row<PER, VEC>(a.logits + (size_t)t0 * a.E, a.E, lane, z);
   Cursor<PER, VEC> cur;
-  for (int t = t0; t < t1; ++t) {
+  for (int t = t0; t < t1;) {
     cur.to(a, t, lane);
-    float zn[PER];
-    int en = -1;
-    float gn = 0.f;
-    if (t + 1 < t1) {  // the next token's row is on its way while this one is worked on
-      load_row<PER, VEC>(a.logits + (size_t)(t + 1) * a.E, a.E, lane, zn);
-      if (mine) en = __ldg(a.idx + (size_t)(t + 1) * a.k + lane);
-      if (mine && a.dw) gn = __ldg(a.dw + (size_t)(t + 1) * a.k + lane);
+    const int nb = min(NB, min(t1, cur.end) - t);  // tokens of one sequence
+    // this lane's pick, of token t + slot
+    int e = -1;
+    if (slot < nb && pick < a.k) e = __ldg(a.idx + (size_t)(t + slot) * a.k + pick);
+    const unsigned pads = __ballot_sync(0xffffffffu, pick == 0 && e < 0);  // bit W i: token i is padding
+    const bool in = e >= 0 && e < a.E && !((pads >> (slot * W)) & 1u) && cur.inside(a);
+    float g = 0.f, zp = -INFINITY;
+    if (a.dw && in) {
+      g = __ldg(a.dw + (size_t)(t + slot) * a.k + pick);
+      zp = __ldg(a.logits + (size_t)(t + slot) * a.E + e);
     }
-    if (cur.inside(a)) {
-      const float* row = a.logits + (size_t)t * a.E;
-      float* out = a.dlogits + (size_t)t * a.E;
-      const bool counted = __shfl_sync(0xffffffffu, e, 0) >= 0;
-      float d[PER];
 #pragma unroll
-      for (int j = 0; j < PER; ++j) d[j] = 0.f;
-      if (counted) {
-        float s[PER], q[PER];
-        const float S = scores<PER, VEC>(z, a.E, lane, s, q);
-        float F = 0.f;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) F = fmaf(cur.f[j], s[j], F);
-        F = warp_sum(F);
-        const float inv = S > 0.f ? 1.0f / S : 0.f;
-        F *= inv;
+    for (int i = 0; i < NB; ++i) {
+      if (i >= nb) break;
+      float zn[PER];
+      if (t + i + 1 < t1) load_row<PER, VEC>(a.logits + (size_t)(t + i + 1) * a.E, a.E, lane, zn);
+      if (cur.inside(a)) {
+        float s[PER], q[PER], d[PER];
+        const float S = scores<PER>(z, a.E, s, q);
+        const float inv = S > 0.f ? rcp_of(S) : 0.f;
+        const float F = dot<PER>(cur.f, s) * inv;
         const float ci = up * cur.inv * inv;
+        const bool pad = (pads >> (i * W)) & 1u;  // selected, not multiplied: a padding row may hold anything
 #pragma unroll
-        for (int j = 0; j < PER; ++j) d[j] = (ci * s[j]) * ((cur.f[j] - F) * q[j]);
-        if (a.dw) {
-          const bool in = e >= 0 && e < a.E;
-          float sp = 0.f, qp = 0.f, zp = -INFINITY;
-          if (in) {
-            zp = __ldg(row + e);
-            sigmoid2(zp, sp, qp);
-          }
-          float add;
-          if (a.renorm) {
-            float W = warp_sum(sp);
-            if (W < LOW_ROW * MAX_TOPK) {  // every pick's score underflows: the same shares from exp(z - max z)
-              const float m = warp_max(zp);
-              sp = in && m > -INFINITY ? __expf(zp - m) : 0.f;
-              W = warp_sum(sp);
-            }
-            const float w = W > 0.f ? sp / W : 0.f;
-            const float D = warp_sum(in ? g * w : 0.f);
-            add = in ? a.routed_scale * w * (g - D) * qp : 0.f;
-          } else {
-            add = in ? a.routed_scale * sp * g * qp : 0.f;
-          }
-          // An expert picked twice: the picks' parts are added in pick order. Each pick signs its expert's
-          // place, and finds another's name there if it is not alone (a match over 32 different values
-          // took longer than the rest of the row: 67 us for 65536 x 256, of 41 million instructions).
-          if (in) reinterpret_cast<int*>(extra)[e] = lane;
-          __syncwarp();
-          const bool shared = in && reinterpret_cast<const int*>(extra)[e] != lane;
-          float sum = add;
-          if (__any_sync(0xffffffffu, shared)) {
-            sum = 0.f;
-            for (int j = 0; j < a.k; ++j) {
-              const float v = __shfl_sync(0xffffffffu, add, j);
-              if (__shfl_sync(0xffffffffu, e, j) == e) sum += v;
-            }
-          }
-          __syncwarp();
-          if (in) extra[e] = sum;
-          __syncwarp();
+        for (int j = 0; j < PER; ++j) d[j] = pad ? 0.f : (ci * s[j]) * ((cur.f[j] - F) * q[j]);
+        float* out = a.dlogits + (size_t)(t + i) * a.E;
+        if (VEC) {
 #pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            const int el = elem<VEC>(lane, j);
-            if (el < a.E) d[j] += extra[el];
+          for (int j = 0; j < PER / 4; ++j) {
+            const int el = 4 * (lane + 32 * j);
+            if (el < a.E)
+              *reinterpret_cast<float4*>(out + el) = make_float4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
           }
-          __syncwarp();
-          if (in) extra[e] = 0.f;
-          __syncwarp();
+        } else {
+#pragma unroll
+          for (int j = 0; j < PER; ++j)
+            if (lane + 32 * j < a.E) out[lane + 32 * j] = d[j];
         }
       }
-      if (VEC) {
 #pragma unroll
-        for (int i = 0; i < PER / 4; ++i) {
-          const int el = 4 * (lane + 32 * i);
-          if (el < a.E)
-            *reinterpret_cast<float4*>(out + el) = make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-          if (lane + 32 * j < a.E) out[lane + 32 * j] = d[j];
-      }
+      for (int j = 0; j < PER; ++j) z[j] = zn[j];
     }
+    if (a.dw && cur.inside(a)) {
+      // sums over a token's lanes
+      auto sum_of = [&](float v) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j) z[j] = zn[j];
-    e = en;
-    g = gn;
+        for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+      };
+      float sp = 0.f, qp = 0.f;
+      if (in) sigmoid2(zp, sp, qp);
+      float add = sp * g * qp;
+      if (a.renorm) {
+        float total = sum_of(sp);
+        if (__any_sync(0xffffffffu, total < LOW_ROW * MAX_TOPK)) {
+          // every score of a token's picks underflows: the same shares from exp(z - max z)
+          float m = zp;
+#pragma unroll
+          for (int o = W / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (total < LOW_ROW * MAX_TOPK) sp = in && m > -INFINITY ? exp_of(zp - m) : 0.f;
+          total = sum_of(sp);
+        }
+        const float w = total > 0.f ? __fdividef(sp, total) : 0.f;
+        add = w * (g - sum_of(g * w)) * qp;
+      }
+      add *= a.routed_scale;
+      // An expert picked twice gets its picks' parts in pick order; each of them writes the same value.
+      float part = 0.f;
+      for (int j = 0; j < a.k; ++j) {
+        const int ej = __shfl_sync(0xffffffffu, e, slot * W + j);
+        const float v = __shfl_sync(0xffffffffu, add, slot * W + j);
+        if (ej == e) part += v;
+      }
+      __syncwarp();  // the rows are written
+      float* place = a.dlogits + (size_t)(t + slot) * a.E + e;
+      float base = 0.f;
+      if (in) base = *place;
+      __syncwarp();
+      if (in) *place = base + part;
+    }
+    t += nb;
   }
 }
 
@@ -444,10 +528,10 @@ constexpr int LOSS_BLOCKS = SMS * loss_blocks<4>();  // the loss kernel's blocks
 constexpr int COUNT_BLOCKS = SMS;
 
 // A launch that may start while the kernel before it drains (each kernel waits for it itself).
-bool launch(void (*kernel)(BalArgs), int grid, cudaStream_t stream, const BalArgs& a) {
+bool launch(void (*kernel)(BalArgs), int grid, cudaStream_t stream, const BalArgs& a, int block = 256) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(block);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -493,7 +577,23 @@ bool launch_loss(const BalArgs& a, cudaStream_t stream) {
 }
 template <int PER, bool VEC>
 bool launch_backward(const BalArgs& a, cudaStream_t stream) {
-  return launch(k_bal_backward<PER, VEC>, row_blocks(a.T, backward_blocks<PER>()), stream, a);
+  const int grid = row_blocks(a.T, backward_blocks<PER>());
+  return a.k <= 8 ? launch(k_bal_backward<PER, VEC, 4>, grid, stream, a) : launch(k_bal_backward<PER, VEC, 2>, grid, stream, a);
+}
+bool one_block(const BalArgs& a) {
+  return a.T <= ONE_TOKENS && a.n_seq <= ONE_TOKENS && (int64_t)a.T * a.E <= ONE_ELEMS && (int64_t)a.n_seq * a.E <= ONE_COUNTS;
+}
+template <int PER, bool VEC>
+bool launch_one(const BalArgs& a, cudaStream_t stream) {
+  return launch(k_bal_one<PER, VEC>, 1, stream, a, 1024);
+}
+// f(PER, VEC) for the row length: elements a lane holds, and whether rows are made of 16-byte pieces.
+template <typename F>
+bool by_row(int E, F f) {
+  if (E % 4) return E <= 128 ? f(std::integral_constant<int, 4>(), std::false_type()) : f(std::integral_constant<int, 16>(), std::false_type());
+  if (E <= 128) return f(std::integral_constant<int, 4>(), std::true_type());
+  if (E <= 256) return f(std::integral_constant<int, 8>(), std::true_type());
+  return f(std::integral_constant<int, 16>(), std::true_type());
 }
 
 }  // namespace
@@ -532,13 +632,13 @@ extern "C" flint_moe_status flint_moe_balance(const flint_moe_config* c, const f
   a.seq_tokens = seq_tokens;
   a.ticket = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + w.ticket);
   a.partial = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + w.partial);
-  bool ok = launch(k_bal_zero, (int)std::min<size_t>(152, ((size_t)n_seq * a.E + 255) / 256), stream, a);
-  if (T > 0) {
-    ok = ok && launch(k_bal_count, std::min(COUNT_BLOCKS, (T + 255) / 256), stream, a);
-    ok = ok && (a.E % 4 != 0 ? launch_loss<16, false>(a, stream)
-                : a.E <= 128 ? launch_loss<4, true>(a, stream)
-                : a.E <= 256 ? launch_loss<8, true>(a, stream)
-                             : launch_loss<16, true>(a, stream));
+  bool ok;
+  if (one_block(a)) {
+    ok = by_row(a.E, [&](auto per, auto vec) { return launch_one<per(), vec()>(a, stream); });
+  } else {
+    ok = launch(k_bal_zero, (int)std::min<size_t>(SMS, ((size_t)n_seq * a.E + 255) / 256), stream, a) &&
+         (T == 0 || (launch(k_bal_count, std::min(COUNT_BLOCKS, (T + 255) / 256), stream, a) &&
+                     by_row(a.E, [&](auto per, auto vec) { return launch_loss<per(), vec()>(a, stream); })));
   }
   return ok ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
 }
@@ -574,9 +674,6 @@ extern "C" flint_moe_status flint_moe_balance_backward(const flint_moe_config* c
   a.dloss = dloss;
   a.dw = dw;
   a.dlogits = dlogits;
-  const bool ok = a.E % 4 != 0 ? launch_backward<16, false>(a, stream)
-                  : a.E <= 128 ? launch_backward<4, true>(a, stream)
-                  : a.E <= 256 ? launch_backward<8, true>(a, stream)
-                               : launch_backward<16, true>(a, stream);
+  const bool ok = by_row(a.E, [&](auto per, auto vec) { return launch_backward<per(), vec()>(a, stream); });
   return ok ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
 }

@@ -407,21 +407,26 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
 // [R x 128 columns] for both halves of h. The (tile, 128 columns) items are one
 // list, and each CTA takes a run of it, so that a tile's h is loaded once per run.
 // Bound by the base rows it reads and the rows it writes: those go through each
-// epilogue warp's own ring of shared memory (32 rows x 64 columns an item, up
-// to three items ahead), without any barrier.
-//   warp 0     weights and a tile's h (TMA)
-//   warp 1     the MMAs into two accumulators of 128 columns
-//   warps 2-9  base rows (asynchronous copies); tensor memory + base -> bf16 in
-//              place in shared memory -> whole 128-byte pieces of rows
+// epilogue warp's own ring of shared memory (32 rows x 32 columns an item, up
+// to three items ahead), without any barrier. Sixteen epilogue warps: with eight
+// of twice the width an item took 3500 cycles at 42 % of the issue slots.
+//   warp 0      weights and a tile's h (TMA)
+//   warp 1      the MMAs into two accumulators of 128 columns
+//   warps 2-17  base rows (asynchronous copies); tensor memory + base -> bf16 in
+//               place in shared memory -> 64-byte pieces of rows
 // ---------------------------------------------------------------------------
-constexpr int EXP_THREADS = 320;
-constexpr int YSLOT = 32 * 128;  // one warp's rows of an item
+constexpr int EXP_WARPS = 16;  // epilogue warps
+constexpr int EXP_THREADS = 64 + 32 * EXP_WARPS;
+constexpr int YSLOT = 32 * 64;  // one warp's rows of an item
+// Byte offset of 16-byte piece c of row r of a warp's rows: two rows to 128 bytes, pieces swizzled by row pair, so
+// that eight rows' same pieces, and two rows' all pieces, each touch every bank once.
+__device__ __forceinline__ uint32_t yoff(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
 __host__ __device__ inline int exp_hbufs(int R) { return R > 64 ? 1 : 2; }
 __host__ __device__ inline int exp_yslots(int R) { return R > 64 ? 3 : 4; }
 __host__ __device__ inline int exp_wbytes(int R) { return R > 64 ? 2 * BOX : BOX; }      // one stage's weights
 __host__ __device__ inline int exp_hbytes(int R) { return R > 64 ? 4 * BOX : 2 * BOX; }  // hi and lo of a tile
 __host__ __device__ inline size_t exp_smem(int R) {
-  return 1024 + (size_t)2 * exp_wbytes(R) + (size_t)exp_hbufs(R) * exp_hbytes(R) + (size_t)exp_yslots(R) * 8 * YSLOT;
+  return 1024 + (size_t)2 * exp_wbytes(R) + (size_t)exp_hbufs(R) * exp_hbytes(R) + (size_t)exp_yslots(R) * EXP_WARPS * YSLOT;
 }
 
 template <bool GRAD, bool WIDE>  // WIDE: rank above 64
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
       mbar_init(&full[b], 1);
       mbar_init(&empty[b], 1);
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);
+      mbar_init(&acc_empty[b], EXP_WARPS);
       mbar_init(&h_full[b], 1);
       mbar_init(&h_empty[b], 1);
     }
@@ -554,40 +559,37 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
     }
     for (int r = (m > 2 ? m - 2 : 0); r < m; ++r) mbar_drain(&acc_full[r & 1], (r >> 1) & 1);
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;  // tensor-memory lanes 32 q .., columns 64 half ..
-    const int rsub = lane >> 3, c8 = (lane & 7) * 8;  // this lane's place in a copy of four rows
+    const int q = warp & 3, c0 = ((warp - 2) >> 2) * 32;  // tensor-memory lanes 32 q .., columns c0 .. of an item
+    const int rsub = lane >> 2, c8 = (lane & 3) * 8;      // this lane's place in a copy of eight rows
     const uint32_t ys = ybase + (uint32_t)((warp - 2) * YS * YSLOT);
     uint8_t* const yp = basep + (ys - base);
-    // Copies run LY items ahead: item (ptile, psub) goes to slot `pslot`, for rows i * 4 + rsub of this warp's 32.
+    // Copies run LY items ahead: item (ptile, psub) goes to slot `pslot`, for rows i * 8 + rsub of this warp's 32.
     int ptile = tile0, psub = sub0, pslot = 0, pcount = 0, left = u1 - u0;
-    int ptok[8];
-    auto rows_of = [&](int tile, int (&t)[8]) {
+    int64_t pat[4];  // first elements of those rows
+    auto rows_of = [&](int tile, int64_t (&at)[4]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = __ldcg(a.rowmap + tile * TM + q * 32 + i * 4 + rsub);
+      for (int i = 0; i < 4; ++i) at[i] = (int64_t)__ldcg(a.rowmap + tile * TM + q * 32 + i * 8 + rsub) * a.ldo;
     };
     if (left > 0) {
       pcount = __ldcg(&a.tiles[ptile].y);
-      rows_of(ptile, ptok);
+      rows_of(ptile, pat);
     }
-    uint32_t off[2];  // this lane's place in rows 0 and 4, 32 bytes swizzled apart
-    off[0] = sw128_off(rsub, c8);
-    off[1] = sw128_off(4 + rsub, c8);
+    const uint32_t off = yoff(rsub, lane & 3);  // this lane's place in eight rows (512 bytes)
     auto fetch = [&]() {
       if (a.in && left > 0) {
         if (psub == nsub) {
           psub = 0;
           ++ptile;
           pcount = __ldcg(&a.tiles[ptile].y);
-          rows_of(ptile, ptok);
+          rows_of(ptile, pat);
         }
-        const int col = psub * 128 + half * 64;
+        const int col = psub * 128 + c0;
         if (q * 32 < pcount && col < D) {
           const uint32_t slot = ys + (uint32_t)pslot * YSLOT;
           const bool in = col + c8 < D;
           const uint16_t* src = a.in + (in ? col + c8 : 0);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            cp_async16(slot + off[i & 1] + (i >> 1) * 1024, src + (int64_t)ptok[i] * a.ldo, in ? 16u : 0u);
+          for (int i = 0; i < 4; ++i) cp_async16(slot + off + i * 512, src + pat[i], in ? 16u : 0u);
         }
         ++psub;
         --left;
@@ -596,7 +598,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
       cp_async_commit();
     };
     int m = 0, tile = tile0, sub = sub0, slot_i = 0;
-    int tok[8];
+    int64_t at[4];
     int2 tl = make_int2(-1, 0);
 #pragma unroll
     for (int i = 0; i < LY; ++i) fetch();
@@ -608,20 +610,18 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
       }
       if (u == u0 || sub == 0) {
         tl = __ldcg(a.tiles + tile);
-        rows_of(tile, tok);
+        rows_of(tile, at);
       }
-      const int col = sub * 128 + half * 64;
+      const int col = sub * 128 + c0;
       const bool mma = tl.x >= 0, live = q * 32 < tl.y && col < D;  // live: this warp's rows and columns hold something
       const int b = m & 1;
-      uint32_t w[2][32];
+      uint32_t w[32];
       if (mma) {
         bool ok = wait_ab(&acc_full[b], (m >> 1) & 1, abort, status);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         if (live) {
-          const uint32_t acc = tmem + b * 128 + half * 64 + ((uint32_t)(q * 32) << 16);
-          tc_ld32_async(acc, w[0]);
-          tc_ld32_async(acc + 32, w[1]);
+          tc_ld32_async(tmem + b * 128 + c0 + ((uint32_t)(q * 32) << 16), w);
           tc_wait_ld();
         }
         tc_fence_before();
@@ -630,19 +630,18 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
         ++m;
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) w[0][j] = w[1][j] = 0u;
+        for (int j = 0; j < 32; ++j) w[j] = 0u;
       }
       cp_async_wait<LY>();
       __syncwarp();
       if (live) {
         uint8_t* slot = yp + slot_i * YSLOT;
-        uint8_t* mine = slot + lane * 128;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint4* p = reinterpret_cast<uint4*>(mine + ((lane & 7) << 4 ^ j << 4));
+        for (int j = 0; j < 4; ++j) {
+          uint4* p = reinterpret_cast<uint4*>(slot + yoff(lane, j));
           uint4 y = make_uint4(0u, 0u, 0u, 0u);
           if (a.in) y = *p;
-          const uint32_t* d = &w[j >> 2][8 * (j & 3)];
+          const uint32_t* d = &w[8 * j];
           y.x = f2b2(bf16lo(y.x) + __uint_as_float(d[0]), bf16hi(y.x) + __uint_as_float(d[1]));
           y.y = f2b2(bf16lo(y.y) + __uint_as_float(d[2]), bf16hi(y.y) + __uint_as_float(d[3]));
           y.z = f2b2(bf16lo(y.z) + __uint_as_float(d[4]), bf16hi(y.z) + __uint_as_float(d[5]));
@@ -652,11 +651,11 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
         __syncwarp();
         if (col + c8 < D) {
           uint16_t* dst = a.out + col + c8;
-          const int rows = tl.y - q * 32 - rsub;  // row i * 4 + rsub is one of the tile's
+          const int rows = tl.y - q * 32 - rsub;  // row i * 8 + rsub is one of the tile's
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 y = lds128(slot + off[i & 1] + (i >> 1) * 1024);
-            if (i * 4 < rows) *reinterpret_cast<uint4*>(dst + (int64_t)tok[i] * a.ldo) = y;
+          for (int i = 0; i < 4; ++i) {
+            const uint4 y = lds128(slot + off + i * 512);
+            if (i * 8 < rows) *reinterpret_cast<uint4*>(dst + at[i]) = y;
           }
         }
         __syncwarp();  // read before the slot's next copies
@@ -1109,12 +1108,13 @@ bool run_plan(const Args& p, cudaStream_t stream) {
          launch(k_lora_plan, dim3(1), 1024, plan_smem(p.n), 0, stream, p);
 }
 
-// h (and with `grads` g) of every tile. CTAs of a tile's cluster: as many as keep two CTAs on every SM busy, were
-// the tiles half filled on average, and no more than a CTA has k-blocks to take.
+// h (and with `grads` g) of every tile. CTAs of a tile's cluster: as many as run at once, two on an SM (4096 tokens of
+// 2048 x 2048, 49 tiles at most: 24.9 us a call with clusters of 4, 27.2 of 2, 27.7 of 8), and no more than a CTA has
+// k-blocks to take.
 bool run_shrink(const Args& p, const Maps& m, bool grads, cudaStream_t stream) {
   const int kb = (std::min(p.K, grads ? p.N : p.K) + BK - 1) / BK, per = p.max_tiles * (grads ? 2 : 1);
   int S = 1;
-  while (S < 8 && per * S * 2 <= 4 * sm_count() && S * 2 <= kb) S *= 2;
+  while (S < 8 && per * S * 2 <= 2 * sm_count() && S * 2 <= kb) S *= 2;
   return want_smem(k_lora_shrink, g_shrink, shrink_smem(FLINT_LORA_MAX_RANK)) &&
          launch(k_lora_shrink, dim3(S, p.max_tiles, grads ? 2 : 1), SHR_THREADS, shrink_smem(p.R), S, stream, p, m);
 }
