@@ -79,6 +79,20 @@ def test_backward(T, K, N, R, n):
     assert torch.equal(dA, got[1]) and torch.equal(dB, got[2])
 
 
+@pytest.mark.parametrize("T,K,N,R,n,run", [(700, 264, 328, 16, 3, 233), (1500, 72, 1000, 80, 2, 700), (640, 128, 40, 8, 5, 32),
+                                           (520, 200, 96, 64, 4, 47), (300, 64, 264, 24, 2, 16)])
+def test_runs_of_neighbouring_tokens(T, K, N, R, n, run):
+    """Requests of `run` tokens each, so that tiles hold whole runs, parts of several and ragged ends: rows that move
+    in boxes beside rows that are gathered."""
+    p = Pool(T, K, N, R, n, 17 * T, [(t // run) % (n + 1) - 1 for t in range(T)]).to(DEV)
+    check(apply(p, p.d_y), *p.expect_apply(f64(p.y)), "runs")
+    inplace = p.d_y.clone()
+    assert torch.equal(apply(p, inplace, inplace), apply(p, p.d_y))
+    refs, tols = p.expect_backward()
+    for v, ref, tol, label in zip(backward(p, p.d_dx), refs, tols, ("dx", "dA", "dB")):
+        check(v, ref, tol, label)
+
+
 @pytest.mark.parametrize("T", [5, 200])
 def test_no_base_means_zero(T):
     p = Pool(T, 256, 264, 16, 3, 3).to(DEV)

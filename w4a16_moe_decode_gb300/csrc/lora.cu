@@ -54,6 +54,9 @@ struct Maps {
   CUtensorMap a;     // A [n][R][K]: boxes 64 x Rp
   CUtensorMap b;     // B [n][N][R]: boxes 64 x 64
   CUtensorMap h, g;  // [2 * max_tiles * 128][R], boxes 64 x 64
+  // Token rows, for runs of neighbouring tokens: boxes of 64 columns x 32 rows (shrink) and x 16 (gradients), and
+  // of 32 columns x 32 rows in the 64-byte swizzle (base and output rows)
+  CUtensorMap x32, dy32, x16, dy16, in, out;
 };
 
 __device__ __forceinline__ uint16_t f2b(float v) {
@@ -214,9 +217,10 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// Token rows come in any order, so they are gathered with 16-byte asynchronous
-// copies that arrive on the stage's mbarrier by themselves, eight lanes to a row's 128 bytes (TMA's four-row gather delivered one
-// such group every 50 to 60 ns and SM, 1.2 TB/s over the card, whatever the order).
+// Token rows: a warp whose rows are neighbouring tokens (a request's prompt) moves them with one TMA box; others,
+// in any order, are gathered with 16-byte asynchronous copies that arrive on the stage's mbarrier by themselves.
+// (TMA's four-row gather delivered one such group every 50 to 60 ns and SM, 1.2 TB/s over the card, whatever the
+// order; base and output rows by 16-byte copies and stores only took 69 us for 8192 tokens of 2048 x 8192.)
 //
 // Shrink: h = s A x of one tile (z = 0) or g = s B^T dy (z = 1), [128 x D] times
 // [D x R] on the tensor cores. A cluster of S CTAs shares a tile; CTA s takes a
@@ -291,6 +295,10 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
     const int ld = grad ? a.lddy : a.ldx;
     const int c8 = (lane & 7) * 8;
     const bool any = warp * 32 < tl.y;
+    // 32 neighbouring tokens (a group's tokens are in ascending order): one box of them
+    const int tok0 = __shfl_sync(0xffffffffu, tok[0], 0);
+    const bool box = warp * 32 + 32 <= tl.y && __shfl_sync(0xffffffffu, tok[7], 31) - tok0 == 31;
+    const CUtensorMap* xm = grad ? &maps.dy32 : &maps.x32;
     uint32_t dst[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) dst[i] = base + sw128_off(warp * 32 + i * 4 + (lane >> 3), c8);
@@ -298,6 +306,14 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
       const int s = i % SHR_STAGES, col = (kb0 + i) * BK;
       const bool ok = i < SHR_STAGES || wait_ab(&empty[s], ((i / SHR_STAGES) - 1) & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
+      if (box) {
+        if (lane == 0) {
+          mbar_expect_tx(&full[s], 32 * 128);
+          tma_load_2d(base + s * stage + warp * 32 * 128, xm, col, tok0, &full[s]);
+        }
+        mbar_arrive(&full[s]);
+        continue;
+      }
       if (any) {
         const bool in = col + c8 < D;
         const uint16_t* at = src + (in ? col + c8 : 0);
@@ -433,10 +449,11 @@ template <bool GRAD, bool WIDE>  // WIDE: rank above 64
 __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, const __grid_constant__ Maps maps) {
   extern __shared__ uint8_t dsmem[];
   __shared__ uint64_t full[2], empty[2], acc_full[2], acc_empty[2], h_full[2], h_empty[2];
+  __shared__ uint64_t y_full[EXP_WARPS][4];  // a warp's slots filled by TMA
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   constexpr int ANY_R = WIDE ? 128 : 64;
-  constexpr int HB = WIDE ? 1 : 2, nbox = WIDE ? 2 : 1, YS = WIDE ? 3 : 4, LY = YS - 1;
+  constexpr int HB = WIDE ? 1 : 2, nbox = WIDE ? 2 : 1, YS = WIDE ? 3 : 4, LY = YS - 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
   uint8_t* const basep = dsmem + (base - smem_addr(dsmem));
@@ -454,6 +471,8 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
       mbar_init(&h_full[b], 1);
       mbar_init(&h_empty[b], 1);
     }
+    for (int w = 0; w < EXP_WARPS; ++w)
+      for (int i = 0; i < YS; ++i) mbar_init(&y_full[w][i], 1);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -563,33 +582,48 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
     const int rsub = lane >> 2, c8 = (lane & 3) * 8;      // this lane's place in a copy of eight rows
     const uint32_t ys = ybase + (uint32_t)((warp - 2) * YS * YSLOT);
     uint8_t* const yp = basep + (ys - base);
-    // Copies run LY items ahead: item (ptile, psub) goes to slot `pslot`, for rows i * 8 + rsub of this warp's 32.
-    int ptile = tile0, psub = sub0, pslot = 0, pcount = 0, left = u1 - u0;
-    int64_t pat[4];  // first elements of those rows
-    auto rows_of = [&](int tile, int64_t (&at)[4]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) at[i] = (int64_t)__ldcg(a.rowmap + tile * TM + q * 32 + i * 8 + rsub) * a.ldo;
+    uint64_t* const ybar = y_full[warp - 2];
+    // Copies run LY items ahead: item (ptile, psub) goes to slot `pslot`, this warp's rows being tokens `p`. Two slots
+    // more than that, so that a slot's last output rows have left it when it is filled again.
+    int ptile = tile0, psub = sub0, pslot = 0, left = a.in ? u1 - u0 : 0;
+    struct Rows {
+      int tok[4];  // tokens of rows i * 8 + rsub
+      int first;   // all 32 rows are the tokens from here on, or -1
+      int count;   // rows of the warp that are the tile's
     };
-    if (left > 0) {
-      pcount = __ldcg(&a.tiles[ptile].y);
-      rows_of(ptile, pat);
-    }
+    auto rows_of = [&](int tile, Rows& r) {
+      const int count = __ldcg(&a.tiles[tile].y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.tok[i] = __ldcg(a.rowmap + tile * TM + q * 32 + i * 8 + rsub);
+      const int lo = __shfl_sync(0xffffffffu, r.tok[0], 0), hi = __shfl_sync(0xffffffffu, r.tok[3], 31);
+      r.count = count - q * 32;
+      r.first = r.count >= 32 && hi - lo == 31 ? lo : -1;  // (a group's tokens are in ascending order)
+    };
+    Rows p = {};
+    if (left > 0) rows_of(ptile, p);
     const uint32_t off = yoff(rsub, lane & 3);  // this lane's place in eight rows (512 bytes)
+    uint32_t phase = 0;                         // bit s: parity of slot s's next fill by TMA
     auto fetch = [&]() {
-      if (a.in && left > 0) {
+      if (left > 0) {
         if (psub == nsub) {
           psub = 0;
           ++ptile;
-          pcount = __ldcg(&a.tiles[ptile].y);
-          rows_of(ptile, pat);
+          rows_of(ptile, p);
         }
         const int col = psub * 128 + c0;
-        if (q * 32 < pcount && col < D) {
+        if (p.count > 0 && col < D) {
           const uint32_t slot = ys + (uint32_t)pslot * YSLOT;
-          const bool in = col + c8 < D;
-          const uint16_t* src = a.in + (in ? col + c8 : 0);
+          if (p.first >= 0) {
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&ybar[pslot], YSLOT);
+              tma_load_2d(slot, &maps.in, col, p.first, &ybar[pslot]);
+            }
+          } else {
+            const bool in = col + c8 < D;
+            const uint16_t* src = a.in + (in ? col + c8 : 0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) cp_async16(slot + off + i * 512, src + pat[i], in ? 16u : 0u);
+            for (int i = 0; i < 4; ++i) cp_async16(slot + off + i * 512, src + (int64_t)p.tok[i] * a.ldo, in ? 16u : 0u);
+          }
         }
         ++psub;
         --left;
@@ -598,26 +632,26 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
       cp_async_commit();
     };
     int m = 0, tile = tile0, sub = sub0, slot_i = 0;
-    int64_t at[4];
+    Rows r = {};
     int2 tl = make_int2(-1, 0);
 #pragma unroll
     for (int i = 0; i < LY; ++i) fetch();
     for (int u = u0; u < u1; ++u, ++sub) {
-      fetch();
       if (sub == nsub) {
         sub = 0;
         ++tile;
       }
       if (u == u0 || sub == 0) {
         tl = __ldcg(a.tiles + tile);
-        rows_of(tile, at);
+        rows_of(tile, r);
       }
       const int col = sub * 128 + c0;
-      const bool mma = tl.x >= 0, live = q * 32 < tl.y && col < D;  // live: this warp's rows and columns hold something
+      const bool mma = tl.x >= 0, live = r.count > 0 && col < D;  // live: this warp's rows and columns hold something
       const int b = m & 1;
       uint32_t w[32];
+      bool ok = true;
       if (mma) {
-        bool ok = wait_ab(&acc_full[b], (m >> 1) & 1, abort, status);
+        ok = wait_ab(&acc_full[b], (m >> 1) & 1, abort, status);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         if (live) {
@@ -626,11 +660,22 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[b]);  // the accumulator is free for the MMAs
+        if (lane == 0) {
+          mbar_arrive(&acc_empty[b]);  // the accumulator is free for the MMAs
+          bulk_wait_read<1>();         // the output of two items ago has left the slot that is filled next
+        }
         ++m;
       } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) w[j] = 0u;
+        if (lane == 0) bulk_wait_read<1>();
+      }
+      __syncwarp();
+      fetch();
+      if (live && a.in && r.first >= 0) {
+        ok = wait_ab(&ybar[slot_i], (phase >> slot_i) & 1, abort, status);
+        phase ^= 1u << slot_i;
+        if (!__all_sync(0xffffffffu, ok)) break;
       }
       cp_async_wait<LY>();
       __syncwarp();
@@ -638,31 +683,41 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
         uint8_t* slot = yp + slot_i * YSLOT;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint4* p = reinterpret_cast<uint4*>(slot + yoff(lane, j));
+          uint4* at = reinterpret_cast<uint4*>(slot + yoff(lane, j));
           uint4 y = make_uint4(0u, 0u, 0u, 0u);
-          if (a.in) y = *p;
+          if (a.in) y = *at;
           const uint32_t* d = &w[8 * j];
           y.x = f2b2(bf16lo(y.x) + __uint_as_float(d[0]), bf16hi(y.x) + __uint_as_float(d[1]));
           y.y = f2b2(bf16lo(y.y) + __uint_as_float(d[2]), bf16hi(y.y) + __uint_as_float(d[3]));
           y.z = f2b2(bf16lo(y.z) + __uint_as_float(d[4]), bf16hi(y.z) + __uint_as_float(d[5]));
           y.w = f2b2(bf16lo(y.w) + __uint_as_float(d[6]), bf16hi(y.w) + __uint_as_float(d[7]));
-          *p = y;
+          *at = y;
         }
-        __syncwarp();
-        if (col + c8 < D) {
-          uint16_t* dst = a.out + col + c8;
-          const int rows = tl.y - q * 32 - rsub;  // row i * 8 + rsub is one of the tile's
+        if (r.first >= 0) {
+          fence_proxy_async();  // these stores -> visible to TMA
+          __syncwarp();
+          if (lane == 0) tma_store_2d(&maps.out, col, r.first, ys + slot_i * YSLOT);
+        } else {
+          __syncwarp();
+          if (col + c8 < D) {
+            uint16_t* dst = a.out + col + c8;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 y = lds128(slot + off + i * 512);
-            if (i * 8 < rows) *reinterpret_cast<uint4*>(dst + at[i]) = y;
+            for (int i = 0; i < 4; ++i) {
+              const uint4 y = lds128(slot + off + i * 512);
+              if (i * 8 + rsub < r.count) *reinterpret_cast<uint4*>(dst + (int64_t)r.tok[i] * a.ldo) = y;
+            }
           }
+          fence_proxy_async();  // these accesses come before a box that may fill the slot next
         }
-        __syncwarp();  // read before the slot's next copies
       }
+      if (lane == 0) bulk_commit();
       slot_i = slot_i + 1 == YS ? 0 : slot_i + 1;
     }
     cp_async_wait<0>();
+    if (lane == 0) bulk_wait_all();
+    // after a failed wait, boxes may still be on their way into this warp's slots
+    if (*abort && lane == 0)
+      for (int i = 0; i < YS; ++i) mbar_drain(&ybar[i], (phase >> i) & 1);
   }
   tc_fence_before();
   __syncthreads();
@@ -716,6 +771,7 @@ __global__ void __launch_bounds__(DW_THREADS, 2) k_lora_dw(const Args a, const _
   const int D = is_b ? a.N : a.K, col0 = (is_b ? slab - a.slabs_a : slab) * 128;
   const int last = __ldcg(a.tiles + ch.y + ch.z - 1).y;
   const int steps = 2 * (ch.z - 1) + (last > 64 ? 2 : 1);  // half tiles of 64 tokens
+  const int rows = TM * (ch.z - 1) + last;
   const uint32_t cols = tmem_cols(a.Rp);
   if (warp == 5) tmem_alloc(&tmem_base, cols);
   tc_fence_before();
@@ -730,18 +786,31 @@ __global__ void __launch_bounds__(DW_THREADS, 2) k_lora_dw(const Args a, const _
     const bool in = col0 + c8 < D;
     src += in ? col0 + c8 : 0;
     const int* map = a.rowmap + ch.y * TM + warp * 16 + (lane & 15);
+    const CUtensorMap* xm = is_b ? &maps.dy16 : &maps.x16;
+    const int boxes = col0 + 64 < D ? 2 : 1;  // 64-column halves that hold columns at all
     int tok = __ldcg(map);
     for (int i = 0; i < steps; ++i) {
       const int s = i % ST;
       const int next = i + 1 < steps ? __ldcg(map + (i + 1) * 64) : 0;
       const bool ok = i < ST || wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
-      const uint32_t xs = base + s * stage + (lane & 8 ? HALF : 0);
+      const uint32_t xs = base + s * stage;
+      const int tok0 = __shfl_sync(0xffffffffu, tok, 0);
+      // 16 neighbouring tokens (ascending, none of them a repeat): boxes of them
+      if (i * 64 + warp * 16 + 16 <= rows && __shfl_sync(0xffffffffu, tok, 15) - tok0 == 15) {
+        if (lane == 0) {
+          mbar_expect_tx(&full[s], boxes * 16 * 128);
+          for (int y = 0; y < boxes; ++y) tma_load_2d(xs + y * HALF + warp * 16 * 128, xm, col0 + 64 * y, tok0, &full[s]);
+        }
+        mbar_arrive(&full[s]);
+        tok = next;
+        continue;
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int r = 2 * j + (lane >> 4);
         const int t = __shfl_sync(0xffffffffu, tok, r);
-        cp_async16(xs + sw128_off(warp * 16 + r, c8 & 63), src + (int64_t)t * ld, in ? 16u : 0u);
+        cp_async16(xs + (lane & 8 ? HALF : 0) + sw128_off(warp * 16 + r, c8 & 63), src + (int64_t)t * ld, in ? 16u : 0u);
       }
       cp_async_arrive(&full[s]);
       tok = next;
@@ -1062,12 +1131,26 @@ bool map_low(CUtensorMap* m, const uint16_t* p, int R, int max_tiles) {
   return encode_bf16(m, p, 2, dims, strides, box);
 }
 
+// Rows of `cols` bf16 values ld apart, in boxes of bcols x brows.
+bool map_rows(CUtensorMap* m, const uint16_t* p, int cols, int ld, int rows, int bcols, int brows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)bcols, (cuuint32_t)brows};
+  return encode_bf16(m, p, 2, dims, strides, box, bcols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 bool make_maps(Maps* m, const flint_lora* l, const Args& p) {
   if (!map_pool(&m->a, l->a, p.K, p.R, p.n, p.Rp) || !map_pool(&m->b, l->b, p.R, p.N, p.n, 64) ||
       !map_low(&m->h, p.h, p.R, p.max_tiles))
     return false;
-  m->g = m->h;
-  return !p.g || map_low(&m->g, p.g, p.R, p.max_tiles);
+  m->g = m->dy32 = m->x16 = m->dy16 = m->in = m->out = m->h;
+  const int D = p.g ? p.K : p.N;  // columns of the base and output rows
+  if (!map_rows(&m->x32, p.x, p.K, p.ldx, p.T, 64, 32)) return false;
+  if (p.g && (!map_low(&m->g, p.g, p.R, p.max_tiles) || !map_rows(&m->dy32, p.dy, p.N, p.lddy, p.T, 64, 32) ||
+              !map_rows(&m->x16, p.x, p.K, p.ldx, p.T, 64, 16) || !map_rows(&m->dy16, p.dy, p.N, p.lddy, p.T, 64, 16)))
+    return false;
+  if (p.in && !map_rows(&m->in, p.in, D, p.ldo, p.T, 32, 32)) return false;
+  return !p.out || map_rows(&m->out, p.out, D, p.ldo, p.T, 32, 32);
 }
 
 // Opts a kernel in to its dynamic shared memory, once for each device.
