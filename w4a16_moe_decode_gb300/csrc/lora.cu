@@ -140,26 +140,31 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const Args a) {
   };
   load(t0);
   __syncthreads();
+  int place[PB];  // of the last batch's tokens within their warp's part of the group
   for (int i = t0; i < t1; i += 32 * PB) {
     if (i > t0) load(i);
 #pragma unroll
     for (int j = 0; j < PB; ++j) {
       if (i + 32 * j >= t1) break;
       const unsigned same = __match_any_sync(0xffffffffu, g[j]);
-      if (g[j] >= 0 && lane == __ffs(same) - 1) mine[g[j]] += __popc(same);
+      const int rank = __popc(same & ((1u << lane) - 1));
+      if (g[j] >= 0) place[j] = mine[g[j]] + rank;
+      __syncwarp();
+      if (g[j] >= 0 && rank == 0) mine[g[j]] += __popc(same);
       __syncwarp();
     }
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < G; c += 1024) {
-    int at = 0;
-#pragma unroll 8
-    for (int w = 0; w < 32; ++w) {
-      const int v = hist[w * G + c];
-      hist[w * G + c] = at;
-      at += v;
+  for (int c = warp; c < G; c += 32) {  // the warps' counts of a group -> their first places in it
+    const int v = hist[lane * G + c];
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
     }
-    cnt[c] = c == a.n && !a.with_none ? 0 : at;
+    hist[lane * G + c] = inc - v;
+    if (lane == 31) cnt[c] = c == a.n && !a.with_none ? 0 : inc;
   }
   __syncthreads();
   auto tiles_of = [&](int c) { return (cnt[c] + TM - 1) / TM; };
@@ -168,18 +173,23 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const Args a) {
   if (warp == 1 && a.chunks) warp_scan(G, lane, cf, chunks_of);
   if (warp == 2 && a.chunks) warp_scan(G, lane, sf, [&](int c) { return chunks_of(c) > 1 ? chunks_of(c) : 0; });
   __syncthreads();
+  const bool again = L > 32 * PB;  // more than one batch: only the last one's places are still known
   for (int i = t0; i < t1; i += 32 * PB) {
-    if (L > 32 * PB) load(i);  // a run of one batch is still in registers
+    if (again) load(i);
 #pragma unroll
     for (int j = 0; j < PB; ++j) {
       if (i + 32 * j >= t1) break;
-      const unsigned same = __match_any_sync(0xffffffffu, g[j]);
-      const int rank = __popc(same & ((1u << lane) - 1));
       int at = 0;
-      if (g[j] >= 0) at = mine[g[j]] + rank;
-      __syncwarp();
-      if (g[j] >= 0 && rank == 0) mine[g[j]] += __popc(same);
-      __syncwarp();
+      if (again) {
+        const unsigned same = __match_any_sync(0xffffffffu, g[j]);
+        const int rank = __popc(same & ((1u << lane) - 1));
+        if (g[j] >= 0) at = mine[g[j]] + rank;
+        __syncwarp();
+        if (g[j] >= 0 && rank == 0) mine[g[j]] += __popc(same);
+        __syncwarp();
+      } else if (g[j] >= 0) {
+        at = mine[g[j]] + place[j];
+      }
       if (g[j] >= 0 && at < cnt[g[j]]) {  // (no place for tokens without an adapter where they need none)
         const int t = i + 32 * j + lane;
         a.rowmap[tf[g[j]] * TM + at] = t;
@@ -233,11 +243,21 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const Args a) {
 //   warp 5     the MMAs (A stored [R][K] is K-major; B stored [N][R] has R
 //              contiguous, an MN-major operand: no transposed copy)
 // ---------------------------------------------------------------------------
-constexpr int SHR_STAGES = 4;
 constexpr int SHR_THREADS = 192;
+constexpr int SHR_MOST = 6;  // stages at most
 
-__host__ __device__ inline int shrink_wbytes(int R) { return R > 64 ? 2 * HALF : HALF; }
-__host__ __device__ inline size_t shrink_smem(int R) { return 1024 + (size_t)SHR_STAGES * (BOX + shrink_wbytes(R)); }
+// One stage's weights: Rp rows of A, or 64 rows of B in 64-column boxes; as many stages as leave room for two CTAs
+// on an SM (one for ranks above 64).
+__host__ __device__ inline int shrink_wbytes(int R, bool grads) {
+  return R > 64 ? 2 * HALF : (grads ? HALF : ((R + 15) & ~15) * 128);
+}
+__host__ __device__ inline int shrink_stages(int R, bool grads) {
+  const int n = (R > 64 ? 220 * 1024 : 111 * 1024) / (BOX + shrink_wbytes(R, grads));
+  return n < SHR_MOST ? n : SHR_MOST;
+}
+__host__ __device__ inline size_t shrink_smem(int R, bool grads) {
+  return 1024 + (size_t)shrink_stages(R, grads) * (BOX + shrink_wbytes(R, grads));
+}
 __host__ __device__ inline uint32_t tmem_cols(int c) { return c <= 32 ? 32 : c <= 64 ? 64 : c <= 128 ? 128 : 256; }
 
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
@@ -251,7 +271,7 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
 
 __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, const __grid_constant__ Maps maps) {
   extern __shared__ uint8_t dsmem[];
-  __shared__ uint64_t full[SHR_STAGES], empty[SHR_STAGES], acc_full;
+  __shared__ uint64_t full[SHR_MOST], empty[SHR_MOST], acc_full;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -259,8 +279,10 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
   uint8_t* const basep = dsmem + (base - smem_addr(dsmem));
   volatile int* abort = &abort_flag;
   int* status = a.hdr + H_STATUS;
+  const bool grads = gridDim.z > 1;
+  const int ST = shrink_stages(a.R, grads), stage = BOX + shrink_wbytes(a.R, grads);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < SHR_STAGES; ++s) {
+    for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 129);  // 128 threads' copies of token rows, the weights' expect-tx arrival
       mbar_init(&empty[s], 1);
     }
@@ -281,7 +303,6 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
   const int S = gridDim.x, rank = blockIdx.x;
   const int D = grad ? a.N : a.K, KB = (D + BK - 1) / BK;
   const int kb0 = rank * KB / S, nkb = (rank + 1) * KB / S - kb0;
-  const int stage = BOX + shrink_wbytes(a.R);
   const uint32_t cols = tmem_cols(a.Rp);
   if (warp == 5) tmem_alloc(&tmem_base, cols);
   tc_fence_before();
@@ -303,8 +324,8 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
 #pragma unroll
     for (int i = 0; i < 2; ++i) dst[i] = base + sw128_off(warp * 32 + i * 4 + (lane >> 3), c8);
     for (int i = 0; i < nkb; ++i) {
-      const int s = i % SHR_STAGES, col = (kb0 + i) * BK;
-      const bool ok = i < SHR_STAGES || wait_ab(&empty[s], ((i / SHR_STAGES) - 1) & 1, abort, status);
+      const int s = i % ST, col = (kb0 + i) * BK;
+      const bool ok = i < ST || wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (box) {
         if (lane == 0) {
@@ -344,8 +365,8 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
     int i = 0;
     if (lane == 0) {
       for (; i < nkb; ++i) {
-        const int s = i % SHR_STAGES, col = (kb0 + i) * BK;
-        if (i >= SHR_STAGES && !wait_ab(&empty[s], ((i / SHR_STAGES) - 1) & 1, abort, status)) break;
+        const int s = i % ST, col = (kb0 + i) * BK;
+        if (i >= ST && !wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, status)) break;
         const uint32_t wsm = base + s * stage + BOX;
         mbar_arrive_expect_tx(&full[s], tx);
         if (grad) {
@@ -356,14 +377,14 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
         }
       }
       // the CTA's memory must outlive every copy in flight
-      for (int r = (i > SHR_STAGES ? i - SHR_STAGES : 0); r < i; ++r) mbar_drain(&full[r % SHR_STAGES], (r / SHR_STAGES) & 1);
+      for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&full[r % ST], (r / ST) & 1);
     }
   } else {
     const uint32_t idesc = idesc_f32acc(TM, a.Rp, true) | (grad ? IDESC_B_MN : 0u);
     int i = 0;
     for (; i < nkb; ++i) {
-      const int s = i % SHR_STAGES;
-      const bool ok = wait_ab(&full[s], (i / SHR_STAGES) & 1, abort, status);
+      const int s = i % ST;
+      const bool ok = wait_ab(&full[s], (i / ST) & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_proxy_async();  // the copies that arrived -> visible to the tensor core
       tc_fence_after();
@@ -380,42 +401,57 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
       }
       __syncwarp();
     }
-    for (int r = (i > SHR_STAGES ? i - SHR_STAGES : 0); r < i; ++r) mbar_drain(&empty[r % SHR_STAGES], (r / SHR_STAGES) & 1);
+    for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&empty[r % ST], (r / ST) & 1);
   }
   __syncthreads();
   if (warp == 5) {
     tc_fence_after();
     tmem_free(tmem, cols);
   }
-  cluster_sync();
+  // The CTAs' sums of this CTA's share of the rows, all asked for at once and added in CTA order.
+  if (S > 1) cluster_sync();
   const int rows = TM / S, r0 = rank * rows, R4 = a.R / 4;
   const float sc = __ldg(a.scale + tl.x);
   uint16_t* hi = grad ? a.g : a.h;
   uint16_t* lo = hi + (size_t)a.max_tiles * TM * a.R;
-  for (int i = threadIdx.x; i < rows * R4; i += SHR_THREADS) {
-    const int r = r0 + i / R4, c = (i % R4) * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < tl.y) {
-      for (int q = 0; q < S; ++q) {
-        const float4 u = ld_dsmem_f4(part + r * PP + c, q);
-        v.x += u.x;
-        v.y += u.y;
-        v.z += u.z;
-        v.w += u.w;
+  const uint32_t part_s = base;
+  for (int i0 = 0; i0 < rows * R4; i0 += SHR_THREADS * 2) {
+    float4 u[2][8];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = i0 + e * SHR_THREADS + threadIdx.x, r = r0 + i / R4, c = (i % R4) * 4;
+      const bool in = i < rows * R4 && r < tl.y;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        u[e][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q < S && in) u[e][q] = ld_dsmem_f4(dsmem_addr(part_s + (uint32_t)(r * PP + c) * 4, q));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = i0 + e * SHR_THREADS + threadIdx.x, r = r0 + i / R4, c = (i % R4) * 4;
+      if (i >= rows * R4) break;
+      float4 v = u[e][0];
+#pragma unroll
+      for (int q = 1; q < 8; ++q) {
+        v.x += u[e][q].x;
+        v.y += u[e][q].y;
+        v.z += u[e][q].z;
+        v.w += u[e][q].w;
       }
       v.x *= sc;
       v.y *= sc;
       v.z *= sc;
       v.w *= sc;
+      // hi + lo carries 16 significant bits of the FP32 sum into the next product
+      const uint2 hv = make_uint2(f2b2(v.x, v.y), f2b2(v.z, v.w));
+      const uint2 lv = make_uint2(f2b2(v.x - bf16lo(hv.x), v.y - bf16hi(hv.x)), f2b2(v.z - bf16lo(hv.y), v.w - bf16hi(hv.y)));
+      const size_t at = ((size_t)tile * TM + r) * a.R + c;
+      *reinterpret_cast<uint2*>(hi + at) = hv;
+      *reinterpret_cast<uint2*>(lo + at) = lv;
     }
-    // hi + lo carries 16 significant bits of the FP32 sum into the next product
-    const uint2 hv = make_uint2(f2b2(v.x, v.y), f2b2(v.z, v.w));
-    const uint2 lv = make_uint2(f2b2(v.x - bf16lo(hv.x), v.y - bf16hi(hv.x)), f2b2(v.z - bf16lo(hv.y), v.w - bf16hi(hv.y)));
-    const size_t at = ((size_t)tile * TM + r) * a.R + c;
-    *reinterpret_cast<uint2*>(hi + at) = hv;
-    *reinterpret_cast<uint2*>(lo + at) = lv;
   }
-  cluster_sync();  // the others' shared memory stays until it has been read
+  if (S > 1) cluster_sync();  // the others' shared memory stays until it has been read
 }
 
 // ---------------------------------------------------------------------------
@@ -482,8 +518,8 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) k_lora_expand(const Args a, co
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   pdl_trigger();
-  // The plan is complete (the shrink kernel lets this one start only after its own wait for it), and so are the
-  // base rows; only h has to be waited for, by the warp that loads it.
+  // The plan is complete (the kernel before lets this one start only after its own wait), and so are the base rows;
+  // only h has to be waited for, by the warp that loads it.
   // This CTA's run [u0, u1) of the items: tile u / nsub, columns 128 (u % nsub) ...
   const long long items = (long long)__ldcg(a.hdr + H_TILES) * nsub;
   const int u0 = (int)(items * blockIdx.x / gridDim.x), u1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
@@ -764,6 +800,7 @@ __global__ void __launch_bounds__(DW_THREADS, 2) k_lora_dw(const Args a, const _
     fence_mbar_init();
   }
   pdl_wait();
+  pdl_trigger();
   const int slab = blockIdx.x;
   if ((int)blockIdx.y >= __ldcg(a.hdr + H_CHUNKS)) return;
   const int4 ch = __ldcg(a.chunks + blockIdx.y);
@@ -1198,8 +1235,8 @@ bool run_shrink(const Args& p, const Maps& m, bool grads, cudaStream_t stream) {
   const int kb = (std::min(p.K, grads ? p.N : p.K) + BK - 1) / BK, per = p.max_tiles * (grads ? 2 : 1);
   int S = 1;
   while (S < 8 && per * S * 2 <= 2 * sm_count() && S * 2 <= kb) S *= 2;
-  return want_smem(k_lora_shrink, g_shrink, shrink_smem(FLINT_LORA_MAX_RANK)) &&
-         launch(k_lora_shrink, dim3(S, p.max_tiles, grads ? 2 : 1), SHR_THREADS, shrink_smem(p.R), S, stream, p, m);
+  return want_smem(k_lora_shrink, g_shrink, shrink_smem(FLINT_LORA_MAX_RANK, true)) &&
+         launch(k_lora_shrink, dim3(S, p.max_tiles, grads ? 2 : 1), SHR_THREADS, shrink_smem(p.R, grads), S, stream, p, m);
 }
 
 template <bool GRAD, bool WIDE>
@@ -1372,9 +1409,10 @@ extern "C" flint_moe_status flint_lora_backward(const flint_lora* l, const uint1
   p.lddy = (int)lddy;
   Maps m;
   if (!make_maps(&m, l, p)) return FLINT_MOE_ECUDA;
-  if (!run_plan(p, stream) || !run_shrink(p, m, true, stream)) return FLINT_MOE_ECUDA;
-  if (dx_out && !run_expand<true>(p, m, stream)) return FLINT_MOE_ECUDA;
-  if (!(p.R > 64 ? run_dw<true>(p, m, stream) : run_dw<false>(p, m, stream))) return FLINT_MOE_ECUDA;
+  // The weights' gradients come first after the shrink: x and dy, which both read, may still be in L2 then.
+  if (!run_plan(p, stream) || !run_shrink(p, m, true, stream) ||
+      !(p.R > 64 ? run_dw<true>(p, m, stream) : run_dw<false>(p, m, stream)) || (dx_out && !run_expand<true>(p, m, stream)))
+    return FLINT_MOE_ECUDA;
   const int64_t all = (int64_t)p.R * (p.K + p.N);
   if (!launch(k_lora_dw_sum, dim3((unsigned)std::min<int64_t>((all + 2047) / 2048, std::max(1, 152 * 8 / p.n)), p.n), 256, 0, 0,
               stream, p))
