@@ -210,6 +210,7 @@ def gemv_lora(p, packed, fmt, stream=None):
 @pytest.mark.parametrize("B,K,N,R,n,fmt", [(1, 256, 64, 8, 1, fb.NVFP4), (1, 2048, 2048, 16, 4, fb.NVFP4),
                                            (5, 768, 1040, 72, 3, fb.BF16), (8, 4096, 272, 32, 8, fb.NVFP4),
                                            (17, 512, 256, 128, 30, fb.NVFP4), (32, 2048, 512, 64, 32, fb.BF16),
+                                           (20, 256, 4352, 128, 2, fb.NVFP4), (9, 512, 8208, 40, 3, fb.NVFP4),
                                            (32, 8192, 64, 24, 2, fb.NVFP4)])
 def test_gemv_lora(B, K, N, R, n, fmt):
     p, packed, W = gemv_case(B, K, N, R, n, fmt, 70 + B)

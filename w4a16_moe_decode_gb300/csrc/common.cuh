@@ -464,10 +464,11 @@ static __device__ __noinline__ uint4 norm8_huge(const uint4 x, const uint4 w, co
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// The dense GEMV behind flint_gemv (decode.cu): with y32 not null the FP32 sums
-// go there, [B][N], and y is left alone.
+// The dense GEMV behind flint_gemv (decode.cu), with FP32 rows add32 [B][N] (or null)
+// that the kernel before it on the stream writes: added before the rounding to the
+// rows t whose adapter[t] lies in 0 .. n_adapters - 1.
 flint_moe_status gemv_impl(const void* packed, int32_t N, int32_t K, int32_t fmt, const uint16_t* x, int32_t B,
-                           uint16_t* y, float* y32, const uint16_t* norm_weight, float eps, int32_t* dev_status,
-                           cudaStream_t stream);
+                           uint16_t* y, const uint16_t* norm_weight, float eps, const float* add32,
+                           const int32_t* adapter, int32_t n_adapters, int32_t* dev_status, cudaStream_t stream);
 
 }  // namespace flint

@@ -1686,7 +1686,12 @@ struct GemvArgs {
   int N, K, B, fmt, prenorm;
   const uint16_t* x;
   uint16_t* y;
-  float* y32;  // not null: the FP32 sums are written here instead of y (flint_gemv_lora adds to them)
+  // flint_gemv_lora (the ADD kernels): FP32 rows [B][N] added to the sums before they are rounded, for the rows t whose adapter[t] lies in
+  // 0 .. n_adapters - 1. The kernel before this one writes them, and waited itself for the kernel that wrote x: so x
+  // is complete from the start, and the wait for the kernel before moves from the top to where add32 is read.
+  const float* add32;
+  const int* adapter;
+  int n_adapters;
   const uint8_t* packed;
   const float* G;  // the tensor scale word after the tiles
   Layout L;
@@ -1708,7 +1713,15 @@ __host__ __device__ inline size_t gemv_smem(int K, int B, int fmt, int nw, int n
   return o;
 }
 
-template <int FMT, int NTMAX>
+// Output n of row t: the product, and what is added to it, rounded once.
+template <bool ADD>
+__device__ __forceinline__ void gemv_store(const GemvArgs& a, int t, int n, float v) {
+  if (ADD && (unsigned)__ldg(a.adapter + t) < (unsigned)a.n_adapters) v += __ldcg(a.add32 + (size_t)t * a.N + n);
+  const __nv_bfloat16 o = __float2bfloat16_rn(v);
+  a.y[(size_t)t * a.N + n] = *reinterpret_cast<const uint16_t*>(&o);
+}
+
+template <int FMT, int NTMAX, bool ADD>
 __global__ void __launch_bounds__(256) k_gemv(GemvArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16;
@@ -1730,7 +1743,7 @@ __global__ void __launch_bounds__(256) k_gemv(GemvArgs a) {
     mbar_arrive_expect_tx(bar, bytes);
     bulk_g2s_stream(wb, a.packed + (int64_t)blockIdx.x * a.L.dn_tile + (int64_t)warp * bytes, bytes, bar);
   }
-  pdl_wait();  // x may be the previous kernel's output
+  if (!ADD) pdl_wait();  // x may be the previous kernel's output
   pdl_trigger();
   stage_rows<FMT>(a.x, a.B, a.K, a.prenorm, a.gamma, a.eps, xs, xstride, s_inv, warp, nw, lane);
   __syncthreads();
@@ -1772,6 +1785,7 @@ __global__ void __launch_bounds__(256) k_gemv(GemvArgs a) {
   for (int nt = 0; nt < NTMAX; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[((warp * NTMAX + nt) * 32 + lane) * 4 + i] = acc[0][nt][i] + acc[1][nt][i];
+  if (ADD) pdl_wait();
   if (!__syncthreads_and(ok)) return;
   // Output (row r of the tile, token t): token tile t / 8, fragment lane
   // 4 (r % 8) + (t % 8) / 2, element 2 (r / 8) + t % 2.
@@ -1781,14 +1795,127 @@ __global__ void __launch_bounds__(256) k_gemv(GemvArgs a) {
     const int ln = 4 * (r & 7) + (c >> 1), i = 2 * (r >> 3) + (c & 1);
     float v = 0.f;
     for (int w2 = 0; w2 < nw; ++w2) v += red[((w2 * NTMAX + nt) * 32 + ln) * 4 + i];
-    const float vg = (v * s_inv[t]) * G;
-    if (a.y32) {
-      a.y32[(size_t)t * a.N + blockIdx.x * 16 + r] = vg;
-      continue;
-    }
-    const __nv_bfloat16 o = __float2bfloat16_rn(vg);
-    a.y[(size_t)t * a.N + blockIdx.x * 16 + r] = *reinterpret_cast<const uint16_t*>(&o);
+    gemv_store<ADD>(a, t, blockIdx.x * 16 + r, (v * s_inv[t]) * G);
   }
+}
+
+// ===========================================================================
+// The same GEMV for 9 to 32 rows of up to 2048 columns and more tiles than SMs. The
+// rows fill most of an SM's shared memory (131 KB for 32 of 2048), and converting
+// them into fragment order takes longer than a tile's products: so a block stages
+// them once and works through the tiles blockIdx.x, + gridDim.x, ..., the next
+// tile's weights on their way meanwhile (8192 x 2048: 32 rows 25.8 -> 12.6 us, 16
+// rows 11.4 -> 7.8). Each tile is summed up in the same order as by k_gemv.
+// ===========================================================================
+// Tiles of weights in flight: two, or one of BF16 weights (65 KB a tile of 2048 columns).
+__host__ __device__ constexpr int GEMV_BUFS(int fmt) { return fmt == FLINT_MOE_NVFP4 ? 2 : 1; }
+__host__ __device__ inline size_t gemv_rows_smem(int K, int B, int fmt, int nw, int ntmax, size_t* xs_off, size_t* inv_off,
+                                                 size_t* red_off, size_t* bar_off) {
+  const int kgb = fmt == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16;
+  size_t o = 0;
+  o += (size_t)GEMV_BUFS(fmt) * (K / KG_COLS) * kgb;
+  *xs_off = o;   o += (size_t)B * (K * 2 + 16);
+  *inv_off = o;  o += sizeof(float) * MAX_BATCH;
+  *red_off = o;  o += sizeof(float) * nw * ntmax * 128;
+  o = (o + 15) & ~(size_t)15;
+  *bar_off = o;  o += sizeof(uint64_t) * nw * 2;
+  return o;
+}
+
+template <int FMT, int NTMAX, bool ADD>
+__global__ void __launch_bounds__(256) k_gemv_rows(GemvArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16, NB = GEMV_BUFS(FMT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int nw = blockDim.x >> 5;
+  const int KGW = (a.K / KG_COLS) / nw;  // k-groups per warp
+  size_t xs_off, inv_off, red_off, bar_off;
+  gemv_rows_smem(a.K, a.B, FMT, nw, NTMAX, &xs_off, &inv_off, &red_off, &bar_off);
+  const uint32_t bytes = (uint32_t)KGW * KGB;
+  uint8_t* const wb0 = smem + (size_t)warp * NB * bytes;  // this warp's NB buffers
+  uint8_t* xs = smem + xs_off;
+  float* s_inv = reinterpret_cast<float*>(smem + inv_off);
+  float* red = reinterpret_cast<float*>(smem + red_off);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + bar_off) + warp * 2;
+  const int xstride = a.K * 2 + 16, tiles = a.N / 16;
+  auto fetch = [&](int tile, int b) {  // by one lane
+    mbar_arrive_expect_tx(&bar[b], bytes);
+    bulk_g2s_stream(wb0 + (size_t)b * bytes, a.packed + (int64_t)tile * a.L.dn_tile + (int64_t)warp * bytes, bytes, &bar[b]);
+  };
+  if (lane == 0) {
+    for (int b = 0; b < NB; ++b) mbar_init(&bar[b], 1);
+    fence_mbar_init();
+    for (int b = 0; b < NB; ++b)
+      if ((int)(blockIdx.x + b * gridDim.x) < tiles) fetch(blockIdx.x + b * gridDim.x, b);
+  }
+  if (!ADD) pdl_wait();  // x may be the previous kernel's output
+  pdl_trigger();
+  stage_rows<FMT>(a.x, a.B, a.K, a.prenorm, a.gamma, a.eps, xs, xstride, s_inv, warp, nw, lane);
+  __syncthreads();
+  const int nt_used = (a.B + 7) >> 3;
+  int tok[NTMAX];  // column g of token tile nt is token 8 nt + g (past B: a repeat of token B - 1)
+#pragma unroll
+  for (int nt = 0; nt < NTMAX; ++nt) tok[nt] = min(nt * 8 + g, a.B - 1);
+  const float G = FMT == FLINT_MOE_NVFP4 ? a.G[0] : 1.0f;
+  int i = 0;
+  bool ok = true;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++i) {
+    const int b = i % NB;
+    float acc[2][NTMAX][4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int nt = 0; nt < NTMAX; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[c][nt][e] = 0.f;
+    ok = mbar_wait(&bar[b], (i / NB) & 1, a.status);
+    // after a failed wait the copy is let land and the products run on it (the
+    // block stops after them): no branch around the loop's mma.sync
+    if (!ok) mbar_drain(&bar[b], (i / NB) & 1);
+    const uint8_t* wb = wb0 + (size_t)b * bytes;
+#pragma unroll 4
+    for (int kl = 0; kl < KGW; ++kl) {
+      const int kg = warp * KGW + kl;
+      uint4 bx[NTMAX][2];
+#pragma unroll
+      for (int nt = 0; nt < NTMAX; ++nt) {
+        if (nt < nt_used) {
+          const uint8_t* rp = xs + (size_t)tok[nt] * xstride + kg * 128 + t4 * 32;
+          bx[nt][0] = lds128(rp);
+          bx[nt][1] = lds128(rp + 16);
+        }
+      }
+      if (kl & 1)
+        tile_kgroup<FMT, NTMAX>(wb + kl * KGB, bx, nt_used, lane, acc[1]);
+      else
+        tile_kgroup<FMT, NTMAX>(wb + kl * KGB, bx, nt_used, lane, acc[0]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NTMAX; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[((warp * NTMAX + nt) * 32 + lane) * 4 + e] = acc[0][nt][e] + acc[1][nt][e];
+    ok = __syncthreads_and(ok);
+    if (!ok) break;  // a wait gave up: the tile and those behind it stay unwritten
+    const int next = tile + NB * (int)gridDim.x;
+    if (lane == 0 && next < tiles) {
+      fence_proxy_async();  // this warp's reads of the buffer come before the copy into it
+      fetch(next, b);
+    }
+    if (ADD && i == 0) pdl_wait();
+    // Output (row r of the tile, token t): token tile t / 8, fragment lane
+    // 4 (r % 8) + (t % 8) / 2, element 2 (r / 8) + t % 2.
+    for (int p = threadIdx.x; p < 16 * a.B; p += blockDim.x) {
+      const int r = p & 15, t = p >> 4, nt = t >> 3, c = t & 7;
+      const int ln = 4 * (r & 7) + (c >> 1), e = 2 * (r >> 3) + (c & 1);
+      float v = 0.f;
+      for (int w2 = 0; w2 < nw; ++w2) v += red[((w2 * NTMAX + nt) * 32 + ln) * 4 + e];
+      gemv_store<ADD>(a, t, tile * 16 + r, (v * s_inv[t]) * G);
+    }
+    __syncthreads();  // the sums are read before the next tile's
+  }
+  if (!ok && lane == 0)  // the block's memory must outlive the copies in flight
+    for (int j = i + 1; j < i + NB; ++j)
+      if ((int)(blockIdx.x + j * gridDim.x) < tiles) mbar_drain(&bar[j % NB], (j / NB) & 1);
 }
 
 // ===========================================================================
@@ -1826,7 +1953,7 @@ __host__ __device__ inline GemvSplitPlan gemv_split_plan(int B, int fmt, int nw,
 // SOLO (one token): at most 64 registers, four CTAs per SM, so that the grid
 // (N / 16 row tiles x K / 2048 slices: 512 CTAs for 2048 x 8192) runs in one
 // wave instead of two at three per SM (2048 x 8192: 7.4 -> 6.3 us per call).
-template <int FMT, int NTMAX, bool SOLO = false>
+template <int FMT, int NTMAX, bool SOLO, bool ADD>
 __global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16;
@@ -1854,7 +1981,7 @@ __global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
     mbar_arrive_expect_tx(bar, bytes);
     bulk_g2s_stream(wb, a.packed + off, bytes, bar);
   }
-  pdl_wait();  // x may be the previous kernel's output
+  if (!ADD) pdl_wait();  // x may be the previous kernel's output
   pdl_trigger();
   // Stage this CTA's slice of every token row: warp w takes tokens w, w + nw, ...
   const int ntw = (a.B - warp + nw - 1) / nw;  // tokens of this warp: at most NTMAX with 8 warps
@@ -1972,6 +2099,7 @@ __global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
     for (int w2 = 0; w2 < nw; ++w2) v2 += red[((w2 * NTMAX + nt) * 32 + ln) * 4 + i];
     part[t * 16 + r] = v2 * s_inv[t];
   }
+  if (ADD) pdl_wait();
   cluster_sync();  // every CTA's partial sums are published
   if (rank == 0) {
     const float G = FMT == FLINT_MOE_NVFP4 ? a.G[0] : 1.0f;
@@ -1979,12 +2107,7 @@ __global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
       float v2 = 0.f;
       for (uint32_t r = 0; r < S; ++r) v2 += ld_dsmem_f32(part + p, r);  // rank order
       const int rr = p & 15, t = p >> 4;
-      if (a.y32) {
-        a.y32[(size_t)t * a.N + blockIdx.x * 16 + rr] = v2 * G;
-        continue;
-      }
-      const __nv_bfloat16 o = __float2bfloat16_rn(v2 * G);
-      a.y[(size_t)t * a.N + blockIdx.x * 16 + rr] = *reinterpret_cast<const uint16_t*>(&o);
+      gemv_store<ADD>(a, t, blockIdx.x * 16 + rr, v2 * G);
     }
   }
   cluster_sync();  // the other CTAs' shared memory stays until CTA 0 has read it
@@ -2509,12 +2632,13 @@ extern "C" flint_moe_status flint_moe_debug_wait_timeout(int32_t* dev_status, cu
 extern "C" flint_moe_status flint_gemv(const void* packed, int32_t N, int32_t K, int32_t fmt, const uint16_t* x,
                                        int32_t B, uint16_t* y, const uint16_t* norm_weight, float eps,
                                        int32_t* dev_status, cudaStream_t stream) {
-  return flint::gemv_impl(packed, N, K, fmt, x, B, y, nullptr, norm_weight, eps, dev_status, stream);
+  return flint::gemv_impl(packed, N, K, fmt, x, B, y, norm_weight, eps, nullptr, nullptr, 0, dev_status, stream);
 }
 
-// flint_gemv, or with y32 the same product left in FP32 [B][N] (y is then only checked).
+// flint_gemv, with FP32 rows to add before the rounding (GemvArgs).
 flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int32_t fmt, const uint16_t* x, int32_t B,
-                                  uint16_t* y, float* y32, const uint16_t* norm_weight, float eps, int32_t* dev_status,
+                                  uint16_t* y, const uint16_t* norm_weight, float eps, const float* add32,
+                                  const int32_t* adapter, int32_t n_adapters, int32_t* dev_status,
                                   cudaStream_t stream) {
   if (flint_gemv_packed_bytes(N, K, fmt) == 0) return FLINT_MOE_EUNSUPPORTED;
   if (B < 0 || B > MAX_BATCH || !(eps >= 0.f) || !(eps <= 3.0e38f)) return FLINT_MOE_EINVAL;
@@ -2530,7 +2654,9 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
   a.prenorm = norm_weight != nullptr;
   a.x = x;
   a.y = y;
-  a.y32 = y32;
+  a.add32 = add32;
+  a.adapter = adapter;
+  a.n_adapters = n_adapters;
   a.packed = static_cast<const uint8_t*>(packed);
   a.L = make_dense_layout(N, K, fmt);
   a.G = reinterpret_cast<const float*>(a.packed + a.L.globals_off + 8);  // [G, G, G, 0]: the third word
@@ -2544,45 +2670,53 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
     if (smem > SMEM_LIMIT) return FLINT_MOE_EUNSUPPORTED;
     const dim3 grid(N / 16, S), block(256);
     cudaError_t e;
-    if (fmt == FLINT_MOE_NVFP4) {
-      switch (B == 1 ? 0 : ntmax) {
-        case 0: e = launch_cluster(k_gemv_split<FLINT_MOE_NVFP4, 1, true>, grid, block, smem, S, stream, a); break;
-        case 1: e = launch_cluster(k_gemv_split<FLINT_MOE_NVFP4, 1>, grid, block, smem, S, stream, a); break;
-        case 2: e = launch_cluster(k_gemv_split<FLINT_MOE_NVFP4, 2>, grid, block, smem, S, stream, a); break;
-        case 3: e = launch_cluster(k_gemv_split<FLINT_MOE_NVFP4, 3>, grid, block, smem, S, stream, a); break;
-        default: e = launch_cluster(k_gemv_split<FLINT_MOE_NVFP4, 4>, grid, block, smem, S, stream, a); break;
-      }
-    } else {
-      switch (B == 1 ? 0 : ntmax) {
-        case 0: e = launch_cluster(k_gemv_split<FLINT_MOE_BF16, 1, true>, grid, block, smem, S, stream, a); break;
-        case 1: e = launch_cluster(k_gemv_split<FLINT_MOE_BF16, 1>, grid, block, smem, S, stream, a); break;
-        case 2: e = launch_cluster(k_gemv_split<FLINT_MOE_BF16, 2>, grid, block, smem, S, stream, a); break;
-        case 3: e = launch_cluster(k_gemv_split<FLINT_MOE_BF16, 3>, grid, block, smem, S, stream, a); break;
-        default: e = launch_cluster(k_gemv_split<FLINT_MOE_BF16, 4>, grid, block, smem, S, stream, a); break;
-      }
+    const bool nv = fmt == FLINT_MOE_NVFP4, add = add32 != nullptr;
+#define FLINT_SPLIT(FMT, NT, SOLO) \
+  (add ? launch_cluster(k_gemv_split<FMT, NT, SOLO, true>, grid, block, smem, S, stream, a) \
+       : launch_cluster(k_gemv_split<FMT, NT, SOLO, false>, grid, block, smem, S, stream, a))
+    switch (B == 1 ? 0 : ntmax) {
+      case 0: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 1, true) : FLINT_SPLIT(FLINT_MOE_BF16, 1, true); break;
+      case 1: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 1, false) : FLINT_SPLIT(FLINT_MOE_BF16, 1, false); break;
+      case 2: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 2, false) : FLINT_SPLIT(FLINT_MOE_BF16, 2, false); break;
+      case 3: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 3, false) : FLINT_SPLIT(FLINT_MOE_BF16, 3, false); break;
+      default: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 4, false) : FLINT_SPLIT(FLINT_MOE_BF16, 4, false); break;
     }
+#undef FLINT_SPLIT
     return e == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
   }
   size_t o1, o2, o3, o4, o5;
-  const size_t smem = gemv_smem(K, B, fmt, nw, ntmax, &o1, &o2, &o3, &o4, &o5);
-  if ((size_t)B * (K * 2 + 16) > 160 * 1024 || smem > SMEM_LIMIT) return FLINT_MOE_EUNSUPPORTED;
-  const dim3 grid(N / 16), block(32 * nw);
+  const size_t one = gemv_smem(K, B, fmt, nw, ntmax, &o1, &o2, &o3, &o4, &o5);
+  if ((size_t)B * (K * 2 + 16) > 160 * 1024 || one > SMEM_LIMIT) return FLINT_MOE_EUNSUPPORTED;
+  const dim3 block(32 * nw);
   cudaError_t e;
-  if (fmt == FLINT_MOE_NVFP4) {
+  const bool nv = fmt == FLINT_MOE_NVFP4, add = add32 != nullptr;
+#define FLINT_GEMV(KERNEL, NT)                                                                          \
+  (nv ? (add ? launch_any(KERNEL<FLINT_MOE_NVFP4, NT, true>, grid, block, smem, stream, a)              \
+             : launch_any(KERNEL<FLINT_MOE_NVFP4, NT, false>, grid, block, smem, stream, a))            \
+      : (add ? launch_any(KERNEL<FLINT_MOE_BF16, NT, true>, grid, block, smem, stream, a)               \
+             : launch_any(KERNEL<FLINT_MOE_BF16, NT, false>, grid, block, smem, stream, a)))
+  const size_t rows_smem = gemv_rows_smem(K, B, fmt, nw, ntmax, &o1, &o2, &o3, &o4);
+  if (ntmax > 1 && N / 16 > sm_count() && rows_smem <= SMEM_LIMIT) {
+    // more tiles than blocks that run at once: blocks that stage the rows once for several tiles
+    const size_t smem = rows_smem;
+    const int per_sm = std::max<int>(1, std::min<int>(2, (int)(SMEM_LIMIT / (smem + 1024))));
+    const dim3 grid(std::min(N / 16, sm_count() * per_sm));
     switch (ntmax) {
-      case 1: e = launch_any(k_gemv<FLINT_MOE_NVFP4, 1>, grid, block, smem, stream, a); break;
-      case 2: e = launch_any(k_gemv<FLINT_MOE_NVFP4, 2>, grid, block, smem, stream, a); break;
-      case 3: e = launch_any(k_gemv<FLINT_MOE_NVFP4, 3>, grid, block, smem, stream, a); break;
-      default: e = launch_any(k_gemv<FLINT_MOE_NVFP4, 4>, grid, block, smem, stream, a); break;
+      case 2: e = FLINT_GEMV(k_gemv_rows, 2); break;
+      case 3: e = FLINT_GEMV(k_gemv_rows, 3); break;
+      default: e = FLINT_GEMV(k_gemv_rows, 4); break;
     }
   } else {
+    const size_t smem = one;
+    const dim3 grid(N / 16);
     switch (ntmax) {
-      case 1: e = launch_any(k_gemv<FLINT_MOE_BF16, 1>, grid, block, smem, stream, a); break;
-      case 2: e = launch_any(k_gemv<FLINT_MOE_BF16, 2>, grid, block, smem, stream, a); break;
-      case 3: e = launch_any(k_gemv<FLINT_MOE_BF16, 3>, grid, block, smem, stream, a); break;
-      default: e = launch_any(k_gemv<FLINT_MOE_BF16, 4>, grid, block, smem, stream, a); break;
+      case 1: e = FLINT_GEMV(k_gemv, 1); break;
+      case 2: e = FLINT_GEMV(k_gemv, 2); break;
+      case 3: e = FLINT_GEMV(k_gemv, 3); break;
+      default: e = FLINT_GEMV(k_gemv, 4); break;
     }
   }
+#undef FLINT_GEMV
   return e == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
 }
 

@@ -964,9 +964,24 @@ __global__ void __launch_bounds__(256) k_lora_dw_sum(const Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// Up to 32 rows.
+// Up to 32 rows (decode). One cluster of FEW_S CTAs for each distinct adapter of
+// the call: CTA s takes a run of the 32-column steps of K for h = A x, the CTAs'
+// sums meet in distributed shared memory (added in CTA order), and each takes its
+// share of the N rows of B for B h. With so few rows every weight is used once,
+// so weights go from memory to tensor-core fragments in registers, 16 (or 8)
+// bytes a lane; mma.sync with the weights as its 16 rows and the tokens as its 8
+// columns. The order of the columns within a step is the same for both operands
+// of a product and otherwise free, so a lane's neighbouring columns need no
+// shuffling. A CTA's share of B is one run of memory: it comes into shared memory
+// in pieces of 256 rows with bulk copies that start before A is read (from L2 into
+// registers it took 10 of 21 us for 32 adapters of rank 64, 2048 x 8192). Bound by
+// latency for one adapter, by the adapters' bytes for many.
 // ---------------------------------------------------------------------------
-struct SArgs {
+constexpr int FEW = MAX_BATCH;
+constexpr int FEW_S = 8;
+constexpr int FEW_THREADS = 256;
+
+struct FewArgs {
   int K, N, R, n, T;
   const uint16_t* A;
   const uint16_t* B;
@@ -974,51 +989,313 @@ struct SArgs {
   const int* adapter;
   const uint16_t* x;
   int64_t ldx;
-  const uint16_t* dy;
-  int64_t lddy;
-  const uint16_t* in;   // y_in or dx_in, bf16, or null
-  const float* in32;    // FP32 base [T][N], or null
-  uint16_t* out;
+  const uint16_t* in;  // base rows (bf16) or null
+  uint16_t* out;       // bf16 rows, or
+  float* out32;        // FP32 rows [T][N] of B h alone
   int64_t ldo;
-  float* h;  // [T][R]
-  float* g;  // [T][R]
+  int with_none;  // rows without an adapter are copied too
+  int* status;
+  int clear;      // the status word starts at zero
+  size_t smem;    // of the launch
 };
 
-__device__ __forceinline__ float b2f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-
-// One warp per (token, rank): h = s A x, or with GRAD g = s B^T dy.
-template <bool GRAD>
-__global__ void __launch_bounds__(256) k_small_shrink(const SArgs p) {
-  const int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (u >= (int64_t)p.T * p.R) return;
-  const int t = (int)(u / p.R), r = (int)(u % p.R), a = p.adapter[t];
-  float acc = 0.f;
-  if (a >= 0 && a < p.n) {
-    if (GRAD) {
-      for (int n = lane; n < p.N; n += 32) acc += b2f(p.dy[t * p.lddy + n]) * b2f(p.B[((int64_t)a * p.N + n) * p.R + r]);
-    } else {
-      for (int k = lane; k < p.K; k += 32) acc += b2f(p.x[t * p.ldx + k]) * b2f(p.A[((int64_t)a * p.R + r) * p.K + k]);
-    }
-    acc *= p.scale[a];
-  }
-  acc = warp_sum(acc);
-  if (lane == 0) (GRAD ? p.g : p.h)[u] = acc;
+__host__ __device__ inline int few_rt(int R) { return (R + 15) / 16; }  // 16-row tiles of the rank
+// Warps side by side over the rank's tiles; the rest of the eight split the columns.
+__host__ __device__ inline int few_wr(int R) { return few_rt(R) >= 8 ? 8 : few_rt(R) >= 4 ? 4 : few_rt(R) >= 2 ? 2 : 1; }
+// Shared memory: pieces of B, the column splits' sums [8 / wr][tokens][rank], the CTA's sums [tokens][rank], h as two
+// bf16 halves. Together a third of an SM's where two pieces leave that.
+constexpr int FEW_PIECE = 256;  // rows of a piece: two tiles of 16 for each warp
+constexpr int FEW_MOST = 8;     // pieces at once
+constexpr int FEW_CTAS = 3;     // CTAs of an SM
+constexpr size_t FEW_SMEM = 224 * 1024 / FEW_CTAS;
+__host__ __device__ inline int few_pieces(int N) { return ((N + 15) / 16 + FEW_S * 16 - 1) / (FEW_S * 16); }  // of a CTA's share, at most
+struct FewPlan {
+  int RP;      // rank padded to 16
+  int pieces;  // held at once
+  size_t red, part, hs, total;
+};
+// `cols`: tokens it is laid out for; `most`: pieces of a CTA's share; `budget`: bytes.
+__host__ __device__ inline FewPlan few_plan(int R, int cols, int most, size_t budget) {
+  FewPlan p;
+  p.RP = few_rt(R) * 16;
+  const size_t rest = sizeof(float) * (8 / few_wr(R) + 1) * cols * p.RP + (size_t)2 * 2 * cols * (p.RP + 8);
+  const size_t piece = (size_t)FEW_PIECE * R * 2;
+  const int fit = rest + 2 * piece > budget ? 2 : (int)((budget - rest) / piece);
+  const int cap = most < FEW_MOST ? most : FEW_MOST;
+  p.pieces = fit > cap ? cap : fit;
+  size_t o = p.pieces * piece;
+  p.red = o;   o += sizeof(float) * (8 / few_wr(R)) * cols * p.RP;
+  p.part = o;  o += sizeof(float) * cols * p.RP;
+  p.hs = o;    o += (size_t)2 * 2 * cols * (p.RP + 8);
+  p.total = o;
+  return p;
 }
 
-template <bool GRAD>
-__global__ void __launch_bounds__(256) k_small_expand(const SArgs p) {
-  const int D = GRAD ? p.K : p.N;
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < (int64_t)p.T * D; u += (int64_t)gridDim.x * 256) {
-    const int t = (int)(u / D), c = (int)(u % D), a = p.adapter[t];
-    float acc = 0.f;
-    if (a >= 0 && a < p.n)
-      for (int r = 0; r < p.R; ++r)
-        acc += GRAD ? p.g[(int64_t)t * p.R + r] * b2f(p.A[((int64_t)a * p.R + r) * p.K + c])
-                    : p.h[(int64_t)t * p.R + r] * b2f(p.B[((int64_t)a * p.N + c) * p.R + r]);
-    const float base = p.in32 ? p.in32[u] : (p.in ? b2f(p.in[t * p.ldo + c]) : 0.f);
-    p.out[t * p.ldo + c] = f2b(base + acc);
+// What the two products of a group share.
+struct FewGroup {
+  const uint16_t* A;  // the adapter's
+  const uint16_t* B;
+  int count;           // tokens
+  int n0, n1;          // this CTA's 16-row tiles of B
+  int k0, k1;          // and its 32-column steps of K
+  int cols;            // tokens that the shared memory is laid out for
+};
+
+// h = A x over this CTA's columns, this warp's share of it, into red[split][token][rank]. NT: token tiles of 8.
+template <int NT>
+__device__ __forceinline__ void few_shrink(const FewArgs& a, const FewGroup& G, const int* toks, float* red, int RP, int warp,
+                                           int lane) {
+  const int g = lane >> 2, t4 = lane & 3;
+  const int wr = few_wr(a.R), wk = 8 / wr, wri = warp % wr, wki = warp / wr, RT = few_rt(a.R);
+  const uint16_t* xr[NT];  // row of token 8 nt + g (past the count: the last token's)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) xr[nt] = a.x + toks[min(nt * 8 + g, G.count - 1)] * a.ldx + t4 * 8;
+  for (int rt = wri; rt < RT; rt += wr) {
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+    const int r0 = rt * 16 + g, r1 = r0 + 8;
+    const uint16_t* p0 = G.A + (int64_t)r0 * a.K + t4 * 8;
+    const uint16_t* p1 = G.A + (int64_t)r1 * a.K + t4 * 8;
+#pragma unroll 4
+    for (int k = G.k0 + wki; k < G.k1; k += wk) {
+      const int c = k * 32;
+      const bool in = c + t4 * 8 < a.K;
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      const uint4 u = in && r0 < a.R ? __ldg(reinterpret_cast<const uint4*>(p0 + c)) : zero;
+      const uint4 v = in && r1 < a.R ? __ldg(reinterpret_cast<const uint4*>(p1 + c)) : zero;
+      const uint32_t f0[4] = {u.x, v.x, u.y, v.y}, f1[4] = {u.z, v.z, u.w, v.w};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 xv = in ? ld_cg_v4(xr[nt] + c) : zero;
+        mma_bf16(acc[nt], f0, xv.x, xv.y);
+        mma_bf16(acc[nt], f1, xv.z, xv.w);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float* o = red + ((size_t)wki * G.cols + nt * 8 + 2 * t4) * RP + rt * 16 + g;
+      o[0] = acc[nt][0];
+      o[RP] = acc[nt][1];
+      o[8] = acc[nt][2];
+      o[RP + 8] = acc[nt][3];
+    }
   }
+}
+
+// B h for this CTA's rows, piece by piece: warp w takes the 16-row tiles w and w + 8 of a piece at once, STEP columns of
+// the rank a step. fetch(i) asks for piece i (thread 0).
+template <int NT, int STEP, typename Fetch>
+__device__ __forceinline__ void few_expand(const FewArgs& a, const FewGroup& G, const int* toks, const uint8_t* smem,
+                                           const uint16_t* hs, const FewPlan& P, uint64_t* full, uint64_t* empty, int npieces,
+                                           int warp, int lane, Fetch fetch) {
+  const int g = lane >> 2, t4 = lane & 3;
+  constexpr int LC = STEP / 4;  // neighbouring columns of a lane
+  constexpr int ACC = NT == 1 ? 2 : 1;  // chains of MMAs: the halves of h apart, where registers allow
+  const int HP = P.RP + 8;
+  const uint16_t* lo = hs + G.cols * HP;
+  const int end = min(G.n1 * 16, a.N);
+  // lane: rows g, g + 8 of tokens 8 nt + 2 t4, + 1
+  int64_t at[NT][2];  // first elements of those tokens' output rows, -1: none
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int j = nt * 8 + 2 * t4 + e;
+      at[nt][e] = j < G.count ? toks[j] * (a.out32 ? (int64_t)a.N : a.ldo) : -1;
+    }
+  for (int i = 0; i < npieces; ++i) {
+    const int sl = i % P.pieces, par = (i / P.pieces) & 1;
+    // after a failed wait the piece is let land and used as it is: the status word tells
+    if (!mbar_wait(&full[sl], par, a.status)) mbar_drain(&full[sl], par);
+    const int row = G.n0 * 16 + i * FEW_PIECE + warp * 16 + g;
+    bool in[4];  // rows row, + 8, + 128, + 136
+#pragma unroll
+    for (int q = 0; q < 4; ++q) in[q] = row + (q & 1) * 8 + (q >> 1) * 128 < end;
+    const uint8_t* p = smem + (size_t)sl * FEW_PIECE * a.R * 2 + (size_t)((warp * 16 + g) * a.R + t4 * LC) * 2;
+    float acc[2][ACC][NT][4];
+#pragma unroll
+    for (int z = 0; z < 2 * ACC * NT * 4; ++z) (&acc[0][0][0][0])[z] = 0.f;
+#pragma unroll 2
+    for (int c = 0; c < a.R; c += STEP) {
+      uint4 w[4];  // STEP 16: two words of each
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        w[q] = make_uint4(0u, 0u, 0u, 0u);
+        const uint8_t* pq = p + (size_t)((q & 1) * 8 + (q >> 1) * 128) * a.R * 2 + c * 2;
+        if (STEP == 32) {
+          if (in[q]) w[q] = lds128(pq);
+        } else if (in[q] && c + t4 * LC < a.R) {
+          const uint2 v = *reinterpret_cast<const uint2*>(pq);
+          w[q].x = v.x, w[q].y = v.y;
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int h = (nt * 8 + g) * HP + c + t4 * LC;
+        uint4 hv = make_uint4(0u, 0u, 0u, 0u), lv = hv;
+        if (STEP == 32) {
+          hv = *reinterpret_cast<const uint4*>(hs + h);
+          lv = *reinterpret_cast<const uint4*>(lo + h);
+        } else {
+          const uint2 h2 = *reinterpret_cast<const uint2*>(hs + h), l2 = *reinterpret_cast<const uint2*>(lo + h);
+          hv.x = h2.x, hv.y = h2.y, lv.x = l2.x, lv.y = l2.y;
+        }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const uint32_t f0[4] = {w[2 * z].x, w[2 * z + 1].x, w[2 * z].y, w[2 * z + 1].y};
+          const uint32_t f1[4] = {w[2 * z].z, w[2 * z + 1].z, w[2 * z].w, w[2 * z + 1].w};
+          mma_bf16(acc[z][0][nt], f0, hv.x, hv.y);
+          mma_bf16(acc[z][ACC - 1][nt], f0, lv.x, lv.y);
+          if (STEP == 32) {
+            mma_bf16(acc[z][0][nt], f1, hv.z, hv.w);
+            mma_bf16(acc[z][ACC - 1][nt], f1, lv.z, lv.w);
+          }
+        }
+      }
+    }
+    if (npieces > P.pieces) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[sl]);
+      if (threadIdx.x == 0 && i + P.pieces < npieces) {
+        mbar_wait(&empty[sl], par, a.status);
+        fetch(i + P.pieces);
+      }
+    }
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (at[nt][e] < 0) continue;
+          float v[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) v[q] = ACC == 2 ? acc[z][0][nt][e + 2 * q] + acc[z][ACC - 1][nt][e + 2 * q] : acc[z][0][nt][e + 2 * q];
+          const int64_t o = at[nt][e] + row + z * 128;
+          if (a.out32) {
+            if (in[2 * z]) a.out32[o] = v[0];
+            if (in[2 * z + 1]) a.out32[o + 8] = v[1];
+          } else {
+            if (in[2 * z]) a.out[o] = f2b((a.in ? __uint_as_float((uint32_t)a.in[o] << 16) : 0.f) + v[0]);
+            if (in[2 * z + 1]) a.out[o + 8] = f2b((a.in ? __uint_as_float((uint32_t)a.in[o + 8] << 16) : 0.f) + v[1]);
+          }
+        }
+  }
+}
+
+template <int NT, int STEP>  // tokens of a call: 8 NT at most; columns of the rank a step: 32 (multiples of it) or 16
+__global__ void __launch_bounds__(FEW_THREADS, FEW_CTAS) k_lora_few(const FewArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int toks[FEW];
+  __shared__ uint64_t full[FEW_MOST], empty[FEW_MOST];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int s = blockIdx.x;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < FEW_MOST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 8);
+    }
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (a.clear && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
+  // The blockIdx.y-th distinct adapter, by first use, and its tokens (every warp finds the same).
+  int mine = lane < a.T ? __ldg(a.adapter + lane) : -2;
+  if (mine < -1 || mine >= a.n) mine = lane < a.T ? -1 : -2;
+  const unsigned same = __match_any_sync(0xffffffffu, mine);
+  unsigned firsts = __ballot_sync(0xffffffffu, lane == __ffs(same) - 1 && mine != -2 && (mine >= 0 || a.with_none));
+  for (int i = 0; i < (int)blockIdx.y; ++i) firsts &= firsts - 1;
+  if (!firsts) return;  // fewer adapters than clusters: the whole cluster leaves
+  const int lead = __ffs(firsts) - 1;
+  const int ad = __shfl_sync(0xffffffffu, mine, lead);
+  const unsigned set = __shfl_sync(0xffffffffu, same, lead);
+  const int count = __popc(set);
+  if (warp == 0 && ((set >> lane) & 1u)) toks[__popc(set & ((1u << lane) - 1))] = lane;
+  __syncthreads();
+  if (ad < 0) {  // no adapter: the base as it is
+    for (int i = s * FEW_THREADS + threadIdx.x; i < count * (a.N / 8); i += FEW_S * FEW_THREADS) {
+      const int t = toks[i / (a.N / 8)], c = i % (a.N / 8) * 8;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (a.in) v = *reinterpret_cast<const uint4*>(a.in + t * a.ldo + c);
+      *reinterpret_cast<uint4*>(a.out + t * a.ldo + c) = v;
+    }
+    return;
+  }
+  // A group of up to 8 tokens needs less for its sums, and holds more of B.
+  const int nt_used = (count + 7) >> 3, cols = nt_used == 1 ? 8 : 8 * NT;
+  const FewPlan P = few_plan(a.R, cols, few_pieces(a.N), a.smem);
+  float* red = reinterpret_cast<float*>(smem + P.red);
+  float* part = reinterpret_cast<float*>(smem + P.part);
+  uint16_t* hs = reinterpret_cast<uint16_t*>(smem + P.hs);
+  const uint16_t* A = a.A + (int64_t)ad * a.R * a.K;
+  const uint16_t* B = a.B + (int64_t)ad * a.N * a.R;
+  const int ntiles = (a.N + 15) / 16, n0 = s * ntiles / FEW_S, n1 = (s + 1) * ntiles / FEW_S;  // this CTA's 16-row tiles of B
+  // This CTA's share of B in pieces.
+  const int npieces = (n1 - n0 + 15) / 16;
+  auto fetch = [&](int i) {  // by thread 0
+    const int r0 = n0 * 16 + i * FEW_PIECE, r1 = min(min(r0 + FEW_PIECE, n1 * 16), a.N);
+    const uint32_t bytes = (uint32_t)((r1 - r0) * a.R * 2);
+    mbar_arrive_expect_tx(&full[i % P.pieces], bytes);
+    bulk_g2s(smem + (size_t)(i % P.pieces) * FEW_PIECE * a.R * 2, B + (int64_t)r0 * a.R, bytes, &full[i % P.pieces]);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < min(P.pieces, npieces); ++i) fetch(i);
+  // ---- h = A x. Most groups have few tokens: those take the code for one token tile, whatever the call's size.
+  const int wk = 8 / few_wr(a.R), steps = (a.K + 31) / 32;
+  const FewGroup G = {A, B, count, n0, n1, s * steps / FEW_S, (s + 1) * steps / FEW_S, cols};
+  if (NT == 1 || nt_used == 1)
+    few_shrink<1>(a, G, toks, red, P.RP, warp, lane);
+  else
+    few_shrink<NT>(a, G, toks, red, P.RP, warp, lane);
+  __syncthreads();
+  const int vals = count * P.RP;
+  for (int i = threadIdx.x; i < vals; i += FEW_THREADS) {
+    float v = 0.f;
+    for (int w = 0; w < wk; ++w) v += red[(size_t)w * cols * P.RP + i];
+    part[i] = v;
+  }
+  cluster_sync();
+  {
+    const float sc = __ldg(a.scale + ad);
+    const uint32_t local = smem_addr(part);
+    uint16_t* lo = hs + cols * (P.RP + 8);
+    for (int i = threadIdx.x * 4; i < cols * P.RP; i += FEW_THREADS * 4) {
+      float4 u[FEW_S];
+#pragma unroll
+      for (int q = 0; q < FEW_S; ++q)
+        u[q] = i < vals ? ld_dsmem_f4(dsmem_addr(local + i * 4, q)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 v = u[0];
+#pragma unroll
+      for (int q = 1; q < FEW_S; ++q) {
+        v.x += u[q].x;
+        v.y += u[q].y;
+        v.z += u[q].z;
+        v.w += u[q].w;
+      }
+      v.x *= sc;
+      v.y *= sc;
+      v.z *= sc;
+      v.w *= sc;
+      // hi + lo carries 16 significant bits of the FP32 sum into the next product
+      const uint2 hv = make_uint2(f2b2(v.x, v.y), f2b2(v.z, v.w));
+      const uint2 lv = make_uint2(f2b2(v.x - bf16lo(hv.x), v.y - bf16hi(hv.x)), f2b2(v.z - bf16lo(hv.y), v.w - bf16hi(hv.y)));
+      const int at = i / P.RP * (P.RP + 8) + i % P.RP;
+      *reinterpret_cast<uint2*>(hs + at) = hv;
+      *reinterpret_cast<uint2*>(lo + at) = lv;
+    }
+  }
+  cluster_arrive();  // this CTA has read the others' sums
+  __syncthreads();
+  // ---- rows of B h
+  if (NT == 1 || nt_used == 1)
+    few_expand<1, STEP>(a, G, toks, smem, hs, P, full, empty, npieces, warp, lane, fetch);
+  else
+    few_expand<NT, STEP>(a, G, toks, smem, hs, P, full, empty, npieces, warp, lane, fetch);
+  cluster_wait();  // the others' shared memory stayed until it had been read
 }
 
 }  // namespace lora
@@ -1091,7 +1368,6 @@ WsPlan ws_plan(const flint_lora* l, int T, bool grad, bool base) {
   WsPlan w = {};
   size_t o = 256;
   if (T <= SMALL_T && !grad) {
-    w.h = o;    o = ws_align(o + sizeof(float) * (size_t)T * l->rank);
     w.y32 = o;  o = ws_align(o + (base ? sizeof(float) * (size_t)T * l->out_dim : 0));
     w.total = o;
     return w;
@@ -1120,8 +1396,8 @@ size_t ws_most(const flint_lora* l, int T, bool grad, bool base) {
   return most + (more > 0 ? ws_align((size_t)more * sizeof(float) * l->rank * (l->in_dim + l->out_dim)) : 0);
 }
 
-SArgs small_args(const flint_lora* l, const int32_t* adapter, int T) {
-  SArgs p = {};
+FewArgs few_args(const flint_lora* l, const int32_t* adapter, int T) {
+  FewArgs p = {};
   p.K = l->in_dim;
   p.N = l->out_dim;
   p.R = l->rank;
@@ -1262,7 +1538,19 @@ bool run_dw(const Args& p, const Maps& m, cudaStream_t stream) {
          launch(k_lora_dw<WIDE>, dim3(p.slabs_a + p.slabs_b, chunks), DW_THREADS, dw_smem(p.R), 0, stream, p, m);
 }
 
-int blocks(int64_t threads) { return (int)std::min<int64_t>(152 * 16, (threads + 255) / 256); }
+template <int NT, int STEP>
+bool run_few_as(FewArgs p, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  const int groups = std::min(p.T, p.n + (p.with_none ? 1 : 0)), most = few_pieces(p.N);
+  p.smem = std::max(few_plan(p.R, 8 * NT, most, FEW_SMEM).total, few_plan(p.R, 8, most, FEW_SMEM).total);
+  return want_smem(k_lora_few<NT, STEP>, done, 184 * 1024) &&
+         launch(k_lora_few<NT, STEP>, dim3(FEW_S, groups), FEW_THREADS, p.smem, FEW_S, stream, p);
+}
+bool run_few(const FewArgs& p, cudaStream_t stream) {
+  if (p.R % 32 == 0)
+    return p.T <= 8 ? run_few_as<1, 32>(p, stream) : p.T <= 16 ? run_few_as<2, 32>(p, stream) : run_few_as<4, 32>(p, stream);
+  return p.T <= 8 ? run_few_as<1, 16>(p, stream) : p.T <= 16 ? run_few_as<2, 16>(p, stream) : run_few_as<4, 16>(p, stream);
+}
 
 }  // namespace
 
@@ -1309,16 +1597,16 @@ extern "C" flint_moe_status flint_lora_apply(const flint_lora* l, const uint16_t
   if (ws_bytes < w.total) return FLINT_MOE_EINVAL;
   uint8_t* wb = static_cast<uint8_t*>(ws);
   if (T <= SMALL_T) {
-    SArgs p = small_args(l, adapter, T);
+    FewArgs p = few_args(l, adapter, T);
     p.x = x;
     p.ldx = ldx;
     p.in = y_in;
     p.out = y_out;
     p.ldo = ldy;
-    p.h = reinterpret_cast<float*>(wb + w.h);
-    k_small_shrink<false><<<(int)(((int64_t)T * p.R + 7) / 8), 256, 0, stream>>>(p);
-    k_small_expand<false><<<blocks((int64_t)T * p.N), 256, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
+    p.with_none = y_in != y_out;
+    p.status = reinterpret_cast<int*>(wb) + H_STATUS;
+    p.clear = 1;
+    return run_few(p, stream) ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
   }
   Args p = tile_args(l, adapter, T, wb, w);
   p.with_none = y_in != y_out;
@@ -1346,19 +1634,15 @@ extern "C" flint_moe_status flint_gemv_lora(const void* packed, int32_t N, int32
   if (overlap(y, N, N, x, K, K, B)) return FLINT_MOE_EINVAL;
   const WsPlan w = ws_plan(l, B, false, true);
   if (ws_bytes < w.total) return FLINT_MOE_EINVAL;
-  SArgs p = small_args(l, adapter, B);
+  FewArgs p = few_args(l, adapter, B);
   p.x = x;
   p.ldx = K;
-  float* y32 = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.y32);
-  p.in32 = y32;
-  p.out = y;
-  p.ldo = N;
-  p.h = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.h);
-  st = gemv_impl(packed, N, K, fmt, x, B, y, y32, nullptr, 0.f, dev_status, stream);
-  if (st != FLINT_MOE_OK) return st;
-  k_small_shrink<false><<<(int)(((int64_t)B * p.R + 7) / 8), 256, 0, stream>>>(p);
-  k_small_expand<false><<<blocks((int64_t)B * p.N), 256, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
+  p.out32 = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.y32);
+  p.status = dev_status ? dev_status : static_cast<int32_t*>(ws) + H_STATUS;
+  p.clear = !dev_status;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(packed, 16)) return FLINT_MOE_EALIGN;  // before the first launch
+  if (!run_few(p, stream)) return FLINT_MOE_ECUDA;
+  return gemv_impl(packed, N, K, fmt, x, B, y, nullptr, 0.f, p.out32, adapter, l->num_adapters, dev_status, stream);
 }
 
 extern "C" flint_moe_status flint_lora_backward(const flint_lora* l, const uint16_t* x, int64_t ldx, const uint16_t* dy,
