@@ -12,6 +12,7 @@
 // One warp per token row, 16-byte loads. Both kernels move T E floats and are
 // bound by memory bandwidth.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -24,6 +25,7 @@ constexpr int MAX_E = MAX_EXPERTS;
 
 struct BalArgs {
   int T, E, k, n_seq, renorm;
+  bool narrow;  // k T E < 2^31
   float routed_scale, alpha;
   const float* logits;
   const int* idx;
@@ -92,6 +94,36 @@ __device__ __forceinline__ void sigmoid2(float z, float& s, float& q) {
   q = e * s;
 }
 
+// Pairs of FP32 values in one instruction.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float ex2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // A row's logits: lane l holds elements 4 (l + 32 i) .. + 3 (VEC, E % 4 == 0) or l + 32 i.
 template <bool VEC>
 __device__ __forceinline__ int elem(int lane, int j) {
@@ -118,44 +150,64 @@ __device__ __forceinline__ void load_row(const float* row, int E, int lane, floa
   }
 }
 
-// s (the row's scores, or for a low row exp(z - max z), which has the same shares) and
-// q = 1 - sigmoid(z) of this lane's elements, and the row's sum of s.
+// Sums of a row: this lane's parts of sum s and sum f s. exp(-z) may overflow to infinity here: that s is 0.
 template <int PER>
-__device__ __forceinline__ float scores(const float (&z)[PER], int E, float (&s)[PER], float (&q)[PER]) {
-  float S = 0.f;
+__device__ __forceinline__ void row_sums(const float (&z)[PER], const float (&f)[PER], float& S, float& F) {
+  f32x2 S2 = 0ull, F2 = 0ull;  // two zeros each
+  const f32x2 one = pack2(1.f, 1.f), k = pack2(-LOG2E, -LOG2E);
+#pragma unroll
+  for (int j = 0; j < PER; j += 2) {
+    float a, b;
+    unpack2(mul2(pack2(z[j], z[j + 1]), k), a, b);
+    unpack2(add2(pack2(ex2_of(a), ex2_of(b)), one), a, b);
+    const f32x2 s = pack2(rcp_of(a), rcp_of(b));
+    S2 = add2(S2, s);
+    F2 = fma2(pack2(f[j], f[j + 1]), s, F2);
+  }
+  float a, b;
+  unpack2(S2, a, b);
+  S = a + b;
+  unpack2(F2, a, b);
+  F = a + b;
+}
+
+// A low row: no s above LOW_ROW, the shares from exp(z - max z) instead. s: this lane's of them (0 for a row of
+// -infinity), S and F the row's sums.
+template <int PER>
+__device__ __noinline__ void low_row(const float (&z)[PER], const float (&f)[PER], float (&s)[PER], float& S, float& F) {
+  float m = z[0];
+#pragma unroll
+  for (int j = 1; j < PER; ++j) m = fmaxf(m, z[j]);
+  m = warp_max(m);
+  S = F = 0.f;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    sigmoid2(z[j], s[j], q[j]);
+    s[j] = m > -INFINITY ? exp_of(z[j] - m) : 0.f;
     S += s[j];
+    F = fmaf(f[j], s[j], F);
   }
   S = warp_sum(S);
-  if (S < LOW_ROW * E) {
-    float m = z[0];
+  F = warp_sum(F);
+}
+
+// One step of sums over lanes of 2 N values at once: the lanes whose `bit` is set go on with the upper N, the others
+// with the lower N, each having got the other lanes' share of them.
+template <int N>
+__device__ __forceinline__ void halve(float (&v)[2 * N], int lane, int bit) {
+  const bool up = lane & bit;
 #pragma unroll
-    for (int j = 1; j < PER; ++j) m = fmaxf(m, z[j]);
-    m = warp_max(m);
-    float acc = 0.f;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      s[j] = m > -INFINITY ? exp_of(z[j] - m) : 0.f;
-      acc += s[j];
-    }
-    S = warp_sum(acc);
+  for (int j = 0; j < N; ++j) {
+    const float keep = up ? v[j + N] : v[j], send = up ? v[j] : v[j + N];
+    v[j] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
   }
-  return S;
 }
+template <int N>
+__device__ __forceinline__ float (&first_of(float (&v)[2 * N]))[N] { return reinterpret_cast<float (&)[N]>(v); }
 
-template <int PER>
-__device__ __forceinline__ float dot(const float (&f)[PER], const float (&s)[PER]) {
-  float F = 0.f;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) F = fmaf(f[j], s[j], F);
-  return warp_sum(F);
-}
-
-// f - 1 of an expert with c of a sequence's picks, even = k T_b and inv = 1 / even (0 for none).
-__device__ __forceinline__ float load_of(int c, int E, long long even, float inv) {
-  return (float)((long long)c * E - even) * inv;
+// f - 1 of an expert with c of a sequence's picks, even = k T_b and inv = 1 / even (0 for none). The difference is a
+// whole number; `narrow`: it fits 32 bits (k T E does), and its conversion spares the FP64 unit.
+__device__ __forceinline__ float load_of(int c, int E, int even, float inv, bool narrow) {
+  return (narrow ? (float)(c * E - even) : (float)((long long)c * E - even)) * inv;
 }
 
 __global__ void __launch_bounds__(256) k_bal_zero(const BalArgs a) {
@@ -172,11 +224,13 @@ __global__ void __launch_bounds__(256) k_bal_zero(const BalArgs a) {
 }
 
 // Picks of a block's run of tokens: counted in shared memory, sequence by sequence, and added to the global
-// counts once per block and sequence. A piece of a sequence of fewer than SHORT tokens in the run goes to the
-// global counts directly: flushing E counters for it would cost more than its own picks do.
+// counts once per block and sequence. A piece of a sequence of fewer than SHORT tokens goes to the global counts
+// directly: flushing E counters for it would cost more than its own picks do. The picks, one run of memory, come to
+// shared memory up to COUNT_INTS at a time, all asked for at once.
 constexpr int SHORT = 64;
+constexpr int COUNT_INTS = 2048;
 __global__ void __launch_bounds__(256) k_bal_count(const BalArgs a) {
-  __shared__ int hist[MAX_E], total[MAX_E];
+  __shared__ int hist[MAX_E], total[MAX_E], picks[COUNT_INTS];
   __shared__ int tokens;
   const int lane = threadIdx.x & 31;
   const int per = (a.T + gridDim.x - 1) / gridDim.x;
@@ -185,28 +239,27 @@ __global__ void __launch_bounds__(256) k_bal_count(const BalArgs a) {
   if (threadIdx.x == 0) tokens = 0;
   pdl_wait();
   pdl_trigger();
-  __syncthreads();
   if (t0 >= t1) return;
   int b = seq_of(a, t0, lane);
   for (int t = t0; t < t1 && b < a.n_seq;) {  // piece [t, end) of sequence b
-    const int end = min(t1, max(t + 1, b < 0 ? seq_at(a, 0) : seq_at(a, b + 1)));
+    const int end = min(min(t1, t + COUNT_INTS / a.k), max(t + 1, b < 0 ? seq_at(a, 0) : seq_at(a, b + 1)));
     if (b >= 0) {
       const bool whole = end - t >= SHORT;
       int* sc = a.seq_counts + (size_t)b * a.E;
+      const int n = (end - t) * a.k;
+      __syncthreads();  // the picks before have been counted
+#pragma unroll 4
+      for (int i = threadIdx.x; i < n; i += 256) picks[i] = __ldg(a.idx + (size_t)t * a.k + i);
+      __syncthreads();
       int mine = 0;
-      for (int i = t + threadIdx.x; i < end; i += 256) {
-        const int* p = a.idx + (size_t)i * a.k;
-        if (__ldg(p) < 0) continue;
-        ++mine;
-        for (int j = 0; j < a.k; ++j) {
-          const int e = __ldg(p + j);
-          if (e < 0 || e >= a.E) continue;
-          atomicAdd(total + e, 1);
-          if (whole)
-            atomicAdd(hist + e, 1);
-          else
-            atomicAdd(sc + e, 1);
-        }
+#pragma unroll 1
+      for (int i = threadIdx.x; i < n; i += 256) {
+        const int at = i / a.k * a.k, e = picks[i];  // a token's first pick tells whether it counts
+        if (picks[at] < 0) continue;
+        if (at == i) ++mine;
+        if (e < 0 || e >= a.E) continue;
+        atomicAdd(total + e, 1);
+        atomicAdd(whole ? hist + e : sc + e, 1);
       }
       mine = __reduce_add_sync(0xffffffffu, mine);
       if (whole) {
@@ -220,14 +273,13 @@ __global__ void __launch_bounds__(256) k_bal_count(const BalArgs a) {
           if (tokens) atomicAdd(a.seq_tokens + b, tokens);
           tokens = 0;
         }
-        __syncthreads();
       } else if (lane == 0 && mine) {
         atomicAdd(a.seq_tokens + b, mine);
       }
     }
     t = end;
-    // the next sequence, or past a run of empty ones the next that holds a token
-    b = b + 1 >= a.n_seq || seq_at(a, b + 2) > t ? b + 1 : seq_of(a, t, lane);
+    // still this sequence, the next one, or past a run of empty ones the next that holds a token
+    if (b < 0 || seq_at(a, b + 1) <= t) b = b + 1 >= a.n_seq || seq_at(a, b + 2) > t ? b + 1 : seq_of(a, t, lane);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += 256)
@@ -241,22 +293,42 @@ struct Cursor {
   float inv = 0.f;       // 1 / T_b
   float f[PER];
   __device__ __forceinline__ bool inside(const BalArgs& a) const { return b >= 0 && b < a.n_seq; }
-  __device__ __forceinline__ void to(const BalArgs& a, int t, int lane) {
-    if (t < end) return;
+  // The sequence of token t, without its counts.
+  __device__ __forceinline__ void find(const BalArgs& a, int t, int lane) {
     b = seq_of(a, t, lane);
     end = max(t + 1, b < 0 ? seq_at(a, 0) : (b < a.n_seq ? seq_at(a, b + 1) : a.T));
+  }
+  __device__ __forceinline__ void to(const BalArgs& a, int t, int lane) {
+    if (t < end) return;
+    find(a, t, lane);
+    load(a, lane);
+  }
+  __device__ __forceinline__ void load(const BalArgs& a, int lane) {
+    int raw[PER], Tb = 0;
+    ask(a, lane, raw, Tb);
+    settle(a, lane, raw, Tb);
+  }
+  // The counts' loads, and what follows from them.
+  __device__ __forceinline__ void ask(const BalArgs& a, int lane, int (&raw)[PER], int& Tb) const {
+    Tb = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) raw[j] = 0;
     if (inside(a)) {
       const int* c = a.seq_counts + (size_t)b * a.E;
-      const int Tb = __ldcg(a.seq_tokens + b);
-      const long long even = (long long)a.k * Tb;
-      const float inv_even = Tb > 0 ? 1.0f / (float)even : 0.f;
-      inv = Tb > 0 ? 1.0f / (float)Tb : 0.f;
+      Tb = __ldcg(a.seq_tokens + b);
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const int e = elem<VEC>(lane, j);
-        f[j] = e < a.E ? load_of(__ldcg(c + e), a.E, even, inv_even) : 0.f;
+        if (e < a.E) raw[j] = __ldcg(c + e);
       }
     }
+  }
+  __device__ __forceinline__ void settle(const BalArgs& a, int lane, const int (&raw)[PER], int Tb) {
+    const int even = a.k * Tb;
+    const float inv_even = Tb > 0 ? 1.0f / (float)even : 0.f;
+    inv = Tb > 0 ? 1.0f / (float)Tb : 0.f;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) f[j] = elem<VEC>(lane, j) < a.E ? load_of(raw[j], a.E, even, inv_even, a.narrow) : 0.f;
   }
 };
 
@@ -267,52 +339,135 @@ __device__ __forceinline__ void warp_run(const BalArgs& a, int warp, int& t0, in
   t1 = min(a.T, t0 + per);
 }
 
-// (1 + F_t) / T_b of one row. FP32 is enough for one token's share; the long sum is held in FP64.
+// Blocks of an SM, by registers (a row's values take four to five times PER) and by the rows in flight.
 template <int PER>
-__device__ __forceinline__ float row_share(const float (&z)[PER], const float (&f)[PER], float inv, int E) {
-  float s[PER], q[PER];
-  const float S = scores<PER>(z, E, s, q);
-  const float F = dot<PER>(f, s);
-  return S > 0.f ? (1.0f + __fdividef(F, S)) * inv : 0.f;
-}
+constexpr int loss_blocks() { return PER > 8 ? 2 : PER > 4 ? 3 : 4; }
+template <int PER>
+constexpr int backward_blocks() { return PER > 8 ? 2 : 3; }
 
-// Blocks of an SM by registers: a row's values and the next row's take 4 to 5 PER of them.
-template <int PER>
-constexpr int loss_blocks() { return PER > 8 ? 2 : 4; }
-template <int PER>
-constexpr int backward_blocks() { return PER > 8 ? 1 : 3; }
+// Rows on their way: each lane copies what it will read itself of the next DEPTH rows into shared memory, so nobody
+// waits for anybody, and a warp has DEPTH rows in flight where registers hold one or two (2.8 TB/s).
+template <int PER, bool VEC>
+struct RowRing {
+  static constexpr int DEPTH = PER > 8 ? 4 : 8;
+  static constexpr int ROW = PER * 32;  // floats of a slot
+  float* slots;                         // this warp's
+  const float* base;                    // row 0 of the matrix
+  int E, next, end, lane;
+  __device__ __forceinline__ void issue() {
+    if (next < end) {
+      float* s = slots + (next & (DEPTH - 1)) * ROW;
+      const float* row = base + (size_t)next * E;
+      if (VEC) {
+#pragma unroll
+        for (int i = 0; i < PER / 4; ++i) {
+          const int e = 4 * (lane + 32 * i);
+          if (e < E)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(s + e)), "l"(row + e) : "memory");
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          const int e = lane + 32 * j;
+          if (e < E) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(s + e)), "l"(row + e) : "memory");
+        }
+      }
+      ++next;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ RowRing(float* smem, const float* logits, int E_, int t0, int t1, int warp, int lane_)
+      : slots(smem + warp * DEPTH * ROW), base(logits), E(E_), next(t0), end(t1), lane(lane_) {
+#pragma unroll
+    for (int i = 0; i < DEPTH - 1; ++i) issue();
+  }
+  // Row t (in order, each once), and the copy of one more row behind the last.
+  __device__ __forceinline__ void take(int t, float (&z)[PER]) {
+    issue();
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    const float* s = slots + (t & (DEPTH - 1)) * ROW;
+    if (VEC) {
+#pragma unroll
+      for (int i = 0; i < PER / 4; ++i) {
+        const int e = 4 * (lane + 32 * i);
+        uint4 v = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);  // -infinity past E
+        if (e < E) v = lds128(s + e);
+        z[4 * i] = __uint_as_float(v.x);
+        z[4 * i + 1] = __uint_as_float(v.y);
+        z[4 * i + 2] = __uint_as_float(v.z);
+        z[4 * i + 3] = __uint_as_float(v.w);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) z[j] = lane + 32 * j < E ? __uint_as_float(lds32(s + lane + 32 * j)) : -INFINITY;
+    }
+  }
+  static size_t bytes() { return sizeof(float) * 8 * DEPTH * ROW; }
+};
 
 // Sum over the block's tokens of (1 + F_t) / T_b in FP64; the last block to finish adds the
-// blocks' sums in block order. The next token's row is on its way while one is summed up.
+// blocks' sums, in a fixed order.
 template <int PER, bool VEC>
 __global__ void __launch_bounds__(256, loss_blocks<PER>()) k_bal_loss(const BalArgs a) {
+  extern __shared__ __align__(16) float ring_smem[];
   __shared__ double red[8];
   __shared__ bool last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int t0, t1;
   warp_run(a, warp, t0, t1);
-  float z[PER];
-  int first = -1;
-  if (t0 < t1) {
-    load_row<PER, VEC>(a.logits + (size_t)t0 * a.E, a.E, lane, z);
-    first = __ldg(a.idx + (size_t)t0 * a.k);
-  }
-  pdl_wait();  // the counts
-  double acc = 0.0;
+  RowRing<PER, VEC> rows(ring_smem, a.logits, a.E, t0, t1, warp, lane);
   Cursor<PER, VEC> cur;
-  for (int t = t0; t < t1; ++t) {
+  if (t0 < t1) cur.find(a, t0, lane);
+  pdl_wait();  // the counts
+  if (t0 < t1) cur.load(a, lane);
+  // Four rows at a time: eight sums over the lanes at once, after which the lanes with bit 4 set and bits 0, 1 clear
+  // hold one row's F each, and the lane 16 below its S.
+  const int row = (lane >> 2) & 3;
+  double acc = 0.0;
+  float few = 0.f;  // up to 16 tokens' shares
+  int n = 0;
+  for (int t = t0; t < t1; ++n) {
     cur.to(a, t, lane);
-    float zn[PER];
-    int firstn = -1;
-    if (t + 1 < t1) {
-      load_row<PER, VEC>(a.logits + (size_t)(t + 1) * a.E, a.E, lane, zn);
-      firstn = __ldg(a.idx + (size_t)(t + 1) * a.k);
-    }
-    if (cur.inside(a) && first >= 0) acc += (double)row_share<PER>(z, cur.f, cur.inv, a.E);
+    const int nb = min(4, min(t1, cur.end) - t);  // tokens of one sequence
+    const bool mine = row < nb && __ldg(a.idx + (size_t)(t + min(row, nb - 1)) * a.k) >= 0 && cur.inside(a);
+    float v[8];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) z[j] = zn[j];
-    first = firstn;
+    for (int i = 0; i < 4; ++i) {
+      v[i] = v[4 + i] = 0.f;
+      if (i < nb) {
+        float z[PER];
+        rows.take(t + i, z);
+        row_sums<PER>(z, cur.f, v[i], v[4 + i]);
+      }
+    }
+    halve<4>(v, lane, 16);
+    halve<2>(first_of<4>(v), lane, 8);
+    halve<1>(first_of<2>(first_of<4>(v)), lane, 4);
+    float x = v[0];
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    float S = __shfl_xor_sync(0xffffffffu, x, 16), F = x;
+    const unsigned low = __ballot_sync(0xffffffffu, mine && (lane & 19) == 16 && S < LOW_ROW * a.E);
+    if (low) {  // rare: row by row, read again
+      for (int i = 0; i < nb; ++i)
+        if ((low >> (16 + 4 * i)) & 1u) {
+          float z[PER], s[PER], Si, Fi;
+          load_row<PER, VEC>(a.logits + (size_t)(t + i) * a.E, a.E, lane, z);
+          low_row<PER>(z, cur.f, s, Si, Fi);
+          if (row == i) {
+            S = Si;
+            F = Fi;
+          }
+        }
+    }
+    if (mine && (lane & 19) == 16 && S > 0.f) few += (1.0f + __fdividef(F, S)) * cur.inv;
+    if ((n & 3) == 3) {
+      acc += (double)few;
+      few = 0.f;
+    }
+    t += nb;
   }
+  acc = warp_sum_d(acc + (double)few);
   if (lane == 0) red[warp] = acc;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -323,12 +478,20 @@ __global__ void __launch_bounds__(256, loss_blocks<PER>()) k_bal_loss(const BalA
     last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
   }
   __syncthreads();
-  if (!last || warp != 0) return;
+  if (!last) return;
+  // the blocks' sums: one load or two a thread (by one warp, fifteen in a row, this took a third of the kernel)
   __threadfence();
   double v = 0.0;
-  for (int i = lane; i < (int)gridDim.x; i += 32) v += __ldcg(a.partial + i);
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += 256) v += __ldcg(a.partial + i);
   v = warp_sum_d(v);
-  if (lane == 0) *a.loss = (float)(v * ((double)a.alpha / (double)a.n_seq));
+  __syncthreads();  // red[] has been read
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double sum = 0.0;
+    for (int w = 0; w < 8; ++w) sum += red[w];
+    *a.loss = (float)(sum * ((double)a.alpha / (double)a.n_seq));
+  }
 }
 
 // Counts and loss of a small call in one block: the counts stay in shared memory, and one launch replaces three.
@@ -392,16 +555,26 @@ __global__ void __launch_bounds__(1024) k_bal_one(const BalArgs g) {
       const int own = seq[i0 + i];
       if (own >= 0 && own != b) {
         b = own;
-        const long long even = (long long)g.k * tokens[b];
+        const int even = g.k * tokens[b];
         inv = 1.0f / (float)tokens[b];
         const float inv_even = 1.0f / (float)even;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
           const int e = elem<VEC>(lane, j);
-          f[j] = e < g.E ? load_of(counts[b * g.E + e], g.E, even, inv_even) : 0.f;
+          f[j] = e < g.E ? load_of(counts[b * g.E + e], g.E, even, inv_even, true) : 0.f;
         }
       }
-      if (own >= 0) acc += (double)row_share<PER>(z[i], f, inv, g.E);
+      if (own >= 0) {
+        float S, F;
+        row_sums<PER>(z[i], f, S, F);
+        S = warp_sum(S);
+        F = warp_sum(F);
+        if (S < LOW_ROW * g.E) {
+          float s[PER];
+          low_row<PER>(z[i], f, s, S, F);
+        }
+        if (S > 0.f) acc += (double)((1.0f + __fdividef(F, S)) * inv);
+      }
       if (i0 + AT + i < t1) load_row<PER, VEC>(g.logits + (size_t)(i0 + AT + i) * g.E, g.E, lane, z[i]);
     }
   }
@@ -413,12 +586,13 @@ __global__ void __launch_bounds__(1024) k_bal_one(const BalArgs g) {
   }
 }
 
-// A warp works on NB tokens at a time: a row each for the loss's part (the next row on its way meanwhile), then the
+// A warp works on NB tokens at a time: their rows for the loss's part, then the
 // NB tokens' picks side by side, 32 / NB lanes to a token (k <= 8: four tokens; picks of one token at a time would
 // leave three lanes in four idle, and the kernel is bound by instructions before it is bound by memory). A pick
 // adds its part to its place in the row just written.
 template <int PER, bool VEC, int NB>
 __global__ void __launch_bounds__(256, backward_blocks<PER>()) k_bal_backward(const BalArgs a) {
+  extern __shared__ __align__(16) float ring_smem[];
   constexpr int W = 32 / NB;  // lanes of a token's picks
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = lane / W, pick = lane % W;
   int t0, t1;
@@ -426,9 +600,13 @@ __global__ void __launch_bounds__(256, backward_blocks<PER>()) k_bal_backward(co
   pdl_wait();
   pdl_trigger();
   const float up = (a.dloss ? __ldg(a.dloss) : 1.0f) * (a.alpha / (float)a.n_seq);
-  float z[PER];
-  if (t0 < t1) load_row<PER, VEC>(a.logits + (size_t)t0 * a.E, a.E, lane, z);
+  // The first sequence's counts are asked for before the rows, behind which they would wait for microseconds.
   Cursor<PER, VEC> cur;
+  int raw[PER], Tb = 0;
+  if (t0 < t1) cur.find(a, t0, lane);
+  cur.ask(a, lane, raw, Tb);
+  RowRing<PER, VEC> rows(ring_smem, a.logits, a.E, t0, t1, warp, lane);
+  cur.settle(a, lane, raw, Tb);
   for (int t = t0; t < t1;) {
     cur.to(a, t, lane);
     const int nb = min(NB, min(t1, cur.end) - t);  // tokens of one sequence
@@ -442,21 +620,69 @@ __global__ void __launch_bounds__(256, backward_blocks<PER>()) k_bal_backward(co
       g = __ldg(a.dw + (size_t)(t + slot) * a.k + pick);
       zp = __ldg(a.logits + (size_t)(t + slot) * a.E + e);
     }
+    // Two rows at a time: their four sums over the lanes at once.
+#pragma unroll 1
+    for (int i = 0; i < nb; i += 2) {
+      f32x2 sq[2][PER / 2];  // s (1 - s)
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      if (i >= nb) break;
-      float zn[PER];
-      if (t + i + 1 < t1) load_row<PER, VEC>(a.logits + (size_t)(t + i + 1) * a.E, a.E, lane, zn);
-      if (cur.inside(a)) {
-        float s[PER], q[PER], d[PER];
-        const float S = scores<PER>(z, a.E, s, q);
-        const float inv = S > 0.f ? rcp_of(S) : 0.f;
-        const float F = dot<PER>(cur.f, s) * inv;
-        const float ci = up * cur.inv * inv;
-        const bool pad = (pads >> (i * W)) & 1u;  // selected, not multiplied: a padding row may hold anything
+      for (int r = 0; r < 2; ++r) {
+        if (i + r >= nb) break;
+        float z[PER];
+        rows.take(t + i + r, z);
+        f32x2 S2 = 0ull, F2 = 0ull;
+        const f32x2 one = pack2(1.f, 1.f), k = pack2(-LOG2E, -LOG2E);
 #pragma unroll
-        for (int j = 0; j < PER; ++j) d[j] = pad ? 0.f : (ci * s[j]) * ((cur.f[j] - F) * q[j]);
-        float* out = a.dlogits + (size_t)(t + i) * a.E;
+        for (int j = 0; j < PER; j += 2) {
+          float x, y;
+          unpack2(mul2(pack2(z[j], z[j + 1]), k), x, y);
+          const f32x2 e = pack2(ex2_of(fminf(x, 122.f)), ex2_of(fminf(y, 122.f)));  // so that e s is no infinity times 0
+          unpack2(add2(e, one), x, y);
+          const f32x2 s = pack2(rcp_of(x), rcp_of(y));
+          S2 = add2(S2, s);
+          F2 = fma2(pack2(cur.f[j], cur.f[j + 1]), s, F2);
+          sq[r][j / 2] = mul2(mul2(e, s), s);
+        }
+        float x, y;
+        unpack2(S2, x, y);
+        v[r] = x + y;
+        unpack2(F2, x, y);
+        v[2 + r] = x + y;
+      }
+      halve<2>(v, lane, 16);
+      halve<1>(first_of<2>(v), lane, 8);
+      float x = v[0];
+      x += __shfl_xor_sync(0xffffffffu, x, 4);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      if (!cur.inside(a)) continue;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (i + r >= nb) break;
+        float S = __shfl_sync(0xffffffffu, x, 8 * r), F = __shfl_sync(0xffffffffu, x, 16 + 8 * r);
+        float* out = a.dlogits + (size_t)(t + i + r) * a.E;
+        const bool pad = (pads >> ((i + r) * W)) & 1u;  // a padding row may hold anything: it is not multiplied
+        if (!pad && S < LOW_ROW * a.E) {
+          float z[PER], s[PER];
+          load_row<PER, VEC>(a.logits + (size_t)(t + i + r) * a.E, a.E, lane, z);
+          low_row<PER>(z, cur.f, s, S, F);
+#pragma unroll
+          for (int j = 0; j < PER; j += 2) {
+            float s0, q0, s1, q1;
+            sigmoid2(z[j], s0, q0);
+            sigmoid2(z[j + 1], s1, q1);
+            sq[r][j / 2] = pack2(s[j] * q0, s[j + 1] * q1);
+          }
+        }
+        const float inv = S > 0.f ? rcp_of(S) : 0.f, ci = up * cur.inv * inv, off = -F * inv * ci;
+        float d[PER];
+#pragma unroll
+        for (int j = 0; j < PER; j += 2)
+          unpack2(mul2(sq[r][j / 2], fma2(pack2(cur.f[j], cur.f[j + 1]), pack2(ci, ci), pack2(off, off))), d[j], d[j + 1]);
+        if (pad) {
+#pragma unroll
+          for (int j = 0; j < PER; ++j) d[j] = 0.f;
+        }
         if (VEC) {
 #pragma unroll
           for (int j = 0; j < PER / 4; ++j) {
@@ -470,8 +696,6 @@ __global__ void __launch_bounds__(256, backward_blocks<PER>()) k_bal_backward(co
             if (lane + 32 * j < a.E) out[lane + 32 * j] = d[j];
         }
       }
-#pragma unroll
-      for (int j = 0; j < PER; ++j) z[j] = zn[j];
     }
     if (a.dw && cur.inside(a)) {
       // sums over a token's lanes
@@ -524,14 +748,29 @@ using namespace flint::bal;
 namespace {
 
 constexpr int SMS = 152;
-constexpr int LOSS_BLOCKS = SMS * loss_blocks<4>();  // the loss kernel's blocks at most
-constexpr int COUNT_BLOCKS = SMS;
+constexpr int LOSS_BLOCKS = SMS * 4;  // the loss kernel's blocks at most
+constexpr int COUNT_BLOCKS = 2 * SMS;
+
+// Prepares a kernel once for each device: its dynamic shared memory, and the largest shared-memory carveout, which all
+// kernels of a call ask for, because an SM runs blocks of two kernels side by side only under one carveout.
+bool prepare(void (*kernel)(BalArgs), std::atomic<uint64_t>& done, size_t smem) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return false;
+  if ((done.load() >> dev) & 1) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return false;
+  done.fetch_or((uint64_t)1 << dev);
+  return true;
+}
 
 // A launch that may start while the kernel before it drains (each kernel waits for it itself).
-bool launch(void (*kernel)(BalArgs), int grid, cudaStream_t stream, const BalArgs& a, int block = 256) {
+bool launch(void (*kernel)(BalArgs), int grid, cudaStream_t stream, const BalArgs& a, int block = 256, size_t smem = 0) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -573,19 +812,29 @@ int row_blocks(int T, int per_sm) { return std::min((T + 7) / 8, SMS * per_sm); 
 
 template <int PER, bool VEC>
 bool launch_loss(const BalArgs& a, cudaStream_t stream) {
-  return launch(k_bal_loss<PER, VEC>, row_blocks(a.T, loss_blocks<PER>()), stream, a);
+  static std::atomic<uint64_t> done{0};
+  const size_t smem = RowRing<PER, VEC>::bytes();
+  return prepare(k_bal_loss<PER, VEC>, done, smem) &&
+         launch(k_bal_loss<PER, VEC>, row_blocks(a.T, loss_blocks<PER>()), stream, a, 256, smem);
+}
+template <int PER, bool VEC, int NB>
+bool launch_backward_as(const BalArgs& a, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  const size_t smem = RowRing<PER, VEC>::bytes();
+  return prepare(k_bal_backward<PER, VEC, NB>, done, smem) &&
+         launch(k_bal_backward<PER, VEC, NB>, row_blocks(a.T, backward_blocks<PER>()), stream, a, 256, smem);
 }
 template <int PER, bool VEC>
 bool launch_backward(const BalArgs& a, cudaStream_t stream) {
-  const int grid = row_blocks(a.T, backward_blocks<PER>());
-  return a.k <= 8 ? launch(k_bal_backward<PER, VEC, 4>, grid, stream, a) : launch(k_bal_backward<PER, VEC, 2>, grid, stream, a);
+  return a.k <= 8 ? launch_backward_as<PER, VEC, 4>(a, stream) : launch_backward_as<PER, VEC, 2>(a, stream);
 }
 bool one_block(const BalArgs& a) {
   return a.T <= ONE_TOKENS && a.n_seq <= ONE_TOKENS && (int64_t)a.T * a.E <= ONE_ELEMS && (int64_t)a.n_seq * a.E <= ONE_COUNTS;
 }
 template <int PER, bool VEC>
 bool launch_one(const BalArgs& a, cudaStream_t stream) {
-  return launch(k_bal_one<PER, VEC>, 1, stream, a, 1024);
+  static std::atomic<uint64_t> done{0};
+  return prepare(k_bal_one<PER, VEC>, done, 0) && launch(k_bal_one<PER, VEC>, 1, stream, a, 1024);
 }
 // f(PER, VEC) for the row length: elements a lane holds, and whether rows are made of 16-byte pieces.
 template <typename F>
@@ -622,6 +871,7 @@ extern "C" flint_moe_status flint_moe_balance(const flint_moe_config* c, const f
   a.E = c->num_experts;
   a.k = c->top_k;
   a.n_seq = n_seq;
+  a.narrow = (int64_t)c->top_k * T * c->num_experts < ((int64_t)1 << 31);
   a.alpha = alpha;
   a.logits = logits;
   a.idx = idx;
@@ -636,7 +886,9 @@ extern "C" flint_moe_status flint_moe_balance(const flint_moe_config* c, const f
   if (one_block(a)) {
     ok = by_row(a.E, [&](auto per, auto vec) { return launch_one<per(), vec()>(a, stream); });
   } else {
-    ok = launch(k_bal_zero, (int)std::min<size_t>(SMS, ((size_t)n_seq * a.E + 255) / 256), stream, a) &&
+    static std::atomic<uint64_t> zero_done{0}, count_done{0};
+    ok = prepare(k_bal_zero, zero_done, 0) && prepare(k_bal_count, count_done, 0) &&
+         launch(k_bal_zero, (int)std::min<size_t>(SMS, ((size_t)n_seq * a.E + 255) / 256), stream, a) &&
          (T == 0 || (launch(k_bal_count, std::min(COUNT_BLOCKS, (T + 255) / 256), stream, a) &&
                      by_row(a.E, [&](auto per, auto vec) { return launch_loss<per(), vec()>(a, stream); })));
   }
@@ -663,6 +915,7 @@ extern "C" flint_moe_status flint_moe_balance_backward(const flint_moe_config* c
   a.E = c->num_experts;
   a.k = c->top_k;
   a.n_seq = n_seq;
+  a.narrow = (int64_t)c->top_k * T * c->num_experts < ((int64_t)1 << 31);
   a.renorm = c->renormalize;
   a.routed_scale = c->routed_scale;
   a.alpha = alpha;

@@ -72,9 +72,13 @@ __device__ __forceinline__ uint32_t f2b2(float lo, float hi) {
 // Plan (one block): tokens sorted by adapter, stably, into tiles. Warp w owns a
 // run of consecutive tokens; the 32 tokens of a step find their fellows with
 // match_any, so every token's place follows from counts and lane masks alone.
+// Short loops on purpose: between calls that stream 100 MB the code itself comes
+// from memory, and every stretch of it costs up to a microsecond.
 // ---------------------------------------------------------------------------
-__host__ __device__ inline size_t plan_smem(int n) { return sizeof(int) * ((size_t)34 * (n + 1) + 3 * (n + 2)); }
-constexpr int PB = 8;  // steps of 32 tokens whose adapters a warp holds at once
+constexpr int PLAN_T = 16384;  // tokens whose adapters fit in shared memory beside the counts
+__host__ __device__ inline size_t plan_smem(int n, int T) {
+  return sizeof(int) * ((size_t)34 * (n + 1) + 3 * (n + 2) + (T <= PLAN_T ? T : 0));
+}
 
 // Exclusive sums of f(0 .. n-1) into out[0 .. n], by one warp.
 template <typename F>
@@ -118,41 +122,42 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const Args a) {
   int* tf = lasts + G;     // first tile of each group
   int* cf = tf + G + 1;    // first chunk
   int* sf = cf + G + 1;    // first partial slot
+  int* ids = sf + G + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < 32 * G; i += 1024) hist[i] = 0;
   pdl_wait();
   pdl_trigger();
+  // The tokens' adapters in shared memory, all asked for at once; past PLAN_T of them they stay where they are.
+  const bool staged = a.T <= PLAN_T;
+  if (staged) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < a.T; i += 1024) ids[i] = __ldg(a.adapter + i);
+  }
+  __syncthreads();
+  const int* src = staged ? ids : a.adapter;
   const int L = (a.T + 1023) / 1024 * 32, t0 = warp * L, t1 = min(a.T, t0 + L);
   int* mine = hist + warp * G;
-  // Groups of up to PB steps of 32 tokens, all loaded at once (-1 past the run).
-  int g[PB];
-  auto load = [&](int i) {
-#pragma unroll
-    for (int j = 0; j < PB; ++j) {
-      const int t = i + 32 * j + lane;
-      g[j] = t < t1 ? __ldg(a.adapter + t) : 0;
+  // One step of 32 tokens from i: the group of this lane's (-1: none) and its place behind what mine[] holds, which
+  // then grows by the step's tokens.
+  auto step = [&](int i, int& g) {
+    g = -1;
+    if (i + lane < t1) {
+      g = src[i + lane];
+      if (g < 0 || g >= a.n) g = a.n;
     }
-#pragma unroll
-    for (int j = 0; j < PB; ++j) {
-      if (g[j] < 0 || g[j] >= a.n) g[j] = a.n;
-      if (i + 32 * j + lane >= t1) g[j] = -1;
-    }
+    const unsigned same = __match_any_sync(0xffffffffu, g);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    int at = 0;
+    if (g >= 0) at = mine[g] + rank;
+    __syncwarp();
+    if (g >= 0 && rank == 0) mine[g] += __popc(same);
+    __syncwarp();
+    return at;
   };
-  load(t0);
-  __syncthreads();
-  int place[PB];  // of the last batch's tokens within their warp's part of the group
-  for (int i = t0; i < t1; i += 32 * PB) {
-    if (i > t0) load(i);
-#pragma unroll
-    for (int j = 0; j < PB; ++j) {
-      if (i + 32 * j >= t1) break;
-      const unsigned same = __match_any_sync(0xffffffffu, g[j]);
-      const int rank = __popc(same & ((1u << lane) - 1));
-      if (g[j] >= 0) place[j] = mine[g[j]] + rank;
-      __syncwarp();
-      if (g[j] >= 0 && rank == 0) mine[g[j]] += __popc(same);
-      __syncwarp();
-    }
+#pragma unroll 1
+  for (int i = t0; i < t1; i += 32) {
+    int g;
+    step(i, g);
   }
   __syncthreads();
   for (int c = warp; c < G; c += 32) {  // the warps' counts of a group -> their first places in it
@@ -173,28 +178,13 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const Args a) {
   if (warp == 1 && a.chunks) warp_scan(G, lane, cf, chunks_of);
   if (warp == 2 && a.chunks) warp_scan(G, lane, sf, [&](int c) { return chunks_of(c) > 1 ? chunks_of(c) : 0; });
   __syncthreads();
-  const bool again = L > 32 * PB;  // more than one batch: only the last one's places are still known
-  for (int i = t0; i < t1; i += 32 * PB) {
-    if (again) load(i);
-#pragma unroll
-    for (int j = 0; j < PB; ++j) {
-      if (i + 32 * j >= t1) break;
-      int at = 0;
-      if (again) {
-        const unsigned same = __match_any_sync(0xffffffffu, g[j]);
-        const int rank = __popc(same & ((1u << lane) - 1));
-        if (g[j] >= 0) at = mine[g[j]] + rank;
-        __syncwarp();
-        if (g[j] >= 0 && rank == 0) mine[g[j]] += __popc(same);
-        __syncwarp();
-      } else if (g[j] >= 0) {
-        at = mine[g[j]] + place[j];
-      }
-      if (g[j] >= 0 && at < cnt[g[j]]) {  // (no place for tokens without an adapter where they need none)
-        const int t = i + 32 * j + lane;
-        a.rowmap[tf[g[j]] * TM + at] = t;
-        if (at == cnt[g[j]] - 1) lasts[g[j]] = t;
-      }
+#pragma unroll 1
+  for (int i = t0; i < t1; i += 32) {
+    int g;
+    const int at = step(i, g);
+    if (g >= 0 && at < cnt[g]) {  // (no place for tokens without an adapter where they need none)
+      a.rowmap[tf[g] * TM + at] = i + lane;
+      if (at == cnt[g] - 1) lasts[g] = i + lane;
     }
   }
   __syncthreads();
@@ -1466,13 +1456,17 @@ bool make_maps(Maps* m, const flint_lora* l, const Args& p) {
   return !p.out || map_rows(&m->out, p.out, D, p.ldo, p.T, 32, 32);
 }
 
-// Opts a kernel in to its dynamic shared memory, once for each device.
+// Prepares a kernel once for each device: its dynamic shared memory, and the largest shared-memory carveout, which all
+// kernels of a call ask for, because an SM runs blocks of two kernels side by side only under one carveout.
 template <typename K>
-bool want_smem(K kernel, std::atomic<uint64_t>& done, size_t smem) {
+bool prepare(K kernel, std::atomic<uint64_t>& done, size_t smem) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return false;
   if ((done.load() >> dev) & 1) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return false;
   done.fetch_or((uint64_t)1 << dev);
   return true;
 }
@@ -1497,11 +1491,11 @@ bool launch(void (*kernel)(P...), dim3 grid, int block, size_t smem, int cx, cud
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
-std::atomic<uint64_t> g_plan{0}, g_shrink{0};
+std::atomic<uint64_t> g_plan{0}, g_shrink{0}, g_dw_sum{0};
 
 bool run_plan(const Args& p, cudaStream_t stream) {
-  return want_smem(k_lora_plan, g_plan, plan_smem(FLINT_LORA_MAX_ADAPTERS)) &&
-         launch(k_lora_plan, dim3(1), 1024, plan_smem(p.n), 0, stream, p);
+  return prepare(k_lora_plan, g_plan, plan_smem(FLINT_LORA_MAX_ADAPTERS, PLAN_T)) &&
+         launch(k_lora_plan, dim3(1), 1024, plan_smem(p.n, p.T), 0, stream, p);
 }
 
 // h (and with `grads` g) of every tile. CTAs of a tile's cluster: as many as run at once, two on an SM (4096 tokens of
@@ -1511,7 +1505,7 @@ bool run_shrink(const Args& p, const Maps& m, bool grads, cudaStream_t stream) {
   const int kb = (std::min(p.K, grads ? p.N : p.K) + BK - 1) / BK, per = p.max_tiles * (grads ? 2 : 1);
   int S = 1;
   while (S < 8 && per * S * 2 <= 2 * sm_count() && S * 2 <= kb) S *= 2;
-  return want_smem(k_lora_shrink, g_shrink, shrink_smem(FLINT_LORA_MAX_RANK, true)) &&
+  return prepare(k_lora_shrink, g_shrink, shrink_smem(FLINT_LORA_MAX_RANK, true)) &&
          launch(k_lora_shrink, dim3(S, p.max_tiles, grads ? 2 : 1), SHR_THREADS, shrink_smem(p.R, grads), S, stream, p, m);
 }
 
@@ -1521,7 +1515,7 @@ bool run_expand_as(const Args& p, const Maps& m, cudaStream_t stream) {
   const int D = GRAD ? p.K : p.N;
   const int64_t items = (int64_t)p.max_tiles * ((D + 127) / 128);
   const size_t smem = exp_smem(p.R);
-  return want_smem(k_lora_expand<GRAD, WIDE>, done, smem) &&
+  return prepare(k_lora_expand<GRAD, WIDE>, done, smem) &&
          launch(k_lora_expand<GRAD, WIDE>, dim3((unsigned)std::min<int64_t>(sm_count(), items)), EXP_THREADS, smem, 0, stream, p, m);
 }
 template <bool GRAD>
@@ -1534,7 +1528,7 @@ bool run_dw(const Args& p, const Maps& m, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   // chunks: the tiles of adapters in runs of CT, and a shorter run for each adapter
   const int chunks = std::min(p.max_tiles, p.max_tiles / p.CT + std::min(p.n, p.T) + 1);
-  return want_smem(k_lora_dw<WIDE>, done, dw_smem(p.R)) &&
+  return prepare(k_lora_dw<WIDE>, done, dw_smem(p.R)) &&
          launch(k_lora_dw<WIDE>, dim3(p.slabs_a + p.slabs_b, chunks), DW_THREADS, dw_smem(p.R), 0, stream, p, m);
 }
 
@@ -1543,7 +1537,7 @@ bool run_few_as(FewArgs p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   const int groups = std::min(p.T, p.n + (p.with_none ? 1 : 0)), most = few_pieces(p.N);
   p.smem = std::max(few_plan(p.R, 8 * NT, most, FEW_SMEM).total, few_plan(p.R, 8, most, FEW_SMEM).total);
-  return want_smem(k_lora_few<NT, STEP>, done, 184 * 1024) &&
+  return prepare(k_lora_few<NT, STEP>, done, 184 * 1024) &&
          launch(k_lora_few<NT, STEP>, dim3(FEW_S, groups), FEW_THREADS, p.smem, FEW_S, stream, p);
 }
 bool run_few(const FewArgs& p, cudaStream_t stream) {
@@ -1698,7 +1692,8 @@ extern "C" flint_moe_status flint_lora_backward(const flint_lora* l, const uint1
       !(p.R > 64 ? run_dw<true>(p, m, stream) : run_dw<false>(p, m, stream)) || (dx_out && !run_expand<true>(p, m, stream)))
     return FLINT_MOE_ECUDA;
   const int64_t all = (int64_t)p.R * (p.K + p.N);
-  if (!launch(k_lora_dw_sum, dim3((unsigned)std::min<int64_t>((all + 2047) / 2048, std::max(1, 152 * 8 / p.n)), p.n), 256, 0, 0,
+  if (!prepare(k_lora_dw_sum, g_dw_sum, 0) ||
+      !launch(k_lora_dw_sum, dim3((unsigned)std::min<int64_t>((all + 2047) / 2048, std::max(1, 152 * 8 / p.n)), p.n), 256, 0, 0,
               stream, p))
     return FLINT_MOE_ECUDA;
   return FLINT_MOE_OK;
