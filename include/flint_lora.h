@@ -19,7 +19,8 @@
  * workspaces 256-byte aligned (FLINT_MOE_EALIGN). A workspace needs no
  * initialisation, holds nothing between calls, and must not be shared by calls
  * in flight at the same time. Results do not depend on timing: every sum has a
- * fixed order.
+ * fixed order. A device-side wait that gave up sets FLINT_MOE_DEV_ERR_TIMEOUT in
+ * the workspace's status word (flint_moe_read_status), which each call clears.
  */
 #ifndef FLINT_LORA_H_
 #define FLINT_LORA_H_
@@ -74,8 +75,11 @@ size_t flint_gemv_lora_workspace_bytes(const flint_lora* lora, int32_t max_batch
  *   y[t] = bf16(G c x[t] + s_a B_a (A_a x[t])),   one rounding.
  * packed, N, K, weight_fmt, x, B, y, dev_status as flint_gemv (without its
  * norm prologue: x is the projection's input as it is); the adapters' out_dim
- * and in_dim must be N and K (FLINT_MOE_EINVAL). x, y contiguous. The
- * adapters' work runs beside the GEMV, which it is launched with. */
+ * and in_dim must be N and K (FLINT_MOE_EINVAL). x, y contiguous, not
+ * overlapping. dev_status NULL: the workspace's status word instead. Two
+ * kernels: the adapters' part in FP32 into the workspace, and the GEMV, launched
+ * with programmatic dependent launch so that it runs beside it up to its last
+ * step, the sum of both. */
 flint_moe_status flint_gemv_lora(const void* packed, int32_t N, int32_t K, int32_t weight_fmt, const uint16_t* x,
                                  int32_t B, uint16_t* y, const flint_lora* lora, const int32_t* adapter,
                                  void* workspace, size_t workspace_bytes, int32_t* dev_status, cudaStream_t stream);
@@ -90,9 +94,10 @@ size_t flint_lora_backward_workspace_bytes(const flint_lora* lora, int32_t max_t
  * with the sums over the tokens of adapter a (zero for an adapter without
  * tokens; all num_adapters gradients are written, also for T = 0). dx_in: the
  * projection's own part of the gradient, NULL means zero; dx_out may be dx_in,
- * or NULL (then only da and db are computed). x rows are ldx apart. da, db:
- * bf16, the shapes of a and b. dx_out must not overlap x, dy or (otherwise)
- * dx_in. */
+ * or NULL (then only da and db are computed; lddx is not read). x rows are ldx
+ * apart. da, db: bf16, the shapes of a and b. Overlaps are refused
+ * (FLINT_MOE_EINVAL): dx_out with x, dy or (otherwise) dx_in; da and db with
+ * one another, the adapters, x, dy or dx. */
 flint_moe_status flint_lora_backward(const flint_lora* lora, const uint16_t* x, int64_t ldx, const uint16_t* dy,
                                      int64_t lddy, const int32_t* adapter, int32_t T, const uint16_t* dx_in,
                                      uint16_t* dx_out, int64_t lddx, uint16_t* da, uint16_t* db, void* workspace,

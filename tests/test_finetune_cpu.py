@@ -55,7 +55,7 @@ def test_lora_apply_refusals(lib):
     assert call(lora=None) == fb.EINVAL
     for kw in (dict(T=-1), dict(T=65537), dict(x=None), dict(ad=None), dict(yo=None), dict(w=None), dict(ldx=248),
                dict(ldy=504), dict(nb=16), dict(yo=0x1000000), dict(yo=0x1000000 + 16), dict(yo=0x2000000 + 16),
-               dict(yi=0x3000000 + 40 * 1024 - 16)):
+               dict(yi=0x3000000 + 40 * 1024 - 16), dict(ldx=1 << 31), dict(ldy=1 << 31)):
         assert call(**kw) == fb.EINVAL, kw
     for kw in (dict(x=0x1000002), dict(yi=0x2000008), dict(yo=0x3000004), dict(ad=0x500002), dict(w=ws + 16), dict(ldx=260),
                dict(ldy=513)):
@@ -81,7 +81,9 @@ def test_lora_backward_refusals(lib):
              db=0x8000000, w=0x4000000, nb=1 << 30):
         return lib.flint_lora_backward(ctypes.byref(l), x, ldx, dy, lddy, ad, T, di, do, lddx, da, db, w, nb, None)
     for kw in (dict(T=-1), dict(T=65537), dict(x=None), dict(dy=None), dict(ad=None), dict(da=None), dict(db=None), dict(w=None),
-               dict(nb=64), dict(ldx=128), dict(lddy=256), dict(lddx=8), dict(do=0x1000000), dict(do=0x2000010), dict(di=0x3000010)):
+               dict(nb=64), dict(ldx=128), dict(lddy=256), dict(lddx=8), dict(do=0x1000000), dict(do=0x2000010), dict(di=0x3000010),
+               dict(da=0x100000), dict(db=0x200010), dict(db=0x100000), dict(da=0x1000000), dict(db=0x2000000), dict(da=0x3000000),
+               dict(da=0x8000000 - 16), dict(ldx=1 << 31), dict(lddy=1 << 31), dict(lddx=1 << 31)):
         assert call(**kw) == fb.EINVAL, kw
     for kw in (dict(x=0x1000004), dict(dy=0x2000004), dict(do=0x3000004), dict(di=0x3000004), dict(da=0x7000002), dict(db=0x8000008),
                dict(w=0x4000020), dict(ad=0x500002), dict(ldx=260), dict(lddx=260)):

@@ -281,6 +281,42 @@ def test_streams_and_graphs():
         assert torch.equal(y, y0) and all(torch.equal(u, v) for u, v in zip((dx, dA, dB), g0))
 
 
+def test_gemv_lora_in_a_graph_and_beside_another_stream():
+    """Captured and replayed on new rows, indexes and adapters while the same operator runs on another stream with its
+    own workspace."""
+    D, R, n, B = 2048, 16, 6, 12
+    p, packed, _ = gemv_case(B, D, D, R, n, fb.NVFP4, 95)
+    q, _, _ = gemv_case(B, D, D, R, n, fb.NVFP4, 96)
+    want_q = gemv_lora(q, packed, fb.NVFP4)
+    lora = fb.flint_lora_init(p.d_A, p.d_B, p.d_scale)
+    ws = ws_of(fb.flint_gemv_lora_workspace_bytes(lora, B))
+    y = torch.empty_like(p.d_x)
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        fb.flint_gemv_lora(packed, D, D, fb.NVFP4, p.d_x, B, y, lora, p.d_adapter, ws)
+    for seed in (1, 2):
+        r = Pool(B, D, D, R, n, seed).to(DEV)
+        for k in ("x", "A", "B", "scale", "adapter"):
+            getattr(p, "d_" + k).copy_(getattr(r, "d_" + k))
+        torch.cuda.synchronize()
+        got_q = []
+        with torch.cuda.stream(other):
+            got_q.append(gemv_lora(q, packed, fb.NVFP4))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got_q[0], want_q) and torch.equal(y, gemv_lora(r, packed, fb.NVFP4))
+
+
+@pytest.mark.parametrize("T,n", [(32, 1), (32, 3), (29, 29), (17, 2), (9, 1)])
+@pytest.mark.parametrize("R", [8, 48, 128])
+def test_groups_of_many_rows_of_one_adapter(T, n, R):
+    """Up to 32 rows of one adapter: more than one tile of 8 tokens in a cluster, more pieces of B than are held."""
+    p = Pool(T, 520, 4360, R, n, 100 * T + R, [t % n for t in range(T)]).to(DEV)
+    check(apply(p, p.d_y), *p.expect_apply(f64(p.y)), "groups")
+
+
 def test_gradients_against_differences():
     """The kernels' gradients along a random direction against central differences of the float64 definition of
     L = sum y dy."""

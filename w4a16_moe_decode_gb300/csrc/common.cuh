@@ -190,7 +190,7 @@ __device__ __forceinline__ uint64_t global_ns() {
 }
 
 // Bounded wait on an mbarrier phase: gives up after ~limit_ns of wall time,
-// setting FLINT_MOE_DEV_ERR_TIMEOUT in *status. Never spins forever.
+// setting FLINT_MOE_DEV_ERR_TIMEOUT in *status (if there is one). Never spins forever.
 constexpr uint64_t WAIT_LIMIT_NS = 200ull * 1000ull * 1000ull;  // 200 ms
 
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* status) {
@@ -199,7 +199,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* s
   for (uint32_t it = 0;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63) == 63 && global_ns() - t0 > WAIT_LIMIT_NS) {
-      atomicOr(status, FLINT_MOE_DEV_ERR_TIMEOUT);
+      if (status) atomicOr(status, FLINT_MOE_DEV_ERR_TIMEOUT);
       return false;
     }
   }

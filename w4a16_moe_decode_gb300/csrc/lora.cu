@@ -1298,12 +1298,16 @@ namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Whether two sets of rows (count rows of `cols` bf16, ld apart) share memory, by their extents.
-bool overlap(const void* p, int64_t ldp, int colsp, const void* q, int64_t ldq, int colsq, int rows) {
-  if (!p || !q || rows == 0) return false;
+// Bytes from the first of `rows` rows (cols bf16 values, ld apart) to the end of the last.
+size_t rows_bytes(int64_t ld, int cols, int rows) { return rows == 0 ? 0 : 2 * ((size_t)(rows - 1) * ld + cols); }
+bool overlap_bytes(const void* p, size_t np, const void* q, size_t nq) {
+  if (!p || !q || np == 0 || nq == 0) return false;
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  const uintptr_t na = 2 * ((uintptr_t)(rows - 1) * ldp + colsp), nb = 2 * ((uintptr_t)(rows - 1) * ldq + colsq);
-  return a < b + nb && b < a + na;
+  return a < b + nq && b < a + np;
+}
+// Whether two sets of rows share memory, by their extents.
+bool overlap(const void* p, int64_t ldp, int colsp, const void* q, int64_t ldq, int colsq, int rows) {
+  return overlap_bytes(p, rows_bytes(ldp, colsp, rows), q, rows_bytes(ldq, colsq, rows));
 }
 
 flint_moe_status check_lora(const flint_lora* l) {
@@ -1636,7 +1640,7 @@ extern "C" flint_moe_status flint_gemv_lora(const void* packed, int32_t N, int32
   p.clear = !dev_status;
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(packed, 16)) return FLINT_MOE_EALIGN;  // before the first launch
   if (!run_few(p, stream)) return FLINT_MOE_ECUDA;
-  return gemv_impl(packed, N, K, fmt, x, B, y, nullptr, 0.f, p.out32, adapter, l->num_adapters, dev_status, stream);
+  return gemv_impl(packed, N, K, fmt, x, B, y, nullptr, 0.f, p.out32, adapter, l->num_adapters, p.status, stream);
 }
 
 extern "C" flint_moe_status flint_lora_backward(const flint_lora* l, const uint16_t* x, int64_t ldx, const uint16_t* dy,
@@ -1665,6 +1669,15 @@ extern "C" flint_moe_status flint_lora_backward(const flint_lora* l, const uint1
                  overlap(dx_out, lddx, l->in_dim, dy, lddy, l->out_dim, T) ||
                  (dx_in != dx_out && overlap(dx_out, lddx, l->in_dim, dx_in, lddx, l->in_dim, T))))
     return FLINT_MOE_EINVAL;
+  // the gradients are written while the rows and the adapters are still read
+  const size_t na = nw * l->in_dim * 2, nb = nw * l->out_dim * 2;
+  const size_t xb = rows_bytes(ldx, l->in_dim, T), yb = rows_bytes(lddy, l->out_dim, T), db_x = rows_bytes(lddx, l->in_dim, T);
+  const struct { const void* p; size_t n; } outs[2] = {{da, na}, {db, nb}},
+      ins[6] = {{l->a, na}, {l->b, nb}, {x, xb}, {dy, yb}, {dx_in, dx_out ? db_x : 0}, {dx_out, dx_out ? db_x : 0}};
+  for (const auto& o : outs)
+    for (const auto& i : ins)
+      if (overlap_bytes(o.p, o.n, i.p, i.n)) return FLINT_MOE_EINVAL;
+  if (overlap_bytes(da, na, db, nb)) return FLINT_MOE_EINVAL;
   const WsPlan w = ws_plan(l, T, true, false);
   if (ws_bytes < w.total) return FLINT_MOE_EINVAL;
   Args p = tile_args(l, adapter, T, static_cast<uint8_t*>(ws), w);
