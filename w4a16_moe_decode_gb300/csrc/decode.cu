@@ -2176,12 +2176,22 @@ int sm_count() {
 template <typename K, typename Args>
 cudaError_t launch_any(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const Args& a);
 
-// The same launch with a cluster of (1, cy, 1) CTAs.
-template <typename K, typename Args>
-cudaError_t launch_cluster(K kernel, dim3 grid, dim3 block, size_t smem, int cy, cudaStream_t stream, const Args& a) {
-  if (smem > 32 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// The GEMV kernels' launches: attributes are set once for each device instead of at every call (two runtime calls of
+// three that a launch would make).
+template <auto KERNEL, typename Args>
+cudaError_t launch_gemv(dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t stream, const Args& a) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev < 64 && ((done.load() >> dev) & 1);
+  if (!known) {
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_LIMIT);
+    // the carveout that all kernels here ask for (see launch_any)
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
+    if (dev < 64) done.fetch_or((uint64_t)1 << dev);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -2193,11 +2203,11 @@ cudaError_t launch_cluster(K kernel, dim3 grid, dim3 block, size_t smem, int cy,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = 1;
-  attr[1].val.clusterDim.y = cy;
+  attr[1].val.clusterDim.y = cluster;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, KERNEL, a);
 }
 
 template <typename K>
@@ -2672,8 +2682,8 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
     cudaError_t e;
     const bool nv = fmt == FLINT_MOE_NVFP4, add = add32 != nullptr;
 #define FLINT_SPLIT(FMT, NT, SOLO) \
-  (add ? launch_cluster(k_gemv_split<FMT, NT, SOLO, true>, grid, block, smem, S, stream, a) \
-       : launch_cluster(k_gemv_split<FMT, NT, SOLO, false>, grid, block, smem, S, stream, a))
+  (add ? launch_gemv<k_gemv_split<FMT, NT, SOLO, true>>(grid, block, smem, S, stream, a) \
+       : launch_gemv<k_gemv_split<FMT, NT, SOLO, false>>(grid, block, smem, S, stream, a))
     switch (B == 1 ? 0 : ntmax) {
       case 0: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 1, true) : FLINT_SPLIT(FLINT_MOE_BF16, 1, true); break;
       case 1: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 1, false) : FLINT_SPLIT(FLINT_MOE_BF16, 1, false); break;
@@ -2691,10 +2701,10 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
   cudaError_t e;
   const bool nv = fmt == FLINT_MOE_NVFP4, add = add32 != nullptr;
 #define FLINT_GEMV(KERNEL, NT)                                                                          \
-  (nv ? (add ? launch_any(KERNEL<FLINT_MOE_NVFP4, NT, true>, grid, block, smem, stream, a)              \
-             : launch_any(KERNEL<FLINT_MOE_NVFP4, NT, false>, grid, block, smem, stream, a))            \
-      : (add ? launch_any(KERNEL<FLINT_MOE_BF16, NT, true>, grid, block, smem, stream, a)               \
-             : launch_any(KERNEL<FLINT_MOE_BF16, NT, false>, grid, block, smem, stream, a)))
+  (nv ? (add ? launch_gemv<KERNEL<FLINT_MOE_NVFP4, NT, true>>(grid, block, smem, 0, stream, a)          \
+             : launch_gemv<KERNEL<FLINT_MOE_NVFP4, NT, false>>(grid, block, smem, 0, stream, a))        \
+      : (add ? launch_gemv<KERNEL<FLINT_MOE_BF16, NT, true>>(grid, block, smem, 0, stream, a)           \
+             : launch_gemv<KERNEL<FLINT_MOE_BF16, NT, false>>(grid, block, smem, 0, stream, a)))
   const size_t rows_smem = gemv_rows_smem(K, B, fmt, nw, ntmax, &o1, &o2, &o3, &o4);
   if (ntmax > 1 && N / 16 > sm_count() && rows_smem <= SMEM_LIMIT) {
     // more tiles than blocks that run at once: blocks that stage the rows once for several tiles

@@ -1340,9 +1340,9 @@ int sm_count() {
 // Tiles at most: full ones, and a part-filled one for each group of tokens.
 int tiles_most(const flint_lora* l, int T) { return T / TM + std::min(l->num_adapters + 1, T); }
 
-// Tiles of a chunk of the weights' gradients, so that slabs x chunks fill the SMs about
-// four times (two CTAs of an SM, twice).
-constexpr int DW_CTAS = 152 * 4;
+// Tiles of a chunk of the weights' gradients, so that slabs x chunks are about as many CTAs as run at once, two on an
+// SM (8192 tokens of 2048 x 2048, rank 32: 62.3 us a call; with three times as many 67.6).
+constexpr int DW_CTAS = 152 * 2;
 int slabs(const flint_lora* l) { return (l->in_dim + 127) / 128 + (l->out_dim + 127) / 128; }
 int chunk_tiles(const flint_lora* l, int T) {
   return std::max(1, (int)(((int64_t)T / TM * slabs(l) + DW_CTAS - 1) / DW_CTAS));
