@@ -7,6 +7,7 @@
 //   dA_a = sum_t g_t x_t^T         dB_a = sum_t dy_t h_t^T
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "flint_lora.h"
@@ -80,24 +81,23 @@ __host__ __device__ inline size_t plan_smem(int n, int T) {
   return sizeof(int) * ((size_t)34 * (n + 1) + 3 * (n + 2) + (T <= PLAN_T ? T : 0));
 }
 
-// Exclusive sums of f(0 .. n-1) into out[0 .. n], by one warp.
+// Exclusive sums of f(0 .. n-1) into out[0 .. n], by one warp, 32 at a time.
 template <typename F>
 __device__ __forceinline__ void warp_scan(int n, int lane, int* out, F f) {
-  const int per = (n + 31) / 32, i0 = min(n, lane * per), i1 = min(n, i0 + per);
-  int own = 0;
-  for (int i = i0; i < i1; ++i) own += f(i);
-  int inc = own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
+  int carry = 0;
+#pragma unroll 1
+  for (int base = 0; base < n; base += 32) {
+    const int i = base + lane, v = i < n ? f(i) : 0;
+    int inc = v;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (i < n) out[i] = carry + inc - v;
+    carry += __shfl_sync(0xffffffffu, inc, 31);
   }
-  int at = inc - own;
-  for (int i = i0; i < i1; ++i) {
-    out[i] = at;
-    at += f(i);
-  }
-  if (lane == 31) out[n] = inc;
+  if (lane == 0) out[n] = carry;
 }
 
 // The last g in [0, n) with first[g] <= i: the group of item i < first[n].
@@ -174,9 +174,13 @@ __global__ void __launch_bounds__(1024) k_lora_plan(const Args a) {
   __syncthreads();
   auto tiles_of = [&](int c) { return (cnt[c] + TM - 1) / TM; };
   auto chunks_of = [&](int c) { return c == a.n ? 0 : (tiles_of(c) + a.CT - 1) / a.CT; };
-  if (warp == 0) warp_scan(G, lane, tf, tiles_of);
-  if (warp == 1 && a.chunks) warp_scan(G, lane, cf, chunks_of);
-  if (warp == 2 && a.chunks) warp_scan(G, lane, sf, [&](int c) { return chunks_of(c) > 1 ? chunks_of(c) : 0; });
+  // warps 0 .. 2: the first tile, chunk and partial slot of each group
+  if (warp < (a.chunks ? 3 : 1))
+    warp_scan(G, lane, warp == 0 ? tf : warp == 1 ? cf : sf, [&](int c) {
+      if (warp == 0) return tiles_of(c);
+      const int k = chunks_of(c);
+      return warp == 2 && k == 1 ? 0 : k;
+    });
   __syncthreads();
 #pragma unroll 1
   for (int i = t0; i < t1; i += 32) {
@@ -405,42 +409,53 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
   uint16_t* hi = grad ? a.g : a.h;
   uint16_t* lo = hi + (size_t)a.max_tiles * TM * a.R;
   const uint32_t part_s = base;
-  for (int i0 = 0; i0 < rows * R4; i0 += SHR_THREADS * 2) {
-    float4 u[2][8];
+  auto reduce = [&](auto s_) {  // for a cluster of that many CTAs: eight loads in flight
+    constexpr int SS = decltype(s_)::value, U = 8 / SS;
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < rows * R4; i0 += SHR_THREADS * U) {
+      float4 u[U][SS];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = i0 + e * SHR_THREADS + threadIdx.x, r = r0 + i / R4, c = (i % R4) * 4;
-      const bool in = i < rows * R4 && r < tl.y;
+      for (int e = 0; e < U; ++e) {
+        const int i = i0 + e * SHR_THREADS, r = r0 + i / R4, c = (i % R4) * 4;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        u[e][q] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (q < S && in) u[e][q] = ld_dsmem_f4(dsmem_addr(part_s + (uint32_t)(r * PP + c) * 4, q));
+        for (int q = 0; q < SS; ++q) {
+          u[e][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < rows * R4 && r < tl.y) u[e][q] = ld_dsmem_f4(dsmem_addr(part_s + (uint32_t)(r * PP + c) * 4, q));
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        const int i = i0 + e * SHR_THREADS, r = r0 + i / R4, c = (i % R4) * 4;
+        if (i >= rows * R4) break;
+        float4 v = u[e][0];
+#pragma unroll
+        for (int q = 1; q < SS; ++q) {
+          v.x += u[e][q].x;
+          v.y += u[e][q].y;
+          v.z += u[e][q].z;
+          v.w += u[e][q].w;
+        }
+        v.x *= sc;
+        v.y *= sc;
+        v.z *= sc;
+        v.w *= sc;
+        // hi + lo carries 16 significant bits of the FP32 sum into the next product
+        const uint2 hv = make_uint2(f2b2(v.x, v.y), f2b2(v.z, v.w));
+        const uint2 lv = make_uint2(f2b2(v.x - bf16lo(hv.x), v.y - bf16hi(hv.x)), f2b2(v.z - bf16lo(hv.y), v.w - bf16hi(hv.y)));
+        const size_t at = ((size_t)tile * TM + r) * a.R + c;
+        *reinterpret_cast<uint2*>(hi + at) = hv;
+        *reinterpret_cast<uint2*>(lo + at) = lv;
       }
     }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = i0 + e * SHR_THREADS + threadIdx.x, r = r0 + i / R4, c = (i % R4) * 4;
-      if (i >= rows * R4) break;
-      float4 v = u[e][0];
-#pragma unroll
-      for (int q = 1; q < 8; ++q) {
-        v.x += u[e][q].x;
-        v.y += u[e][q].y;
-        v.z += u[e][q].z;
-        v.w += u[e][q].w;
-      }
-      v.x *= sc;
-      v.y *= sc;
-      v.z *= sc;
-      v.w *= sc;
-      // hi + lo carries 16 significant bits of the FP32 sum into the next product
-      const uint2 hv = make_uint2(f2b2(v.x, v.y), f2b2(v.z, v.w));
-      const uint2 lv = make_uint2(f2b2(v.x - bf16lo(hv.x), v.y - bf16hi(hv.x)), f2b2(v.z - bf16lo(hv.y), v.w - bf16hi(hv.y)));
-      const size_t at = ((size_t)tile * TM + r) * a.R + c;
-      *reinterpret_cast<uint2*>(hi + at) = hv;
-      *reinterpret_cast<uint2*>(lo + at) = lv;
-    }
-  }
+  };
+  if (S == 8)
+    reduce(std::integral_constant<int, 8>());
+  else if (S == 4)
+    reduce(std::integral_constant<int, 4>());
+  else if (S == 2)
+    reduce(std::integral_constant<int, 2>());
+  else
+    reduce(std::integral_constant<int, 1>());
   if (S > 1) cluster_sync();  // the others' shared memory stays until it has been read
 }
 
