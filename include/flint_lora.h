@@ -63,7 +63,9 @@ size_t flint_lora_workspace_bytes(const flint_lora* lora, int32_t max_tokens);
  * apart; y_in, y_out bf16 [T] rows of N, ldy elements apart (ldx >= K, ldy >=
  * N, multiples of 8 below 2^31). adapter: int32 [T]. y_in NULL means zero. y_out may be
  * y_in (rows without an adapter are then left untouched); any other overlap of
- * y_out with x or y_in is refused (FLINT_MOE_EINVAL). */
+ * y_out with x or y_in is refused (FLINT_MOE_EINVAL). Rows count as overlapping
+ * where their extents, first element to last, do: also the columns of one
+ * buffer side by side. */
 flint_moe_status flint_lora_apply(const flint_lora* lora, const uint16_t* x, int64_t ldx, const int32_t* adapter,
                                   int32_t T, const uint16_t* y_in, uint16_t* y_out, int64_t ldy, void* workspace,
                                   size_t workspace_bytes, cudaStream_t stream);
@@ -94,7 +96,7 @@ size_t flint_lora_backward_workspace_bytes(const flint_lora* lora, int32_t max_t
  * with the sums over the tokens of adapter a (zero for an adapter without
  * tokens; all num_adapters gradients are written, also for T = 0). dx_in: the
  * projection's own part of the gradient, NULL means zero; dx_out may be dx_in,
- * or NULL (then only da and db are computed; lddx is not read). x rows are ldx
+ * or NULL (then only da and db are computed; dx_in and lddx are not read). x rows are ldx
  * apart. da, db: bf16, the shapes of a and b. Overlaps are refused
  * (FLINT_MOE_EINVAL): dx_out with x, dy or (otherwise) dx_in; da and db with
  * one another, the adapters, x, dy or dx. */

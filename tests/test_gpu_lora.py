@@ -167,6 +167,17 @@ def test_strided_rows_and_guards(T):
     assert torch.equal(want.view(torch.int16), db.view(torch.int16))
 
 
+@pytest.mark.parametrize("T", [20, 200])
+def test_without_dx_its_arguments_are_not_read(T):
+    p = Pool(T, 72, 136, 16, 3, 60 + T).to(DEV)
+    _, dA0, dB0 = backward(p, None, None)
+    lora = fb.flint_lora_init(p.d_A, p.d_B, p.d_scale)
+    dA, dB = (torch.full_like(v, float("nan")) for v in (p.d_A, p.d_B))
+    fb.flint_lora_backward(lora, p.d_x, p.d_dy, p.d_adapter, T, p.d_dx, None, dA, dB,
+                           ws_of(fb.flint_lora_backward_workspace_bytes(lora, T)), lddx=0)
+    assert torch.equal(dA, dA0) and torch.equal(dB, dB0)
+
+
 def test_zero_tokens():
     p = Pool(0, 64, 64, 8, 2, 1).to(DEV)
     lora = fb.flint_lora_init(p.d_A, p.d_B, p.d_scale)

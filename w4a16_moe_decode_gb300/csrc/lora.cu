@@ -1698,7 +1698,7 @@ extern "C" flint_moe_status flint_lora_backward(const flint_lora* l, const uint1
   Args p = tile_args(l, adapter, T, static_cast<uint8_t*>(ws), w);
   p.with_none = dx_out && dx_in != dx_out;
   p.g = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + w.g);
-  p.in = dx_in;
+  p.in = dx_out ? dx_in : nullptr;
   p.out = dx_out;
   p.ldo = (int)lddx;
   p.CT = chunk_tiles(l, T);
