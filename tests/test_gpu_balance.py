@@ -150,6 +150,24 @@ def test_padding_rows_may_hold_anything():
     assert torch.equal(dz, gradient(z, idx, start, 3, 0.5, a[1], a[2], None, dw)) and not dz[[0, 17, 63]].any()
 
 
+@pytest.mark.parametrize("T,E", [(40, 32), (1200, 130), (1200, 512)])
+def test_a_nan_logit_shows(T, E):
+    """A NaN in the row of a token that counts: the loss and that row's gradient are NaN, nothing else changes."""
+    k = 3
+    z, idx, start, dw = router(T, E, k, T + 1, [0, T // 2, T])
+    _, _, sc, st = forward(z, idx, start, k, 0.5)
+    want = [gradient(z, idx, start, k, 0.5, sc, st, None, g) for g in (None, dw)]
+    bad = [5, T // 2 + 2]
+    z[bad[0], E - 1] = float("nan")
+    z[bad[1], int(idx[bad[1], 0])] = float("nan")
+    loss, counts, sc2, st2 = forward(z, idx, start, k, 0.5)
+    assert torch.isnan(loss).all() and torch.equal(sc2, sc) and torch.equal(st2, st)
+    rest = [t for t in range(T) if t not in bad]
+    for g, w in zip((None, dw), want):
+        dz = gradient(z, idx, start, k, 0.5, sc, st, None, g)
+        assert torch.isnan(dz[bad]).all() and torch.equal(dz[rest], w[rest])
+
+
 def test_an_expert_picked_twice_counts_twice():
     z, idx, start, dw = router(20, 16, 4, 8)
     idx[3] = torch.tensor([2, 2, 2, 9])

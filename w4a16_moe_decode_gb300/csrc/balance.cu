@@ -84,12 +84,19 @@ __device__ __forceinline__ float rcp_of(float x) {
   return y;
 }
 
+// The smaller of both, NaN if one is: a NaN logit must not look like a very negative one.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // s = sigmoid(z) and q = 1 - s without cancellation: with e = exp(-z), s = 1 / (1 + e) and
 // q = e s. e is held at 1e37, where s is still an FP32 normal; rows in which no s is above
 // 1e-30 take the exact shares below instead.
 constexpr float LOW_ROW = 1e-30f;
 __device__ __forceinline__ void sigmoid2(float z, float& s, float& q) {
-  const float e = fminf(exp_of(-z), 1e37f);
+  const float e = min_nan(exp_of(-z), 1e37f);
   s = rcp_of(1.0f + e);
   q = e * s;
 }
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(256, loss_blocks<PER>()) k_bal_loss(const BalA
           }
         }
     }
-    if (mine && (lane & 19) == 16 && S > 0.f) few += (1.0f + __fdividef(F, S)) * cur.inv;
+    if (mine && (lane & 19) == 16 && S != 0.f) few += (1.0f + __fdividef(F, S)) * cur.inv;
     if ((n & 3) == 3) {
       acc += (double)few;
       few = 0.f;
@@ -573,7 +580,7 @@ __global__ void __launch_bounds__(1024) k_bal_one(const BalArgs g) {
           float s[PER];
           low_row<PER>(z[i], f, s, S, F);
         }
-        if (S > 0.f) acc += (double)((1.0f + __fdividef(F, S)) * inv);
+        if (S != 0.f) acc += (double)((1.0f + __fdividef(F, S)) * inv);
       }
       if (i0 + AT + i < t1) load_row<PER, VEC>(g.logits + (size_t)(i0 + AT + i) * g.E, g.E, lane, z[i]);
     }
@@ -636,7 +643,7 @@ __global__ void __launch_bounds__(256, backward_blocks<PER>()) k_bal_backward(co
         for (int j = 0; j < PER; j += 2) {
           float x, y;
           unpack2(mul2(pack2(z[j], z[j + 1]), k), x, y);
-          const f32x2 e = pack2(ex2_of(fminf(x, 122.f)), ex2_of(fminf(y, 122.f)));  // so that e s is no infinity times 0
+          const f32x2 e = pack2(ex2_of(min_nan(x, 122.f)), ex2_of(min_nan(y, 122.f)));  // so that e s is no infinity times 0
           unpack2(add2(e, one), x, y);
           const f32x2 s = pack2(rcp_of(x), rcp_of(y));
           S2 = add2(S2, s);
@@ -674,7 +681,7 @@ __global__ void __launch_bounds__(256, backward_blocks<PER>()) k_bal_backward(co
             sq[r][j / 2] = pack2(s[j] * q0, s[j + 1] * q1);
           }
         }
-        const float inv = S > 0.f ? rcp_of(S) : 0.f, ci = up * cur.inv * inv, off = -F * inv * ci;
+        const float inv = S != 0.f ? rcp_of(S) : 0.f, ci = up * cur.inv * inv, off = -F * inv * ci;
         float d[PER];
 #pragma unroll
         for (int j = 0; j < PER; j += 2)
@@ -717,7 +724,7 @@ __global__ void __launch_bounds__(256, backward_blocks<PER>()) k_bal_backward(co
           if (total < LOW_ROW * MAX_TOPK) sp = in && m > -INFINITY ? exp_of(zp - m) : 0.f;
           total = sum_of(sp);
         }
-        const float w = total > 0.f ? __fdividef(sp, total) : 0.f;
+        const float w = total != 0.f ? __fdividef(sp, total) : 0.f;
         add = w * (g - sum_of(g * w)) * qp;
       }
       add *= a.routed_scale;
