@@ -62,6 +62,24 @@ def test_lora_apply_refusals(lib):
         assert call(**kw) == fb.EALIGN, kw
 
 
+def test_row_strides_of_tensors(lib):
+    """The binding reads row strides off the tensors, and refuses those that one stride cannot describe."""
+    _, l = handle()  # K 256, N 512
+    x, y = torch.zeros(40, 256, dtype=torch.bfloat16), torch.zeros(40, 1024, dtype=torch.bfloat16)
+    def refused(f):
+        with pytest.raises(fb.FlintMoeError) as e:
+            f()
+        assert e.value.status == fb.EINVAL
+    go = lambda x, yi, yo: fb.flint_lora_apply(l, x, 0x500000, 40, yi, yo, 0x4000000, workspace_bytes=16, stream=0)  # noqa: E731
+    refused(lambda: go(x, y[:, :512].contiguous(), y[:, 512:]))
+    refused(lambda: go(x, y[:, :512], y[:, ::2]))
+    refused(lambda: go(torch.zeros(256, 40, dtype=torch.bfloat16).t(), y[:, :512], y[:, :512]))
+    assert fb._ld(x[:, :128], 40, 128, None) == 256 and fb._ld(x[:1, :128], 1, 128, None) == 128
+    assert fb._ld(y, 40, 1024, None, y.clone()) == 1024 and fb._ld(y, 40, 1024, 7, x) == 7
+    refused(lambda: fb.flint_lora_backward(l, x, 0x600000, 0x500000, 40, x, y[:, :256], 0x700000, 0x800000, 0x4000000,
+                                           workspace_bytes=16, stream=0))
+
+
 def test_gemv_lora_refusals(lib):
     _, l = handle(K=2048, N=2048)
     def call(N=2048, K=2048, fmt=fb.NVFP4, x=0x1000000, B=4, y=0x2000000, ad=0x500000, w=0x4000000, nb=1 << 30, p=0x6000000, st=None):

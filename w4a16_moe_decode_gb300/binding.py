@@ -366,14 +366,20 @@ def _nbytes(workspace, workspace_bytes) -> int:
     return workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
 
 
-def _ld(t, rows: int, cols: int, ld) -> int:
+def _ld(t, rows: int, cols: int, ld, like=None) -> int:
     """Elements between the rows of t: `ld` if given, else a 2-D tensor's own row stride (cols where
-    there is one row, no tensor or a bare pointer)."""
+    there is one row, no tensor or a bare pointer). Refused: elements of a row that do not lie side by
+    side, and a tensor `like`, read by the same stride, that has another."""
     if ld is not None:
         return ld
-    if rows < 2 or t is None or isinstance(t, int) or t.dim() != 2:
+    if t is None or isinstance(t, int) or t.dim() != 2:
         return cols
-    return t.stride(0)
+    if t.stride(1) != 1 and cols > 1:
+        raise FlintMoeError("row elements apart", EINVAL)
+    ld = cols if rows < 2 else t.stride(0)
+    if like is not None and not isinstance(like, int) and like is not t and _ld(like, rows, cols, None) != ld:
+        raise FlintMoeError("row strides differ", EINVAL)
+    return ld
 
 
 def flint_lora_init(a, b, scale, in_dim=None, out_dim=None, rank=None, num_adapters=None) -> flint_lora:
@@ -395,10 +401,10 @@ def flint_lora_workspace_bytes(lora: flint_lora, max_tokens: int) -> int:
 def flint_lora_apply(lora: flint_lora, x, adapter, T: int, y_in, y_out, workspace, ldx=None, ldy=None,
                      workspace_bytes=None, stream=None) -> None:
     """y_out[t] = bf16(y_in[t] + scale_a B_a (A_a x[t])), a = adapter[t] (include/flint_lora.h). Row strides
-    are those of x and y_out (y_in has y_out's)."""
+    are those of x and y_out (y_in has to have y_out's)."""
     _check("flint_lora_apply",
            lib().flint_lora_apply(ctypes.byref(lora), _ptr(x), _ld(x, T, lora.in_dim, ldx), _ptr(adapter), T,
-                                  _ptr(y_in), _ptr(y_out), _ld(y_out, T, lora.out_dim, ldy), _ptr(workspace),
+                                  _ptr(y_in), _ptr(y_out), _ld(y_out, T, lora.out_dim, ldy, y_in), _ptr(workspace),
                                   _nbytes(workspace, workspace_bytes), _stream(stream)))
 
 
@@ -425,7 +431,7 @@ def flint_lora_backward(lora: flint_lora, x, dy, adapter, T: int, dx_in, dx_out,
     _check("flint_lora_backward",
            lib().flint_lora_backward(ctypes.byref(lora), _ptr(x), _ld(x, T, lora.in_dim, ldx), _ptr(dy),
                                      _ld(dy, T, lora.out_dim, lddy), _ptr(adapter), T, _ptr(dx_in), _ptr(dx_out),
-                                     _ld(dx_out, T, lora.in_dim, lddx), _ptr(da), _ptr(db), _ptr(workspace),
+                                     _ld(dx_out, T, lora.in_dim, lddx, dx_in), _ptr(da), _ptr(db), _ptr(workspace),
                                      _nbytes(workspace, workspace_bytes), _stream(stream)))
 
 
