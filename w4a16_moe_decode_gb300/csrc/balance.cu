@@ -9,8 +9,10 @@
 // so a row needs two sums, sum_e s and sum_e (f - 1) s, and no second look at
 // memory: the counts come first, from the picks alone.
 //
-// One warp per token row, 16-byte loads. Both kernels move T E floats and are
-// bound by memory bandwidth.
+// One warp per token row, 16-byte copies. The rows are bound by memory bandwidth
+// and nearly as much by instructions; the counts in front of them by latency.
+// 65536 tokens of 256 experts, alone and cold: zeros 2.2 us, counts 8.4, loss 23.8
+// (69 MB), gradient 29.9 (67 MB in, 67 MB out: 4.5 TB/s).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
