@@ -1950,40 +1950,12 @@ __host__ __device__ inline GemvSplitPlan gemv_split_plan(int B, int fmt, int nw,
   return p;
 }
 
-// SOLO (one token): at most 64 registers, four CTAs per SM, so that the grid
-// (N / 16 row tiles x K / 2048 slices: 512 CTAs for 2048 x 8192) runs in one
-// wave instead of two at three per SM (2048 x 8192: 7.4 -> 6.3 us per call).
-template <int FMT, int NTMAX, bool SOLO, bool ADD>
-__global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16;
+// Stages this CTA's slice of every token row: warp w takes tokens w, w + nw, ...
+template <int FMT, int NTMAX>
+__device__ __forceinline__ void stage_slice(const GemvArgs& a, uint8_t* xs, float* s_ss, float* s_inv, size_t col0, uint32_t S,
+                                            int warp, int nw, int lane) {
   constexpr int NCH = GEMV_SLICE / 256;  // 16-byte chunks per lane of a slice row
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const int nw = blockDim.x >> 5;
-  const uint32_t rank = cluster_rank(), S = gridDim.y;
-  const int KGW = (GEMV_SLICE / KG_COLS) / nw;  // k-groups per warp
-  const GemvSplitPlan P = gemv_split_plan(a.B, FMT, nw, NTMAX);
-  uint8_t* wb = smem + P.wbuf_off + (size_t)warp * KGW * KGB;
-  uint8_t* xs = smem + P.xs_off;
-  float* red = reinterpret_cast<float*>(smem + P.red_off);
-  float* part = reinterpret_cast<float*>(smem + P.part_off);  // [B][16] this CTA's partial y
-  float* s_ss = reinterpret_cast<float*>(smem + P.ss_off);    // [B] this slice's sums of squares
-  float* s_inv = reinterpret_cast<float*>(smem + P.inv_off);  // [B] inverse prescale
-  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + P.bar_off) + warp;
-  const int xstride = GEMV_SLICE * 2 + 16;
-  const size_t col0 = (size_t)rank * GEMV_SLICE;
-  if (lane == 0) {
-    mbar_init(bar, 1);
-    fence_mbar_init();
-    const uint32_t bytes = (uint32_t)KGW * KGB;
-    const int64_t off = (int64_t)blockIdx.x * a.L.dn_tile + (int64_t)rank * (GEMV_SLICE / KG_COLS) * KGB +
-                        (int64_t)warp * bytes;
-    mbar_arrive_expect_tx(bar, bytes);
-    bulk_g2s_stream(wb, a.packed + off, bytes, bar);
-  }
-  if (!ADD) pdl_wait();  // x may be the previous kernel's output
-  pdl_trigger();
-  // Stage this CTA's slice of every token row: warp w takes tokens w, w + nw, ...
+  constexpr int xstride = GEMV_SLICE * 2 + 16;
   const int ntw = (a.B - warp + nw - 1) / nw;  // tokens of this warp: at most NTMAX with 8 warps
   uint4 v[NTMAX][NCH];
   float sq[NTMAX];
@@ -2051,6 +2023,41 @@ __global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
       if (lane == 0) s_inv[t] = exp2i(-kx);
     }
   }
+}
+
+// SOLO (one token): at most 64 registers, four CTAs per SM, so that the grid
+// (N / 16 row tiles x K / 2048 slices: 512 CTAs for 2048 x 8192) runs in one
+// wave instead of two at three per SM (2048 x 8192: 7.4 -> 6.3 us per call).
+template <int FMT, int NTMAX, bool SOLO, bool ADD>
+__global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int nw = blockDim.x >> 5;
+  const uint32_t rank = cluster_rank(), S = gridDim.y;
+  const int KGW = (GEMV_SLICE / KG_COLS) / nw;  // k-groups per warp
+  const GemvSplitPlan P = gemv_split_plan(a.B, FMT, nw, NTMAX);
+  uint8_t* wb = smem + P.wbuf_off + (size_t)warp * KGW * KGB;
+  uint8_t* xs = smem + P.xs_off;
+  float* red = reinterpret_cast<float*>(smem + P.red_off);
+  float* part = reinterpret_cast<float*>(smem + P.part_off);  // [B][16] this CTA's partial y
+  float* s_ss = reinterpret_cast<float*>(smem + P.ss_off);    // [B] this slice's sums of squares
+  float* s_inv = reinterpret_cast<float*>(smem + P.inv_off);  // [B] inverse prescale
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + P.bar_off) + warp;
+  const int xstride = GEMV_SLICE * 2 + 16;
+  const size_t col0 = (size_t)rank * GEMV_SLICE;
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    fence_mbar_init();
+    const uint32_t bytes = (uint32_t)KGW * KGB;
+    const int64_t off = (int64_t)blockIdx.x * a.L.dn_tile + (int64_t)rank * (GEMV_SLICE / KG_COLS) * KGB +
+                        (int64_t)warp * bytes;
+    mbar_arrive_expect_tx(bar, bytes);
+    bulk_g2s_stream(wb, a.packed + off, bytes, bar);
+  }
+  if (!ADD) pdl_wait();  // x may be the previous kernel's output
+  pdl_trigger();
+  stage_slice<FMT, NTMAX>(a, xs, s_ss, s_inv, col0, S, warp, nw, lane);
   __syncthreads();
   const int nt_used = (a.B + 7) >> 3;
   float acc[2][NTMAX][4];
@@ -2109,6 +2116,132 @@ __global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
       const int rr = p & 15, t = p >> 4;
       gemv_store<ADD>(a, t, blockIdx.x * 16 + rr, v2 * G);
     }
+  }
+  cluster_sync();  // the other CTAs' shared memory stays until CTA 0 has read it
+}
+
+// ===========================================================================
+// The split GEMV for 9 to 32 rows and more tiles than clusters run at once: as in
+// k_gemv_rows a cluster stages its rows once and works through the tiles
+// blockIdx.x, + gridDim.x, ... The partial sums alternate between two places, so
+// that one cluster barrier a tile is enough: CTA 0 arrives at a tile's barrier
+// after it has read the tile's before, and no CTA writes there earlier. Each tile
+// is summed up in the same order as by k_gemv_split.
+// ===========================================================================
+struct GemvSplitRowsPlan {
+  size_t xs_off, red_off, part_off, ss_off, inv_off, bar_off, total;
+};
+__host__ __device__ inline GemvSplitRowsPlan gemv_split_rows_plan(int B, int fmt, int nw, int ntmax) {
+  const int kgb = fmt == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16;
+  GemvSplitRowsPlan p;
+  size_t o = (size_t)GEMV_BUFS(fmt) * (GEMV_SLICE / KG_COLS) * kgb;
+  p.xs_off = o;    o += (size_t)B * (GEMV_SLICE * 2 + 16);
+  p.red_off = o;   o += sizeof(float) * nw * ntmax * 128;
+  p.part_off = o;  o += sizeof(float) * 2 * B * 16;
+  p.ss_off = o;    o += sizeof(float) * MAX_BATCH;
+  p.inv_off = o;   o += sizeof(float) * MAX_BATCH;
+  o = (o + 15) & ~(size_t)15;
+  p.bar_off = o;   o += sizeof(uint64_t) * nw * 2;
+  p.total = o;
+  return p;
+}
+
+template <int FMT, int NTMAX, bool ADD>
+__global__ void __launch_bounds__(256, NTMAX == 2 ? 2 : 1) k_gemv_split_rows(GemvArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16, NB = GEMV_BUFS(FMT);
+  constexpr int nw = 8, KGW = (GEMV_SLICE / KG_COLS) / nw;  // k-groups per warp
+  constexpr uint32_t bytes = (uint32_t)KGW * KGB;
+  constexpr int xstride = GEMV_SLICE * 2 + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const uint32_t rank = cluster_rank(), S = gridDim.y;
+  const GemvSplitRowsPlan P = gemv_split_rows_plan(a.B, FMT, nw, NTMAX);
+  uint8_t* const wb0 = smem + (size_t)warp * NB * bytes;  // this warp's NB buffers
+  uint8_t* xs = smem + P.xs_off;
+  float* red = reinterpret_cast<float*>(smem + P.red_off);
+  float* part0 = reinterpret_cast<float*>(smem + P.part_off);  // 2 x [B][16] partial y
+  float* s_ss = reinterpret_cast<float*>(smem + P.ss_off);
+  float* s_inv = reinterpret_cast<float*>(smem + P.inv_off);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + P.bar_off) + warp * 2;
+  const int tiles = a.N / 16;
+  auto fetch = [&](int tile, int b) {  // by one lane
+    const int64_t off = (int64_t)tile * a.L.dn_tile + (int64_t)rank * (GEMV_SLICE / KG_COLS) * KGB + (int64_t)warp * bytes;
+    mbar_arrive_expect_tx(&bar[b], bytes);
+    bulk_g2s_stream(wb0 + (size_t)b * bytes, a.packed + off, bytes, &bar[b]);
+  };
+  if (lane == 0) {
+    for (int b = 0; b < NB; ++b) mbar_init(&bar[b], 1);
+    fence_mbar_init();
+    for (int b = 0; b < NB; ++b)
+      if ((int)(blockIdx.x + b * gridDim.x) < tiles) fetch(blockIdx.x + b * gridDim.x, b);
+  }
+  if (!ADD) pdl_wait();  // x may be the previous kernel's output
+  pdl_trigger();
+  stage_slice<FMT, NTMAX>(a, xs, s_ss, s_inv, (size_t)rank * GEMV_SLICE, S, warp, nw, lane);
+  __syncthreads();
+  const int nt_used = (a.B + 7) >> 3;
+  int tok[NTMAX];
+#pragma unroll
+  for (int nt = 0; nt < NTMAX; ++nt) tok[nt] = min(nt * 8 + g, a.B - 1);
+  const float G = FMT == FLINT_MOE_NVFP4 ? a.G[0] : 1.0f;
+  int i = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++i) {
+    const int b = i % NB;
+    float acc[2][NTMAX][4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int nt = 0; nt < NTMAX; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[c][nt][e] = 0.f;
+    // after a failed wait the copy is let land and the products run on it: the status word tells, and the cluster's
+    // barriers stay matched
+    if (!mbar_wait(&bar[b], (i / NB) & 1, a.status)) mbar_drain(&bar[b], (i / NB) & 1);
+    const uint8_t* wb = wb0 + (size_t)b * bytes;
+#pragma unroll
+    for (int kl = 0; kl < KGW; ++kl) {
+      const int kg = warp * KGW + kl;
+      uint4 bx[NTMAX][2];
+#pragma unroll
+      for (int nt = 0; nt < NTMAX; ++nt) {
+        if (nt < nt_used) {
+          const uint8_t* rp = xs + (size_t)tok[nt] * xstride + kg * 128 + t4 * 32;
+          bx[nt][0] = lds128(rp);
+          bx[nt][1] = lds128(rp + 16);
+        }
+      }
+      if (kl & 1)
+        tile_kgroup<FMT, NTMAX>(wb + kl * KGB, bx, nt_used, lane, acc[1]);
+      else
+        tile_kgroup<FMT, NTMAX>(wb + kl * KGB, bx, nt_used, lane, acc[0]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NTMAX; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[((warp * NTMAX + nt) * 32 + lane) * 4 + e] = acc[0][nt][e] + acc[1][nt][e];
+    __syncthreads();
+    const int next = tile + NB * (int)gridDim.x;
+    if (lane == 0 && next < tiles) {
+      fence_proxy_async();  // this warp's reads of the buffer come before the copy into it
+      fetch(next, b);
+    }
+    // This CTA's partial sums (prescale undone), output (row r, token t) at [t][r].
+    float* part = part0 + (i & 1) * 16 * a.B;
+    for (int p = threadIdx.x; p < 16 * a.B; p += blockDim.x) {
+      const int r = p & 15, t = p >> 4, nt = t >> 3, c = t & 7;
+      const int ln = 4 * (r & 7) + (c >> 1), e = 2 * (r >> 3) + (c & 1);
+      float v = 0.f;
+      for (int w2 = 0; w2 < nw; ++w2) v += red[((w2 * NTMAX + nt) * 32 + ln) * 4 + e];
+      part[p] = v * s_inv[t];
+    }
+    if (ADD && i == 0) pdl_wait();
+    cluster_sync();  // every CTA's partial sums of this tile are published, and red[] has been read
+    if (rank == 0)
+      for (int p = threadIdx.x; p < 16 * a.B; p += blockDim.x) {
+        float v = 0.f;
+        for (uint32_t r = 0; r < S; ++r) v += ld_dsmem_f32(part + p, r);  // rank order
+        gemv_store<ADD>(a, p >> 4, tile * 16 + (p & 15), v * G);
+      }
   }
   cluster_sync();  // the other CTAs' shared memory stays until CTA 0 has read it
 }
@@ -2684,6 +2817,22 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
 #define FLINT_SPLIT(FMT, NT, SOLO) \
   (add ? launch_gemv<k_gemv_split<FMT, NT, SOLO, true>>(grid, block, smem, S, stream, a) \
        : launch_gemv<k_gemv_split<FMT, NT, SOLO, false>>(grid, block, smem, S, stream, a))
+#define FLINT_SPLIT_ROWS(FMT, NT)                                                                     \
+  (add ? launch_gemv<k_gemv_split_rows<FMT, NT, true>>(rgrid, block, rplan.total, S, stream, a)       \
+       : launch_gemv<k_gemv_split_rows<FMT, NT, false>>(rgrid, block, rplan.total, S, stream, a))
+    const GemvSplitRowsPlan rplan = gemv_split_rows_plan(B, fmt, 8, ntmax);
+    const int tiles = N / 16, per_sm = ntmax == 2 && 2 * (rplan.total + 1024) <= SMEM_LIMIT + 1024 ? 2 : 1;
+    const int most = std::max(1, sm_count() * per_sm / S), rounds = (tiles + most - 1) / most;  // clusters at once
+    if (ntmax > 1 && rounds > 1 && rplan.total <= SMEM_LIMIT) {
+      const dim3 rgrid((tiles + rounds - 1) / rounds, S);
+      switch (ntmax) {
+        case 2: e = nv ? FLINT_SPLIT_ROWS(FLINT_MOE_NVFP4, 2) : FLINT_SPLIT_ROWS(FLINT_MOE_BF16, 2); break;
+        case 3: e = nv ? FLINT_SPLIT_ROWS(FLINT_MOE_NVFP4, 3) : FLINT_SPLIT_ROWS(FLINT_MOE_BF16, 3); break;
+        default: e = nv ? FLINT_SPLIT_ROWS(FLINT_MOE_NVFP4, 4) : FLINT_SPLIT_ROWS(FLINT_MOE_BF16, 4); break;
+      }
+      return e == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
+    }
+#undef FLINT_SPLIT_ROWS
     switch (B == 1 ? 0 : ntmax) {
       case 0: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 1, true) : FLINT_SPLIT(FLINT_MOE_BF16, 1, true); break;
       case 1: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 1, false) : FLINT_SPLIT(FLINT_MOE_BF16, 1, false); break;
