@@ -1,4 +1,4 @@
-"""The dense GEMV for 9 to 32 rows and many tiles, whose blocks stage their rows once for several tiles: every row's
+"""The dense GEMV for many tiles, whose blocks stage their rows once for several tiles: every row's
 sums have the order that calls of up to eight rows use, so the results are the same bits; and with adapters beside it
 (their bound as in test_gpu_lora.py)."""
 import pytest
@@ -51,3 +51,20 @@ def test_adapters_beside_split_rows(B, K, N, R, n, fmt):
     y = gemv_lora(p, packed, fmt)
     check(y, ref, tol, "gemv_lora")
     assert torch.equal(gemv_lora(p, packed, fmt), y)
+
+
+@pytest.mark.parametrize("B,K,N,R,n,fmt", [(1, 2048, 4992, 8, 1, fb.NVFP4), (8, 512, 5008, 24, 2, fb.NVFP4), (3, 768, 4928, 16, 3, fb.BF16),
+                                           (1, 4096, 2464, 16, 2, fb.NVFP4), (5, 8192, 1360, 40, 5, fb.NVFP4),
+                                           (8, 6144, 1040, 8, 1, fb.BF16)])
+def test_few_rows_of_many_tiles(B, K, N, R, n, fmt):
+    """Parity, and the bits of each row alone."""
+    test_adapters_beside_split_rows(B, K, N, R, n, fmt)
+    packed, _ = layers.synth_dense(N, K, 7, 0, fmt, DEV)
+    x = layers.synth_x(B, K, 7, 0, DEV)
+    for g in (None, layers.synth_norm(K, 7, 0, DEV)):
+        y = torch.full((B, N), 0x7FC0, dtype=torch.int16, device=DEV)
+        fb.flint_gemv(packed, N, K, fmt, x, B, y, g, 1e-6)
+        for t in range(B):
+            one = torch.full((1, N), 0x7FC0, dtype=torch.int16, device=DEV)
+            fb.flint_gemv(packed, N, K, fmt, x[t:t + 1], 1, one, g, 1e-6)
+            assert torch.equal(one[0], y[t]), t

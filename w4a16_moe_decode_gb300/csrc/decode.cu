@@ -1800,12 +1800,15 @@ __global__ void __launch_bounds__(256) k_gemv(GemvArgs a) {
 }
 
 // ===========================================================================
-// The same GEMV for 9 to 32 rows of up to 2048 columns and more tiles than SMs. The
-// rows fill most of an SM's shared memory (131 KB for 32 of 2048), and converting
-// them into fragment order takes longer than a tile's products: so a block stages
-// them once and works through the tiles blockIdx.x, + gridDim.x, ..., the next
-// tile's weights on their way meanwhile (8192 x 2048: 32 rows 25.8 -> 12.6 us, 16
-// rows 11.4 -> 7.8). Each tile is summed up in the same order as by k_gemv.
+// The same GEMV for more tiles than blocks that run at once (two an SM, or one
+// where the rows fill it: 131 KB for 32 of 2048). Staging a block's rows in
+// fragment order takes as long as a tile's products with one row and longer with
+// more: so a block stages them once and works through the tiles blockIdx.x,
+// + gridDim.x, ..., the next tile's weights on their way meanwhile. A chain of
+// calls, us each, 8192 x 2048: 1 row 5.5 -> 4.5, 8 rows 7.5 -> 5.2, 16 rows
+// 11.4 -> 7.8, 32 rows 25.8 -> 12.6; with tiles for one round only there is
+// nothing to gain (4096 x 1024, 1 row: 2.5 -> 2.7; three blocks an SM: 8192 x 2048,
+// 8 rows 7.6). Each tile is summed up in the same order as by k_gemv.
 // ===========================================================================
 // Tiles of weights in flight: two, or one of BF16 weights (65 KB a tile of 2048 columns).
 __host__ __device__ constexpr int GEMV_BUFS(int fmt) { return fmt == FLINT_MOE_NVFP4 ? 2 : 1; }
@@ -2025,11 +2028,8 @@ __device__ __forceinline__ void stage_slice(const GemvArgs& a, uint8_t* xs, floa
   }
 }
 
-// SOLO (one token): at most 64 registers, four CTAs per SM, so that the grid
-// (N / 16 row tiles x K / 2048 slices: 512 CTAs for 2048 x 8192) runs in one
-// wave instead of two at three per SM (2048 x 8192: 7.4 -> 6.3 us per call).
-template <int FMT, int NTMAX, bool SOLO, bool ADD>
-__global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
+template <int FMT, int NTMAX, bool ADD>
+__global__ void __launch_bounds__(256) k_gemv_split(GemvArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -2121,12 +2121,13 @@ __global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
 }
 
 // ===========================================================================
-// The split GEMV for 9 to 32 rows and more tiles than clusters run at once: as in
-// k_gemv_rows a cluster stages its rows once and works through the tiles
-// blockIdx.x, + gridDim.x, ... The partial sums alternate between two places, so
-// that one cluster barrier a tile is enough: CTA 0 arrives at a tile's barrier
-// after it has read the tile's before, and no CTA writes there earlier. Each tile
-// is summed up in the same order as by k_gemv_split.
+// The split GEMV for more tiles than clusters run at once: as in k_gemv_rows a
+// cluster stages its rows once and works through the tiles blockIdx.x,
+// + gridDim.x, ... The partial sums alternate between two places, so that one
+// cluster barrier a tile is enough: CTA 0 arrives at a tile's barrier after it has
+// read the tile's before, and no CTA writes there earlier. Each tile is summed up
+// in the same order as by k_gemv_split. A chain of calls, us each, 2048 x 8192:
+// 1 row 6.3 -> 5.2, 8 rows 9.3 -> 6.3, 16 rows 14.4 -> 9.4, 32 rows 32 -> 15.7.
 // ===========================================================================
 struct GemvSplitRowsPlan {
   size_t xs_off, red_off, part_off, ss_off, inv_off, bar_off, total;
@@ -2147,7 +2148,7 @@ __host__ __device__ inline GemvSplitRowsPlan gemv_split_rows_plan(int B, int fmt
 }
 
 template <int FMT, int NTMAX, bool ADD>
-__global__ void __launch_bounds__(256, NTMAX == 2 ? 2 : 1) k_gemv_split_rows(GemvArgs a) {
+__global__ void __launch_bounds__(256, NTMAX <= 2 ? 2 : 1) k_gemv_split_rows(GemvArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16, NB = GEMV_BUFS(FMT);
   constexpr int nw = 8, KGW = (GEMV_SLICE / KG_COLS) / nw;  // k-groups per warp
@@ -2814,18 +2815,19 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
     const dim3 grid(N / 16, S), block(256);
     cudaError_t e;
     const bool nv = fmt == FLINT_MOE_NVFP4, add = add32 != nullptr;
-#define FLINT_SPLIT(FMT, NT, SOLO) \
-  (add ? launch_gemv<k_gemv_split<FMT, NT, SOLO, true>>(grid, block, smem, S, stream, a) \
-       : launch_gemv<k_gemv_split<FMT, NT, SOLO, false>>(grid, block, smem, S, stream, a))
+#define FLINT_SPLIT(FMT, NT)                                                           \
+  (add ? launch_gemv<k_gemv_split<FMT, NT, true>>(grid, block, smem, S, stream, a)     \
+       : launch_gemv<k_gemv_split<FMT, NT, false>>(grid, block, smem, S, stream, a))
 #define FLINT_SPLIT_ROWS(FMT, NT)                                                                     \
   (add ? launch_gemv<k_gemv_split_rows<FMT, NT, true>>(rgrid, block, rplan.total, S, stream, a)       \
        : launch_gemv<k_gemv_split_rows<FMT, NT, false>>(rgrid, block, rplan.total, S, stream, a))
     const GemvSplitRowsPlan rplan = gemv_split_rows_plan(B, fmt, 8, ntmax);
-    const int tiles = N / 16, per_sm = ntmax == 2 && 2 * (rplan.total + 1024) <= SMEM_LIMIT + 1024 ? 2 : 1;
+    const int tiles = N / 16, per_sm = ntmax <= 2 && 2 * (rplan.total + 1024) <= SMEM_LIMIT + 1024 ? 2 : 1;
     const int most = std::max(1, sm_count() * per_sm / S), rounds = (tiles + most - 1) / most;  // clusters at once
-    if (ntmax > 1 && rounds > 1 && rplan.total <= SMEM_LIMIT) {
+    if (rounds > 1 && rplan.total <= SMEM_LIMIT) {
       const dim3 rgrid((tiles + rounds - 1) / rounds, S);
       switch (ntmax) {
+        case 1: e = nv ? FLINT_SPLIT_ROWS(FLINT_MOE_NVFP4, 1) : FLINT_SPLIT_ROWS(FLINT_MOE_BF16, 1); break;
         case 2: e = nv ? FLINT_SPLIT_ROWS(FLINT_MOE_NVFP4, 2) : FLINT_SPLIT_ROWS(FLINT_MOE_BF16, 2); break;
         case 3: e = nv ? FLINT_SPLIT_ROWS(FLINT_MOE_NVFP4, 3) : FLINT_SPLIT_ROWS(FLINT_MOE_BF16, 3); break;
         default: e = nv ? FLINT_SPLIT_ROWS(FLINT_MOE_NVFP4, 4) : FLINT_SPLIT_ROWS(FLINT_MOE_BF16, 4); break;
@@ -2833,12 +2835,11 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
       return e == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
     }
 #undef FLINT_SPLIT_ROWS
-    switch (B == 1 ? 0 : ntmax) {
-      case 0: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 1, true) : FLINT_SPLIT(FLINT_MOE_BF16, 1, true); break;
-      case 1: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 1, false) : FLINT_SPLIT(FLINT_MOE_BF16, 1, false); break;
-      case 2: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 2, false) : FLINT_SPLIT(FLINT_MOE_BF16, 2, false); break;
-      case 3: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 3, false) : FLINT_SPLIT(FLINT_MOE_BF16, 3, false); break;
-      default: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 4, false) : FLINT_SPLIT(FLINT_MOE_BF16, 4, false); break;
+    switch (ntmax) {
+      case 1: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 1) : FLINT_SPLIT(FLINT_MOE_BF16, 1); break;
+      case 2: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 2) : FLINT_SPLIT(FLINT_MOE_BF16, 2); break;
+      case 3: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 3) : FLINT_SPLIT(FLINT_MOE_BF16, 3); break;
+      default: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 4) : FLINT_SPLIT(FLINT_MOE_BF16, 4); break;
     }
 #undef FLINT_SPLIT
     return e == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
@@ -2855,12 +2856,13 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
       : (add ? launch_gemv<KERNEL<FLINT_MOE_BF16, NT, true>>(grid, block, smem, 0, stream, a)           \
              : launch_gemv<KERNEL<FLINT_MOE_BF16, NT, false>>(grid, block, smem, 0, stream, a)))
   const size_t rows_smem = gemv_rows_smem(K, B, fmt, nw, ntmax, &o1, &o2, &o3, &o4);
-  if (ntmax > 1 && N / 16 > sm_count() && rows_smem <= SMEM_LIMIT) {
+  const int at_once = sm_count() * std::max<int>(1, std::min<int>(2, (int)(SMEM_LIMIT / (rows_smem + 1024))));
+  if (N / 16 > at_once && rows_smem <= SMEM_LIMIT) {
     // more tiles than blocks that run at once: blocks that stage the rows once for several tiles
     const size_t smem = rows_smem;
-    const int per_sm = std::max<int>(1, std::min<int>(2, (int)(SMEM_LIMIT / (smem + 1024))));
-    const dim3 grid(std::min(N / 16, sm_count() * per_sm));
+    const dim3 grid(at_once);
     switch (ntmax) {
+      case 1: e = FLINT_GEMV(k_gemv_rows, 1); break;
       case 2: e = FLINT_GEMV(k_gemv_rows, 2); break;
       case 3: e = FLINT_GEMV(k_gemv_rows, 3); break;
       default: e = FLINT_GEMV(k_gemv_rows, 4); break;
