@@ -16,7 +16,9 @@
  * above 2048), 0 <= B <= 32 (B = 0 is a no-op), else FLINT_MOE_EUNSUPPORTED
  * (shape) or FLINT_MOE_EINVAL (B). For K > 2048 the K / 2048 column slices of
  * a 16-row tile go to the CTAs of one thread-block cluster, whose partial sums
- * are added in distributed shared memory in a fixed order.
+ * are added in distributed shared memory in a fixed order. A row's result does
+ * not depend on the other rows of the call. With low-rank adapters beside the
+ * matrix: flint_lora.h.
  */
 #ifndef FLINT_GEMV_H
 #define FLINT_GEMV_H
