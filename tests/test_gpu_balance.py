@@ -168,6 +168,16 @@ def test_a_nan_logit_shows(T, E):
         assert torch.isnan(dz[bad]).all() and torch.equal(dz[rest], w[rest])
 
 
+@pytest.mark.parametrize("T,k", [(50, 1), (400, 4), (300, 12)])
+def test_a_single_pick_has_no_weight_gradient(T, k):
+    """The weight of a token's only pick that counts is one: its gradient adds exactly nothing."""
+    E = 64
+    z, idx, start, dw = router(T, E, k, 30 + T, [0, T // 3, T])
+    idx[:, : k - 1] = E + 3
+    _, _, sc, st = forward(z, idx, start, k, 0.5)
+    assert torch.equal(gradient(z, idx, start, k, 0.5, sc, st, None, 1e3 * dw), gradient(z, idx, start, k, 0.5, sc, st))
+
+
 def test_an_expert_picked_twice_counts_twice():
     z, idx, start, dw = router(20, 16, 4, 8)
     idx[3] = torch.tensor([2, 2, 2, 9])

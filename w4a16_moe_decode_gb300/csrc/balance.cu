@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(256) k_bal_count(const BalArgs a) {
   const int t0 = min(a.T, (int)blockIdx.x * per), t1 = min(a.T, t0 + per);
   for (int e = threadIdx.x; e < a.E; e += 256) hist[e] = total[e] = 0;
   if (threadIdx.x == 0) tokens = 0;
+  pdl_trigger();  // the rows' kernel needs what is written here at its end only
   pdl_wait();
-  pdl_trigger();
   if (t0 >= t1) return;
   int b = seq_of(a, t0, lane);
   for (int t = t0; t < t1 && b < a.n_seq;) {  // piece [t, end) of sequence b
@@ -414,8 +414,11 @@ struct RowRing {
   static size_t bytes() { return sizeof(float) * 8 * DEPTH * ROW; }
 };
 
-// Sum over the block's tokens of (1 + F_t) / T_b in FP64; the last block to finish adds the
-// blocks' sums, in a fixed order.
+// The loss is sum_b 1/T_b (tokens + sum_e (f_be - 1) P_be) with P_be = sum_t p_te, so the rows need no counts: a warp
+// adds up its tokens' shares in registers, expert by expert, beside the kernels that count, and multiplies them by f - 1
+// at the end of its piece of a sequence (with the counts first and f in every row: 28.6 us for 65536 x 256). Shares are
+// summed in FP32 16 tokens at a time and those sums in FP32 again, everything behind that in FP64; the last block to
+// finish adds the blocks' sums, in a fixed order.
 template <int PER, bool VEC>
 __global__ void __launch_bounds__(256, loss_blocks<PER>()) k_bal_loss(const BalArgs a) {
   extern __shared__ __align__(16) float ring_smem[];
@@ -426,57 +429,86 @@ __global__ void __launch_bounds__(256, loss_blocks<PER>()) k_bal_loss(const BalA
   warp_run(a, warp, t0, t1);
   RowRing<PER, VEC> rows(ring_smem, a.logits, a.E, t0, t1, warp, lane);
   Cursor<PER, VEC> cur;
-  if (t0 < t1) cur.find(a, t0, lane);
-  pdl_wait();  // the counts
-  if (t0 < t1) cur.load(a, lane);
-  // Four rows at a time: eight sums over the lanes at once, after which the lanes with bit 4 set and bits 0, 1 clear
-  // hold one row's F each, and the lane 16 below its S.
-  const int row = (lane >> 2) & 3;
-  double acc = 0.0;
-  float few = 0.f;  // up to 16 tokens' shares
-  int n = 0;
-  for (int t = t0; t < t1; ++n) {
-    cur.to(a, t, lane);
-    const int nb = min(4, min(t1, cur.end) - t);  // tokens of one sequence
-    const bool mine = row < nb && __ldg(a.idx + (size_t)(t + min(row, nb - 1)) * a.k) >= 0 && cur.inside(a);
-    float v[8];
+  float P[PER], Q[PER];  // shares of up to 16 tokens, and of those before
+  int counted = 0, n = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = v[4 + i] = 0.f;
-      if (i < nb) {
-        float z[PER];
-        rows.take(t + i, z);
-        row_sums<PER>(z, cur.f, v[i], v[4 + i]);
+  for (int j = 0; j < PER; ++j) P[j] = Q[j] = 0.f;
+  double acc = 0.0;
+  for (int t = t0; t < t1;) {
+    if (t >= cur.end) cur.find(a, t, lane);
+    const int nb = min(2, min(t1, cur.end) - t);  // tokens of one sequence
+    // bit r: token t + r counts
+    const unsigned live = cur.inside(a) ? __ballot_sync(0xffffffffu, lane < nb && __ldg(a.idx + (size_t)(t + lane) * a.k) >= 0) : 0u;
+    f32x2 sv[2][PER / 2];
+    float v[2] = {0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (r >= nb) break;
+      float z[PER];
+      rows.take(t + r, z);
+      f32x2 S2 = 0ull;
+      const f32x2 one = pack2(1.f, 1.f), k = pack2(-LOG2E, -LOG2E);
+#pragma unroll
+      for (int j = 0; j < PER; j += 2) {  // exp(-z) may overflow to infinity here: that s is 0
+        float x, y;
+        unpack2(mul2(pack2(z[j], z[j + 1]), k), x, y);
+        unpack2(add2(pack2(ex2_of(x), ex2_of(y)), one), x, y);
+        sv[r][j / 2] = pack2(rcp_of(x), rcp_of(y));
+        S2 = add2(S2, sv[r][j / 2]);
       }
+      float x, y;
+      unpack2(S2, x, y);
+      v[r] = x + y;
     }
-    halve<4>(v, lane, 16);
-    halve<2>(first_of<4>(v), lane, 8);
-    halve<1>(first_of<2>(first_of<4>(v)), lane, 4);
+    halve<1>(v, lane, 16);
     float x = v[0];
-    x += __shfl_xor_sync(0xffffffffu, x, 2);
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-    float S = __shfl_xor_sync(0xffffffffu, x, 16), F = x;
-    const unsigned low = __ballot_sync(0xffffffffu, mine && (lane & 19) == 16 && S < LOW_ROW * a.E);
-    if (low) {  // rare: row by row, read again
-      for (int i = 0; i < nb; ++i)
-        if ((low >> (16 + 4 * i)) & 1u) {
-          float z[PER], s[PER], Si, Fi;
-          load_row<PER, VEC>(a.logits + (size_t)(t + i) * a.E, a.E, lane, z);
-          low_row<PER>(z, cur.f, s, Si, Fi);
-          if (row == i) {
-            S = Si;
-            F = Fi;
-          }
-        }
-    }
-    if (mine && (lane & 19) == 16 && S != 0.f) few += (1.0f + __fdividef(F, S)) * cur.inv;
-    if ((n & 3) == 3) {
-      acc += (double)few;
-      few = 0.f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float S = __shfl_sync(0xffffffffu, x, 16 * r);
+      if (!((live >> r) & 1u)) continue;
+      if (S < LOW_ROW * a.E) {  // rare: the row again
+        float z[PER], s[PER], zero[PER], F;
+        load_row<PER, VEC>(a.logits + (size_t)(t + r) * a.E, a.E, lane, z);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) zero[j] = 0.f;
+        low_row<PER>(z, zero, s, S, F);
+#pragma unroll
+        for (int j = 0; j < PER; j += 2) sv[r][j / 2] = pack2(s[j], s[j + 1]);
+      }
+      if (S == 0.f) continue;  // a row of -infinity has no shares
+      ++counted;
+      const float inv = rcp_of(S);
+#pragma unroll
+      for (int j = 0; j < PER; j += 2) unpack2(fma2(sv[r][j / 2], pack2(inv, inv), pack2(P[j], P[j + 1])), P[j], P[j + 1]);
     }
     t += nb;
+    const bool flush = t >= t1 || t >= cur.end;
+    if (flush || ++n == 8) {
+      n = 0;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        Q[j] += P[j];
+        P[j] = 0.f;
+      }
+    }
+    if (flush && counted) {
+      pdl_wait();  // the counts
+      cur.load(a, lane);
+      float d = 0.f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) d = fmaf(cur.f[j], Q[j], d);
+      acc += ((double)d + (lane == 0 ? (double)counted : 0.0)) * (double)cur.inv;
+    }
+    if (flush) {
+      counted = 0;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) Q[j] = 0.f;
+    }
   }
-  acc = warp_sum_d(acc + (double)few);
+  pdl_wait();  // (also of warps without tokens: the ticket)
+  acc = warp_sum_d(acc);
   if (lane == 0) red[warp] = acc;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -726,6 +758,11 @@ __global__ void __launch_bounds__(256, backward_blocks<PER>()) k_bal_backward(co
           if (total < LOW_ROW * MAX_TOPK) sp = in && m > -INFINITY ? exp_of(zp - m) : 0.f;
           total = sum_of(sp);
         }
+        // The weights' sum of one makes any constant in g drop out: with the first pick's g taken off, a token of one
+        // pick gets an exact zero, whatever the quotient's rounding.
+        const unsigned ins = __ballot_sync(0xffffffffu, in) >> (slot * W) & ((1u << W) - 1);
+        g -= __shfl_sync(0xffffffffu, g, slot * W + max(__ffs(ins) - 1, 0));
+        if (!in) g = 0.f;
         const float w = total != 0.f ? __fdividef(sp, total) : 0.f;
         add = w * (g - sum_of(g * w)) * qp;
       }
