@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(256) k_bal_count(const BalArgs a) {
   if (t0 >= t1) return;
   int b = seq_of(a, t0, lane);
   for (int t = t0; t < t1 && b < a.n_seq;) {  // piece [t, end) of sequence b
-    const int end = min(min(t1, t + COUNT_INTS / a.k), max(t + 1, b < 0 ? seq_at(a, 0) : seq_at(a, b + 1)));
+    const int end = min(min(t1, t + COUNT_INTS / a.k), max(t + 1, seq_at(a, b + 1)));
     if (b >= 0) {
       const bool whole = end - t >= SHORT;
       int* sc = a.seq_counts + (size_t)b * a.E;
@@ -288,8 +288,9 @@ __global__ void __launch_bounds__(256) k_bal_count(const BalArgs a) {
       }
     }
     t = end;
-    // still this sequence, the next one, or past a run of empty ones the next that holds a token
-    if (b < 0 || seq_at(a, b + 1) <= t) b = b + 1 >= a.n_seq || seq_at(a, b + 2) > t ? b + 1 : seq_of(a, t, lane);
+    // still this sequence (or before the first, whose pieces end before its start too), the next one, or past a run of
+    // empty ones the next that holds a token
+    if (seq_at(a, b + 1) <= t) b = b + 1 >= a.n_seq || seq_at(a, b + 2) > t ? b + 1 : seq_of(a, t, lane);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += 256)
