@@ -767,11 +767,11 @@ __global__ void __launch_bounds__(256, backward_blocks<PER>()) k_bal_backward(co
           if (total < LOW_ROW * MAX_TOPK) sp = in && m > -INFINITY ? exp_of(zp - m) : 0.f;
           total = sum_of(sp);
         }
-        // The weights' sum of one makes any constant in g drop out: with the first pick's g taken off, a token of one
-        // pick gets an exact zero, whatever the quotient's rounding.
+        // The weights' sum of one makes any constant in g drop out: a token of one pick gets an exact zero, whatever the
+        // quotient's rounding (and NaN shows). Of several picks nothing is taken off: where a pick of a small weight has
+        // a large g, the others would lose their digits.
         const unsigned ins = __ballot_sync(0xffffffffu, in) >> (slot * W) & ((1u << W) - 1);
-        g -= __shfl_sync(0xffffffffu, g, slot * W + max(__ffs(ins) - 1, 0));
-        if (!in) g = 0.f;
+        if (__popc(ins) == 1) g -= g;
         const float w = total != 0.f ? __fdividef(sp, total) : 0.f;
         add = w * (g - sum_of(g * w)) * qp;
       }
