@@ -8,7 +8,7 @@ from w4a16_moe_decode_gb300 import binding as fb
 from w4a16_moe_decode_gb300.build import build
 
 from _finetune import router
-from test_gpu_balance import check_all
+from test_gpu_balance import check_all, gradient
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +32,29 @@ def test_a_large_gradient_of_an_unlikely_pick(k, big):
     z[0, :3] = torch.tensor([-14.0, 1.0, 0.0])
     dw[0, :3] = torch.tensor([big, 1.0, 2.0])
     check_all(z, idx, start, dw, k)
+
+
+@pytest.mark.parametrize("E,k", [(2, 1), (32, 4), (130, 3), (36, 12)])
+def test_rows_of_very_low_scores(E, k):
+    """Rows of logits from -10 down to -90 with experts that are masked or far below the rest: their shares are those
+    of the definition, and a masked expert's gradient is exactly zero."""
+    T = 40
+    z, _, start, dw = router(T, E, k, 50 + E, [0, T])
+    z[:] = 0.25 * z - torch.linspace(10.0, 90.0, T)[:, None]
+    z[1::3, E - 1] = -float("inf")
+    z[26:36:3, 0] = -95.0  # rows of -62 and below
+    z[27:36:3, 0] = torch.finfo(torch.float32).min
+    idx = torch.topk(z, k, dim=1).indices.to(torch.int32)
+    _, sc, st = check_all(z, idx, start, dw, k)
+    for g in (None, dw):
+        assert not gradient(z, idx, start, k, 0.5, sc, st, 1e20, g)[1::3, E - 1].any()
+
+
+def test_a_masked_expert_beside_ordinary_scores():
+    """Picked or not, in a row of any size: zero."""
+    z, idx, start, dw = router(30, 64, 4, 60, [0, 30])
+    z[::2, 5] = z[::2, 40] = -float("inf")
+    idx[::4, 1] = 5
+    _, sc, st = check_all(z, idx, start, dw, 4)
+    dz = gradient(z, idx, start, 4, 0.5, sc, st, 1e38, dw)
+    assert not dz[::2, 5].any() and not dz[::2, 40].any()

@@ -95,13 +95,16 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 }
 
 // s = sigmoid(z) and q = 1 - s without cancellation: with e = exp(-z), s = 1 / (1 + e) and
-// q = e s. e is held at 1e37, where s is still an FP32 normal; rows in which no s is above
-// 1e-30 take the exact shares below instead.
-constexpr float LOW_ROW = 1e-30f;
+// q = e s. Scores below the smallest FP32 normal (z under -87.3) are zero, and e is held
+// below infinity in q only, so that e s s is zero there. Rows in which no s is above 1e-12
+// take the shares of exp(z - max z) instead, which are theirs to 1e-12 E < 2^-30 of the
+// value (sigmoid(z) = exp(z) / (1 + exp(z))): so what is lost to zero is below 1e-26 of a row.
+constexpr float LOW_ROW = 1e-12f;
+constexpr float E_MOST = 8.5e37f;  // 2^126: 1 / (1 + e) of a larger e is zero
 __device__ __forceinline__ void sigmoid2(float z, float& s, float& q) {
-  const float e = min_nan(exp_of(-z), 1e37f);
+  const float e = exp_of(-z);
   s = rcp_of(1.0f + e);
-  q = e * s;
+  q = e > 1e9f ? 1.0f : e * s;
 }
 
 // Pairs of FP32 values in one instruction.
@@ -140,7 +143,7 @@ __device__ __forceinline__ int elem(int lane, int j) {
   return VEC ? 4 * (lane + 32 * (j >> 2)) + (j & 3) : lane + 32 * j;
 }
 
-// -infinity stands for the places past E: their s of 1e-37 is lost in any sum that counts.
+// -infinity stands for the places past E: their s is zero.
 template <int PER, bool VEC>
 __device__ __forceinline__ void load_row(const float* row, int E, int lane, float (&z)[PER]) {
   if (VEC) {
@@ -686,8 +689,10 @@ __global__ void __launch_bounds__(256, backward_blocks<PER>()) k_bal_backward(co
         for (int j = 0; j < PER; j += 2) {
           float x, y;
           unpack2(mul2(pack2(z[j], z[j + 1]), k), x, y);
-          const f32x2 e = pack2(ex2_of(min_nan(x, 122.f)), ex2_of(min_nan(y, 122.f)));  // so that e s is no infinity times 0
-          unpack2(add2(e, one), x, y);
+          x = ex2_of(x);
+          y = ex2_of(y);
+          const f32x2 e = pack2(min_nan(x, E_MOST), min_nan(y, E_MOST));  // so that e s is no infinity times 0
+          unpack2(add2(pack2(x, y), one), x, y);
           const f32x2 s = pack2(rcp_of(x), rcp_of(y));
           S2 = add2(S2, s);
           F2 = fma2(pack2(cur.f[j], cur.f[j + 1]), s, F2);
