@@ -85,3 +85,23 @@ def test_tokens_before_the_first_sequence(T, E, k, start):
     """More of them than a block counts at once, ending inside its run, at its end and blocks further on."""
     z, idx, dw, _ = routed(T, E, k, T + k)
     check_large(z, idx, torch.tensor(start, dtype=torch.int32), dw, k)
+
+
+@pytest.mark.parametrize("E,k", [(256, 6), (64, 8), (37, 3), (255, 12), (512, 16), (16, 2)])
+@pytest.mark.parametrize("renormalize,scale", [(True, 1.0), (False, 2.5)])
+def test_many_rows_a_warp(E, k, renormalize, scale):
+    """Sequences of one to seven tokens, empty ones and long ones, tokens outside them all, padding at every place among
+    a warp's tokens, dropped picks and experts picked twice."""
+    T = 60000
+    z, idx, dw, g = routed(T, E, k, E + k)
+    short = 100 + torch.cumsum(torch.randint(0, 8, (4000,), generator=g), 0)
+    start = torch.cat([torch.tensor([100]), short, torch.tensor([20000, 20000, 41111, T - 300])]).to(torch.int32)
+    hit = lambda share: torch.rand(T, generator=g) < share  # noqa: E731
+    if k > 1:
+        idx[hit(0.1), k - 1] = E + 7
+        idx[hit(0.05), k - 1] = -3
+        twice = hit(0.1)
+        idx[twice, 1] = idx[twice, 0]
+    idx[hit(0.07), 0] = -1
+    idx[30000:30400, 0] = -1
+    check_large(z, idx, start, dw, k, renormalize=renormalize, routed_scale=scale)
