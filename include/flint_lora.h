@@ -4,14 +4,20 @@
  * nor exchanged per request. What a request or a fine-tune changes is a
  * low-rank adapter beside the matrix. For token row x_t (bf16 [K]) with
  * adapter a = adapter[t], and the projection's own output row base_t:
- *   y_t = bf16(base_t + s_a B_a (A_a x_t))        (FP32 or better throughout)
+ *   y_t = bf16(base_t + s_a B_a (A_a x_t))
  * with A_a bf16 [R][K], B_a bf16 [N][R] and the FP32 scale s_a. Tokens of
  * different adapters share one call in any order. An index outside
  * 0 .. num_adapters - 1 (by custom -1) means no adapter: y_t = bf16(base_t).
  *
- * The low-rank row A_a x_t is summed in FP32 and enters the second product as
- * the sum of two bf16 values (hi = bf16(h), lo = bf16(h - hi)): 16 significant
- * bits, so the only rounding that shows is the one of the output.
+ * Every sum is FP32. The low-rank row h_t = s_a A_a x_t enters the second product
+ * as the sum of two bf16 values (hi = bf16(h), lo = bf16(h - hi)), 16 significant
+ * bits: each term is within 2^-16 of its value, where the output's rounding is
+ * 2^-8. The same holds for g_t of the gradients.
+ * Values that are not finite: infinite values of h and g, and finite ones above
+ * bf16's largest, go through; where x, dy or an adapter itself holds an infinity,
+ * an output that it makes infinite by the formula may be NaN (x: its columns of
+ * da, dy: its rows of db, an adapter: its outputs). Outputs that the formula
+ * makes finite stay as they are.
  *
  * Conventions as in flint_moe.h: device pointers, caller-owned memory, no
  * allocation, asynchronous on `stream`, status codes. Matrices, rows and row

@@ -69,6 +69,22 @@ __device__ __forceinline__ uint32_t f2b2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&o);
 }
 
+// Four values of h or g as bf16 halves: hi + lo carries 16 significant bits of the FP32 sum into the next product,
+// whose operands are bf16 on the tensor cores; a third half would carry 24, for half as many MMAs again and half as
+// much more of h in memory, and change an output by 2^-16 of a term where its own rounding changes it by 2^-8.
+// A finite value that rounds beyond bf16's largest keeps that as its hi and the rest in lo; an infinity has no rest.
+constexpr float BF16_MAX = 3.3895313892515355e38f;
+__device__ __forceinline__ void halves(const float4 v, uint2& hi, uint2& lo) {
+  hi = make_uint2(f2b2(v.x, v.y), f2b2(v.z, v.w));
+  lo = make_uint2(f2b2(v.x - bf16lo(hi.x), v.y - bf16hi(hi.x)), f2b2(v.z - bf16lo(hi.y), v.w - bf16hi(hi.y)));
+  if (fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))) > BF16_MAX) {  // rare
+    auto top = [](float t) { return fabsf(t) > BF16_MAX && fabsf(t) < INFINITY ? copysignf(BF16_MAX, t) : t; };
+    auto rest = [](float t, float h) { return fabsf(t) == INFINITY ? 0.f : t - h; };
+    hi = make_uint2(f2b2(top(v.x), top(v.y)), f2b2(top(v.z), top(v.w)));
+    lo = make_uint2(f2b2(rest(v.x, bf16lo(hi.x)), rest(v.y, bf16hi(hi.x))), f2b2(rest(v.z, bf16lo(hi.y)), rest(v.w, bf16hi(hi.y))));
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Plan (one block): tokens sorted by adapter, stably, into tiles. Warp w owns a
 // run of consecutive tokens; the 32 tokens of a step find their fellows with
@@ -442,9 +458,8 @@ __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, co
         v.y *= sc;
         v.z *= sc;
         v.w *= sc;
-        // hi + lo carries 16 significant bits of the FP32 sum into the next product
-        const uint2 hv = make_uint2(f2b2(v.x, v.y), f2b2(v.z, v.w));
-        const uint2 lv = make_uint2(f2b2(v.x - bf16lo(hv.x), v.y - bf16hi(hv.x)), f2b2(v.z - bf16lo(hv.y), v.w - bf16hi(hv.y)));
+        uint2 hv, lv;
+        halves(v, hv, lv);
         const size_t at = ((size_t)tile * TM + r) * a.R + c;
         *reinterpret_cast<uint2*>(hi + at) = hv;
         *reinterpret_cast<uint2*>(lo + at) = lv;
@@ -1278,8 +1293,8 @@ __global__ void __launch_bounds__(FEW_THREADS, FEW_CTAS) k_lora_few(const FewArg
     for (int i = threadIdx.x * 4; i < cols * P.RP; i += FEW_THREADS * 4) {
       float4 u[FEW_S];
 #pragma unroll
-      for (int q = 0; q < FEW_S; ++q)
-        u[q] = i < vals ? ld_dsmem_f4(dsmem_addr(local + i * 4, q)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < FEW_S; ++q)  // (ranks past R are zero also beside an infinite x)
+        u[q] = i < vals && i % P.RP < a.R ? ld_dsmem_f4(dsmem_addr(local + i * 4, q)) : make_float4(0.f, 0.f, 0.f, 0.f);
       float4 v = u[0];
 #pragma unroll
       for (int q = 1; q < FEW_S; ++q) {
@@ -1292,9 +1307,8 @@ __global__ void __launch_bounds__(FEW_THREADS, FEW_CTAS) k_lora_few(const FewArg
       v.y *= sc;
       v.z *= sc;
       v.w *= sc;
-      // hi + lo carries 16 significant bits of the FP32 sum into the next product
-      const uint2 hv = make_uint2(f2b2(v.x, v.y), f2b2(v.z, v.w));
-      const uint2 lv = make_uint2(f2b2(v.x - bf16lo(hv.x), v.y - bf16hi(hv.x)), f2b2(v.z - bf16lo(hv.y), v.w - bf16hi(hv.y)));
+      uint2 hv, lv;
+      halves(v, hv, lv);
       const int at = i / P.RP * (P.RP + 8) + i % P.RP;
       *reinterpret_cast<uint2*>(hs + at) = hv;
       *reinterpret_cast<uint2*>(lo + at) = lv;
