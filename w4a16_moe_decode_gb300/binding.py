@@ -366,17 +366,41 @@ def _nbytes(workspace, workspace_bytes) -> int:
     return workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
 
 
+def _row_stride(t, rows: int, cols: int) -> int | None:
+    """Elements between the rows of a tensor of other than two dimensions that holds `rows` rows of `cols` values; None
+    if one stride does not describe them."""
+    if t.numel() < rows * cols:
+        return None
+    dims = [(n, st) for n, st in zip(t.shape, t.stride()) if n != 1]
+    n = 1  # elements of a row found so far, side by side
+    while dims and n < cols and dims[-1][1] == n:
+        n *= dims.pop()[0]
+    if n != cols:  # also a contiguous buffer that no boundary cuts into rows
+        return cols if t.is_contiguous() and (t.dim() < 2 or t.numel() == rows * cols) else None
+    for (_, outer), (m, st) in zip(dims, dims[1:]):
+        if outer != m * st:
+            return None
+    return dims[-1][1] if dims and rows > 1 else cols
+
+
 def _ld(t, rows: int, cols: int, ld, like=None) -> int:
-    """Elements between the rows of t: `ld` if given, else a 2-D tensor's own row stride (cols where
-    there is one row, no tensor or a bare pointer). Refused: elements of a row that do not lie side by
-    side, and a tensor `like`, read by the same stride, that has another."""
+    """Elements between the rows of t: `ld` if given, else a tensor's own row stride (cols where there is one row, no
+    tensor or a bare pointer). Refused: elements of a row that do not lie side by side, rows that one stride does not
+    describe, fewer of either than are read, and a tensor `like`, read by the same stride, that has another."""
     if ld is not None:
         return ld
-    if t is None or isinstance(t, int) or t.dim() != 2:
+    if t is None or isinstance(t, int) or rows < 1:
         return cols
-    if t.stride(1) != 1 and cols > 1:
-        raise FlintMoeError("row elements apart", EINVAL)
-    ld = cols if rows < 2 else t.stride(0)
+    if t.dim() != 2:
+        ld = _row_stride(t, rows, cols)
+        if ld is None:
+            raise FlintMoeError("rows apart", EINVAL)
+    else:
+        if t.stride(1) != 1 and cols > 1:
+            raise FlintMoeError("row elements apart", EINVAL)
+        if t.shape[0] < rows or t.shape[1] < cols:
+            raise FlintMoeError("fewer rows or columns", EINVAL)
+        ld = cols if rows < 2 else t.stride(0)
     if like is not None and not isinstance(like, int) and like is not t and _ld(like, rows, cols, None) != ld:
         raise FlintMoeError("row strides differ", EINVAL)
     return ld
