@@ -66,3 +66,23 @@ def test_calls_refuse_such_rows(monkeypatch):
         refused(fb.flint_lora_apply, lora, x, ad, 16, yi, yo, ws, **kw)
     for x, dy, di, do in ((wide, flat, None, None), (flat, wide, None, None), (flat, flat, wide, flat), (flat, flat, None, wide)):
         refused(fb.flint_lora_backward, lora, x, dy, ad, 16, di, do, 0x700000, 0x800000, ws, **kw)
+
+
+def test_pools_of_adapters():
+    n, R, K, N = 4, 16, 64, 128
+    a, b, s = bf(n, R, K), bf(n, N, R), torch.zeros(n)
+    lora = fb.flint_lora_init(a, b, s)
+    assert (lora.num_adapters, lora.rank, lora.in_dim, lora.out_dim) == (n, R, K, N)
+    fb.flint_lora_init(a.view(torch.int16), b.view(torch.int16), s)              # the values' bits
+    fb.flint_lora_init(a.flatten(), b.flatten(), s, K, N, R, n)
+    fb.flint_lora_init(a, b, s, K, N, R, n - 1)                                 # the first of a pool
+    fb.flint_lora_init(0x100000, 0x200000, 0x300000, K, N, R, n)
+    for bad in (bf(n, N, R // 2), bf(n, N, 2 * R), bf(n - 1, N, R), bf(n + 1, N, R), bf(n, R, N).transpose(1, 2), bf(n, N, 2 * R)[:, :, :R],
+                torch.zeros(n, N, R), torch.zeros(n, N, R, dtype=torch.float16), bf(n, N * R)):
+        refused(fb.flint_lora_init, a, bad, s)
+    for bad in (bf(n, K, R).transpose(1, 2), bf(n, R, 2 * K)[:, :, :K], torch.zeros(n, R, K), bf(n * R, K), bf(2 * n, R, K)[::2]):
+        refused(fb.flint_lora_init, bad, b, s)
+    for bad in (torch.zeros(n - 1), torch.zeros(n, dtype=torch.float64), bf(n), torch.zeros(2 * n)[::2]):
+        refused(fb.flint_lora_init, a, b, bad)
+    refused(fb.flint_lora_init, a, b, s, K, N, R, n + 1)                        # past the tensors' ends
+    refused(fb.flint_lora_init, a, b, s, 2 * K, N, R, n)

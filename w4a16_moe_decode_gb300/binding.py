@@ -9,6 +9,7 @@ implementation.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 from .build import LIB
@@ -406,12 +407,29 @@ def _ld(t, rows: int, cols: int, ld, like=None) -> int:
     return ld
 
 
+def _pool(t, shape, bf16: bool, exact: bool) -> None:
+    """Refuses a tensor that does not hold an adapter pool's values side by side: bf16 (or their bits) or float32, of
+    this shape, or (where the shape was given beside it) at least as many."""
+    if t is None or isinstance(t, int):
+        return
+    import torch
+    kinds = (torch.bfloat16, torch.int16, torch.uint16) if bf16 else (torch.float32,)
+    if t.dtype not in kinds or not t.is_contiguous() or (tuple(t.shape) != shape if exact else t.numel() < math.prod(shape)):
+        raise FlintMoeError(f"adapter pool {tuple(t.shape)} for {shape}", EINVAL)
+
+
 def flint_lora_init(a, b, scale, in_dim=None, out_dim=None, rank=None, num_adapters=None) -> flint_lora:
-    """A pool of adapters: a [n][R][K], b [n][N][R] (bf16), scale [n] (float32). The shapes come from the
+    """A pool of adapters: a [n][R][K], b [n][N][R] (bf16), scale [n] (float32), contiguous. The shapes come from the
     tensors unless given. The caller keeps the tensors alive."""
-    if num_adapters is None:
+    given = num_adapters is not None
+    if not given:
+        if a.dim() != 3 or b.dim() != 3:
+            raise FlintMoeError("adapter pool", EINVAL)
         num_adapters, rank, in_dim = a.shape
         out_dim = b.shape[1]
+    _pool(a, (num_adapters, rank, in_dim), True, not given)
+    _pool(b, (num_adapters, out_dim, rank), True, not given)
+    _pool(scale, (num_adapters,), False, False)
     lora = flint_lora()
     _check("flint_lora_init", lib().flint_lora_init(in_dim, out_dim, rank, num_adapters, _ptr(a), _ptr(b),
                                                     _ptr(scale), ctypes.byref(lora)))
