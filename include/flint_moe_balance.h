@@ -50,7 +50,8 @@ size_t flint_moe_balance_workspace_bytes(const flint_moe_config* cfg, int32_t ma
  * Writes loss float32 [1], counts int32 [E] (over all sequences: what an
  * update of the selection bias goes by), seq_counts int32 [n_seq][E] (c_be)
  * and seq_tokens int32 [n_seq] (T_b), which the backward call takes. T = 0
- * writes zeros. */
+ * writes zeros. Outputs and workspace that overlap one another or an input are
+ * refused (FLINT_MOE_EINVAL), counts and seq_counts of one sequence too. */
 flint_moe_status flint_moe_balance(const flint_moe_config* cfg, const float* logits, const int32_t* idx, int32_t T,
                                    const int32_t* seq_start, int32_t n_seq, float alpha, float* loss,
                                    int32_t* counts, int32_t* seq_counts, int32_t* seq_tokens, void* workspace,
@@ -63,8 +64,8 @@ flint_moe_status flint_moe_balance(const flint_moe_config* cfg, const float* log
  *            routed_scale s_tj dw_tj (1 - s_tj)
  * dloss: float32 [1] on the device, NULL means 1. dw: float32 [T][k], the
  * gradient of the routing weights, NULL for none. seq_counts and seq_tokens as
- * flint_moe_balance wrote them. dlogits float32 [T][E] (not overlapping
- * logits): padding tokens get zeros; rows of tokens in no sequence are left as
+ * flint_moe_balance wrote them. dlogits float32 [T][E] (refused where it
+ * overlaps an input: FLINT_MOE_EINVAL): padding tokens get zeros; rows of tokens in no sequence are left as
  * they were. An expert picked twice by a token gets both gradients. */
 flint_moe_status flint_moe_balance_backward(const flint_moe_config* cfg, const float* logits, const int32_t* idx,
                                             int32_t T, const int32_t* seq_start, int32_t n_seq, float alpha,

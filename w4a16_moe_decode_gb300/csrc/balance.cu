@@ -16,6 +16,7 @@
 // (69 MB), gradient 29.9 (67 MB in, 67 MB out: 4.5 TB/s); whole calls 28.0 and 32.0.
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 #include <type_traits>
 
 #include "common.cuh"
@@ -853,9 +854,24 @@ BalWs bal_ws() {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-bool overlap(const void* p, size_t np, const void* q, size_t nq) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + nq && b < a + np;
+struct Span {
+  const void* p;
+  size_t n;
+};
+// Whether one of the outputs shares memory with another or with an input: kernels of a call write the one while they
+// read or add to the other.
+bool overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  auto meet = [](const Span& u, const Span& v) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(u.p), b = reinterpret_cast<uintptr_t>(v.p);
+    return u.p && v.p && u.n && v.n && a < b + v.n && b < a + u.n;
+  };
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span* q = o + 1; q != outs.end(); ++q)
+      if (meet(*o, *q)) return true;
+    for (const Span& i : ins)
+      if (meet(*o, i)) return true;
+  }
+  return false;
 }
 
 flint_moe_status check_sizes(const flint_moe_config* c, int32_t T, const int32_t* seq_start, int32_t n_seq, float alpha) {
@@ -926,6 +942,10 @@ extern "C" flint_moe_status flint_moe_balance(const flint_moe_config* c, const f
     return FLINT_MOE_EALIGN;
   const BalWs w = bal_ws();
   if (ws_bytes < w.total) return FLINT_MOE_EINVAL;
+  const size_t E4 = sizeof(float) * c->num_experts, n4 = sizeof(int) * (size_t)n_seq;
+  if (overlap({{loss, 4}, {counts, E4}, {seq_counts, E4 * n_seq}, {seq_tokens, n4}, {ws, w.total}},
+              {{logits, E4 * T}, {idx, sizeof(int) * (size_t)T * c->top_k}, {seq_start, n4 + 4}}))
+    return FLINT_MOE_EINVAL;
   BalArgs a = {};
   a.T = T;
   a.E = c->num_experts;
@@ -968,8 +988,10 @@ extern "C" flint_moe_status flint_moe_balance_backward(const flint_moe_config* c
   if (!aligned(logits, row) || !aligned(dlogits, row) || !aligned(idx, 4) || !aligned(seq_start, 4) ||
       !aligned(seq_counts, 4) || !aligned(seq_tokens, 4) || !aligned(dloss, 4) || !aligned(dw, 4))
     return FLINT_MOE_EALIGN;
-  const size_t bytes = (size_t)T * c->num_experts * 4;
-  if (overlap(logits, bytes, dlogits, bytes)) return FLINT_MOE_EINVAL;
+  const size_t E4 = sizeof(float) * c->num_experts, k4 = sizeof(int) * (size_t)T * c->top_k, n4 = sizeof(int) * (size_t)n_seq;
+  if (overlap({{dlogits, E4 * T}},
+              {{logits, E4 * T}, {idx, k4}, {seq_start, n4 + 4}, {seq_counts, E4 * n_seq}, {seq_tokens, n4}, {dloss, 4}, {dw, k4}}))
+    return FLINT_MOE_EINVAL;
   BalArgs a = {};
   a.T = T;
   a.E = c->num_experts;
