@@ -1686,18 +1686,19 @@ struct GemvArgs {
   int N, K, B, fmt, prenorm;
   const uint16_t* x;
   uint16_t* y;
-  // flint_gemv_lora (the ADD kernels): FP32 rows [B][N] added to the sums before they are rounded, for the rows t whose adapter[t] lies in
-  // 0 .. n_adapters - 1. The kernel before this one writes them, and waited itself for the kernel that wrote x: so x
-  // is complete from the start, and the wait for the kernel before moves from the top to where add32 is read.
-  const float* add32;
-  const int* adapter;
-  int n_adapters;
   const uint8_t* packed;
   const float* G;  // the tensor scale word after the tiles
   Layout L;
   const uint16_t* gamma;
   float eps;
   int* status;
+  // flint_gemv_lora (the ADD kernels): FP32 rows [B][N] added to the sums before they are rounded, for the rows t whose
+  // adapter[t] lies in 0 .. n_adapters - 1. The kernel before this one writes them, and waited itself for the kernel
+  // that wrote x: so x is complete from the start, and the wait for the kernel before moves from the top to where add32
+  // is read. (At the end: between the others they cost the plain GEMV 3 %, 4864 x 2048, 4 rows 3.30 -> 3.42 us.)
+  const float* add32;
+  const int* adapter;
+  int n_adapters;
 };
 
 __host__ __device__ inline size_t gemv_smem(int K, int B, int fmt, int nw, int ntmax, size_t* xs_off,
@@ -2028,8 +2029,10 @@ __device__ __forceinline__ void stage_slice(const GemvArgs& a, uint8_t* xs, floa
   }
 }
 
-template <int FMT, int NTMAX, bool ADD>
-__global__ void __launch_bounds__(256) k_gemv_split(GemvArgs a) {
+// SOLO (one token): at most 64 registers, four CTAs per SM, so that a call of up to 304 CTAs leaves room for all of the
+// next one's, which fetch their weights meanwhile (2432 x 4096: 4.7 -> 4.0 us per call at 80 registers and 64).
+template <int FMT, int NTMAX, bool ADD, bool SOLO = false>
+__global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -2310,12 +2313,11 @@ int sm_count() {
 template <typename K, typename Args>
 cudaError_t launch_any(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const Args& a);
 
-// The GEMV kernels' launches: attributes are set once for each device instead of at every call (two runtime calls of
+// The GEMV kernels' attributes are set once for each device instead of at every call (two runtime calls of
 // three that a launch would make).
-template <auto KERNEL, typename Args>
-cudaError_t launch_gemv(dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t stream, const Args& a) {
+template <auto KERNEL>
+cudaError_t prepare_gemv(int& dev) {
   static std::atomic<uint64_t> done{0};
-  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const bool known = dev < 64 && ((done.load() >> dev) & 1);
@@ -2327,6 +2329,14 @@ cudaError_t launch_gemv(dim3 grid, dim3 block, size_t smem, int cluster, cudaStr
     if (e != cudaSuccess) return e;
     if (dev < 64) done.fetch_or((uint64_t)1 << dev);
   }
+  return cudaSuccess;
+}
+
+template <auto KERNEL, typename Args>
+cudaError_t launch_gemv(dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t stream, const Args& a) {
+  int dev = 0;
+  const cudaError_t e = prepare_gemv<KERNEL>(dev);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -2342,6 +2352,63 @@ cudaError_t launch_gemv(dim3 grid, dim3 block, size_t smem, int cluster, cudaStr
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, KERNEL, a);
+}
+
+// Clusters of S blocks of a split GEMV kernel that run at once on the current device: asked once for each device, S
+// and blocks an SM's shared memory holds. The SMs of a cluster lie in one part of the chip, so these are fewer than
+// SMs x blocks / S (200 clusters of 3 in two rounds of 100, of which 97 ran at once: 17.8 us for 3200 x 6144 BF16
+// instead of 14.2).
+template <auto KERNEL>
+int clusters_at_once(int S, size_t smem) {
+  static std::atomic<int> known[64][5][5];
+  int dev = 0;
+  if (prepare_gemv<KERNEL>(dev) != cudaSuccess) return 1;
+  const int per = (int)std::min<size_t>(4, (SMEM_LIMIT + 1024) / (smem + 1024));
+  if (dev < 64)
+    if (const int n = known[dev][S][per].load()) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, S);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 1;
+  attr.val.clusterDim.y = S;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(KERNEL), &cfg) != cudaSuccess || n < 1) return std::max(1, sm_count() / S);
+  if (dev < 64) known[dev][S][per].store(n);
+  return n;
+}
+
+// The split GEMV: one tile a cluster, or, for more tiles than clusters run at once, clusters that stage their rows
+// once for several tiles, in as few rounds as run at once. With one row of NVFP4 one tile a cluster stays ahead while
+// this call's clusters and the next one's fit side by side (2432 x 4096: 4.0 us and 4.7; 2464 x 4096, which do not,
+// 4.7 and 4.6). A cluster holds one BF16 tile at a time (65 KB a CTA), so its next tile's weights wait for the products
+// before; with one row, three CTAs of the one-tile kernel fit an SM. Where more of those run at once, BF16 takes them
+// for tiles that all run at once (2560 x 4096: 7.3 us, 9.0 with two tiles a cluster; 2432 x 6144, which do not, 12.4
+// and 10.3), and for three rounds or more of which over a fifth would be empty (3200 x 6144: 14.2 and 14.8;
+// 3648 x 8192: 19.2 and 19.9; 7296 x 4096 in full rounds: 17.4 and 16.3).
+template <int FMT, int NT, bool ADD, bool SOLO>
+cudaError_t launch_split(const GemvArgs& a, int S, cudaStream_t stream) {
+  const dim3 block(256);
+  const int tiles = a.N / 16;
+  const size_t one = gemv_split_plan(a.B, FMT, 8, NT).total, rows = gemv_split_rows_plan(a.B, FMT, 8, NT).total;
+  if (rows <= SMEM_LIMIT) {
+    const int most = clusters_at_once<k_gemv_split_rows<FMT, NT, ADD>>(S, rows), rounds = (tiles + most - 1) / most;
+    bool several = rounds > 1;
+    if (several && (SOLO || FMT == FLINT_MOE_BF16)) {
+      const int ones = clusters_at_once<k_gemv_split<FMT, NT, ADD, SOLO>>(S, one);
+      if (FMT == FLINT_MOE_NVFP4 ? 2 * tiles <= ones
+                                 : ones > most && (tiles <= ones || (rounds > 2 && 4 * rounds * most > 5 * tiles)))
+        several = false;
+    }
+    if (several)
+      return launch_gemv<k_gemv_split_rows<FMT, NT, ADD>>(dim3((tiles + rounds - 1) / rounds, S), block, rows, S, stream, a);
+  }
+  return launch_gemv<k_gemv_split<FMT, NT, ADD, SOLO>>(dim3(tiles, S), block, one, S, stream, a);
 }
 
 template <typename K>
@@ -2810,36 +2877,19 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
   const int kg = K / KG_COLS, nw = kg % 8 == 0 ? 8 : 4, ntmax = (B + 7) / 8;
   if (K > GEMV_SLICE) {  // split along K over a cluster of K / 2048 CTAs
     const int S = K / GEMV_SLICE;
-    const size_t smem = gemv_split_plan(B, fmt, 8, ntmax).total;
-    if (smem > SMEM_LIMIT) return FLINT_MOE_EUNSUPPORTED;
-    const dim3 grid(N / 16, S), block(256);
-    cudaError_t e;
+    if (gemv_split_plan(B, fmt, 8, ntmax).total > SMEM_LIMIT) return FLINT_MOE_EUNSUPPORTED;
     const bool nv = fmt == FLINT_MOE_NVFP4, add = add32 != nullptr;
-#define FLINT_SPLIT(FMT, NT)                                                           \
-  (add ? launch_gemv<k_gemv_split<FMT, NT, true>>(grid, block, smem, S, stream, a)     \
-       : launch_gemv<k_gemv_split<FMT, NT, false>>(grid, block, smem, S, stream, a))
-#define FLINT_SPLIT_ROWS(FMT, NT)                                                                     \
-  (add ? launch_gemv<k_gemv_split_rows<FMT, NT, true>>(rgrid, block, rplan.total, S, stream, a)       \
-       : launch_gemv<k_gemv_split_rows<FMT, NT, false>>(rgrid, block, rplan.total, S, stream, a))
-    const GemvSplitRowsPlan rplan = gemv_split_rows_plan(B, fmt, 8, ntmax);
-    const int tiles = N / 16, per_sm = ntmax <= 2 && 2 * (rplan.total + 1024) <= SMEM_LIMIT + 1024 ? 2 : 1;
-    const int most = std::max(1, sm_count() * per_sm / S), rounds = (tiles + most - 1) / most;  // clusters at once
-    if (rounds > 1 && rplan.total <= SMEM_LIMIT) {
-      const dim3 rgrid((tiles + rounds - 1) / rounds, S);
-      switch (ntmax) {
-        case 1: e = nv ? FLINT_SPLIT_ROWS(FLINT_MOE_NVFP4, 1) : FLINT_SPLIT_ROWS(FLINT_MOE_BF16, 1); break;
-        case 2: e = nv ? FLINT_SPLIT_ROWS(FLINT_MOE_NVFP4, 2) : FLINT_SPLIT_ROWS(FLINT_MOE_BF16, 2); break;
-        case 3: e = nv ? FLINT_SPLIT_ROWS(FLINT_MOE_NVFP4, 3) : FLINT_SPLIT_ROWS(FLINT_MOE_BF16, 3); break;
-        default: e = nv ? FLINT_SPLIT_ROWS(FLINT_MOE_NVFP4, 4) : FLINT_SPLIT_ROWS(FLINT_MOE_BF16, 4); break;
-      }
-      return e == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
-    }
-#undef FLINT_SPLIT_ROWS
-    switch (ntmax) {
-      case 1: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 1) : FLINT_SPLIT(FLINT_MOE_BF16, 1); break;
-      case 2: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 2) : FLINT_SPLIT(FLINT_MOE_BF16, 2); break;
-      case 3: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 3) : FLINT_SPLIT(FLINT_MOE_BF16, 3); break;
-      default: e = nv ? FLINT_SPLIT(FLINT_MOE_NVFP4, 4) : FLINT_SPLIT(FLINT_MOE_BF16, 4); break;
+#define FLINT_SPLIT(NT, SOLO)                                                                                 \
+  (nv ? (add ? launch_split<FLINT_MOE_NVFP4, NT, true, SOLO>(a, S, stream)                                    \
+             : launch_split<FLINT_MOE_NVFP4, NT, false, SOLO>(a, S, stream))                                  \
+      : (add ? launch_split<FLINT_MOE_BF16, NT, true, SOLO>(a, S, stream) : launch_split<FLINT_MOE_BF16, NT, false, SOLO>(a, S, stream)))
+    cudaError_t e;
+    switch (B == 1 ? 0 : ntmax) {
+      case 0: e = FLINT_SPLIT(1, true); break;
+      case 1: e = FLINT_SPLIT(1, false); break;
+      case 2: e = FLINT_SPLIT(2, false); break;
+      case 3: e = FLINT_SPLIT(3, false); break;
+      default: e = FLINT_SPLIT(4, false); break;
     }
 #undef FLINT_SPLIT
     return e == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
@@ -2856,7 +2906,8 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
       : (add ? launch_gemv<KERNEL<FLINT_MOE_BF16, NT, true>>(grid, block, smem, 0, stream, a)           \
              : launch_gemv<KERNEL<FLINT_MOE_BF16, NT, false>>(grid, block, smem, 0, stream, a)))
   const size_t rows_smem = gemv_rows_smem(K, B, fmt, nw, ntmax, &o1, &o2, &o3, &o4);
-  const int at_once = sm_count() * std::max<int>(1, std::min<int>(2, (int)(SMEM_LIMIT / (rows_smem + 1024))));
+  // blocks that run at once, sixteen warps an SM (widths of no multiple of 512 have four warps a block)
+  const int at_once = sm_count() * std::max<int>(1, std::min<int>(16 / nw, (int)(SMEM_LIMIT / (rows_smem + 1024))));
   if (N / 16 > at_once && rows_smem <= SMEM_LIMIT) {
     // more tiles than blocks that run at once: blocks that stage the rows once for several tiles
     const size_t smem = rows_smem;
