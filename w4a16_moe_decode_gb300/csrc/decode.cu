@@ -1899,7 +1899,10 @@ __global__ void __launch_bounds__(256) k_gemv_rows(GemvArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) red[((warp * NTMAX + nt) * 32 + lane) * 4 + e] = acc[0][nt][e] + acc[1][nt][e];
     ok = __syncthreads_and(ok);
-    if (!ok) break;  // a wait gave up: the tile and those behind it stay unwritten
+    if (!ok) {  // a wait gave up: the tile and those behind it stay unwritten
+      if (ADD && i == 0) pdl_wait();  // the call must not end before the adapters' kernel
+      break;
+    }
     const int next = tile + NB * (int)gridDim.x;
     if (lane == 0 && next < tiles) {
       fence_proxy_async();  // this warp's reads of the buffer come before the copy into it
