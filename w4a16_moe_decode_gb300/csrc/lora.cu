@@ -72,17 +72,15 @@ __device__ __forceinline__ uint32_t f2b2(float lo, float hi) {
 // Four values of h or g as bf16 halves: hi + lo carries 16 significant bits of the FP32 sum into the next product,
 // whose operands are bf16 on the tensor cores; a third half would carry 24, for half as many MMAs again and half as
 // much more of h in memory, and change an output by 2^-16 of a term where its own rounding changes it by 2^-8.
-// A finite value that rounds beyond bf16's largest keeps that as its hi and the rest in lo; an infinity has no rest.
-constexpr float BF16_MAX = 3.3895313892515355e38f;
+// hi stops at bf16's largest: of a finite value beyond it lo holds the rest, of an infinity lo is infinite.
+__device__ __forceinline__ uint32_t f2b2_finite(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
 __device__ __forceinline__ void halves(const float4 v, uint2& hi, uint2& lo) {
-  hi = make_uint2(f2b2(v.x, v.y), f2b2(v.z, v.w));
+  hi = make_uint2(f2b2_finite(v.x, v.y), f2b2_finite(v.z, v.w));
   lo = make_uint2(f2b2(v.x - bf16lo(hi.x), v.y - bf16hi(hi.x)), f2b2(v.z - bf16lo(hi.y), v.w - bf16hi(hi.y)));
-  if (fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))) > BF16_MAX) {  // rare
-    auto top = [](float t) { return fabsf(t) > BF16_MAX && fabsf(t) < INFINITY ? copysignf(BF16_MAX, t) : t; };
-    auto rest = [](float t, float h) { return fabsf(t) == INFINITY ? 0.f : t - h; };
-    hi = make_uint2(f2b2(top(v.x), top(v.y)), f2b2(top(v.z), top(v.w)));
-    lo = make_uint2(f2b2(rest(v.x, bf16lo(hi.x)), rest(v.y, bf16hi(hi.x))), f2b2(rest(v.z, bf16lo(hi.y)), rest(v.w, bf16hi(hi.y))));
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1101,13 +1099,14 @@ __device__ __forceinline__ void few_shrink(const FewArgs& a, const FewGroup& G, 
         mma_bf16(acc[nt], f1, xv.z, xv.w);
       }
     }
+    const bool upper = rt * 16 + 8 < a.R;  // places past the rank are zero also beside an infinite x
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float* o = red + ((size_t)wki * G.cols + nt * 8 + 2 * t4) * RP + rt * 16 + g;
       o[0] = acc[nt][0];
       o[RP] = acc[nt][1];
-      o[8] = acc[nt][2];
-      o[RP + 8] = acc[nt][3];
+      o[8] = upper ? acc[nt][2] : 0.f;
+      o[RP + 8] = upper ? acc[nt][3] : 0.f;
     }
   }
 }
@@ -1293,8 +1292,8 @@ __global__ void __launch_bounds__(FEW_THREADS, FEW_CTAS) k_lora_few(const FewArg
     for (int i = threadIdx.x * 4; i < cols * P.RP; i += FEW_THREADS * 4) {
       float4 u[FEW_S];
 #pragma unroll
-      for (int q = 0; q < FEW_S; ++q)  // (ranks past R are zero also beside an infinite x)
-        u[q] = i < vals && i % P.RP < a.R ? ld_dsmem_f4(dsmem_addr(local + i * 4, q)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < FEW_S; ++q)
+        u[q] = i < vals ? ld_dsmem_f4(dsmem_addr(local + i * 4, q)) : make_float4(0.f, 0.f, 0.f, 0.f);
       float4 v = u[0];
 #pragma unroll
       for (int q = 1; q < FEW_S; ++q) {
