@@ -1801,15 +1801,16 @@ __global__ void __launch_bounds__(256) k_gemv(GemvArgs a) {
 }
 
 // ===========================================================================
-// The same GEMV for more tiles than blocks that run at once (two an SM, or one
-// where the rows fill it: 131 KB for 32 of 2048). Staging a block's rows in
+// The same GEMV for more tiles than blocks that run at once (two an SM, four of
+// four warps, fewer where the rows fill it: 131 KB for 32 of 2048). Staging a block's rows in
 // fragment order takes as long as a tile's products with one row and longer with
 // more: so a block stages them once and works through the tiles blockIdx.x,
 // + gridDim.x, ..., the next tile's weights on their way meanwhile. A chain of
 // calls, us each, 8192 x 2048: 1 row 5.5 -> 4.5, 8 rows 7.5 -> 5.2, 16 rows
 // 11.4 -> 7.8, 32 rows 25.8 -> 12.6; with tiles for one round only there is
 // nothing to gain (4096 x 1024, 1 row: 2.5 -> 2.7; three blocks an SM: 8192 x 2048,
-// 8 rows 7.6). Each tile is summed up in the same order as by k_gemv.
+// 8 rows 7.6). BF16, 8192 x 2048: 1 row 9.8 -> 9.3, 8 rows 12.0 -> 10.0, 32 rows
+// 26.9 -> 16.5. Each tile is summed up in the same order as by k_gemv.
 // ===========================================================================
 // Tiles of weights in flight: two, or one of BF16 weights (65 KB a tile of 2048 columns).
 __host__ __device__ constexpr int GEMV_BUFS(int fmt) { return fmt == FLINT_MOE_NVFP4 ? 2 : 1; }
@@ -2133,7 +2134,8 @@ __global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
 // cluster barrier a tile is enough: CTA 0 arrives at a tile's barrier after it has
 // read the tile's before, and no CTA writes there earlier. Each tile is summed up
 // in the same order as by k_gemv_split. A chain of calls, us each, 2048 x 8192:
-// 1 row 6.3 -> 5.2, 8 rows 9.3 -> 6.3, 16 rows 14.4 -> 9.4, 32 rows 32 -> 15.7.
+// 1 row 6.3 -> 5.2, 8 rows 9.3 -> 6.3, 16 rows 14.4 -> 9.4, 32 rows 32 -> 15.7;
+// BF16 1 row 12.6 -> 10.7, 8 rows 14.4 -> 11.9, 32 rows 32.5 -> 19.0.
 // ===========================================================================
 struct GemvSplitRowsPlan {
   size_t xs_off, red_off, part_off, ss_off, inv_off, bar_off, total;
@@ -2359,8 +2361,8 @@ cudaError_t launch_gemv(dim3 grid, dim3 block, size_t smem, int cluster, cudaStr
 
 // Clusters of S blocks of a split GEMV kernel that run at once on the current device: asked once for each device, S
 // and blocks an SM's shared memory holds. The SMs of a cluster lie in one part of the chip, so these are fewer than
-// SMs x blocks / S (200 clusters of 3 in two rounds of 100, of which 97 ran at once: 17.8 us for 3200 x 6144 BF16
-// instead of 14.2).
+// SMs x blocks / S (3200 x 6144 BF16, 1 row, in two rounds of 100 clusters of 3, which did not all run at once: 17.8 us
+// instead of 14.1; NVFP4 4096 x 8192, 32 rows, in seven rounds of 37 of 4: 39.8 instead of 25.5).
 template <auto KERNEL>
 int clusters_at_once(int S, size_t smem) {
   static std::atomic<int> known[64][5][5];
@@ -2381,7 +2383,8 @@ int clusters_at_once(int S, size_t smem) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(KERNEL), &cfg) != cudaSuccess || n < 1) return std::max(1, sm_count() / S);
+  if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(KERNEL), &cfg) != cudaSuccess || n < 1)
+    return std::max(1, sm_count() / S);
   if (dev < 64) known[dev][S][per].store(n);
   return n;
 }

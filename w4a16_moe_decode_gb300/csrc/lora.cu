@@ -999,7 +999,7 @@ __global__ void __launch_bounds__(256) k_lora_dw_sum(const Args a) {
 // shuffling. A CTA's share of B is one run of memory: it comes into shared memory
 // in pieces of 256 rows with bulk copies that start before A is read (from L2 into
 // registers it took 10 of 21 us for 32 adapters of rank 64, 2048 x 8192). Bound by
-// latency for one adapter (3.6 us: 2048 x 2048, rank 16), by the adapters' bytes for
+// latency for one adapter (6.4 us alone and cold: 2048 x 2048, rank 16), by the adapters' bytes for
 // many (15.0 us alone and cold for those 32: 42 MB, 2.8 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int FEW = MAX_BATCH;
@@ -1031,7 +1031,7 @@ __host__ __device__ inline int few_wr(int R) { return few_rt(R) >= 8 ? 8 : few_r
 // bf16 halves. Together a third of an SM's where two pieces leave that.
 constexpr int FEW_PIECE = 256;  // rows of a piece: two tiles of 16 for each warp
 constexpr int FEW_MOST = 8;     // pieces at once
-constexpr int FEW_CTAS = 3;     // CTAs of an SM
+constexpr int FEW_CTAS = 3;     // CTAs of an SM at most (shared memory holds two of rank 64 with 16 rows, one of rank 128)
 constexpr size_t FEW_SMEM = 224 * 1024 / FEW_CTAS;
 __host__ __device__ inline int few_pieces(int N) { return ((N + 15) / 16 + FEW_S * 16 - 1) / (FEW_S * 16); }  // of a CTA's share, at most
 struct FewPlan {
@@ -1537,9 +1537,11 @@ bool run_plan(const Args& p, cudaStream_t stream) {
          launch(k_lora_plan, dim3(1), 1024, plan_smem(p.n, p.T), 0, stream, p);
 }
 
-// h (and with `grads` g) of every tile. CTAs of a tile's cluster: as many as run at once, two on an SM (4096 tokens of
-// 2048 x 2048, 49 tiles at most: 24.9 us a call with clusters of 4, 27.2 of 2, 27.7 of 8), and no more than a CTA has
-// k-blocks to take.
+// h (and with `grads` g) of every tile. CTAs of a tile's cluster: as many as run at once, two on an SM, if there were
+// all the tiles that T tokens of this pool can make (4096 tokens of 2048 x 2048, 49 tiles at most: 24.9 us a call with
+// clusters of 4, 27.2 of 2, 27.7 of 8), and no more than a CTA has k-blocks to take. The host does not know how many
+// adapters a batch uses: a large pool leaves room for tiles that are not there, and the clusters are smaller then
+// (777 tokens: 8 CTAs with a pool of 16, 2 with 100, 1 from 150 on).
 bool run_shrink(const Args& p, const Maps& m, bool grads, cudaStream_t stream) {
   const int kb = (std::min(p.K, grads ? p.N : p.K) + BK - 1) / BK, per = p.max_tiles * (grads ? 2 : 1);
   int S = 1;
