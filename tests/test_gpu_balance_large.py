@@ -6,7 +6,6 @@ positive terms (E / 32 + 5) u): dz as there. The loss adds up to 16 tokens' shar
 (a warp has at most T / 1000 of them here) and E of them times f - 1: relative to sum |f - 1| p of the tokens
 2 r + (E / 8 + 64 + T / 1000) u, and one rounding at the end.
 """
-import numpy as np
 import pytest
 import torch
 

@@ -11,6 +11,8 @@ from w4a16_moe_decode_gb300 import binding as fb
 from w4a16_moe_decode_gb300 import layers
 from w4a16_moe_decode_gb300.build import build
 
+from test_gpu_gemv_rows import test_adapters_beside_split_rows as adapters_beside
+
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 
@@ -45,6 +47,26 @@ def test_rows_equal_single_calls(N, K, fmt, B):
     fb.flint_gemv(part, few, K, fmt, x, B, alone, None, 1e-6, status)
     if fmt == fb.BF16:  # (an NVFP4 matrix' scale is its own largest value's)
         assert torch.equal(alone, y[:, :few])
+
+
+@pytest.mark.parametrize("B,K,N,R,n,fmt", [(1, 4096, 512, 16, 2, fb.NVFP4), (1, 8192, 1168, 40, 1, fb.NVFP4), (1, 8192, 272, 24, 3, fb.BF16),
+                                           (1, 6144, 2000, 8, 1, fb.BF16), (1, 6144, 3200, 16, 2, fb.BF16), (3, 1280, 9760, 16, 2, fb.NVFP4),
+                                           (6, 768, 9760, 24, 3, fb.BF16)])
+def test_adapters_beside_each_choice(B, K, N, R, n, fmt):
+    """One tile a cluster for one row, with room for the next call and without; blocks of four warps with several tiles."""
+    adapters_beside(B, K, N, R, n, fmt)
+
+
+@pytest.mark.parametrize("N,K,fmt", [(512, 4096, fb.NVFP4), (1168, 8192, fb.NVFP4), (2000, 6144, fb.BF16)])
+def test_one_normalised_row_has_the_bits_of_any_batch(N, K, fmt):
+    packed, _ = layers.synth_dense(N, K, 11, 0, fmt, DEV)
+    x, g = layers.synth_x(5, K, 11, 0, DEV), layers.synth_norm(K, 11, 0, DEV)
+    y = torch.full((5, N), 0x7FC0, dtype=torch.int16, device=DEV)
+    fb.flint_gemv(packed, N, K, fmt, x, 5, y, g, 1e-6)
+    for t in range(5):
+        one = torch.full((1, N), 0x7FC0, dtype=torch.int16, device=DEV)
+        fb.flint_gemv(packed, N, K, fmt, x[t:t + 1], 1, one, g, 1e-6)
+        assert torch.equal(one[0], y[t]), t
 
 
 FIRST = """

@@ -2,7 +2,6 @@
 chunks of several tiles for the weights' gradients. All rows and all gradients against the float64 definition, computed
 on the GPU, with the bounds of _finetune (derived there).
 """
-import numpy as np
 import pytest
 import torch
 
