@@ -64,6 +64,31 @@ flint_moe_status flint_gemv(const void* packed, int32_t N, int32_t K, int32_t we
                             int32_t B, uint16_t* y, const uint16_t* norm_weight, float eps, int32_t* dev_status,
                             cudaStream_t stream);
 
+/* Gate and up projections of a dense gated block in one call, for the first
+ * layers of the stack ("Day-0 Support for Flint on vLLM", section "Model
+ * architecture": dense MLPs), with the rounding point of the experts:
+ *   h[i] = bf16(silu(Gg sum_k cg[i][k] x[k]) * (Gu sum_k cu[i][k] x[k]))
+ * The block's output is flint_gemv of its down matrix on h; the two calls chain
+ * with programmatic dependent launch. Many tokens and gradients: flint_ffn.h. */
+
+/* Bytes of a packed pair of matrices [I][K]; 0 for an unsupported shape (I a
+ * multiple of 8 up to 2^19, K as for flint_gemv) or format. */
+size_t flint_gemv_glu_packed_bytes(int32_t I, int32_t K, int32_t weight_fmt);
+
+/* Lossless repack of gate and up [I][K] into one layout, the tiles of a MoE
+ * expert's gate and up matrices (eight rows of each to a tile). Otherwise as
+ * flint_gemv_pack. */
+flint_moe_status flint_gemv_glu_pack(const flint_gemv_src* gate, const flint_gemv_src* up, int32_t I, int32_t K,
+                                     int32_t weight_fmt, void* dst, size_t dst_bytes, int32_t* dev_status,
+                                     cudaStream_t stream);
+
+/* h bf16 [B][I] from x bf16 [B][K], 0 <= B <= 32; everything else as flint_gemv
+ * (norm_weight: the pre-norm of the block). A row's result does not depend on
+ * the other rows of the call. */
+flint_moe_status flint_gemv_glu(const void* packed, int32_t I, int32_t K, int32_t weight_fmt, const uint16_t* x,
+                                int32_t B, uint16_t* h, const uint16_t* norm_weight, float eps, int32_t* dev_status,
+                                cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

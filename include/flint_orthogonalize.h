@@ -1,0 +1,65 @@
+/* Orthogonalised updates of the matrices that are trained (adapters, routers,
+ * dense blocks) by Newton-Schulz steps: C ABI.
+ *
+ * For each matrix M [rows][cols] of a batch, with X X^T taken over the shorter
+ * side (X^T X and X on the left where rows > cols):
+ *   X = M / (|M| + eps)                        |M|: Frobenius norm
+ *   for each step (a, b, c):  S = X X^T,  X <- a X + (b S + c S S) X
+ *   out = bf16(scale X)
+ * The steps act on the singular values alone, s <- a s + b s^3 + c s^5: with
+ * (3.4445, -4.7750, 2.0315) five times, values of 0.01 to 1 end between 0.7
+ * and 1.2, the singular vectors as they were.
+ *
+ * Numerics: every sum is FP32 (the norm FP64). X is kept as the sum of two f16
+ * values (22 significant bits), because what its rounding adds to the weak
+ * directions the later steps amplify by up to a^steps; S and P = b S + c S S
+ * multiply X, where a relative error stays relative, and are single f16 values.
+ * The last step multiplies by X's larger part only. The result is within about
+ * 2^-9 of the exact one in the norm, as its rounding to bf16 is. Singular values
+ * must stay below 8 during the steps (S) and b s^2 + c s^4 below 255 (P), as any
+ * useful steps' do: beyond, results are not finite.
+ *
+ * Conventions as in flint_moe.h: device pointers, caller-owned memory, no
+ * allocation, asynchronous on `stream`, status codes. Matrices are contiguous,
+ * the batch's one behind the other; the first is 16-byte aligned, the workspace
+ * 256-byte aligned (FLINT_MOE_EALIGN). Inputs must be finite; a matrix of zeros
+ * gives zeros. A workspace needs no initialisation, holds nothing between
+ * calls, and must not be shared by calls in flight at the same time. Results do
+ * not depend on timing. A device-side wait that gave up sets
+ * FLINT_MOE_DEV_ERR_TIMEOUT in the workspace's status word
+ * (flint_moe_read_status), which each call clears.
+ */
+#ifndef FLINT_ORTHOGONALIZE_H_
+#define FLINT_ORTHOGONALIZE_H_
+
+#include "flint_moe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define FLINT_ORTHOGONALIZE_MAX_STEPS 16
+#define FLINT_ORTHOGONALIZE_MAX_SIDE 65536  /* the longer side; the shorter one is at most 16384 */
+#define FLINT_ORTHOGONALIZE_MAX_MATRICES 65535
+
+typedef enum { FLINT_ORTHOGONALIZE_F32 = 0, FLINT_ORTHOGONALIZE_BF16 = 1 } flint_orthogonalize_fmt;
+
+/* Bytes of the workspace for batches of n_mat matrices [rows][cols]; 0 if the
+ * arguments are not supported. */
+size_t flint_orthogonalize_workspace_bytes(int32_t n_mat, int32_t rows, int32_t cols);
+
+/* in: float32 or bf16 (in_fmt) [n_mat][rows][cols], out: bf16, the same shape;
+ * out may be in, and any other overlap of the two is allowed as well. coeffs:
+ * HOST memory, float [steps][3] = a, b, c of each step, finite, read before the
+ * call returns; 1 <= steps <= FLINT_ORTHOGONALIZE_MAX_STEPS. eps > 0 and scale
+ * finite. n_mat = 0 is a no-op; rows and cols from 1. The workspace must not
+ * overlap in or out (FLINT_MOE_EINVAL). */
+flint_moe_status flint_orthogonalize(const void* in, int32_t in_fmt, int32_t n_mat, int32_t rows, int32_t cols,
+                                     const float* coeffs, int32_t steps, float eps, float scale, uint16_t* out,
+                                     void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FLINT_ORTHOGONALIZE_H_ */

@@ -55,6 +55,10 @@ class flint_lora(ctypes.Structure):
                 ("a", c_void_p), ("b", c_void_p), ("scale", c_void_p)]
 
 
+class flint_ffn(ctypes.Structure):
+    _fields_ = [("hidden", c_int32), ("inter", c_int32), ("gate", c_void_p), ("up", c_void_p), ("down", c_void_p)]
+
+
 class flint_gemv_src(ctypes.Structure):
     _fields_ = [("codes", c_void_p), ("scales", c_void_p), ("global_", c_void_p), ("bf16", c_void_p)]
 
@@ -130,6 +134,22 @@ def lib() -> ctypes.CDLL:
             "flint_moe_balance_backward": (c_int32, [P(flint_moe_config), c_void_p, c_void_p, c_int32, c_void_p,
                                                      c_int32, ctypes.c_float, c_void_p, c_void_p, c_void_p, c_void_p,
                                                      c_void_p, c_void_p]),
+            "flint_gemv_glu_packed_bytes": (c_size_t, [c_int32, c_int32, c_int32]),
+            "flint_gemv_glu_pack": (c_int32, [P(flint_gemv_src), P(flint_gemv_src), c_int32, c_int32, c_int32, c_void_p,
+                                              c_size_t, c_void_p, c_void_p]),
+            "flint_gemv_glu": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
+                                         ctypes.c_float, c_void_p, c_void_p]),
+            "flint_ffn_init": (c_int32, [c_int32, c_int32, c_void_p, c_void_p, c_void_p, P(flint_ffn)]),
+            "flint_ffn_workspace_bytes": (c_size_t, [P(flint_ffn), c_int32]),
+            "flint_ffn_forward": (c_int32, [P(flint_ffn), c_void_p, c_int64, c_int32, c_void_p, c_int64, c_void_p,
+                                            c_void_p, c_void_p, c_size_t, c_void_p]),
+            "flint_ffn_backward_workspace_bytes": (c_size_t, [P(flint_ffn), c_int32]),
+            "flint_ffn_backward": (c_int32, [P(flint_ffn), c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_int64,
+                                             c_int32, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
+                                             c_size_t, c_void_p]),
+            "flint_orthogonalize_workspace_bytes": (c_size_t, [c_int32, c_int32, c_int32]),
+            "flint_orthogonalize": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_int32, P(ctypes.c_float), c_int32,
+                                              ctypes.c_float, ctypes.c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
             "flint_synth_stream_key": (ctypes.c_uint64, [ctypes.c_uint64, ctypes.c_uint32, ctypes.c_uint32,
                                                          ctypes.c_uint32]),
             "flint_synth_normal": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_uint64, c_size_t, ctypes.c_float, c_int32,
@@ -497,6 +517,111 @@ def flint_moe_balance_backward(cfg: flint_moe_config, logits, idx, T: int, seq_s
            lib().flint_moe_balance_backward(ctypes.byref(cfg), _ptr(logits), _ptr(idx), T, _ptr(seq_start), n_seq,
                                             alpha, _ptr(seq_counts), _ptr(seq_tokens), _ptr(dloss), _ptr(dw),
                                             _ptr(dlogits), _stream(stream)))
+
+
+def flint_gemv_glu_packed_bytes(I: int, K: int, fmt: int = NVFP4) -> int:
+    return lib().flint_gemv_glu_packed_bytes(I, K, fmt)
+
+
+def flint_gemv_glu_pack(gate: dict, up: dict, I: int, K: int, fmt, dst, dev_status=None, stream=None) -> None:
+    """gate, up: {codes, scales, global} (NVFP4) or {bf16} tensors of matrices [I][K]."""
+    g, u = _gemv_src(gate), _gemv_src(up)
+    _check("flint_gemv_glu_pack",
+           lib().flint_gemv_glu_pack(ctypes.byref(g), ctypes.byref(u), I, K, fmt, _ptr(dst),
+                                     dst.numel() * dst.element_size(), _ptr(dev_status), _stream(stream)))
+
+
+def flint_gemv_glu(packed, I: int, K: int, fmt, x, B: int, h, norm_weight=None, eps: float = 0.0, dev_status=None,
+                   stream=None) -> None:
+    """h = bf16(silu(gate x) * (up x)) for up to 32 rows (include/flint_gemv.h)."""
+    _check("flint_gemv_glu", lib().flint_gemv_glu(_ptr(packed), I, K, fmt, _ptr(x), B, _ptr(h), _ptr(norm_weight),
+                                                  float(eps), _ptr(dev_status), _stream(stream)))
+
+
+def _values(t, what: str, shape, bf16: bool = True) -> None:
+    """Refuses a tensor that does not hold these values side by side: bf16 (or their bits) or float32, of this shape."""
+    if t is None or isinstance(t, int):
+        return
+    import torch
+    kinds = (torch.bfloat16, torch.int16, torch.uint16) if bf16 else (torch.float32,)
+    if t.dtype not in kinds or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise FlintMoeError(f"{what} {t.dtype} {tuple(t.shape)} for {tuple(shape)}", EINVAL)
+
+
+def flint_ffn_init(gate, up, down, hidden=None, inter=None) -> flint_ffn:
+    """A dense gated block: gate, up [I][H], down [H][I] (bf16, contiguous). The shapes come from the tensors unless
+    given. The caller keeps the tensors alive."""
+    if hidden is None or inter is None:
+        if gate.dim() != 2:
+            raise FlintMoeError("gate", EINVAL)
+        inter, hidden = gate.shape
+    _values(gate, "gate", (inter, hidden))
+    _values(up, "up", (inter, hidden))
+    _values(down, "down", (hidden, inter))
+    ffn = flint_ffn()
+    _check("flint_ffn_init", lib().flint_ffn_init(hidden, inter, _ptr(gate), _ptr(up), _ptr(down), ctypes.byref(ffn)))
+    return ffn
+
+
+def flint_ffn_workspace_bytes(ffn: flint_ffn, max_tokens: int) -> int:
+    return lib().flint_ffn_workspace_bytes(ctypes.byref(ffn), max_tokens)
+
+
+def flint_ffn_forward(ffn: flint_ffn, x, T: int, y, workspace, gate_out=None, up_out=None, ldx=None, ldy=None,
+                      workspace_bytes=None, stream=None) -> None:
+    """y[t] = down(silu(gate x[t]) * (up x[t])) for T tokens (include/flint_ffn.h). gate_out, up_out [T][I] receive
+    what the gradients need."""
+    _values(gate_out, "gate_out", (T, ffn.inter))
+    _values(up_out, "up_out", (T, ffn.inter))
+    _check("flint_ffn_forward",
+           lib().flint_ffn_forward(ctypes.byref(ffn), _ptr(x), _ld(x, T, ffn.hidden, ldx), T, _ptr(y),
+                                   _ld(y, T, ffn.hidden, ldy), _ptr(gate_out), _ptr(up_out), _ptr(workspace),
+                                   _nbytes(workspace, workspace_bytes), _stream(stream)))
+
+
+def flint_ffn_backward_workspace_bytes(ffn: flint_ffn, max_tokens: int) -> int:
+    return lib().flint_ffn_backward_workspace_bytes(ctypes.byref(ffn), max_tokens)
+
+
+def flint_ffn_backward(ffn: flint_ffn, x, gate_act, up_act, dy, T: int, dx, dgate, dup, ddown, workspace, ldx=None,
+                       lddy=None, lddx=None, workspace_bytes=None, stream=None) -> None:
+    """Gradients of flint_ffn_forward from dy and the products it kept (include/flint_ffn.h). dx None skips it; dgate,
+    dup and ddown None skip the weights'."""
+    _values(gate_act, "gate_act", (T, ffn.inter))
+    _values(up_act, "up_act", (T, ffn.inter))
+    _values(dgate, "dgate", (ffn.inter, ffn.hidden))
+    _values(dup, "dup", (ffn.inter, ffn.hidden))
+    _values(ddown, "ddown", (ffn.hidden, ffn.inter))
+    _check("flint_ffn_backward",
+           lib().flint_ffn_backward(ctypes.byref(ffn), _ptr(x), _ld(x, T, ffn.hidden, ldx), _ptr(gate_act), _ptr(up_act),
+                                    _ptr(dy), _ld(dy, T, ffn.hidden, lddy), T, _ptr(dx), _ld(dx, T, ffn.hidden, lddx),
+                                    _ptr(dgate), _ptr(dup), _ptr(ddown), _ptr(workspace),
+                                    _nbytes(workspace, workspace_bytes), _stream(stream)))
+
+
+def flint_orthogonalize_workspace_bytes(n_mat: int, rows: int, cols: int) -> int:
+    return lib().flint_orthogonalize_workspace_bytes(n_mat, rows, cols)
+
+
+def flint_orthogonalize(m, out, coeffs, eps: float, workspace, scale: float = 1.0, workspace_bytes=None,
+                        stream=None) -> None:
+    """out = bf16(scale X) after the Newton-Schulz steps `coeffs` ((a, b, c) each) from X = m / (|m| + eps), for a matrix
+    or a batch of them, float32 or bf16, contiguous (include/flint_orthogonalize.h)."""
+    import torch
+    f32 = m.dtype == torch.float32
+    shape = tuple(m.shape)
+    if m.dim() not in (2, 3):
+        raise FlintMoeError("matrices", EINVAL)
+    _values(m, "matrices", shape, not f32)
+    _values(out, "out", shape)
+    n, rows, cols = shape if len(shape) == 3 else (1, *shape)
+    flat = [float(v) for step in coeffs for v in step]
+    if len(flat) != 3 * len(coeffs):
+        raise FlintMoeError("coefficients", EINVAL)
+    _check("flint_orthogonalize",
+           lib().flint_orthogonalize(_ptr(m), 0 if f32 else 1, n, rows, cols, (ctypes.c_float * len(flat))(*flat),
+                                     len(coeffs), float(eps), float(scale), _ptr(out), _ptr(workspace),
+                                     _nbytes(workspace, workspace_bytes), _stream(stream)))
 
 
 def flint_synth_stream_key(seed, layer, tensor, expert) -> int:

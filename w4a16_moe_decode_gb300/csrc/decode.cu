@@ -1722,8 +1722,21 @@ __device__ __forceinline__ void gemv_store(const GemvArgs& a, int t, int n, floa
   a.y[(size_t)t * a.N + n] = *reinterpret_cast<const uint16_t*>(&o);
 }
 
-template <int FMT, int NTMAX, bool ADD>
+// What a GEMV kernel makes of its sums: bf16 outputs, the same with FP32 rows added before the rounding, or, for tiles of
+// eight gate rows above the same eight up rows, h = bf16(silu(g) u) of their pairs.
+enum GemvEnd { GEMV_PLAIN, GEMV_ADD, GEMV_GLU };
+
+// Output r of a GLU tile, row t: the rounding points of the expert kernels (k_gateup).
+__device__ __forceinline__ void glu_store(const GemvArgs& a, int t, int tile, int r, float gv, float uv) {
+  const float ey = 1.0f + expf(-gv);
+  const float sv = ey < RCP_NR_MAX ? gv * rcp_nr(ey) : div_ieee(gv, ey);  // SiLU
+  const __nv_bfloat16 h = __float2bfloat16_rn(sv * uv);
+  a.y[(size_t)t * (a.N / 2) + tile * 8 + r] = *reinterpret_cast<const uint16_t*>(&h);
+}
+
+template <int FMT, int NTMAX, GemvEnd END>
 __global__ void __launch_bounds__(256) k_gemv(GemvArgs a) {
+  constexpr bool ADD = END == GEMV_ADD;
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -1791,6 +1804,20 @@ __global__ void __launch_bounds__(256) k_gemv(GemvArgs a) {
   // Output (row r of the tile, token t): token tile t / 8, fragment lane
   // 4 (r % 8) + (t % 8) / 2, element 2 (r / 8) + t % 2.
   const float G = FMT == FLINT_MOE_NVFP4 ? a.G[0] : 1.0f;
+  if constexpr (END == GEMV_GLU) {
+    const float Gu = FMT == FLINT_MOE_NVFP4 ? a.G[1] : 1.0f;
+    for (int p = threadIdx.x; p < 8 * a.B; p += blockDim.x) {
+      const int r = p & 7, t = p >> 3, nt = t >> 3, c = t & 7;
+      float gv = 0.f, uv = 0.f;
+      for (int w2 = 0; w2 < nw; ++w2) {
+        const float* q = red + ((w2 * NTMAX + nt) * 32 + 4 * r + (c >> 1)) * 4 + (c & 1);
+        gv += q[0];
+        uv += q[2];
+      }
+      glu_store(a, t, blockIdx.x, r, (gv * s_inv[t]) * G, (uv * s_inv[t]) * Gu);
+    }
+    return;
+  }
   for (int p = threadIdx.x; p < 16 * a.B; p += blockDim.x) {
     const int r = p & 15, t = p >> 4, nt = t >> 3, c = t & 7;
     const int ln = 4 * (r & 7) + (c >> 1), i = 2 * (r >> 3) + (c & 1);
@@ -1827,8 +1854,9 @@ __host__ __device__ inline size_t gemv_rows_smem(int K, int B, int fmt, int nw, 
   return o;
 }
 
-template <int FMT, int NTMAX, bool ADD>
+template <int FMT, int NTMAX, GemvEnd END>
 __global__ void __launch_bounds__(256) k_gemv_rows(GemvArgs a) {
+  constexpr bool ADD = END == GEMV_ADD;
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16, NB = GEMV_BUFS(FMT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -1861,7 +1889,7 @@ __global__ void __launch_bounds__(256) k_gemv_rows(GemvArgs a) {
   int tok[NTMAX];  // column g of token tile nt is token 8 nt + g (past B: a repeat of token B - 1)
 #pragma unroll
   for (int nt = 0; nt < NTMAX; ++nt) tok[nt] = min(nt * 8 + g, a.B - 1);
-  const float G = FMT == FLINT_MOE_NVFP4 ? a.G[0] : 1.0f;
+  const float G = FMT == FLINT_MOE_NVFP4 ? a.G[0] : 1.0f, Gu = END == GEMV_GLU && FMT == FLINT_MOE_NVFP4 ? a.G[1] : 1.0f;
   int i = 0;
   bool ok = true;
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++i) {
@@ -1912,12 +1940,25 @@ __global__ void __launch_bounds__(256) k_gemv_rows(GemvArgs a) {
     if (ADD && i == 0) pdl_wait();
     // Output (row r of the tile, token t): token tile t / 8, fragment lane
     // 4 (r % 8) + (t % 8) / 2, element 2 (r / 8) + t % 2.
-    for (int p = threadIdx.x; p < 16 * a.B; p += blockDim.x) {
-      const int r = p & 15, t = p >> 4, nt = t >> 3, c = t & 7;
-      const int ln = 4 * (r & 7) + (c >> 1), e = 2 * (r >> 3) + (c & 1);
-      float v = 0.f;
-      for (int w2 = 0; w2 < nw; ++w2) v += red[((w2 * NTMAX + nt) * 32 + ln) * 4 + e];
-      gemv_store<ADD>(a, t, tile * 16 + r, (v * s_inv[t]) * G);
+    if constexpr (END == GEMV_GLU) {
+      for (int p = threadIdx.x; p < 8 * a.B; p += blockDim.x) {
+        const int r = p & 7, t = p >> 3, nt = t >> 3, c = t & 7;
+        float gv = 0.f, uv = 0.f;
+        for (int w2 = 0; w2 < nw; ++w2) {
+          const float* q = red + ((w2 * NTMAX + nt) * 32 + 4 * r + (c >> 1)) * 4 + (c & 1);
+          gv += q[0];
+          uv += q[2];
+        }
+        glu_store(a, t, tile, r, (gv * s_inv[t]) * G, (uv * s_inv[t]) * Gu);
+      }
+    } else {
+      for (int p = threadIdx.x; p < 16 * a.B; p += blockDim.x) {
+        const int r = p & 15, t = p >> 4, nt = t >> 3, c = t & 7;
+        const int ln = 4 * (r & 7) + (c >> 1), e = 2 * (r >> 3) + (c & 1);
+        float v = 0.f;
+        for (int w2 = 0; w2 < nw; ++w2) v += red[((w2 * NTMAX + nt) * 32 + ln) * 4 + e];
+        gemv_store<ADD>(a, t, tile * 16 + r, (v * s_inv[t]) * G);
+      }
     }
     __syncthreads();  // the sums are read before the next tile's
   }
@@ -2033,10 +2074,24 @@ __device__ __forceinline__ void stage_slice(const GemvArgs& a, uint8_t* xs, floa
   }
 }
 
+// The end of a GLU tile of the split kernels: the cluster's partial sums [B][16] of gate and up rows, in rank order.
+__device__ __forceinline__ void glu_tile(const GemvArgs& a, const float* part, int tile, uint32_t S, float Gg, float Gu) {
+  for (int p = threadIdx.x; p < 8 * a.B; p += blockDim.x) {
+    const int r = p & 7, t = p >> 3;
+    float gv = 0.f, uv = 0.f;
+    for (uint32_t c = 0; c < S; ++c) {
+      gv += ld_dsmem_f32(part + t * 16 + r, c);
+      uv += ld_dsmem_f32(part + t * 16 + 8 + r, c);
+    }
+    glu_store(a, t, tile, r, gv * Gg, uv * Gu);
+  }
+}
+
 // SOLO (one token): at most 64 registers, four CTAs per SM, so that a call of up to 304 CTAs leaves room for all of the
 // next one's, which fetch their weights meanwhile (2432 x 4096: 4.7 -> 4.0 us per call at 80 registers and 64).
-template <int FMT, int NTMAX, bool ADD, bool SOLO = false>
+template <int FMT, int NTMAX, GemvEnd END, bool SOLO = false>
 __global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
+  constexpr bool ADD = END == GEMV_ADD;
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -2117,11 +2172,15 @@ __global__ void __launch_bounds__(256, SOLO ? 4 : 0) k_gemv_split(GemvArgs a) {
   cluster_sync();  // every CTA's partial sums are published
   if (rank == 0) {
     const float G = FMT == FLINT_MOE_NVFP4 ? a.G[0] : 1.0f;
-    for (int p = threadIdx.x; p < 16 * a.B; p += blockDim.x) {
-      float v2 = 0.f;
-      for (uint32_t r = 0; r < S; ++r) v2 += ld_dsmem_f32(part + p, r);  // rank order
-      const int rr = p & 15, t = p >> 4;
-      gemv_store<ADD>(a, t, blockIdx.x * 16 + rr, v2 * G);
+    if constexpr (END == GEMV_GLU) {
+      glu_tile(a, part, blockIdx.x, S, G, FMT == FLINT_MOE_NVFP4 ? a.G[1] : 1.0f);
+    } else {
+      for (int p = threadIdx.x; p < 16 * a.B; p += blockDim.x) {
+        float v2 = 0.f;
+        for (uint32_t r = 0; r < S; ++r) v2 += ld_dsmem_f32(part + p, r);  // rank order
+        const int rr = p & 15, t = p >> 4;
+        gemv_store<ADD>(a, t, blockIdx.x * 16 + rr, v2 * G);
+      }
     }
   }
   cluster_sync();  // the other CTAs' shared memory stays until CTA 0 has read it
@@ -2155,8 +2214,9 @@ __host__ __device__ inline GemvSplitRowsPlan gemv_split_rows_plan(int B, int fmt
   return p;
 }
 
-template <int FMT, int NTMAX, bool ADD>
+template <int FMT, int NTMAX, GemvEnd END>
 __global__ void __launch_bounds__(256, NTMAX <= 2 ? 2 : 1) k_gemv_split_rows(GemvArgs a) {
+  constexpr bool ADD = END == GEMV_ADD;
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16, NB = GEMV_BUFS(FMT);
   constexpr int nw = 8, KGW = (GEMV_SLICE / KG_COLS) / nw;  // k-groups per warp
@@ -2245,12 +2305,17 @@ __global__ void __launch_bounds__(256, NTMAX <= 2 ? 2 : 1) k_gemv_split_rows(Gem
     }
     if (ADD && i == 0) pdl_wait();
     cluster_sync();  // every CTA's partial sums of this tile are published, and red[] has been read
-    if (rank == 0)
-      for (int p = threadIdx.x; p < 16 * a.B; p += blockDim.x) {
-        float v = 0.f;
-        for (uint32_t r = 0; r < S; ++r) v += ld_dsmem_f32(part + p, r);  // rank order
-        gemv_store<ADD>(a, p >> 4, tile * 16 + (p & 15), v * G);
+    if (rank == 0) {
+      if constexpr (END == GEMV_GLU) {
+        glu_tile(a, part, tile, S, G, FMT == FLINT_MOE_NVFP4 ? a.G[1] : 1.0f);
+      } else {
+        for (int p = threadIdx.x; p < 16 * a.B; p += blockDim.x) {
+          float v = 0.f;
+          for (uint32_t r = 0; r < S; ++r) v += ld_dsmem_f32(part + p, r);  // rank order
+          gemv_store<ADD>(a, p >> 4, tile * 16 + (p & 15), v * G);
+        }
       }
+    }
   }
   cluster_sync();  // the other CTAs' shared memory stays until CTA 0 has read it
 }
@@ -2397,24 +2462,24 @@ int clusters_at_once(int S, size_t smem) {
 // for tiles that all run at once (2560 x 4096: 7.3 us, 9.0 with two tiles a cluster; 2432 x 6144, which do not, 12.4
 // and 10.3), and for three rounds or more of which over a fifth would be empty (3200 x 6144: 14.2 and 14.8;
 // 3648 x 8192: 19.2 and 19.9; 7296 x 4096 in full rounds: 17.4 and 16.3).
-template <int FMT, int NT, bool ADD, bool SOLO>
+template <int FMT, int NT, GemvEnd END, bool SOLO>
 cudaError_t launch_split(const GemvArgs& a, int S, cudaStream_t stream) {
   const dim3 block(256);
   const int tiles = a.N / 16;
   const size_t one = gemv_split_plan(a.B, FMT, 8, NT).total, rows = gemv_split_rows_plan(a.B, FMT, 8, NT).total;
   if (rows <= SMEM_LIMIT) {
-    const int most = clusters_at_once<k_gemv_split_rows<FMT, NT, ADD>>(S, rows), rounds = (tiles + most - 1) / most;
+    const int most = clusters_at_once<k_gemv_split_rows<FMT, NT, END>>(S, rows), rounds = (tiles + most - 1) / most;
     bool several = rounds > 1;
     if (several && (SOLO || FMT == FLINT_MOE_BF16)) {
-      const int ones = clusters_at_once<k_gemv_split<FMT, NT, ADD, SOLO>>(S, one);
+      const int ones = clusters_at_once<k_gemv_split<FMT, NT, END, SOLO>>(S, one);
       if (FMT == FLINT_MOE_NVFP4 ? 2 * tiles <= ones
                                  : ones > most && (tiles <= ones || (rounds > 2 && 4 * rounds * most > 5 * tiles)))
         several = false;
     }
     if (several)
-      return launch_gemv<k_gemv_split_rows<FMT, NT, ADD>>(dim3((tiles + rounds - 1) / rounds, S), block, rows, S, stream, a);
+      return launch_gemv<k_gemv_split_rows<FMT, NT, END>>(dim3((tiles + rounds - 1) / rounds, S), block, rows, S, stream, a);
   }
-  return launch_gemv<k_gemv_split<FMT, NT, ADD, SOLO>>(dim3(tiles, S), block, one, S, stream, a);
+  return launch_gemv<k_gemv_split<FMT, NT, END, SOLO>>(dim3(tiles, S), block, one, S, stream, a);
 }
 
 template <typename K>
@@ -2846,17 +2911,11 @@ extern "C" flint_moe_status flint_moe_debug_wait_timeout(int32_t* dev_status, cu
   return cudaGetLastError() == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
 }
 
-extern "C" flint_moe_status flint_gemv(const void* packed, int32_t N, int32_t K, int32_t fmt, const uint16_t* x,
-                                       int32_t B, uint16_t* y, const uint16_t* norm_weight, float eps,
-                                       int32_t* dev_status, cudaStream_t stream) {
-  return flint::gemv_impl(packed, N, K, fmt, x, B, y, norm_weight, eps, nullptr, nullptr, 0, dev_status, stream);
-}
-
-// flint_gemv, with FP32 rows to add before the rounding (GemvArgs).
-flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int32_t fmt, const uint16_t* x, int32_t B,
-                                  uint16_t* y, const uint16_t* norm_weight, float eps, const float* add32,
-                                  const int32_t* adapter, int32_t n_adapters, int32_t* dev_status,
-                                  cudaStream_t stream) {
+// flint_gemv, with FP32 rows to add before the rounding (GemvArgs), or as the gate and up rows of a GLU (N of them).
+static flint_moe_status gemv_any(const void* packed, int32_t N, int32_t K, int32_t fmt, const uint16_t* x, int32_t B,
+                                 uint16_t* y, const uint16_t* norm_weight, float eps, const float* add32,
+                                 const int32_t* adapter, int32_t n_adapters, bool glu, int32_t* dev_status,
+                                 cudaStream_t stream) {
   if (flint_gemv_packed_bytes(N, K, fmt) == 0) return FLINT_MOE_EUNSUPPORTED;
   if (B < 0 || B > MAX_BATCH || !(eps >= 0.f) || !(eps <= 3.0e38f)) return FLINT_MOE_EINVAL;
   if (B == 0) return FLINT_MOE_OK;
@@ -2876,7 +2935,8 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
   a.n_adapters = n_adapters;
   a.packed = static_cast<const uint8_t*>(packed);
   a.L = make_dense_layout(N, K, fmt);
-  a.G = reinterpret_cast<const float*>(a.packed + a.L.globals_off + 8);  // [G, G, G, 0]: the third word
+  // [G, G, G, 0], or [G of the gate, of the up rows, ...]
+  a.G = reinterpret_cast<const float*>(a.packed + a.L.globals_off);
   a.gamma = norm_weight;
   a.eps = eps;
   a.status = dev_status;
@@ -2884,11 +2944,12 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
   if (K > GEMV_SLICE) {  // split along K over a cluster of K / 2048 CTAs
     const int S = K / GEMV_SLICE;
     if (gemv_split_plan(B, fmt, 8, ntmax).total > SMEM_LIMIT) return FLINT_MOE_EUNSUPPORTED;
-    const bool nv = fmt == FLINT_MOE_NVFP4, add = add32 != nullptr;
-#define FLINT_SPLIT(NT, SOLO)                                                                                 \
-  (nv ? (add ? launch_split<FLINT_MOE_NVFP4, NT, true, SOLO>(a, S, stream)                                    \
-             : launch_split<FLINT_MOE_NVFP4, NT, false, SOLO>(a, S, stream))                                  \
-      : (add ? launch_split<FLINT_MOE_BF16, NT, true, SOLO>(a, S, stream) : launch_split<FLINT_MOE_BF16, NT, false, SOLO>(a, S, stream)))
+    const bool nv = fmt == FLINT_MOE_NVFP4;
+#define FLINT_SPLIT_AS(FMT, NT, SOLO)                                       \
+  (glu     ? launch_split<FMT, NT, GEMV_GLU, SOLO>(a, S, stream)            \
+   : add32 ? launch_split<FMT, NT, GEMV_ADD, SOLO>(a, S, stream)            \
+           : launch_split<FMT, NT, GEMV_PLAIN, SOLO>(a, S, stream))
+#define FLINT_SPLIT(NT, SOLO) (nv ? FLINT_SPLIT_AS(FLINT_MOE_NVFP4, NT, SOLO) : FLINT_SPLIT_AS(FLINT_MOE_BF16, NT, SOLO))
     cudaError_t e;
     switch (B == 1 ? 0 : ntmax) {
       case 0: e = FLINT_SPLIT(1, true); break;
@@ -2898,6 +2959,7 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
       default: e = FLINT_SPLIT(4, false); break;
     }
 #undef FLINT_SPLIT
+#undef FLINT_SPLIT_AS
     return e == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
   }
   size_t o1, o2, o3, o4, o5;
@@ -2905,12 +2967,12 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
   if ((size_t)B * (K * 2 + 16) > 160 * 1024 || one > SMEM_LIMIT) return FLINT_MOE_EUNSUPPORTED;
   const dim3 block(32 * nw);
   cudaError_t e;
-  const bool nv = fmt == FLINT_MOE_NVFP4, add = add32 != nullptr;
-#define FLINT_GEMV(KERNEL, NT)                                                                          \
-  (nv ? (add ? launch_gemv<KERNEL<FLINT_MOE_NVFP4, NT, true>>(grid, block, smem, 0, stream, a)          \
-             : launch_gemv<KERNEL<FLINT_MOE_NVFP4, NT, false>>(grid, block, smem, 0, stream, a))        \
-      : (add ? launch_gemv<KERNEL<FLINT_MOE_BF16, NT, true>>(grid, block, smem, 0, stream, a)           \
-             : launch_gemv<KERNEL<FLINT_MOE_BF16, NT, false>>(grid, block, smem, 0, stream, a)))
+  const bool nv = fmt == FLINT_MOE_NVFP4;
+#define FLINT_GEMV_AS(KERNEL, FMT, NT)                                                   \
+  (glu     ? launch_gemv<KERNEL<FMT, NT, GEMV_GLU>>(grid, block, smem, 0, stream, a)     \
+   : add32 ? launch_gemv<KERNEL<FMT, NT, GEMV_ADD>>(grid, block, smem, 0, stream, a)     \
+           : launch_gemv<KERNEL<FMT, NT, GEMV_PLAIN>>(grid, block, smem, 0, stream, a))
+#define FLINT_GEMV(KERNEL, NT) (nv ? FLINT_GEMV_AS(KERNEL, FLINT_MOE_NVFP4, NT) : FLINT_GEMV_AS(KERNEL, FLINT_MOE_BF16, NT))
   const size_t rows_smem = gemv_rows_smem(K, B, fmt, nw, ntmax, &o1, &o2, &o3, &o4);
   // blocks that run at once, sixteen warps an SM (widths of no multiple of 512 have four warps a block)
   const int at_once = sm_count() * std::max<int>(1, std::min<int>(16 / nw, (int)(SMEM_LIMIT / (rows_smem + 1024))));
@@ -2935,7 +2997,28 @@ flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int3
     }
   }
 #undef FLINT_GEMV
+#undef FLINT_GEMV_AS
   return e == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
+}
+
+extern "C" flint_moe_status flint_gemv(const void* packed, int32_t N, int32_t K, int32_t fmt, const uint16_t* x,
+                                       int32_t B, uint16_t* y, const uint16_t* norm_weight, float eps,
+                                       int32_t* dev_status, cudaStream_t stream) {
+  return gemv_any(packed, N, K, fmt, x, B, y, norm_weight, eps, nullptr, nullptr, 0, false, dev_status, stream);
+}
+
+extern "C" flint_moe_status flint_gemv_glu(const void* packed, int32_t I, int32_t K, int32_t fmt, const uint16_t* x,
+                                           int32_t B, uint16_t* h, const uint16_t* norm_weight, float eps,
+                                           int32_t* dev_status, cudaStream_t stream) {
+  if (flint_gemv_glu_packed_bytes(I, K, fmt) == 0) return FLINT_MOE_EUNSUPPORTED;
+  return gemv_any(packed, 2 * I, K, fmt, x, B, h, norm_weight, eps, nullptr, nullptr, 0, true, dev_status, stream);
+}
+
+flint_moe_status flint::gemv_impl(const void* packed, int32_t N, int32_t K, int32_t fmt, const uint16_t* x, int32_t B,
+                                  uint16_t* y, const uint16_t* norm_weight, float eps, const float* add32,
+                                  const int32_t* adapter, int32_t n_adapters, int32_t* dev_status,
+                                  cudaStream_t stream) {
+  return gemv_any(packed, N, K, fmt, x, B, y, norm_weight, eps, add32, adapter, n_adapters, false, dev_status, stream);
 }
 
 extern "C" flint_moe_status flint_moe_read_status(const void* ws, int32_t* host_status, cudaStream_t stream) {

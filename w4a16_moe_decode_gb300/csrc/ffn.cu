@@ -1,0 +1,319 @@
+// Dense gated feed-forward block on BF16 weights and its gradients (flint_ffn.h), as matrix products of gemm.cuh with
+// what stands between them in their epilogues.
+#include "flint_ffn.h"
+#include "gemm.cuh"
+
+namespace flint {
+namespace ffn {
+
+using namespace gemm;
+
+// sigmoid(g) and 1 - sigmoid(g), each to FP32's accuracy at both ends.
+__device__ __forceinline__ float2 sigmoid2(float g) {
+  const float t = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + t);
+  return g >= 0.f ? make_float2(r, t * r) : make_float2(t * r, r);
+}
+
+// bf16 rows [M][N] as they are.
+struct Store {
+  static constexpr int COLS = TILE;
+  static constexpr bool PAIR = false;
+  struct Args {};
+  static __device__ __forceinline__ void run(const Args&, const Maps& maps, const Tile& t, bool leader) {
+#pragma unroll
+    for (int c = 0; c < TILE; c += 32) {
+      uint32_t w[32];
+      tc_ld32_async(t.tmem + c, w);
+      tc_wait_ld();
+      uint8_t* box = t.sm + (c >> 6) * 2 * BOX;
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) stage8(box, t.row, (c & 63) + j, pack8_bf16(reinterpret_cast<const float*>(w) + j));
+    }
+    fence_proxy_async();
+    epi_sync();
+    if (leader) {
+      store_boxes(&maps.out[0], t, t.sm_addr, 2, t.n0);
+      bulk_commit();
+      bulk_wait_all();
+    }
+  }
+};
+
+// h = silu(g) u from 64 columns of g and the same 64 of u side by side in the accumulator, and g and u themselves.
+template <bool SAVE>
+struct Glu {
+  static constexpr int COLS = TILE / 2;
+  static constexpr bool PAIR = true;
+  struct Args {};
+  static __device__ __forceinline__ void run(const Args&, const Maps& maps, const Tile& t, bool leader) {
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+      uint32_t wg[32], wu[32];
+      tc_ld32_async(t.tmem + c, wg);
+      tc_ld32_async(t.tmem + 64 + c, wu);
+      tc_wait_ld();
+      const float* g = reinterpret_cast<const float*>(wg);
+      const float* u = reinterpret_cast<const float*>(wu);
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) {
+        float h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = __fdividef(g[j + e], 1.0f + __expf(-g[j + e])) * u[j + e];
+        stage8(t.sm, t.row, c + j, pack8_bf16(h));
+        if (SAVE) {
+          stage8(t.sm + 2 * BOX, t.row, c + j, pack8_bf16(g + j));
+          stage8(t.sm + 4 * BOX, t.row, c + j, pack8_bf16(u + j));
+        }
+      }
+    }
+    fence_proxy_async();
+    epi_sync();
+    if (leader) {
+      for (int o = 0; o < (SAVE ? 3 : 1); ++o) store_boxes(&maps.out[o], t, t.sm_addr + o * 2 * BOX, 1, t.n0);
+      bulk_commit();
+      bulk_wait_all();
+    }
+  }
+};
+
+// dg, du and h from dh and the kept g and u.
+struct DGlu {
+  static constexpr int COLS = TILE;
+  static constexpr bool PAIR = false;
+  struct Args {
+    const uint16_t* g;  // [M][N]
+    const uint16_t* u;
+  };
+  static __device__ __forceinline__ void run(const Args& a, const Maps& maps, const Tile& t, bool leader) {
+    const int row = t.m0 + t.row;
+    const size_t at = (size_t)row * t.N + t.n0;
+#pragma unroll 1
+    for (int c = 0; c < TILE; c += 32) {
+      uint32_t w[32];
+      tc_ld32_async(t.tmem + c, w);
+      uint4 gv[4], uv[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = row < t.M && t.n0 + c + 8 * j < t.N;
+        gv[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.g + at + c + 8 * j)) : make_uint4(0, 0, 0, 0);
+        uv[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.u + at + c + 8 * j)) : make_uint4(0, 0, 0, 0);
+      }
+      tc_wait_ld();
+      const float* d = reinterpret_cast<const float*>(w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float g[8], u[8], dg[8], du[8], h[8];
+        unpack8_bf16(gv[j], g);
+        unpack8_bf16(uv[j], u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 s = sigmoid2(g[e]);
+          const float dh = d[8 * j + e], act = g[e] * s.x;
+          dg[e] = dh * u[e] * (s.x * fmaf(g[e], s.y, 1.0f));
+          du[e] = dh * act;
+          h[e] = act * u[e];
+        }
+        uint8_t* box = t.sm + (c >> 6) * 2 * BOX;
+        stage8(box, t.row, (c & 63) + 8 * j, pack8_bf16(dg));
+        stage8(box + 4 * BOX, t.row, (c & 63) + 8 * j, pack8_bf16(du));
+        stage8(box + 8 * BOX, t.row, (c & 63) + 8 * j, pack8_bf16(h));
+      }
+    }
+    fence_proxy_async();
+    epi_sync();
+    if (leader) {
+      for (int o = 0; o < 3; ++o) store_boxes(&maps.out[o], t, t.sm_addr + o * 4 * BOX, 2, t.n0);
+      bulk_commit();
+      bulk_wait_all();
+    }
+  }
+};
+static_assert(12 * BOX <= STAGES * STAGE, "dg, du and h of a tile");
+
+}  // namespace ffn
+}  // namespace flint
+
+using namespace flint;
+using namespace flint::ffn;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+flint_moe_status check_shape(const flint_ffn* f) {
+  if (!f) return FLINT_MOE_EINVAL;
+  if (f->hidden < 8 || f->hidden > 65536 || f->hidden % 8 || f->inter < 8 || f->inter > 65536 || f->inter % 8)
+    return FLINT_MOE_EUNSUPPORTED;
+  return FLINT_MOE_OK;
+}
+
+flint_moe_status check_weights(const flint_ffn* f) {
+  const flint_moe_status st = check_shape(f);
+  if (st != FLINT_MOE_OK) return st;
+  if (!f->gate || !f->up || !f->down) return FLINT_MOE_EINVAL;
+  if (!aligned(f->gate, 16) || !aligned(f->up, 16) || !aligned(f->down, 16)) return FLINT_MOE_EALIGN;
+  return FLINT_MOE_OK;
+}
+
+constexpr int64_t LD_MOST = 0x7fffffff;
+bool bad_ld(int64_t ld, int cols) { return ld < cols || ld > LD_MOST; }
+
+// Memory that a call reads or writes; what it writes overlaps nothing else.
+struct Span {
+  const void* p;
+  size_t bytes;
+  bool written;
+};
+size_t rows_bytes(int64_t ld, int cols, int rows) { return rows == 0 ? 0 : 2 * ((size_t)(rows - 1) * ld + cols); }
+bool overlap(const Span* s, int n) {
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < i; ++j) {
+      if (!(s[i].written || s[j].written) || !s[i].p || !s[j].p || !s[i].bytes || !s[j].bytes) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p), b = reinterpret_cast<uintptr_t>(s[j].p);
+      if (a < b + s[j].bytes && b < a + s[i].bytes) return true;
+    }
+  return false;
+}
+
+constexpr int H_STATUS = 1;  // word of the header that flint_moe_read_status reads
+
+struct WsPlan {
+  size_t h, dg, du, total;
+};
+WsPlan ws_plan(const flint_ffn* f, int T, bool grad) {
+  WsPlan w = {};
+  const size_t act = ws_align((size_t)2 * T * f->inter);
+  size_t o = 256;
+  w.h = o;
+  o += act;
+  if (grad) {
+    w.dg = o;
+    o += act;
+    w.du = o;
+    o += act;
+  }
+  w.total = o;
+  return w;
+}
+
+size_t ws_bytes(const flint_ffn* f, int32_t T, bool grad) {
+  if (check_shape(f) != FLINT_MOE_OK || T < 1 || T > FLINT_FFN_MAX_TOKENS) return 0;
+  return ws_plan(f, T, grad).total;
+}
+
+int blocks_of(int k) { return (k + BK - 1) / BK; }
+
+}  // namespace
+
+extern "C" flint_moe_status flint_ffn_init(int32_t hidden, int32_t inter, const uint16_t* gate, const uint16_t* up,
+                                           const uint16_t* down, flint_ffn* out) {
+  if (!out) return FLINT_MOE_EINVAL;
+  const flint_ffn f = {hidden, inter, gate, up, down};
+  const flint_moe_status st = check_weights(&f);
+  if (st == FLINT_MOE_OK) *out = f;
+  return st;
+}
+
+extern "C" size_t flint_ffn_workspace_bytes(const flint_ffn* f, int32_t T) { return ws_bytes(f, T, false); }
+extern "C" size_t flint_ffn_backward_workspace_bytes(const flint_ffn* f, int32_t T) { return ws_bytes(f, T, true); }
+
+extern "C" flint_moe_status flint_ffn_forward(const flint_ffn* f, const uint16_t* x, int64_t ldx, int32_t T, uint16_t* y,
+                                              int64_t ldy, uint16_t* g, uint16_t* u, void* ws, size_t ws_size,
+                                              cudaStream_t stream) {
+  flint_moe_status st = check_weights(f);
+  if (st != FLINT_MOE_OK) return st;
+  if (T < 0 || T > FLINT_FFN_MAX_TOKENS) return FLINT_MOE_EINVAL;
+  if (T == 0) return FLINT_MOE_OK;
+  const int H = f->hidden, I = f->inter;
+  if (!x || !y || !ws || !g != !u || bad_ld(ldx, H) || bad_ld(ldy, H)) return FLINT_MOE_EINVAL;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(g, 16) || !aligned(u, 16) || !aligned(ws, 256) || ldx % 8 || ldy % 8)
+    return FLINT_MOE_EALIGN;
+  const WsPlan w = ws_plan(f, T, false);
+  if (ws_size < w.total) return FLINT_MOE_EINVAL;
+  const size_t wb = (size_t)2 * H * I, act = (size_t)2 * T * I;
+  const Span spans[] = {{f->gate, wb, false}, {f->up, wb, false}, {f->down, wb, false}, {x, rows_bytes(ldx, H, T), false},
+                        {y, rows_bytes(ldy, H, T), true}, {g, act, true}, {u, act, true}, {ws, w.total, true}};
+  if (overlap(spans, 8)) return FLINT_MOE_EINVAL;
+  uint8_t* wsp = static_cast<uint8_t*>(ws);
+  uint16_t* h = reinterpret_cast<uint16_t*>(wsp + w.h);
+  int* status = reinterpret_cast<int*>(ws) + H_STATUS;
+  Maps m1, m2;
+  bool ok = map_matrix(&m1.a[0], x, H, T, ldx) && map_matrix(&m1.b[0], f->gate, H, I, H) && map_matrix(&m1.b[1], f->up, H, I, H) &&
+            map_matrix(&m1.out[0], h, I, T, I) && map_matrix(&m2.b[0], f->down, I, H, I) && map_matrix(&m2.out[0], y, H, T, ldy);
+  if (ok && g) ok = map_matrix(&m1.out[1], g, I, T, I) && map_matrix(&m1.out[2], u, I, T, I);
+  if (!ok) return FLINT_MOE_ECUDA;
+  m1.a[1] = m1.a[0];
+  if (!g) m1.out[1] = m1.out[2] = m1.out[0];
+  m2.a[0] = m2.a[1] = m1.out[0];
+  m2.b[1] = m2.b[0];
+  m2.out[1] = m2.out[2] = m2.out[0];
+  const Args a1 = {T, I, {blocks_of(H), 0}, status, 1}, a2 = {T, H, {blocks_of(I), 0}, status, 0};
+  ok = g ? run<Glu<true>, false, false, false>(a1, m1, {}, 1, stream) : run<Glu<false>, false, false, false>(a1, m1, {}, 1, stream);
+  ok = ok && run<Store, false, false, false>(a2, m2, {}, 1, stream);
+  return ok ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
+}
+
+extern "C" flint_moe_status flint_ffn_backward(const flint_ffn* f, const uint16_t* x, int64_t ldx, const uint16_t* g,
+                                               const uint16_t* u, const uint16_t* dy, int64_t lddy, int32_t T, uint16_t* dx,
+                                               int64_t lddx, uint16_t* dgate, uint16_t* dup, uint16_t* ddown, void* ws,
+                                               size_t ws_size, cudaStream_t stream) {
+  flint_moe_status st = check_weights(f);
+  if (st != FLINT_MOE_OK) return st;
+  if (T < 0 || T > FLINT_FFN_MAX_TOKENS || !dgate != !dup || !dgate != !ddown) return FLINT_MOE_EINVAL;
+  const int H = f->hidden, I = f->inter;
+  const size_t wb = (size_t)2 * H * I, act = (size_t)2 * T * I;
+  if (!aligned(dgate, 16) || !aligned(dup, 16) || !aligned(ddown, 16)) return FLINT_MOE_EALIGN;
+  if (T > 0) {
+    if (!x || !g || !u || !dy || !ws || bad_ld(ldx, H) || bad_ld(lddy, H) || (dx && bad_ld(lddx, H))) return FLINT_MOE_EINVAL;
+    if (!aligned(x, 16) || !aligned(g, 16) || !aligned(u, 16) || !aligned(dy, 16) || !aligned(dx, 16) || !aligned(ws, 256) ||
+        ldx % 8 || lddy % 8 || (dx && lddx % 8))
+      return FLINT_MOE_EALIGN;
+  }
+  const WsPlan w = ws_plan(f, T, true);
+  if (T > 0 && ws_size < w.total) return FLINT_MOE_EINVAL;
+  const Span spans[] = {{f->gate, wb, false}, {f->up, wb, false}, {f->down, wb, false}, {x, rows_bytes(ldx, H, T), false},
+                        {g, act, false}, {u, act, false}, {dy, rows_bytes(lddy, H, T), false},
+                        {dx, dx ? rows_bytes(lddx, H, T) : 0, true}, {dgate, wb, true}, {dup, wb, true}, {ddown, wb, true},
+                        {ws, T > 0 ? w.total : 0, true}};
+  if (overlap(spans, 12)) return FLINT_MOE_EINVAL;
+  if (T == 0) {
+    if (dgate)
+      for (uint16_t* p : {dgate, dup, ddown})
+        if (cudaMemsetAsync(p, 0, wb, stream) != cudaSuccess) return FLINT_MOE_ECUDA;
+    return FLINT_MOE_OK;
+  }
+  if (!dx && !dgate) return FLINT_MOE_OK;
+  uint8_t* wsp = static_cast<uint8_t*>(ws);
+  uint16_t *h = reinterpret_cast<uint16_t*>(wsp + w.h), *dg = reinterpret_cast<uint16_t*>(wsp + w.dg),
+           *du = reinterpret_cast<uint16_t*>(wsp + w.du);
+  int* status = reinterpret_cast<int*>(ws) + H_STATUS;
+  CUtensorMap mx, mdy, mg, mu, mgate, mup, mdown, mh;
+  if (!map_matrix(&mx, x, H, T, ldx) || !map_matrix(&mdy, dy, H, T, lddy) || !map_matrix(&mg, dg, I, T, I) ||
+      !map_matrix(&mu, du, I, T, I) || !map_matrix(&mgate, f->gate, H, I, H) || !map_matrix(&mup, f->up, H, I, H) ||
+      !map_matrix(&mdown, f->down, I, H, I) || !map_matrix(&mh, h, I, T, I))
+    return FLINT_MOE_ECUDA;
+  auto maps = [](const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
+                 const CUtensorMap& o0, const CUtensorMap& o1, const CUtensorMap& o2) {
+    Maps m;
+    m.a[0] = a0, m.a[1] = a1, m.b[0] = b0, m.b[1] = b1, m.out[0] = o0, m.out[1] = o1, m.out[2] = o2;
+    return m;
+  };
+  if (!run<DGlu, false, true, false>({T, I, {blocks_of(H), 0}, status, 1}, maps(mdy, mdy, mdown, mdown, mg, mu, mh), {g, u}, 1, stream))
+    return FLINT_MOE_ECUDA;
+  if (dx) {
+    CUtensorMap o;
+    if (!map_matrix(&o, dx, H, T, lddx) ||
+        !run<Store, false, true, false>({T, H, {blocks_of(I), blocks_of(I)}, status, 0}, maps(mg, mu, mgate, mup, o, o, o), {}, 1, stream))
+      return FLINT_MOE_ECUDA;
+  }
+  if (dgate) {
+    CUtensorMap og, ou, od;
+    if (!map_matrix(&og, dgate, H, I, H) || !map_matrix(&ou, dup, H, I, H) || !map_matrix(&od, ddown, I, H, I)) return FLINT_MOE_ECUDA;
+    const int kb = blocks_of(T);
+    if (!run<Store, true, true, false>({I, H, {kb, 0}, status, 0}, maps(mg, mg, mx, mx, og, og, og), {}, 1, stream) ||
+        !run<Store, true, true, false>({I, H, {kb, 0}, status, 0}, maps(mu, mu, mx, mx, ou, ou, ou), {}, 1, stream) ||
+        !run<Store, true, true, false>({H, I, {kb, 0}, status, 0}, maps(mdy, mdy, mh, mh, od, od, od), {}, 1, stream))
+      return FLINT_MOE_ECUDA;
+  }
+  return FLINT_MOE_OK;
+}

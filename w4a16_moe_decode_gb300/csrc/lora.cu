@@ -271,15 +271,6 @@ __host__ __device__ inline size_t shrink_smem(int R, bool grads) {
 }
 __host__ __device__ inline uint32_t tmem_cols(int c) { return c <= 32 ? 32 : c <= 64 ? 64 : c <= 128 ? 128 : 256; }
 
-__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(cols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
-}
-
 __global__ void __launch_bounds__(SHR_THREADS, 2) k_lora_shrink(const Args a, const __grid_constant__ Maps maps) {
   extern __shared__ uint8_t dsmem[];
   __shared__ uint64_t full[SHR_MOST], empty[SHR_MOST], acc_full;

@@ -1,0 +1,405 @@
+// Orthogonalised updates by Newton-Schulz steps (flint_orthogonalize.h), as matrix products of gemm.cuh.
+//
+// Scaled values: X is kept times 2^10 as hi + lo (f16), S times 2^10 and P times 2^8 (f16).
+#include <cmath>
+
+#include "flint_orthogonalize.h"
+#include "gemm.cuh"
+
+namespace flint {
+namespace ortho {
+
+using namespace gemm;
+
+constexpr float X_SCALE = 1024.f, S_SCALE = 1024.f, P_SCALE = 256.f;
+
+__device__ __forceinline__ uint32_t f2h2(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float2 h2f2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ uint4 pack8_f16(const float* v) {
+  return make_uint4(f2h2(v[0], v[1]), f2h2(v[2], v[3]), f2h2(v[4], v[5]), f2h2(v[6], v[7]));
+}
+__device__ __forceinline__ void unpack8_f16(const uint4 u, float* v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = h2f2(w[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+// hi + lo = v to 22 bits.
+__device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
+  float h[8], l[8];
+  hi = pack8_f16(v);
+  unpack8_f16(hi, h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) l[i] = v[i] - h[i];
+  lo = pack8_f16(l);
+}
+
+// ---------------------------------------------------------------------------
+// X = M / (|M| + eps): the sums of squares in FP64 (a block's partial sum each),
+// then hi and lo. Eight values share a power of two, so that squares neither
+// overflow nor vanish.
+// ---------------------------------------------------------------------------
+struct Start {
+  const void* in;
+  int bf16, n, rows, cols, pitch, parts;
+  float eps;
+  double* part;  // [n][parts]
+  uint16_t *hi, *lo;
+  int* status;
+};
+
+constexpr int START_THREADS = 256;
+
+__device__ __forceinline__ float load1(const Start& a, size_t i) {
+  return a.bf16 ? bf16lo(static_cast<const uint16_t*>(a.in)[i]) : static_cast<const float*>(a.in)[i];
+}
+// Values i .. i + 7 (i a multiple of 8 from an aligned start).
+__device__ __forceinline__ void load8(const Start& a, size_t i, float* v) {
+  if (a.bf16) {
+    unpack8_bf16(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.in) + i), v);
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.in) + i);
+    const float4 x = p[0], y = p[1];
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+  }
+}
+
+__global__ void __launch_bounds__(START_THREADS) k_ortho_norm(const Start a) {
+  __shared__ double s_sum[START_THREADS / 32];
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0 && blockIdx.x + blockIdx.y == 0) *a.status = 0;
+  const size_t all = (size_t)a.rows * a.cols, first = blockIdx.y * all;
+  const bool vec = all % 8 == 0;
+  double sum = 0.0;
+  for (size_t i = 8 * ((size_t)blockIdx.x * START_THREADS + threadIdx.x); i < all; i += (size_t)gridDim.x * START_THREADS * 8) {
+    float v[8];
+    if (vec) {
+      load8(a, first + i, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = i + e < all ? load1(a, first + i + e) : 0.f;
+    }
+    float mx = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
+    const int ex = min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);
+    const float sc = exp2i(-ex);
+    float q = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q = fmaf(v[e] * sc, v[e] * sc, q);
+    sum = fma((double)q, __longlong_as_double((long long)(1023 + 2 * ex) << 52), sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < START_THREADS / 32; ++w) sum += s_sum[w];
+    a.part[(size_t)blockIdx.y * a.parts + blockIdx.x] = sum;
+  }
+}
+
+__global__ void __launch_bounds__(START_THREADS) k_ortho_split(const Start a) {
+  __shared__ float s_scale[2];
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x < 32) {
+    double sum = 0.0;
+    for (int p = threadIdx.x; p < a.parts; p += 32) sum += __ldcg(a.part + (size_t)blockIdx.y * a.parts + p);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (threadIdx.x == 0) {  // 1 / (|M| + eps) as two FP32 factors, since a large norm's is below FP32's normals
+      const double d = sqrt(sum) + (double)a.eps;
+      const int half = ((int)(__double_as_longlong(d) >> 52) - 1023) / 2;
+      s_scale[0] = exp2i(-half);
+      s_scale[1] = (float)(X_SCALE / (d * __longlong_as_double((long long)(1023 - half) << 52)));
+    }
+  }
+  __syncthreads();
+  const float s0 = s_scale[0], s1 = s_scale[1];
+  const size_t all = (size_t)a.rows * a.cols, first = blockIdx.y * all, out = (size_t)blockIdx.y * a.rows * a.pitch;
+  const size_t step = (size_t)gridDim.x * START_THREADS;
+  if (a.pitch == a.cols) {  // rows of whole pieces of eight
+    for (size_t i = 8 * ((size_t)blockIdx.x * START_THREADS + threadIdx.x); i < all; i += 8 * step) {
+      float v[8];
+      load8(a, first + i, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (v[e] * s0) * s1;
+      uint4 hi, lo;
+      split8(v, hi, lo);
+      *reinterpret_cast<uint4*>(a.hi + out + i) = hi;
+      *reinterpret_cast<uint4*>(a.lo + out + i) = lo;
+    }
+  } else {
+    for (size_t i = (size_t)blockIdx.x * START_THREADS + threadIdx.x; i < all; i += step) {
+      const size_t r = i / a.cols, at = out + r * a.pitch + (i - r * a.cols);
+      const float v = (load1(a, first + i) * s0) * s1;
+      const __half h = __float2half_rn(v);
+      a.hi[at] = *reinterpret_cast<const uint16_t*>(&h);
+      const __half l = __float2half_rn(v - __half2float(h));
+      a.lo[at] = *reinterpret_cast<const uint16_t*>(&l);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Epilogues: S, P = b S + c S S, X <- a X + P X.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void finish(const Maps& maps, const Tile& t, bool leader, int outs) {
+  fence_proxy_async();
+  epi_sync();
+  if (leader) {
+    for (int o = 0; o < outs; ++o) store_boxes(&maps.out[o], t, t.sm_addr + o * 4 * BOX, 2, t.n0);
+    bulk_commit();
+    bulk_wait_all();
+  }
+}
+
+struct Gram {
+  static constexpr int COLS = TILE;
+  static constexpr bool PAIR = false;
+  struct Args {};
+  static __device__ __forceinline__ void run(const Args&, const Maps& maps, const Tile& t, bool leader) {
+#pragma unroll
+    for (int c = 0; c < TILE; c += 32) {
+      uint32_t w[32];
+      tc_ld32_async(t.tmem + c, w);
+      tc_wait_ld();
+      float* v = reinterpret_cast<float*>(w);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] *= S_SCALE / (X_SCALE * X_SCALE);
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) stage8(t.sm + (c >> 6) * 2 * BOX, t.row, (c & 63) + j, pack8_f16(v + j));
+    }
+    finish(maps, t, leader, 1);
+  }
+};
+
+struct Poly {
+  static constexpr int COLS = TILE;
+  static constexpr bool PAIR = false;
+  struct Args {
+    const uint16_t* s;  // [batch][M][pitch]
+    int pitch;
+    float b, c;
+  };
+  static __device__ __forceinline__ void run(const Args& a, const Maps& maps, const Tile& t, bool leader) {
+    const int row = t.m0 + t.row;
+    const uint16_t* s = a.s + ((size_t)t.z * t.M + row) * a.pitch + t.n0;
+    const float fs = a.b * (P_SCALE / S_SCALE), fq = a.c * (P_SCALE / (S_SCALE * S_SCALE));
+#pragma unroll 1
+    for (int c = 0; c < TILE; c += 32) {
+      uint32_t w[32];
+      tc_ld32_async(t.tmem + c, w);
+      uint4 sv[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        sv[j] = row < t.M && t.n0 + c + 8 * j < t.N ? __ldcg(reinterpret_cast<const uint4*>(s + c + 8 * j)) : make_uint4(0, 0, 0, 0);
+      tc_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v[8];
+        unpack8_f16(sv[j], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(fs, v[e], fq * __uint_as_float(w[8 * j + e]));
+        stage8(t.sm + (c >> 6) * 2 * BOX, t.row, (c & 63) + 8 * j, pack8_f16(v));
+      }
+    }
+    finish(maps, t, leader, 1);
+  }
+};
+
+template <bool LAST>
+struct Update {
+  static constexpr int COLS = TILE;
+  static constexpr bool PAIR = false;
+  struct Args {
+    const uint16_t *hi, *lo;  // [batch][M][pitch]
+    int pitch;
+    float a, scale;
+    uint16_t* out;  // LAST: [batch][M][N], 16-byte pieces of a row not aligned where N % 8
+  };
+  static __device__ __forceinline__ void run(const Args& a, const Maps& maps, const Tile& t, bool leader) {
+    const int row = t.m0 + t.row;
+    const size_t at = ((size_t)t.z * t.M + row) * a.pitch + t.n0;
+    constexpr float fp = 1.0f / P_SCALE;  // P X comes scaled by both
+#pragma unroll 1
+    for (int c = 0; c < TILE; c += 32) {
+      uint32_t w[32];
+      tc_ld32_async(t.tmem + c, w);
+      uint4 hv[4], lv[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = row < t.M && t.n0 + c + 8 * j < t.N;
+        hv[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.hi + at + c + 8 * j)) : make_uint4(0, 0, 0, 0);
+        lv[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.lo + at + c + 8 * j)) : make_uint4(0, 0, 0, 0);
+      }
+      tc_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float h[8], l[8], v[8];
+        unpack8_f16(hv[j], h);
+        unpack8_f16(lv[j], l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(fp, __uint_as_float(w[8 * j + e]), a.a * (h[e] + l[e]));
+        uint8_t* box = t.sm + (c >> 6) * 2 * BOX;
+        if (LAST) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= a.scale;
+          stage8(box, t.row, (c & 63) + 8 * j, pack8_bf16(v));
+        } else {
+          uint4 hi, lo;
+          split8(v, hi, lo);
+          stage8(box, t.row, (c & 63) + 8 * j, hi);
+          stage8(box + 4 * BOX, t.row, (c & 63) + 8 * j, lo);
+        }
+      }
+    }
+    if (!LAST) {
+      finish(maps, t, leader, 2);
+    } else if (t.N % 8 == 0) {
+      finish(maps, t, leader, 1);
+    } else {  // rows that TMA cannot reach: a warp writes its own 32 rows, a row's neighbours by neighbouring lanes
+      __syncwarp();
+      const int lane = t.row & 31, r0 = t.row - lane;
+      for (int r = r0; r < r0 + 32 && t.m0 + r < t.M; ++r) {
+        uint16_t* dst = a.out + ((size_t)t.z * t.M + t.m0 + r) * t.N + t.n0;
+        for (int c = lane; c < TILE && t.n0 + c < t.N; c += 32)
+          dst[c] = *reinterpret_cast<const uint16_t*>(t.sm + (c >> 6) * 2 * BOX + sw128_off(r, c & 63));
+      }
+    }
+  }
+};
+
+}  // namespace ortho
+}  // namespace flint
+
+using namespace flint;
+using namespace flint::ortho;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+constexpr int H_STATUS = 1;  // word of the header that flint_moe_read_status reads
+
+bool supported(int n, int rows, int cols) {
+  return n >= 0 && n <= FLINT_ORTHOGONALIZE_MAX_MATRICES && rows >= 1 && cols >= 1 &&
+         std::max(rows, cols) <= FLINT_ORTHOGONALIZE_MAX_SIDE && std::min(rows, cols) <= 16384;
+}
+
+// Blocks of a matrix in the first two kernels: eight pieces of eight values a thread, 128 at most.
+int parts_of(int rows, int cols) {
+  const int64_t per = 8 * 8 * START_THREADS;
+  return (int)std::min<int64_t>(128, ((int64_t)rows * cols + per - 1) / per);
+}
+
+struct WsPlan {
+  int m, pitch, mpitch, parts;
+  size_t part, x[2][2], s, p, total;  // x: of even and odd steps, hi and lo
+};
+WsPlan ws_plan(int n, int rows, int cols) {
+  WsPlan w = {};
+  w.m = std::min(rows, cols);
+  w.pitch = (cols + 7) & ~7;
+  w.mpitch = (w.m + 7) & ~7;
+  w.parts = parts_of(rows, cols);
+  const size_t xb = ws_align((size_t)2 * n * rows * w.pitch), mb = ws_align((size_t)2 * n * w.m * w.mpitch);
+  size_t o = 256;
+  w.part = o;
+  o += ws_align(sizeof(double) * n * w.parts);
+  for (int i = 0; i < 4; ++i) {
+    w.x[i >> 1][i & 1] = o;
+    o += xb;
+  }
+  w.s = o;
+  o += mb;
+  w.p = o;
+  o += mb;
+  w.total = o;
+  return w;
+}
+
+bool overlaps(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + nq && b < a + np;
+}
+
+}  // namespace
+
+extern "C" size_t flint_orthogonalize_workspace_bytes(int32_t n, int32_t rows, int32_t cols) {
+  return n > 0 && supported(n, rows, cols) ? ws_plan(n, rows, cols).total : 0;
+}
+
+extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int32_t n, int32_t rows, int32_t cols,
+                                                const float* coeffs, int32_t steps, float eps, float scale, uint16_t* out,
+                                                void* ws, size_t ws_size, cudaStream_t stream) {
+  if (!supported(n, rows, cols) || (fmt != FLINT_ORTHOGONALIZE_F32 && fmt != FLINT_ORTHOGONALIZE_BF16))
+    return FLINT_MOE_EUNSUPPORTED;
+  if (!coeffs || steps < 1 || steps > FLINT_ORTHOGONALIZE_MAX_STEPS || !(eps > 0.f) || !std::isfinite(eps) || !std::isfinite(scale))
+    return FLINT_MOE_EINVAL;
+  for (int i = 0; i < 3 * steps; ++i)
+    if (!std::isfinite(coeffs[i])) return FLINT_MOE_EINVAL;
+  if (n == 0) return FLINT_MOE_OK;
+  if (!in || !out || !ws) return FLINT_MOE_EINVAL;
+  if (!aligned(in, 16) || !aligned(out, 16) || !aligned(ws, 256)) return FLINT_MOE_EALIGN;
+  const WsPlan w = ws_plan(n, rows, cols);
+  const size_t values = (size_t)n * rows * cols;
+  if (ws_size < w.total || overlaps(ws, w.total, in, values * (fmt == FLINT_ORTHOGONALIZE_F32 ? 4 : 2)) ||
+      overlaps(ws, w.total, out, values * 2))
+    return FLINT_MOE_EINVAL;
+  uint8_t* wsp = static_cast<uint8_t*>(ws);
+  int* status = reinterpret_cast<int*>(ws) + H_STATUS;
+  auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(wsp + o); };
+  const bool tall = rows > cols;
+  const int m = w.m;
+  CUtensorMap x[2][2], s, p, o;
+  bool ok = true;
+  for (int i = 0; i < 4; ++i)
+    ok = ok && map_matrix(&x[i >> 1][i & 1], at(w.x[i >> 1][i & 1]), cols, rows, w.pitch, n, (int64_t)rows * w.pitch);
+  ok = ok && map_matrix(&s, at(w.s), m, m, w.mpitch, n, (int64_t)m * w.mpitch) &&
+       map_matrix(&p, at(w.p), m, m, w.mpitch, n, (int64_t)m * w.mpitch);
+  o = p;
+  if (cols % 8 == 0) ok = ok && map_matrix(&o, out, cols, rows, cols, n, (int64_t)rows * cols);
+  if (!ok) return FLINT_MOE_ECUDA;
+  auto maps = [](const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
+                 const CUtensorMap& o0, const CUtensorMap& o1) {
+    Maps mm;
+    mm.a[0] = a0, mm.a[1] = a1, mm.b[0] = b0, mm.b[1] = b1, mm.out[0] = o0, mm.out[1] = o1, mm.out[2] = o1;
+    return mm;
+  };
+  const Start st = {in, fmt == FLINT_ORTHOGONALIZE_BF16, n, rows, cols, w.pitch, w.parts, eps,
+                    reinterpret_cast<double*>(wsp + w.part), at(w.x[0][0]), at(w.x[0][1]), status};
+  const dim3 grid((unsigned)w.parts, (unsigned)n);
+  if (!launch<k_ortho_norm>(grid, START_THREADS, 0, stream, st) || !launch<k_ortho_split>(grid, START_THREADS, 0, stream, st))
+    return FLINT_MOE_ECUDA;
+  const int kx = ((tall ? rows : cols) + BK - 1) / BK, km = (m + BK - 1) / BK;
+  for (int i = 0; i < steps; ++i) {
+    const CUtensorMap *xi = x[i & 1], *xo = x[(i + 1) & 1];
+    const float *cf = coeffs + 3 * i;
+    const bool last = i + 1 == steps;
+    const Args gram = {m, m, {kx, 0}, status, 0}, poly = {m, m, {km, 0}, status, 0};
+    const Args upd = {rows, cols, {km, last ? 0 : km}, status, 0};
+    const Maps mg = maps(xi[0], xi[0], xi[0], xi[0], s, s), mp = maps(s, s, s, s, p, p);
+    ok = tall ? run<Gram, true, true, true>(gram, mg, {}, n, stream) : run<Gram, false, false, true>(gram, mg, {}, n, stream);
+    ok = ok && run<Poly, false, false, true>(poly, mp, {at(w.s), w.mpitch, cf[1], cf[2]}, n, stream);
+    const uint16_t *hi = at(w.x[i & 1][0]), *lo = at(w.x[i & 1][1]);
+    if (last) {
+      const Update<true>::Args e = {hi, lo, w.pitch, cf[0], scale / X_SCALE, out};
+      ok = ok && (tall ? run<Update<true>, false, false, true>(upd, maps(xi[0], xi[1], p, p, o, o), e, n, stream)
+                       : run<Update<true>, false, true, true>(upd, maps(p, p, xi[0], xi[1], o, o), e, n, stream));
+    } else {
+      const Update<false>::Args e = {hi, lo, w.pitch, cf[0], 1.0f, nullptr};
+      ok = ok && (tall ? run<Update<false>, false, false, true>(upd, maps(xi[0], xi[1], p, p, xo[0], xo[1]), e, n, stream)
+                       : run<Update<false>, false, true, true>(upd, maps(p, p, xi[0], xi[1], xo[0], xo[1]), e, n, stream));
+    }
+    if (!ok) return FLINT_MOE_ECUDA;
+  }
+  return FLINT_MOE_OK;
+}

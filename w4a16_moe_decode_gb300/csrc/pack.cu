@@ -564,3 +564,61 @@ extern "C" flint_moe_status flint_gemv_unpack_debug(const void* packed, int32_t 
   }
   return cudaGetLastError() == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
 }
+
+// ---------------------------------------------------------------------------
+// Gate and up matrices of a dense block for flint_gemv_glu: one expert's gate/up
+// tiles without down tiles, 16 rows a tile like a dense matrix of 2 I rows.
+// ---------------------------------------------------------------------------
+static Layout glu_layout(int I, int K, int fmt) {
+  Layout L = make_dense_layout(2 * I, K, fmt);
+  L.gu_tile = L.dn_tile;
+  L.gu_bytes = L.expert_bytes;
+  return L;
+}
+static bool glu_shape_ok(int32_t I, int32_t K, int32_t fmt) {
+  return I >= 8 && I % 8 == 0 && I <= (1 << 19) && gemv_shape_ok(2 * I, K, fmt);
+}
+
+extern "C" size_t flint_gemv_glu_packed_bytes(int32_t I, int32_t K, int32_t fmt) {
+  return glu_shape_ok(I, K, fmt) ? (size_t)glu_layout(I, K, fmt).total : 0;
+}
+
+extern "C" flint_moe_status flint_gemv_glu_pack(const flint_gemv_src* gate, const flint_gemv_src* up, int32_t I, int32_t K,
+                                                int32_t fmt, void* dst, size_t dst_bytes, int32_t* dev_status,
+                                                cudaStream_t stream) {
+  if (!glu_shape_ok(I, K, fmt)) return FLINT_MOE_EUNSUPPORTED;
+  if (!gate || !up || !dst) return FLINT_MOE_EINVAL;
+  const Layout L = glu_layout(I, K, fmt);
+  if (dst_bytes < (size_t)L.total) return FLINT_MOE_EINVAL;
+  if (!aligned16(dst)) return FLINT_MOE_EALIGN;
+  PackArgs a = {};
+  GlobalsArgs ga;
+  const flint_gemv_src* src[2] = {gate, up};
+  for (int m = 0; m < 2; ++m) {
+    if (fmt == FLINT_MOE_NVFP4) {
+      if (!src[m]->codes || !src[m]->scales || !src[m]->global_) return FLINT_MOE_EINVAL;
+      if (!aligned16(src[m]->scales)) return FLINT_MOE_EALIGN;
+    } else {
+      if (!src[m]->bf16) return FLINT_MOE_EINVAL;
+      if (!aligned16(src[m]->bf16)) return FLINT_MOE_EALIGN;
+    }
+    a.codes[m] = src[m]->codes;
+    a.scales[m] = src[m]->scales;
+    a.bf16[m] = reinterpret_cast<const uint8_t*>(src[m]->bf16);
+    ga.g[m] = src[m]->global_;
+  }
+  a.L = L;
+  a.H = K;
+  a.I = I;
+  a.fmt = fmt;
+  a.n_words = L.globals_off / 4;
+  a.dst = static_cast<uint8_t*>(dst);
+  a.status = dev_status;
+  k_pack<<<grid_for(a.n_words, 256), 256, 0, stream>>>(a);
+  ga.g[2] = ga.g[1];
+  ga.dst = reinterpret_cast<float*>(static_cast<uint8_t*>(dst) + L.globals_off);
+  ga.n = 1;
+  ga.fmt = fmt;
+  k_pack_globals<<<1, 32, 0, stream>>>(ga);
+  return cudaGetLastError() == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
+}
