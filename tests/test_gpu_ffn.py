@@ -57,9 +57,11 @@ def backward(p, dx=True, weights=True):
 # 64 or 16, long and short ones, widths that end inside a tile
 SHAPES = [(1, 8, 8), (1, 2048, 512), (2, 72, 200), (7, 256, 64), (31, 136, 1032), (33, 1000, 40), (64, 64, 64), (127, 64, 136), (128, 256, 128),
           (129, 128, 264), (200, 520, 328), (256, 256, 256), (257, 264, 520), (513, 200, 776), (1000, 328, 72), (2050, 136, 96)]
+# enough tiles of 256 x 256 for pairs of CTAs: in the first products, the last ones, and the weights' gradients
+LARGE = [(1300, 72, 1704), (2600, 2040, 72), (40, 2040, 2600), (4100, 1288, 1160)]
 
 
-@pytest.mark.parametrize("T,H,I", SHAPES)
+@pytest.mark.parametrize("T,H,I", SHAPES + LARGE)
 def test_forward(T, H, I):
     p = Block(T, H, I, 7 * T + H).to(DEV)
     refs, tols = p.expect_forward()
@@ -71,7 +73,7 @@ def test_forward(T, H, I):
     assert torch.equal(forward(p)[0], got[0])  # the same bits again
 
 
-@pytest.mark.parametrize("T,H,I", SHAPES)
+@pytest.mark.parametrize("T,H,I", SHAPES + LARGE)
 def test_backward(T, H, I):
     p = Block(T, H, I, 5 * T + I).to(DEV)
     refs, tols = p.expect_backward()

@@ -46,7 +46,8 @@ def compare(m, got, **kw):
 
 # wide, square and tall; one row or column; sides that are no multiple of 8, 64 or 128; several matrices
 SHAPES = [(1, 1, 1), (3, 1, 70), (2, 70, 1), (2, 8, 264), (5, 16, 1000), (3, 33, 129), (2, 129, 33), (1, 127, 128), (2, 128, 128), (1, 129, 130),
-          (1, 64, 2048), (2, 2048, 64), (1, 256, 1024), (1, 300, 260), (1, 257, 515), (1, 640, 384), (3, 131, 131), (40, 24, 40)]
+          (1, 64, 2048), (2, 2048, 64), (1, 256, 1024), (1, 300, 260), (1, 257, 515), (1, 640, 384), (3, 131, 131), (40, 24, 40),
+          (90, 40, 100), (80, 100, 40), (21, 300, 260), (20, 260, 515), (20, 520, 257)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

@@ -16,119 +16,108 @@ __device__ __forceinline__ float2 sigmoid2(float g) {
 
 // bf16 rows [M][N] as they are.
 struct Store {
-  static constexpr int COLS = TILE;
   static constexpr bool PAIR = false;
   struct Args {};
-  static __device__ __forceinline__ void run(const Args&, const Maps& maps, const Tile& t, bool leader) {
-#pragma unroll
-    for (int c = 0; c < TILE; c += 32) {
+  template <typename C, typename Release>
+  static __device__ __forceinline__ void run(const Args&, const Maps& maps, Part& t, Release release) {
+#pragma unroll 1
+    for (int c = 128 * t.group; c < 128 * t.group + 128; c += 32) {
       uint32_t w[32];
       tc_ld32_async(t.tmem + c, w);
       tc_wait_ld();
-      uint8_t* box = t.sm + (c >> 6) * 2 * BOX;
-#pragma unroll
-      for (int j = 0; j < 32; j += 8) stage8(box, t.row, (c & 63) + j, pack8_bf16(reinterpret_cast<const float*>(w) + j));
-    }
-    fence_proxy_async();
-    epi_sync();
-    if (leader) {
-      store_boxes(&maps.out[0], t, t.sm_addr, 2, t.n0);
-      bulk_commit();
-      bulk_wait_all();
+      if ((c & 127) == 96) release();
+      const float* v = reinterpret_cast<const float*>(w);
+      const uint4 o[4] = {pack8_bf16(v), pack8_bf16(v + 8), pack8_bf16(v + 16), pack8_bf16(v + 24)};
+      t.put(&maps.out[0], t.n0 + c, o);
     }
   }
 };
 
-// h = silu(g) u from 64 columns of g and the same 64 of u side by side in the accumulator, and g and u themselves.
+// h = silu(g) u from half of the accumulator's columns of g and the same columns of u behind them, and g and u themselves.
 template <bool SAVE>
 struct Glu {
-  static constexpr int COLS = TILE / 2;
   static constexpr bool PAIR = true;
   struct Args {};
-  static __device__ __forceinline__ void run(const Args&, const Maps& maps, const Tile& t, bool leader) {
-#pragma unroll
-    for (int c = 0; c < 64; c += 32) {
+  template <typename C, typename Release>
+  static __device__ __forceinline__ void run(const Args&, const Maps& maps, Part& t, Release release) {
+#pragma unroll 1
+    for (int c = 64 * t.group; c < 64 * t.group + 64; c += 32) {
       uint32_t wg[32], wu[32];
       tc_ld32_async(t.tmem + c, wg);
-      tc_ld32_async(t.tmem + 64 + c, wu);
+      tc_ld32_async(t.tmem + C::TN / 2 + c, wu);
       tc_wait_ld();
+      if (c & 32) release();
       const float* g = reinterpret_cast<const float*>(wg);
       const float* u = reinterpret_cast<const float*>(wu);
+      uint4 o[4];
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) {
+      for (int j = 0; j < 4; ++j) {
         float h[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = __fdividef(g[j + e], 1.0f + __expf(-g[j + e])) * u[j + e];
-        stage8(t.sm, t.row, c + j, pack8_bf16(h));
-        if (SAVE) {
-          stage8(t.sm + 2 * BOX, t.row, c + j, pack8_bf16(g + j));
-          stage8(t.sm + 4 * BOX, t.row, c + j, pack8_bf16(u + j));
-        }
+        for (int i = 0; i < 8; ++i) h[i] = __fdividef(g[8 * j + i], 1.0f + __expf(-g[8 * j + i])) * u[8 * j + i];
+        o[j] = pack8_bf16(h);
       }
-    }
-    fence_proxy_async();
-    epi_sync();
-    if (leader) {
-      for (int o = 0; o < (SAVE ? 3 : 1); ++o) store_boxes(&maps.out[o], t, t.sm_addr + o * 2 * BOX, 1, t.n0);
-      bulk_commit();
-      bulk_wait_all();
+      t.put(&maps.out[0], t.n0 + c, o);
+      if (SAVE) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = pack8_bf16(g + 8 * j);
+        t.put(&maps.out[1], t.n0 + c, o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = pack8_bf16(u + 8 * j);
+        t.put(&maps.out[2], t.n0 + c, o);
+      }
     }
   }
 };
 
 // dg, du and h from dh and the kept g and u.
 struct DGlu {
-  static constexpr int COLS = TILE;
   static constexpr bool PAIR = false;
   struct Args {
     const uint16_t* g;  // [M][N]
     const uint16_t* u;
   };
-  static __device__ __forceinline__ void run(const Args& a, const Maps& maps, const Tile& t, bool leader) {
-    const int row = t.m0 + t.row;
-    const size_t at = (size_t)row * t.N + t.n0;
+  template <typename C, typename Release>
+  static __device__ __forceinline__ void run(const Args& a, const Maps& maps, Part& t, Release release) {
+    const size_t at = (size_t)t.row * t.N + t.n0;
 #pragma unroll 1
-    for (int c = 0; c < TILE; c += 32) {
+    for (int c = 128 * t.group; c < 128 * t.group + 128; c += 32) {
       uint32_t w[32];
       tc_ld32_async(t.tmem + c, w);
       uint4 gv[4], uv[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bool in = row < t.M && t.n0 + c + 8 * j < t.N;
+        const bool in = t.row < t.M && t.n0 + c + 8 * j < t.N;
         gv[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.g + at + c + 8 * j)) : make_uint4(0, 0, 0, 0);
         uv[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.u + at + c + 8 * j)) : make_uint4(0, 0, 0, 0);
       }
       tc_wait_ld();
+      if ((c & 127) == 96) release();
       const float* d = reinterpret_cast<const float*>(w);
+      uint4 og[4], ou[4], oh[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float g[8], u[8], dg[8], du[8], h[8];
         unpack8_bf16(gv[j], g);
         unpack8_bf16(uv[j], u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 s = sigmoid2(g[e]);
-          const float dh = d[8 * j + e], act = g[e] * s.x;
-          dg[e] = dh * u[e] * (s.x * fmaf(g[e], s.y, 1.0f));
-          du[e] = dh * act;
-          h[e] = act * u[e];
+        for (int i = 0; i < 8; ++i) {
+          const float2 s = sigmoid2(g[i]);
+          const float dh = d[8 * j + i], act = g[i] * s.x;
+          dg[i] = dh * u[i] * (s.x * fmaf(g[i], s.y, 1.0f));
+          du[i] = dh * act;
+          h[i] = act * u[i];
         }
-        uint8_t* box = t.sm + (c >> 6) * 2 * BOX;
-        stage8(box, t.row, (c & 63) + 8 * j, pack8_bf16(dg));
-        stage8(box + 4 * BOX, t.row, (c & 63) + 8 * j, pack8_bf16(du));
-        stage8(box + 8 * BOX, t.row, (c & 63) + 8 * j, pack8_bf16(h));
+        og[j] = pack8_bf16(dg);
+        ou[j] = pack8_bf16(du);
+        oh[j] = pack8_bf16(h);
       }
-    }
-    fence_proxy_async();
-    epi_sync();
-    if (leader) {
-      for (int o = 0; o < 3; ++o) store_boxes(&maps.out[o], t, t.sm_addr + o * 4 * BOX, 2, t.n0);
-      bulk_commit();
-      bulk_wait_all();
+      t.put(&maps.out[0], t.n0 + c, og);
+      t.put(&maps.out[1], t.n0 + c, ou);
+      t.put(&maps.out[2], t.n0 + c, oh);
     }
   }
 };
-static_assert(12 * BOX <= STAGES * STAGE, "dg, du and h of a tile");
 
 }  // namespace ffn
 }  // namespace flint
@@ -238,18 +227,19 @@ extern "C" flint_moe_status flint_ffn_forward(const flint_ffn* f, const uint16_t
   uint16_t* h = reinterpret_cast<uint16_t*>(wsp + w.h);
   int* status = reinterpret_cast<int*>(ws) + H_STATUS;
   Maps m1, m2;
-  bool ok = map_matrix(&m1.a[0], x, H, T, ldx) && map_matrix(&m1.b[0], f->gate, H, I, H) && map_matrix(&m1.b[1], f->up, H, I, H) &&
-            map_matrix(&m1.out[0], h, I, T, I) && map_matrix(&m2.b[0], f->down, I, H, I) && map_matrix(&m2.out[0], y, H, T, ldy);
-  if (ok && g) ok = map_matrix(&m1.out[1], g, I, T, I) && map_matrix(&m1.out[2], u, I, T, I);
+  bool ok = map_in(&m1.a[0], x, H, T, ldx) && map_in(&m1.b[0], f->gate, H, I, H) && map_in(&m1.b[1], f->up, H, I, H) &&
+            map_out(&m1.out[0], h, I, T, I) && map_in(&m2.a[0], h, I, T, I) && map_in(&m2.b[0], f->down, I, H, I) &&
+            map_out(&m2.out[0], y, H, T, ldy);
+  if (ok && g) ok = map_out(&m1.out[1], g, I, T, I) && map_out(&m1.out[2], u, I, T, I);
   if (!ok) return FLINT_MOE_ECUDA;
   m1.a[1] = m1.a[0];
   if (!g) m1.out[1] = m1.out[2] = m1.out[0];
-  m2.a[0] = m2.a[1] = m1.out[0];
+  m2.a[1] = m2.a[0];
   m2.b[1] = m2.b[0];
   m2.out[1] = m2.out[2] = m2.out[0];
-  const Args a1 = {T, I, {blocks_of(H), 0}, status, 1}, a2 = {T, H, {blocks_of(I), 0}, status, 0};
-  ok = g ? run<Glu<true>, false, false, false>(a1, m1, {}, 1, stream) : run<Glu<false>, false, false, false>(a1, m1, {}, 1, stream);
-  ok = ok && run<Store, false, false, false>(a2, m2, {}, 1, stream);
+  const Args a1 = {{T, I, {blocks_of(H), 0}, 0, 0}, 0, 1, status, 1}, a2 = {{T, H, {blocks_of(I), 0}, 0, 0}, 0, 1, status, 0};
+  ok = g ? run<Glu<true>>(a1, m1, {}, stream) : run<Glu<false>>(a1, m1, {}, stream);
+  ok = ok && run<Store>(a2, m2, {}, stream);
   return ok ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
 }
 
@@ -287,10 +277,10 @@ extern "C" flint_moe_status flint_ffn_backward(const flint_ffn* f, const uint16_
   uint16_t *h = reinterpret_cast<uint16_t*>(wsp + w.h), *dg = reinterpret_cast<uint16_t*>(wsp + w.dg),
            *du = reinterpret_cast<uint16_t*>(wsp + w.du);
   int* status = reinterpret_cast<int*>(ws) + H_STATUS;
-  CUtensorMap mx, mdy, mg, mu, mgate, mup, mdown, mh;
-  if (!map_matrix(&mx, x, H, T, ldx) || !map_matrix(&mdy, dy, H, T, lddy) || !map_matrix(&mg, dg, I, T, I) ||
-      !map_matrix(&mu, du, I, T, I) || !map_matrix(&mgate, f->gate, H, I, H) || !map_matrix(&mup, f->up, H, I, H) ||
-      !map_matrix(&mdown, f->down, I, H, I) || !map_matrix(&mh, h, I, T, I))
+  CUtensorMap mx, mdy, mg, mu, mgate, mup, mdown, mh, og, ou, oh;
+  if (!map_in(&mx, x, H, T, ldx) || !map_in(&mdy, dy, H, T, lddy) || !map_in(&mg, dg, I, T, I) || !map_in(&mu, du, I, T, I) ||
+      !map_in(&mgate, f->gate, H, I, H) || !map_in(&mup, f->up, H, I, H) || !map_in(&mdown, f->down, I, H, I) ||
+      !map_in(&mh, h, I, T, I) || !map_out(&og, dg, I, T, I) || !map_out(&ou, du, I, T, I) || !map_out(&oh, h, I, T, I))
     return FLINT_MOE_ECUDA;
   auto maps = [](const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
                  const CUtensorMap& o0, const CUtensorMap& o1, const CUtensorMap& o2) {
@@ -298,21 +288,21 @@ extern "C" flint_moe_status flint_ffn_backward(const flint_ffn* f, const uint16_
     m.a[0] = a0, m.a[1] = a1, m.b[0] = b0, m.b[1] = b1, m.out[0] = o0, m.out[1] = o1, m.out[2] = o2;
     return m;
   };
-  if (!run<DGlu, false, true, false>({T, I, {blocks_of(H), 0}, status, 1}, maps(mdy, mdy, mdown, mdown, mg, mu, mh), {g, u}, 1, stream))
+  if (!run<DGlu>({{T, I, {blocks_of(H), 0}, 0, 1}, 0, 1, status, 1}, maps(mdy, mdy, mdown, mdown, og, ou, oh), {g, u}, stream))
     return FLINT_MOE_ECUDA;
   if (dx) {
     CUtensorMap o;
-    if (!map_matrix(&o, dx, H, T, lddx) ||
-        !run<Store, false, true, false>({T, H, {blocks_of(I), blocks_of(I)}, status, 0}, maps(mg, mu, mgate, mup, o, o, o), {}, 1, stream))
+    if (!map_out(&o, dx, H, T, lddx) ||
+        !run<Store>({{T, H, {blocks_of(I), blocks_of(I)}, 0, 1}, 0, 1, status, 0}, maps(mg, mu, mgate, mup, o, o, o), {}, stream))
       return FLINT_MOE_ECUDA;
   }
   if (dgate) {
-    CUtensorMap og, ou, od;
-    if (!map_matrix(&og, dgate, H, I, H) || !map_matrix(&ou, dup, H, I, H) || !map_matrix(&od, ddown, I, H, I)) return FLINT_MOE_ECUDA;
+    CUtensorMap wg, wu, wd;
+    if (!map_out(&wg, dgate, H, I, H) || !map_out(&wu, dup, H, I, H) || !map_out(&wd, ddown, I, H, I)) return FLINT_MOE_ECUDA;
     const int kb = blocks_of(T);
-    if (!run<Store, true, true, false>({I, H, {kb, 0}, status, 0}, maps(mg, mg, mx, mx, og, og, og), {}, 1, stream) ||
-        !run<Store, true, true, false>({I, H, {kb, 0}, status, 0}, maps(mu, mu, mx, mx, ou, ou, ou), {}, 1, stream) ||
-        !run<Store, true, true, false>({H, I, {kb, 0}, status, 0}, maps(mdy, mdy, mh, mh, od, od, od), {}, 1, stream))
+    if (!run<Store>({{I, H, {kb, 0}, 1, 1}, 0, 1, status, 0}, maps(mg, mg, mx, mx, wg, wg, wg), {}, stream) ||
+        !run<Store>({{I, H, {kb, 0}, 1, 1}, 0, 1, status, 0}, maps(mu, mu, mx, mx, wu, wu, wu), {}, stream) ||
+        !run<Store>({{H, I, {kb, 0}, 1, 1}, 0, 1, status, 0}, maps(mdy, mdy, mh, mh, wd, wd, wd), {}, stream))
       return FLINT_MOE_ECUDA;
   }
   return FLINT_MOE_OK;

@@ -13,22 +13,42 @@
 namespace flint {
 namespace gemm {
 
-constexpr int TILE = 128;               // rows and columns of an output tile
-constexpr int BK = 64;                  // reduction of a stage: one 128-byte swizzled row of 16-bit values
-constexpr int BOX = 64 * BK * 2;        // 8 KiB: 64 x 64 values, what one TMA load moves
-constexpr int STAGE = 4 * BOX;          // 128 x 64 of A, 128 x 64 of B
-constexpr int STAGES = 3;
-constexpr int THREADS = 192;            // warp 0 loads, warp 1 issues the MMAs, warps 2-5 the epilogue
-constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE;
+constexpr int BK = 64;               // reduction of a stage: one 128-byte swizzled row of 16-bit values
+constexpr int BOX = 64 * BK * 2;     // 8 KiB: 64 x 64 values, what one TMA load moves
+constexpr int STAGE = 4 * BOX;       // a CTA's operands of a stage: 128 x 64 of A, 128 x 64 of B
+constexpr int SLOT = 32 * 64;        // 2 KiB: 32 rows x 32 columns of 16-bit values, what one TMA store moves
+constexpr int SLOTS = 4;             // of each epilogue warp
 
+// k_gemm: one 128 x 128 tile a CTA, two CTAs on an SM, so that the one's epilogue runs beside the other's products.
+struct One {
+  static constexpr int TM = 128, TN = 128, CTAS = 1, STAGES = 3, GROUPS = 1;
+};
+// k_gemm_pair: 256 x 256 tiles by pairs of CTAs (cta_group::2), each with half of A's rows and half of B's, 128 x 256 sums
+// a CTA; persistent, with two accumulators, so that a tile's epilogue runs beside the next one's products.
+struct Two {
+  static constexpr int TM = 256, TN = 256, CTAS = 2, STAGES = 5, GROUPS = 2;
+};
+// Epilogue warps come in GROUPS of four (tensor memory's lanes), 128 of the accumulator's columns each.
+template <typename C>
+constexpr int THREADS = 64 + 128 * C::GROUPS;  // warp 0 loads, warp 1 issues the MMAs, the others the epilogue
+template <typename C>
+constexpr size_t SMEM = 1024 + (size_t)C::STAGES * STAGE + (C::CTAS == 2 ? (size_t)C::GROUPS * 4 * SLOTS * SLOT : 0);
+static_assert(4 * SLOTS * SLOT <= One::STAGES * STAGE, "k_gemm's epilogue writes where its operands were");
+
+struct Problem {
+  int M, N;         // output rows and columns (of one matrix of the batch)
+  int kb[2];        // k-blocks of the two segments (0: no second segment)
+  int a_mn, b_mn;   // operands stored MN-major
+};
 struct Args {
-  int M, N;        // output rows and columns (of one matrix of the batch)
-  int kb[2];       // k-blocks of the two segments (0: no second segment)
+  Problem p;
+  int f16;          // operands are f16, not bf16
+  int batch;
   int* status;
-  int clear;       // the first kernel of a call clears the status word
+  int clear;        // the first kernel of a call clears the status word
 };
 
-// 64 x 64 boxes (x: the contiguous dimension, y: rows, z: matrix of the batch).
+// Operands in 64 x 64 boxes (x: the contiguous dimension, y: rows, z: matrix of the batch), outputs in 32 x 32 boxes.
 struct Maps {
   CUtensorMap a[2], b[2];  // of each segment
   CUtensorMap out[3];
@@ -41,32 +61,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int 
                : "memory");
 }
 
-// What an epilogue works on: a thread is one row of the tile.
-struct Tile {
-  uint32_t tmem;  // this warp's lanes of the accumulator
-  uint8_t* sm;    // staging memory: the tile's operands have been used
-  uint32_t sm_addr;
-  int row, m0, n0, z;  // row of the tile 0 .. 127, the tile's first output row, column tile's first column, matrix
-  int M, N;
-};
-
-// The epilogue's four warps meet; epi_all: whether all of them say yes.
-__device__ __forceinline__ void epi_sync() { asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool epi_all(bool ok) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred.aligned q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((int)ok)
-      : "memory");
-  return r != 0;
-}
-
-// Eight 16-bit values to columns c .. c + 7 of row r of a staged 64-column box of 128 rows.
-__device__ __forceinline__ void stage8(uint8_t* box, int r, int c, const uint4 v) {
-  *reinterpret_cast<uint4*>(box + sw128_off(r, c)) = v;
-}
 __device__ __forceinline__ uint32_t f2b2(float lo, float hi) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -79,26 +73,70 @@ __device__ __forceinline__ void unpack8_bf16(const uint4 u, float* v) {
   v[4] = bf16lo(u.z), v[5] = bf16hi(u.z), v[6] = bf16lo(u.w), v[7] = bf16hi(u.w);
 }
 
-// Stores `boxes` staged boxes of 128 rows x 64 columns as columns n0, n0 + 64, ... of rows m0 ... of out (what lies
-// outside is left out); by one thread, after the staging threads have met.
-__device__ __forceinline__ void store_boxes(const CUtensorMap* out, const Tile& t, uint32_t src, int boxes, int n0) {
-  for (int b = 0; b < boxes; ++b)
-    for (int y = 0; y < 2; ++y)
-      if (n0 + 64 * b < t.N && t.m0 + 64 * y < t.M) tma_store_3d(out, n0 + 64 * b, t.m0 + 64 * y, t.z, src + b * 2 * BOX + y * BOX);
+// What an epilogue warp works on: 32 rows, a lane each, and its group's columns of the accumulator.
+struct Part {
+  uint32_t tmem;  // the accumulator's first column, this warp's lanes
+  int row0, row;  // the warp's first output row, and this lane's
+  int n0, group;  // the tile's first output column
+  int z, M, N;
+  int lane;
+  uint8_t* sm;    // the warp's slots
+  uint32_t sm_addr;
+  int slot;       // the next one to fill
+
+  // The place of 16-byte piece c of this lane's row in a slot: the 64-byte swizzle.
+  __device__ __forceinline__ uint4* piece(int s, int c) const {
+    return reinterpret_cast<uint4*>(sm + s * SLOT + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+  }
+  // 32 columns x .. of the warp's rows, this lane's row in v: to the next slot, and from there to memory (what lies
+  // outside the matrix is left out).
+  __device__ __forceinline__ void put(const CUtensorMap* map, int x, const uint4 (&v)[4]) {
+    if (lane == 0) bulk_wait_read<SLOTS - 1>();
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) *piece(slot, c) = v[c];
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+      if (x < N && row0 < M) tma_store_3d(map, x, row0, z, sm_addr + slot * SLOT);
+      bulk_commit();
+    }
+    slot = slot + 1 == SLOTS ? 0 : slot + 1;
+  }
+};
+
+// Descriptors of one operand of a stage (128 rows or columns x 64 of the reduction).
+struct Operand {
+  uint64_t desc;  // without the address
+  uint32_t step;  // 16 of the reduction further
+};
+__device__ __forceinline__ Operand operand(bool mn) {
+  return mn ? Operand{sw128_desc_mn(0, BOX), 2048 >> 4} : Operand{sw128_desc(0), 32 >> 4};
 }
 
-// One output tile a CTA, two CTAs on an SM: the one's epilogue runs beside the other's products.
-template <typename E, bool A_MN, bool B_MN, bool F16>
-__global__ void __launch_bounds__(THREADS, 2) k_gemm(const Args a, const __grid_constant__ Maps maps, const typename E::Args e) {
+// This CTA's share of a stage: rows m, m + 64 of A and n[0], n[1] of B from k on, by one thread.
+template <typename Load>
+__device__ __forceinline__ void load_stage(const Problem& p, int k, int m, const int (&n)[2], Load load) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int mm = m + 64 * h;
+    load(h * BOX, true, h, p.a_mn ? mm : k, p.a_mn ? k : mm);
+    load((2 + h) * BOX, false, h, p.b_mn ? n[h] : k, p.b_mn ? k : n[h]);
+  }
+}
+
+template <typename E>
+__global__ void __launch_bounds__(THREADS<One>, 2) k_gemm(const Args a, const __grid_constant__ Maps maps, const typename E::Args e) {
   extern __shared__ uint8_t dsmem[];
-  __shared__ uint64_t full[STAGES], empty[STAGES], acc_full;
+  constexpr int ST = One::STAGES;
+  __shared__ uint64_t full[ST], empty[ST], acc_full;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
   volatile int* abort = &abort_flag;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -106,7 +144,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_gemm(const Args a, const __grid_
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&tmem_base, TILE);
+  if (warp == 1) tmem_alloc(&tmem_base, One::TN);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -114,85 +152,272 @@ __global__ void __launch_bounds__(THREADS, 2) k_gemm(const Args a, const __grid_
   pdl_wait();
   pdl_trigger();
   if (a.clear && threadIdx.x == 0 && blockIdx.x + blockIdx.y + blockIdx.z == 0) *a.status = 0;
-  const int m0 = blockIdx.y * TILE, n0 = blockIdx.x * E::COLS, z = blockIdx.z;
-  const int blocks = a.kb[0] + a.kb[1];
+  constexpr int COLS = E::PAIR ? One::TN / 2 : One::TN;
+  const int m0 = blockIdx.y * One::TM, n0 = blockIdx.x * COLS, z = blockIdx.z;
+  const int blocks = a.p.kb[0] + a.p.kb[1];
   if (warp == 0) {
     if (lane == 0) {
+      const int n[2] = {n0, E::PAIR ? n0 : n0 + 64};
       int i = 0;
       for (; i < blocks; ++i) {
-        const int s = i % STAGES, seg = i >= a.kb[0] ? 1 : 0, k = (seg ? i - a.kb[0] : i) * BK;
-        if (i >= STAGES && !wait_ab(&empty[s], ((i / STAGES) - 1) & 1, abort, a.status)) break;
-        const uint32_t as = base + s * STAGE, bs = as + 2 * BOX;
+        const int s = i % ST, seg = i >= a.p.kb[0] ? 1 : 0, k = (seg ? i - a.p.kb[0] : i) * BK;
+        if (i >= ST && !wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, a.status)) break;
+        const uint32_t sm = base + s * STAGE;
         mbar_arrive_expect_tx(&full[s], STAGE);
-        for (int h = 0; h < 2; ++h) {
-          const int m = m0 + 64 * h, n = E::PAIR ? n0 : n0 + 64 * h;
-          const CUtensorMap* bm = E::PAIR ? &maps.b[h] : &maps.b[seg];
-          tma_load_3d(as + h * BOX, &maps.a[seg], A_MN ? m : k, A_MN ? k : m, z, &full[s]);
-          tma_load_3d(bs + h * BOX, bm, B_MN ? n : k, B_MN ? k : n, z, &full[s]);
-        }
+        load_stage(a.p, k, m0, n, [&](int off, bool is_a, int h, int x, int y) {
+          tma_load_3d(sm + off, is_a ? &maps.a[seg] : &maps.b[E::PAIR ? h : seg], x, y, z, &full[s]);
+        });
       }
-      for (int r = (i > STAGES ? i - STAGES : 0); r < i; ++r) mbar_drain(&full[r % STAGES], (r / STAGES) & 1);
+      for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&full[r % ST], (r / ST) & 1);
     }
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_f32acc(TILE, TILE, !F16) | (A_MN ? IDESC_A_MN : 0u) | (B_MN ? IDESC_B_MN : 0u);
+    const uint32_t idesc = idesc_f32acc(One::TM, One::TN, !a.f16) | (a.p.a_mn ? IDESC_A_MN : 0u) | (a.p.b_mn ? IDESC_B_MN : 0u);
+    const Operand oa = operand(a.p.a_mn), ob = operand(a.p.b_mn);
     int i = 0;
     for (; i < blocks; ++i) {
-      const int s = i % STAGES;
-      const bool ok = wait_ab(&full[s], (i / STAGES) & 1, abort, a.status);
+      const int s = i % ST;
+      const bool ok = wait_ab(&full[s], (i / ST) & 1, abort, a.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t as = base + s * STAGE, bs = as + 2 * BOX;
+        const uint64_t ad = oa.desc | ((base + s * STAGE) >> 4), bd = ob.desc | ((base + s * STAGE + 2 * BOX) >> 4);
 #pragma unroll
-        for (int ks = 0; ks < BK / 16; ++ks) {
-          const uint64_t ad = A_MN ? sw128_desc_mn(as + ks * 2048, BOX) : sw128_desc(as) + (uint64_t)(ks * 2);
-          const uint64_t bd = B_MN ? sw128_desc_mn(bs + ks * 2048, BOX) : sw128_desc(bs) + (uint64_t)(ks * 2);
-          tc_mma(tmem, ad, bd, idesc, (i > 0 || ks > 0) ? 1u : 0u);
-        }
+        for (int ks = 0; ks < BK / 16; ++ks) tc_mma(tmem, ad + ks * oa.step, bd + ks * ob.step, idesc, (i > 0 || ks > 0) ? 1u : 0u);
         tc_commit(&empty[s]);
         if (i + 1 == blocks) tc_commit(&acc_full);
       }
       __syncwarp();
     }
-    for (int r = (i > STAGES ? i - STAGES : 0); r < i; ++r) mbar_drain(&empty[r % STAGES], (r / STAGES) & 1);
+    for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&empty[r % ST], (r / ST) & 1);
   } else {
-    const bool ok = __all_sync(0xffffffffu, wait_ab(&acc_full, 0, abort, a.status));
-    if (epi_all(ok)) {  // a warp that gave up takes the others along: they meet again below
+    const bool ok = wait_ab(&acc_full, 0, abort, a.status);
+    if (__all_sync(0xffffffffu, ok)) {
       tc_fence_after();
       const int q = warp & 3;
-      Tile t;
+      Part t;
       t.tmem = tmem + ((uint32_t)(q * 32) << 16);
-      t.sm = dsmem + (base - smem_addr(dsmem));
-      t.sm_addr = base;
-      t.row = q * 32 + lane;
-      t.m0 = m0;
+      t.row0 = m0 + q * 32;
+      t.row = t.row0 + lane;
       t.n0 = n0;
+      t.group = 0;
       t.z = z;
-      t.M = a.M;
-      t.N = a.N;
-      E::run(e, maps, t, warp == 2 && lane == 0);
+      t.M = a.p.M;
+      t.N = a.p.N;
+      t.lane = lane;
+      t.sm_addr = base + q * SLOTS * SLOT;  // the tile's operands have been used
+      t.sm = dsmem + (t.sm_addr - smem_addr(dsmem));
+      t.slot = 0;
+      if (t.row0 < t.M) E::template run<One>(e, maps, t, [] {});
+      if (lane == 0) bulk_wait_all();
       tc_fence_before();
     }
   }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_free(tmem, TILE);
+    tmem_free(tmem, One::TN);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Pairs of CTAs. Each loads its own halves of the operands; all copies arrive on the first CTA's barriers, whose MMA warp
+// multiplies for both and tells both when a stage or a tile's sums are done.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives once on bar in both CTAs when every tcgen05 operation this thread issued so far has completed.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t base, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Tiles in bands of eight rows of tiles, column by column: the tiles that run at once share their operands in L2.
+struct Walk {
+  int mt, nt;  // tiles down and across
+  __device__ __forceinline__ void at(int t, int& m, int& n, int& z) const {
+    const int per = mt * nt;
+    z = t / per;
+    t -= z * per;
+    const int band = t / (8 * nt), first = band * 8, rows = min(8, mt - first);
+    t -= band * 8 * nt;
+    n = t / rows;
+    m = first + t - n * rows;
+  }
+};
+
+template <typename E>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
+    k_gemm_pair(const Args a, const __grid_constant__ Maps maps, const typename E::Args e) {
+  extern __shared__ uint8_t dsmem[];
+  constexpr int ST = Two::STAGES, EPI = 4 * Two::GROUPS;
+  __shared__ uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
+  volatile int* abort = &abort_flag;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * EPI);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(&tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the other CTA's barriers are there
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_wait();
+  pdl_trigger();
+  if (a.clear && threadIdx.x == 0 && blockIdx.x == 0) *a.status = 0;
+  constexpr int COLS = E::PAIR ? Two::TN / 2 : Two::TN;
+  const Walk walk = {(a.p.M + Two::TM - 1) / Two::TM, (a.p.N + COLS - 1) / COLS};
+  const int tiles = walk.mt * walk.nt * a.batch, step = gridDim.x >> 1, first = blockIdx.x >> 1;
+  const int blocks = a.p.kb[0] + a.p.kb[1];
+  if (warp == 0) {
+    if (lane == 0) {
+      int i = 0;  // stages so far
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        int mi, ni, z;
+        walk.at(t, mi, ni, z);
+        // The first CTA holds the tile's columns 0 .. 127 of B (or the gate's rows), the second the others.
+        const int m = mi * Two::TM + (int)rank * 128, nb = ni * COLS + (E::PAIR ? 0 : (int)rank * 128);
+        const int n[2] = {nb, nb + 64};
+        for (int kb = 0; kb < blocks; ++kb, ++i) {
+          const int s = i % ST, seg = kb >= a.p.kb[0] ? 1 : 0, k = (seg ? kb - a.p.kb[0] : kb) * BK;
+          if (i >= ST && !(ok = wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, a.status))) break;
+          const uint32_t sm = base + s * STAGE, bar = dsmem_addr(smem_addr(&full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE);
+          const CUtensorMap *am = &maps.a[seg], *bm = &maps.b[E::PAIR ? rank : seg];
+          load_stage(a.p, k, m, n, [&](int off, bool is_a, int, int x, int y) {
+            tma_load_3d_pair(sm + off, is_a ? am : bm, x, y, z, bar);
+          });
+        }
+      }
+      // The second CTA's copies count on the first's barriers: it stays until the first has seen them (cluster_sync).
+      if (rank == 0)
+        for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&full[r % ST], (r / ST) & 1);
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t idesc = idesc_f32acc(Two::TM, Two::TN, !a.f16) | (a.p.a_mn ? IDESC_A_MN : 0u) | (a.p.b_mn ? IDESC_B_MN : 0u);
+      const Operand oa = operand(a.p.a_mn), ob = operand(a.p.b_mn);
+      int i = 0, n = 0;  // stages and tiles so far
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step, ++n) {
+        const int b = n & 1;
+        ok = n < 2 || wait_ab(&acc_empty[b], ((n >> 1) - 1) & 1, abort, a.status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        for (int kb = 0; kb < blocks; ++kb, ++i) {
+          const int s = i % ST;
+          ok = wait_ab(&full[s], (i / ST) & 1, abort, a.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t ad = oa.desc | ((base + s * STAGE) >> 4), bd = ob.desc | ((base + s * STAGE + 2 * BOX) >> 4);
+#pragma unroll
+            for (int ks = 0; ks < BK / 16; ++ks)
+              tc_mma_pair(tmem + b * Two::TN, ad + ks * oa.step, bd + ks * ob.step, idesc, (kb > 0 || ks > 0) ? 1u : 0u);
+            tc_commit_pair(&empty[s]);
+            if (kb + 1 == blocks) tc_commit_pair(&acc_full[b]);
+          }
+          __syncwarp();
+        }
+      }
+      for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&empty[r % ST], (r / ST) & 1);
+    }
+  } else {
+    const int q = warp & 3, group = (warp - 2) >> 2;
+    Part t;
+    t.group = group;
+    t.M = a.p.M;
+    t.N = a.p.N;
+    t.lane = lane;
+    t.sm_addr = base + ST * STAGE + (uint32_t)((warp - 2) * SLOTS * SLOT);
+    t.sm = dsmem + (t.sm_addr - smem_addr(dsmem));
+    t.slot = 0;
+    int n = 0;
+    for (int ti = first; ti < tiles; ti += step, ++n) {
+      const int b = n & 1;
+      int mi, ni;
+      walk.at(ti, mi, ni, t.z);
+      const bool ok = wait_ab(&acc_full[b], (n >> 1) & 1, abort, a.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      t.row0 = mi * Two::TM + (int)rank * 128 + q * 32;
+      t.row = t.row0 + lane;
+      t.n0 = ni * COLS;
+      t.tmem = tmem + b * Two::TN + ((uint32_t)(q * 32) << 16);
+      bool freed = false;
+      auto release = [&] {  // this warp has read the accumulator
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_addr(&acc_empty[b]), 0));
+        freed = true;
+      };
+      if (t.row0 < t.M) E::template run<Two>(e, maps, t, release);
+      if (!freed) release();
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // nothing of the other CTA's still counts on this one's barriers or reads its memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free_pair(tmem, 512);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-// A batch of matrices [rows][cols] of 16-bit values (rows ld apart, matrices `apart`) in 64 x 64 boxes.
-inline bool map_matrix(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld, int64_t batch, int64_t apart) {
+// A batch of matrices [rows][cols] of 16-bit values (rows ld apart, matrices `apart`), as an operand or as an output.
+inline bool map_matrix(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld, int64_t batch, int64_t apart, bool out) {
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
   const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)apart * 2};
-  const cuuint32_t box[3] = {64, 64, 1};
-  return encode_bf16(m, p, 3, dims, strides, box);
+  const cuuint32_t side = out ? 32 : 64, box[3] = {side, side, 1};
+  return encode_bf16(m, p, 3, dims, strides, box, out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
-inline bool map_matrix(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld) {
-  return map_matrix(m, p, cols, rows, ld, 1, ld);  // one matrix: its distance to the next is never used
+inline bool map_in(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld) {
+  return map_matrix(m, p, cols, rows, ld, 1, ld, false);  // one matrix: its distance to the next is never used
+}
+inline bool map_out(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld) {
+  return map_matrix(m, p, cols, rows, ld, 1, ld, true);
 }
 
 // Prepares a kernel once for each device: its dynamic shared memory, and the carveout that all kernels here ask for.
@@ -227,10 +452,24 @@ bool launch(dim3 grid, int block, size_t smem, cudaStream_t stream, const P&... 
   return cudaLaunchKernelEx(&cfg, KERNEL, args...) == cudaSuccess;
 }
 
-template <typename E, bool A_MN, bool B_MN, bool F16>
-bool run(const Args& a, const Maps& m, const typename E::Args& e, int batch, cudaStream_t stream) {
-  const dim3 grid((unsigned)((a.N + E::COLS - 1) / E::COLS), (unsigned)((a.M + TILE - 1) / TILE), (unsigned)batch);
-  return launch<k_gemm<E, A_MN, B_MN, F16>>(grid, THREADS, SMEM, stream, a, m, e);
+inline int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2)
+    n = 152;
+  return n;
+}
+
+template <typename E>
+bool run(const Args& a, const Maps& m, const typename E::Args& e, cudaStream_t stream) {
+  auto tiles = [&](int tm, int tn) {
+    const int cols = E::PAIR ? tn / 2 : tn;
+    return dim3((unsigned)((a.p.N + cols - 1) / cols), (unsigned)((a.p.M + tm - 1) / tm), (unsigned)a.batch);
+  };
+  const dim3 one = tiles(One::TM, One::TN), two = tiles(Two::TM, Two::TN);
+  const int64_t pairs = (int64_t)two.x * two.y * two.z, most = sm_count() / 2;
+  if (pairs >= most)
+    return launch<k_gemm_pair<E>>(dim3(2 * (unsigned)std::min(pairs, most)), THREADS<Two>, SMEM<Two>, stream, a, m, e);
+  return launch<k_gemm<E>>(one, THREADS<One>, SMEM<One>, stream, a, m, e);
 }
 
 }  // namespace gemm

@@ -152,127 +152,115 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_split(const Start a) {
 // ---------------------------------------------------------------------------
 // Epilogues: S, P = b S + c S S, X <- a X + P X.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void finish(const Maps& maps, const Tile& t, bool leader, int outs) {
-  fence_proxy_async();
-  epi_sync();
-  if (leader) {
-    for (int o = 0; o < outs; ++o) store_boxes(&maps.out[o], t, t.sm_addr + o * 4 * BOX, 2, t.n0);
-    bulk_commit();
-    bulk_wait_all();
-  }
-}
-
 struct Gram {
-  static constexpr int COLS = TILE;
   static constexpr bool PAIR = false;
   struct Args {};
-  static __device__ __forceinline__ void run(const Args&, const Maps& maps, const Tile& t, bool leader) {
-#pragma unroll
-    for (int c = 0; c < TILE; c += 32) {
+  template <typename C, typename Release>
+  static __device__ __forceinline__ void run(const Args&, const Maps& maps, Part& t, Release release) {
+#pragma unroll 1
+    for (int c = 128 * t.group; c < 128 * t.group + 128; c += 32) {
       uint32_t w[32];
       tc_ld32_async(t.tmem + c, w);
       tc_wait_ld();
+      if ((c & 127) == 96) release();
       float* v = reinterpret_cast<float*>(w);
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] *= S_SCALE / (X_SCALE * X_SCALE);
-#pragma unroll
-      for (int j = 0; j < 32; j += 8) stage8(t.sm + (c >> 6) * 2 * BOX, t.row, (c & 63) + j, pack8_f16(v + j));
+      const uint4 o[4] = {pack8_f16(v), pack8_f16(v + 8), pack8_f16(v + 16), pack8_f16(v + 24)};
+      t.put(&maps.out[0], t.n0 + c, o);
     }
-    finish(maps, t, leader, 1);
   }
 };
 
+// Pieces c, c + 8, .. of this lane's row of a matrix (columns from `at` on, the tile's column c first); zero outside.
+__device__ __forceinline__ void load_row(const Part& t, const uint16_t* at, int c, uint4 (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = t.row < t.M && t.n0 + c + 8 * j < t.N ? __ldcg(reinterpret_cast<const uint4*>(at + c + 8 * j)) : make_uint4(0, 0, 0, 0);
+}
+
 struct Poly {
-  static constexpr int COLS = TILE;
   static constexpr bool PAIR = false;
   struct Args {
     const uint16_t* s;  // [batch][M][pitch]
     int pitch;
     float b, c;
   };
-  static __device__ __forceinline__ void run(const Args& a, const Maps& maps, const Tile& t, bool leader) {
-    const int row = t.m0 + t.row;
-    const uint16_t* s = a.s + ((size_t)t.z * t.M + row) * a.pitch + t.n0;
+  template <typename C, typename Release>
+  static __device__ __forceinline__ void run(const Args& a, const Maps& maps, Part& t, Release release) {
+    const uint16_t* s = a.s + ((size_t)t.z * t.M + t.row) * a.pitch + t.n0;
     const float fs = a.b * (P_SCALE / S_SCALE), fq = a.c * (P_SCALE / (S_SCALE * S_SCALE));
 #pragma unroll 1
-    for (int c = 0; c < TILE; c += 32) {
+    for (int c = 128 * t.group; c < 128 * t.group + 128; c += 32) {
       uint32_t w[32];
       tc_ld32_async(t.tmem + c, w);
-      uint4 sv[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        sv[j] = row < t.M && t.n0 + c + 8 * j < t.N ? __ldcg(reinterpret_cast<const uint4*>(s + c + 8 * j)) : make_uint4(0, 0, 0, 0);
+      uint4 sv[4], o[4];
+      load_row(t, s, c, sv);
       tc_wait_ld();
+      if ((c & 127) == 96) release();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float v[8];
         unpack8_f16(sv[j], v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(fs, v[e], fq * __uint_as_float(w[8 * j + e]));
-        stage8(t.sm + (c >> 6) * 2 * BOX, t.row, (c & 63) + 8 * j, pack8_f16(v));
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(fs, v[i], fq * __uint_as_float(w[8 * j + i]));
+        o[j] = pack8_f16(v);
       }
+      t.put(&maps.out[0], t.n0 + c, o);
     }
-    finish(maps, t, leader, 1);
   }
 };
 
 template <bool LAST>
 struct Update {
-  static constexpr int COLS = TILE;
   static constexpr bool PAIR = false;
   struct Args {
     const uint16_t *hi, *lo;  // [batch][M][pitch]
     int pitch;
     float a, scale;
-    uint16_t* out;  // LAST: [batch][M][N], 16-byte pieces of a row not aligned where N % 8
+    uint16_t* out;  // LAST: [batch][M][N]
   };
-  static __device__ __forceinline__ void run(const Args& a, const Maps& maps, const Tile& t, bool leader) {
-    const int row = t.m0 + t.row;
-    const size_t at = ((size_t)t.z * t.M + row) * a.pitch + t.n0;
+  template <typename C, typename Release>
+  static __device__ __forceinline__ void run(const Args& a, const Maps& maps, Part& t, Release release) {
+    const size_t at = ((size_t)t.z * t.M + t.row) * a.pitch + t.n0;
     constexpr float fp = 1.0f / P_SCALE;  // P X comes scaled by both
 #pragma unroll 1
-    for (int c = 0; c < TILE; c += 32) {
+    for (int c = 128 * t.group; c < 128 * t.group + 128; c += 32) {
       uint32_t w[32];
       tc_ld32_async(t.tmem + c, w);
       uint4 hv[4], lv[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = row < t.M && t.n0 + c + 8 * j < t.N;
-        hv[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.hi + at + c + 8 * j)) : make_uint4(0, 0, 0, 0);
-        lv[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.lo + at + c + 8 * j)) : make_uint4(0, 0, 0, 0);
-      }
+      load_row(t, a.hi + at, c, hv);
+      load_row(t, a.lo + at, c, lv);
       tc_wait_ld();
+      if ((c & 127) == 96) release();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float h[8], l[8], v[8];
         unpack8_f16(hv[j], h);
         unpack8_f16(lv[j], l);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(fp, __uint_as_float(w[8 * j + e]), a.a * (h[e] + l[e]));
-        uint8_t* box = t.sm + (c >> 6) * 2 * BOX;
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(fp, __uint_as_float(w[8 * j + i]), a.a * (h[i] + l[i]));
         if (LAST) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= a.scale;
-          stage8(box, t.row, (c & 63) + 8 * j, pack8_bf16(v));
+          for (int i = 0; i < 8; ++i) v[i] *= a.scale;
+          hv[j] = pack8_bf16(v);
         } else {
-          uint4 hi, lo;
-          split8(v, hi, lo);
-          stage8(box, t.row, (c & 63) + 8 * j, hi);
-          stage8(box + 4 * BOX, t.row, (c & 63) + 8 * j, lo);
+          split8(v, hv[j], lv[j]);
         }
       }
-    }
-    if (!LAST) {
-      finish(maps, t, leader, 2);
-    } else if (t.N % 8 == 0) {
-      finish(maps, t, leader, 1);
-    } else {  // rows that TMA cannot reach: a warp writes its own 32 rows, a row's neighbours by neighbouring lanes
-      __syncwarp();
-      const int lane = t.row & 31, r0 = t.row - lane;
-      for (int r = r0; r < r0 + 32 && t.m0 + r < t.M; ++r) {
-        uint16_t* dst = a.out + ((size_t)t.z * t.M + t.m0 + r) * t.N + t.n0;
-        for (int c = lane; c < TILE && t.n0 + c < t.N; c += 32)
-          dst[c] = *reinterpret_cast<const uint16_t*>(t.sm + (c >> 6) * 2 * BOX + sw128_off(r, c & 63));
+      if (!LAST || t.N % 8 == 0) {
+        t.put(&maps.out[0], t.n0 + c, hv);
+        if (!LAST) t.put(&maps.out[1], t.n0 + c, lv);
+      } else {  // rows that TMA cannot reach: through a slot, a row's neighbours by neighbouring lanes
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *t.piece(0, j) = hv[j];
+        __syncwarp();
+        const int col = t.n0 + c + t.lane;
+        for (int r = 0; r < 32 && t.row0 + r < t.M; ++r)
+          if (col < t.N)
+            a.out[((size_t)t.z * t.M + t.row0 + r) * t.N + col] =
+                *reinterpret_cast<const uint16_t*>(t.sm + r * 64 + ((((t.lane >> 3) ^ (r >> 1)) & 3) << 4) + (t.lane & 7) * 2);
       }
     }
   }
@@ -359,14 +347,18 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
   auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(wsp + o); };
   const bool tall = rows > cols;
   const int m = w.m;
-  CUtensorMap x[2][2], s, p, o;
+  CUtensorMap x[2][2], xout[2][2], s, sout, p, pout, o;
   bool ok = true;
-  for (int i = 0; i < 4; ++i)
-    ok = ok && map_matrix(&x[i >> 1][i & 1], at(w.x[i >> 1][i & 1]), cols, rows, w.pitch, n, (int64_t)rows * w.pitch);
-  ok = ok && map_matrix(&s, at(w.s), m, m, w.mpitch, n, (int64_t)m * w.mpitch) &&
-       map_matrix(&p, at(w.p), m, m, w.mpitch, n, (int64_t)m * w.mpitch);
-  o = p;
-  if (cols % 8 == 0) ok = ok && map_matrix(&o, out, cols, rows, cols, n, (int64_t)rows * cols);
+  for (int i = 0; i < 4; ++i) {
+    const size_t off = w.x[i >> 1][i & 1];
+    ok = ok && map_matrix(&x[i >> 1][i & 1], at(off), cols, rows, w.pitch, n, (int64_t)rows * w.pitch, false) &&
+         map_matrix(&xout[i >> 1][i & 1], at(off), cols, rows, w.pitch, n, (int64_t)rows * w.pitch, true);
+  }
+  for (int i = 0; i < 2; ++i)
+    ok = ok && map_matrix(i ? &sout : &s, at(w.s), m, m, w.mpitch, n, (int64_t)m * w.mpitch, i) &&
+         map_matrix(i ? &pout : &p, at(w.p), m, m, w.mpitch, n, (int64_t)m * w.mpitch, i);
+  o = pout;
+  if (cols % 8 == 0) ok = ok && map_matrix(&o, out, cols, rows, cols, n, (int64_t)rows * cols, true);
   if (!ok) return FLINT_MOE_ECUDA;
   auto maps = [](const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
                  const CUtensorMap& o0, const CUtensorMap& o1) {
@@ -381,24 +373,18 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
     return FLINT_MOE_ECUDA;
   const int kx = ((tall ? rows : cols) + BK - 1) / BK, km = (m + BK - 1) / BK;
   for (int i = 0; i < steps; ++i) {
-    const CUtensorMap *xi = x[i & 1], *xo = x[(i + 1) & 1];
-    const float *cf = coeffs + 3 * i;
+    const CUtensorMap *xi = x[i & 1], *xo = xout[(i + 1) & 1];
+    const float* cf = coeffs + 3 * i;
     const bool last = i + 1 == steps;
-    const Args gram = {m, m, {kx, 0}, status, 0}, poly = {m, m, {km, 0}, status, 0};
-    const Args upd = {rows, cols, {km, last ? 0 : km}, status, 0};
-    const Maps mg = maps(xi[0], xi[0], xi[0], xi[0], s, s), mp = maps(s, s, s, s, p, p);
-    ok = tall ? run<Gram, true, true, true>(gram, mg, {}, n, stream) : run<Gram, false, false, true>(gram, mg, {}, n, stream);
-    ok = ok && run<Poly, false, false, true>(poly, mp, {at(w.s), w.mpitch, cf[1], cf[2]}, n, stream);
+    // S = X X^T (X^T X), both operands the same matrix; P from S, which is its own transpose; X's rows times P, or P times X
+    ok = run<Gram>({{m, m, {kx, 0}, tall, tall}, 1, n, status, 0}, maps(xi[0], xi[0], xi[0], xi[0], sout, sout), {}, stream) &&
+         run<Poly>({{m, m, {km, 0}, 0, 0}, 1, n, status, 0}, maps(s, s, s, s, pout, pout), {at(w.s), w.mpitch, cf[1], cf[2]}, stream);
+    const Args upd = {{rows, cols, {km, last ? 0 : km}, 0, !tall}, 1, n, status, 0};
+    const CUtensorMap &o0 = last ? o : xo[0], &o1 = last ? o : xo[1];
+    const Maps mu = tall ? maps(xi[0], xi[1], p, p, o0, o1) : maps(p, p, xi[0], xi[1], o0, o1);
     const uint16_t *hi = at(w.x[i & 1][0]), *lo = at(w.x[i & 1][1]);
-    if (last) {
-      const Update<true>::Args e = {hi, lo, w.pitch, cf[0], scale / X_SCALE, out};
-      ok = ok && (tall ? run<Update<true>, false, false, true>(upd, maps(xi[0], xi[1], p, p, o, o), e, n, stream)
-                       : run<Update<true>, false, true, true>(upd, maps(p, p, xi[0], xi[1], o, o), e, n, stream));
-    } else {
-      const Update<false>::Args e = {hi, lo, w.pitch, cf[0], 1.0f, nullptr};
-      ok = ok && (tall ? run<Update<false>, false, false, true>(upd, maps(xi[0], xi[1], p, p, xo[0], xo[1]), e, n, stream)
-                       : run<Update<false>, false, true, true>(upd, maps(p, p, xi[0], xi[1], xo[0], xo[1]), e, n, stream));
-    }
+    ok = ok && (last ? run<Update<true>>(upd, mu, {hi, lo, w.pitch, cf[0], scale / X_SCALE, out}, stream)
+                     : run<Update<false>>(upd, mu, {hi, lo, w.pitch, cf[0], 1.0f, nullptr}, stream));
     if (!ok) return FLINT_MOE_ECUDA;
   }
   return FLINT_MOE_OK;
