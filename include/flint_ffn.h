@@ -70,7 +70,8 @@ size_t flint_ffn_backward_workspace_bytes(const flint_ffn* ffn, int32_t max_toke
  *   dgate = bf16(sum_t dg_t x_t^T), dup = bf16(sum_t du_t x_t^T),
  *   ddown = bf16(sum_t dy_t h_t^T)                       shapes of the weights
  * dx NULL skips the gradient of x; dgate, dup and ddown all NULL skip those of
- * the weights (frozen), one of them alone is refused (FLINT_MOE_EINVAL). T = 0
+ * the weights (frozen), one of them alone is refused (FLINT_MOE_EINVAL); what is
+ * left has the same bits. T = 0
  * writes zeros to the weights' gradients. Outputs and workspace must not overlap
  * one another or an input (FLINT_MOE_EINVAL). */
 flint_moe_status flint_ffn_backward(const flint_ffn* ffn, const uint16_t* x, int64_t ldx, const uint16_t* gate_act,

@@ -12,12 +12,12 @@
  *
  * Numerics: every sum is FP32 (the norm FP64). X is kept as the sum of two f16
  * values (22 significant bits), because what its rounding adds to the weak
- * directions the later steps amplify by up to a^steps; S and P = b S + c S S
- * multiply X, where a relative error stays relative, and are single f16 values.
- * The last step multiplies by X's larger part only. The result is within about
- * 2^-9 of the exact one in the norm, as its rounding to bf16 is. Singular values
- * must stay below 8 during the steps (S) and b s^2 + c s^4 below 255 (P), as any
- * useful steps' do: beyond, results are not finite.
+ * directions the later steps amplify by up to a^steps. In the products, where a
+ * relative error stays relative, X, S and P = b S + c S S are single f16
+ * values. The result is within about 2^-8.5 of the exact one in the norm, of
+ * which its own rounding to bf16 is 2^-9.2. Singular values must stay below 8
+ * during the steps (S) and b s^2 + c s^4 below 255 (P), as any useful steps'
+ * do: beyond, results are not finite.
  *
  * Conventions as in flint_moe.h: device pointers, caller-owned memory, no
  * allocation, asynchronous on `stream`, status codes. Matrices are contiguous,

@@ -14,22 +14,22 @@ __device__ __forceinline__ float2 sigmoid2(float g) {
   return g >= 0.f ? make_float2(r, t * r) : make_float2(t * r, r);
 }
 
+struct NoPre {
+  template <typename A>
+  __device__ __forceinline__ NoPre(const A&, const Part&, int) {}
+};
+
 // bf16 rows [M][N] as they are.
 struct Store {
   static constexpr bool PAIR = false;
+  static constexpr int MAPS = MOST;
   struct Args {};
-  template <typename C, typename Release>
-  static __device__ __forceinline__ void run(const Args&, const Maps& maps, Part& t, Release release) {
-#pragma unroll 1
-    for (int c = 128 * t.group; c < 128 * t.group + 128; c += 32) {
-      uint32_t w[32];
-      tc_ld32_async(t.tmem + c, w);
-      tc_wait_ld();
-      if ((c & 127) == 96) release();
-      const float* v = reinterpret_cast<const float*>(w);
-      const uint4 o[4] = {pack8_bf16(v), pack8_bf16(v + 8), pack8_bf16(v + 16), pack8_bf16(v + 24)};
-      t.put(&maps.out[0], t.n0 + c, o);
-    }
+  using Pre = NoPre;
+  static __device__ __forceinline__ void chunk(const Args&, const Maps& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
+                                               const Pre&) {
+    const float* v = reinterpret_cast<const float*>(w);
+    const uint4 o[4] = {pack8_bf16(v), pack8_bf16(v + 8), pack8_bf16(v + 16), pack8_bf16(v + 24)};
+    t.put(&maps.out[0], t.n0 + c, o);
   }
 };
 
@@ -37,35 +37,29 @@ struct Store {
 template <bool SAVE>
 struct Glu {
   static constexpr bool PAIR = true;
+  static constexpr int MAPS = 1;
   struct Args {};
-  template <typename C, typename Release>
-  static __device__ __forceinline__ void run(const Args&, const Maps& maps, Part& t, Release release) {
-#pragma unroll 1
-    for (int c = 64 * t.group; c < 64 * t.group + 64; c += 32) {
-      uint32_t wg[32], wu[32];
-      tc_ld32_async(t.tmem + c, wg);
-      tc_ld32_async(t.tmem + C::TN / 2 + c, wu);
-      tc_wait_ld();
-      if (c & 32) release();
-      const float* g = reinterpret_cast<const float*>(wg);
-      const float* u = reinterpret_cast<const float*>(wu);
-      uint4 o[4];
+  using Pre = NoPre;
+  static __device__ __forceinline__ void chunk(const Args&, const Maps& maps, Part& t, int c, uint32_t (&wg)[32], uint32_t (&wu)[32],
+                                               const Pre&) {
+    const float* g = reinterpret_cast<const float*>(wg);
+    const float* u = reinterpret_cast<const float*>(wu);
+    uint4 o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float h[8];
+    for (int j = 0; j < 4; ++j) {
+      float h[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = __fdividef(g[8 * j + i], 1.0f + __expf(-g[8 * j + i])) * u[8 * j + i];
-        o[j] = pack8_bf16(h);
-      }
-      t.put(&maps.out[0], t.n0 + c, o);
-      if (SAVE) {
+      for (int i = 0; i < 8; ++i) h[i] = __fdividef(g[8 * j + i], 1.0f + __expf(-g[8 * j + i])) * u[8 * j + i];
+      o[j] = pack8_bf16(h);
+    }
+    t.put(&maps.out[0], t.n0 + c, o);
+    if (SAVE) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = pack8_bf16(g + 8 * j);
-        t.put(&maps.out[1], t.n0 + c, o);
+      for (int j = 0; j < 4; ++j) o[j] = pack8_bf16(g + 8 * j);
+      t.put(&maps.out[1], t.n0 + c, o);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = pack8_bf16(u + 8 * j);
-        t.put(&maps.out[2], t.n0 + c, o);
-      }
+      for (int j = 0; j < 4; ++j) o[j] = pack8_bf16(u + 8 * j);
+      t.put(&maps.out[2], t.n0 + c, o);
     }
   }
 };
@@ -73,49 +67,47 @@ struct Glu {
 // dg, du and h from dh and the kept g and u.
 struct DGlu {
   static constexpr bool PAIR = false;
+  static constexpr int MAPS = 1;
   struct Args {
     const uint16_t* g;  // [M][N]
     const uint16_t* u;
   };
-  template <typename C, typename Release>
-  static __device__ __forceinline__ void run(const Args& a, const Maps& maps, Part& t, Release release) {
-    const size_t at = (size_t)t.row * t.N + t.n0;
-#pragma unroll 1
-    for (int c = 128 * t.group; c < 128 * t.group + 128; c += 32) {
-      uint32_t w[32];
-      tc_ld32_async(t.tmem + c, w);
-      uint4 gv[4], uv[4];
+  struct Pre {
+    uint4 g[4], u[4];
+    __device__ __forceinline__ Pre(const Args& a, const Part& t, int c) {
+      const size_t at = (size_t)t.row * t.N + t.n0 + c;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bool in = t.row < t.M && t.n0 + c + 8 * j < t.N;
-        gv[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.g + at + c + 8 * j)) : make_uint4(0, 0, 0, 0);
-        uv[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.u + at + c + 8 * j)) : make_uint4(0, 0, 0, 0);
+        g[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.g + at + 8 * j)) : make_uint4(0, 0, 0, 0);
+        u[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.u + at + 8 * j)) : make_uint4(0, 0, 0, 0);
       }
-      tc_wait_ld();
-      if ((c & 127) == 96) release();
-      const float* d = reinterpret_cast<const float*>(w);
-      uint4 og[4], ou[4], oh[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float g[8], u[8], dg[8], du[8], h[8];
-        unpack8_bf16(gv[j], g);
-        unpack8_bf16(uv[j], u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 s = sigmoid2(g[i]);
-          const float dh = d[8 * j + i], act = g[i] * s.x;
-          dg[i] = dh * u[i] * (s.x * fmaf(g[i], s.y, 1.0f));
-          du[i] = dh * act;
-          h[i] = act * u[i];
-        }
-        og[j] = pack8_bf16(dg);
-        ou[j] = pack8_bf16(du);
-        oh[j] = pack8_bf16(h);
-      }
-      t.put(&maps.out[0], t.n0 + c, og);
-      t.put(&maps.out[1], t.n0 + c, ou);
-      t.put(&maps.out[2], t.n0 + c, oh);
     }
+  };
+  static __device__ __forceinline__ void chunk(const Args&, const Maps& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
+                                               const Pre& pre) {
+    const float* d = reinterpret_cast<const float*>(w);
+    uint4 og[4], ou[4], oh[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float g[8], u[8], dg[8], du[8], h[8];
+      unpack8_bf16(pre.g[j], g);
+      unpack8_bf16(pre.u[j], u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 s = sigmoid2(g[i]);
+        const float dh = d[8 * j + i], act = g[i] * s.x;
+        dg[i] = dh * u[i] * (s.x * fmaf(g[i], s.y, 1.0f));
+        du[i] = dh * act;
+        h[i] = act * u[i];
+      }
+      og[j] = pack8_bf16(dg);
+      ou[j] = pack8_bf16(du);
+      oh[j] = pack8_bf16(h);
+    }
+    t.put(&maps.out[0], t.n0 + c, og);
+    t.put(&maps.out[1], t.n0 + c, ou);
+    t.put(&maps.out[2], t.n0 + c, oh);
   }
 };
 
@@ -226,18 +218,16 @@ extern "C" flint_moe_status flint_ffn_forward(const flint_ffn* f, const uint16_t
   uint8_t* wsp = static_cast<uint8_t*>(ws);
   uint16_t* h = reinterpret_cast<uint16_t*>(wsp + w.h);
   int* status = reinterpret_cast<int*>(ws) + H_STATUS;
-  Maps m1, m2;
-  bool ok = map_in(&m1.a[0], x, H, T, ldx) && map_in(&m1.b[0], f->gate, H, I, H) && map_in(&m1.b[1], f->up, H, I, H) &&
-            map_out(&m1.out[0], h, I, T, I) && map_in(&m2.a[0], h, I, T, I) && map_in(&m2.b[0], f->down, I, H, I) &&
-            map_out(&m2.out[0], y, H, T, ldy);
-  if (ok && g) ok = map_out(&m1.out[1], g, I, T, I) && map_out(&m1.out[2], u, I, T, I);
+  AllMaps<1> m1;
+  AllMaps<MOST> m2;
+  Maps &glu = m1.of[0], &out = m2.of[0];
+  bool ok = map_in(&glu.a[0], x, H, T, ldx) && map_in(&glu.b[0], f->gate, H, I, H) && map_in(&glu.b[1], f->up, H, I, H) &&
+            map_out(&glu.out[0], h, I, T, I) && map_in(&out.a[0], h, I, T, I) && map_in(&out.b[0], f->down, I, H, I) &&
+            map_out(&out.out[0], y, H, T, ldy);
+  if (ok && g) ok = map_out(&glu.out[1], g, I, T, I) && map_out(&glu.out[2], u, I, T, I);
   if (!ok) return FLINT_MOE_ECUDA;
-  m1.a[1] = m1.a[0];
-  if (!g) m1.out[1] = m1.out[2] = m1.out[0];
-  m2.a[1] = m2.a[0];
-  m2.b[1] = m2.b[0];
-  m2.out[1] = m2.out[2] = m2.out[0];
-  const Args a1 = {{T, I, {blocks_of(H), 0}, 0, 0}, 0, 1, status, 1}, a2 = {{T, H, {blocks_of(I), 0}, 0, 0}, 0, 1, status, 0};
+  const gemm::Args a1 = {{{T, I, blocks_of(H), 1, 0, 0, 0, 0, 0, 1}}, 1, 0, status, 1};
+  const gemm::Args a2 = {{{T, H, blocks_of(I), 1, 0, 0, 0, 0, 0, 1}}, 1, 0, status, 0};
   ok = g ? run<Glu<true>>(a1, m1, {}, stream) : run<Glu<false>>(a1, m1, {}, stream);
   ok = ok && run<Store>(a2, m2, {}, stream);
   return ok ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
@@ -282,28 +272,31 @@ extern "C" flint_moe_status flint_ffn_backward(const flint_ffn* f, const uint16_
       !map_in(&mgate, f->gate, H, I, H) || !map_in(&mup, f->up, H, I, H) || !map_in(&mdown, f->down, I, H, I) ||
       !map_in(&mh, h, I, T, I) || !map_out(&og, dg, I, T, I) || !map_out(&ou, du, I, T, I) || !map_out(&oh, h, I, T, I))
     return FLINT_MOE_ECUDA;
-  auto maps = [](const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
-                 const CUtensorMap& o0, const CUtensorMap& o1, const CUtensorMap& o2) {
-    Maps m;
-    m.a[0] = a0, m.a[1] = a1, m.b[0] = b0, m.b[1] = b1, m.out[0] = o0, m.out[1] = o1, m.out[2] = o2;
-    return m;
+  AllMaps<1> m1;
+  Maps& first = m1.of[0];
+  first.a[0] = mdy, first.b[0] = mdown, first.out[0] = og, first.out[1] = ou, first.out[2] = oh;
+  if (!run<DGlu>({{{T, I, blocks_of(H), 1, 0, 0, 0, 1, 0, 1}}, 1, 0, status, 1}, m1, {g, u}, stream)) return FLINT_MOE_ECUDA;
+  // dx and the weights' gradients need nothing of one another: one launch, laid out as if all of them were asked for, so
+  // that each has the same bits with and without the others.
+  const int kb = blocks_of(T);
+  const Problem px = {T, H, blocks_of(I), 2, 2, 2, 0, 1, 0, 1}, pw = {I, H, kb, 1, 0, 0, 1, 1, 0, 1}, pd = {H, I, kb, 1, 0, 0, 1, 1, 0, 1};
+  const Choice choice = choose<Store>({{px, pw, pw, pd}, 4, 0, nullptr, 0});
+  AllMaps<MOST> m2;
+  gemm::Args a = {{}, 0, 0, status, 0};
+  bool ok = true;
+  auto add = [&](const Problem& p, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
+                 uint16_t* out, int64_t ld) {
+    Maps& m = m2.of[a.n];
+    m.a[0] = a0, m.a[1] = a1, m.b[0] = b0, m.b[1] = b1;
+    ok = ok && map_out(&m.out[0], out, p.N, p.M, ld);
+    a.p[a.n++] = p;
   };
-  if (!run<DGlu>({{T, I, {blocks_of(H), 0}, 0, 1}, 0, 1, status, 1}, maps(mdy, mdy, mdown, mdown, og, ou, oh), {g, u}, stream))
-    return FLINT_MOE_ECUDA;
-  if (dx) {
-    CUtensorMap o;
-    if (!map_out(&o, dx, H, T, lddx) ||
-        !run<Store>({{T, H, {blocks_of(I), blocks_of(I)}, 0, 1}, 0, 1, status, 0}, maps(mg, mu, mgate, mup, o, o, o), {}, stream))
-      return FLINT_MOE_ECUDA;
-  }
+  if (dx) add(px, mg, mu, mgate, mup, dx, lddx);
   if (dgate) {
-    CUtensorMap wg, wu, wd;
-    if (!map_out(&wg, dgate, H, I, H) || !map_out(&wu, dup, H, I, H) || !map_out(&wd, ddown, I, H, I)) return FLINT_MOE_ECUDA;
-    const int kb = blocks_of(T);
-    if (!run<Store>({{I, H, {kb, 0}, 1, 1}, 0, 1, status, 0}, maps(mg, mg, mx, mx, wg, wg, wg), {}, stream) ||
-        !run<Store>({{I, H, {kb, 0}, 1, 1}, 0, 1, status, 0}, maps(mu, mu, mx, mx, wu, wu, wu), {}, stream) ||
-        !run<Store>({{H, I, {kb, 0}, 1, 1}, 0, 1, status, 0}, maps(mdy, mdy, mh, mh, wd, wd, wd), {}, stream))
-      return FLINT_MOE_ECUDA;
+    add(pw, mg, mg, mx, mx, dgate, H);
+    add(pw, mu, mu, mx, mx, dup, H);
+    add(pd, mdy, mdy, mh, mh, ddown, I);
   }
+  if (!ok || !run<Store>(a, m2, {}, stream, choice)) return FLINT_MOE_ECUDA;
   return FLINT_MOE_OK;
 }

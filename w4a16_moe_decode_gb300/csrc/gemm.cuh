@@ -3,7 +3,8 @@
 //
 // D[m][n] = sum_k A[m][k] B[n][k], 16-bit operands (both bf16 or both f16), FP32 sums in tensor memory. Each operand is
 // used as it lies in memory: K-major (rows of k) or MN-major (rows of m or n, the reduction being the rows), so that no
-// matrix is ever transposed in memory. The reduction may run over two pairs of operands one after the other (segments).
+// matrix is ever transposed in memory. The reduction may run over several pairs of operands one after the other
+// (segments).
 #pragma once
 
 #include <algorithm>
@@ -35,23 +36,34 @@ template <typename C>
 constexpr size_t SMEM = 1024 + (size_t)C::STAGES * STAGE + (C::CTAS == 2 ? (size_t)C::GROUPS * 4 * SLOTS * SLOT : 0);
 static_assert(4 * SLOTS * SLOT <= One::STAGES * STAGE, "k_gemm's epilogue writes where its operands were");
 
+constexpr int MOST = 4;  // products of one launch
+
 struct Problem {
   int M, N;         // output rows and columns (of one matrix of the batch)
-  int kb[2];        // k-blocks of the two segments (0: no second segment)
+  int kb;           // k-blocks of a segment
+  int segs;         // segments: products of the operands' matrices that the masks' bits name, added up
+  int a_of, b_of;
   int a_mn, b_mn;   // operands stored MN-major
+  int sym;          // D is its own transpose: the tiles above the diagonal are computed, and written twice
+  int batch;
+  __host__ __device__ int blocks() const { return kb * segs; }
 };
 struct Args {
-  Problem p;
+  Problem p[MOST];
+  int n;            // of them
   int f16;          // operands are f16, not bf16
-  int batch;
   int* status;
   int clear;        // the first kernel of a call clears the status word
 };
 
 // Operands in 64 x 64 boxes (x: the contiguous dimension, y: rows, z: matrix of the batch), outputs in 32 x 32 boxes.
 struct Maps {
-  CUtensorMap a[2], b[2];  // of each segment
+  CUtensorMap a[2], b[2];
   CUtensorMap out[3];
+};
+template <int N>
+struct AllMaps {
+  Maps of[N];
 };
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
@@ -73,12 +85,12 @@ __device__ __forceinline__ void unpack8_bf16(const uint4 u, float* v) {
   v[4] = bf16lo(u.z), v[5] = bf16hi(u.z), v[6] = bf16lo(u.w), v[7] = bf16hi(u.w);
 }
 
-// What an epilogue warp works on: 32 rows, a lane each, and its group's columns of the accumulator.
+// What an epilogue warp works on: 32 rows, a lane each.
 struct Part {
-  uint32_t tmem;  // the accumulator's first column, this warp's lanes
   int row0, row;  // the warp's first output row, and this lane's
-  int n0, group;  // the tile's first output column
+  int n0;         // the tile's first output column
   int z, M, N;
+  bool twice;     // the transposed place gets the same values
   int lane;
   uint8_t* sm;    // the warp's slots
   uint32_t sm_addr;
@@ -88,20 +100,77 @@ struct Part {
   __device__ __forceinline__ uint4* piece(int s, int c) const {
     return reinterpret_cast<uint4*>(sm + s * SLOT + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
   }
-  // 32 columns x .. of the warp's rows, this lane's row in v: to the next slot, and from there to memory (what lies
-  // outside the matrix is left out).
-  __device__ __forceinline__ void put(const CUtensorMap* map, int x, const uint4 (&v)[4]) {
+  __device__ __forceinline__ void begin() const {
     if (lane == 0) bulk_wait_read<SLOTS - 1>();
     __syncwarp();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) *piece(slot, c) = v[c];
+  }
+  __device__ __forceinline__ void end(const CUtensorMap* map, int x, int y, bool in) {
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) {
-      if (x < N && row0 < M) tma_store_3d(map, x, row0, z, sm_addr + slot * SLOT);
+      if (in) tma_store_3d(map, x, y, z, sm_addr + slot * SLOT);
       bulk_commit();
     }
     slot = slot + 1 == SLOTS ? 0 : slot + 1;
+  }
+  // 32 columns x .. of the warp's rows, this lane's row in v: to the next slot, and from there to memory (what lies
+  // outside the matrix is left out).
+  __device__ __forceinline__ void put(const CUtensorMap* map, int x, const uint4 (&v)[4]) {
+    begin();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) *piece(slot, c) = v[c];
+    end(map, x, row0, x < N && row0 < M);
+  }
+  // The same values as columns row0 .. of rows x ..
+  __device__ __forceinline__ void put_transposed(const CUtensorMap* map, int x, const uint4 (&v)[4]) {
+    begin();
+    uint8_t* s = sm + slot * SLOT + (lane & 7) * 2;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      const uint4& u = v[c >> 3];
+      const uint32_t w = (c & 6) == 0 ? u.x : (c & 6) == 2 ? u.y : (c & 6) == 4 ? u.z : u.w;
+      *reinterpret_cast<uint16_t*>(s + c * 64 + ((((lane >> 3) ^ (c >> 1)) & 3) << 4)) = (uint16_t)(c & 1 ? w >> 16 : w);
+    }
+    end(map, row0, x, x < N && row0 < M);
+  }
+};
+
+// Tiles of a launch: its products one after the other, each batch of one in bands of eight rows of tiles, column by
+// column, so that the tiles that run at once share their operands in L2; above the diagonal only, row by row, where the
+// result is its own transpose.
+template <typename C, bool PAIR>
+struct Walk {
+  static constexpr int COLS = PAIR ? C::TN / 2 : C::TN;
+  __host__ __device__ static int down(const Problem& p) { return (p.M + C::TM - 1) / C::TM; }
+  __host__ __device__ static int across(const Problem& p) { return (p.N + COLS - 1) / COLS; }
+  __host__ __device__ static int each(const Problem& p) { return p.sym ? down(p) * (down(p) + 1) / 2 : down(p) * across(p); }
+  __host__ __device__ static int64_t tiles(const Args& a) {
+    int64_t t = 0;
+    for (int i = 0; i < a.n; ++i) t += (int64_t)each(a.p[i]) * a.p[i].batch;
+    return t;
+  }
+  int i, m, n, z;  // product, tile and matrix of it
+  __device__ __forceinline__ Walk(const Args& a, int t) {
+    i = 0;
+    int per = each(a.p[0]);
+    if constexpr (!PAIR)
+      while (i + 1 < a.n && t >= per * a.p[i].batch) {
+        t -= per * a.p[i].batch;
+        per = each(a.p[++i]);
+      }
+    const Problem& p = a.p[i];
+    const int mt = down(p), nt = across(p);
+    z = t / per;
+    t -= z * per;
+    if (p.sym) {
+      for (m = 0; t >= mt - m; ++m) t -= mt - m;
+      n = m + t;
+    } else {
+      const int band = t / (8 * nt), first = band * 8, rows = min(8, mt - first);
+      t -= band * 8 * nt;
+      n = t / rows;
+      m = first + t - n * rows;
+    }
   }
 };
 
@@ -109,6 +178,8 @@ struct Part {
 struct Operand {
   uint64_t desc;  // without the address
   uint32_t step;  // 16 of the reduction further
+  // A CTA of a cluster finds its rank in the upper bits of its shared-memory addresses: they are not the descriptor's.
+  __device__ __forceinline__ uint64_t at(uint32_t saddr) const { return desc | ((saddr & 0x3FFFFu) >> 4); }
 };
 __device__ __forceinline__ Operand operand(bool mn) {
   return mn ? Operand{sw128_desc_mn(0, BOX), 2048 >> 4} : Operand{sw128_desc(0), 32 >> 4};
@@ -116,17 +187,25 @@ __device__ __forceinline__ Operand operand(bool mn) {
 
 // This CTA's share of a stage: rows m, m + 64 of A and n[0], n[1] of B from k on, by one thread.
 template <typename Load>
-__device__ __forceinline__ void load_stage(const Problem& p, int k, int m, const int (&n)[2], Load load) {
+__device__ __forceinline__ void load_stage(bool a_mn, bool b_mn, int k, int m, const int (&n)[2], Load load) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int mm = m + 64 * h;
-    load(h * BOX, true, h, p.a_mn ? mm : k, p.a_mn ? k : mm);
-    load((2 + h) * BOX, false, h, p.b_mn ? n[h] : k, p.b_mn ? k : n[h]);
+    load(h * BOX, true, h, a_mn ? mm : k, a_mn ? k : mm);
+    load((2 + h) * BOX, false, h, b_mn ? n[h] : k, b_mn ? k : n[h]);
   }
 }
 
+__device__ __forceinline__ uint32_t idesc_of(const Args& a, const Problem& p, int m, int n) {
+  return idesc_f32acc(m, n, !a.f16) | (p.a_mn ? IDESC_A_MN : 0u) | (p.b_mn ? IDESC_B_MN : 0u);
+}
+
+// One 128 x 128 tile a CTA, or a cluster of S = 2, 4 or 8 CTAs a tile, each with a run of the k-blocks: their sums meet in
+// distributed shared memory, 32 x 32 blocks of the tile shared out among the CTAs' epilogue warps, and are added in CTA
+// order.
 template <typename E>
-__global__ void __launch_bounds__(THREADS<One>, 2) k_gemm(const Args a, const __grid_constant__ Maps maps, const typename E::Args e) {
+__global__ void __launch_bounds__(THREADS<One>, 2)
+    k_gemm(const Args a, const __grid_constant__ AllMaps<E::MAPS> all, const typename E::Args e) {
   extern __shared__ uint8_t dsmem[];
   constexpr int ST = One::STAGES;
   __shared__ uint64_t full[ST], empty[ST], acc_full;
@@ -151,67 +230,139 @@ __global__ void __launch_bounds__(THREADS<One>, 2) k_gemm(const Args a, const __
   const uint32_t tmem = tmem_base;
   pdl_wait();
   pdl_trigger();
-  if (a.clear && threadIdx.x == 0 && blockIdx.x + blockIdx.y + blockIdx.z == 0) *a.status = 0;
-  constexpr int COLS = E::PAIR ? One::TN / 2 : One::TN;
-  const int m0 = blockIdx.y * One::TM, n0 = blockIdx.x * COLS, z = blockIdx.z;
-  const int blocks = a.p.kb[0] + a.p.kb[1];
+  if (a.clear && threadIdx.x == 0 && blockIdx.x + blockIdx.y == 0) *a.status = 0;
+  // (x: the CTAs of a tile, y: tiles)
+  const int S = gridDim.x, rank = blockIdx.x;
+  const Walk<One, E::PAIR> w(a, blockIdx.y);
+  const Problem& p = a.p[w.i];
+  const Maps& maps = all.of[w.i];
+  const int blocks = p.blocks(), b0 = blocks * rank / S, b1 = blocks * (rank + 1) / S;
+  const int m0 = w.m * One::TM, n0 = w.n * w.COLS;
   if (warp == 0) {
     if (lane == 0) {
       const int n[2] = {n0, E::PAIR ? n0 : n0 + 64};
-      int i = 0;
-      for (; i < blocks; ++i) {
-        const int s = i % ST, seg = i >= a.p.kb[0] ? 1 : 0, k = (seg ? i - a.p.kb[0] : i) * BK;
+      const bool a_mn = p.a_mn, b_mn = p.b_mn;
+      const int per = p.kb;
+      int i = 0, seg = b0 / per, kb = b0 - seg * per;
+      const CUtensorMap *am = &maps.a[(p.a_of >> seg) & 1], *bm = &maps.b[(p.b_of >> seg) & 1];
+      for (; i < b1 - b0; ++i, ++kb) {
+        const int s = i % ST;
+        if (kb == per) {
+          kb = 0;
+          ++seg;
+          am = &maps.a[(p.a_of >> seg) & 1], bm = &maps.b[(p.b_of >> seg) & 1];
+        }
         if (i >= ST && !wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, a.status)) break;
         const uint32_t sm = base + s * STAGE;
         mbar_arrive_expect_tx(&full[s], STAGE);
-        load_stage(a.p, k, m0, n, [&](int off, bool is_a, int h, int x, int y) {
-          tma_load_3d(sm + off, is_a ? &maps.a[seg] : &maps.b[E::PAIR ? h : seg], x, y, z, &full[s]);
+        load_stage(a_mn, b_mn, kb * BK, m0, n, [&](int off, bool is_a, int h, int x, int y) {
+          tma_load_3d(sm + off, is_a ? am : E::PAIR ? &maps.b[h] : bm, x, y, w.z, &full[s]);
         });
       }
       for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&full[r % ST], (r / ST) & 1);
     }
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_f32acc(One::TM, One::TN, !a.f16) | (a.p.a_mn ? IDESC_A_MN : 0u) | (a.p.b_mn ? IDESC_B_MN : 0u);
-    const Operand oa = operand(a.p.a_mn), ob = operand(a.p.b_mn);
+    const uint32_t idesc = idesc_of(a, p, One::TM, One::TN);
+    const Operand oa = operand(p.a_mn), ob = operand(p.b_mn);
     int i = 0;
-    for (; i < blocks; ++i) {
+    for (; i < b1 - b0; ++i) {
       const int s = i % ST;
       const bool ok = wait_ab(&full[s], (i / ST) & 1, abort, a.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t ad = oa.desc | ((base + s * STAGE) >> 4), bd = ob.desc | ((base + s * STAGE + 2 * BOX) >> 4);
+        const uint64_t ad = oa.at(base + s * STAGE), bd = ob.at(base + s * STAGE + 2 * BOX);
 #pragma unroll
         for (int ks = 0; ks < BK / 16; ++ks) tc_mma(tmem, ad + ks * oa.step, bd + ks * ob.step, idesc, (i > 0 || ks > 0) ? 1u : 0u);
         tc_commit(&empty[s]);
-        if (i + 1 == blocks) tc_commit(&acc_full);
+        if (i + 1 == b1 - b0) tc_commit(&acc_full);
       }
       __syncwarp();
     }
     for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&empty[r % ST], (r / ST) & 1);
-  } else {
-    const bool ok = wait_ab(&acc_full, 0, abort, a.status);
-    if (__all_sync(0xffffffffu, ok)) {
-      tc_fence_after();
-      const int q = warp & 3;
-      Part t;
-      t.tmem = tmem + ((uint32_t)(q * 32) << 16);
+  }
+  // The epilogue's warps: slots and partial sums lie where the operands were.
+  const int q = warp & 3;
+  uint32_t w1[32], w2[32];
+  Part t;
+  t.n0 = n0;
+  t.z = w.z;
+  t.M = p.M;
+  t.N = p.N;
+  t.twice = p.sym && w.m != w.n;
+  t.lane = lane;
+  t.sm_addr = base + q * SLOTS * SLOT;
+  t.sm = dsmem + (t.sm_addr - smem_addr(dsmem));
+  t.slot = 0;
+  constexpr int CHUNKS = Walk<One, E::PAIR>::COLS / 32;
+  if (warp >= 2) {
+    bool ok = wait_ab(&acc_full, 0, abort, a.status);
+    ok = __all_sync(0xffffffffu, ok);
+    const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16);
+    tc_fence_after();
+    if (S == 1) {
       t.row0 = m0 + q * 32;
       t.row = t.row0 + lane;
-      t.n0 = n0;
-      t.group = 0;
-      t.z = z;
-      t.M = a.p.M;
-      t.N = a.p.N;
-      t.lane = lane;
-      t.sm_addr = base + q * SLOTS * SLOT;  // the tile's operands have been used
-      t.sm = dsmem + (t.sm_addr - smem_addr(dsmem));
-      t.slot = 0;
-      if (t.row0 < t.M) E::template run<One>(e, maps, t, [] {});
-      if (lane == 0) bulk_wait_all();
-      tc_fence_before();
+      if (ok && t.row0 < t.M)
+#pragma unroll 1
+        for (int c = 0; c < w.COLS; c += 32) {
+          tc_ld32_async(acc + c, w1);
+          if constexpr (E::PAIR) tc_ld32_async(acc + One::TN / 2 + c, w2);
+          const typename E::Pre pre(e, t, c);
+          tc_wait_ld();
+          E::chunk(e, maps, t, c, w1, w2, pre);
+        }
+    } else if (ok) {
+      // Row r's four columns 4 c .. at piece c * 128 + r, behind the slots.
+      float4* part = reinterpret_cast<float4*>(dsmem + (base - smem_addr(dsmem)) + 4 * SLOTS * SLOT) + q * 32 + lane;
+#pragma unroll 1
+      for (int c = 0; c < One::TN; c += 32) {
+        tc_ld32_async(acc + c, w1);
+        tc_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          part[(c / 4 + j) * 128] = make_float4(__uint_as_float(w1[4 * j]), __uint_as_float(w1[4 * j + 1]),
+                                                __uint_as_float(w1[4 * j + 2]), __uint_as_float(w1[4 * j + 3]));
+      }
     }
+    tc_fence_before();
   }
+  if (S > 1) {
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2) {
+      const uint32_t part = base + 4 * SLOTS * SLOT;
+      for (int u = rank * 4 + q; u < 4 * CHUNKS; u += 4 * S) {  // block u of the tile: rows 32 (u % 4), columns 32 (u / 4)
+        t.row0 = m0 + (u & 3) * 32;
+        t.row = t.row0 + lane;
+        if (t.row0 >= t.M) continue;
+        const int c = (u >> 2) * 32;
+        const typename E::Pre pre(e, t, c);
+        auto sums = [&](int col, uint32_t (&v)[32]) {
+          float acc[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[j] = 0.f;
+#pragma unroll 1
+          for (int r = 0; r < S; ++r) {
+            const uint32_t at = dsmem_addr(part + (uint32_t)((col / 4 * 128 + (u & 3) * 32 + lane) * 16), r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 f = ld_dsmem_f4(at + j * 2048);
+              acc[4 * j] += f.x, acc[4 * j + 1] += f.y, acc[4 * j + 2] += f.z, acc[4 * j + 3] += f.w;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(acc[j]);
+        };
+        sums(c, w1);
+        if constexpr (E::PAIR) sums(One::TN / 2 + c, w2);
+        E::chunk(e, maps, t, c, w1, w2, pre);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // the other CTAs have read this one's sums
+  }
+  if (warp >= 2 && lane == 0) bulk_wait_all();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -255,23 +406,9 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Tiles in bands of eight rows of tiles, column by column: the tiles that run at once share their operands in L2.
-struct Walk {
-  int mt, nt;  // tiles down and across
-  __device__ __forceinline__ void at(int t, int& m, int& n, int& z) const {
-    const int per = mt * nt;
-    z = t / per;
-    t -= z * per;
-    const int band = t / (8 * nt), first = band * 8, rows = min(8, mt - first);
-    t -= band * 8 * nt;
-    n = t / rows;
-    m = first + t - n * rows;
-  }
-};
-
 template <typename E>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
-    k_gemm_pair(const Args a, const __grid_constant__ Maps maps, const typename E::Args e) {
+    k_gemm_pair(const Args a, const __grid_constant__ AllMaps<E::MAPS> all, const typename E::Args e) {
   extern __shared__ uint8_t dsmem[];
   constexpr int ST = Two::STAGES, EPI = 4 * Two::GROUPS;
   __shared__ uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2];
@@ -302,29 +439,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
   pdl_wait();
   pdl_trigger();
   if (a.clear && threadIdx.x == 0 && blockIdx.x == 0) *a.status = 0;
-  constexpr int COLS = E::PAIR ? Two::TN / 2 : Two::TN;
-  const Walk walk = {(a.p.M + Two::TM - 1) / Two::TM, (a.p.N + COLS - 1) / COLS};
-  const int tiles = walk.mt * walk.nt * a.batch, step = gridDim.x >> 1, first = blockIdx.x >> 1;
-  const int blocks = a.p.kb[0] + a.p.kb[1];
+  using W = Walk<Two, E::PAIR>;
+  const int tiles = (int)W::tiles(a), step = gridDim.x >> 1, first = blockIdx.x >> 1;
   if (warp == 0) {
     if (lane == 0) {
-      int i = 0;  // stages so far
+      int i = 0, s = 0;  // stages so far, the next one's place
+      uint32_t phase = 0;
+      const uint32_t bar0 = dsmem_addr(smem_addr(full), 0);
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
-        int mi, ni, z;
-        walk.at(t, mi, ni, z);
+        const W w(a, t);
+        const Problem& p = a.p[w.i];
+        const Maps& maps = all.of[w.i];
         // The first CTA holds the tile's columns 0 .. 127 of B (or the gate's rows), the second the others.
-        const int m = mi * Two::TM + (int)rank * 128, nb = ni * COLS + (E::PAIR ? 0 : (int)rank * 128);
-        const int n[2] = {nb, nb + 64};
-        for (int kb = 0; kb < blocks; ++kb, ++i) {
-          const int s = i % ST, seg = kb >= a.p.kb[0] ? 1 : 0, k = (seg ? kb - a.p.kb[0] : kb) * BK;
-          if (i >= ST && !(ok = wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, a.status))) break;
-          const uint32_t sm = base + s * STAGE, bar = dsmem_addr(smem_addr(&full[s]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE);
-          const CUtensorMap *am = &maps.a[seg], *bm = &maps.b[E::PAIR ? rank : seg];
-          load_stage(a.p, k, m, n, [&](int off, bool is_a, int, int x, int y) {
-            tma_load_3d_pair(sm + off, is_a ? am : bm, x, y, z, bar);
-          });
+        const int m = w.m * Two::TM + (int)rank * 128, nb = w.n * W::COLS + (E::PAIR ? 0 : (int)rank * 128);
+        const int n[2] = {nb, nb + 64}, per = p.kb;
+        const bool a_mn = p.a_mn, b_mn = p.b_mn;
+        for (int seg = 0; seg < p.segs && ok; ++seg) {
+          const CUtensorMap *am = &maps.a[(p.a_of >> seg) & 1], *bm = &maps.b[E::PAIR ? rank : (p.b_of >> seg) & 1];
+          for (int kb = 0; kb < per; ++kb) {
+            if (i >= ST && !(ok = wait_ab(&empty[s], phase ^ 1, abort, a.status))) break;
+            const uint32_t sm = base + s * STAGE, bar = bar0 + s * 8;
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE);
+            load_stage(a_mn, b_mn, kb * BK, m, n,
+                       [&](int off, bool is_a, int, int x, int y) { tma_load_3d_pair(sm + off, is_a ? am : bm, x, y, w.z, bar); });
+            ++i;
+            if (++s == ST) s = 0, phase ^= 1;
+          }
         }
       }
       // The second CTA's copies count on the first's barriers: it stays until the first has seen them (cluster_sync).
@@ -333,22 +474,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      const uint32_t idesc = idesc_f32acc(Two::TM, Two::TN, !a.f16) | (a.p.a_mn ? IDESC_A_MN : 0u) | (a.p.b_mn ? IDESC_B_MN : 0u);
-      const Operand oa = operand(a.p.a_mn), ob = operand(a.p.b_mn);
-      int i = 0, n = 0;  // stages and tiles so far
+      int i = 0, n = 0, s = 0;  // stages and tiles so far, the next stage's place
+      uint32_t phase = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step, ++n) {
+        const Problem& p = a.p[W(a, t).i];
+        const uint32_t idesc = idesc_of(a, p, Two::TM, Two::TN);
+        const Operand oa = operand(p.a_mn), ob = operand(p.b_mn);
+        const int blocks = p.blocks();
         const int b = n & 1;
         ok = n < 2 || wait_ab(&acc_empty[b], ((n >> 1) - 1) & 1, abort, a.status);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         for (int kb = 0; kb < blocks; ++kb, ++i) {
-          const int s = i % ST;
-          ok = wait_ab(&full[s], (i / ST) & 1, abort, a.status);
+          ok = wait_ab(&full[s], phase, abort, a.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t ad = oa.desc | ((base + s * STAGE) >> 4), bd = ob.desc | ((base + s * STAGE + 2 * BOX) >> 4);
+            const uint64_t ad = oa.at(base + s * STAGE), bd = ob.at(base + s * STAGE + 2 * BOX);
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks)
               tc_mma_pair(tmem + b * Two::TN, ad + ks * oa.step, bd + ks * ob.step, idesc, (kb > 0 || ks > 0) ? 1u : 0u);
@@ -356,6 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
             if (kb + 1 == blocks) tc_commit_pair(&acc_full[b]);
           }
           __syncwarp();
+          if (++s == ST) s = 0, phase ^= 1;
         }
       }
       for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&empty[r % ST], (r / ST) & 1);
@@ -363,34 +507,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
   } else {
     const int q = warp & 3, group = (warp - 2) >> 2;
     Part t;
-    t.group = group;
-    t.M = a.p.M;
-    t.N = a.p.N;
     t.lane = lane;
     t.sm_addr = base + ST * STAGE + (uint32_t)((warp - 2) * SLOTS * SLOT);
     t.sm = dsmem + (t.sm_addr - smem_addr(dsmem));
     t.slot = 0;
+    uint32_t w1[32], w2[32];
     int n = 0;
     for (int ti = first; ti < tiles; ti += step, ++n) {
       const int b = n & 1;
-      int mi, ni;
-      walk.at(ti, mi, ni, t.z);
+      const W w(a, ti);
+      const Problem& p = a.p[w.i];
+      t.z = w.z;
+      t.M = p.M;
+      t.N = p.N;
+      t.n0 = w.n * W::COLS;
+      t.row0 = w.m * Two::TM + (int)rank * 128 + q * 32;
+      t.row = t.row0 + lane;
+      t.twice = p.sym && w.m != w.n;
       const bool ok = wait_ab(&acc_full[b], (n >> 1) & 1, abort, a.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      t.row0 = mi * Two::TM + (int)rank * 128 + q * 32;
-      t.row = t.row0 + lane;
-      t.n0 = ni * COLS;
-      t.tmem = tmem + b * Two::TN + ((uint32_t)(q * 32) << 16);
-      bool freed = false;
-      auto release = [&] {  // this warp has read the accumulator
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_addr(&acc_empty[b]), 0));
-        freed = true;
-      };
-      if (t.row0 < t.M) E::template run<Two>(e, maps, t, release);
-      if (!freed) release();
+      const uint32_t acc = tmem + b * Two::TN + ((uint32_t)(q * 32) << 16);
+      constexpr int EACH = W::COLS / Two::GROUPS;
+      const bool live = t.row0 < t.M;
+#pragma unroll 1
+      for (int c = group * EACH; c < (group + 1) * EACH; c += 32) {
+        const bool last = c + 32 == (group + 1) * EACH;
+        if (live) {
+          tc_ld32_async(acc + c, w1);
+          if constexpr (E::PAIR) tc_ld32_async(acc + Two::TN / 2 + c, w2);
+        }
+        const typename E::Pre pre(e, t, c);
+        tc_wait_ld();
+        if (last) {  // this warp has read the accumulator
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_addr(&acc_empty[b]), 0));
+        }
+        if (live) E::chunk(e, all.of[w.i], t, c, w1, w2, pre);
+      }
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -435,20 +590,24 @@ bool prepare(size_t smem) {
   return true;
 }
 
-// A launch that may start while the kernel before it drains (each kernel waits for it itself).
+// A launch that may start while the kernel before it drains (each kernel waits for it itself), in clusters of `cx`.
 template <auto KERNEL, typename... P>
-bool launch(dim3 grid, int block, size_t smem, cudaStream_t stream, const P&... args) {
+bool launch(dim3 grid, int block, size_t smem, int cx, cudaStream_t stream, const P&... args) {
   if (!prepare<KERNEL>(smem)) return false;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cx;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cx > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, KERNEL, args...) == cudaSuccess;
 }
 
@@ -459,17 +618,34 @@ inline int sm_count() {
   return n;
 }
 
+// How a launch's products are computed: by pairs of CTAs where their tiles fill the card, or else by S CTAs a tile, as many
+// as run one on an SM and have four k-blocks each: 77 tokens of 2048 x 8192 36.7 us a call and 72.6 with one CTA a tile;
+// 509 of 1000 x 2040 21.4, 27.7, and 28.7 with two on an SM.
+struct Choice {
+  bool pair;
+  int S;
+};
 template <typename E>
-bool run(const Args& a, const Maps& m, const typename E::Args& e, cudaStream_t stream) {
-  auto tiles = [&](int tm, int tn) {
-    const int cols = E::PAIR ? tn / 2 : tn;
-    return dim3((unsigned)((a.p.N + cols - 1) / cols), (unsigned)((a.p.M + tm - 1) / tm), (unsigned)a.batch);
-  };
-  const dim3 one = tiles(One::TM, One::TN), two = tiles(Two::TM, Two::TN);
-  const int64_t pairs = (int64_t)two.x * two.y * two.z, most = sm_count() / 2;
-  if (pairs >= most)
-    return launch<k_gemm_pair<E>>(dim3(2 * (unsigned)std::min(pairs, most)), THREADS<Two>, SMEM<Two>, stream, a, m, e);
-  return launch<k_gemm<E>>(one, THREADS<One>, SMEM<One>, stream, a, m, e);
+Choice choose(const Args& a) {
+  const int64_t pairs = Walk<Two, E::PAIR>::tiles(a), ones = Walk<One, E::PAIR>::tiles(a), most = sm_count() / 2;
+  if (pairs >= most) return {true, 1};
+  int blocks = 1 << 30, S = 1;
+  for (int i = 0; i < a.n; ++i) blocks = std::min(blocks, a.p[i].blocks());
+  while (S < 8 && ones * S * 2 <= 2 * most && S * 8 <= blocks) S *= 2;
+  return {false, S};
+}
+
+template <typename E>
+bool run(const Args& a, const AllMaps<E::MAPS>& m, const typename E::Args& e, cudaStream_t stream, const Choice& c) {
+  if (c.pair) {
+    const int64_t pairs = std::min<int64_t>(Walk<Two, E::PAIR>::tiles(a), sm_count() / 2);
+    return launch<k_gemm_pair<E>>(dim3(2 * (unsigned)pairs), THREADS<Two>, SMEM<Two>, 0, stream, a, m, e);
+  }
+  return launch<k_gemm<E>>(dim3(c.S, (unsigned)Walk<One, E::PAIR>::tiles(a)), THREADS<One>, SMEM<One>, c.S, stream, a, m, e);
+}
+template <typename E>
+bool run(const Args& a, const AllMaps<E::MAPS>& m, const typename E::Args& e, cudaStream_t stream) {
+  return run<E>(a, m, e, stream, choose<E>(a));
 }
 
 }  // namespace gemm

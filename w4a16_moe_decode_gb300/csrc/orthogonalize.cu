@@ -154,59 +154,60 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_split(const Start a) {
 // ---------------------------------------------------------------------------
 struct Gram {
   static constexpr bool PAIR = false;
+  static constexpr int MAPS = 1;
   struct Args {};
-  template <typename C, typename Release>
-  static __device__ __forceinline__ void run(const Args&, const Maps& maps, Part& t, Release release) {
-#pragma unroll 1
-    for (int c = 128 * t.group; c < 128 * t.group + 128; c += 32) {
-      uint32_t w[32];
-      tc_ld32_async(t.tmem + c, w);
-      tc_wait_ld();
-      if ((c & 127) == 96) release();
-      float* v = reinterpret_cast<float*>(w);
+  struct Pre {
+    __device__ __forceinline__ Pre(const Args&, const Part&, int) {}
+  };
+  static __device__ __forceinline__ void chunk(const Args&, const Maps& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
+                                               const Pre&) {
+    float* v = reinterpret_cast<float*>(w);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] *= S_SCALE / (X_SCALE * X_SCALE);
-      const uint4 o[4] = {pack8_f16(v), pack8_f16(v + 8), pack8_f16(v + 16), pack8_f16(v + 24)};
-      t.put(&maps.out[0], t.n0 + c, o);
-    }
+    for (int j = 0; j < 32; ++j) v[j] *= S_SCALE / (X_SCALE * X_SCALE);
+    const uint4 o[4] = {pack8_f16(v), pack8_f16(v + 8), pack8_f16(v + 16), pack8_f16(v + 24)};
+    t.put(&maps.out[0], t.n0 + c, o);
+    if (t.twice) t.put_transposed(&maps.out[0], t.n0 + c, o);
   }
 };
 
-// Pieces c, c + 8, .. of this lane's row of a matrix (columns from `at` on, the tile's column c first); zero outside.
-__device__ __forceinline__ void load_row(const Part& t, const uint16_t* at, int c, uint4 (&v)[4]) {
+// 32 columns of this lane's row of a matrix [batch][M][pitch], from the tile's column c on; zero outside.
+__device__ __forceinline__ void load_row(const Part& t, const uint16_t* m, int pitch, int c, uint4 (&v)[4]) {
+  const uint16_t* at = m + ((size_t)t.z * t.M + t.row) * pitch + t.n0 + c;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    v[j] = t.row < t.M && t.n0 + c + 8 * j < t.N ? __ldcg(reinterpret_cast<const uint4*>(at + c + 8 * j)) : make_uint4(0, 0, 0, 0);
+    v[j] = t.row < t.M && t.n0 + c + 8 * j < t.N ? __ldcg(reinterpret_cast<const uint4*>(at + 8 * j)) : make_uint4(0, 0, 0, 0);
 }
 
 struct Poly {
   static constexpr bool PAIR = false;
+  static constexpr int MAPS = 1;
   struct Args {
-    const uint16_t* s;  // [batch][M][pitch]
+    const uint16_t* s;
     int pitch;
     float b, c;
+    int lo;  // P's second half too
   };
-  template <typename C, typename Release>
-  static __device__ __forceinline__ void run(const Args& a, const Maps& maps, Part& t, Release release) {
-    const uint16_t* s = a.s + ((size_t)t.z * t.M + t.row) * a.pitch + t.n0;
+  struct Pre {
+    uint4 s[4];
+    __device__ __forceinline__ Pre(const Args& a, const Part& t, int c) { load_row(t, a.s, a.pitch, c, s); }
+  };
+  static __device__ __forceinline__ void chunk(const Args& a, const Maps& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
+                                               const Pre& pre) {
     const float fs = a.b * (P_SCALE / S_SCALE), fq = a.c * (P_SCALE / (S_SCALE * S_SCALE));
-#pragma unroll 1
-    for (int c = 128 * t.group; c < 128 * t.group + 128; c += 32) {
-      uint32_t w[32];
-      tc_ld32_async(t.tmem + c, w);
-      uint4 sv[4], o[4];
-      load_row(t, s, c, sv);
-      tc_wait_ld();
-      if ((c & 127) == 96) release();
+    uint4 hi[4], lo[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float v[8];
-        unpack8_f16(sv[j], v);
+    for (int j = 0; j < 4; ++j) {
+      float v[8];
+      unpack8_f16(pre.s[j], v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaf(fs, v[i], fq * __uint_as_float(w[8 * j + i]));
-        o[j] = pack8_f16(v);
-      }
-      t.put(&maps.out[0], t.n0 + c, o);
+      for (int i = 0; i < 8; ++i) v[i] = fmaf(fs, v[i], fq * __uint_as_float(w[8 * j + i]));
+      split8(v, hi[j], lo[j]);
+    }
+    t.put(&maps.out[0], t.n0 + c, hi);
+    if (t.twice) t.put_transposed(&maps.out[0], t.n0 + c, hi);
+    if (a.lo) {
+      t.put(&maps.out[1], t.n0 + c, lo);
+      if (t.twice) t.put_transposed(&maps.out[1], t.n0 + c, lo);
     }
   }
 };
@@ -214,54 +215,52 @@ struct Poly {
 template <bool LAST>
 struct Update {
   static constexpr bool PAIR = false;
+  static constexpr int MAPS = 1;
   struct Args {
-    const uint16_t *hi, *lo;  // [batch][M][pitch]
+    const uint16_t *hi, *lo;
     int pitch;
     float a, scale;
     uint16_t* out;  // LAST: [batch][M][N]
   };
-  template <typename C, typename Release>
-  static __device__ __forceinline__ void run(const Args& a, const Maps& maps, Part& t, Release release) {
-    const size_t at = ((size_t)t.z * t.M + t.row) * a.pitch + t.n0;
+  struct Pre {
+    uint4 hi[4], lo[4];
+    __device__ __forceinline__ Pre(const Args& a, const Part& t, int c) {
+      load_row(t, a.hi, a.pitch, c, hi);
+      load_row(t, a.lo, a.pitch, c, lo);
+    }
+  };
+  static __device__ __forceinline__ void chunk(const Args& a, const Maps& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
+                                               const Pre& pre) {
     constexpr float fp = 1.0f / P_SCALE;  // P X comes scaled by both
-#pragma unroll 1
-    for (int c = 128 * t.group; c < 128 * t.group + 128; c += 32) {
-      uint32_t w[32];
-      tc_ld32_async(t.tmem + c, w);
-      uint4 hv[4], lv[4];
-      load_row(t, a.hi + at, c, hv);
-      load_row(t, a.lo + at, c, lv);
-      tc_wait_ld();
-      if ((c & 127) == 96) release();
+    uint4 hv[4], lv[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float h[8], l[8], v[8];
-        unpack8_f16(hv[j], h);
-        unpack8_f16(lv[j], l);
+    for (int j = 0; j < 4; ++j) {
+      float h[8], l[8], v[8];
+      unpack8_f16(pre.hi[j], h);
+      unpack8_f16(pre.lo[j], l);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaf(fp, __uint_as_float(w[8 * j + i]), a.a * (h[i] + l[i]));
-        if (LAST) {
+      for (int i = 0; i < 8; ++i) v[i] = fmaf(fp, __uint_as_float(w[8 * j + i]), a.a * (h[i] + l[i]));
+      if (LAST) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] *= a.scale;
-          hv[j] = pack8_bf16(v);
-        } else {
-          split8(v, hv[j], lv[j]);
-        }
+        for (int i = 0; i < 8; ++i) v[i] *= a.scale;
+        hv[j] = pack8_bf16(v);
+      } else {
+        split8(v, hv[j], lv[j]);
       }
-      if (!LAST || t.N % 8 == 0) {
-        t.put(&maps.out[0], t.n0 + c, hv);
-        if (!LAST) t.put(&maps.out[1], t.n0 + c, lv);
-      } else {  // rows that TMA cannot reach: through a slot, a row's neighbours by neighbouring lanes
-        __syncwarp();
+    }
+    if (!LAST || t.N % 8 == 0) {
+      t.put(&maps.out[0], t.n0 + c, hv);
+      if (!LAST) t.put(&maps.out[1], t.n0 + c, lv);
+    } else {  // rows that TMA cannot reach: through a slot, a row's neighbours by neighbouring lanes
+      __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) *t.piece(0, j) = hv[j];
-        __syncwarp();
-        const int col = t.n0 + c + t.lane;
-        for (int r = 0; r < 32 && t.row0 + r < t.M; ++r)
-          if (col < t.N)
-            a.out[((size_t)t.z * t.M + t.row0 + r) * t.N + col] =
-                *reinterpret_cast<const uint16_t*>(t.sm + r * 64 + ((((t.lane >> 3) ^ (r >> 1)) & 3) << 4) + (t.lane & 7) * 2);
-      }
+      for (int j = 0; j < 4; ++j) *t.piece(0, j) = hv[j];
+      __syncwarp();
+      const int col = t.n0 + c + t.lane;
+      for (int r = 0; r < 32 && t.row0 + r < t.M; ++r)
+        if (col < t.N)
+          a.out[((size_t)t.z * t.M + t.row0 + r) * t.N + col] =
+              *reinterpret_cast<const uint16_t*>(t.sm + r * 64 + ((((t.lane >> 3) ^ (r >> 1)) & 3) << 4) + (t.lane & 7) * 2);
     }
   }
 };
@@ -288,9 +287,13 @@ int parts_of(int rows, int cols) {
   return (int)std::min<int64_t>(128, ((int64_t)rows * cols + per - 1) / per);
 }
 
+// P X as P_hi X_hi + P_lo X_hi + P_hi X_lo up to this many rows, where the products are cheap beside X's traffic and few
+// rounding errors meet in a result; above, as P_hi X_hi, whose errors average out.
+bool few_rows(int m) { return m <= 128; }
+
 struct WsPlan {
   int m, pitch, mpitch, parts;
-  size_t part, x[2][2], s, p, total;  // x: of even and odd steps, hi and lo
+  size_t part, x[2][2], s, p[2], total;  // x: of even and odd steps; x, p: hi and lo
 };
 WsPlan ws_plan(int n, int rows, int cols) {
   WsPlan w = {};
@@ -308,8 +311,10 @@ WsPlan ws_plan(int n, int rows, int cols) {
   }
   w.s = o;
   o += mb;
-  w.p = o;
-  o += mb;
+  for (int i = 0; i < 2; ++i) {
+    w.p[i] = o;
+    o += i == 0 || few_rows(w.m) ? mb : 0;
+  }
   w.total = o;
   return w;
 }
@@ -347,41 +352,46 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
   auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(wsp + o); };
   const bool tall = rows > cols;
   const int m = w.m;
-  CUtensorMap x[2][2], xout[2][2], s, sout, p, pout, o;
-  bool ok = true;
-  for (int i = 0; i < 4; ++i) {
-    const size_t off = w.x[i >> 1][i & 1];
-    ok = ok && map_matrix(&x[i >> 1][i & 1], at(off), cols, rows, w.pitch, n, (int64_t)rows * w.pitch, false) &&
-         map_matrix(&xout[i >> 1][i & 1], at(off), cols, rows, w.pitch, n, (int64_t)rows * w.pitch, true);
+  CUtensorMap x[2][2], xout[2][2], s, sout, p[2], pout[2], o;
+  auto map = [&](CUtensorMap* mp, size_t off, int64_t c, int64_t r, int64_t pitch, bool as_out) {
+    return map_matrix(mp, at(off), c, r, pitch, n, r * pitch, as_out);
+  };
+  bool ok = map(&s, w.s, m, m, w.mpitch, false) && map(&sout, w.s, m, m, w.mpitch, true);
+  for (int i = 0; i < 2; ++i) {
+    for (int h = 0; h < 2; ++h)
+      ok = ok && map(&x[i][h], w.x[i][h], cols, rows, w.pitch, false) && map(&xout[i][h], w.x[i][h], cols, rows, w.pitch, true);
+    ok = ok && map(&p[i], w.p[i], m, m, w.mpitch, false) && map(&pout[i], w.p[i], m, m, w.mpitch, true);
   }
-  for (int i = 0; i < 2; ++i)
-    ok = ok && map_matrix(i ? &sout : &s, at(w.s), m, m, w.mpitch, n, (int64_t)m * w.mpitch, i) &&
-         map_matrix(i ? &pout : &p, at(w.p), m, m, w.mpitch, n, (int64_t)m * w.mpitch, i);
-  o = pout;
+  o = sout;
   if (cols % 8 == 0) ok = ok && map_matrix(&o, out, cols, rows, cols, n, (int64_t)rows * cols, true);
   if (!ok) return FLINT_MOE_ECUDA;
-  auto maps = [](const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
-                 const CUtensorMap& o0, const CUtensorMap& o1) {
-    Maps mm;
-    mm.a[0] = a0, mm.a[1] = a1, mm.b[0] = b0, mm.b[1] = b1, mm.out[0] = o0, mm.out[1] = o1, mm.out[2] = o1;
-    return mm;
-  };
   const Start st = {in, fmt == FLINT_ORTHOGONALIZE_BF16, n, rows, cols, w.pitch, w.parts, eps,
                     reinterpret_cast<double*>(wsp + w.part), at(w.x[0][0]), at(w.x[0][1]), status};
   const dim3 grid((unsigned)w.parts, (unsigned)n);
-  if (!launch<k_ortho_norm>(grid, START_THREADS, 0, stream, st) || !launch<k_ortho_split>(grid, START_THREADS, 0, stream, st))
+  if (!launch<k_ortho_norm>(grid, START_THREADS, 0, 0, stream, st) || !launch<k_ortho_split>(grid, START_THREADS, 0, 0, stream, st))
     return FLINT_MOE_ECUDA;
   const int kx = ((tall ? rows : cols) + BK - 1) / BK, km = (m + BK - 1) / BK;
+  AllMaps<1> mg, mp, mu;
+  mp.of[0].a[0] = mp.of[0].b[0] = s;
+  mg.of[0].out[0] = sout;
+  const bool few = few_rows(m);
+  for (int h = 0; h < 2; ++h) {
+    mp.of[0].out[h] = pout[h];
+    (tall ? mu.of[0].b : mu.of[0].a)[h] = p[h];
+  }
   for (int i = 0; i < steps; ++i) {
-    const CUtensorMap *xi = x[i & 1], *xo = xout[(i + 1) & 1];
     const float* cf = coeffs + 3 * i;
     const bool last = i + 1 == steps;
     // S = X X^T (X^T X), both operands the same matrix; P from S, which is its own transpose; X's rows times P, or P times X
-    ok = run<Gram>({{m, m, {kx, 0}, tall, tall}, 1, n, status, 0}, maps(xi[0], xi[0], xi[0], xi[0], sout, sout), {}, stream) &&
-         run<Poly>({{m, m, {km, 0}, 0, 0}, 1, n, status, 0}, maps(s, s, s, s, pout, pout), {at(w.s), w.mpitch, cf[1], cf[2]}, stream);
-    const Args upd = {{rows, cols, {km, last ? 0 : km}, 0, !tall}, 1, n, status, 0};
-    const CUtensorMap &o0 = last ? o : xo[0], &o1 = last ? o : xo[1];
-    const Maps mu = tall ? maps(xi[0], xi[1], p, p, o0, o1) : maps(p, p, xi[0], xi[1], o0, o1);
+    mg.of[0].a[0] = mg.of[0].b[0] = x[i & 1][0];
+    for (int h = 0; h < 2; ++h) {
+      (tall ? mu.of[0].a : mu.of[0].b)[h] = x[i & 1][h];
+      mu.of[0].out[h] = last ? o : xout[(i + 1) & 1][h];
+    }
+    ok = run<Gram>({{{m, m, kx, 1, 0, 0, tall, tall, 1, n}}, 1, 1, status, 0}, mg, {}, stream) &&
+         run<Poly>({{{m, m, km, 1, 0, 0, 0, 0, 1, n}}, 1, 1, status, 0}, mp, {at(w.s), w.mpitch, cf[1], cf[2], few}, stream);
+    const int p_of = 2, x_of = 4;  // hi hi, then P_lo, then X_lo
+    const gemm::Args upd = {{{rows, cols, km, few ? 3 : 1, tall ? x_of : p_of, tall ? p_of : x_of, 0, !tall, 0, n}}, 1, 1, status, 0};
     const uint16_t *hi = at(w.x[i & 1][0]), *lo = at(w.x[i & 1][1]);
     ok = ok && (last ? run<Update<true>>(upd, mu, {hi, lo, w.pitch, cf[0], scale / X_SCALE, out}, stream)
                      : run<Update<false>>(upd, mu, {hi, lo, w.pitch, cf[0], 1.0f, nullptr}, stream));
