@@ -25,7 +25,9 @@
  * 256-byte aligned (FLINT_MOE_EALIGN). Inputs must be finite; a matrix of zeros
  * gives zeros. A workspace needs no initialisation, holds nothing between
  * calls, and must not be shared by calls in flight at the same time. Results do
- * not depend on timing. A device-side wait that gave up sets
+ * not depend on timing, nor a matrix's on the others of its batch; the batch's
+ * size decides how long sums are split, and with it the last bits of larger
+ * matrices. A device-side wait that gave up sets
  * FLINT_MOE_DEV_ERR_TIMEOUT in the workspace's status word
  * (flint_moe_read_status), which each call clears.
  */
@@ -49,8 +51,8 @@ typedef enum { FLINT_ORTHOGONALIZE_F32 = 0, FLINT_ORTHOGONALIZE_BF16 = 1 } flint
 size_t flint_orthogonalize_workspace_bytes(int32_t n_mat, int32_t rows, int32_t cols);
 
 /* in: float32 or bf16 (in_fmt) [n_mat][rows][cols], out: bf16, the same shape;
- * out may be in, and any other overlap of the two is allowed as well. coeffs:
- * HOST memory, float [steps][3] = a, b, c of each step, finite, read before the
+ * out may be in (bf16), any other overlap of the two is refused
+ * (FLINT_MOE_EINVAL). coeffs: HOST memory, float [steps][3] = a, b, c of each step, finite, read before the
  * call returns; 1 <= steps <= FLINT_ORTHOGONALIZE_MAX_STEPS. eps > 0 and scale
  * finite. n_mat = 0 is a no-op; rows and cols from 1. The workspace must not
  * overlap in or out (FLINT_MOE_EINVAL). */

@@ -148,7 +148,7 @@ def test_orthogonalize_refusals(lib):
     inf, nan = float("inf"), float("nan")
     for kw in (dict(m=None), dict(out=None), dict(w=None), dict(co=None), dict(steps=0), dict(steps=17), dict(eps=0.0), dict(eps=-1.0),
                dict(eps=nan), dict(eps=inf), dict(scale=nan), dict(scale=inf), dict(co=(1.0, nan, 0.0)), dict(co=(1.0, 0.0, inf)),
-               dict(nb=4096), dict(w=0x10000000), dict(w=0x20000000), dict(m=0x30000100)):
+               dict(nb=4096), dict(out=0x10000000), dict(out=0x10000010), dict(fmt=1, out=0x10000010), dict(w=0x10000000), dict(w=0x20000000), dict(m=0x30000100)):
         assert call(**kw) == fb.EINVAL, kw
     for kw in (dict(fmt=2), dict(r=0), dict(c=-1), dict(r=65537), dict(n=-1), dict(n=65536)):
         assert call(**kw) == fb.EUNSUPPORTED, kw

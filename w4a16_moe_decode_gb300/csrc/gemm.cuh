@@ -16,25 +16,32 @@ namespace gemm {
 
 constexpr int BK = 64;               // reduction of a stage: one 128-byte swizzled row of 16-bit values
 constexpr int BOX = 64 * BK * 2;     // 8 KiB: 64 x 64 values, what one TMA load moves
-constexpr int STAGE = 4 * BOX;       // a CTA's operands of a stage: 128 x 64 of A, 128 x 64 of B
 constexpr int SLOT = 32 * 64;        // 2 KiB: 32 rows x 32 columns of 16-bit values, what one TMA store moves
 constexpr int SLOTS = 4;             // of each epilogue warp
 
-// k_gemm: one 128 x 128 tile a CTA, two CTAs on an SM, so that the one's epilogue runs beside the other's products.
+// k_gemm: one 128 x 128 tile a CTA, two CTAs on an SM, so that the one's epilogue runs beside the other's products; or
+// 128 x 64.
 struct One {
-  static constexpr int TM = 128, TN = 128, CTAS = 1, STAGES = 3, GROUPS = 1;
+  static constexpr int TM = 128, TN = 128, CTAS = 1, STAGES = 3, GROUPS = 1, BBOXES = 2;
+};
+struct Half {
+  static constexpr int TM = 128, TN = 64, CTAS = 1, STAGES = 4, GROUPS = 1, BBOXES = 1;
 };
 // k_gemm_pair: 256 x 256 tiles by pairs of CTAs (cta_group::2), each with half of A's rows and half of B's, 128 x 256 sums
 // a CTA; persistent, with two accumulators, so that a tile's epilogue runs beside the next one's products.
 struct Two {
-  static constexpr int TM = 256, TN = 256, CTAS = 2, STAGES = 5, GROUPS = 2;
+  static constexpr int TM = 256, TN = 256, CTAS = 2, STAGES = 5, GROUPS = 2, BBOXES = 2;
 };
+// A CTA's operands of a stage: 128 x 64 of A, 64 BBOXES x 64 of B.
+template <typename C>
+constexpr int STAGE = (2 + C::BBOXES) * BOX;
 // Epilogue warps come in GROUPS of four (tensor memory's lanes), 128 of the accumulator's columns each.
 template <typename C>
 constexpr int THREADS = 64 + 128 * C::GROUPS;  // warp 0 loads, warp 1 issues the MMAs, the others the epilogue
 template <typename C>
-constexpr size_t SMEM = 1024 + (size_t)C::STAGES * STAGE + (C::CTAS == 2 ? (size_t)C::GROUPS * 4 * SLOTS * SLOT : 0);
-static_assert(4 * SLOTS * SLOT <= One::STAGES * STAGE, "k_gemm's epilogue writes where its operands were");
+constexpr size_t SMEM = 1024 + (size_t)C::STAGES * STAGE<C> + (C::CTAS == 2 ? (size_t)C::GROUPS * 4 * SLOTS * SLOT : 0);
+static_assert(4 * SLOTS * SLOT + One::TM * One::TN * 4 <= One::STAGES * STAGE<One> && Half::STAGES * STAGE<Half> == One::STAGES * STAGE<One>,
+              "k_gemm's epilogue writes where its operands were");
 
 constexpr int MOST = 4;  // products of one launch
 
@@ -186,13 +193,13 @@ __device__ __forceinline__ Operand operand(bool mn) {
 }
 
 // This CTA's share of a stage: rows m, m + 64 of A and n[0], n[1] of B from k on, by one thread.
-template <typename Load>
+template <typename C, typename Load>
 __device__ __forceinline__ void load_stage(bool a_mn, bool b_mn, int k, int m, const int (&n)[2], Load load) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int mm = m + 64 * h;
     load(h * BOX, true, h, a_mn ? mm : k, a_mn ? k : mm);
-    load((2 + h) * BOX, false, h, b_mn ? n[h] : k, b_mn ? k : n[h]);
+    if (h < C::BBOXES) load((2 + h) * BOX, false, h, b_mn ? n[h] : k, b_mn ? k : n[h]);
   }
 }
 
@@ -200,14 +207,14 @@ __device__ __forceinline__ uint32_t idesc_of(const Args& a, const Problem& p, in
   return idesc_f32acc(m, n, !a.f16) | (p.a_mn ? IDESC_A_MN : 0u) | (p.b_mn ? IDESC_B_MN : 0u);
 }
 
-// One 128 x 128 tile a CTA, or a cluster of S = 2, 4 or 8 CTAs a tile, each with a run of the k-blocks: their sums meet in
+// One tile a CTA, or a cluster of S = 2, 4 or 8 CTAs a tile, each with a run of the k-blocks: their sums meet in
 // distributed shared memory, 32 x 32 blocks of the tile shared out among the CTAs' epilogue warps, and are added in CTA
 // order.
-template <typename E>
-__global__ void __launch_bounds__(THREADS<One>, 2)
+template <typename C, typename E>
+__global__ void __launch_bounds__(THREADS<C>, 2)
     k_gemm(const Args a, const __grid_constant__ AllMaps<E::MAPS> all, const typename E::Args e) {
   extern __shared__ uint8_t dsmem[];
-  constexpr int ST = One::STAGES;
+  constexpr int ST = C::STAGES;
   __shared__ uint64_t full[ST], empty[ST], acc_full;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
@@ -223,7 +230,7 @@ __global__ void __launch_bounds__(THREADS<One>, 2)
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&tmem_base, One::TN);
+  if (warp == 1) tmem_alloc(&tmem_base, C::TN);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -233,11 +240,11 @@ __global__ void __launch_bounds__(THREADS<One>, 2)
   if (a.clear && threadIdx.x == 0 && blockIdx.x + blockIdx.y == 0) *a.status = 0;
   // (x: the CTAs of a tile, y: tiles)
   const int S = gridDim.x, rank = blockIdx.x;
-  const Walk<One, E::PAIR> w(a, blockIdx.y);
+  const Walk<C, E::PAIR> w(a, blockIdx.y);
   const Problem& p = a.p[w.i];
   const Maps& maps = all.of[w.i];
   const int blocks = p.blocks(), b0 = blocks * rank / S, b1 = blocks * (rank + 1) / S;
-  const int m0 = w.m * One::TM, n0 = w.n * w.COLS;
+  const int m0 = w.m * C::TM, n0 = w.n * w.COLS;
   if (warp == 0) {
     if (lane == 0) {
       const int n[2] = {n0, E::PAIR ? n0 : n0 + 64};
@@ -253,16 +260,16 @@ __global__ void __launch_bounds__(THREADS<One>, 2)
           am = &maps.a[(p.a_of >> seg) & 1], bm = &maps.b[(p.b_of >> seg) & 1];
         }
         if (i >= ST && !wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, a.status)) break;
-        const uint32_t sm = base + s * STAGE;
-        mbar_arrive_expect_tx(&full[s], STAGE);
-        load_stage(a_mn, b_mn, kb * BK, m0, n, [&](int off, bool is_a, int h, int x, int y) {
+        const uint32_t sm = base + s * STAGE<C>;
+        mbar_arrive_expect_tx(&full[s], STAGE<C>);
+        load_stage<C>(a_mn, b_mn, kb * BK, m0, n, [&](int off, bool is_a, int h, int x, int y) {
           tma_load_3d(sm + off, is_a ? am : E::PAIR ? &maps.b[h] : bm, x, y, w.z, &full[s]);
         });
       }
       for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&full[r % ST], (r / ST) & 1);
     }
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_of(a, p, One::TM, One::TN);
+    const uint32_t idesc = idesc_of(a, p, C::TM, C::TN);
     const Operand oa = operand(p.a_mn), ob = operand(p.b_mn);
     int i = 0;
     for (; i < b1 - b0; ++i) {
@@ -271,7 +278,7 @@ __global__ void __launch_bounds__(THREADS<One>, 2)
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t ad = oa.at(base + s * STAGE), bd = ob.at(base + s * STAGE + 2 * BOX);
+        const uint64_t ad = oa.at(base + s * STAGE<C>), bd = ob.at(base + s * STAGE<C> + 2 * BOX);
 #pragma unroll
         for (int ks = 0; ks < BK / 16; ++ks) tc_mma(tmem, ad + ks * oa.step, bd + ks * ob.step, idesc, (i > 0 || ks > 0) ? 1u : 0u);
         tc_commit(&empty[s]);
@@ -294,29 +301,31 @@ __global__ void __launch_bounds__(THREADS<One>, 2)
   t.sm_addr = base + q * SLOTS * SLOT;
   t.sm = dsmem + (t.sm_addr - smem_addr(dsmem));
   t.slot = 0;
-  constexpr int CHUNKS = Walk<One, E::PAIR>::COLS / 32;
+  constexpr int CHUNKS = Walk<C, E::PAIR>::COLS / 32;
   if (warp >= 2) {
-    bool ok = wait_ab(&acc_full, 0, abort, a.status);
-    ok = __all_sync(0xffffffffu, ok);
     const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16);
-    tc_fence_after();
     if (S == 1) {
       t.row0 = m0 + q * 32;
       t.row = t.row0 + lane;
-      if (ok && t.row0 < t.M)
+      typename E::Pre pre(e, t, 0);  // what a chunk reads besides the sums is asked for a chunk ahead
+      if (__all_sync(0xffffffffu, wait_ab(&acc_full, 0, abort, a.status)) && t.row0 < t.M) {
+        tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < w.COLS; c += 32) {
           tc_ld32_async(acc + c, w1);
-          if constexpr (E::PAIR) tc_ld32_async(acc + One::TN / 2 + c, w2);
-          const typename E::Pre pre(e, t, c);
+          if constexpr (E::PAIR) tc_ld32_async(acc + C::TN / 2 + c, w2);
+          const typename E::Pre now = pre;
+          if (c + 32 < w.COLS) pre = typename E::Pre(e, t, c + 32);
           tc_wait_ld();
-          E::chunk(e, maps, t, c, w1, w2, pre);
+          E::chunk(e, maps, t, c, w1, w2, now);
         }
-    } else if (ok) {
+      }
+    } else if (__all_sync(0xffffffffu, wait_ab(&acc_full, 0, abort, a.status))) {
+      tc_fence_after();
       // Row r's four columns 4 c .. at piece c * 128 + r, behind the slots.
       float4* part = reinterpret_cast<float4*>(dsmem + (base - smem_addr(dsmem)) + 4 * SLOTS * SLOT) + q * 32 + lane;
 #pragma unroll 1
-      for (int c = 0; c < One::TN; c += 32) {
+      for (int c = 0; c < C::TN; c += 32) {
         tc_ld32_async(acc + c, w1);
         tc_wait_ld();
 #pragma unroll
@@ -332,6 +341,7 @@ __global__ void __launch_bounds__(THREADS<One>, 2)
     cluster_sync();
     if (warp >= 2) {
       const uint32_t part = base + 4 * SLOTS * SLOT;
+#pragma unroll 1
       for (int u = rank * 4 + q; u < 4 * CHUNKS; u += 4 * S) {  // block u of the tile: rows 32 (u % 4), columns 32 (u / 4)
         t.row0 = m0 + (u & 3) * 32;
         t.row = t.row0 + lane;
@@ -355,7 +365,7 @@ __global__ void __launch_bounds__(THREADS<One>, 2)
           for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(acc[j]);
         };
         sums(c, w1);
-        if constexpr (E::PAIR) sums(One::TN / 2 + c, w2);
+        if constexpr (E::PAIR) sums(C::TN / 2 + c, w2);
         E::chunk(e, maps, t, c, w1, w2, pre);
       }
     }
@@ -366,7 +376,7 @@ __global__ void __launch_bounds__(THREADS<One>, 2)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_free(tmem, One::TN);
+    tmem_free(tmem, C::TN);
   }
 }
 
@@ -459,9 +469,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
           const CUtensorMap *am = &maps.a[(p.a_of >> seg) & 1], *bm = &maps.b[E::PAIR ? rank : (p.b_of >> seg) & 1];
           for (int kb = 0; kb < per; ++kb) {
             if (i >= ST && !(ok = wait_ab(&empty[s], phase ^ 1, abort, a.status))) break;
-            const uint32_t sm = base + s * STAGE, bar = bar0 + s * 8;
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE);
-            load_stage(a_mn, b_mn, kb * BK, m, n,
+            const uint32_t sm = base + s * STAGE<Two>, bar = bar0 + s * 8;
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE<Two>);
+            load_stage<Two>(a_mn, b_mn, kb * BK, m, n,
                        [&](int off, bool is_a, int, int x, int y) { tma_load_3d_pair(sm + off, is_a ? am : bm, x, y, w.z, bar); });
             ++i;
             if (++s == ST) s = 0, phase ^= 1;
@@ -491,7 +501,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t ad = oa.at(base + s * STAGE), bd = ob.at(base + s * STAGE + 2 * BOX);
+            const uint64_t ad = oa.at(base + s * STAGE<Two>), bd = ob.at(base + s * STAGE<Two> + 2 * BOX);
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks)
               tc_mma_pair(tmem + b * Two::TN, ad + ks * oa.step, bd + ks * ob.step, idesc, (kb > 0 || ks > 0) ? 1u : 0u);
@@ -508,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
     const int q = warp & 3, group = (warp - 2) >> 2;
     Part t;
     t.lane = lane;
-    t.sm_addr = base + ST * STAGE + (uint32_t)((warp - 2) * SLOTS * SLOT);
+    t.sm_addr = base + ST * STAGE<Two> + (uint32_t)((warp - 2) * SLOTS * SLOT);
     t.sm = dsmem + (t.sm_addr - smem_addr(dsmem));
     t.slot = 0;
     uint32_t w1[32], w2[32];
@@ -524,11 +534,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
       t.row0 = w.m * Two::TM + (int)rank * 128 + q * 32;
       t.row = t.row0 + lane;
       t.twice = p.sym && w.m != w.n;
+      constexpr int EACH = W::COLS / Two::GROUPS;
+      typename E::Pre pre(e, t, group * EACH);  // what a chunk reads besides the sums is asked for a chunk ahead
       const bool ok = wait_ab(&acc_full[b], (n >> 1) & 1, abort, a.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t acc = tmem + b * Two::TN + ((uint32_t)(q * 32) << 16);
-      constexpr int EACH = W::COLS / Two::GROUPS;
       const bool live = t.row0 < t.M;
 #pragma unroll 1
       for (int c = group * EACH; c < (group + 1) * EACH; c += 32) {
@@ -537,14 +548,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
           tc_ld32_async(acc + c, w1);
           if constexpr (E::PAIR) tc_ld32_async(acc + Two::TN / 2 + c, w2);
         }
-        const typename E::Pre pre(e, t, c);
+        const typename E::Pre now = pre;
+        if (!last) pre = typename E::Pre(e, t, c + 32);
         tc_wait_ld();
         if (last) {  // this warp has read the accumulator
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_addr(&acc_empty[b]), 0));
         }
-        if (live) E::chunk(e, all.of[w.i], t, c, w1, w2, pre);
+        if (live) E::chunk(e, all.of[w.i], t, c, w1, w2, now);
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -622,26 +634,44 @@ inline int sm_count() {
 // as run one on an SM and have four k-blocks each: 77 tokens of 2048 x 8192 36.7 us a call and 72.6 with one CTA a tile;
 // 509 of 1000 x 2040 21.4, 27.7, and 28.7 with two on an SM.
 struct Choice {
-  bool pair;
+  int kind;  // 0: pairs, 1: 128 x 128 tiles, 2: 128 x 64
   int S;
 };
+// The same products with all their tiles.
+inline Args whole(Args a) {
+  for (int i = 0; i < a.n; ++i) a.p[i].sym = 0;
+  return a;
+}
 template <typename E>
 Choice choose(const Args& a) {
-  const int64_t pairs = Walk<Two, E::PAIR>::tiles(a), ones = Walk<One, E::PAIR>::tiles(a), most = sm_count() / 2;
-  if (pairs >= most) return {true, 1};
-  int blocks = 1 << 30, S = 1;
+  const int64_t pairs = Walk<Two, E::PAIR>::tiles(a), sms = sm_count() & ~1;
+  if (2 * pairs >= sms) return {0, 1};
+  int blocks = 1 << 30;
   for (int i = 0; i < a.n; ++i) blocks = std::min(blocks, a.p[i].blocks());
-  while (S < 8 && ones * S * 2 <= 2 * most && S * 8 <= blocks) S *= 2;
-  return {false, S};
+  auto split = [&](int64_t tiles) {
+    int S = 1;
+    while (S < 8 && tiles * S * 2 <= sms && S * 8 <= blocks) S *= 2;
+    return S;
+  };
+  if constexpr (!E::PAIR) {
+    const int64_t halves = Walk<Half, false>::tiles(whole(a));
+    if (halves <= sms) return {2, split(halves)};
+  }
+  return {1, split(Walk<One, E::PAIR>::tiles(a))};
 }
 
 template <typename E>
 bool run(const Args& a, const AllMaps<E::MAPS>& m, const typename E::Args& e, cudaStream_t stream, const Choice& c) {
-  if (c.pair) {
+  if (c.kind == 0) {
     const int64_t pairs = std::min<int64_t>(Walk<Two, E::PAIR>::tiles(a), sm_count() / 2);
     return launch<k_gemm_pair<E>>(dim3(2 * (unsigned)pairs), THREADS<Two>, SMEM<Two>, 0, stream, a, m, e);
   }
-  return launch<k_gemm<E>>(dim3(c.S, (unsigned)Walk<One, E::PAIR>::tiles(a)), THREADS<One>, SMEM<One>, c.S, stream, a, m, e);
+  if constexpr (!E::PAIR)
+    if (c.kind == 2) {
+      const Args all = whole(a);
+      return launch<k_gemm<Half, E>>(dim3(c.S, (unsigned)Walk<Half, false>::tiles(all)), THREADS<Half>, SMEM<Half>, c.S, stream, all, m, e);
+    }
+  return launch<k_gemm<One, E>>(dim3(c.S, (unsigned)Walk<One, E::PAIR>::tiles(a)), THREADS<One>, SMEM<One>, c.S, stream, a, m, e);
 }
 template <typename E>
 bool run(const Args& a, const AllMaps<E::MAPS>& m, const typename E::Args& e, cudaStream_t stream) {

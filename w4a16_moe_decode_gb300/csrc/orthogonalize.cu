@@ -70,6 +70,24 @@ __device__ __forceinline__ void load8(const Start& a, size_t i, float* v) {
   }
 }
 
+__device__ __forceinline__ double add_squares(const float (&v)[8], double sum) {
+  float mx = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
+  const int ex = min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);
+  const float sc = exp2i(-ex);
+  float q = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q = fmaf(v[e] * sc, v[e] * sc, q);
+  return fma((double)q, __longlong_as_double((long long)(1023 + 2 * ex) << 52), sum);
+}
+// X_SCALE / (|M| + eps) as two FP32 factors, since a large norm's is below FP32's normals.
+__device__ __forceinline__ float2 inverse(double sum, float eps) {
+  const double d = sqrt(sum) + (double)eps;
+  const int half = ((int)(__double_as_longlong(d) >> 52) - 1023) / 2;
+  return make_float2(exp2i(-half), (float)(X_SCALE / (d * __longlong_as_double((long long)(1023 - half) << 52))));
+}
+
 __global__ void __launch_bounds__(START_THREADS) k_ortho_norm(const Start a) {
   __shared__ double s_sum[START_THREADS / 32];
   pdl_wait();
@@ -86,15 +104,7 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_norm(const Start a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = i + e < all ? load1(a, first + i + e) : 0.f;
     }
-    float mx = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
-    const int ex = min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);
-    const float sc = exp2i(-ex);
-    float q = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q = fmaf(v[e] * sc, v[e] * sc, q);
-    sum = fma((double)q, __longlong_as_double((long long)(1023 + 2 * ex) << 52), sum);
+    sum = add_squares(v, sum);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -115,11 +125,10 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_split(const Start a) {
     for (int p = threadIdx.x; p < a.parts; p += 32) sum += __ldcg(a.part + (size_t)blockIdx.y * a.parts + p);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (threadIdx.x == 0) {  // 1 / (|M| + eps) as two FP32 factors, since a large norm's is below FP32's normals
-      const double d = sqrt(sum) + (double)a.eps;
-      const int half = ((int)(__double_as_longlong(d) >> 52) - 1023) / 2;
-      s_scale[0] = exp2i(-half);
-      s_scale[1] = (float)(X_SCALE / (d * __longlong_as_double((long long)(1023 - half) << 52)));
+    if (threadIdx.x == 0) {
+      const float2 f = inverse(sum, a.eps);
+      s_scale[0] = f.x;
+      s_scale[1] = f.y;
     }
   }
   __syncthreads();
@@ -265,6 +274,323 @@ struct Update {
   }
 };
 
+// ---------------------------------------------------------------------------
+// Few rows (the shorter side up to 128) that fit the shared memory of a cluster:
+// all steps in one kernel, one cluster of CTAs a matrix. The matrix lies on its
+// long side here, X [k][m] with m <= 128: each CTA keeps kc of the k rows as hi
+// and lo, in the swizzled layout in which the same bytes serve as both operands
+// of S = X^T X (MN-major, the rows being the reduction) and as X in X P
+// (K-major). A step:
+//   S's partial sums of the CTA's rows (tcgen05) -> shared memory; each CTA adds
+//   its share of them over the cluster and hands the f16 result to all;
+//   P = b S + c S S, by every CTA for itself;
+//   X <- a X + X_hi P_hi + X_hi P_lo + X_lo P_hi, by rows.
+// Bound by latency: two cluster barriers and three products that wait for one
+// another a step. 8 matrices of 16 x 2048: 96 us with the general path's 17
+// launches, 28 with this.
+// ---------------------------------------------------------------------------
+constexpr int FEW_THREADS = 256;
+
+struct FewArgs {
+  const void* in;
+  uint16_t* out;
+  int bf16, rows, cols, steps;
+  int m, k, kc;  // the shorter and the longer side, rows of the long side a CTA keeps (multiple of 128)
+  float eps, scale;
+  float coeffs[3 * FLINT_ORTHOGONALIZE_MAX_STEPS];
+  int* status;
+};
+
+struct FewPlan {
+  int mp, mb, xbox, sbox, pbox, tmem;  // columns padded to 16, boxes of 64; bytes of a box of X, S and P; tensor memory
+  size_t x[2], s, p, total;            // p: P hi and lo, and S's partial sums before
+};
+__host__ __device__ inline FewPlan few_plan(int m, int kc) {
+  FewPlan f;
+  f.mp = (m + 15) & ~15;
+  f.mb = m > 64 ? 2 : 1;
+  f.xbox = kc * 128;
+  f.sbox = 128 * 128;
+  f.pbox = f.mb == 1 ? 64 * 128 : 128 * 128;
+  size_t o = 0;
+  for (int i = 0; i < 2; ++i) {
+    f.x[i] = o;
+    o += (size_t)f.mb * f.xbox;
+  }
+  f.s = o;
+  o += (size_t)f.mb * f.sbox;
+  f.p = o;
+  const size_t p = (size_t)2 * f.mb * f.pbox, sums = (size_t)f.mp / 4 * 128 * 16;
+  o += p > sums ? p : sums;
+  f.total = 1024 + o;
+  const int cols = (kc / 128 + 2) * f.mp;
+  f.tmem = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
+  return f;
+}
+
+__device__ __forceinline__ void st_dsmem_v2(uint32_t remote, uint32_t x, uint32_t y) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(remote), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ double ld_dsmem_f64(uint32_t remote) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(remote) : "memory");
+  return v;
+}
+// Shared-memory accesses of any CTA of the cluster before, the tensor core's after.
+__device__ __forceinline__ void fence_proxy_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// K-major operand at saddr (boxes of 64 columns `box` bytes apart): 16 columns from 16 ks on.
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr, int box, int ks) {
+  return sw128_desc(saddr + (uint32_t)((ks >> 2) * box)) + (uint64_t)((ks & 3) * 2);
+}
+
+__global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
+  extern __shared__ uint8_t dsmem[];
+  __shared__ double s_sum[FEW_THREADS / 32], s_part;
+  __shared__ float2 s_inv;
+  __shared__ uint64_t bar;
+  __shared__ uint32_t tmem_base;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, group = warp >> 2;
+  const int C = gridDim.x, rank = blockIdx.x;
+  const FewPlan f = few_plan(a.m, a.kc);
+  const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
+  uint8_t* const sm = dsmem + (base - smem_addr(dsmem));
+  const uint32_t xs = base + (uint32_t)f.x[0], xls = base + (uint32_t)f.x[1], ss = base + (uint32_t)f.s, ps = base + (uint32_t)f.p;
+  uint8_t *const xp = sm + f.x[0], *const xlp = sm + f.x[1], *const sp = sm + f.s, *const pp = sm + f.p;
+  const int plo = f.mb * f.pbox;  // P's second half behind the first
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(&tmem_base, f.tmem);
+  for (int i = threadIdx.x; i < f.mb * f.sbox / 16; i += FEW_THREADS) reinterpret_cast<uint4*>(sp)[i] = make_uint4(0, 0, 0, 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0 && blockIdx.x + blockIdx.y == 0) *a.status = 0;
+
+  // Eight values of a row of X: row l (of the CTA's), columns 8 c .. ; the matrix as it lies in memory has l down (tall)
+  // or across. Neighbouring threads take neighbouring values.
+  const bool tall = a.rows > a.cols, vec = tall && a.cols % 8 == 0;
+  const int pieces = f.mp / 8, units = a.kc * pieces, l0 = rank * a.kc;
+  const size_t first = (size_t)blockIdx.y * a.rows * a.cols;
+  Start src;
+  src.in = a.in;
+  src.bf16 = a.bf16;
+  auto place = [&](int u, int& l, int& c) {
+    l = tall ? u / pieces : u % a.kc;
+    c = tall ? u - l * pieces : u / a.kc;
+  };
+  auto load = [&](int l, int c, float (&v)[8]) {
+    const int at = l0 + l;
+    if (vec && at < a.k && 8 * c < a.m) {
+      load8(src, first + (size_t)at * a.cols + 8 * c, v);
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = 8 * c + e;
+      v[e] = at < a.k && i < a.m ? load1(src, first + (tall ? (size_t)at * a.cols + i : (size_t)i * a.cols + at)) : 0.f;
+    }
+  };
+  auto xoff = [&](int l, int c) { return (uint32_t)((c >> 3) * f.xbox + l * 128 + (((c & 7) ^ (l & 7)) << 4)); };
+
+  double sum = 0.0;
+  for (int u = threadIdx.x; u < units; u += FEW_THREADS) {
+    int l, c;
+    place(u, l, c);
+    float v[8];
+    load(l, c, v);
+    sum = add_squares(v, sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < FEW_THREADS / 32; ++w) sum += s_sum[w];
+    s_part = sum;
+  }
+  cluster_sync();
+  if (threadIdx.x == 0) {
+    sum = 0.0;
+    for (int r = 0; r < C; ++r) sum += ld_dsmem_f64(dsmem_addr(smem_addr(&s_part), r));
+    s_inv = inverse(sum, a.eps);
+  }
+  __syncthreads();
+  const float2 inv = s_inv;
+  for (int u = threadIdx.x; u < units; u += FEW_THREADS) {
+    int l, c;
+    place(u, l, c);
+    float v[8];
+    load(l, c, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (v[e] * inv.x) * inv.y;
+    uint4 hi, lo;
+    split8(v, hi, lo);
+    *reinterpret_cast<uint4*>(xp + xoff(l, c)) = hi;
+    *reinterpret_cast<uint4*>(xlp + xoff(l, c)) = lo;
+  }
+
+  const uint32_t d_s = tmem, d_q = tmem + f.mp, d_x = tmem + 2 * f.mp;  // S, S S, and X P by tiles of 128 rows
+  const uint32_t lanes = (uint32_t)(q * 32) << 16;
+  const int tiles = a.kc / 128, i0 = q * 32 + lane;  // this thread's row of S and P
+  uint32_t phase = 0;
+  bool ok = true;
+  auto arrived = [&] {  // the products asked for last; after a wait that gave up the others are not waited for
+    ok = ok && mbar_wait(&bar, phase, a.status);
+    phase ^= 1;
+    tc_fence_after();
+  };
+  auto ready = [&] {  // shared memory as all threads left it, for the tensor core; and tensor memory as they read it
+    fence_proxy_all();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  };
+  for (int step = 0; step < a.steps; ++step) {
+    const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1], cc = a.coeffs[3 * step + 2];
+    const bool last = step + 1 == a.steps;
+    ready();
+    if (warp == 0 && elect_one()) {
+      // Rows of D from 64 on come from X's lo where X has one box of columns: they are not read.
+      const uint32_t idesc = idesc_f32acc(128, f.mp, false) | IDESC_A_MN | IDESC_B_MN;
+      for (int ks = 0; ks < a.kc / 16; ++ks) {
+        const uint64_t d = sw128_desc_mn(xs + ks * 2048, f.xbox);
+        tc_mma(d_s, d, d, idesc, ks > 0);
+      }
+      tc_commit(&bar);
+    }
+    __syncwarp();
+    arrived();
+    // This CTA's sums: row i's columns 4 c .. at piece c * 128 + i.
+    for (int c = 16 * group; c < f.mp; c += 32) {
+      uint32_t w[16];
+      __syncwarp();
+      tc_ld16(d_s + lanes + c, w);
+      if (i0 < a.m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(pp + ((c / 4 + j) * 128 + i0) * 16) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    }
+    tc_fence_before();
+    cluster_sync();
+    {
+      const int all = f.mp / 4 * a.m, e1 = (int)((long long)all * (rank + 1) / C);
+      for (int e = (int)((long long)all * rank / C) + threadIdx.x; e < e1; e += FEW_THREADS) {
+        const int c = e / a.m, i = e - c * a.m;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 part[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < C) part[r] = ld_dsmem_f4(dsmem_addr(ps + (uint32_t)(c * 128 + i) * 16, r));
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < C) v.x += part[r].x, v.y += part[r].y, v.z += part[r].z, v.w += part[r].w;
+        constexpr float fs = S_SCALE / (X_SCALE * X_SCALE);
+        const uint32_t w0 = f2h2(v.x * fs, v.y * fs), w1 = f2h2(v.z * fs, v.w * fs);
+        const uint32_t at = ss + (uint32_t)((c >> 4) * f.sbox + i * 128 + ((((c >> 1) & 7) ^ (i & 7)) << 4) + (c & 1) * 8);
+        for (int r = 0; r < C; ++r) st_dsmem_v2(dsmem_addr(at, r), w0, w1);
+      }
+    }
+    fence_proxy_all();
+    cluster_sync();
+    fence_proxy_all();
+    tc_fence_after();
+    if (warp == 0 && elect_one()) {
+      const uint32_t idesc = idesc_f32acc(128, f.mp, false);
+      for (int ks = 0; ks < f.mp / 16; ++ks) {
+        const uint64_t d = desc_k(ss, f.sbox, ks);
+        tc_mma(d_q, d, d, idesc, ks > 0);
+      }
+      tc_commit(&bar);
+    }
+    __syncwarp();
+    arrived();
+    const float fs = cb * (P_SCALE / S_SCALE), fq = cc * (P_SCALE / (S_SCALE * S_SCALE));
+    for (int c = 16 * group; c < f.mp; c += 32) {
+      uint32_t w[16];
+      __syncwarp();
+      tc_ld16(d_q + lanes + c, w);
+      if (i0 < f.mp)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int pc = c / 8 + j;
+          float v[8];
+          const uint32_t at = (uint32_t)(i0 * 128 + (((pc & 7) ^ (i0 & 7)) << 4));
+          unpack8_f16(*reinterpret_cast<const uint4*>(sp + (pc >> 3) * f.sbox + at), v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = fmaf(fs, v[e], fq * __uint_as_float(w[8 * j + e]));
+          uint4 hi, lo;
+          split8(v, hi, lo);
+          *reinterpret_cast<uint4*>(pp + (pc >> 3) * f.pbox + at) = hi;
+          *reinterpret_cast<uint4*>(pp + plo + (pc >> 3) * f.pbox + at) = lo;
+        }
+    }
+    ready();
+    if (warp == 0 && elect_one()) {
+      const uint32_t idesc = idesc_f32acc(128, f.mp, false);
+      for (int t = 0; t < tiles; ++t)
+        for (int g = 0; g < 3; ++g)
+          for (int ks = 0; ks < f.mp / 16; ++ks)
+            tc_mma(d_x + t * f.mp, desc_k((g == 2 ? xls : xs) + t * 128 * 128, f.xbox, ks), desc_k(ps + (g == 1 ? plo : 0), f.pbox, ks),
+                   idesc, g > 0 || ks > 0);
+      tc_commit(&bar);
+    }
+    __syncwarp();
+    arrived();
+    const int chunks = f.mp / 16;  // of 16 columns, shared out between the two groups of warps
+    for (int u = group; u < tiles * chunks; u += 2) {
+      const int t = u / chunks, c = (u - t * chunks) * 16, l = t * 128 + i0;
+      uint32_t w[16];
+      __syncwarp();
+      tc_ld16(d_x + lanes + t * f.mp + c, w);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int pc = c / 8 + j;
+        uint4* const hp = reinterpret_cast<uint4*>(xp + xoff(l, pc));
+        uint4* const lp = reinterpret_cast<uint4*>(xlp + xoff(l, pc));
+        float h[8], lo[8], v[8];
+        unpack8_f16(*hp, h);
+        unpack8_f16(*lp, lo);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(1.0f / P_SCALE, __uint_as_float(w[8 * j + e]), ca * (h[e] + lo[e]));
+        if (!last) {
+          split8(v, *hp, *lp);
+          continue;
+        }
+        const int at = l0 + l;
+        if (at >= a.k) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= a.scale;
+        const uint4 o = pack8_bf16(v);
+        if (vec && 8 * pc < a.m) {
+          *reinterpret_cast<uint4*>(a.out + first + (size_t)at * a.cols + 8 * pc) = o;
+        } else {
+          const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int i = 8 * pc + e;
+            if (i < a.m)
+              a.out[first + (tall ? (size_t)at * a.cols + i : (size_t)i * a.cols + at)] = (uint16_t)(e & 1 ? ow[e >> 1] >> 16 : ow[e >> 1]);
+          }
+        }
+      }
+    }
+  }
+  if (!ok) mbar_drain(&bar, phase ^ 1);  // products may still be under way
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // nothing of the other CTAs' still reads or writes this one's memory
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_free(tmem, f.tmem);
+  }
+}
+
 }  // namespace ortho
 }  // namespace flint
 
@@ -319,6 +645,17 @@ WsPlan ws_plan(int n, int rows, int cols) {
   return w;
 }
 
+// The cluster kernel's CTAs a matrix and their rows of the long side, or 0 where a matrix does not fit eight of them. By
+// the shape alone, so that a matrix has the same bits in every batch.
+int few_ctas(int m, int k, int* kc) {
+  if (m > 128) return 0;
+  for (int C = 1; C <= 8; C *= 2) {
+    *kc = ((k + C - 1) / C + 127) / 128 * 128;
+    if (*kc <= 256 || (C == 8 && few_plan(m, *kc).total <= 226 * 1024 && (*kc / 128 + 2) * few_plan(m, *kc).mp <= 512)) return C;
+  }
+  return 0;
+}
+
 bool overlaps(const void* p, size_t np, const void* q, size_t nq) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return a < b + nq && b < a + np;
@@ -347,8 +684,19 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
   if (ws_size < w.total || overlaps(ws, w.total, in, values * (fmt == FLINT_ORTHOGONALIZE_F32 ? 4 : 2)) ||
       overlaps(ws, w.total, out, values * 2))
     return FLINT_MOE_EINVAL;
+  // out may be in, value for value; another overlap would let a matrix's result fall on one that is still to be read
+  if (overlaps(in, values * (fmt == FLINT_ORTHOGONALIZE_F32 ? 4 : 2), out, values * 2) &&
+      (fmt == FLINT_ORTHOGONALIZE_F32 || in != out))
+    return FLINT_MOE_EINVAL;
   uint8_t* wsp = static_cast<uint8_t*>(ws);
   int* status = reinterpret_cast<int*>(ws) + H_STATUS;
+  int kc = 0;
+  if (const int C = few_ctas(w.m, std::max(rows, cols), &kc)) {
+    FewArgs a = {in, out, fmt == FLINT_ORTHOGONALIZE_BF16, rows, cols, steps, w.m, std::max(rows, cols), kc, eps, scale / X_SCALE, {}, status};
+    std::copy(coeffs, coeffs + 3 * steps, a.coeffs);
+    if (!prepare<k_ortho_few>(227 * 1024 - 1024)) return FLINT_MOE_ECUDA;
+    return launch<k_ortho_few>(dim3(C, n), FEW_THREADS, few_plan(w.m, kc).total, C, stream, a) ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
+  }
   auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(wsp + o); };
   const bool tall = rows > cols;
   const int m = w.m;
