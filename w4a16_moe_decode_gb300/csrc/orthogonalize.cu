@@ -2,6 +2,7 @@
 //
 // Scaled values: X is kept times 2^10 as hi + lo (f16), S times 2^10 and P times 2^8 (f16).
 #include <cmath>
+#include <type_traits>
 
 #include "flint_orthogonalize.h"
 #include "gemm.cuh"
@@ -10,6 +11,10 @@ namespace flint {
 namespace ortho {
 
 using namespace gemm;
+
+// P X as P_hi X_hi + P_lo X_hi + P_hi X_lo up to this many rows, where few rounding errors meet in a result and the products
+// cost little; above, as P_hi X_hi, whose errors average out.
+__host__ __device__ inline bool few_rows(int m) { return m <= 32; }
 
 constexpr float X_SCALE = 1024.f, S_SCALE = 1024.f, P_SCALE = 256.f;
 
@@ -41,9 +46,10 @@ __device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
 }
 
 // ---------------------------------------------------------------------------
-// X = M / (|M| + eps): the sums of squares in FP64 (a block's partial sum each),
-// then hi and lo. Eight values share a power of two, so that squares neither
-// overflow nor vanish.
+// X = M / (|M| + eps): the sums of squares (a thread's in FP32 with an exponent
+// of its own, so that squares neither overflow nor vanish, the threads' and
+// blocks' in FP64, of which this card computes two a cycle and SM), then hi and
+// lo.
 // ---------------------------------------------------------------------------
 struct Start {
   const void* in;
@@ -56,31 +62,43 @@ struct Start {
 
 constexpr int START_THREADS = 256;
 
+__device__ __forceinline__ float value(float v) { return v; }
+__device__ __forceinline__ float value(uint16_t v) { return bf16lo(v); }
+// Eight values from an aligned place.
+__device__ __forceinline__ void load8(const uint16_t* p, float* v) { unpack8_bf16(*reinterpret_cast<const uint4*>(p), v); }
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+  v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+}
 __device__ __forceinline__ float load1(const Start& a, size_t i) {
-  return a.bf16 ? bf16lo(static_cast<const uint16_t*>(a.in)[i]) : static_cast<const float*>(a.in)[i];
+  return a.bf16 ? value(static_cast<const uint16_t*>(a.in)[i]) : value(static_cast<const float*>(a.in)[i]);
 }
 // Values i .. i + 7 (i a multiple of 8 from an aligned start).
 __device__ __forceinline__ void load8(const Start& a, size_t i, float* v) {
-  if (a.bf16) {
-    unpack8_bf16(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.in) + i), v);
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.in) + i);
-    const float4 x = p[0], y = p[1];
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-  }
+  if (a.bf16)
+    load8(static_cast<const uint16_t*>(a.in) + i, v);
+  else
+    load8(static_cast<const float*>(a.in) + i, v);
 }
 
-__device__ __forceinline__ double add_squares(const float (&v)[8], double sum) {
-  float mx = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
-  const int ex = min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);
-  const float sc = exp2i(-ex);
+// A sum of squares as q 4^ex: neither overflows nor vanishes.
+struct Squares {
   float q = 0.f;
+  int ex = -126;
+  template <int N>
+  __device__ __forceinline__ void add(const float (&v)[N]) {
+    float mx = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) q = fmaf(v[e] * sc, v[e] * sc, q);
-  return fma((double)q, __longlong_as_double((long long)(1023 + 2 * ex) << 52), sum);
-}
+    for (int e = 0; e < N; ++e) mx = fmaxf(mx, fabsf(v[e]));
+    const int to = min(max((int)(__float_as_uint(mx) >> 23) - 127, ex), 126);
+    const float down = exp2i(max(ex - to, -126)), sc = exp2i(-to);
+    q = q * down * down;
+    ex = to;
+#pragma unroll
+    for (int e = 0; e < N; ++e) q = fmaf(v[e] * sc, v[e] * sc, q);
+  }
+  __device__ __forceinline__ double value() const { return (double)q * __longlong_as_double((long long)(1023 + 2 * ex) << 52); }
+};
 // X_SCALE / (|M| + eps) as two FP32 factors, since a large norm's is below FP32's normals.
 __device__ __forceinline__ float2 inverse(double sum, float eps) {
   const double d = sqrt(sum) + (double)eps;
@@ -95,7 +113,7 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_norm(const Start a) {
   if (threadIdx.x == 0 && blockIdx.x + blockIdx.y == 0) *a.status = 0;
   const size_t all = (size_t)a.rows * a.cols, first = blockIdx.y * all;
   const bool vec = all % 8 == 0;
-  double sum = 0.0;
+  Squares sq;
   for (size_t i = 8 * ((size_t)blockIdx.x * START_THREADS + threadIdx.x); i < all; i += (size_t)gridDim.x * START_THREADS * 8) {
     float v[8];
     if (vec) {
@@ -104,8 +122,9 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_norm(const Start a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = i + e < all ? load1(a, first + i + e) : 0.f;
     }
-    sum = add_squares(v, sum);
+    sq.add(v);
   }
+  double sum = sq.value();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
@@ -277,19 +296,21 @@ struct Update {
 // ---------------------------------------------------------------------------
 // Few rows (the shorter side up to 128) that fit the shared memory of a cluster:
 // all steps in one kernel, one cluster of CTAs a matrix. The matrix lies on its
-// long side here, X [k][m] with m <= 128: each CTA keeps kc of the k rows as hi
-// and lo, in the swizzled layout in which the same bytes serve as both operands
-// of S = X^T X (MN-major, the rows being the reduction) and as X in X P
-// (K-major). A step:
+// long side here, X [k][m] with m <= 128: each CTA keeps kc of the k rows, in
+// FP32 in its threads' registers and as f16 in the swizzled layout in which the
+// same bytes serve as both operands of S = X^T X (MN-major, the rows being the
+// reduction) and as X in X P (K-major). A step:
 //   S's partial sums of the CTA's rows (tcgen05) -> shared memory; each CTA adds
 //   its share of them over the cluster and hands the f16 result to all;
 //   P = b S + c S S, by every CTA for itself;
-//   X <- a X + X_hi P_hi + X_hi P_lo + X_lo P_hi, by rows.
-// Bound by latency: two cluster barriers and three products that wait for one
-// another a step. 8 matrices of 16 x 2048: 96 us with the general path's 17
-// launches, 28 with this.
+//   X <- a X + X P, by rows (few_rows: with the second halves of X and P).
+// Bound by latency: two cluster barriers, the exchange between them and three
+// products that wait for one another a step. 8 matrices of 16 x 2048: 105 us
+// with the general path's 17 launches.
 // ---------------------------------------------------------------------------
-constexpr int FEW_THREADS = 256;
+constexpr int FEW_THREADS = 512;
+constexpr int FEW_GROUPS = FEW_THREADS / 128;  // four warps reach all of tensor memory's lanes
+constexpr int FEW_UNITS = 4;                   // of 16 columns of a row, that a thread keeps at most
 
 struct FewArgs {
   const void* in;
@@ -303,7 +324,7 @@ struct FewArgs {
 
 struct FewPlan {
   int mp, mb, xbox, sbox, pbox, tmem;  // columns padded to 16, boxes of 64; bytes of a box of X, S and P; tensor memory
-  size_t x[2], s, p, total;            // p: P hi and lo, and S's partial sums before
+  size_t x[2], s, p, total;            // x: hi, lo; p: P's halves, and S's partial sums before
 };
 __host__ __device__ inline FewPlan few_plan(int m, int kc) {
   FewPlan f;
@@ -312,38 +333,32 @@ __host__ __device__ inline FewPlan few_plan(int m, int kc) {
   f.xbox = kc * 128;
   f.sbox = 128 * 128;
   f.pbox = f.mb == 1 ? 64 * 128 : 128 * 128;
-  size_t o = 0;
-  for (int i = 0; i < 2; ++i) {
-    f.x[i] = o;
-    o += (size_t)f.mb * f.xbox;
-  }
-  f.s = o;
-  o += (size_t)f.mb * f.sbox;
-  f.p = o;
-  const size_t p = (size_t)2 * f.mb * f.pbox, sums = (size_t)f.mp / 4 * 128 * 16;
-  o += p > sums ? p : sums;
-  f.total = 1024 + o;
+  const int halves = few_rows(m) ? 2 : 1;
+  f.x[0] = 0;
+  f.x[1] = (size_t)(halves - 1) * f.mb * f.xbox;
+  f.s = (size_t)halves * f.mb * f.xbox;
+  f.p = f.s + (size_t)f.mb * f.sbox;
+  const size_t p = (size_t)halves * f.mb * f.pbox, sums = (size_t)f.mp * m * 4;
+  f.total = 1024 + f.p + (p > sums ? p : sums);
   const int cols = (kc / 128 + 2) * f.mp;
   f.tmem = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
   return f;
 }
+// Units a thread keeps.
+__host__ __device__ inline int few_units(int m, int kc) { return (kc / 128 * ((m + 15) / 16) + FEW_GROUPS - 1) / FEW_GROUPS; }
 
-__device__ __forceinline__ void st_dsmem_v2(uint32_t remote, uint32_t x, uint32_t y) {
-  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(remote), "r"(x), "r"(y) : "memory");
+__device__ __forceinline__ void st_dsmem_v4(uint32_t remote, const uint4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ double ld_dsmem_f64(uint32_t remote) {
   double v;
   asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(remote) : "memory");
   return v;
 }
-// Shared-memory accesses of any CTA of the cluster before, the tensor core's after.
-__device__ __forceinline__ void fence_proxy_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// What 16 ks columns of a K-major operand in boxes of 64 columns add to its descriptor.
+__device__ __forceinline__ uint32_t k_step(int ks, int box) { return (uint32_t)((ks >> 2) * (box >> 4) + (ks & 3) * 2); }
 
-// K-major operand at saddr (boxes of 64 columns `box` bytes apart): 16 columns from 16 ks on.
-__device__ __forceinline__ uint64_t desc_k(uint32_t saddr, int box, int ks) {
-  return sw128_desc(saddr + (uint32_t)((ks >> 2) * box)) + (uint64_t)((ks & 3) * 2);
-}
-
+template <int UNITS>
 __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
   extern __shared__ uint8_t dsmem[];
   __shared__ double s_sum[FEW_THREADS / 32], s_part;
@@ -353,6 +368,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, group = warp >> 2;
   const int C = gridDim.x, rank = blockIdx.x;
   const FewPlan f = few_plan(a.m, a.kc);
+  const bool both = few_rows(a.m);
   const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
   uint8_t* const sm = dsmem + (base - smem_addr(dsmem));
   const uint32_t xs = base + (uint32_t)f.x[0], xls = base + (uint32_t)f.x[1], ss = base + (uint32_t)f.s, ps = base + (uint32_t)f.p;
@@ -372,40 +388,49 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
   pdl_trigger();
   if (threadIdx.x == 0 && blockIdx.x + blockIdx.y == 0) *a.status = 0;
 
-  // Eight values of a row of X: row l (of the CTA's), columns 8 c .. ; the matrix as it lies in memory has l down (tall)
-  // or across. Neighbouring threads take neighbouring values.
+  // Unit n of this thread: row 128 t + i0 of the CTA's, columns c .. c + 15. The matrix as it lies in memory has X's rows
+  // down (tall) or across.
   const bool tall = a.rows > a.cols, vec = tall && a.cols % 8 == 0;
-  const int pieces = f.mp / 8, units = a.kc * pieces, l0 = rank * a.kc;
+  const int chunks = f.mp / 16, tiles = a.kc / 128, i0 = q * 32 + lane, l0 = rank * a.kc;
   const size_t first = (size_t)blockIdx.y * a.rows * a.cols;
-  Start src;
-  src.in = a.in;
-  src.bf16 = a.bf16;
-  auto place = [&](int u, int& l, int& c) {
-    l = tall ? u / pieces : u % a.kc;
-    c = tall ? u - l * pieces : u / a.kc;
+  auto unit = [&](int n, int& t, int& c) {
+    const int u = group + n * FEW_GROUPS;
+    t = u / chunks;
+    c = (u - t * chunks) * 16;
+    return u < tiles * chunks;
   };
-  auto load = [&](int l, int c, float (&v)[8]) {
-    const int at = l0 + l;
-    if (vec && at < a.k && 8 * c < a.m) {
-      load8(src, first + (size_t)at * a.cols + 8 * c, v);
-      return;
-    }
+  auto xoff = [&](int l, int pc) { return (uint32_t)((pc >> 3) * f.xbox + l * 128 + (((pc & 7) ^ (l & 7)) << 4)); };
+  float x[UNITS][16];
+  auto load = [&](auto* in) {  // float or bf16 bits
+    using T = std::remove_const_t<std::remove_pointer_t<decltype(in)>>;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = 8 * c + e;
-      v[e] = at < a.k && i < a.m ? load1(src, first + (tall ? (size_t)at * a.cols + i : (size_t)i * a.cols + at)) : 0.f;
+    for (int n = 0; n < UNITS; ++n) {
+      int t, c;
+      const bool live = unit(n, t, c);
+      const int at = l0 + t * 128 + i0, most = live && at < a.k ? a.m - c : 0;  // columns that there are
+      const size_t step = tall ? 1 : a.cols;
+      const T* p = in + first + (tall ? (size_t)at * a.cols : (size_t)at) + (size_t)c * step;
+      if (vec) {
+#pragma unroll
+        for (int h = 0; h < 16; h += 8) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[n][h + e] = 0.f;
+          if (h < most) load8(p + h, &x[n][h]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[n][e] = e < most ? value(p[e * step]) : 0.f;
+      }
     }
   };
-  auto xoff = [&](int l, int c) { return (uint32_t)((c >> 3) * f.xbox + l * 128 + (((c & 7) ^ (l & 7)) << 4)); };
-
-  double sum = 0.0;
-  for (int u = threadIdx.x; u < units; u += FEW_THREADS) {
-    int l, c;
-    place(u, l, c);
-    float v[8];
-    load(l, c, v);
-    sum = add_squares(v, sum);
-  }
+  if (a.bf16)
+    load(static_cast<const uint16_t*>(a.in));
+  else
+    load(static_cast<const float*>(a.in));
+  Squares sq;
+#pragma unroll
+  for (int n = 0; n < UNITS; ++n) sq.add(x[n]);
+  double sum = sq.value();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) s_sum[warp] = sum;
@@ -422,96 +447,118 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
   }
   __syncthreads();
   const float2 inv = s_inv;
-  for (int u = threadIdx.x; u < units; u += FEW_THREADS) {
-    int l, c;
-    place(u, l, c);
-    float v[8];
-    load(l, c, v);
+  // Unit n's f16 values to where the products read them.
+  auto hand_over = [&](int n, int t, int c) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = (v[e] * inv.x) * inv.y;
-    uint4 hi, lo;
-    split8(v, hi, lo);
-    *reinterpret_cast<uint4*>(xp + xoff(l, c)) = hi;
-    *reinterpret_cast<uint4*>(xlp + xoff(l, c)) = lo;
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t o = xoff(t * 128 + i0, c / 8 + h);
+      if (both) {
+        uint4 hi, lo;
+        split8(&x[n][8 * h], hi, lo);
+        *reinterpret_cast<uint4*>(xp + o) = hi;
+        *reinterpret_cast<uint4*>(xlp + o) = lo;
+      } else {
+        *reinterpret_cast<uint4*>(xp + o) = pack8_f16(&x[n][8 * h]);
+      }
+    }
+  };
+#pragma unroll
+  for (int n = 0; n < UNITS; ++n) {
+    int t, c;
+    if (!unit(n, t, c)) break;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[n][e] = (x[n][e] * inv.x) * inv.y;
+    hand_over(n, t, c);
   }
 
   const uint32_t d_s = tmem, d_q = tmem + f.mp, d_x = tmem + 2 * f.mp;  // S, S S, and X P by tiles of 128 rows
   const uint32_t lanes = (uint32_t)(q * 32) << 16;
-  const int tiles = a.kc / 128, i0 = q * 32 + lane;  // this thread's row of S and P
+  const int swz = f.mp % 32 == 0 ? 7 : 3;
   uint32_t phase = 0;
   bool ok = true;
   auto arrived = [&] {  // the products asked for last; after a wait that gave up the others are not waited for
     ok = ok && mbar_wait(&bar, phase, a.status);
     phase ^= 1;
+    __syncwarp();
     tc_fence_after();
   };
-  auto ready = [&] {  // shared memory as all threads left it, for the tensor core; and tensor memory as they read it
-    fence_proxy_all();
+  auto ready = [&] {  // all threads have written their shared memory and read their tensor memory
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
   };
+  // The thread that issues a product orders what it has seen the others write before the tensor core's reads of it.
   for (int step = 0; step < a.steps; ++step) {
     const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1], cc = a.coeffs[3 * step + 2];
-    const bool last = step + 1 == a.steps;
     ready();
     if (warp == 0 && elect_one()) {
-      // Rows of D from 64 on come from X's lo where X has one box of columns: they are not read.
+      fence_proxy_async();
+      // With one box of columns, rows of D from 64 on (which are not read) come from eight rows of X further on, and at the
+      // end from the 1 KiB behind X, which is S's: the second box's place could lie outside the shared memory.
       const uint32_t idesc = idesc_f32acc(128, f.mp, false) | IDESC_A_MN | IDESC_B_MN;
-      for (int ks = 0; ks < a.kc / 16; ++ks) {
-        const uint64_t d = sw128_desc_mn(xs + ks * 2048, f.xbox);
-        tc_mma(d_s, d, d, idesc, ks > 0);
-      }
+      uint64_t d = sw128_desc_mn(xs, f.mb == 1 ? 1024 : f.xbox);
+#pragma unroll 4
+      for (int ks = 0; ks < a.kc / 16; ++ks, d += 2048 >> 4) tc_mma(d_s, d, d, idesc, ks > 0);
       tc_commit(&bar);
     }
     __syncwarp();
     arrived();
-    // This CTA's sums: row i's columns 4 c .. at piece c * 128 + i.
-    for (int c = 16 * group; c < f.mp; c += 32) {
+    // This CTA's sums, by rows, pieces of four swizzled by row.
+    for (int c = 16 * group; c < f.mp; c += 16 * FEW_GROUPS) {
       uint32_t w[16];
       __syncwarp();
       tc_ld16(d_s + lanes + c, w);
       if (i0 < a.m)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(pp + ((c / 4 + j) * 128 + i0) * 16) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          *reinterpret_cast<uint4*>(pp + (i0 * (f.mp / 4) + ((c / 4 + j) ^ (i0 & swz))) * 16) =
+              make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     }
     tc_fence_before();
     cluster_sync();
     {
-      const int all = f.mp / 4 * a.m, e1 = (int)((long long)all * (rank + 1) / C);
-      for (int e = (int)((long long)all * rank / C) + threadIdx.x; e < e1; e += FEW_THREADS) {
-        const int c = e / a.m, i = e - c * a.m;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 part[8];
+      // Pieces of four columns, neighbouring threads a row's; two threads join theirs to one piece of eight f16 values and
+      // hand it to half of the CTAs each. A CTA begins with its own sums and goes round, so that no CTA's memory is asked
+      // by all at once.
+      const int per = f.mp / 4, all = f.mp / 8 * a.m, e1 = 2 * (all * (rank + 1) / C);
+      for (int e0 = 2 * (all * rank / C) + warp * 32; e0 < e1; e0 += FEW_THREADS) {
+        const int e = min(e0 + lane, e1 - 1), i = e / per, c = e - i * per;
+        const uint32_t at = ps + (uint32_t)(i * per + (c ^ (i & swz))) * 16;
+        float4 p[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r)
-          if (r < C) part[r] = ld_dsmem_f4(dsmem_addr(ps + (uint32_t)(c * 128 + i) * 16, r));
+          if (r < C) p[r] = ld_dsmem_f4(dsmem_addr(at, (rank + r) & (C - 1)));
+        float4 v = p[0];
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < C) v.x += part[r].x, v.y += part[r].y, v.z += part[r].z, v.w += part[r].w;
+        for (int r = 1; r < 8; ++r)
+          if (r < C) v.x += p[r].x, v.y += p[r].y, v.z += p[r].z, v.w += p[r].w;
         constexpr float fs = S_SCALE / (X_SCALE * X_SCALE);
         const uint32_t w0 = f2h2(v.x * fs, v.y * fs), w1 = f2h2(v.z * fs, v.w * fs);
-        const uint32_t at = ss + (uint32_t)((c >> 4) * f.sbox + i * 128 + ((((c >> 1) & 7) ^ (i & 7)) << 4) + (c & 1) * 8);
-        for (int r = 0; r < C; ++r) st_dsmem_v2(dsmem_addr(at, r), w0, w1);
+        const uint32_t o0 = __shfl_xor_sync(0xffffffffu, w0, 1), o1 = __shfl_xor_sync(0xffffffffu, w1, 1);
+        const uint4 o = lane & 1 ? make_uint4(o0, o1, w0, w1) : make_uint4(w0, w1, o0, o1);
+        const uint32_t to = ss + (uint32_t)((c >> 4) * f.sbox + i * 128 + ((((c >> 1) & 7) ^ (i & 7)) << 4));
+        if (e0 + lane < e1)
+          for (int r = lane & 1; r < C; r += 2) st_dsmem_v4(dsmem_addr(to, (rank + r) & (C - 1)), o);
+        if (C == 1 && (lane & 1) == 0 && e0 + lane < e1) st_dsmem_v4(to, o);
       }
     }
-    fence_proxy_all();
     cluster_sync();
-    fence_proxy_all();
     tc_fence_after();
     if (warp == 0 && elect_one()) {
+      fence_proxy_async();
       const uint32_t idesc = idesc_f32acc(128, f.mp, false);
+      const uint64_t d = sw128_desc(ss);
+#pragma unroll 4
       for (int ks = 0; ks < f.mp / 16; ++ks) {
-        const uint64_t d = desc_k(ss, f.sbox, ks);
-        tc_mma(d_q, d, d, idesc, ks > 0);
+        const uint32_t o = k_step(ks, f.sbox);
+        tc_mma(d_q, d + o, d + o, idesc, ks > 0);
       }
       tc_commit(&bar);
     }
     __syncwarp();
     arrived();
     const float fs = cb * (P_SCALE / S_SCALE), fq = cc * (P_SCALE / (S_SCALE * S_SCALE));
-    for (int c = 16 * group; c < f.mp; c += 32) {
+    for (int c = 16 * group; c < f.mp; c += 16 * FEW_GROUPS) {
       uint32_t w[16];
       __syncwarp();
       tc_ld16(d_q + lanes + c, w);
@@ -527,58 +574,61 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
           uint4 hi, lo;
           split8(v, hi, lo);
           *reinterpret_cast<uint4*>(pp + (pc >> 3) * f.pbox + at) = hi;
-          *reinterpret_cast<uint4*>(pp + plo + (pc >> 3) * f.pbox + at) = lo;
+          if (both) *reinterpret_cast<uint4*>(pp + plo + (pc >> 3) * f.pbox + at) = lo;
         }
     }
     ready();
     if (warp == 0 && elect_one()) {
+      fence_proxy_async();
       const uint32_t idesc = idesc_f32acc(128, f.mp, false);
-      for (int t = 0; t < tiles; ++t)
-        for (int g = 0; g < 3; ++g)
-          for (int ks = 0; ks < f.mp / 16; ++ks)
-            tc_mma(d_x + t * f.mp, desc_k((g == 2 ? xls : xs) + t * 128 * 128, f.xbox, ks), desc_k(ps + (g == 1 ? plo : 0), f.pbox, ks),
-                   idesc, g > 0 || ks > 0);
+      const uint64_t dh = sw128_desc(xs), dl = sw128_desc(xls), ph = sw128_desc(ps), pl = sw128_desc(ps + plo);
+      for (int t = 0; t < tiles; ++t) {
+        const uint32_t row = (uint32_t)t * (128 * 128 >> 4);
+#pragma unroll 4
+        for (int ks = 0; ks < f.mp / 16; ++ks) {
+          const uint32_t ox = row + k_step(ks, f.xbox), op = k_step(ks, f.pbox);
+          tc_mma(d_x + t * f.mp, dh + ox, ph + op, idesc, ks > 0);
+          if (both) {
+            tc_mma(d_x + t * f.mp, dh + ox, pl + op, idesc, 1);
+            tc_mma(d_x + t * f.mp, dl + ox, ph + op, idesc, 1);
+          }
+        }
+      }
       tc_commit(&bar);
     }
     __syncwarp();
     arrived();
-    const int chunks = f.mp / 16;  // of 16 columns, shared out between the two groups of warps
-    for (int u = group; u < tiles * chunks; u += 2) {
-      const int t = u / chunks, c = (u - t * chunks) * 16, l = t * 128 + i0;
+#pragma unroll
+    for (int n = 0; n < UNITS; ++n) {
+      int t, c;
+      if (!unit(n, t, c)) break;
       uint32_t w[16];
-      __syncwarp();
       tc_ld16(d_x + lanes + t * f.mp + c, w);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int pc = c / 8 + j;
-        uint4* const hp = reinterpret_cast<uint4*>(xp + xoff(l, pc));
-        uint4* const lp = reinterpret_cast<uint4*>(xlp + xoff(l, pc));
-        float h[8], lo[8], v[8];
-        unpack8_f16(*hp, h);
-        unpack8_f16(*lp, lo);
+      for (int e = 0; e < 16; ++e) x[n][e] = fmaf(1.0f / P_SCALE, __uint_as_float(w[e]), ca * x[n][e]);
+      if (step + 1 < a.steps) hand_over(n, t, c);
+    }
+  }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(1.0f / P_SCALE, __uint_as_float(w[8 * j + e]), ca * (h[e] + lo[e]));
-        if (!last) {
-          split8(v, *hp, *lp);
-          continue;
-        }
-        const int at = l0 + l;
-        if (at >= a.k) continue;
+  for (int n = 0; n < UNITS; ++n) {
+    int t, c;
+    if (!unit(n, t, c)) break;
+    const int at = l0 + t * 128 + i0;
+    if (at >= a.k) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= a.scale;
-        const uint4 o = pack8_bf16(v);
-        if (vec && 8 * pc < a.m) {
-          *reinterpret_cast<uint4*>(a.out + first + (size_t)at * a.cols + 8 * pc) = o;
-        } else {
-          const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+    for (int e = 0; e < 16; ++e) x[n][e] *= a.scale;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int i = 8 * pc + e;
-            if (i < a.m)
-              a.out[first + (tall ? (size_t)at * a.cols + i : (size_t)i * a.cols + at)] = (uint16_t)(e & 1 ? ow[e >> 1] >> 16 : ow[e >> 1]);
-          }
-        }
+    for (int h = 0; h < 16; h += 8) {
+      const uint4 o = pack8_bf16(&x[n][h]);
+      if (vec) {
+        if (c + h < a.m) *reinterpret_cast<uint4*>(a.out + first + (size_t)at * a.cols + c + h) = o;
+        continue;
       }
+      const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+      const size_t step = tall ? 1 : a.cols, from = first + (tall ? (size_t)at * a.cols : (size_t)at) + (size_t)(c + h) * step;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + h + e < a.m) a.out[from + e * step] = (uint16_t)(e & 1 ? ow[e >> 1] >> 16 : ow[e >> 1]);
     }
   }
   if (!ok) mbar_drain(&bar, phase ^ 1);  // products may still be under way
@@ -612,10 +662,6 @@ int parts_of(int rows, int cols) {
   const int64_t per = 8 * 8 * START_THREADS;
   return (int)std::min<int64_t>(128, ((int64_t)rows * cols + per - 1) / per);
 }
-
-// P X as P_hi X_hi + P_lo X_hi + P_hi X_lo up to this many rows, where the products are cheap beside X's traffic and few
-// rounding errors meet in a result; above, as P_hi X_hi, whose errors average out.
-bool few_rows(int m) { return m <= 128; }
 
 struct WsPlan {
   int m, pitch, mpitch, parts;
@@ -651,9 +697,15 @@ int few_ctas(int m, int k, int* kc) {
   if (m > 128) return 0;
   for (int C = 1; C <= 8; C *= 2) {
     *kc = ((k + C - 1) / C + 127) / 128 * 128;
-    if (*kc <= 256 || (C == 8 && few_plan(m, *kc).total <= 226 * 1024 && (*kc / 128 + 2) * few_plan(m, *kc).mp <= 512)) return C;
+    if (few_units(m, *kc) <= FEW_UNITS && *kc <= 1024 && few_plan(m, *kc).total <= 226 * 1024 && (*kc / 128 + 2) * few_plan(m, *kc).mp <= 512) return C;
   }
   return 0;
+}
+
+template <int UNITS>
+bool run_few(const FewArgs& a, int C, int n, cudaStream_t stream) {
+  return prepare<k_ortho_few<UNITS>>(226 * 1024) &&
+         launch<k_ortho_few<UNITS>>(dim3(C, n), FEW_THREADS, few_plan(a.m, a.kc).total, C, stream, a);
 }
 
 bool overlaps(const void* p, size_t np, const void* q, size_t nq) {
@@ -691,11 +743,13 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
   uint8_t* wsp = static_cast<uint8_t*>(ws);
   int* status = reinterpret_cast<int*>(ws) + H_STATUS;
   int kc = 0;
+  bool ok = true;
   if (const int C = few_ctas(w.m, std::max(rows, cols), &kc)) {
     FewArgs a = {in, out, fmt == FLINT_ORTHOGONALIZE_BF16, rows, cols, steps, w.m, std::max(rows, cols), kc, eps, scale / X_SCALE, {}, status};
     std::copy(coeffs, coeffs + 3 * steps, a.coeffs);
-    if (!prepare<k_ortho_few>(227 * 1024 - 1024)) return FLINT_MOE_ECUDA;
-    return launch<k_ortho_few>(dim3(C, n), FEW_THREADS, few_plan(w.m, kc).total, C, stream, a) ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
+    const int units = few_units(w.m, kc);
+    ok = units <= 1 ? run_few<1>(a, C, n, stream) : units <= 2 ? run_few<2>(a, C, n, stream) : run_few<4>(a, C, n, stream);
+    return ok ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
   }
   auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(wsp + o); };
   const bool tall = rows > cols;
@@ -704,7 +758,7 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
   auto map = [&](CUtensorMap* mp, size_t off, int64_t c, int64_t r, int64_t pitch, bool as_out) {
     return map_matrix(mp, at(off), c, r, pitch, n, r * pitch, as_out);
   };
-  bool ok = map(&s, w.s, m, m, w.mpitch, false) && map(&sout, w.s, m, m, w.mpitch, true);
+  ok = map(&s, w.s, m, m, w.mpitch, false) && map(&sout, w.s, m, m, w.mpitch, true);
   for (int i = 0; i < 2; ++i) {
     for (int h = 0; h < 2; ++h)
       ok = ok && map(&x[i][h], w.x[i][h], cols, rows, w.pitch, false) && map(&xout[i][h], w.x[i][h], cols, rows, w.pitch, true);
