@@ -14,22 +14,18 @@ __device__ __forceinline__ float2 sigmoid2(float g) {
   return g >= 0.f ? make_float2(r, t * r) : make_float2(t * r, r);
 }
 
-struct NoPre {
-  template <typename A>
-  __device__ __forceinline__ NoPre(const A&, const Part&, int) {}
-};
 
 // bf16 rows [M][N] as they are.
 struct Store {
   static constexpr bool PAIR = false;
-  static constexpr int MAPS = MOST;
+  static constexpr int MAPS = MOST, OUTS = 1, INS = 0;
   struct Args {};
   using Pre = NoPre;
-  static __device__ __forceinline__ void chunk(const Args&, const Maps& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
+  static __device__ __forceinline__ void chunk(const Args&, const MapsOf<Store>& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
                                                const Pre&) {
     const float* v = reinterpret_cast<const float*>(w);
     const uint4 o[4] = {pack8_bf16(v), pack8_bf16(v + 8), pack8_bf16(v + 16), pack8_bf16(v + 24)};
-    t.put(&maps.out[0], t.n0 + c, o);
+    t.put(&maps.io[0], t.n0 + c, o);
   }
 };
 
@@ -37,10 +33,10 @@ struct Store {
 template <bool SAVE>
 struct Glu {
   static constexpr bool PAIR = true;
-  static constexpr int MAPS = 1;
+  static constexpr int MAPS = 1, OUTS = 3, INS = 0;
   struct Args {};
   using Pre = NoPre;
-  static __device__ __forceinline__ void chunk(const Args&, const Maps& maps, Part& t, int c, uint32_t (&wg)[32], uint32_t (&wu)[32],
+  static __device__ __forceinline__ void chunk(const Args&, const MapsOf<Glu>& maps, Part& t, int c, uint32_t (&wg)[32], uint32_t (&wu)[32],
                                                const Pre&) {
     const float* g = reinterpret_cast<const float*>(wg);
     const float* u = reinterpret_cast<const float*>(wu);
@@ -52,14 +48,14 @@ struct Glu {
       for (int i = 0; i < 8; ++i) h[i] = __fdividef(g[8 * j + i], 1.0f + __expf(-g[8 * j + i])) * u[8 * j + i];
       o[j] = pack8_bf16(h);
     }
-    t.put(&maps.out[0], t.n0 + c, o);
+    t.put(&maps.io[0], t.n0 + c, o);
     if (SAVE) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = pack8_bf16(g + 8 * j);
-      t.put(&maps.out[1], t.n0 + c, o);
+      t.put(&maps.io[1], t.n0 + c, o);
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = pack8_bf16(u + 8 * j);
-      t.put(&maps.out[2], t.n0 + c, o);
+      t.put(&maps.io[2], t.n0 + c, o);
     }
   }
 };
@@ -67,7 +63,7 @@ struct Glu {
 // dg, du and h from dh and the kept g and u.
 struct DGlu {
   static constexpr bool PAIR = false;
-  static constexpr int MAPS = 1;
+  static constexpr int MAPS = 1, OUTS = 3, INS = 2;
   struct Args {
     const uint16_t* g;  // [M][N]
     const uint16_t* u;
@@ -83,8 +79,12 @@ struct DGlu {
         u[j] = in ? __ldcg(reinterpret_cast<const uint4*>(a.u + at + 8 * j)) : make_uint4(0, 0, 0, 0);
       }
     }
+    __device__ __forceinline__ Pre(const Part& t, const uint8_t* in) {
+      slot_row(t, in, g);
+      slot_row(t, in + SLOT, u);
+    }
   };
-  static __device__ __forceinline__ void chunk(const Args&, const Maps& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
+  static __device__ __forceinline__ void chunk(const Args&, const MapsOf<DGlu>& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
                                                const Pre& pre) {
     const float* d = reinterpret_cast<const float*>(w);
     uint4 og[4], ou[4], oh[4];
@@ -105,9 +105,9 @@ struct DGlu {
       ou[j] = pack8_bf16(du);
       oh[j] = pack8_bf16(h);
     }
-    t.put(&maps.out[0], t.n0 + c, og);
-    t.put(&maps.out[1], t.n0 + c, ou);
-    t.put(&maps.out[2], t.n0 + c, oh);
+    t.put(&maps.io[0], t.n0 + c, og);
+    t.put(&maps.io[1], t.n0 + c, ou);
+    t.put(&maps.io[2], t.n0 + c, oh);
   }
 };
 
@@ -218,13 +218,14 @@ extern "C" flint_moe_status flint_ffn_forward(const flint_ffn* f, const uint16_t
   uint8_t* wsp = static_cast<uint8_t*>(ws);
   uint16_t* h = reinterpret_cast<uint16_t*>(wsp + w.h);
   int* status = reinterpret_cast<int*>(ws) + H_STATUS;
-  AllMaps<1> m1;
-  AllMaps<MOST> m2;
-  Maps &glu = m1.of[0], &out = m2.of[0];
+  AllMaps<Glu<true>> m1;
+  AllMaps<Store> m2;
+  auto& glu = m1.of[0];
+  auto& out = m2.of[0];
   bool ok = map_in(&glu.a[0], x, H, T, ldx) && map_in(&glu.b[0], f->gate, H, I, H) && map_in(&glu.b[1], f->up, H, I, H) &&
-            map_out(&glu.out[0], h, I, T, I) && map_in(&out.a[0], h, I, T, I) && map_in(&out.b[0], f->down, I, H, I) &&
-            map_out(&out.out[0], y, H, T, ldy);
-  if (ok && g) ok = map_out(&glu.out[1], g, I, T, I) && map_out(&glu.out[2], u, I, T, I);
+            map_out(&glu.io[0], h, I, T, I) && map_in(&out.a[0], h, I, T, I) && map_in(&out.b[0], f->down, I, H, I) &&
+            map_out(&out.io[0], y, H, T, ldy);
+  if (ok && g) ok = map_out(&glu.io[1], g, I, T, I) && map_out(&glu.io[2], u, I, T, I);
   if (!ok) return FLINT_MOE_ECUDA;
   const gemm::Args a1 = {{{T, I, blocks_of(H), 1, 0, 0, 0, 0, 0, 1}}, 1, 0, status, 1};
   const gemm::Args a2 = {{{T, H, blocks_of(I), 1, 0, 0, 0, 0, 0, 1}}, 1, 0, status, 0};
@@ -272,23 +273,24 @@ extern "C" flint_moe_status flint_ffn_backward(const flint_ffn* f, const uint16_
       !map_in(&mgate, f->gate, H, I, H) || !map_in(&mup, f->up, H, I, H) || !map_in(&mdown, f->down, I, H, I) ||
       !map_in(&mh, h, I, T, I) || !map_out(&og, dg, I, T, I) || !map_out(&ou, du, I, T, I) || !map_out(&oh, h, I, T, I))
     return FLINT_MOE_ECUDA;
-  AllMaps<1> m1;
-  Maps& first = m1.of[0];
-  first.a[0] = mdy, first.b[0] = mdown, first.out[0] = og, first.out[1] = ou, first.out[2] = oh;
+  AllMaps<DGlu> m1;
+  auto& first = m1.of[0];
+  first.a[0] = mdy, first.b[0] = mdown, first.io[0] = og, first.io[1] = ou, first.io[2] = oh;
+  if (!map_out(&first.io[3], g, I, T, I) || !map_out(&first.io[4], u, I, T, I)) return FLINT_MOE_ECUDA;
   if (!run<DGlu>({{{T, I, blocks_of(H), 1, 0, 0, 0, 1, 0, 1}}, 1, 0, status, 1}, m1, {g, u}, stream)) return FLINT_MOE_ECUDA;
   // dx and the weights' gradients need nothing of one another: one launch, laid out as if all of them were asked for, so
   // that each has the same bits with and without the others.
   const int kb = blocks_of(T);
   const Problem px = {T, H, blocks_of(I), 2, 2, 2, 0, 1, 0, 1}, pw = {I, H, kb, 1, 0, 0, 1, 1, 0, 1}, pd = {H, I, kb, 1, 0, 0, 1, 1, 0, 1};
   const Choice choice = choose<Store>({{px, pw, pw, pd}, 4, 0, nullptr, 0});
-  AllMaps<MOST> m2;
+  AllMaps<Store> m2;
   gemm::Args a = {{}, 0, 0, status, 0};
   bool ok = true;
   auto add = [&](const Problem& p, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
                  uint16_t* out, int64_t ld) {
-    Maps& m = m2.of[a.n];
+    MapsOf<Store>& m = m2.of[a.n];
     m.a[0] = a0, m.a[1] = a1, m.b[0] = b0, m.b[1] = b1;
-    ok = ok && map_out(&m.out[0], out, p.N, p.M, ld);
+    ok = ok && map_out(&m.io[0], out, p.N, p.M, ld);
     a.p[a.n++] = p;
   };
   if (dx) add(px, mg, mu, mgate, mup, dx, lddx);

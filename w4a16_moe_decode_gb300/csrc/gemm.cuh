@@ -17,7 +17,7 @@ namespace gemm {
 constexpr int BK = 64;               // reduction of a stage: one 128-byte swizzled row of 16-bit values
 constexpr int BOX = 64 * BK * 2;     // 8 KiB: 64 x 64 values, what one TMA load moves
 constexpr int SLOT = 32 * 64;        // 2 KiB: 32 rows x 32 columns of 16-bit values, what one TMA store moves
-constexpr int SLOTS = 4;             // of each epilogue warp
+constexpr int SLOTS = 4;             // of each epilogue warp in k_gemm
 
 // k_gemm: one 128 x 128 tile a CTA, two CTAs on an SM, so that the one's epilogue runs beside the other's products; or
 // 128 x 64.
@@ -28,10 +28,15 @@ struct Half {
   static constexpr int TM = 128, TN = 64, CTAS = 1, STAGES = 4, GROUPS = 1, BBOXES = 1;
 };
 // k_gemm_pair: 256 x 256 tiles by pairs of CTAs (cta_group::2), each with half of A's rows and half of B's, 128 x 256 sums
-// a CTA; persistent, with two accumulators, so that a tile's epilogue runs beside the next one's products.
-struct Two {
-  static constexpr int TM = 256, TN = 256, CTAS = 2, STAGES = 5, GROUPS = 2, BBOXES = 2;
+// a CTA; persistent, with two accumulators, so that a tile's epilogue runs beside the next one's products. Epilogues that
+// read matrices have them brought by TMA, a chunk ahead, in the room of a stage (the gradients' first product, 8192 tokens
+// of 2048 x 8192: 309 us with loads by rows).
+template <int INS>
+struct Pairs {
+  static constexpr int TM = 256, TN = 256, CTAS = 2, STAGES = INS ? 4 : 5, GROUPS = 2, BBOXES = 2;
+  static constexpr int OUT_SLOTS = INS ? 2 : 4, IN_SLOTS = 2 * INS;  // of each epilogue warp
 };
+using Two = Pairs<0>;  // (the tiles are the same)
 // A CTA's operands of a stage: 128 x 64 of A, 64 BBOXES x 64 of B.
 template <typename C>
 constexpr int STAGE = (2 + C::BBOXES) * BOX;
@@ -39,7 +44,10 @@ constexpr int STAGE = (2 + C::BBOXES) * BOX;
 template <typename C>
 constexpr int THREADS = 64 + 128 * C::GROUPS;  // warp 0 loads, warp 1 issues the MMAs, the others the epilogue
 template <typename C>
-constexpr size_t SMEM = 1024 + (size_t)C::STAGES * STAGE<C> + (C::CTAS == 2 ? (size_t)C::GROUPS * 4 * SLOTS * SLOT : 0);
+constexpr size_t SMEM = 1024 + (size_t)C::STAGES * STAGE<C>;
+template <typename C>
+constexpr size_t PAIR_SMEM = SMEM<C> + (size_t)C::GROUPS * 4 * (C::OUT_SLOTS + C::IN_SLOTS) * SLOT;
+static_assert(PAIR_SMEM<Pairs<0>> <= 227 * 1024 - 512 && PAIR_SMEM<Pairs<2>> <= 227 * 1024 - 512, "shared memory of a CTA");
 static_assert(4 * SLOTS * SLOT + One::TM * One::TN * 4 <= One::STAGES * STAGE<One> && Half::STAGES * STAGE<Half> == One::STAGES * STAGE<One>,
               "k_gemm's epilogue writes where its operands were");
 
@@ -63,15 +71,22 @@ struct Args {
   int clear;        // the first kernel of a call clears the status word
 };
 
-// Operands in 64 x 64 boxes (x: the contiguous dimension, y: rows, z: matrix of the batch), outputs in 32 x 32 boxes.
+// Operands in 64 x 64 boxes (x: the contiguous dimension, y: rows, z: matrix of the batch); what an epilogue writes and,
+// behind that, what it reads in 32 x 32 boxes.
+template <int IO>
 struct Maps {
   CUtensorMap a[2], b[2];
-  CUtensorMap out[3];
+  CUtensorMap io[IO];
 };
-template <int N>
-struct AllMaps {
-  Maps of[N];
+// An epilogue E has OUTS and INS of them, for each of up to MAPS products of a launch.
+template <typename E>
+using MapsOf = Maps<E::OUTS + E::INS>;
+template <int IO, int N>
+struct MapSet {
+  Maps<IO> of[N];
 };
+template <typename E>
+using AllMaps = MapSet<E::OUTS + E::INS, E::MAPS>;
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
@@ -92,6 +107,10 @@ __device__ __forceinline__ void unpack8_bf16(const uint4 u, float* v) {
   v[4] = bf16lo(u.z), v[5] = bf16hi(u.z), v[6] = bf16lo(u.w), v[7] = bf16hi(u.w);
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // What an epilogue warp works on: 32 rows, a lane each.
 struct Part {
   int row0, row;  // the warp's first output row, and this lane's
@@ -101,14 +120,17 @@ struct Part {
   int lane;
   uint8_t* sm;    // the warp's slots
   uint32_t sm_addr;
-  int slot;       // the next one to fill
+  int slot, slots;  // the next one to fill, of how many
 
   // The place of 16-byte piece c of this lane's row in a slot: the 64-byte swizzle.
-  __device__ __forceinline__ uint4* piece(int s, int c) const {
-    return reinterpret_cast<uint4*>(sm + s * SLOT + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
-  }
+  static __device__ __forceinline__ uint32_t piece(int lane, int c) { return (uint32_t)(lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)); }
   __device__ __forceinline__ void begin() const {
-    if (lane == 0) bulk_wait_read<SLOTS - 1>();
+    if (lane == 0) {
+      if (slots == 4)
+        bulk_wait_read<3>();
+      else
+        bulk_wait_read<1>();
+    }
     __syncwarp();
   }
   __device__ __forceinline__ void end(const CUtensorMap* map, int x, int y, bool in) {
@@ -118,14 +140,14 @@ struct Part {
       if (in) tma_store_3d(map, x, y, z, sm_addr + slot * SLOT);
       bulk_commit();
     }
-    slot = slot + 1 == SLOTS ? 0 : slot + 1;
+    slot = slot + 1 == slots ? 0 : slot + 1;
   }
   // 32 columns x .. of the warp's rows, this lane's row in v: to the next slot, and from there to memory (what lies
   // outside the matrix is left out).
   __device__ __forceinline__ void put(const CUtensorMap* map, int x, const uint4 (&v)[4]) {
     begin();
 #pragma unroll
-    for (int c = 0; c < 4; ++c) *piece(slot, c) = v[c];
+    for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(sm + slot * SLOT + piece(lane, c)) = v[c];
     end(map, x, row0, x < N && row0 < M);
   }
   // The same values as columns row0 .. of rows x ..
@@ -141,6 +163,18 @@ struct Part {
     end(map, row0, x, x < N && row0 < M);
   }
 };
+
+// Nothing read beside the sums.
+struct NoPre {
+  template <typename A>
+  __device__ __forceinline__ NoPre(const A&, const Part&, int) {}
+  __device__ __forceinline__ NoPre(const Part&, const uint8_t*) {}
+};
+// This lane's row of an input slot.
+__device__ __forceinline__ void slot_row(const Part& t, const uint8_t* in, uint4 (&v)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v[c] = lds128(in + Part::piece(t.lane, c));
+}
 
 // Tiles of a launch: its products one after the other, each batch of one in bands of eight rows of tiles, column by
 // column, so that the tiles that run at once share their operands in L2; above the diagonal only, row by row, where the
@@ -212,7 +246,7 @@ __device__ __forceinline__ uint32_t idesc_of(const Args& a, const Problem& p, in
 // order.
 template <typename C, typename E>
 __global__ void __launch_bounds__(THREADS<C>, 2)
-    k_gemm(const Args a, const __grid_constant__ AllMaps<E::MAPS> all, const typename E::Args e) {
+    k_gemm(const Args a, const __grid_constant__ AllMaps<E> all, const typename E::Args e) {
   extern __shared__ uint8_t dsmem[];
   constexpr int ST = C::STAGES;
   __shared__ uint64_t full[ST], empty[ST], acc_full;
@@ -235,14 +269,19 @@ __global__ void __launch_bounds__(THREADS<C>, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  pdl_wait();
-  pdl_trigger();
-  if (a.clear && threadIdx.x == 0 && blockIdx.x + blockIdx.y == 0) *a.status = 0;
   // (x: the CTAs of a tile, y: tiles)
   const int S = gridDim.x, rank = blockIdx.x;
   const Walk<C, E::PAIR> w(a, blockIdx.y);
   const Problem& p = a.p[w.i];
-  const Maps& maps = all.of[w.i];
+  const MapsOf<E>& maps = all.of[w.i];
+  if (threadIdx.x == 0) {
+    prefetch_map(&maps.a[0]);
+    prefetch_map(&maps.b[0]);
+    prefetch_map(&maps.io[0]);
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (a.clear && threadIdx.x == 0 && blockIdx.x + blockIdx.y == 0) *a.status = 0;
   const int blocks = p.blocks(), b0 = blocks * rank / S, b1 = blocks * (rank + 1) / S;
   const int m0 = w.m * C::TM, n0 = w.n * w.COLS;
   if (warp == 0) {
@@ -301,6 +340,7 @@ __global__ void __launch_bounds__(THREADS<C>, 2)
   t.sm_addr = base + q * SLOTS * SLOT;
   t.sm = dsmem + (t.sm_addr - smem_addr(dsmem));
   t.slot = 0;
+  t.slots = SLOTS;
   constexpr int CHUNKS = Walk<C, E::PAIR>::COLS / 32;
   if (warp >= 2) {
     const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16);
@@ -418,10 +458,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
 
 template <typename E>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
-    k_gemm_pair(const Args a, const __grid_constant__ AllMaps<E::MAPS> all, const typename E::Args e) {
+    k_gemm_pair(const Args a, const __grid_constant__ AllMaps<E> all, const typename E::Args e) {
   extern __shared__ uint8_t dsmem[];
-  constexpr int ST = Two::STAGES, EPI = 4 * Two::GROUPS;
+  using C = Pairs<E::INS>;
+  constexpr int ST = C::STAGES, EPI = 4 * C::GROUPS;
   __shared__ uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2];
+  __shared__ uint64_t in_full[EPI][2];  // a warp's input slots filled
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -437,6 +479,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 2 * EPI);
     }
+    if (E::INS)
+      for (int w = 0; w < EPI; ++w)
+        for (int b = 0; b < 2; ++b) mbar_init(&in_full[w][b], 1);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -450,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
   pdl_trigger();
   if (a.clear && threadIdx.x == 0 && blockIdx.x == 0) *a.status = 0;
   using W = Walk<Two, E::PAIR>;
-  const int tiles = (int)W::tiles(a), step = gridDim.x >> 1, first = blockIdx.x >> 1;
+  const int step = gridDim.x >> 1, first = blockIdx.x >> 1, tiles = (int)W::tiles(a);
   if (warp == 0) {
     if (lane == 0) {
       int i = 0, s = 0;  // stages so far, the next one's place
@@ -460,8 +505,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
       for (int t = first; t < tiles && ok; t += step) {
         const W w(a, t);
         const Problem& p = a.p[w.i];
-        const Maps& maps = all.of[w.i];
-        // The first CTA holds the tile's columns 0 .. 127 of B (or the gate's rows), the second the others.
+        const MapsOf<E>& maps = all.of[w.i];
+        // The first CTA holds the first half of the tile's columns of B (or the gate's rows), the second the others.
         const int m = w.m * Two::TM + (int)rank * 128, nb = w.n * W::COLS + (E::PAIR ? 0 : (int)rank * 128);
         const int n[2] = {nb, nb + 64}, per = p.kb;
         const bool a_mn = p.a_mn, b_mn = p.b_mn;
@@ -472,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
             const uint32_t sm = base + s * STAGE<Two>, bar = bar0 + s * 8;
             if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE<Two>);
             load_stage<Two>(a_mn, b_mn, kb * BK, m, n,
-                       [&](int off, bool is_a, int, int x, int y) { tma_load_3d_pair(sm + off, is_a ? am : bm, x, y, w.z, bar); });
+                            [&](int off, bool is_a, int, int x, int y) { tma_load_3d_pair(sm + off, is_a ? am : bm, x, y, w.z, bar); });
             ++i;
             if (++s == ST) s = 0, phase ^= 1;
           }
@@ -488,7 +533,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step, ++n) {
-        const Problem& p = a.p[W(a, t).i];
+        const W w(a, t);
+        const Problem& p = a.p[w.i];
         const uint32_t idesc = idesc_of(a, p, Two::TM, Two::TN);
         const Operand oa = operand(p.a_mn), ob = operand(p.b_mn);
         const int blocks = p.blocks();
@@ -516,13 +562,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
     }
   } else {
     const int q = warp & 3, group = (warp - 2) >> 2;
+    constexpr int each = W::COLS / C::GROUPS;  // columns of a tile for this warp's group
     Part t;
     t.lane = lane;
-    t.sm_addr = base + ST * STAGE<Two> + (uint32_t)((warp - 2) * SLOTS * SLOT);
+    t.sm_addr = base + ST * STAGE<Two> + (uint32_t)((warp - 2) * (C::OUT_SLOTS + C::IN_SLOTS) * SLOT);
     t.sm = dsmem + (t.sm_addr - smem_addr(dsmem));
     t.slot = 0;
+    t.slots = C::OUT_SLOTS;
+    const uint32_t in_addr = t.sm_addr + C::OUT_SLOTS * SLOT;
+    const uint8_t* const in_sm = t.sm + C::OUT_SLOTS * SLOT;
+    int fetched = 0, used = 0;  // chunks
+    // What the epilogue reads beside the sums for the chunk at column c of tile `w`.
+    auto fetch = [&](const W& w, int c) {
+      if constexpr (E::INS > 0) {
+        const int row0 = w.m * Two::TM + (int)rank * 128 + q * 32;
+        if (row0 >= a.p[w.i].M) return;
+        if (lane == 0) {
+          const int b = fetched & 1;
+          mbar_arrive_expect_tx(&in_full[warp - 2][b], E::INS * SLOT);
+          for (int i = 0; i < E::INS; ++i)
+            tma_load_3d(in_addr + (b * E::INS + i) * SLOT, &all.of[w.i].io[E::OUTS + i], w.n * W::COLS + c, row0, w.z, &in_full[warp - 2][b]);
+        }
+        ++fetched;
+      }
+    };
     uint32_t w1[32], w2[32];
     int n = 0;
+    bool ok = true;
+    if (first < tiles) fetch(W(a, first), group * each);
     for (int ti = first; ti < tiles; ti += step, ++n) {
       const int b = n & 1;
       const W w(a, ti);
@@ -534,31 +601,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
       t.row0 = w.m * Two::TM + (int)rank * 128 + q * 32;
       t.row = t.row0 + lane;
       t.twice = p.sym && w.m != w.n;
-      constexpr int EACH = W::COLS / Two::GROUPS;
-      typename E::Pre pre(e, t, group * EACH);  // what a chunk reads besides the sums is asked for a chunk ahead
-      const bool ok = wait_ab(&acc_full[b], (n >> 1) & 1, abort, a.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      ok = __all_sync(0xffffffffu, wait_ab(&acc_full[b], (n >> 1) & 1, abort, a.status));
+      if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tmem + b * Two::TN + ((uint32_t)(q * 32) << 16);
       const bool live = t.row0 < t.M;
 #pragma unroll 1
-      for (int c = group * EACH; c < (group + 1) * EACH; c += 32) {
-        const bool last = c + 32 == (group + 1) * EACH;
+      for (int c = group * each; c < (group + 1) * each; c += 32) {
+        const bool last = c + 32 == (group + 1) * each;
         if (live) {
           tc_ld32_async(acc + c, w1);
           if constexpr (E::PAIR) tc_ld32_async(acc + Two::TN / 2 + c, w2);
         }
-        const typename E::Pre now = pre;
-        if (!last) pre = typename E::Pre(e, t, c + 32);
         tc_wait_ld();
         if (last) {  // this warp has read the accumulator
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_addr(&acc_empty[b]), 0));
         }
-        if (live) E::chunk(e, all.of[w.i], t, c, w1, w2, now);
+        // The next chunk's into the other slots, which all lanes have read.
+        if (E::INS) {
+          __syncwarp();
+          if (!last)
+            fetch(w, c + 32);
+          else if (ti + step < tiles)
+            fetch(W(a, ti + step), group * each);
+        }
+        if (live) {
+          if (E::INS) {
+            ok = __all_sync(0xffffffffu, wait_ab(&in_full[warp - 2][used & 1], (used >> 1) & 1, abort, a.status));
+            if (!ok) break;
+          }
+          const typename E::Pre pre(t, in_sm + (used & 1) * E::INS * SLOT);
+          if (E::INS) fence_proxy_async();  // these reads come before the copies into the slots
+          E::chunk(e, all.of[w.i], t, c, w1, w2, pre);
+          ++used;
+        }
       }
+      if (!ok) break;
     }
+    if (E::INS && lane == 0)  // after a failed wait: copies still on their way
+      for (; used < fetched; ++used) mbar_drain(&in_full[warp - 2][used & 1], (used >> 1) & 1);
     if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
@@ -630,9 +713,7 @@ inline int sm_count() {
   return n;
 }
 
-// How a launch's products are computed: by pairs of CTAs where their tiles fill the card, or else by S CTAs a tile, as many
-// as run one on an SM and have four k-blocks each: 77 tokens of 2048 x 8192 36.7 us a call and 72.6 with one CTA a tile;
-// 509 of 1000 x 2040 21.4, 27.7, and 28.7 with two on an SM.
+// How a launch's products are computed: by pairs of CTAs, or by S CTAs a tile of 128 x 128 or 128 x 64.
 struct Choice {
   int kind;  // 0: pairs, 1: 128 x 128 tiles, 2: 128 x 64
   int S;
@@ -642,29 +723,43 @@ inline Args whole(Args a) {
   for (int i = 0; i < a.n; ++i) a.p[i].sym = 0;
   return a;
 }
+// The one with the fewest cycles by this estimate, of rounds of CTAs, a k-block's cycles and a tile's beginning and end
+// (from the times of products of 128 to 8192 rows): pairs take 600 cycles a k-block; a CTA alone on its SM 450 (300 with
+// 64 columns), since two or three stages in flight do not cover memory's latency, and two on an SM 850 (500) together; a
+// tile's beginning and end take 9000, 6500 (5000), sums over a cluster 3000 more.
 template <typename E>
 Choice choose(const Args& a) {
-  const int64_t pairs = Walk<Two, E::PAIR>::tiles(a), sms = sm_count() & ~1;
-  if (2 * pairs >= sms) return {0, 1};
-  int blocks = 1 << 30;
-  for (int i = 0; i < a.n; ++i) blocks = std::min(blocks, a.p[i].blocks());
-  auto split = [&](int64_t tiles) {
-    int S = 1;
-    while (S < 8 && tiles * S * 2 <= sms && S * 8 <= blocks) S *= 2;
-    return S;
+  const int64_t sms = sm_count() & ~1;
+  int64_t blocks = 0, least = 1 << 30;
+  for (int i = 0; i < a.n; ++i) {
+    blocks = std::max<int64_t>(blocks, a.p[i].blocks());
+    least = std::min<int64_t>(least, a.p[i].blocks());
+  }
+  const int64_t pairs = Walk<Two, E::PAIR>::tiles(a);
+  Choice best = {0, 1};
+  int64_t cost = (2 * pairs + sms - 1) / sms * blocks * 600 + 9000;
+  auto consider = [&](int kind, int64_t tiles, int alone, int two, int ends) {
+    for (int S = 1; S <= 8; S *= 2) {
+      if (S > 1 && (tiles * S > sms || 4 * S > least)) break;
+      const int64_t per = (blocks + S - 1) / S, n = tiles * S;
+      const int64_t c = (n <= sms ? per * alone : (n + 2 * sms - 1) / (2 * sms) * (per * two + ends / 2)) + ends + (S > 1 ? 3000 : 0);
+      if (c < cost) cost = c, best = {kind, S};
+    }
   };
+  const int64_t ones = Walk<One, E::PAIR>::tiles(a);
+  if (ones <= 65535) consider(1, ones, 450, 850, 6500);  // (a grid's second dimension)
   if constexpr (!E::PAIR) {
     const int64_t halves = Walk<Half, false>::tiles(whole(a));
-    if (halves <= sms) return {2, split(halves)};
+    if (halves <= 65535) consider(2, halves, 300, 500, 5000);
   }
-  return {1, split(Walk<One, E::PAIR>::tiles(a))};
+  return best;
 }
 
 template <typename E>
-bool run(const Args& a, const AllMaps<E::MAPS>& m, const typename E::Args& e, cudaStream_t stream, const Choice& c) {
+bool run(const Args& a, const AllMaps<E>& m, const typename E::Args& e, cudaStream_t stream, const Choice& c) {
   if (c.kind == 0) {
     const int64_t pairs = std::min<int64_t>(Walk<Two, E::PAIR>::tiles(a), sm_count() / 2);
-    return launch<k_gemm_pair<E>>(dim3(2 * (unsigned)pairs), THREADS<Two>, SMEM<Two>, 0, stream, a, m, e);
+    return launch<k_gemm_pair<E>>(dim3(2 * (unsigned)pairs), THREADS<Two>, PAIR_SMEM<Pairs<E::INS>>, 0, stream, a, m, e);
   }
   if constexpr (!E::PAIR)
     if (c.kind == 2) {
@@ -674,7 +769,7 @@ bool run(const Args& a, const AllMaps<E::MAPS>& m, const typename E::Args& e, cu
   return launch<k_gemm<One, E>>(dim3(c.S, (unsigned)Walk<One, E::PAIR>::tiles(a)), THREADS<One>, SMEM<One>, c.S, stream, a, m, e);
 }
 template <typename E>
-bool run(const Args& a, const AllMaps<E::MAPS>& m, const typename E::Args& e, cudaStream_t stream) {
+bool run(const Args& a, const AllMaps<E>& m, const typename E::Args& e, cudaStream_t stream) {
   return run<E>(a, m, e, stream, choose<E>(a));
 }
 

@@ -182,19 +182,17 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_split(const Start a) {
 // ---------------------------------------------------------------------------
 struct Gram {
   static constexpr bool PAIR = false;
-  static constexpr int MAPS = 1;
+  static constexpr int MAPS = 1, OUTS = 1, INS = 0;
   struct Args {};
-  struct Pre {
-    __device__ __forceinline__ Pre(const Args&, const Part&, int) {}
-  };
-  static __device__ __forceinline__ void chunk(const Args&, const Maps& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
+  using Pre = NoPre;
+  static __device__ __forceinline__ void chunk(const Args&, const MapsOf<Gram>& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
                                                const Pre&) {
     float* v = reinterpret_cast<float*>(w);
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= S_SCALE / (X_SCALE * X_SCALE);
     const uint4 o[4] = {pack8_f16(v), pack8_f16(v + 8), pack8_f16(v + 16), pack8_f16(v + 24)};
-    t.put(&maps.out[0], t.n0 + c, o);
-    if (t.twice) t.put_transposed(&maps.out[0], t.n0 + c, o);
+    t.put(&maps.io[0], t.n0 + c, o);
+    if (t.twice) t.put_transposed(&maps.io[0], t.n0 + c, o);
   }
 };
 
@@ -208,7 +206,7 @@ __device__ __forceinline__ void load_row(const Part& t, const uint16_t* m, int p
 
 struct Poly {
   static constexpr bool PAIR = false;
-  static constexpr int MAPS = 1;
+  static constexpr int MAPS = 1, OUTS = 2, INS = 1;
   struct Args {
     const uint16_t* s;
     int pitch;
@@ -218,8 +216,9 @@ struct Poly {
   struct Pre {
     uint4 s[4];
     __device__ __forceinline__ Pre(const Args& a, const Part& t, int c) { load_row(t, a.s, a.pitch, c, s); }
+    __device__ __forceinline__ Pre(const Part& t, const uint8_t* in) { slot_row(t, in, s); }
   };
-  static __device__ __forceinline__ void chunk(const Args& a, const Maps& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
+  static __device__ __forceinline__ void chunk(const Args& a, const MapsOf<Poly>& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
                                                const Pre& pre) {
     const float fs = a.b * (P_SCALE / S_SCALE), fq = a.c * (P_SCALE / (S_SCALE * S_SCALE));
     uint4 hi[4], lo[4];
@@ -231,11 +230,11 @@ struct Poly {
       for (int i = 0; i < 8; ++i) v[i] = fmaf(fs, v[i], fq * __uint_as_float(w[8 * j + i]));
       split8(v, hi[j], lo[j]);
     }
-    t.put(&maps.out[0], t.n0 + c, hi);
-    if (t.twice) t.put_transposed(&maps.out[0], t.n0 + c, hi);
+    t.put(&maps.io[0], t.n0 + c, hi);
+    if (t.twice) t.put_transposed(&maps.io[0], t.n0 + c, hi);
     if (a.lo) {
-      t.put(&maps.out[1], t.n0 + c, lo);
-      if (t.twice) t.put_transposed(&maps.out[1], t.n0 + c, lo);
+      t.put(&maps.io[1], t.n0 + c, lo);
+      if (t.twice) t.put_transposed(&maps.io[1], t.n0 + c, lo);
     }
   }
 };
@@ -243,7 +242,7 @@ struct Poly {
 template <bool LAST>
 struct Update {
   static constexpr bool PAIR = false;
-  static constexpr int MAPS = 1;
+  static constexpr int MAPS = 1, OUTS = 2, INS = 2;
   struct Args {
     const uint16_t *hi, *lo;
     int pitch;
@@ -256,8 +255,12 @@ struct Update {
       load_row(t, a.hi, a.pitch, c, hi);
       load_row(t, a.lo, a.pitch, c, lo);
     }
+    __device__ __forceinline__ Pre(const Part& t, const uint8_t* in) {
+      slot_row(t, in, hi);
+      slot_row(t, in + SLOT, lo);
+    }
   };
-  static __device__ __forceinline__ void chunk(const Args& a, const Maps& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
+  static __device__ __forceinline__ void chunk(const Args& a, const MapsOf<Update>& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
                                                const Pre& pre) {
     constexpr float fp = 1.0f / P_SCALE;  // P X comes scaled by both
     uint4 hv[4], lv[4];
@@ -277,18 +280,18 @@ struct Update {
       }
     }
     if (!LAST || t.N % 8 == 0) {
-      t.put(&maps.out[0], t.n0 + c, hv);
-      if (!LAST) t.put(&maps.out[1], t.n0 + c, lv);
+      t.put(&maps.io[0], t.n0 + c, hv);
+      if (!LAST) t.put(&maps.io[1], t.n0 + c, lv);
     } else {  // rows that TMA cannot reach: through a slot, a row's neighbours by neighbouring lanes
       __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) *t.piece(0, j) = hv[j];
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(t.sm + Part::piece(t.lane, j)) = hv[j];
       __syncwarp();
       const int col = t.n0 + c + t.lane;
       for (int r = 0; r < 32 && t.row0 + r < t.M; ++r)
         if (col < t.N)
           a.out[((size_t)t.z * t.M + t.row0 + r) * t.N + col] =
-              *reinterpret_cast<const uint16_t*>(t.sm + r * 64 + ((((t.lane >> 3) ^ (r >> 1)) & 3) << 4) + (t.lane & 7) * 2);
+              *reinterpret_cast<const uint16_t*>(t.sm + Part::piece(r, t.lane >> 3) + (t.lane & 7) * 2);
     }
   }
 };
@@ -657,10 +660,10 @@ bool supported(int n, int rows, int cols) {
          std::max(rows, cols) <= FLINT_ORTHOGONALIZE_MAX_SIDE && std::min(rows, cols) <= 16384;
 }
 
-// Blocks of a matrix in the first two kernels: eight pieces of eight values a thread, 128 at most.
+// Blocks of a matrix in the first two kernels: four pieces of eight values a thread, 1024 at most.
 int parts_of(int rows, int cols) {
-  const int64_t per = 8 * 8 * START_THREADS;
-  return (int)std::min<int64_t>(128, ((int64_t)rows * cols + per - 1) / per);
+  const int64_t per = 4 * 8 * START_THREADS;
+  return (int)std::min<int64_t>(1024, ((int64_t)rows * cols + per - 1) / per);
 }
 
 struct WsPlan {
@@ -773,12 +776,14 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
   if (!launch<k_ortho_norm>(grid, START_THREADS, 0, 0, stream, st) || !launch<k_ortho_split>(grid, START_THREADS, 0, 0, stream, st))
     return FLINT_MOE_ECUDA;
   const int kx = ((tall ? rows : cols) + BK - 1) / BK, km = (m + BK - 1) / BK;
-  AllMaps<1> mg, mp, mu;
+  AllMaps<Gram> mg;
+  AllMaps<Poly> mp;
+  AllMaps<Update<false>> mu;
   mp.of[0].a[0] = mp.of[0].b[0] = s;
-  mg.of[0].out[0] = sout;
+  mp.of[0].io[2] = mg.of[0].io[0] = sout;
   const bool few = few_rows(m);
   for (int h = 0; h < 2; ++h) {
-    mp.of[0].out[h] = pout[h];
+    mp.of[0].io[h] = pout[h];
     (tall ? mu.of[0].b : mu.of[0].a)[h] = p[h];
   }
   for (int i = 0; i < steps; ++i) {
@@ -788,7 +793,8 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
     mg.of[0].a[0] = mg.of[0].b[0] = x[i & 1][0];
     for (int h = 0; h < 2; ++h) {
       (tall ? mu.of[0].a : mu.of[0].b)[h] = x[i & 1][h];
-      mu.of[0].out[h] = last ? o : xout[(i + 1) & 1][h];
+      mu.of[0].io[h] = last ? o : xout[(i + 1) & 1][h];
+      mu.of[0].io[2 + h] = xout[i & 1][h];
     }
     ok = run<Gram>({{{m, m, kx, 1, 0, 0, tall, tall, 1, n}}, 1, 1, status, 0}, mg, {}, stream) &&
          run<Poly>({{{m, m, km, 1, 0, 0, 0, 0, 1, n}}, 1, 1, status, 0}, mp, {at(w.s), w.mpitch, cf[1], cf[2], few}, stream);
