@@ -1841,36 +1841,65 @@ __global__ void __launch_bounds__(256) k_gemv(GemvArgs a) {
 // ===========================================================================
 // Tiles of weights in flight: two, or one of BF16 weights (65 KB a tile of 2048 columns).
 __host__ __device__ constexpr int GEMV_BUFS(int fmt) { return fmt == FLINT_MOE_NVFP4 ? 2 : 1; }
-__host__ __device__ inline size_t gemv_rows_smem(int K, int B, int fmt, int nw, int ntmax, size_t* xs_off, size_t* inv_off,
+// (nw: warps of a group, of GR groups)
+__host__ __device__ inline size_t gemv_rows_smem(int K, int B, int fmt, int nw, int ntmax, int GR, size_t* xs_off, size_t* inv_off,
                                                  size_t* red_off, size_t* bar_off) {
   const int kgb = fmt == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16;
   size_t o = 0;
-  o += (size_t)GEMV_BUFS(fmt) * (K / KG_COLS) * kgb;
+  o += (size_t)(GR > 1 ? GR : GEMV_BUFS(fmt)) * (K / KG_COLS) * kgb;
   *xs_off = o;   o += (size_t)B * (K * 2 + 16);
   *inv_off = o;  o += sizeof(float) * MAX_BATCH;
-  *red_off = o;  o += sizeof(float) * nw * ntmax * 128;
+  *red_off = o;  o += sizeof(float) * GR * nw * ntmax * 128;
   o = (o + 15) & ~(size_t)15;
-  *bar_off = o;  o += sizeof(uint64_t) * nw * 2;
+  *bar_off = o;  o += sizeof(uint64_t) * GR * nw * 2;
   return o;
 }
 
-template <int FMT, int NTMAX, GemvEnd END>
-__global__ void __launch_bounds__(256) k_gemv_rows(GemvArgs a) {
+// The threads of a group meet; whether all of them say yes.
+template <int GR>
+__device__ __forceinline__ void group_sync(int group) {
+  if constexpr (GR == 1)
+    __syncthreads();
+  else
+    asm volatile("barrier.cta.sync.aligned %0, 256;" ::"r"(group + 1) : "memory");
+}
+template <int GR>
+__device__ __forceinline__ bool group_all(int group, bool ok) {
+  if constexpr (GR == 1) {
+    return __syncthreads_and(ok);
+  } else {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred.aligned q, %2, 256, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((int)ok), "r"(group + 1)
+        : "memory");
+    return r != 0;
+  }
+}
+
+// GR = 2: two groups of eight warps share a block's rows, each with its own tiles (and one buffer of weights). Rows that
+// leave an SM room for one block only would have eight warps on it otherwise, which take turns waiting.
+template <int FMT, int NTMAX, GemvEnd END, int GR = 1>
+__global__ void __launch_bounds__(256 * GR) k_gemv_rows(GemvArgs a) {
   constexpr bool ADD = END == GEMV_ADD;
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16, NB = GEMV_BUFS(FMT);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const int nw = blockDim.x >> 5;
+  constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16, NB = GR > 1 ? 1 : GEMV_BUFS(FMT);
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int nw = (blockDim.x >> 5) / GR;  // of the group
+  const int group = GR > 1 ? wid >> 3 : 0, warp = wid - group * nw, thread = threadIdx.x - group * nw * 32;
   const int KGW = (a.K / KG_COLS) / nw;  // k-groups per warp
   size_t xs_off, inv_off, red_off, bar_off;
-  gemv_rows_smem(a.K, a.B, FMT, nw, NTMAX, &xs_off, &inv_off, &red_off, &bar_off);
+  gemv_rows_smem(a.K, a.B, FMT, nw, NTMAX, GR, &xs_off, &inv_off, &red_off, &bar_off);
   const uint32_t bytes = (uint32_t)KGW * KGB;
-  uint8_t* const wb0 = smem + (size_t)warp * NB * bytes;  // this warp's NB buffers
+  uint8_t* const wb0 = smem + (size_t)wid * NB * bytes;  // this warp's NB buffers
   uint8_t* xs = smem + xs_off;
   float* s_inv = reinterpret_cast<float*>(smem + inv_off);
-  float* red = reinterpret_cast<float*>(smem + red_off);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + bar_off) + warp * 2;
+  float* red = reinterpret_cast<float*>(smem + red_off) + group * nw * NTMAX * 128;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + bar_off) + wid * 2;
   const int xstride = a.K * 2 + 16, tiles = a.N / 16;
+  const int first = blockIdx.x * GR + group, step = gridDim.x * GR;
   auto fetch = [&](int tile, int b) {  // by one lane
     mbar_arrive_expect_tx(&bar[b], bytes);
     bulk_g2s_stream(wb0 + (size_t)b * bytes, a.packed + (int64_t)tile * a.L.dn_tile + (int64_t)warp * bytes, bytes, &bar[b]);
@@ -1879,11 +1908,11 @@ __global__ void __launch_bounds__(256) k_gemv_rows(GemvArgs a) {
     for (int b = 0; b < NB; ++b) mbar_init(&bar[b], 1);
     fence_mbar_init();
     for (int b = 0; b < NB; ++b)
-      if ((int)(blockIdx.x + b * gridDim.x) < tiles) fetch(blockIdx.x + b * gridDim.x, b);
+      if (first + b * step < tiles) fetch(first + b * step, b);
   }
   if (!ADD) pdl_wait();  // x may be the previous kernel's output
   pdl_trigger();
-  stage_rows<FMT>(a.x, a.B, a.K, a.prenorm, a.gamma, a.eps, xs, xstride, s_inv, warp, nw, lane);
+  stage_rows<FMT>(a.x, a.B, a.K, a.prenorm, a.gamma, a.eps, xs, xstride, s_inv, wid, GR * nw, lane);
   __syncthreads();
   const int nt_used = (a.B + 7) >> 3;
   int tok[NTMAX];  // column g of token tile nt is token 8 nt + g (past B: a repeat of token B - 1)
@@ -1892,7 +1921,7 @@ __global__ void __launch_bounds__(256) k_gemv_rows(GemvArgs a) {
   const float G = FMT == FLINT_MOE_NVFP4 ? a.G[0] : 1.0f, Gu = END == GEMV_GLU && FMT == FLINT_MOE_NVFP4 ? a.G[1] : 1.0f;
   int i = 0;
   bool ok = true;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++i) {
+  for (int tile = first; tile < tiles; tile += step, ++i) {
     const int b = i % NB;
     float acc[2][NTMAX][4];
 #pragma unroll
@@ -1927,12 +1956,12 @@ __global__ void __launch_bounds__(256) k_gemv_rows(GemvArgs a) {
     for (int nt = 0; nt < NTMAX; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) red[((warp * NTMAX + nt) * 32 + lane) * 4 + e] = acc[0][nt][e] + acc[1][nt][e];
-    ok = __syncthreads_and(ok);
+    ok = group_all<GR>(group, ok);
     if (!ok) {  // a wait gave up: the tile and those behind it stay unwritten
       if (ADD && i == 0) pdl_wait();  // the call must not end before the adapters' kernel
       break;
     }
-    const int next = tile + NB * (int)gridDim.x;
+    const int next = tile + NB * step;
     if (lane == 0 && next < tiles) {
       fence_proxy_async();  // this warp's reads of the buffer come before the copy into it
       fetch(next, b);
@@ -1941,7 +1970,7 @@ __global__ void __launch_bounds__(256) k_gemv_rows(GemvArgs a) {
     // Output (row r of the tile, token t): token tile t / 8, fragment lane
     // 4 (r % 8) + (t % 8) / 2, element 2 (r / 8) + t % 2.
     if constexpr (END == GEMV_GLU) {
-      for (int p = threadIdx.x; p < 8 * a.B; p += blockDim.x) {
+      for (int p = thread; p < 8 * a.B; p += 32 * nw) {
         const int r = p & 7, t = p >> 3, nt = t >> 3, c = t & 7;
         float gv = 0.f, uv = 0.f;
         for (int w2 = 0; w2 < nw; ++w2) {
@@ -1952,7 +1981,7 @@ __global__ void __launch_bounds__(256) k_gemv_rows(GemvArgs a) {
         glu_store(a, t, tile, r, (gv * s_inv[t]) * G, (uv * s_inv[t]) * Gu);
       }
     } else {
-      for (int p = threadIdx.x; p < 16 * a.B; p += blockDim.x) {
+      for (int p = thread; p < 16 * a.B; p += 32 * nw) {
         const int r = p & 15, t = p >> 4, nt = t >> 3, c = t & 7;
         const int ln = 4 * (r & 7) + (c >> 1), e = 2 * (r >> 3) + (c & 1);
         float v = 0.f;
@@ -1960,11 +1989,11 @@ __global__ void __launch_bounds__(256) k_gemv_rows(GemvArgs a) {
         gemv_store<ADD>(a, t, tile * 16 + r, (v * s_inv[t]) * G);
       }
     }
-    __syncthreads();  // the sums are read before the next tile's
+    group_sync<GR>(group);  // the sums are read before the next tile's
   }
   if (!ok && lane == 0)  // the block's memory must outlive the copies in flight
     for (int j = i + 1; j < i + NB; ++j)
-      if ((int)(blockIdx.x + j * gridDim.x) < tiles) mbar_drain(&bar[j % NB], (j / NB) & 1);
+      if (first + j * step < tiles) mbar_drain(&bar[j % NB], (j / NB) & 1);
 }
 
 // ===========================================================================
@@ -2972,10 +3001,20 @@ static flint_moe_status gemv_any(const void* packed, int32_t N, int32_t K, int32
   (glu     ? launch_gemv<KERNEL<FMT, NT, GEMV_GLU>>(grid, block, smem, 0, stream, a)     \
    : add32 ? launch_gemv<KERNEL<FMT, NT, GEMV_ADD>>(grid, block, smem, 0, stream, a)     \
            : launch_gemv<KERNEL<FMT, NT, GEMV_PLAIN>>(grid, block, smem, 0, stream, a))
+#define FLINT_GEMV2_AS(FMT, NT)                                                                  \
+  (glu     ? launch_gemv<k_gemv_rows<FMT, NT, GEMV_GLU, 2>>(grid, block, smem, 0, stream, a)     \
+   : add32 ? launch_gemv<k_gemv_rows<FMT, NT, GEMV_ADD, 2>>(grid, block, smem, 0, stream, a)     \
+           : launch_gemv<k_gemv_rows<FMT, NT, GEMV_PLAIN, 2>>(grid, block, smem, 0, stream, a))
 #define FLINT_GEMV(KERNEL, NT) (nv ? FLINT_GEMV_AS(KERNEL, FLINT_MOE_NVFP4, NT) : FLINT_GEMV_AS(KERNEL, FLINT_MOE_BF16, NT))
-  const size_t rows_smem = gemv_rows_smem(K, B, fmt, nw, ntmax, &o1, &o2, &o3, &o4);
+  const size_t rows_smem = gemv_rows_smem(K, B, fmt, nw, ntmax, 1, &o1, &o2, &o3, &o4);
+  const size_t two_smem = gemv_rows_smem(K, B, fmt, nw, ntmax, 2, &o1, &o2, &o3, &o4);
   // blocks that run at once, sixteen warps an SM (widths of no multiple of 512 have four warps a block)
-  const int at_once = sm_count() * std::max<int>(1, std::min<int>(16 / nw, (int)(SMEM_LIMIT / (rows_smem + 1024))));
+  const int per_sm = std::max<int>(1, std::min<int>(16 / nw, (int)(SMEM_LIMIT / (rows_smem + 1024)))), at_once = sm_count() * per_sm;
+  if (nv && nw == 8 && per_sm == 1 && ntmax >= 3 && N / 16 > at_once && two_smem <= SMEM_LIMIT) {
+    const size_t smem = two_smem;
+    const dim3 grid(at_once), block(512);
+    return (ntmax == 3 ? FLINT_GEMV2_AS(FLINT_MOE_NVFP4, 3) : FLINT_GEMV2_AS(FLINT_MOE_NVFP4, 4)) == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
+  }
   if (N / 16 > at_once && rows_smem <= SMEM_LIMIT) {
     // more tiles than blocks that run at once: blocks that stage the rows once for several tiles
     const size_t smem = rows_smem;
@@ -2998,6 +3037,7 @@ static flint_moe_status gemv_any(const void* packed, int32_t N, int32_t K, int32
   }
 #undef FLINT_GEMV
 #undef FLINT_GEMV_AS
+#undef FLINT_GEMV2_AS
   return e == cudaSuccess ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
 }
 

@@ -278,11 +278,15 @@ extern "C" flint_moe_status flint_ffn_backward(const flint_ffn* f, const uint16_
   first.a[0] = mdy, first.b[0] = mdown, first.io[0] = og, first.io[1] = ou, first.io[2] = oh;
   if (!map_out(&first.io[3], g, I, T, I) || !map_out(&first.io[4], u, I, T, I)) return FLINT_MOE_ECUDA;
   if (!run<DGlu>({{{T, I, blocks_of(H), 1, 0, 0, 0, 1, 0, 1}}, 1, 0, status, 1}, m1, {g, u}, stream)) return FLINT_MOE_ECUDA;
-  // dx and the weights' gradients need nothing of one another: one launch, laid out as if all of them were asked for, so
-  // that each has the same bits with and without the others.
+  // dx and the weights' gradients need nothing of one another: one launch, or two where dx has few tiles and many k-blocks
+  // (200 tokens of 2048 x 8192: 150 us a call in one). Laid out as if all of them were asked for, so that each has the same
+  // bits with and without the others.
   const int kb = blocks_of(T);
   const Problem px = {T, H, blocks_of(I), 2, 2, 2, 0, 1, 0, 1}, pw = {I, H, kb, 1, 0, 0, 1, 1, 0, 1}, pd = {H, I, kb, 1, 0, 0, 1, 1, 0, 1};
-  const Choice choice = choose<Store>({{px, pw, pw, pd}, 4, 0, nullptr, 0});
+  int64_t cycles[3];
+  const Choice together = choose<Store>({{px, pw, pw, pd}, 4, 0, nullptr, 0}, &cycles[0]);
+  const Choice alone = choose<Store>({{px}, 1, 0, nullptr, 0}, &cycles[1]), rest = choose<Store>({{pw, pw, pd}, 3, 0, nullptr, 0}, &cycles[2]);
+  const bool one = cycles[0] <= cycles[1] + cycles[2];
   AllMaps<Store> m2;
   gemm::Args a = {{}, 0, 0, status, 0};
   bool ok = true;
@@ -294,11 +298,15 @@ extern "C" flint_moe_status flint_ffn_backward(const flint_ffn* f, const uint16_
     a.p[a.n++] = p;
   };
   if (dx) add(px, mg, mu, mgate, mup, dx, lddx);
+  if (dx && !one) {
+    if (!ok || !run<Store>(a, m2, {}, stream, alone)) return FLINT_MOE_ECUDA;
+    a.n = 0;
+  }
   if (dgate) {
     add(pw, mg, mg, mx, mx, dgate, H);
     add(pw, mu, mu, mx, mx, dup, H);
     add(pd, mdy, mdy, mh, mh, ddown, I);
   }
-  if (!ok || !run<Store>(a, m2, {}, stream, choice)) return FLINT_MOE_ECUDA;
+  if (!ok || (a.n > 0 && !run<Store>(a, m2, {}, stream, one ? together : rest))) return FLINT_MOE_ECUDA;
   return FLINT_MOE_OK;
 }

@@ -21,11 +21,12 @@ constexpr int SLOTS = 4;             // of each epilogue warp in k_gemm
 
 // k_gemm: one 128 x 128 tile a CTA, two CTAs on an SM, so that the one's epilogue runs beside the other's products; or
 // 128 x 64.
+// STAGES beside another CTA, up to DEEP on an SM of its own.
 struct One {
-  static constexpr int TM = 128, TN = 128, CTAS = 1, STAGES = 3, GROUPS = 1, BBOXES = 2;
+  static constexpr int TM = 128, TN = 128, CTAS = 1, STAGES = 3, DEEP = 6, GROUPS = 1, BBOXES = 2;
 };
 struct Half {
-  static constexpr int TM = 128, TN = 64, CTAS = 1, STAGES = 4, GROUPS = 1, BBOXES = 1;
+  static constexpr int TM = 128, TN = 64, CTAS = 1, STAGES = 4, DEEP = 8, GROUPS = 1, BBOXES = 1;
 };
 // k_gemm_pair: 256 x 256 tiles by pairs of CTAs (cta_group::2), each with half of A's rows and half of B's, 128 x 256 sums
 // a CTA; persistent, with two accumulators, so that a tile's epilogue runs beside the next one's products. Epilogues that
@@ -44,14 +45,15 @@ constexpr int STAGE = (2 + C::BBOXES) * BOX;
 template <typename C>
 constexpr int THREADS = 64 + 128 * C::GROUPS;  // warp 0 loads, warp 1 issues the MMAs, the others the epilogue
 template <typename C>
-constexpr size_t SMEM = 1024 + (size_t)C::STAGES * STAGE<C>;
+constexpr size_t SMEM = 1024 + (size_t)C::DEEP * STAGE<C>;
 template <typename C>
-constexpr size_t PAIR_SMEM = SMEM<C> + (size_t)C::GROUPS * 4 * (C::OUT_SLOTS + C::IN_SLOTS) * SLOT;
+constexpr size_t PAIR_SMEM = 1024 + (size_t)C::STAGES * STAGE<C> + (size_t)C::GROUPS * 4 * (C::OUT_SLOTS + C::IN_SLOTS) * SLOT;
 static_assert(PAIR_SMEM<Pairs<0>> <= 227 * 1024 - 512 && PAIR_SMEM<Pairs<2>> <= 227 * 1024 - 512, "shared memory of a CTA");
 static_assert(4 * SLOTS * SLOT + One::TM * One::TN * 4 <= One::STAGES * STAGE<One> && Half::STAGES * STAGE<Half> == One::STAGES * STAGE<One>,
               "k_gemm's epilogue writes where its operands were");
 
-constexpr int MOST = 4;  // products of one launch
+constexpr int MOST = 4;        // products of one launch
+constexpr int DEEP_FROM = 40;  // k-blocks of a CTA from which it takes all of its SM's memory
 
 struct Problem {
   int M, N;         // output rows and columns (of one matrix of the batch)
@@ -242,26 +244,24 @@ __device__ __forceinline__ uint32_t idesc_of(const Args& a, const Problem& p, in
 }
 
 // One tile a CTA, or a cluster of S = 2, 4 or 8 CTAs a tile, each with a run of the k-blocks: their sums meet in
-// distributed shared memory, 32 x 32 blocks of the tile shared out among the CTAs' epilogue warps, and are added in CTA
-// order.
-template <typename C, typename E>
-__global__ void __launch_bounds__(THREADS<C>, 2)
-    k_gemm(const Args a, const __grid_constant__ AllMaps<E> all, const typename E::Args e) {
+// distributed shared memory, 32 x 32 blocks of the tile shared out among the CTAs' epilogue warps, which add them in CTA
+// order from their own CTA on (so that no CTA's memory is asked by all at once).
+template <typename C, typename E, int ST>
+__global__ void __launch_bounds__(THREADS<C>, 2) k_gemm(const Args a, const __grid_constant__ AllMaps<E> all, const typename E::Args e) {
   extern __shared__ uint8_t dsmem[];
-  constexpr int ST = C::STAGES;
   __shared__ uint64_t full[ST], empty[ST], acc_full;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
   volatile int* abort = &abort_flag;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+  if (threadIdx.x < ST) {
+    mbar_init(&full[threadIdx.x], 1);
+    mbar_init(&empty[threadIdx.x], 1);
+    if (threadIdx.x == 0) {
+      mbar_init(&acc_full, 1);
+      abort_flag = 0;
     }
-    mbar_init(&acc_full, 1);
-    abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&tmem_base, C::TN);
@@ -291,29 +291,31 @@ __global__ void __launch_bounds__(THREADS<C>, 2)
       const int per = p.kb;
       int i = 0, seg = b0 / per, kb = b0 - seg * per;
       const CUtensorMap *am = &maps.a[(p.a_of >> seg) & 1], *bm = &maps.b[(p.b_of >> seg) & 1];
+      int s = 0;
+      uint32_t phase = 0;
       for (; i < b1 - b0; ++i, ++kb) {
-        const int s = i % ST;
         if (kb == per) {
           kb = 0;
           ++seg;
           am = &maps.a[(p.a_of >> seg) & 1], bm = &maps.b[(p.b_of >> seg) & 1];
         }
-        if (i >= ST && !wait_ab(&empty[s], ((i / ST) - 1) & 1, abort, a.status)) break;
+        if (i >= ST && !wait_ab(&empty[s], phase ^ 1, abort, a.status)) break;
         const uint32_t sm = base + s * STAGE<C>;
         mbar_arrive_expect_tx(&full[s], STAGE<C>);
         load_stage<C>(a_mn, b_mn, kb * BK, m0, n, [&](int off, bool is_a, int h, int x, int y) {
           tma_load_3d(sm + off, is_a ? am : E::PAIR ? &maps.b[h] : bm, x, y, w.z, &full[s]);
         });
+        if (++s == ST) s = 0, phase ^= 1;
       }
       for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&full[r % ST], (r / ST) & 1);
     }
   } else if (warp == 1) {
     const uint32_t idesc = idesc_of(a, p, C::TM, C::TN);
     const Operand oa = operand(p.a_mn), ob = operand(p.b_mn);
-    int i = 0;
+    int i = 0, s = 0;
+    uint32_t phase = 0;
     for (; i < b1 - b0; ++i) {
-      const int s = i % ST;
-      const bool ok = wait_ab(&full[s], (i / ST) & 1, abort, a.status);
+      const bool ok = wait_ab(&full[s], phase, abort, a.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       if (elect_one()) {
@@ -324,6 +326,7 @@ __global__ void __launch_bounds__(THREADS<C>, 2)
         if (i + 1 == b1 - b0) tc_commit(&acc_full);
       }
       __syncwarp();
+      if (++s == ST) s = 0, phase ^= 1;
     }
     for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&empty[r % ST], (r / ST) & 1);
   }
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(THREADS<C>, 2)
           for (int j = 0; j < 32; ++j) acc[j] = 0.f;
 #pragma unroll 1
           for (int r = 0; r < S; ++r) {
-            const uint32_t at = dsmem_addr(part + (uint32_t)((col / 4 * 128 + (u & 3) * 32 + lane) * 16), r);
+            const uint32_t at = dsmem_addr(part + (uint32_t)((col / 4 * 128 + (u & 3) * 32 + lane) * 16), (rank + r) & (S - 1));
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float4 f = ld_dsmem_f4(at + j * 2048);
@@ -686,9 +689,9 @@ bool prepare(size_t smem) {
 }
 
 // A launch that may start while the kernel before it drains (each kernel waits for it itself), in clusters of `cx`.
-template <auto KERNEL, typename... P>
+template <auto KERNEL, size_t MOST_SMEM, typename... P>
 bool launch(dim3 grid, int block, size_t smem, int cx, cudaStream_t stream, const P&... args) {
-  if (!prepare<KERNEL>(smem)) return false;
+  if (!prepare<KERNEL>(MOST_SMEM)) return false;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
@@ -706,10 +709,14 @@ bool launch(dim3 grid, int block, size_t smem, int cx, cudaStream_t stream, cons
   return cudaLaunchKernelEx(&cfg, KERNEL, args...) == cudaSuccess;
 }
 
+// SMs of the current device, asked for once.
 inline int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2)
-    n = 152;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return 152;
+  if ((n = known[dev].load()) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2) return 152;
+  known[dev].store(n);
   return n;
 }
 
@@ -723,50 +730,70 @@ inline Args whole(Args a) {
   for (int i = 0; i < a.n; ++i) a.p[i].sym = 0;
   return a;
 }
-// The one with the fewest cycles by this estimate, of rounds of CTAs, a k-block's cycles and a tile's beginning and end
-// (from the times of products of 128 to 8192 rows): pairs take 600 cycles a k-block; a CTA alone on its SM 450 (300 with
-// 64 columns), since two or three stages in flight do not cover memory's latency, and two on an SM 850 (500) together; a
-// tile's beginning and end take 9000, 6500 (5000), sums over a cluster 3000 more.
+// The one with the fewest cycles by this estimate (from the times of products of 32 to 8192 rows): a k-block takes pairs
+// 600 cycles, a CTA alone on its SM 450 (300 with 64 columns; memory's latency over the stages in flight: with many stages
+// 320 and 220), two on an SM 850 (500) together; a tile at least its epilogue's 4000; beginning and end take 9000, 6500
+// (5000), half of them again for a tile that others follow, sums over a cluster 3000 more. A launch takes as long as its
+// longest tile, or as many rounds of the mean one as it has.
 template <typename E>
-Choice choose(const Args& a) {
+Choice choose(const Args& a, int64_t* cycles = nullptr) {
   const int64_t sms = sm_count() & ~1;
-  int64_t blocks = 0, least = 1 << 30;
-  for (int i = 0; i < a.n; ++i) {
-    blocks = std::max<int64_t>(blocks, a.p[i].blocks());
-    least = std::min<int64_t>(least, a.p[i].blocks());
-  }
-  const int64_t pairs = Walk<Two, E::PAIR>::tiles(a);
   Choice best = {0, 1};
-  int64_t cost = (2 * pairs + sms - 1) / sms * blocks * 600 + 9000;
-  auto consider = [&](int kind, int64_t tiles, int alone, int two, int ends) {
-    for (int S = 1; S <= 8; S *= 2) {
-      if (S > 1 && (tiles * S > sms || 4 * S > least)) break;
-      const int64_t per = (blocks + S - 1) / S, n = tiles * S;
-      const int64_t c = (n <= sms ? per * alone : (n + 2 * sms - 1) / (2 * sms) * (per * two + ends / 2)) + ends + (S > 1 ? 3000 : 0);
-      if (c < cost) cost = c, best = {kind, S};
+  int64_t cost = INT64_MAX;
+  auto deep = [&](int per, int64_t slots) { return slots == sms && per >= DEEP_FROM; };
+  auto consider = [&](int kind, int S, int64_t slots, const Args& p, auto tiles, int block, int ends) {
+    int64_t work = 0, longest = 0, n = 0;
+    for (int i = 0; i < p.n; ++i) {
+      const int per = (p.p[i].blocks() + S - 1) / S;
+      const int64_t t = std::max<int64_t>((int64_t)per * (deep(per, slots) ? block * 7 / 10 : block), 4000) + (slots > sms ? ends / 2 : 0);
+      const int64_t m = (int64_t)tiles(p.p[i]) * p.p[i].batch * S;
+      work += m * t;
+      n += m;
+      longest = std::max(longest, t);
+    }
+    const int64_t rounds = (n + slots - 1) / slots;
+    const int64_t c = std::max(longest, work / n * rounds) + ends + (S > 1 ? 3000 : 0);
+    if (c < cost) cost = c, best = {kind, S};
+  };
+  consider(0, 1, sms / 2, a, Walk<Two, E::PAIR>::each, 600, 9000);
+  int64_t least = 1 << 30;
+  for (int i = 0; i < a.n; ++i) least = std::min<int64_t>(least, a.p[i].blocks());
+  auto narrow = [&](int kind, const Args& p, int64_t n, auto tiles, int alone, int two, int ends) {
+    for (int S = 1; S <= 8 && n <= 65535; S *= 2) {  // (a grid's second dimension)
+      if (S > 1 && (n * S > sms || 4 * S > least)) break;
+      consider(kind, S, n * S <= sms ? sms : 2 * sms, p, tiles, n * S <= sms ? alone : two, ends);
     }
   };
-  const int64_t ones = Walk<One, E::PAIR>::tiles(a);
-  if (ones <= 65535) consider(1, ones, 450, 850, 6500);  // (a grid's second dimension)
-  if constexpr (!E::PAIR) {
-    const int64_t halves = Walk<Half, false>::tiles(whole(a));
-    if (halves <= 65535) consider(2, halves, 300, 500, 5000);
-  }
+  narrow(1, a, Walk<One, E::PAIR>::tiles(a), Walk<One, E::PAIR>::each, 450, 850, 6500);
+  if constexpr (!E::PAIR) narrow(2, whole(a), Walk<Half, false>::tiles(whole(a)), Walk<Half, false>::each, 300, 500, 5000);
+  if (cycles) *cycles = cost;
   return best;
+}
+
+// k_gemm on S CTAs a tile. Its CTAs take an SM's whole memory for their stages where they have one each and many k-blocks
+// (the second product of 1024 tokens of 2048 x 8192, 128 each: 102 -> 90 us a call); with fewer, room for the next launch's
+// CTAs to begin in counts more (77 tokens, 16 and 32: 35 us, and 42 with all the memory).
+template <typename C, typename E>
+bool run_tiles(const Args& a, const AllMaps<E>& m, const typename E::Args& e, int S, cudaStream_t stream) {
+  const int64_t tiles = Walk<C, E::PAIR>::tiles(a);
+  int most = 0;
+  for (int i = 0; i < a.n; ++i) most = std::max(most, (a.p[i].blocks() + S - 1) / S);
+  const dim3 grid(S, (unsigned)tiles);
+  if (tiles * S <= sm_count() && most >= DEEP_FROM)
+    return launch<k_gemm<C, E, C::DEEP>, SMEM<C>>(grid, THREADS<C>, SMEM<C>, S, stream, a, m, e);
+  constexpr size_t smem = 1024 + (size_t)C::STAGES * STAGE<C>;
+  return launch<k_gemm<C, E, C::STAGES>, smem>(grid, THREADS<C>, smem, S, stream, a, m, e);
 }
 
 template <typename E>
 bool run(const Args& a, const AllMaps<E>& m, const typename E::Args& e, cudaStream_t stream, const Choice& c) {
   if (c.kind == 0) {
     const int64_t pairs = std::min<int64_t>(Walk<Two, E::PAIR>::tiles(a), sm_count() / 2);
-    return launch<k_gemm_pair<E>>(dim3(2 * (unsigned)pairs), THREADS<Two>, PAIR_SMEM<Pairs<E::INS>>, 0, stream, a, m, e);
+    return launch<k_gemm_pair<E>, PAIR_SMEM<Pairs<E::INS>>>(dim3(2 * (unsigned)pairs), THREADS<Two>, PAIR_SMEM<Pairs<E::INS>>, 0, stream, a, m, e);
   }
   if constexpr (!E::PAIR)
-    if (c.kind == 2) {
-      const Args all = whole(a);
-      return launch<k_gemm<Half, E>>(dim3(c.S, (unsigned)Walk<Half, false>::tiles(all)), THREADS<Half>, SMEM<Half>, c.S, stream, all, m, e);
-    }
-  return launch<k_gemm<One, E>>(dim3(c.S, (unsigned)Walk<One, E::PAIR>::tiles(a)), THREADS<One>, SMEM<One>, c.S, stream, a, m, e);
+    if (c.kind == 2) return run_tiles<Half, E>(whole(a), m, e, c.S, stream);
+  return run_tiles<One, E>(a, m, e, c.S, stream);
 }
 template <typename E>
 bool run(const Args& a, const AllMaps<E>& m, const typename E::Args& e, cudaStream_t stream) {

@@ -707,8 +707,7 @@ int few_ctas(int m, int k, int* kc) {
 
 template <int UNITS>
 bool run_few(const FewArgs& a, int C, int n, cudaStream_t stream) {
-  return prepare<k_ortho_few<UNITS>>(226 * 1024) &&
-         launch<k_ortho_few<UNITS>>(dim3(C, n), FEW_THREADS, few_plan(a.m, a.kc).total, C, stream, a);
+  return launch<k_ortho_few<UNITS>, 226 * 1024>(dim3(C, n), FEW_THREADS, few_plan(a.m, a.kc).total, C, stream, a);
 }
 
 bool overlaps(const void* p, size_t np, const void* q, size_t nq) {
@@ -773,7 +772,7 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
   const Start st = {in, fmt == FLINT_ORTHOGONALIZE_BF16, n, rows, cols, w.pitch, w.parts, eps,
                     reinterpret_cast<double*>(wsp + w.part), at(w.x[0][0]), at(w.x[0][1]), status};
   const dim3 grid((unsigned)w.parts, (unsigned)n);
-  if (!launch<k_ortho_norm>(grid, START_THREADS, 0, 0, stream, st) || !launch<k_ortho_split>(grid, START_THREADS, 0, 0, stream, st))
+  if (!launch<k_ortho_norm, 0>(grid, START_THREADS, 0, 0, stream, st) || !launch<k_ortho_split, 0>(grid, START_THREADS, 0, 0, stream, st))
     return FLINT_MOE_ECUDA;
   const int kx = ((tall ? rows : cols) + BK - 1) / BK, km = (m + BK - 1) / BK;
   AllMaps<Gram> mg;
