@@ -228,7 +228,7 @@ extern "C" flint_moe_status flint_ffn_forward(const flint_ffn* f, const uint16_t
   if (ok && g) ok = map_out(&glu.io[1], g, I, T, I) && map_out(&glu.io[2], u, I, T, I);
   if (!ok) return FLINT_MOE_ECUDA;
   const gemm::Args a1 = {{{T, I, blocks_of(H), 1, 0, 0, 0, 0, 0, 1}}, 1, 0, status, 1};
-  const gemm::Args a2 = {{{T, H, blocks_of(I), 1, 0, 0, 0, 0, 0, 1}}, 1, 0, status, 0};
+  const gemm::Args a2 = {{{T, H, blocks_of(I), 1, 0, 0, 0, 0, 0, 1, 2}}, 1, 0, status, 0};
   ok = g ? run<Glu<true>>(a1, m1, {}, stream) : run<Glu<false>>(a1, m1, {}, stream);
   ok = ok && run<Store>(a2, m2, {}, stream);
   return ok ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
@@ -282,7 +282,7 @@ extern "C" flint_moe_status flint_ffn_backward(const flint_ffn* f, const uint16_
   // (200 tokens of 2048 x 8192: 150 us a call in one). Laid out as if all of them were asked for, so that each has the same
   // bits with and without the others.
   const int kb = blocks_of(T);
-  const Problem px = {T, H, blocks_of(I), 2, 2, 2, 0, 1, 0, 1}, pw = {I, H, kb, 1, 0, 0, 1, 1, 0, 1}, pd = {H, I, kb, 1, 0, 0, 1, 1, 0, 1};
+  const Problem px = {T, H, blocks_of(I), 2, 2, 2, 0, 1, 0, 1, 2}, pw = {I, H, kb, 1, 0, 0, 1, 1, 0, 1, 2}, pd = {H, I, kb, 1, 0, 0, 1, 1, 0, 1, 1};
   int64_t cycles[3];
   const Choice together = choose<Store>({{px, pw, pw, pd}, 4, 0, nullptr, 0}, &cycles[0]);
   const Choice alone = choose<Store>({{px}, 1, 0, nullptr, 0}, &cycles[1]), rest = choose<Store>({{pw, pw, pd}, 3, 0, nullptr, 0}, &cycles[2]);

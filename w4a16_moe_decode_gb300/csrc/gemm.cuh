@@ -63,6 +63,9 @@ struct Problem {
   int a_mn, b_mn;   // operands stored MN-major
   int sym;          // D is its own transpose: the tiles above the diagonal are computed, and written twice
   int batch;
+  // Operands (1: A, 2: B) that k_gemm asks for without waiting for the launch before: what neither that launch writes nor
+  // anything before it still does, since that launch lets this one begin only after its own wait.
+  int early;
   __host__ __device__ int blocks() const { return kb * segs; }
 };
 struct Args {
@@ -279,33 +282,59 @@ __global__ void __launch_bounds__(THREADS<C>, 2) k_gemm(const Args a, const __gr
     prefetch_map(&maps.b[0]);
     prefetch_map(&maps.io[0]);
   }
-  pdl_wait();
-  pdl_trigger();
-  if (a.clear && threadIdx.x == 0 && blockIdx.x + blockIdx.y == 0) *a.status = 0;
   const int blocks = p.blocks(), b0 = blocks * rank / S, b1 = blocks * (rank + 1) / S;
   const int m0 = w.m * C::TM, n0 = w.n * w.COLS;
+  if (warp != 0) {
+    pdl_wait();
+    pdl_trigger();
+    if (a.clear && warp == 1 && lane == 0 && blockIdx.x + blockIdx.y == 0) *a.status = 0;
+  }
   if (warp == 0) {
     if (lane == 0) {
       const int n[2] = {n0, E::PAIR ? n0 : n0 + 64};
       const bool a_mn = p.a_mn, b_mn = p.b_mn;
+      // Boxes that lie outside the matrix are not asked for: the rows and columns that come of them are not read.
+      const bool a_both = m0 + 64 < p.M, b_both = C::BBOXES == 2 && (E::PAIR || n[1] < p.N);
+      const uint32_t bytes = (2 + (a_both ? 1 : 0) + (b_both ? 1 : 0)) * BOX;
       const int per = p.kb;
-      int i = 0, seg = b0 / per, kb = b0 - seg * per;
-      const CUtensorMap *am = &maps.a[(p.a_of >> seg) & 1], *bm = &maps.b[(p.b_of >> seg) & 1];
-      int s = 0;
+      // The stages that need not wait for room: at first the operands that are there already, then the others.
+      const int n_blocks = b1 - b0, stages = min(ST, n_blocks);
+      int i = 0, s = 0, seg = 0, kb = 0;
       uint32_t phase = 0;
-      for (; i < b1 - b0; ++i, ++kb) {
-        if (kb == per) {
+      const CUtensorMap *am = nullptr, *bm = nullptr;
+      auto begin = [&] {
+        i = 0, s = 0;
+        seg = b0 / per, kb = b0 - seg * per;
+        am = &maps.a[(p.a_of >> seg) & 1], bm = &maps.b[(p.b_of >> seg) & 1];
+      };
+      auto next = [&] {
+        ++i;
+        if (++kb == per) {
           kb = 0;
           ++seg;
           am = &maps.a[(p.a_of >> seg) & 1], bm = &maps.b[(p.b_of >> seg) & 1];
         }
-        if (i >= ST && !wait_ab(&empty[s], phase ^ 1, abort, a.status)) break;
-        const uint32_t sm = base + s * STAGE<C>;
-        mbar_arrive_expect_tx(&full[s], STAGE<C>);
-        load_stage<C>(a_mn, b_mn, kb * BK, m0, n, [&](int off, bool is_a, int h, int x, int y) {
-          tma_load_3d(sm + off, is_a ? am : E::PAIR ? &maps.b[h] : bm, x, y, w.z, &full[s]);
-        });
         if (++s == ST) s = 0, phase ^= 1;
+      };
+      auto load = [&](bool with_a, bool with_b) {
+        const uint32_t sm = base + s * STAGE<C>;
+        load_stage<C>(a_mn, b_mn, kb * BK, m0, n, [&](int off, bool is_a, int h, int x, int y) {
+          if (is_a ? with_a && (h == 0 || a_both) : with_b && (h == 0 || b_both))
+            tma_load_3d(sm + off, is_a ? am : E::PAIR ? &maps.b[h] : bm, x, y, w.z, &full[s]);
+        });
+      };
+      for (begin(); i < stages; next()) {
+        mbar_arrive_expect_tx(&full[s], bytes);
+        load(p.early & 1, p.early & 2);
+      }
+      pdl_wait();
+      pdl_trigger();
+      phase = 0;
+      for (begin(); i < stages; next()) load(!(p.early & 1), !(p.early & 2));
+      for (; i < n_blocks; next()) {
+        if (!wait_ab(&empty[s], phase ^ 1, abort, a.status)) break;
+        mbar_arrive_expect_tx(&full[s], bytes);
+        load(true, true);
       }
       for (int r = (i > ST ? i - ST : 0); r < i; ++r) mbar_drain(&full[r % ST], (r / ST) & 1);
     }
@@ -415,7 +444,7 @@ __global__ void __launch_bounds__(THREADS<C>, 2) k_gemm(const Args a, const __gr
     __syncwarp();
     cluster_sync();  // the other CTAs have read this one's sums
   }
-  if (warp >= 2 && lane == 0) bulk_wait_all();
+  if (warp >= 2 && lane == 0) bulk_wait_read<0>();  // (the memory that the stores read; they are done when the grid is)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -645,7 +674,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
     }
     if (E::INS && lane == 0)  // after a failed wait: copies still on their way
       for (; used < fetched; ++used) mbar_drain(&in_full[warp - 2][used & 1], (used >> 1) & 1);
-    if (lane == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_read<0>();  // (the memory that the stores read; they are done when the grid is)
   }
   tc_fence_before();
   __syncthreads();
@@ -664,7 +693,8 @@ inline bool map_matrix(CUtensorMap* m, const void* p, int64_t cols, int64_t rows
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
   const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)apart * 2};
   const cuuint32_t side = out ? 32 : 64, box[3] = {side, side, 1};
-  return encode_bf16(m, p, 3, dims, strides, box, out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+  return encode_bf16(m, p, 3, dims, strides, box, out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                     out ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 inline bool map_in(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld) {
   return map_matrix(m, p, cols, rows, ld, 1, ld, false);  // one matrix: its distance to the next is never used

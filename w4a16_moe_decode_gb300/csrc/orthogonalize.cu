@@ -798,7 +798,7 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
     ok = run<Gram>({{{m, m, kx, 1, 0, 0, tall, tall, 1, n}}, 1, 1, status, 0}, mg, {}, stream) &&
          run<Poly>({{{m, m, km, 1, 0, 0, 0, 0, 1, n}}, 1, 1, status, 0}, mp, {at(w.s), w.mpitch, cf[1], cf[2], few}, stream);
     const int p_of = 2, x_of = 4;  // hi hi, then P_lo, then X_lo
-    const gemm::Args upd = {{{rows, cols, km, few ? 3 : 1, tall ? x_of : p_of, tall ? p_of : x_of, 0, !tall, 0, n}}, 1, 1, status, 0};
+    const gemm::Args upd = {{{rows, cols, km, few ? 3 : 1, tall ? x_of : p_of, tall ? p_of : x_of, 0, !tall, 0, n, tall ? 1 : 2}}, 1, 1, status, 0};
     const uint16_t *hi = at(w.x[i & 1][0]), *lo = at(w.x[i & 1][1]);
     ok = ok && (last ? run<Update<true>>(upd, mu, {hi, lo, w.pitch, cf[0], scale / X_SCALE, out}, stream)
                      : run<Update<false>>(upd, mu, {hi, lo, w.pitch, cf[0], 1.0f, nullptr}, stream));
