@@ -17,7 +17,7 @@ from w4a16_moe_decode_gb300.build import build
 
 from _common import bits_to_f64
 from _dense import FN
-from _finetune import HALF_BF16, SLACK, SUM, TINY, check  # noqa: F401
+from _finetune import HALF_BF16, SLACK, SUM, TINY, check
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -90,6 +90,12 @@ def test_several_tiles_a_block(I, K, B, fmt):
     run(I, K, B, 80 + B, fmt, rows=[0, B - 1])
 
 
+@pytest.mark.parametrize("I,K,B,norm", [(1304, 2048, 17, False), (1304, 2048, 32, True), (2472, 2048, 25, False), (1600, 1536, 32, False)])
+def test_two_groups_a_block(I, K, B, norm):
+    """Rows that fill an SM: two groups of warps, each with its own tiles."""
+    run(I, K, B, 110 + B, fb.NVFP4, norm, rows=[0, B // 2, B - 1])
+
+
 @pytest.mark.parametrize("fmt", [fb.NVFP4, fb.BF16])
 @pytest.mark.parametrize("I,K,B,norm", [(16, 4096, 1, False), (40, 8192, 2, True), (24, 6144, 9, False), (32, 4096, 32, True),
                                         (1400, 4096, 1, False), (1304, 8192, 3, True), (1208, 4096, 16, False), (1000, 4096, 27, False)])
@@ -103,7 +109,7 @@ def test_norm_prologue(I, K, B, fmt):
     run(I, K, B, 100 + B, fmt, norm=True)
 
 
-@pytest.mark.parametrize("I,K", [(64, 512), (2600, 256), (48, 4096)])
+@pytest.mark.parametrize("I,K", [(64, 512), (2600, 256), (48, 4096), (1304, 2048)])
 def test_a_row_stands_alone(I, K):
     """A row's bits do not depend on the other rows of the call."""
     packed, x, h, _ = run(I, K, 32, 7, fb.NVFP4, rows=[0])
@@ -123,3 +129,19 @@ def test_pack_reports_nan_scales():
         st = torch.zeros(1, dtype=torch.int32, device=DEV)
         fb.flint_gemv_glu_pack(src[0], src[1], 16, 256, fb.NVFP4, dst, st)
         assert int(st.item()) == want
+
+
+def test_gemv_of_two_groups_has_the_rows_of_smaller_calls():
+    """flint_gemv with 17 to 32 rows of 2048, more tiles than blocks: the bits of calls of fewer rows."""
+    N, K = 2608, 2048
+    packed, _ = layers.synth_dense(N, K, 5, 0, fb.NVFP4, DEV)
+    x = layers.synth_x(32, K, 5, 0, DEV)
+    y = torch.empty(32, N, dtype=torch.int16, device=DEV)
+    for B in (17, 24, 25, 32):
+        y.fill_(0x7FC0)
+        fb.flint_gemv(packed, N, K, fb.NVFP4, x, B, y)
+        for r in (0, 8, B - 1):
+            one = torch.empty(1, N, dtype=torch.int16, device=DEV)
+            fb.flint_gemv(packed, N, K, fb.NVFP4, x[r : r + 1].contiguous(), 1, one)
+            assert torch.equal(one[0], y[r]), (B, r)
+        assert bool((y[B:] == 0x7FC0).all())
