@@ -166,13 +166,26 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_split(const Start a) {
       *reinterpret_cast<uint4*>(a.lo + out + i) = lo;
     }
   } else {
-    for (size_t i = (size_t)blockIdx.x * START_THREADS + threadIdx.x; i < all; i += step) {
-      const size_t r = i / a.cols, at = out + r * a.pitch + (i - r * a.cols);
-      const float v = (load1(a, first + i) * s0) * s1;
-      const __half h = __float2half_rn(v);
-      a.hi[at] = *reinterpret_cast<const uint16_t*>(&h);
-      const __half l = __float2half_rn(v - __half2float(h));
-      a.lo[at] = *reinterpret_cast<const uint16_t*>(&l);
+    // a warp a row, each lane up to eight of its values at a time
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (START_THREADS / 32);
+    for (int r = blockIdx.x * (START_THREADS / 32) + (threadIdx.x >> 5); r < a.rows; r += warps) {
+      const size_t from = first + (size_t)r * a.cols, to = out + (size_t)r * a.pitch;
+      for (int c0 = lane; c0 < a.cols; c0 += 256) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = c0 + 32 * e < a.cols ? load1(a, from + c0 + 32 * e) : 0.f;
+        uint4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (v[e] * s0) * s1;
+        split8(v, hi, lo);
+        const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c0 + 32 * e < a.cols) {
+            a.hi[to + c0 + 32 * e] = (uint16_t)(e & 1 ? h[e >> 1] >> 16 : h[e >> 1]);
+            a.lo[to + c0 + 32 * e] = (uint16_t)(e & 1 ? l[e >> 1] >> 16 : l[e >> 1]);
+          }
+      }
     }
   }
 }
