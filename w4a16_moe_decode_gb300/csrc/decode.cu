@@ -18,7 +18,8 @@
 //                 for k_gateup, then, once h exists, multiplies and accumulates
 //                 w * y per warp, adds the warps in a fixed order and writes
 //                 out = bf16(sum) (plus the residual for the pre-norm block).
-//   k_gemv        dense y = x W^T on the same packed layout.
+//   k_gemv        dense y = x W^T on the same packed layout; its GLU forms (flint_gemv_glu) take gate and up rows in one
+//                 tile, as an expert's, and write h = bf16(silu(g) u).
 //
 // Launch order inside a layer and across layers (same stream):
 //   k_router waits for the previous layer, then lets k_gateup launch;
@@ -1880,7 +1881,8 @@ __device__ __forceinline__ bool group_all(int group, bool ok) {
 }
 
 // GR = 2: two groups of eight warps share a block's rows, each with its own tiles (and one buffer of weights). Rows that
-// leave an SM room for one block only would have eight warps on it otherwise, which take turns waiting.
+// leave an SM room for one block only would have eight warps on it otherwise, which take turns waiting (gemv_glu of 32 x
+// 2048 x 8192: 25.8 -> 21.1 us; 32 x 2048 x 2048 8.9 -> 7.7).
 template <int FMT, int NTMAX, GemvEnd END, int GR = 1>
 __global__ void __launch_bounds__(256 * GR) k_gemv_rows(GemvArgs a) {
   constexpr bool ADD = END == GEMV_ADD;

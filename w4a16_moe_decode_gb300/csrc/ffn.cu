@@ -1,5 +1,17 @@
 // Dense gated feed-forward block on BF16 weights and its gradients (flint_ffn.h), as matrix products of gemm.cuh with
-// what stands between them in their epilogues.
+// what stands between them in their epilogues: g and u are columns of one product, whose epilogue makes h of them; dh's
+// epilogue makes dg, du and h; dx and the weights' gradients are one launch, since none needs another.
+//
+// Roundings: h, dg and du enter the next product as bf16, the type of the weights and tokens they are multiplied with (one
+// MMA takes one type). h is the rounding point of the expert kernels, so that a dense layer and an expert of the same
+// weights agree. Each adds an error of the size of the result's own rounding: the results are within 0.0024 of the exact
+// ones in the norm, where rounding once at the end gives 0.0017. Keeping 16 bits as two bf16 halves, as the adapters do
+// for their narrow h, would take half as many MMAs again in the forward pass and nearly twice as many in the gradients,
+// which the tensor cores bound. All sums are FP32.
+//
+// 8192 tokens of 2048 x 8192, us a call: forward with g and u kept 555 (1480 TFLOP/s; the first product alone 1650, at
+// what the card sustains within its power limit), gradients 1127 (1460; the last four products alone 1750). 77 tokens:
+// 33.6, bound by the weights' stream at 3.4 TB/s and two launches' latency.
 #include "flint_ffn.h"
 #include "gemm.cuh"
 

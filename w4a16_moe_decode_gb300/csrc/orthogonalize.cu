@@ -1,6 +1,16 @@
-// Orthogonalised updates by Newton-Schulz steps (flint_orthogonalize.h), as matrix products of gemm.cuh.
+// Orthogonalised updates by Newton-Schulz steps (flint_orthogonalize.h), as matrix products of gemm.cuh, or in one kernel
+// where a matrix fits a cluster's shared memory.
 //
-// Scaled values: X is kept times 2^10 as hi + lo (f16), S times 2^10 and P times 2^8 (f16).
+// A step's X <- a X + P X with P = b S + c S S, S = X X^T. What is added to X is amplified by the later steps where X is
+// weak, by up to a^steps (485 after five steps of 3.4445): X is kept to 22 bits or more (hi + lo f16, or FP32). An error
+// relative to X from the left, (1 + e) X, only turns the result by e: so the products take f16 values, S from X's hi, P
+// from one rounding of each of its parts, and the tensor cores run at one product's rate instead of three. S, P and the
+// update of wide X read their transposes as they lie (S and P are their own); S and P are computed above the diagonal.
+// Scaled values: X is kept times 2^10, S times 2^10 and P times 2^8, so that f16 holds them to 2^-34 and below.
+//
+// Two updates of 8192 x 2048, us: 980 (1130 TFLOP/s of the products that cannot be left out), bound by the tensor cores
+// in X P and, in the two products of S, by one round of 72 tiles; norm and conversion take 60 of it from memory. 256 x
+// 2048: 85, seventeen launches of 5 us that wait for one another.
 #include <cmath>
 #include <type_traits>
 
@@ -322,7 +332,10 @@ struct Update {
 //   X <- a X + X P, by rows (few_rows: with the second halves of X and P).
 // Bound by latency: two cluster barriers, the exchange between them and three
 // products that wait for one another a step. 8 matrices of 16 x 2048: 105 us
-// with the general path's 17 launches.
+// with the general path's 17 launches, 23.5 here; 16 of 64 x 2048 183 and 41;
+// four of 128 x 2048 140 and 52. Tried: clusters of eight for 64 rows (one matrix
+// 47 us, 16 in two rounds 94), X in shared memory as hi and lo alone (63), the
+// sums read in rank order (the exchange 14500 cycles instead of 6300).
 // ---------------------------------------------------------------------------
 constexpr int FEW_THREADS = 512;
 constexpr int FEW_GROUPS = FEW_THREADS / 128;  // four warps reach all of tensor memory's lanes
