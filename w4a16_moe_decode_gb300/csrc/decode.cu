@@ -1889,8 +1889,8 @@ __global__ void __launch_bounds__(256 * GR) k_gemv_rows(GemvArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int KGB = FMT == FLINT_MOE_NVFP4 ? KG_NVFP4 : KG_BF16, NB = GR > 1 ? 1 : GEMV_BUFS(FMT);
   const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const int nw = (blockDim.x >> 5) / GR;  // of the group
-  const int group = GR > 1 ? wid >> 3 : 0, warp = wid - group * nw, thread = threadIdx.x - group * nw * 32;
+  const int nw = GR > 1 ? 8 : blockDim.x >> 5;  // of the group
+  const int group = GR > 1 ? wid >> 3 : 0, warp = GR > 1 ? wid & 7 : wid, thread = GR > 1 ? threadIdx.x & 255 : threadIdx.x;
   const int KGW = (a.K / KG_COLS) / nw;  // k-groups per warp
   size_t xs_off, inv_off, red_off, bar_off;
   gemv_rows_smem(a.K, a.B, FMT, nw, NTMAX, GR, &xs_off, &inv_off, &red_off, &bar_off);
@@ -1898,10 +1898,11 @@ __global__ void __launch_bounds__(256 * GR) k_gemv_rows(GemvArgs a) {
   uint8_t* const wb0 = smem + (size_t)wid * NB * bytes;  // this warp's NB buffers
   uint8_t* xs = smem + xs_off;
   float* s_inv = reinterpret_cast<float*>(smem + inv_off);
-  float* red = reinterpret_cast<float*>(smem + red_off) + group * nw * NTMAX * 128;
+  float* red = reinterpret_cast<float*>(smem + red_off);
+  if constexpr (GR > 1) red += group * nw * NTMAX * 128;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + bar_off) + wid * 2;
   const int xstride = a.K * 2 + 16, tiles = a.N / 16;
-  const int first = blockIdx.x * GR + group, step = gridDim.x * GR;
+  auto mine = [&](int n) { return GR > 1 ? (int)(GR * (blockIdx.x + n * gridDim.x)) + group : (int)(blockIdx.x + n * gridDim.x); };
   auto fetch = [&](int tile, int b) {  // by one lane
     mbar_arrive_expect_tx(&bar[b], bytes);
     bulk_g2s_stream(wb0 + (size_t)b * bytes, a.packed + (int64_t)tile * a.L.dn_tile + (int64_t)warp * bytes, bytes, &bar[b]);
@@ -1910,7 +1911,7 @@ __global__ void __launch_bounds__(256 * GR) k_gemv_rows(GemvArgs a) {
     for (int b = 0; b < NB; ++b) mbar_init(&bar[b], 1);
     fence_mbar_init();
     for (int b = 0; b < NB; ++b)
-      if (first + b * step < tiles) fetch(first + b * step, b);
+      if (mine(b) < tiles) fetch(mine(b), b);
   }
   if (!ADD) pdl_wait();  // x may be the previous kernel's output
   pdl_trigger();
@@ -1923,7 +1924,7 @@ __global__ void __launch_bounds__(256 * GR) k_gemv_rows(GemvArgs a) {
   const float G = FMT == FLINT_MOE_NVFP4 ? a.G[0] : 1.0f, Gu = END == GEMV_GLU && FMT == FLINT_MOE_NVFP4 ? a.G[1] : 1.0f;
   int i = 0;
   bool ok = true;
-  for (int tile = first; tile < tiles; tile += step, ++i) {
+  for (int tile = mine(0); tile < tiles; tile += GR * gridDim.x, ++i) {
     const int b = i % NB;
     float acc[2][NTMAX][4];
 #pragma unroll
@@ -1963,7 +1964,7 @@ __global__ void __launch_bounds__(256 * GR) k_gemv_rows(GemvArgs a) {
       if (ADD && i == 0) pdl_wait();  // the call must not end before the adapters' kernel
       break;
     }
-    const int next = tile + NB * step;
+    const int next = tile + NB * GR * (int)gridDim.x;
     if (lane == 0 && next < tiles) {
       fence_proxy_async();  // this warp's reads of the buffer come before the copy into it
       fetch(next, b);
@@ -1972,7 +1973,7 @@ __global__ void __launch_bounds__(256 * GR) k_gemv_rows(GemvArgs a) {
     // Output (row r of the tile, token t): token tile t / 8, fragment lane
     // 4 (r % 8) + (t % 8) / 2, element 2 (r / 8) + t % 2.
     if constexpr (END == GEMV_GLU) {
-      for (int p = thread; p < 8 * a.B; p += 32 * nw) {
+      for (int p = thread; p < 8 * a.B; p += GR > 1 ? 256 : blockDim.x) {
         const int r = p & 7, t = p >> 3, nt = t >> 3, c = t & 7;
         float gv = 0.f, uv = 0.f;
         for (int w2 = 0; w2 < nw; ++w2) {
@@ -1983,7 +1984,7 @@ __global__ void __launch_bounds__(256 * GR) k_gemv_rows(GemvArgs a) {
         glu_store(a, t, tile, r, (gv * s_inv[t]) * G, (uv * s_inv[t]) * Gu);
       }
     } else {
-      for (int p = thread; p < 16 * a.B; p += 32 * nw) {
+      for (int p = thread; p < 16 * a.B; p += GR > 1 ? 256 : blockDim.x) {
         const int r = p & 15, t = p >> 4, nt = t >> 3, c = t & 7;
         const int ln = 4 * (r & 7) + (c >> 1), e = 2 * (r >> 3) + (c & 1);
         float v = 0.f;
@@ -1995,7 +1996,7 @@ __global__ void __launch_bounds__(256 * GR) k_gemv_rows(GemvArgs a) {
   }
   if (!ok && lane == 0)  // the block's memory must outlive the copies in flight
     for (int j = i + 1; j < i + NB; ++j)
-      if (first + j * step < tiles) mbar_drain(&bar[j % NB], (j / NB) & 1);
+      if (mine(j) < tiles) mbar_drain(&bar[j % NB], (j / NB) & 1);
 }
 
 // ===========================================================================
