@@ -59,9 +59,11 @@ SHAPES = [(1, 8, 8), (1, 2048, 512), (2, 72, 200), (7, 256, 64), (31, 136, 1032)
           (129, 128, 264), (200, 520, 328), (256, 256, 256), (257, 264, 520), (513, 200, 776), (1000, 328, 72), (2050, 136, 96)]
 # enough tiles of 256 x 256 for pairs of CTAs: in the first products, the last ones, and the weights' gradients
 LARGE = [(1300, 72, 1704), (2600, 2040, 72), (40, 2040, 2600), (4100, 1288, 1160)]
+# one tile a CTA and SM with long runs of k-blocks, in the second product and in the first
+LONG = [(1024, 832, 2600), (100, 2600, 8000)]
 
 
-@pytest.mark.parametrize("T,H,I", SHAPES + LARGE)
+@pytest.mark.parametrize("T,H,I", SHAPES + LARGE + LONG)
 def test_forward(T, H, I):
     p = Block(T, H, I, 7 * T + H).to(DEV)
     refs, tols = p.expect_forward()
