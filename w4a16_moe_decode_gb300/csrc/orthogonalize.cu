@@ -22,9 +22,13 @@ namespace ortho {
 
 using namespace gemm;
 
-// P X as P_hi X_hi + P_lo X_hi + P_hi X_lo up to this many rows, where few rounding errors meet in a result and the products
-// cost little; above, as P_hi X_hi, whose errors average out.
+// P X as P_hi X_hi + P_lo X_hi + P_hi X_lo up to 32 rows, where few rounding errors meet in a result and the products cost
+// little; as P_hi X_hi + P_lo X_hi up to 48, where S is nearly diagonal for long matrices, so that one rounding of a place
+// of P's diagonal turns a whole row (33 x 700 of noise: 0.0041 off with P_hi alone, 0.0025 so; 8 matrices of 48 x 1000 36.0
+// and 37.5 us); above, as P_hi X_hi, whose errors average out (64 x 700 of noise: 0.0027; both halves there cost 40.7 -> 43.4
+// us for 16 of 64 x 2048).
 __host__ __device__ inline bool few_rows(int m) { return m <= 32; }
+__host__ __device__ inline bool p_halves(int m) { return m <= 48; }
 
 constexpr float X_SCALE = 1024.f, S_SCALE = 1024.f, P_SCALE = 256.f;
 
@@ -234,7 +238,7 @@ struct Poly {
     const uint16_t* s;
     int pitch;
     float b, c;
-    int lo;  // P's second half too
+    int lo;  // P's second half too (p_halves)
   };
   struct Pre {
     uint4 s[4];
@@ -329,7 +333,7 @@ struct Update {
 //   S's partial sums of the CTA's rows (tcgen05) -> shared memory; each CTA adds
 //   its share of them over the cluster and hands the f16 result to all;
 //   P = b S + c S S, by every CTA for itself;
-//   X <- a X + X P, by rows (few_rows: with the second halves of X and P).
+//   X <- a X + X P, by rows (few_rows, p_halves: with the second halves of X and P).
 // Bound by latency: two cluster barriers, the exchange between them and three
 // products that wait for one another a step. 8 matrices of 16 x 2048: 105 us
 // with the general path's 17 launches, 23.5 here; 16 of 64 x 2048 183 and 41;
@@ -367,7 +371,7 @@ __host__ __device__ inline FewPlan few_plan(int m, int kc) {
   f.x[1] = (size_t)(halves - 1) * f.mb * f.xbox;
   f.s = (size_t)halves * f.mb * f.xbox;
   f.p = f.s + (size_t)f.mb * f.sbox;
-  const size_t p = (size_t)halves * f.mb * f.pbox, sums = (size_t)f.mp * m * 4;
+  const size_t p = (size_t)(p_halves(m) ? 2 : 1) * f.mb * f.pbox, sums = (size_t)f.mp * m * 4;
   f.total = 1024 + f.p + (p > sums ? p : sums);
   const int cols = (kc / 128 + 2) * f.mp;
   f.tmem = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, group = warp >> 2;
   const int C = gridDim.x, rank = blockIdx.x;
   const FewPlan f = few_plan(a.m, a.kc);
-  const bool both = few_rows(a.m);
+  const bool both = few_rows(a.m), both_p = p_halves(a.m);
   const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
   uint8_t* const sm = dsmem + (base - smem_addr(dsmem));
   const uint32_t xs = base + (uint32_t)f.x[0], xls = base + (uint32_t)f.x[1], ss = base + (uint32_t)f.s, ps = base + (uint32_t)f.p;
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
           uint4 hi, lo;
           split8(v, hi, lo);
           *reinterpret_cast<uint4*>(pp + (pc >> 3) * f.pbox + at) = hi;
-          if (both) *reinterpret_cast<uint4*>(pp + plo + (pc >> 3) * f.pbox + at) = lo;
+          if (both_p) *reinterpret_cast<uint4*>(pp + plo + (pc >> 3) * f.pbox + at) = lo;
         }
     }
     ready();
@@ -617,10 +621,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
         for (int ks = 0; ks < f.mp / 16; ++ks) {
           const uint32_t ox = row + k_step(ks, f.xbox), op = k_step(ks, f.pbox);
           tc_mma(d_x + t * f.mp, dh + ox, ph + op, idesc, ks > 0);
-          if (both) {
-            tc_mma(d_x + t * f.mp, dh + ox, pl + op, idesc, 1);
-            tc_mma(d_x + t * f.mp, dl + ox, ph + op, idesc, 1);
-          }
+          if (both_p) tc_mma(d_x + t * f.mp, dh + ox, pl + op, idesc, 1);
+          if (both) tc_mma(d_x + t * f.mp, dl + ox, ph + op, idesc, 1);
         }
       }
       tc_commit(&bar);
@@ -714,7 +716,7 @@ WsPlan ws_plan(int n, int rows, int cols) {
   o += mb;
   for (int i = 0; i < 2; ++i) {
     w.p[i] = o;
-    o += i == 0 || few_rows(w.m) ? mb : 0;
+    o += i == 0 || p_halves(w.m) ? mb : 0;
   }
   w.total = o;
   return w;
@@ -806,7 +808,7 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
   AllMaps<Update<false>> mu;
   mp.of[0].a[0] = mp.of[0].b[0] = s;
   mp.of[0].io[2] = mg.of[0].io[0] = sout;
-  const bool few = few_rows(m);
+  const int segs = few_rows(m) ? 3 : p_halves(m) ? 2 : 1;
   for (int h = 0; h < 2; ++h) {
     mp.of[0].io[h] = pout[h];
     (tall ? mu.of[0].b : mu.of[0].a)[h] = p[h];
@@ -822,9 +824,9 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
       mu.of[0].io[2 + h] = xout[i & 1][h];
     }
     ok = run<Gram>({{{m, m, kx, 1, 0, 0, tall, tall, 1, n}}, 1, 1, status, 0}, mg, {}, stream) &&
-         run<Poly>({{{m, m, km, 1, 0, 0, 0, 0, 1, n}}, 1, 1, status, 0}, mp, {at(w.s), w.mpitch, cf[1], cf[2], few}, stream);
+         run<Poly>({{{m, m, km, 1, 0, 0, 0, 0, 1, n}}, 1, 1, status, 0}, mp, {at(w.s), w.mpitch, cf[1], cf[2], segs > 1}, stream);
     const int p_of = 2, x_of = 4;  // hi hi, then P_lo, then X_lo
-    const gemm::Args upd = {{{rows, cols, km, few ? 3 : 1, tall ? x_of : p_of, tall ? p_of : x_of, 0, !tall, 0, n, tall ? 1 : 2}}, 1, 1, status, 0};
+    const gemm::Args upd = {{{rows, cols, km, segs, tall ? x_of : p_of, tall ? p_of : x_of, 0, !tall, 0, n, tall ? 1 : 2}}, 1, 1, status, 0};
     const uint16_t *hi = at(w.x[i & 1][0]), *lo = at(w.x[i & 1][1]);
     ok = ok && (last ? run<Update<true>>(upd, mu, {hi, lo, w.pitch, cf[0], scale / X_SCALE, out}, stream)
                      : run<Update<false>>(upd, mu, {hi, lo, w.pitch, cf[0], 1.0f, nullptr}, stream));
