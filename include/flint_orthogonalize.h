@@ -14,7 +14,7 @@
  * values (22 significant bits), because what its rounding adds to the weak
  * directions the later steps amplify by up to a^steps. In the products, where a
  * relative error stays relative, X, S and P = b S + c S S are single f16
- * values (P two of them up to 48 rows, X up to 32). With the steps above the
+ * values (P two of them up to 64 rows, X up to 32). With the steps above the
  * result of random entries is within 2^-8 of the exact one in the norm, 2^-8.5
  * as a rule, of which its own rounding to bf16 is 2^-9.2. A step multiplies a
  * relative error of a singular value by up to 5 where that is near 1.2: with a

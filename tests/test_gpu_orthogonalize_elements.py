@@ -90,3 +90,17 @@ def test_the_last_of_many_alone(n, rows, cols):
     values(got, ref, "last")
     values(alone, ref, "alone")
     near(got, f64(alone), 2 * LIMIT, "both")
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 600), (64, 600), (600, 64), (128, 600)])
+def test_steps_of_large_coefficients(rows, cols):
+    """Coefficients up to 24, whose P is larger than that of the usual steps and its roundings with it: within the same
+    bound."""
+    steps = ((8.287, -23.596, 17.3), (4.107, -2.947, 0.545), (3.949, -2.909, 0.552), (3.318, -2.488, 0.51))
+    m = momentum(4, rows, cols, 9, "noise")
+    m = (m / torch.linalg.matrix_norm(m)[:, None, None]).contiguous()
+    ws = torch.full((fb.flint_orthogonalize_workspace_bytes(*m.shape),), 0xFF, dtype=torch.uint8, device=DEV)
+    out = torch.full(m.shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+    fb.flint_orthogonalize(m.to(DEV), out, steps, 1.0, ws, 2.0)
+    for i in range(4):
+        near(out[i], oorth.orthogonalize(f64(m[i]), steps, 1.0, 2.0), LIMIT, f"matrix {i}")

@@ -23,12 +23,12 @@ namespace ortho {
 using namespace gemm;
 
 // P X as P_hi X_hi + P_lo X_hi + P_hi X_lo up to 32 rows, where few rounding errors meet in a result and the products cost
-// little; as P_hi X_hi + P_lo X_hi up to 48, where S is nearly diagonal for long matrices, so that one rounding of a place
-// of P's diagonal turns a whole row (33 x 700 of noise: 0.0041 off with P_hi alone, 0.0025 so; 8 matrices of 48 x 1000 36.0
-// and 37.5 us); above, as P_hi X_hi, whose errors average out (64 x 700 of noise: 0.0027; both halves there cost 40.7 -> 43.4
-// us for 16 of 64 x 2048).
+// little; as P_hi X_hi + P_lo X_hi up to 64, where S is nearly diagonal for long matrices, so that one rounding of a place
+// of P's diagonal turns a whole row (33 x 700 of noise: 0.0041 off with P_hi alone, 0.0025 so, 8 matrices of 48 x 1000 36.0
+// and 37.5 us; 64 x 600 with steps of coefficients up to 24: 0.0040, 16 of 64 x 2048 40.7 and 43.4); above, as P_hi X_hi,
+// whose errors average out (128 x 2000 of noise: 0.0024).
 __host__ __device__ inline bool few_rows(int m) { return m <= 32; }
-__host__ __device__ inline bool p_halves(int m) { return m <= 48; }
+__host__ __device__ inline bool p_halves(int m) { return m <= 64; }
 
 constexpr float X_SCALE = 1024.f, S_SCALE = 1024.f, P_SCALE = 256.f;
 
