@@ -18,9 +18,11 @@
  * result of random entries is within 2^-8 of the exact one in the norm, 2^-8.5
  * as a rule, of which its own rounding to bf16 is 2^-9.2. A step multiplies a
  * relative error of a singular value by up to 5 where that is near 1.2: with a
- * few rows (1 to 4), whose values may all lie there, 2^-7 was found. Singular values must stay below 8
- * during the steps (S) and b s^2 + c s^4 below 255 (P), as any useful steps'
- * do: beyond, results are not finite.
+ * few rows (1 to 4), whose values may all lie there, 2^-7 was found. What is
+ * kept of an X far below one (|M| far below eps) is a power of two times it, so
+ * that all of this holds down to |M| = 2^-100 eps. Singular values must stay
+ * below 8 during the steps (S) and b s^2 + c s^4 below 255 (P), as any useful
+ * steps' do: beyond, results are not finite.
  *
  * Conventions as in flint_moe.h: device pointers, caller-owned memory, no
  * allocation, asynchronous on `stream`, status codes. Matrices are contiguous,

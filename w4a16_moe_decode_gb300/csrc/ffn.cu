@@ -33,6 +33,7 @@ struct Store {
   static constexpr int MAPS = MOST, OUTS = 1, INS = 0;
   struct Args {};
   using Pre = NoPre;
+  static __device__ __forceinline__ void matrix(const Args&, Part&) {}
   static __device__ __forceinline__ void chunk(const Args&, const MapsOf<Store>& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
                                                const Pre&) {
     const float* v = reinterpret_cast<const float*>(w);
@@ -48,6 +49,7 @@ struct Glu {
   static constexpr int MAPS = 1, OUTS = 3, INS = 0;
   struct Args {};
   using Pre = NoPre;
+  static __device__ __forceinline__ void matrix(const Args&, Part&) {}
   static __device__ __forceinline__ void chunk(const Args&, const MapsOf<Glu>& maps, Part& t, int c, uint32_t (&wg)[32], uint32_t (&wu)[32],
                                                const Pre&) {
     const float* g = reinterpret_cast<const float*>(wg);
@@ -96,6 +98,7 @@ struct DGlu {
       slot_row(t, in + SLOT, u);
     }
   };
+  static __device__ __forceinline__ void matrix(const Args&, Part&) {}
   static __device__ __forceinline__ void chunk(const Args&, const MapsOf<DGlu>& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
                                                const Pre& pre) {
     const float* d = reinterpret_cast<const float*>(w);

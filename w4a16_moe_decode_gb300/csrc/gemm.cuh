@@ -129,6 +129,7 @@ struct Part {
   uint8_t* sm;    // the warp's slots
   uint32_t sm_addr;
   int slot, slots;  // the next one to fill, of how many
+  float4 f;         // what the epilogue keeps of its matrix (E::matrix, once a tile)
 
   // The place of 16-byte piece c of this lane's row in a slot: the 64-byte swizzle.
   static __device__ __forceinline__ uint32_t piece(int lane, int c) { return (uint32_t)(lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)); }
@@ -378,6 +379,7 @@ __global__ void __launch_bounds__(THREADS<C>, 2) k_gemm(const Args a, const __gr
   t.slots = SLOTS;
   constexpr int CHUNKS = Walk<C, E::PAIR>::COLS / 32;
   if (warp >= 2) {
+    E::matrix(e, t);
     const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16);
     if (S == 1) {
       t.row0 = m0 + q * 32;
@@ -636,6 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<Two>, 1)
       t.row0 = w.m * Two::TM + (int)rank * 128 + q * 32;
       t.row = t.row0 + lane;
       t.twice = p.sym && w.m != w.n;
+      E::matrix(e, t);
       ok = __all_sync(0xffffffffu, wait_ab(&acc_full[b], (n >> 1) & 1, abort, a.status));
       if (!ok) break;
       tc_fence_after();

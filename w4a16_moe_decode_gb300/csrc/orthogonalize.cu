@@ -6,7 +6,9 @@
 // relative to X from the left, (1 + e) X, only turns the result by e: so the products take f16 values, S from X's hi, P
 // from one rounding of each of its parts, and the tensor cores run at one product's rate instead of three. S, P and the
 // update of wide X read their transposes as they lie (S and P are their own); S and P are computed above the diagonal.
-// Scaled values: X is kept times 2^10, S times 2^10 and P times 2^8, so that f16 holds them to 2^-34 and below.
+// Scaled values: X is kept times 2^10, S times 2^10 and P times 2^8, so that f16 holds X and S to 2^-35 and P to 2^-33, or to
+// a relative 2^-12 (X's two values 2^-23) where that is more. A matrix whose norm is far below eps gives an X far below one:
+// it is kept times a further power of two, which falls as the steps let X grow (Size).
 //
 // Two updates of 8192 x 2048, us: 980 (1130 TFLOP/s of the products that cannot be left out), bound by the tensor cores
 // in X P and, in the two products of S, by one round of 72 tiles; norm and conversion take 60 of it from memory. 256 x
@@ -72,6 +74,35 @@ struct Start {
   double* part;  // [n][parts]
   uint16_t *hi, *lo;
   int* status;
+  int steps;
+  float coeffs[3 * FLINT_ORTHOGONALIZE_MAX_STEPS];
+  float4* factors;  // [n][FLINT_ORTHOGONALIZE_MAX_STEPS]: Size::Step of each step
+};
+
+// What X is kept times, 2^e, from a bound of its size, which a step raises to |a| n + |b| n^3 + |c| n^5 at most. So a small
+// X fills f16's range as a large one does, its S and P with it, and the bound of a grown one ends at e = 0.
+constexpr int SIZE_MOST = 100;  // (an X below 2^-100 keeps fewer digits)
+__device__ __forceinline__ int exponent(float v) { return (int)(__float_as_uint(v) >> 23) - 127; }  // of v >= 0
+struct Size {
+  float n;  // bound of what is kept, 2^e X
+  int e;
+  // P = ps S + pq S S, X <- ua X + up P X, of what is kept of each.
+  struct Step {
+    float ps, pq, up, ua;
+  };
+  // The factors of a step; after the last one X is kept as it is.
+  __device__ __forceinline__ Step next(float a, float b, float c, bool last) {
+    const float w = exp2i(-e), t = n * w, t2 = t * t;
+    const float n1 = fminf(n * (fabsf(a) + t2 * (fabsf(b) + fabsf(c) * t2)), 0x1p120f);
+    const int e1 = last ? 0 : n1 > 0.f ? min(max(e - exponent(n1) - 1, 0), SIZE_MOST) : e;
+    // P of a small X is 2^2e times its value: coefficients that f16 would not hold then are scaled down.
+    const int pe = e > 0 ? max(exponent(fabsf(b) + fabsf(c) * w * w) - 6, 0) : 0;
+    const Step s = {b * (P_SCALE / S_SCALE) * exp2i(-pe), c * (P_SCALE / (S_SCALE * S_SCALE)) * exp2i(max(-2 * e - pe, -126)),
+                    (1.0f / P_SCALE) * exp2i(min(max(pe - 2 * e + e1 - e, -126), 126)), a * exp2i(e1 - e)};
+    n = n1 * exp2i(e1 - e);
+    e = e1;
+    return s;
+  }
 };
 
 constexpr int START_THREADS = 256;
@@ -113,11 +144,13 @@ struct Squares {
   }
   __device__ __forceinline__ double value() const { return (double)q * __longlong_as_double((long long)(1023 + 2 * ex) << 52); }
 };
-// X_SCALE / (|M| + eps) as two FP32 factors, since a large norm's is below FP32's normals.
-__device__ __forceinline__ float2 inverse(double sum, float eps) {
-  const double d = sqrt(sum) + (double)eps;
-  const int half = ((int)(__double_as_longlong(d) >> 52) - 1023) / 2;
-  return make_float2(exp2i(-half), (float)(X_SCALE / (d * __longlong_as_double((long long)(1023 - half) << 52))));
+// 2^e X_SCALE / (|M| + eps) as two FP32 factors, since a large norm's is below FP32's normals, and X's size.
+__device__ __forceinline__ float2 inverse(double sum, float eps, Size& size) {
+  const double norm = sqrt(sum), d = norm + (double)eps;
+  const int ed = (int)(__double_as_longlong(d) >> 52) - 1023, en = (int)(__double_as_longlong(norm) >> 52) - 1023, half = ed / 2;
+  size = {1.0f, norm > 0.0 ? min(max(ed - en - 1, 0), SIZE_MOST) : 0};
+  const int e0 = size.e / 2;
+  return make_float2(exp2i(e0 - half), (float)(X_SCALE / (d * __longlong_as_double((long long)(1023 - half - (size.e - e0)) << 52))));
 }
 
 __global__ void __launch_bounds__(START_THREADS) k_ortho_norm(const Start a) {
@@ -151,6 +184,9 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_norm(const Start a) {
 
 __global__ void __launch_bounds__(START_THREADS) k_ortho_split(const Start a) {
   __shared__ float s_scale[2];
+  Size size = {1.0f, 0};  // (thread 0)
+  // The last block is for the steps' factors alone, which take as long as a block's share of a small matrix.
+  const bool factors = blockIdx.x == a.parts;
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x < 32) {
@@ -159,15 +195,31 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_split(const Start a) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (threadIdx.x == 0) {
-      const float2 f = inverse(sum, a.eps);
+      const float2 f = inverse(sum, a.eps, size);
       s_scale[0] = f.x;
       s_scale[1] = f.y;
     }
   }
   __syncthreads();
   const float s0 = s_scale[0], s1 = s_scale[1];
+  if (factors) {
+    if (threadIdx.x >= 32) return;
+    auto step = [&](int i, Size& z) {
+      const Size::Step s = z.next(a.coeffs[3 * i], a.coeffs[3 * i + 1], a.coeffs[3 * i + 2], i + 1 == a.steps);
+      a.factors[(size_t)blockIdx.y * FLINT_ORTHOGONALIZE_MAX_STEPS + i] = make_float4(s.ps, s.pq, s.up, s.ua);
+    };
+    const int i = threadIdx.x;
+    const bool mine = i < a.steps, grows = !mine || fabsf(a.coeffs[3 * i]) >= 1.0f;
+    if (__all_sync(0xffffffffu, grows) && __shfl_sync(0xffffffffu, size.e, 0) == 0) {  // kept as it is in every step
+      size = {1.0f, 0};
+      if (mine) step(i, size);
+    } else if (i == 0) {
+      for (int k = 0; k < a.steps; ++k) step(k, size);
+    }
+    return;
+  }
   const size_t all = (size_t)a.rows * a.cols, first = blockIdx.y * all, out = (size_t)blockIdx.y * a.rows * a.pitch;
-  const size_t step = (size_t)gridDim.x * START_THREADS;
+  const size_t step = (size_t)a.parts * START_THREADS;
   if (a.pitch == a.cols) {  // rows of whole pieces of eight
     for (size_t i = 8 * ((size_t)blockIdx.x * START_THREADS + threadIdx.x); i < all; i += 8 * step) {
       float v[8];
@@ -181,7 +233,7 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_split(const Start a) {
     }
   } else {
     // a warp a row, each lane up to eight of its values at a time
-    const int lane = threadIdx.x & 31, warps = gridDim.x * (START_THREADS / 32);
+    const int lane = threadIdx.x & 31, warps = a.parts * (START_THREADS / 32);
     for (int r = blockIdx.x * (START_THREADS / 32) + (threadIdx.x >> 5); r < a.rows; r += warps) {
       const size_t from = first + (size_t)r * a.cols, to = out + (size_t)r * a.pitch;
       for (int c0 = lane; c0 < a.cols; c0 += 256) {
@@ -212,6 +264,7 @@ struct Gram {
   static constexpr int MAPS = 1, OUTS = 1, INS = 0;
   struct Args {};
   using Pre = NoPre;
+  static __device__ __forceinline__ void matrix(const Args&, Part&) {}
   static __device__ __forceinline__ void chunk(const Args&, const MapsOf<Gram>& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
                                                const Pre&) {
     float* v = reinterpret_cast<float*>(w);
@@ -231,13 +284,16 @@ __device__ __forceinline__ void load_row(const Part& t, const uint16_t* m, int p
     v[j] = t.row < t.M && t.n0 + c + 8 * j < t.N ? __ldcg(reinterpret_cast<const uint4*>(at + 8 * j)) : make_uint4(0, 0, 0, 0);
 }
 
+// A matrix's factors of a step, which k_ortho_split left.
+__device__ __forceinline__ float4 factors_of(const float4* f, int z) { return __ldcg(f + (size_t)z * FLINT_ORTHOGONALIZE_MAX_STEPS); }
+
 struct Poly {
   static constexpr bool PAIR = false;
   static constexpr int MAPS = 1, OUTS = 2, INS = 1;
   struct Args {
     const uint16_t* s;
     int pitch;
-    float b, c;
+    const float4* factors;  // of this step, FLINT_ORTHOGONALIZE_MAX_STEPS apart
     int lo;  // P's second half too (p_halves)
   };
   struct Pre {
@@ -245,9 +301,10 @@ struct Poly {
     __device__ __forceinline__ Pre(const Args& a, const Part& t, int c) { load_row(t, a.s, a.pitch, c, s); }
     __device__ __forceinline__ Pre(const Part& t, const uint8_t* in) { slot_row(t, in, s); }
   };
+  static __device__ __forceinline__ void matrix(const Args& a, Part& t) { t.f = factors_of(a.factors, t.z); }
   static __device__ __forceinline__ void chunk(const Args& a, const MapsOf<Poly>& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
                                                const Pre& pre) {
-    const float fs = a.b * (P_SCALE / S_SCALE), fq = a.c * (P_SCALE / (S_SCALE * S_SCALE));
+    const float fs = t.f.x, fq = t.f.y;
     uint4 hi[4], lo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -273,7 +330,8 @@ struct Update {
   struct Args {
     const uint16_t *hi, *lo;
     int pitch;
-    float a, scale;
+    const float4* factors;
+    float scale;
     uint16_t* out;  // LAST: [batch][M][N]
   };
   struct Pre {
@@ -287,9 +345,10 @@ struct Update {
       slot_row(t, in + SLOT, lo);
     }
   };
+  static __device__ __forceinline__ void matrix(const Args& a, Part& t) { t.f = factors_of(a.factors, t.z); }
   static __device__ __forceinline__ void chunk(const Args& a, const MapsOf<Update>& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
                                                const Pre& pre) {
-    constexpr float fp = 1.0f / P_SCALE;  // P X comes scaled by both
+    const float fp = t.f.z, fa = t.f.w;
     uint4 hv[4], lv[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -297,7 +356,7 @@ struct Update {
       unpack8_f16(pre.hi[j], h);
       unpack8_f16(pre.lo[j], l);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = fmaf(fp, __uint_as_float(w[8 * j + i]), a.a * (h[i] + l[i]));
+      for (int i = 0; i < 8; ++i) v[i] = fmaf(fp, __uint_as_float(w[8 * j + i]), fa * (h[i] + l[i]));
       if (LAST) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= a.scale;
@@ -396,6 +455,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
   extern __shared__ uint8_t dsmem[];
   __shared__ double s_sum[FEW_THREADS / 32], s_part;
   __shared__ float2 s_inv;
+  __shared__ Size::Step s_step;
   __shared__ uint64_t bar;
   __shared__ uint32_t tmem_base;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, group = warp >> 2;
@@ -417,6 +477,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
+  Size size;  // (this thread's: not one of the warp that issues the products)
+  const bool sizes = threadIdx.x == FEW_THREADS - 32;
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x == 0 && blockIdx.x + blockIdx.y == 0) *a.status = 0;
@@ -473,10 +535,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
     s_part = sum;
   }
   cluster_sync();
-  if (threadIdx.x == 0) {
+  if (sizes) {
     sum = 0.0;
     for (int r = 0; r < C; ++r) sum += ld_dsmem_f64(dsmem_addr(smem_addr(&s_part), r));
-    s_inv = inverse(sum, a.eps);
+    s_inv = inverse(sum, a.eps, size);
   }
   __syncthreads();
   const float2 inv = s_inv;
@@ -522,8 +584,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
   };
   // The thread that issues a product orders what it has seen the others write before the tensor core's reads of it.
   for (int step = 0; step < a.steps; ++step) {
-    const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1], cc = a.coeffs[3 * step + 2];
     ready();
+    if (sizes) s_step = size.next(a.coeffs[3 * step], a.coeffs[3 * step + 1], a.coeffs[3 * step + 2], step + 1 == a.steps);
     if (warp == 0 && elect_one()) {
       fence_proxy_async();
       // With one box of columns, rows of D from 64 on (which are not read) come from eight rows of X further on, and at the
@@ -590,7 +652,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
     }
     __syncwarp();
     arrived();
-    const float fs = cb * (P_SCALE / S_SCALE), fq = cc * (P_SCALE / (S_SCALE * S_SCALE));
+    const float fs = s_step.ps, fq = s_step.pq;
     for (int c = 16 * group; c < f.mp; c += 16 * FEW_GROUPS) {
       uint32_t w[16];
       __syncwarp();
@@ -628,6 +690,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
       tc_commit(&bar);
     }
     __syncwarp();
+    const float fp = s_step.up, fa = s_step.ua;
     arrived();
 #pragma unroll
     for (int n = 0; n < UNITS; ++n) {
@@ -636,7 +699,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
       uint32_t w[16];
       tc_ld16(d_x + lanes + t * f.mp + c, w);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[n][e] = fmaf(1.0f / P_SCALE, __uint_as_float(w[e]), ca * x[n][e]);
+      for (int e = 0; e < 16; ++e) x[n][e] = fmaf(fp, __uint_as_float(w[e]), fa * x[n][e]);
       if (step + 1 < a.steps) hand_over(n, t, c);
     }
   }
@@ -696,7 +759,7 @@ int parts_of(int rows, int cols) {
 
 struct WsPlan {
   int m, pitch, mpitch, parts;
-  size_t part, x[2][2], s, p[2], total;  // x: of even and odd steps; x, p: hi and lo
+  size_t part, factors, x[2][2], s, p[2], total;  // x: of even and odd steps; x, p: hi and lo
 };
 WsPlan ws_plan(int n, int rows, int cols) {
   WsPlan w = {};
@@ -708,6 +771,8 @@ WsPlan ws_plan(int n, int rows, int cols) {
   size_t o = 256;
   w.part = o;
   o += ws_align(sizeof(double) * n * w.parts);
+  w.factors = o;
+  o += ws_align(sizeof(float4) * FLINT_ORTHOGONALIZE_MAX_STEPS * n);
   for (int i = 0; i < 4; ++i) {
     w.x[i >> 1][i & 1] = o;
     o += xb;
@@ -797,10 +862,12 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
   o = sout;
   if (cols % 8 == 0) ok = ok && map_matrix(&o, out, cols, rows, cols, n, (int64_t)rows * cols, true);
   if (!ok) return FLINT_MOE_ECUDA;
-  const Start st = {in, fmt == FLINT_ORTHOGONALIZE_BF16, n, rows, cols, w.pitch, w.parts, eps,
-                    reinterpret_cast<double*>(wsp + w.part), at(w.x[0][0]), at(w.x[0][1]), status};
-  const dim3 grid((unsigned)w.parts, (unsigned)n);
-  if (!launch<k_ortho_norm, 0>(grid, START_THREADS, 0, 0, stream, st) || !launch<k_ortho_split, 0>(grid, START_THREADS, 0, 0, stream, st))
+  Start st = {in, fmt == FLINT_ORTHOGONALIZE_BF16, n, rows, cols, w.pitch, w.parts, eps,
+                    reinterpret_cast<double*>(wsp + w.part), at(w.x[0][0]), at(w.x[0][1]), status, steps, {}, reinterpret_cast<float4*>(wsp + w.factors)};
+  std::copy(coeffs, coeffs + 3 * steps, st.coeffs);
+  const unsigned parts = (unsigned)w.parts, mats = (unsigned)n;
+  if (!launch<k_ortho_norm, 0>(dim3(parts, mats), START_THREADS, 0, 0, stream, st) ||
+      !launch<k_ortho_split, 0>(dim3(parts + 1, mats), START_THREADS, 0, 0, stream, st))
     return FLINT_MOE_ECUDA;
   const int kx = ((tall ? rows : cols) + BK - 1) / BK, km = (m + BK - 1) / BK;
   AllMaps<Gram> mg;
@@ -814,7 +881,7 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
     (tall ? mu.of[0].b : mu.of[0].a)[h] = p[h];
   }
   for (int i = 0; i < steps; ++i) {
-    const float* cf = coeffs + 3 * i;
+    const float4* factors = st.factors + i;
     const bool last = i + 1 == steps;
     // S = X X^T (X^T X), both operands the same matrix; P from S, which is its own transpose; X's rows times P, or P times X
     mg.of[0].a[0] = mg.of[0].b[0] = x[i & 1][0];
@@ -824,12 +891,12 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
       mu.of[0].io[2 + h] = xout[i & 1][h];
     }
     ok = run<Gram>({{{m, m, kx, 1, 0, 0, tall, tall, 1, n}}, 1, 1, status, 0}, mg, {}, stream) &&
-         run<Poly>({{{m, m, km, 1, 0, 0, 0, 0, 1, n}}, 1, 1, status, 0}, mp, {at(w.s), w.mpitch, cf[1], cf[2], segs > 1}, stream);
+         run<Poly>({{{m, m, km, 1, 0, 0, 0, 0, 1, n}}, 1, 1, status, 0}, mp, {at(w.s), w.mpitch, factors, segs > 1}, stream);
     const int p_of = 2, x_of = 4;  // hi hi, then P_lo, then X_lo
     const gemm::Args upd = {{{rows, cols, km, segs, tall ? x_of : p_of, tall ? p_of : x_of, 0, !tall, 0, n, tall ? 1 : 2}}, 1, 1, status, 0};
     const uint16_t *hi = at(w.x[i & 1][0]), *lo = at(w.x[i & 1][1]);
-    ok = ok && (last ? run<Update<true>>(upd, mu, {hi, lo, w.pitch, cf[0], scale / X_SCALE, out}, stream)
-                     : run<Update<false>>(upd, mu, {hi, lo, w.pitch, cf[0], 1.0f, nullptr}, stream));
+    ok = ok && (last ? run<Update<true>>(upd, mu, {hi, lo, w.pitch, factors, scale / X_SCALE, out}, stream)
+                     : run<Update<false>>(upd, mu, {hi, lo, w.pitch, factors, 1.0f, nullptr}, stream));
     if (!ok) return FLINT_MOE_ECUDA;
   }
   return FLINT_MOE_OK;
