@@ -20,12 +20,18 @@ namespace ffn {
 
 using namespace gemm;
 
-// sigmoid(g) and 1 - sigmoid(g), each to FP32's accuracy at both ends.
+// sigmoid(g) and 1 - sigmoid(g), neither as the difference of the other from one. e^-|g| is off by up to 2 + 1.2 |g| steps
+// of 2^-23, so that the smaller of the two is.
 __device__ __forceinline__ float2 sigmoid2(float g) {
   const float t = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + t);
   return g >= 0.f ? make_float2(r, t * r) : make_float2(t * r, r);
 }
-
+// g sigmoid(g): from e^-|g| as well, so that the quotient's divisor lies between one and two. (e^-g itself is too large for
+// the fast quotient from g = -87.4 on, and for FP32 from -88.8 on, where g e^g still is a value.)
+__device__ __forceinline__ float silu(float g) {
+  const float t = __expf(-fabsf(g));
+  return __fdividef(g >= 0.f ? g : g * t, 1.0f + t);
+}
 
 // bf16 rows [M][N] as they are.
 struct Store {
@@ -59,7 +65,7 @@ struct Glu {
     for (int j = 0; j < 4; ++j) {
       float h[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = __fdividef(g[8 * j + i], 1.0f + __expf(-g[8 * j + i])) * u[8 * j + i];
+      for (int i = 0; i < 8; ++i) h[i] = silu(g[8 * j + i]) * u[8 * j + i];
       o[j] = pack8_bf16(h);
     }
     t.put(&maps.io[0], t.n0 + c, o);
