@@ -9,6 +9,7 @@ implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -519,23 +520,94 @@ def flint_moe_balance_backward(cfg: flint_moe_config, logits, idx, T: int, seq_s
                                             _ptr(dlogits), _stream(stream)))
 
 
+@functools.lru_cache(maxsize=None)
+def _bf16() -> tuple:
+    """The types of tensors that hold bf16 values, or their bits."""
+    import torch
+    return torch.bfloat16, torch.int16, torch.uint16
+
+
+def _rows(t, what: str, rows: int, cols: int) -> int | None:
+    """The pointer of a tensor that begins with `rows` rows of `cols` bf16 values (or their bits) side by side; others are
+    refused. What decode calls bring first, since each look at a tensor takes 0.1 us of a call of 5."""
+    try:
+        if t.nbytes == 2 * rows * cols and t.is_contiguous() and t.dtype in _bf16():
+            return t.data_ptr()
+    except AttributeError:  # a pointer or None
+        return t
+    shape = t.shape  # more rows, rows of several dimensions, values one behind the other
+    n = shape.numel()
+    fits = rows < 1 or n == rows * cols or (n > rows * cols and (len(shape) < 2 or shape[-1] == cols))
+    if not fits or t.dtype not in _bf16() or not t.is_contiguous():
+        raise FlintMoeError(f"{what} {t.dtype} {tuple(shape)} for {(rows, cols)}", EINVAL)
+    return t.data_ptr()
+
+
+def _status_word(t) -> int | None:
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if t.dtype != torch.int32 or t.numel() < 1:
+        raise FlintMoeError(f"status {t.dtype} {tuple(t.shape)}", EINVAL)
+    return t.data_ptr()
+
+
+def _matrix(t, what: str, shape, size: int) -> None:
+    """Refuses a tensor of other than `shape` (or its values one behind the other), not contiguous, or whose elements are
+    not of `size` bytes (2: bf16 values or their bits)."""
+    if t is None or isinstance(t, int):
+        return
+    flat = t.dim() == 1 and t.numel() == math.prod(shape)
+    if t.element_size() != size or (size == 2 and t.dtype not in _bf16()) or not t.is_contiguous() or not (flat or tuple(t.shape) == shape):
+        raise FlintMoeError(f"{what} {t.dtype} {tuple(t.shape)} for {shape}", EINVAL)
+
+
+@functools.lru_cache(maxsize=None)
+def _glu_packed_bytes(I: int, K: int, fmt: int) -> int:
+    return lib().flint_gemv_glu_packed_bytes(I, K, fmt)
+
+
 def flint_gemv_glu_packed_bytes(I: int, K: int, fmt: int = NVFP4) -> int:
     return lib().flint_gemv_glu_packed_bytes(I, K, fmt)
 
 
 def flint_gemv_glu_pack(gate: dict, up: dict, I: int, K: int, fmt, dst, dev_status=None, stream=None) -> None:
-    """gate, up: {codes, scales, global} (NVFP4) or {bf16} tensors of matrices [I][K]."""
+    """gate, up: {codes, scales, global} (NVFP4) or {bf16} tensors of matrices [I][K], contiguous."""
+    for what, src in (("gate", gate), ("up", up)):
+        if fmt == NVFP4:
+            _matrix(src.get("codes"), what + " codes", (I, K // 2), 1)
+            _matrix(src.get("scales"), what + " scales", (I, K // 16), 1)
+            glob = src.get("global")
+            if glob is not None and not isinstance(glob, int):
+                import torch
+                if glob.dtype != torch.float32 or glob.numel() != 1:
+                    raise FlintMoeError(f"{what} global {glob.dtype} {tuple(glob.shape)}", EINVAL)
+        else:
+            _matrix(src.get("bf16"), what, (I, K), 2)
+    status = _status_word(dev_status)
+    if not dst.is_contiguous():
+        raise FlintMoeError("dst", EINVAL)
     g, u = _gemv_src(gate), _gemv_src(up)
     _check("flint_gemv_glu_pack",
            lib().flint_gemv_glu_pack(ctypes.byref(g), ctypes.byref(u), I, K, fmt, _ptr(dst),
-                                     dst.numel() * dst.element_size(), _ptr(dev_status), _stream(stream)))
+                                     dst.numel() * dst.element_size(), status, _stream(stream)))
 
 
 def flint_gemv_glu(packed, I: int, K: int, fmt, x, B: int, h, norm_weight=None, eps: float = 0.0, dev_status=None,
                    stream=None) -> None:
-    """h = bf16(silu(gate x) * (up x)) for up to 32 rows (include/flint_gemv.h)."""
-    _check("flint_gemv_glu", lib().flint_gemv_glu(_ptr(packed), I, K, fmt, _ptr(x), B, _ptr(h), _ptr(norm_weight),
-                                                  float(eps), _ptr(dev_status), _stream(stream)))
+    """h = bf16(silu(gate x) * (up x)) for up to 32 rows (include/flint_gemv.h): x and h begin with B contiguous rows of K
+    and I values."""
+    if not (packed is None or isinstance(packed, int)):
+        if packed.nbytes < (_glu_packed_bytes(I, K, fmt) if B > 0 else 0) or not packed.is_contiguous():
+            raise FlintMoeError(f"packed matrices {tuple(packed.shape)}", EINVAL)
+        packed = packed.data_ptr()
+    if dev_status is not None:
+        dev_status = _status_word(dev_status)
+    st = lib().flint_gemv_glu(packed, I, K, fmt, _rows(x, "x", B, K), B, _rows(h, "h", B, I),
+                              None if norm_weight is None else _rows(norm_weight, "norm weight", 1, K), float(eps),
+                              dev_status, _stream(stream))
+    if st != OK:
+        raise FlintMoeError("flint_gemv_glu", st)
 
 
 def _values(t, what: str, shape, bf16: bool = True) -> None:
@@ -543,7 +615,7 @@ def _values(t, what: str, shape, bf16: bool = True) -> None:
     if t is None or isinstance(t, int):
         return
     import torch
-    kinds = (torch.bfloat16, torch.int16, torch.uint16) if bf16 else (torch.float32,)
+    kinds = _bf16() if bf16 else (torch.float32,)
     if t.dtype not in kinds or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
         raise FlintMoeError(f"{what} {t.dtype} {tuple(t.shape)} for {tuple(shape)}", EINVAL)
 
