@@ -83,3 +83,25 @@ def test_gemv_glu_pack(reached):
         refused(reached, fb.flint_gemv_glu_pack, {"bf16": bad}, {"bf16": bf(I, K)}, I, K, fb.BF16, dst, stream=0)
     refused(reached, fb.flint_gemv_glu_pack, good, good, I, K, fb.NVFP4, u8(8192)[::2], stream=0)
     refused(reached, fb.flint_gemv_glu_pack, good, good, I, K, fb.NVFP4, dst, torch.zeros(1, dtype=torch.int64), stream=0)
+
+
+def test_ffn_rows(reached):
+    """Token rows of other types: their bits would be read as bf16."""
+    T, H, I = 6, 64, 128
+    f = fb.flint_ffn(H, I, 0x1000, 0x2000, 0x3000)
+    ws = 0x100000
+    rows, act = bf(T, H), bf(T, I)
+    taken(reached, fb.flint_ffn_forward, f, rows, T, rows.clone(), ws, act, act.clone(), **WS)
+    taken(reached, fb.flint_ffn_forward, f, rows.view(torch.int16), T, rows.view(torch.int16), ws, **WS)
+    taken(reached, fb.flint_ffn_forward, f, 0x10000, T, 0x20000, ws, **WS)
+    for bad in (rows.float(), rows.half(), rows.double(), torch.zeros(T, H, dtype=torch.int32), torch.zeros(T, 2 * H, dtype=torch.uint8)):
+        refused(reached, fb.flint_ffn_forward, f, bad, T, rows, ws, **WS)
+        refused(reached, fb.flint_ffn_forward, f, rows, T, bad, ws, **WS)
+        refused(reached, fb.flint_ffn_forward, f, bad, T, rows, ws, ldx=H, **WS)
+    w = [bf(I, H), bf(I, H), bf(H, I)]
+    taken(reached, fb.flint_ffn_backward, f, rows, act, act, rows, T, rows, *w, ws, **WS)
+    taken(reached, fb.flint_ffn_backward, f, rows, act, act, rows, T, None, *w, ws, **WS)
+    for bad in (rows.float(), rows.half(), torch.zeros(T, H, dtype=torch.int32)):
+        refused(reached, fb.flint_ffn_backward, f, bad, act, act, rows, T, rows, *w, ws, **WS)
+        refused(reached, fb.flint_ffn_backward, f, rows, act, act, bad, T, rows, *w, ws, **WS)
+        refused(reached, fb.flint_ffn_backward, f, rows, act, act, rows, T, bad, *w, ws, **WS)

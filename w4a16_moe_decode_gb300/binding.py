@@ -635,6 +635,13 @@ def flint_ffn_init(gate, up, down, hidden=None, inter=None) -> flint_ffn:
     return ffn
 
 
+def _tokens(**rows) -> None:
+    """Refuses tensors of token rows that hold other than bf16 values or their bits (their strides: _ld)."""
+    for what, t in rows.items():
+        if not (t is None or isinstance(t, int)) and t.dtype not in _bf16():
+            raise FlintMoeError(f"{what} {t.dtype}", EINVAL)
+
+
 def flint_ffn_workspace_bytes(ffn: flint_ffn, max_tokens: int) -> int:
     return lib().flint_ffn_workspace_bytes(ctypes.byref(ffn), max_tokens)
 
@@ -643,6 +650,7 @@ def flint_ffn_forward(ffn: flint_ffn, x, T: int, y, workspace, gate_out=None, up
                       workspace_bytes=None, stream=None) -> None:
     """y[t] = down(silu(gate x[t]) * (up x[t])) for T tokens (include/flint_ffn.h). gate_out, up_out [T][I] receive
     what the gradients need."""
+    _tokens(x=x, y=y)
     _values(gate_out, "gate_out", (T, ffn.inter))
     _values(up_out, "up_out", (T, ffn.inter))
     _check("flint_ffn_forward",
@@ -659,6 +667,7 @@ def flint_ffn_backward(ffn: flint_ffn, x, gate_act, up_act, dy, T: int, dx, dgat
                        lddy=None, lddx=None, workspace_bytes=None, stream=None) -> None:
     """Gradients of flint_ffn_forward from dy and the products it kept (include/flint_ffn.h). dx None skips it; dgate,
     dup and ddown None skip the weights'."""
+    _tokens(x=x, dy=dy, dx=dx)
     _values(gate_act, "gate_act", (T, ffn.inter))
     _values(up_act, "up_act", (T, ffn.inter))
     _values(dgate, "dgate", (ffn.inter, ffn.hidden))
