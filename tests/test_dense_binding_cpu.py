@@ -105,3 +105,11 @@ def test_ffn_rows(reached):
         refused(reached, fb.flint_ffn_backward, f, bad, act, act, rows, T, rows, *w, ws, **WS)
         refused(reached, fb.flint_ffn_backward, f, rows, act, act, bad, T, rows, *w, ws, **WS)
         refused(reached, fb.flint_ffn_backward, f, rows, act, act, rows, T, bad, *w, ws, **WS)
+
+
+def test_coefficients_are_triples(reached):
+    """Steps of other lengths whose values add up to triples all the same."""
+    m, out = torch.zeros(8, 16), bf(8, 16)
+    taken(reached, fb.flint_orthogonalize, m, out, ((1.0, -0.5, 0.1), (1.0, 0.0, 0.0)), 1e-7, 0x1000, **WS)
+    for bad in (((1.0, -0.5), (0.1, 1.0, 0.0, 0.0)), ((1.0, -0.5, 0.1, 0.0), (1.0, 0.0)), ((1.0,) * 6, ())):
+        refused(reached, fb.flint_orthogonalize, m, out, bad, 1e-7, 0x1000, **WS)

@@ -697,7 +697,7 @@ def flint_orthogonalize(m, out, coeffs, eps: float, workspace, scale: float = 1.
     _values(out, "out", shape)
     n, rows, cols = shape if len(shape) == 3 else (1, *shape)
     flat = [float(v) for step in coeffs for v in step]
-    if len(flat) != 3 * len(coeffs):
+    if any(len(step) != 3 for step in coeffs):
         raise FlintMoeError("coefficients", EINVAL)
     _check("flint_orthogonalize",
            lib().flint_orthogonalize(_ptr(m), 0 if f32 else 1, n, rows, cols, (ctypes.c_float * len(flat))(*flat),
