@@ -1882,7 +1882,9 @@ __device__ __forceinline__ bool group_all(int group, bool ok) {
 
 // GR = 2: two groups of eight warps share a block's rows, each with its own tiles (and one buffer of weights). Rows that
 // leave an SM room for one block only would have eight warps on it otherwise, which take turns waiting (gemv_glu of 32 x
-// 2048 x 8192: 25.8 -> 21.1 us; 32 x 2048 x 2048 8.9 -> 7.7).
+// 2048 x 8192: 25.8 -> 21.1 us; 32 x 2048 x 2048 8.9 -> 7.7). Tiles are dealt to all blocks' first groups before any second
+// one gets a tile, so that no SM idles beside one with two (320 tiles, 17 rows: 8.7 us a block's two tiles together, 7.8
+// so; 1024 tiles 14.0 and 13.2).
 template <int FMT, int NTMAX, GemvEnd END, int GR = 1>
 __global__ void __launch_bounds__(256 * GR) k_gemv_rows(GemvArgs a) {
   constexpr bool ADD = END == GEMV_ADD;
@@ -1902,7 +1904,7 @@ __global__ void __launch_bounds__(256 * GR) k_gemv_rows(GemvArgs a) {
   if constexpr (GR > 1) red += group * nw * NTMAX * 128;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + bar_off) + wid * 2;
   const int xstride = a.K * 2 + 16, tiles = a.N / 16;
-  auto mine = [&](int n) { return GR > 1 ? (int)(GR * (blockIdx.x + n * gridDim.x)) + group : (int)(blockIdx.x + n * gridDim.x); };
+  auto mine = [&](int n) { return (int)(blockIdx.x + (GR * n + group) * gridDim.x); };  // (blocks first, then their groups)
   auto fetch = [&](int tile, int b) {  // by one lane
     mbar_arrive_expect_tx(&bar[b], bytes);
     bulk_g2s_stream(wb0 + (size_t)b * bytes, a.packed + (int64_t)tile * a.L.dn_tile + (int64_t)warp * bytes, bytes, &bar[b]);
