@@ -17,7 +17,8 @@
  * between calls, and must not be shared by calls in flight at the same time.
  * Results do not depend on timing: every sum has a fixed order. A device-side
  * wait that gave up sets FLINT_MOE_DEV_ERR_TIMEOUT in the workspace's status
- * word (flint_moe_read_status), which each call clears.
+ * word (flint_moe_read_status), which each call clears that has anything to
+ * compute (tokens, and an output).
  */
 #ifndef FLINT_FFN_H_
 #define FLINT_FFN_H_

@@ -10,19 +10,21 @@
  * (3.4445, -4.7750, 2.0315) five times, values of 0.01 to 1 end between 0.7
  * and 1.2, the singular vectors as they were.
  *
- * Numerics: every sum is FP32 (the norm FP64). X is kept as the sum of two f16
- * values (22 significant bits), because what its rounding adds to the weak
- * directions the later steps amplify by up to a^steps. In the products, where a
- * relative error stays relative, X, S and P = b S + c S S are single f16
- * values (P two of them up to 64 rows, X up to 32). With the steps above the
- * result of random entries is within 2^-8 of the exact one in the norm, 2^-8.5
- * as a rule, of which its own rounding to bf16 is 2^-9.2. A step multiplies a
- * relative error of a singular value by up to 5 where that is near 1.2: with a
- * few rows (1 to 4), whose values may all lie there, 2^-7 was found. What is
- * kept of an X far below one (|M| far below eps) is a power of two times it, so
- * that all of this holds down to |M| = 2^-100 eps. Singular values must stay
- * below 8 during the steps (S) and b s^2 + c s^4 below 255 (P), as any useful
- * steps' do: beyond, results are not finite.
+ * Numerics: sums are FP32; of the norm's squares a thread adds up to 4096 in
+ * FP32, FP64 adds the threads'. X is kept as the sum of two f16 values, to 2^-22
+ * of a value or to 2^-35 where that is more (in one kernel's registers, up to
+ * 128 rows, as FP32), because what its rounding adds to the weak directions the
+ * later steps amplify by up to a^steps. In the products, where a relative error
+ * stays relative, X, S and P = b S + c S S are single f16 values, to 2^-11 of a
+ * value or to 2^-35 (P: 2^-33); up to 64 rows P is two of them, up to 32 X is.
+ * With the steps above the result of random entries is within 2^-8 of the exact
+ * one in the norm, 2^-8.5 as a rule, of which its own rounding to bf16 is
+ * 2^-9.2. A step multiplies a relative error of a singular value by up to 5
+ * where that is near 1.2: with a few rows (1 to 4), whose values may all lie
+ * there, 2^-7 was found. What is kept of an X far below one (|M| far below eps)
+ * is a power of two times it, so that all of this holds down to |M| = 2^-100
+ * eps. Singular values must stay below 8 during the steps (S) and b s^2 + c s^4
+ * below 255 (P), as any useful steps' do: beyond, results are not finite.
  *
  * Conventions as in flint_moe.h: device pointers, caller-owned memory, no
  * allocation, asynchronous on `stream`, status codes. Matrices are contiguous,
@@ -34,7 +36,7 @@
  * size decides how long sums are split, and with it the last bits of larger
  * matrices. A device-side wait that gave up sets
  * FLINT_MOE_DEV_ERR_TIMEOUT in the workspace's status word
- * (flint_moe_read_status), which each call clears.
+ * (flint_moe_read_status), which each call with matrices clears.
  */
 #ifndef FLINT_ORTHOGONALIZE_H_
 #define FLINT_ORTHOGONALIZE_H_
@@ -57,8 +59,8 @@ size_t flint_orthogonalize_workspace_bytes(int32_t n_mat, int32_t rows, int32_t 
 
 /* in: float32 or bf16 (in_fmt) [n_mat][rows][cols], out: bf16, the same shape;
  * out may be in (bf16), any other overlap of the two is refused
- * (FLINT_MOE_EINVAL). coeffs: HOST memory, float [steps][3] = a, b, c of each step, finite, read before the
- * call returns; 1 <= steps <= FLINT_ORTHOGONALIZE_MAX_STEPS. eps > 0 and scale
+ * (FLINT_MOE_EINVAL). coeffs: HOST memory, float [steps][3] = a, b, c of each
+ * step, finite, read before the call returns; 1 <= steps <= FLINT_ORTHOGONALIZE_MAX_STEPS. eps > 0 and scale
  * finite. n_mat = 0 is a no-op; rows and cols from 1. The workspace must not
  * overlap in or out (FLINT_MOE_EINVAL). */
 flint_moe_status flint_orthogonalize(const void* in, int32_t in_fmt, int32_t n_mat, int32_t rows, int32_t cols,

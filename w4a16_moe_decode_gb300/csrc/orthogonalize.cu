@@ -2,12 +2,12 @@
 // where a matrix fits a cluster's shared memory.
 //
 // A step's X <- a X + P X with P = b S + c S S, S = X X^T. What is added to X is amplified by the later steps where X is
-// weak, by up to a^steps (485 after five steps of 3.4445): X is kept to 22 bits or more (hi + lo f16, or FP32). An error
+// weak, by up to a^steps (485 after five steps of 3.4445): X is kept as hi + lo f16, or in FP32. An error
 // relative to X from the left, (1 + e) X, only turns the result by e: so the products take f16 values, S from X's hi, P
 // from one rounding of each of its parts, and the tensor cores run at one product's rate instead of three. S, P and the
 // update of wide X read their transposes as they lie (S and P are their own); S and P are computed above the diagonal.
 // Scaled values: X is kept times 2^10, S times 2^10 and P times 2^8, so that f16 holds X and S to 2^-35 and P to 2^-33, or to
-// a relative 2^-12 (X's two values 2^-23) where that is more. A matrix whose norm is far below eps gives an X far below one:
+// a relative 2^-11 (X's two values 2^-22) where that is more. A matrix whose norm is far below eps gives an X far below one:
 // it is kept times a further power of two, which falls as the steps let X grow (Size).
 //
 // Two updates of 8192 x 2048, us: 980 (1130 TFLOP/s of the products that cannot be left out), bound by the tensor cores
@@ -402,7 +402,7 @@ struct Update {
 // ---------------------------------------------------------------------------
 constexpr int FEW_THREADS = 512;
 constexpr int FEW_GROUPS = FEW_THREADS / 128;  // four warps reach all of tensor memory's lanes
-constexpr int FEW_UNITS = 4;                   // of 16 columns of a row, that a thread keeps at most
+constexpr int FEW_UNITS = 4;                   // of 16 columns of a row, that a thread keeps at most (128 registers and 8 bytes spilt)
 
 struct FewArgs {
   const void* in;
@@ -634,7 +634,6 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
         const uint32_t to = ss + (uint32_t)((c >> 4) * f.sbox + i * 128 + ((((c >> 1) & 7) ^ (i & 7)) << 4));
         if (e0 + lane < e1)
           for (int r = lane & 1; r < C; r += 2) st_dsmem_v4(dsmem_addr(to, (rank + r) & (C - 1)), o);
-        if (C == 1 && (lane & 1) == 0 && e0 + lane < e1) st_dsmem_v4(to, o);
       }
     }
     cluster_sync();
