@@ -14,17 +14,18 @@
  * FP32, FP64 adds the threads'. X is kept as the sum of two f16 values, to 2^-22
  * of a value or to 2^-35 where that is more (in one kernel's registers, up to
  * 128 rows, as FP32), because what its rounding adds to the weak directions the
- * later steps amplify by up to a^steps. In the products, where a relative error
- * stays relative, X, S and P = b S + c S S are single f16 values, to 2^-11 of a
- * value or to 2^-35 (P: 2^-33); up to 64 rows P is two of them, up to 32 X is.
- * With the steps above the result of random entries is within 2^-8 of the exact
- * one in the norm, 2^-8.5 as a rule, of which its own rounding to bf16 is
- * 2^-9.2. A step multiplies a relative error of a singular value by up to 5
- * where that is near 1.2: with a few rows (1 to 4), whose values may all lie
- * there, 2^-7 was found. What is kept of an X far below one (|M| far below eps)
- * is a power of two times it, so that all of this holds down to |M| = 2^-100
- * eps. Singular values must stay below 8 during the steps (S) and b s^2 + c s^4
- * below 255 (P), as any useful steps' do: beyond, results are not finite.
+ * later steps amplify by up to a^steps. Up to 32 rows the products take X, S and
+ * P = b S + c S S as two f16 values too: with the steps above results are the
+ * exact ones rounded to bf16 (2^-9.2 of the norm), to 2^-11 of the norm. Above,
+ * where a relative error stays relative, X, S and P (from 65 rows on) are single
+ * f16 values in the products, to 2^-11 of a value or to 2^-35 (P: 2^-33), and
+ * results are within 2^-8 of the exact ones in the norm, 2^-8.5 as a rule;
+ * singular values that all pass near 1.2, where a step multiplies a relative
+ * error by up to 5, were found to give 0.004. What is kept of an X far below one
+ * (|M| far below eps) is a power of two times it, so that all of this holds down
+ * to |M| = 2^-100 eps. Singular values must stay below 8 during the steps (S)
+ * and b s^2 + c s^4 below 255 (P), as any useful steps' do: beyond, results are
+ * not finite.
  *
  * Conventions as in flint_moe.h: device pointers, caller-owned memory, no
  * allocation, asynchronous on `stream`, status codes. Matrices are contiguous,

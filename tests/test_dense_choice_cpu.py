@@ -27,8 +27,9 @@ int main() {
   while (scanf(" %c %d %d %d", &op, &a, &b, &c) == 4) {
     if (op == 'o') {  // matrices, rows, columns: the operands' sizes of orthogonalize.cu
       const int m = std::min(b, c), k = std::max(b, c), segs = m <= 32 ? 3 : m <= 64 ? 2 : 1;
-      put("gram", choose<Plain>({{{m, m, blocks(k), 1, 0, 0, 0, 0, 1, a}}, 1, 1, nullptr, 0}));
-      put("poly", choose<Plain>({{{m, m, blocks(m), 1, 0, 0, 0, 0, 1, a}}, 1, 1, nullptr, 0}));
+      const int halves = m <= 32 ? 3 : 1;
+      put("gram", choose<Plain>({{{m, m, blocks(k), halves, 0, 0, 0, 0, 1, a}}, 1, 1, nullptr, 0}));
+      put("poly", choose<Plain>({{{m, m, blocks(m), halves, 0, 0, 0, 0, 1, a}}, 1, 1, nullptr, 0}));
       put("update", choose<Plain>({{{b, c, blocks(m), segs, 0, 0, 0, 0, 0, a}}, 1, 1, nullptr, 0}));
     } else {  // tokens, hidden, inter: those of ffn.cu
       put("glu", choose<Gated>({{{a, c, blocks(b), 1, 0, 0, 0, 0, 0, 1}}, 1, 0, nullptr, 0}));

@@ -18,6 +18,7 @@ from w4a16_moe_decode_gb300.build import build
 from _dense import STEPS, momentum, near
 from _dense_shapes import UPDATES_BY_PAIRS
 from _finetune import HALF_BF16, check, f64
+from _orthogonal import rounded, steps_error
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -92,15 +93,43 @@ def test_the_last_of_many_alone(n, rows, cols):
     near(got, f64(alone), 2 * LIMIT, "both")
 
 
+BIG_STEPS = ((8.287, -23.596, 17.3), (4.107, -2.947, 0.545), (3.949, -2.909, 0.552), (3.318, -2.488, 0.51))
+
+
 @pytest.mark.parametrize("rows,cols", [(40, 600), (64, 600), (600, 64), (128, 600)])
 def test_steps_of_large_coefficients(rows, cols):
-    """Coefficients up to 24, whose P is larger than that of the usual steps and its roundings with it: within the same
-    bound."""
-    steps = ((8.287, -23.596, 17.3), (4.107, -2.947, 0.545), (3.949, -2.909, 0.552), (3.318, -2.488, 0.51))
+    """Coefficients up to 24, whose P is larger than that of the usual steps and its roundings with it, and whose slopes
+    carry errors on: below what _orthogonal derives from them, a bf16 rounding of a root mean square of 2^-8 / sqrt(3)
+    beside it. (As it is with 40 rows, where slopes reach 30.)"""
     m = momentum(4, rows, cols, 9, "noise")
     m = (m / torch.linalg.matrix_norm(m)[:, None, None]).contiguous()
     ws = torch.full((fb.flint_orthogonalize_workspace_bytes(*m.shape),), 0xFF, dtype=torch.uint8, device=DEV)
     out = torch.full(m.shape, float("nan"), dtype=torch.bfloat16, device=DEV)
-    fb.flint_orthogonalize(m.to(DEV), out, steps, 1.0, ws, 2.0)
+    fb.flint_orthogonalize(m.to(DEV), out, BIG_STEPS, 1.0, ws, 2.0)
     for i in range(4):
-        near(out[i], oorth.orthogonalize(f64(m[i]), steps, 1.0, 2.0), LIMIT, f"matrix {i}")
+        limit = np.hypot(steps_error(f64(m[i]), BIG_STEPS, 1.0), HALF_BF16 / np.sqrt(3))
+        near(out[i], oorth.orthogonalize(f64(m[i]), BIG_STEPS, 1.0, 2.0), limit, f"matrix {i}")
+
+
+def alike(n, rows, cols, seed):
+    """Matrices whose singular values lie within a fifth of one another: no averaging over them."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.linalg.qr(torch.randn(n, max(rows, cols), min(rows, cols), generator=g, dtype=torch.float64))[0]
+    m = q * (0.8 + 0.4 * torch.rand(n, 1, min(rows, cols), generator=g))
+    return (m if rows >= cols else m.transpose(1, 2)).float().contiguous()
+
+
+@pytest.mark.parametrize("steps", [STEPS, BIG_STEPS])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 9), (2, 2), (2, 30), (3, 4), (40, 3), (4, 4), (6, 60), (8, 8), (90, 8), (16, 500), (24, 40), (32, 32),
+                                       (32, 2000), (3, 9000), (9000, 2), (16, 8200), (6200, 32)])
+def test_few_rows_round_once(rows, cols, steps):
+    """Up to 32 rows (or columns) the steps add next to nothing to the result's own rounding, whatever the singular values:
+    |bf16(v + d) - v| <= |bf16(v) - v| + 2 |d|."""
+    n = 30 if rows * cols < 5000 else 4
+    for m in (momentum(n, rows, cols, rows, "noise"), alike(n, rows, cols, cols)):
+        ws = torch.full((fb.flint_orthogonalize_workspace_bytes(*m.shape),), 0xFF, dtype=torch.uint8, device=DEV)
+        out = torch.full(m.shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+        fb.flint_orthogonalize(m.to(DEV), out, steps, EPS, ws)
+        for i in range(n):
+            ref = oorth.orthogonalize(f64(m[i]), steps, EPS)
+            near(out[i], ref, rounded(ref) + 2 * steps_error(f64(m[i]), steps, EPS), f"matrix {i}")

@@ -4,7 +4,8 @@
 // A step's X <- a X + P X with P = b S + c S S, S = X X^T. What is added to X is amplified by the later steps where X is
 // weak, by up to a^steps (485 after five steps of 3.4445): X is kept as hi + lo f16, or in FP32. An error
 // relative to X from the left, (1 + e) X, only turns the result by e: so the products take f16 values, S from X's hi, P
-// from one rounding of each of its parts, and the tensor cores run at one product's rate instead of three. S, P and the
+// from one rounding of each of its parts, and the tensor cores run at one product's rate instead of three (few rows apart,
+// below). S, P and the
 // update of wide X read their transposes as they lie (S and P are their own); S and P are computed above the diagonal.
 // Scaled values: X is kept times 2^10, S times 2^10 and P times 2^8, so that f16 holds X and S to 2^-35 and P to 2^-33, or to
 // a relative 2^-11 (X's two values 2^-22) where that is more. A matrix whose norm is far below eps gives an X far below one:
@@ -24,11 +25,12 @@ namespace ortho {
 
 using namespace gemm;
 
-// P X as P_hi X_hi + P_lo X_hi + P_hi X_lo up to 32 rows, where few rounding errors meet in a result and the products cost
-// little; as P_hi X_hi + P_lo X_hi up to 64, where S is nearly diagonal for long matrices, so that one rounding of a place
-// of P's diagonal turns a whole row (33 x 700 of noise: 0.0041 off with P_hi alone, 0.0025 so, 8 matrices of 48 x 1000 36.0
-// and 37.5 us; 64 x 600 with steps of coefficients up to 24: 0.0040, 16 of 64 x 2048 40.7 and 43.4); above, as P_hi X_hi,
-// whose errors average out (128 x 2000 of noise: 0.0024).
+// X, S and P as two f16 values each up to 32 rows, and products of them as three (hi hi, hi lo, lo hi): few rounding errors
+// meet in a result there, and a step multiplies a singular value's by up to 5 near 1.2 (with S as one value, 600 matrices of
+// 2 rows were up to 0.0097 off and of 6 0.0045; so 0.0033 and 0.0024, what rounding them once gives. 8 of 16 x 2048: 23.8
+// and 25.2 us). Up to 64 P alone is, where S is nearly diagonal for long matrices, so that one rounding of a place of P's
+// diagonal turns a whole row (33 x 700 of noise: 0.0041 off with P_hi alone, 0.0025 so; 16 of 64 x 2048 40.7 and 41.7).
+// Above, one value of each, whose errors average out (128 x 2000 of noise: 0.0024).
 __host__ __device__ inline bool few_rows(int m) { return m <= 32; }
 __host__ __device__ inline bool p_halves(int m) { return m <= 64; }
 
@@ -259,9 +261,10 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_split(const Start a) {
 // ---------------------------------------------------------------------------
 // Epilogues: S, P = b S + c S S, X <- a X + P X.
 // ---------------------------------------------------------------------------
+template <bool LO>  // S's second half too (few_rows: one tile a matrix)
 struct Gram {
   static constexpr bool PAIR = false;
-  static constexpr int MAPS = 1, OUTS = 1, INS = 0;
+  static constexpr int MAPS = 1, OUTS = LO ? 2 : 1, INS = 0;
   struct Args {};
   using Pre = NoPre;
   static __device__ __forceinline__ void matrix(const Args&, Part&) {}
@@ -273,6 +276,15 @@ struct Gram {
     const uint4 o[4] = {pack8_f16(v), pack8_f16(v + 8), pack8_f16(v + 16), pack8_f16(v + 24)};
     t.put(&maps.io[0], t.n0 + c, o);
     if (t.twice) t.put_transposed(&maps.io[0], t.n0 + c, o);
+    if constexpr (LO) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float2 hi = h2f2(f2h2(v[j], v[j + 1]));
+        v[j] -= hi.x, v[j + 1] -= hi.y;
+      }
+      const uint4 l[4] = {pack8_f16(v), pack8_f16(v + 8), pack8_f16(v + 16), pack8_f16(v + 24)};
+      t.put(&maps.io[1], t.n0 + c, l);
+    }
   }
 };
 
@@ -287,19 +299,26 @@ __device__ __forceinline__ void load_row(const Part& t, const uint16_t* m, int p
 // A matrix's factors of a step, which k_ortho_split left.
 __device__ __forceinline__ float4 factors_of(const float4* f, int z) { return __ldcg(f + (size_t)z * FLINT_ORTHOGONALIZE_MAX_STEPS); }
 
+template <bool LO>  // S's second half (few_rows)
 struct Poly {
   static constexpr bool PAIR = false;
-  static constexpr int MAPS = 1, OUTS = 2, INS = 1;
+  static constexpr int MAPS = 1, OUTS = 2, INS = LO ? 2 : 1;
   struct Args {
-    const uint16_t* s;
+    const uint16_t *s, *s_lo;
     int pitch;
     const float4* factors;  // of this step, FLINT_ORTHOGONALIZE_MAX_STEPS apart
-    int lo;  // P's second half too (p_halves)
+    int lo;                 // P's second half too (p_halves)
   };
   struct Pre {
-    uint4 s[4];
-    __device__ __forceinline__ Pre(const Args& a, const Part& t, int c) { load_row(t, a.s, a.pitch, c, s); }
-    __device__ __forceinline__ Pre(const Part& t, const uint8_t* in) { slot_row(t, in, s); }
+    uint4 s[4], l[LO ? 4 : 1];
+    __device__ __forceinline__ Pre(const Args& a, const Part& t, int c) {
+      load_row(t, a.s, a.pitch, c, s);
+      if constexpr (LO) load_row(t, a.s_lo, a.pitch, c, l);
+    }
+    __device__ __forceinline__ Pre(const Part& t, const uint8_t* in) {
+      slot_row(t, in, s);
+      if constexpr (LO) slot_row(t, in + SLOT, l);
+    }
   };
   static __device__ __forceinline__ void matrix(const Args& a, Part& t) { t.f = factors_of(a.factors, t.z); }
   static __device__ __forceinline__ void chunk(const Args& a, const MapsOf<Poly>& maps, Part& t, int c, uint32_t (&w)[32], uint32_t (&)[32],
@@ -310,6 +329,12 @@ struct Poly {
     for (int j = 0; j < 4; ++j) {
       float v[8];
       unpack8_f16(pre.s[j], v);
+      if constexpr (LO) {
+        float l[8];
+        unpack8_f16(pre.l[j], l);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += l[i];
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = fmaf(fs, v[i], fq * __uint_as_float(w[8 * j + i]));
       split8(v, hi[j], lo[j]);
@@ -392,17 +417,18 @@ struct Update {
 //   S's partial sums of the CTA's rows (tcgen05) -> shared memory; each CTA adds
 //   its share of them over the cluster and hands the f16 result to all;
 //   P = b S + c S S, by every CTA for itself;
-//   X <- a X + X P, by rows (few_rows, p_halves: with the second halves of X and P).
+//   X <- a X + X P, by rows (few_rows, p_halves: with the second halves of X, S and P).
 // Bound by latency: two cluster barriers, the exchange between them and three
 // products that wait for one another a step. 8 matrices of 16 x 2048: 105 us
-// with the general path's 17 launches, 23.5 here; 16 of 64 x 2048 183 and 41;
+// with the general path's 17 launches, 25 here; 16 of 64 x 2048 183 and 42;
 // four of 128 x 2048 140 and 52. Tried: clusters of eight for 64 rows (one matrix
 // 47 us, 16 in two rounds 94), X in shared memory as hi and lo alone (63), the
 // sums read in rank order (the exchange 14500 cycles instead of 6300).
 // ---------------------------------------------------------------------------
 constexpr int FEW_THREADS = 512;
 constexpr int FEW_GROUPS = FEW_THREADS / 128;  // four warps reach all of tensor memory's lanes
-constexpr int FEW_UNITS = 4;                   // of 16 columns of a row, that a thread keeps at most (128 registers and 8 bytes spilt)
+constexpr uint32_t S_LO = 64 * 128;            // S's second half (few_rows): the rows of its box from 64 on
+constexpr int FEW_UNITS = 4;                   // of 16 columns of a row, that a thread keeps at most (128 registers, up to 32 words spilt)
 
 struct FewArgs {
   const void* in;
@@ -415,7 +441,7 @@ struct FewArgs {
 };
 
 struct FewPlan {
-  int mp, mb, xbox, sbox, pbox, tmem;  // columns padded to 16, boxes of 64; bytes of a box of X, S and P; tensor memory
+  int mp, mb, xbox, sbox, pbox, sums, tmem;  // columns padded to 16, boxes of 64; bytes of a box of X, S, P and of sums; tensor memory
   size_t x[2], s, p, total;            // x: hi, lo; p: P's halves, and S's partial sums before
 };
 __host__ __device__ inline FewPlan few_plan(int m, int kc) {
@@ -430,7 +456,8 @@ __host__ __device__ inline FewPlan few_plan(int m, int kc) {
   f.x[1] = (size_t)(halves - 1) * f.mb * f.xbox;
   f.s = (size_t)halves * f.mb * f.xbox;
   f.p = f.s + (size_t)f.mb * f.sbox;
-  const size_t p = (size_t)(p_halves(m) ? 2 : 1) * f.mb * f.pbox, sums = (size_t)f.mp * m * 4;
+  f.sums = f.mp * m * 4;
+  const size_t p = (size_t)(p_halves(m) ? 2 : 1) * f.mb * f.pbox, sums = (size_t)halves * f.sums;
   f.total = 1024 + f.p + (p > sums ? p : sums);
   const int cols = (kc / 128 + 2) * f.mp;
   f.tmem = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
@@ -450,7 +477,7 @@ __device__ __forceinline__ double ld_dsmem_f64(uint32_t remote) {
 // What 16 ks columns of a K-major operand in boxes of 64 columns add to its descriptor.
 __device__ __forceinline__ uint32_t k_step(int ks, int box) { return (uint32_t)((ks >> 2) * (box >> 4) + (ks & 3) * 2); }
 
-template <int UNITS>
+template <int UNITS, bool BOTH>  // (few_rows)
 __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
   extern __shared__ uint8_t dsmem[];
   __shared__ double s_sum[FEW_THREADS / 32], s_part;
@@ -461,7 +488,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, group = warp >> 2;
   const int C = gridDim.x, rank = blockIdx.x;
   const FewPlan f = few_plan(a.m, a.kc);
-  const bool both = few_rows(a.m), both_p = p_halves(a.m);
+  const bool both_p = BOTH || p_halves(a.m);
   const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
   uint8_t* const sm = dsmem + (base - smem_addr(dsmem));
   const uint32_t xs = base + (uint32_t)f.x[0], xls = base + (uint32_t)f.x[1], ss = base + (uint32_t)f.s, ps = base + (uint32_t)f.p;
@@ -547,7 +574,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t o = xoff(t * 128 + i0, c / 8 + h);
-      if (both) {
+      if constexpr (BOTH) {
         uint4 hi, lo;
         split8(&x[n][8 * h], hi, lo);
         *reinterpret_cast<uint4*>(xp + o) = hi;
@@ -588,28 +615,42 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
     if (sizes) s_step = size.next(a.coeffs[3 * step], a.coeffs[3 * step + 1], a.coeffs[3 * step + 2], step + 1 == a.steps);
     if (warp == 0 && elect_one()) {
       fence_proxy_async();
-      // With one box of columns, rows of D from 64 on (which are not read) come from eight rows of X further on, and at the
-      // end from the 1 KiB behind X, which is S's: the second box's place could lie outside the shared memory.
+      // With one box of columns, rows of D from 64 on come from X's lo (BOTH), or, not read, from eight rows of X further
+      // on, and at the end from the 1 KiB behind X, which is S's: a second box's place could lie outside the shared memory.
       const uint32_t idesc = idesc_f32acc(128, f.mp, false) | IDESC_A_MN | IDESC_B_MN;
-      uint64_t d = sw128_desc_mn(xs, f.mb == 1 ? 1024 : f.xbox);
+      uint64_t d = sw128_desc_mn(xs, f.mb == 1 && !BOTH ? 1024 : f.xbox);
 #pragma unroll 4
       for (int ks = 0; ks < a.kc / 16; ++ks, d += 2048 >> 4) tc_mma(d_s, d, d, idesc, ks > 0);
       tc_commit(&bar);
     }
     __syncwarp();
     arrived();
-    // This CTA's sums, by rows, pieces of four swizzled by row.
+    // This CTA's sums, by rows, pieces of four swizzled by row; those of X's lo behind them.
+    const bool lo_row = BOTH && i0 >= 64;
+    const int si = lo_row ? i0 - 64 : i0;
+    uint8_t* const sums = pp + (lo_row ? f.sums : 0);
     for (int c = 16 * group; c < f.mp; c += 16 * FEW_GROUPS) {
       uint32_t w[16];
       __syncwarp();
       tc_ld16(d_s + lanes + c, w);
-      if (i0 < a.m)
+      if (si < a.m)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(pp + (i0 * (f.mp / 4) + ((c / 4 + j) ^ (i0 & swz))) * 16) =
+          *reinterpret_cast<uint4*>(sums + (si * (f.mp / 4) + ((c / 4 + j) ^ (si & swz))) * 16) =
               make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     }
     tc_fence_before();
+    if constexpr (BOTH) {  // S = hi hi + lo hi + hi lo, the last the transpose of the one before
+      __syncthreads();
+      auto place = [&](int i, int n) { return (uint32_t)((i * (f.mp / 4) + ((n >> 2) ^ (i & swz))) * 16 + (n & 3) * 4); };
+      const uint8_t* const lo = pp + f.sums;
+      for (int i = threadIdx.x >> (f.mp == 16 ? 4 : 5), n = threadIdx.x & (f.mp - 1); i < a.m; i += FEW_THREADS / f.mp) {
+        if (n < a.m)
+          *reinterpret_cast<float*>(pp + place(i, n)) +=
+              *reinterpret_cast<const float*>(lo + place(i, n)) + *reinterpret_cast<const float*>(lo + place(n, i));
+      }
+    }
+    __syncwarp();
     cluster_sync();
     {
       // Pieces of four columns, neighbouring threads a row's; two threads join theirs to one piece of eight f16 values and
@@ -628,12 +669,20 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
         for (int r = 1; r < 8; ++r)
           if (r < C) v.x += p[r].x, v.y += p[r].y, v.z += p[r].z, v.w += p[r].w;
         constexpr float fs = S_SCALE / (X_SCALE * X_SCALE);
-        const uint32_t w0 = f2h2(v.x * fs, v.y * fs), w1 = f2h2(v.z * fs, v.w * fs);
-        const uint32_t o0 = __shfl_xor_sync(0xffffffffu, w0, 1), o1 = __shfl_xor_sync(0xffffffffu, w1, 1);
-        const uint4 o = lane & 1 ? make_uint4(o0, o1, w0, w1) : make_uint4(w0, w1, o0, o1);
+        v.x *= fs, v.y *= fs, v.z *= fs, v.w *= fs;
+        // (returns what the f16 values leave)
+        auto give = [&](const float4 u, uint32_t to) {
+          const uint32_t w0 = f2h2(u.x, u.y), w1 = f2h2(u.z, u.w);
+          const uint32_t o0 = __shfl_xor_sync(0xffffffffu, w0, 1), o1 = __shfl_xor_sync(0xffffffffu, w1, 1);
+          const uint4 o = lane & 1 ? make_uint4(o0, o1, w0, w1) : make_uint4(w0, w1, o0, o1);
+          if (e0 + lane < e1)
+            for (int r = lane & 1; r < C; r += 2) st_dsmem_v4(dsmem_addr(to, (rank + r) & (C - 1)), o);
+          const float2 x = h2f2(w0), y = h2f2(w1);
+          return make_float4(u.x - x.x, u.y - x.y, u.z - y.x, u.w - y.y);
+        };
         const uint32_t to = ss + (uint32_t)((c >> 4) * f.sbox + i * 128 + ((((c >> 1) & 7) ^ (i & 7)) << 4));
-        if (e0 + lane < e1)
-          for (int r = lane & 1; r < C; r += 2) st_dsmem_v4(dsmem_addr(to, (rank + r) & (C - 1)), o);
+        const float4 rest = give(v, to);
+        if constexpr (BOTH) give(rest, to + S_LO);
       }
     }
     cluster_sync();
@@ -641,11 +690,16 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
     if (warp == 0 && elect_one()) {
       fence_proxy_async();
       const uint32_t idesc = idesc_f32acc(128, f.mp, false);
-      const uint64_t d = sw128_desc(ss);
+      // (S's lo as A takes its rows from 64 on, which are not read, from behind S: P's place, which is as long)
+      const uint64_t d = sw128_desc(ss), dl = sw128_desc(ss + S_LO);
 #pragma unroll 4
       for (int ks = 0; ks < f.mp / 16; ++ks) {
         const uint32_t o = k_step(ks, f.sbox);
         tc_mma(d_q, d + o, d + o, idesc, ks > 0);
+        if constexpr (BOTH) {
+          tc_mma(d_q, dl + o, d + o, idesc, 1);
+          tc_mma(d_q, d + o, dl + o, idesc, 1);
+        }
       }
       tc_commit(&bar);
     }
@@ -663,6 +717,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
           float v[8];
           const uint32_t at = (uint32_t)(i0 * 128 + (((pc & 7) ^ (i0 & 7)) << 4));
           unpack8_f16(*reinterpret_cast<const uint4*>(sp + (pc >> 3) * f.sbox + at), v);
+          if constexpr (BOTH) {
+            float lo[8];
+            unpack8_f16(*reinterpret_cast<const uint4*>(sp + S_LO + at), lo);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += lo[e];
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = fmaf(fs, v[e], fq * __uint_as_float(w[8 * j + e]));
           uint4 hi, lo;
@@ -683,7 +743,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) k_ortho_few(const FewArgs a) {
           const uint32_t ox = row + k_step(ks, f.xbox), op = k_step(ks, f.pbox);
           tc_mma(d_x + t * f.mp, dh + ox, ph + op, idesc, ks > 0);
           if (both_p) tc_mma(d_x + t * f.mp, dh + ox, pl + op, idesc, 1);
-          if (both) tc_mma(d_x + t * f.mp, dl + ox, ph + op, idesc, 1);
+          if constexpr (BOTH) tc_mma(d_x + t * f.mp, dl + ox, ph + op, idesc, 1);
         }
       }
       tc_commit(&bar);
@@ -758,7 +818,7 @@ int parts_of(int rows, int cols) {
 
 struct WsPlan {
   int m, pitch, mpitch, parts;
-  size_t part, factors, x[2][2], s, p[2], total;  // x: of even and odd steps; x, p: hi and lo
+  size_t part, factors, x[2][2], s[2], p[2], total;  // x: of even and odd steps; x, s, p: hi and lo
 };
 WsPlan ws_plan(int n, int rows, int cols) {
   WsPlan w = {};
@@ -776,8 +836,10 @@ WsPlan ws_plan(int n, int rows, int cols) {
     w.x[i >> 1][i & 1] = o;
     o += xb;
   }
-  w.s = o;
-  o += mb;
+  for (int i = 0; i < 2; ++i) {
+    w.s[i] = o;
+    o += i == 0 || few_rows(w.m) ? mb : 0;
+  }
   for (int i = 0; i < 2; ++i) {
     w.p[i] = o;
     o += i == 0 || p_halves(w.m) ? mb : 0;
@@ -797,9 +859,9 @@ int few_ctas(int m, int k, int* kc) {
   return 0;
 }
 
-template <int UNITS>
+template <int UNITS, bool BOTH>
 bool run_few(const FewArgs& a, int C, int n, cudaStream_t stream) {
-  return launch<k_ortho_few<UNITS>, 226 * 1024>(dim3(C, n), FEW_THREADS, few_plan(a.m, a.kc).total, C, stream, a);
+  return launch<k_ortho_few<UNITS, BOTH>, 226 * 1024>(dim3(C, n), FEW_THREADS, few_plan(a.m, a.kc).total, C, stream, a);
 }
 
 bool overlaps(const void* p, size_t np, const void* q, size_t nq) {
@@ -842,23 +904,26 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
     FewArgs a = {in, out, fmt == FLINT_ORTHOGONALIZE_BF16, rows, cols, steps, w.m, std::max(rows, cols), kc, eps, scale / X_SCALE, {}, status};
     std::copy(coeffs, coeffs + 3 * steps, a.coeffs);
     const int units = few_units(w.m, kc);
-    ok = units <= 1 ? run_few<1>(a, C, n, stream) : units <= 2 ? run_few<2>(a, C, n, stream) : run_few<4>(a, C, n, stream);
+    if (few_rows(w.m))
+      ok = units <= 1 ? run_few<1, true>(a, C, n, stream) : units <= 2 ? run_few<2, true>(a, C, n, stream) : run_few<4, true>(a, C, n, stream);
+    else
+      ok = units <= 1 ? run_few<1, false>(a, C, n, stream) : units <= 2 ? run_few<2, false>(a, C, n, stream) : run_few<4, false>(a, C, n, stream);
     return ok ? FLINT_MOE_OK : FLINT_MOE_ECUDA;
   }
   auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(wsp + o); };
   const bool tall = rows > cols;
   const int m = w.m;
-  CUtensorMap x[2][2], xout[2][2], s, sout, p[2], pout[2], o;
+  CUtensorMap x[2][2], xout[2][2], s[2], sout[2], p[2], pout[2], o;
   auto map = [&](CUtensorMap* mp, size_t off, int64_t c, int64_t r, int64_t pitch, bool as_out) {
     return map_matrix(mp, at(off), c, r, pitch, n, r * pitch, as_out);
   };
-  ok = map(&s, w.s, m, m, w.mpitch, false) && map(&sout, w.s, m, m, w.mpitch, true);
   for (int i = 0; i < 2; ++i) {
+    ok = ok && map(&s[i], w.s[i], m, m, w.mpitch, false) && map(&sout[i], w.s[i], m, m, w.mpitch, true);
     for (int h = 0; h < 2; ++h)
       ok = ok && map(&x[i][h], w.x[i][h], cols, rows, w.pitch, false) && map(&xout[i][h], w.x[i][h], cols, rows, w.pitch, true);
     ok = ok && map(&p[i], w.p[i], m, m, w.mpitch, false) && map(&pout[i], w.p[i], m, m, w.mpitch, true);
   }
-  o = sout;
+  o = sout[0];
   if (cols % 8 == 0) ok = ok && map_matrix(&o, out, cols, rows, cols, n, (int64_t)rows * cols, true);
   if (!ok) return FLINT_MOE_ECUDA;
   Start st = {in, fmt == FLINT_ORTHOGONALIZE_BF16, n, rows, cols, w.pitch, w.parts, eps,
@@ -869,29 +934,39 @@ extern "C" flint_moe_status flint_orthogonalize(const void* in, int32_t fmt, int
       !launch<k_ortho_split, 0>(dim3(parts + 1, mats), START_THREADS, 0, 0, stream, st))
     return FLINT_MOE_ECUDA;
   const int kx = ((tall ? rows : cols) + BK - 1) / BK, km = (m + BK - 1) / BK;
-  AllMaps<Gram> mg;
-  AllMaps<Poly> mp;
+  AllMaps<Gram<false>> mg;
+  AllMaps<Gram<true>> mgl;
+  AllMaps<Poly<false>> mp;
+  AllMaps<Poly<true>> mpl;
   AllMaps<Update<false>> mu;
-  mp.of[0].a[0] = mp.of[0].b[0] = s;
-  mp.of[0].io[2] = mg.of[0].io[0] = sout;
-  const int segs = few_rows(m) ? 3 : p_halves(m) ? 2 : 1;
+  // Products of two halves: hi hi, then the second operand's lo (of P X: P's), then the other's.
+  const bool few = few_rows(m);
+  const int halves = few ? 3 : 1, segs = few ? 3 : p_halves(m) ? 2 : 1, second = 2, third = 4;
+  mp.of[0].a[0] = mp.of[0].b[0] = s[0];
+  mp.of[0].io[2] = mg.of[0].io[0] = sout[0];
   for (int h = 0; h < 2; ++h) {
-    mp.of[0].io[h] = pout[h];
+    mgl.of[0].io[h] = sout[h];
+    mpl.of[0].a[h] = mpl.of[0].b[h] = s[h];
+    mpl.of[0].io[2 + h] = sout[h];
+    mp.of[0].io[h] = mpl.of[0].io[h] = pout[h];
     (tall ? mu.of[0].b : mu.of[0].a)[h] = p[h];
   }
   for (int i = 0; i < steps; ++i) {
     const float4* factors = st.factors + i;
     const bool last = i + 1 == steps;
     // S = X X^T (X^T X), both operands the same matrix; P from S, which is its own transpose; X's rows times P, or P times X
-    mg.of[0].a[0] = mg.of[0].b[0] = x[i & 1][0];
     for (int h = 0; h < 2; ++h) {
+      mg.of[0].a[h] = mg.of[0].b[h] = mgl.of[0].a[h] = mgl.of[0].b[h] = x[i & 1][h];
       (tall ? mu.of[0].a : mu.of[0].b)[h] = x[i & 1][h];
       mu.of[0].io[h] = last ? o : xout[(i + 1) & 1][h];
       mu.of[0].io[2 + h] = xout[i & 1][h];
     }
-    ok = run<Gram>({{{m, m, kx, 1, 0, 0, tall, tall, 1, n}}, 1, 1, status, 0}, mg, {}, stream) &&
-         run<Poly>({{{m, m, km, 1, 0, 0, 0, 0, 1, n}}, 1, 1, status, 0}, mp, {at(w.s), w.mpitch, factors, segs > 1}, stream);
-    const int p_of = 2, x_of = 4;  // hi hi, then P_lo, then X_lo
+    const gemm::Args gram = {{{m, m, kx, halves, third, second, tall, tall, 1, n}}, 1, 1, status, 0};
+    const gemm::Args poly = {{{m, m, km, halves, third, second, 0, 0, 1, n}}, 1, 1, status, 0};
+    ok = few ? run<Gram<true>>(gram, mgl, {}, stream) && run<Poly<true>>(poly, mpl, {at(w.s[0]), at(w.s[1]), w.mpitch, factors, 1}, stream)
+             : run<Gram<false>>(gram, mg, {}, stream) &&
+                   run<Poly<false>>(poly, mp, {at(w.s[0]), nullptr, w.mpitch, factors, segs > 1}, stream);
+    const int p_of = second, x_of = third;
     const gemm::Args upd = {{{rows, cols, km, segs, tall ? x_of : p_of, tall ? p_of : x_of, 0, !tall, 0, n, tall ? 1 : 2}}, 1, 1, status, 0};
     const uint16_t *hi = at(w.x[i & 1][0]), *lo = at(w.x[i & 1][1]);
     ok = ok && (last ? run<Update<true>>(upd, mu, {hi, lo, w.pitch, factors, scale / X_SCALE, out}, stream)
