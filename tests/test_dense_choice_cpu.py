@@ -17,8 +17,9 @@ PROGRAM = r"""
 #include <cstdio>
 #include "gemm.cuh"
 using namespace flint::gemm;
-struct Plain { static constexpr bool PAIR = false; };
-struct Gated { static constexpr bool PAIR = true; };
+struct Plain { static constexpr bool PAIR = false, SMALL = false; };
+struct Gated { static constexpr bool PAIR = true, SMALL = false; };
+struct Few { static constexpr bool PAIR = false, SMALL = true; };
 static void put(const char* what, const Choice& c) { printf("%s:%s%d ", what, c.kind == 0 ? "pairs" : c.kind == 1 ? "one" : "half", c.S); }
 static int blocks(int k) { return (k + BK - 1) / BK; }
 int main() {
@@ -28,8 +29,9 @@ int main() {
     if (op == 'o') {  // matrices, rows, columns: the operands' sizes of orthogonalize.cu
       const int m = std::min(b, c), k = std::max(b, c), segs = m <= 32 ? 3 : m <= 64 ? 2 : 1;
       const int halves = m <= 32 ? 3 : 1;
-      put("gram", choose<Plain>({{{m, m, blocks(k), halves, 0, 0, 0, 0, 1, a}}, 1, 1, nullptr, 0}));
-      put("poly", choose<Plain>({{{m, m, blocks(m), halves, 0, 0, 0, 0, 1, a}}, 1, 1, nullptr, 0}));
+      const Args gram = {{{m, m, blocks(k), halves, 0, 0, 0, 0, 1, a}}, 1, 1, nullptr, 0}, poly = {{{m, m, blocks(m), halves, 0, 0, 0, 0, 1, a}}, 1, 1, nullptr, 0};
+      put("gram", m <= 32 ? choose<Few>(gram) : choose<Plain>(gram));
+      put("poly", m <= 32 ? choose<Few>(poly) : choose<Plain>(poly));
       put("update", choose<Plain>({{{b, c, blocks(m), segs, 0, 0, 0, 0, 0, a}}, 1, 1, nullptr, 0}));
     } else {  // tokens, hidden, inter: those of ffn.cu
       put("glu", choose<Gated>({{{a, c, blocks(b), 1, 0, 0, 0, 0, 0, 1}}, 1, 0, nullptr, 0}));

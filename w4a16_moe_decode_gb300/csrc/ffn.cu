@@ -35,7 +35,7 @@ __device__ __forceinline__ float silu(float g) {
 
 // bf16 rows [M][N] as they are.
 struct Store {
-  static constexpr bool PAIR = false;
+  static constexpr bool PAIR = false, SMALL = false;
   static constexpr int MAPS = MOST, OUTS = 1, INS = 0;
   struct Args {};
   using Pre = NoPre;
@@ -51,7 +51,7 @@ struct Store {
 // h = silu(g) u from half of the accumulator's columns of g and the same columns of u behind them, and g and u themselves.
 template <bool SAVE>
 struct Glu {
-  static constexpr bool PAIR = true;
+  static constexpr bool PAIR = true, SMALL = false;
   static constexpr int MAPS = 1, OUTS = 3, INS = 0;
   struct Args {};
   using Pre = NoPre;
@@ -82,7 +82,7 @@ struct Glu {
 
 // dg, du and h from dh and the kept g and u.
 struct DGlu {
-  static constexpr bool PAIR = false;
+  static constexpr bool PAIR = false, SMALL = false;
   static constexpr int MAPS = 1, OUTS = 3, INS = 2;
   struct Args {
     const uint16_t* g;  // [M][N]

@@ -86,7 +86,8 @@ struct Maps {
   CUtensorMap a[2], b[2];
   CUtensorMap io[IO];
 };
-// An epilogue E has OUTS and INS of them, for each of up to MAPS products of a launch.
+// An epilogue E has OUTS and INS of them, for each of up to MAPS products of a launch. PAIR: its columns are two products'
+// (B has two operands). SMALL: its matrices have one tile of 64 columns at most, which k_gemm alone is for.
 template <typename E>
 using MapsOf = Maps<E::OUTS + E::INS>;
 template <int IO, int N>
@@ -791,7 +792,7 @@ Choice choose(const Args& a, int64_t* cycles = nullptr) {
     const int64_t c = std::max(longest, work / n * rounds) + ends + (S > 1 ? 3000 : 0);
     if (c < cost) cost = c, best = {kind, S};
   };
-  consider(0, 1, sms / 2, a, Walk<Two, E::PAIR>::each, 600, 9000);
+  if constexpr (!E::SMALL) consider(0, 1, sms / 2, a, Walk<Two, E::PAIR>::each, 600, 9000);
   int64_t least = 1 << 30;
   for (int i = 0; i < a.n; ++i) least = std::min<int64_t>(least, a.p[i].blocks());
   auto narrow = [&](int kind, const Args& p, int64_t n, auto tiles, int alone, int two, int ends) {
@@ -800,7 +801,7 @@ Choice choose(const Args& a, int64_t* cycles = nullptr) {
       consider(kind, S, n * S <= sms ? sms : 2 * sms, p, tiles, n * S <= sms ? alone : two, ends);
     }
   };
-  narrow(1, a, Walk<One, E::PAIR>::tiles(a), Walk<One, E::PAIR>::each, 450, 850, 6500);
+  if constexpr (!E::SMALL) narrow(1, a, Walk<One, E::PAIR>::tiles(a), Walk<One, E::PAIR>::each, 450, 850, 6500);
   if constexpr (!E::PAIR) narrow(2, whole(a), Walk<Half, false>::tiles(whole(a)), Walk<Half, false>::each, 300, 500, 5000);
   if (cycles) *cycles = cost;
   return best;
@@ -823,13 +824,13 @@ bool run_tiles(const Args& a, const AllMaps<E>& m, const typename E::Args& e, in
 
 template <typename E>
 bool run(const Args& a, const AllMaps<E>& m, const typename E::Args& e, cudaStream_t stream, const Choice& c) {
-  if (c.kind == 0) {
+  if constexpr (!E::PAIR)
+    if (E::SMALL || c.kind == 2) return run_tiles<Half, E>(whole(a), m, e, c.S, stream);
+  if constexpr (!E::SMALL) {
+    if (c.kind == 1) return run_tiles<One, E>(a, m, e, c.S, stream);
     const int64_t pairs = std::min<int64_t>(Walk<Two, E::PAIR>::tiles(a), sm_count() / 2);
     return launch<k_gemm_pair<E>, PAIR_SMEM<Pairs<E::INS>>>(dim3(2 * (unsigned)pairs), THREADS<Two>, PAIR_SMEM<Pairs<E::INS>>, 0, stream, a, m, e);
   }
-  if constexpr (!E::PAIR)
-    if (c.kind == 2) return run_tiles<Half, E>(whole(a), m, e, c.S, stream);
-  return run_tiles<One, E>(a, m, e, c.S, stream);
 }
 template <typename E>
 bool run(const Args& a, const AllMaps<E>& m, const typename E::Args& e, cudaStream_t stream) {

@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(START_THREADS) k_ortho_split(const Start a) {
 // ---------------------------------------------------------------------------
 template <bool LO>  // S's second half too (few_rows: one tile a matrix)
 struct Gram {
-  static constexpr bool PAIR = false;
+  static constexpr bool PAIR = false, SMALL = LO;
   static constexpr int MAPS = 1, OUTS = LO ? 2 : 1, INS = 0;
   struct Args {};
   using Pre = NoPre;
@@ -301,7 +301,7 @@ __device__ __forceinline__ float4 factors_of(const float4* f, int z) { return __
 
 template <bool LO>  // S's second half (few_rows)
 struct Poly {
-  static constexpr bool PAIR = false;
+  static constexpr bool PAIR = false, SMALL = LO;
   static constexpr int MAPS = 1, OUTS = 2, INS = LO ? 2 : 1;
   struct Args {
     const uint16_t *s, *s_lo;
@@ -350,7 +350,7 @@ struct Poly {
 
 template <bool LAST>
 struct Update {
-  static constexpr bool PAIR = false;
+  static constexpr bool PAIR = false, SMALL = false;
   static constexpr int MAPS = 1, OUTS = 2, INS = 2;
   struct Args {
     const uint16_t *hi, *lo;
