@@ -529,13 +529,10 @@ def _bf16() -> tuple:
 
 def _rows(t, what: str, rows: int, cols: int) -> int | None:
     """The pointer of a tensor that begins with `rows` rows of `cols` bf16 values (or their bits) side by side; others are
-    refused. What decode calls bring first, since each look at a tensor takes 0.1 us of a call of 5."""
-    try:
-        if t.nbytes == 2 * rows * cols and t.is_contiguous() and t.dtype in _bf16():
-            return t.data_ptr()
-    except AttributeError:  # a pointer or None
+    refused."""
+    if t is None or isinstance(t, int):
         return t
-    shape = t.shape  # more rows, rows of several dimensions, values one behind the other
+    shape = t.shape
     n = shape.numel()
     fits = rows < 1 or n == rows * cols or (n > rows * cols and (len(shape) < 2 or shape[-1] == cols))
     if not fits or t.dtype not in _bf16() or not t.is_contiguous():
@@ -597,15 +594,27 @@ def flint_gemv_glu(packed, I: int, K: int, fmt, x, B: int, h, norm_weight=None, 
                    stream=None) -> None:
     """h = bf16(silu(gate x) * (up x)) for up to 32 rows (include/flint_gemv.h): x and h begin with B contiguous rows of K
     and I values."""
-    if not (packed is None or isinstance(packed, int)):
-        if packed.nbytes < (_glu_packed_bytes(I, K, fmt) if B > 0 else 0) or not packed.is_contiguous():
-            raise FlintMoeError(f"packed matrices {tuple(packed.shape)}", EINVAL)
-        packed = packed.data_ptr()
+    need = _glu_packed_bytes(I, K, fmt) if B > 0 else 0
+    # Decode calls are a few microseconds apart and every look at a tensor takes a tenth of one: what they bring as a rule
+    # first, with as few looks as tell.
+    try:
+        plain = (x.dtype is h.dtype is _bf16()[0] and x.nbytes == 2 * B * K and h.nbytes == 2 * B * I and packed.nbytes >= need
+                 and x.is_contiguous() and h.is_contiguous() and packed.is_contiguous())
+    except AttributeError:  # pointers
+        plain = False
+    if plain:
+        px, ph, pp = x.data_ptr(), h.data_ptr(), packed.data_ptr()
+    else:
+        px, ph, pp = _rows(x, "x", B, K), _rows(h, "h", B, I), packed
+        if not (pp is None or isinstance(pp, int)):
+            if pp.nbytes < need or not pp.is_contiguous():
+                raise FlintMoeError(f"packed matrices {tuple(pp.shape)}", EINVAL)
+            pp = pp.data_ptr()
+    if norm_weight is not None:
+        norm_weight = _rows(norm_weight, "norm weight", 1, K)
     if dev_status is not None:
         dev_status = _status_word(dev_status)
-    st = lib().flint_gemv_glu(packed, I, K, fmt, _rows(x, "x", B, K), B, _rows(h, "h", B, I),
-                              None if norm_weight is None else _rows(norm_weight, "norm weight", 1, K), float(eps),
-                              dev_status, _stream(stream))
+    st = lib().flint_gemv_glu(pp, I, K, fmt, px, B, ph, norm_weight, float(eps), dev_status, _stream(stream))
     if st != OK:
         raise FlintMoeError("flint_gemv_glu", st)
 
