@@ -1882,7 +1882,7 @@ __device__ __forceinline__ bool group_all(int group, bool ok) {
 
 // GR = 2: two groups of eight warps share a block's rows, each with its own tiles (and one buffer of weights). Rows that
 // leave an SM room for one block only would have eight warps on it otherwise, which take turns waiting (gemv_glu of 32 x
-// 2048 x 8192: 25.8 -> 21.1 us; 32 x 2048 x 2048 8.9 -> 7.7). Tiles are dealt to all blocks' first groups before any second
+// 2048 x 8192: 25.8 -> 19.9 us; 32 x 2048 x 2048 8.9 -> 7.7). Tiles are dealt to all blocks' first groups before any second
 // one gets a tile, so that no SM idles beside one with two (320 tiles, 17 rows: 8.7 us a block's two tiles together, 7.8
 // so; 1024 tiles 14.0 and 13.2).
 template <int FMT, int NTMAX, GemvEnd END, int GR = 1>

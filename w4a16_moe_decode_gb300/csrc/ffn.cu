@@ -9,8 +9,8 @@
 // for their narrow h, would take half as many MMAs again in the forward pass and nearly twice as many in the gradients,
 // which the tensor cores bound. All sums are FP32.
 //
-// 8192 tokens of 2048 x 8192, us a call: forward with g and u kept 555 (1480 TFLOP/s; the first product alone 1650, at
-// what the card sustains within its power limit), gradients 1127 (1460; the last four products alone 1750). 77 tokens:
+// 8192 tokens of 2048 x 8192, us a call: forward with g and u kept 555 (1490 TFLOP/s; the first product alone 1650, at
+// what the card sustains within its power limit), gradients 1143 (1440; the last four products alone 1750). 77 tokens:
 // 33.6, bound by the weights' stream at 3.4 TB/s and two launches' latency.
 #include "flint_ffn.h"
 #include "gemm.cuh"
