@@ -16,7 +16,7 @@
  * 128 rows, as FP32), because what its rounding adds to the weak directions the
  * later steps amplify by up to a^steps. Up to 32 rows the products take X, S and
  * P = b S + c S S as two f16 values too: with the steps above results are the
- * exact ones rounded to bf16 (2^-9.2 of the norm), to 2^-11 of the norm. Above,
+ * exact ones rounded to bf16 (2^-9.2 of the norm), to 2^-16 of the norm. Above,
  * where a relative error stays relative, X, S and P (from 65 rows on) are single
  * f16 values in the products, to 2^-11 of a value or to 2^-35 (P: 2^-33), and
  * results are within 2^-8 of the exact ones in the norm, 2^-8.5 as a rule;
